@@ -32,6 +32,12 @@
  *   kda_recoverssm_commit_step -- those three (plan, compaction, commit)
  *       with the same results, in one launch.
  *
+ *   kda_conv_update_decode -- the layer on single tokens: one step of the
+ *       recurrence on the checkpoints that the verify starts from.
+ *
+ *   kda_step_tables -- a step's index arrays built on the GPU from request
+ *       lengths: token offsets, new blocks, state slots, cache slots.
+ *
  * plus host-only argument checks mirroring the pages' validation
  * (kernels page `_check_layouts`, `can_use_cute_recoverssm`; ops page
  * `kda_recoverssm_verify`, `KDARecoverSSMCommitContext.create/commit`).
@@ -324,6 +330,87 @@ typedef struct {
   const int32_t* boundary_recovery_lens;
 } kda_compact_args;
 
+/* Arguments of kda_conv_update_decode and kda_decode_qkv: one token for each
+   of `batch` requests (row b of the activations is request b's), one step of
+   the recurrence from the request's state slot, with q, k, v, g, beta formed
+   exactly as in the verify:
+     c = beta (v - S diag(e^g) k_hat),  S' = S diag(e^g) + c k_hat^T,
+     out = S' q.
+   The new state goes to the final slot (NULL: in place); with the fused conv, the newest three raw
+   inputs go to entries [0, 3) of the final slot's conv state, other entries
+   stay.  A request whose state slot is null gets +0.0 outputs and nothing
+   else; one whose final slot alone is null gets its output and no state. */
+typedef struct {
+  kda_tensor mixed_qkv;    /* act [B, 3HD] */
+  kda_tensor raw_gate;     /* act [B, HD] */
+  kda_tensor raw_beta;     /* act [B, H] */
+  kda_tensor A_log;        /* as kda_verify_args, down to state */
+  kda_tensor dt_bias;
+  kda_tensor state;
+  kda_tensor out;          /* F32 or act [B, HD] */
+  kda_tensor conv_state;
+  kda_tensor conv_weight;
+  const int32_t* state_indices;        /* [batch] */
+  const int32_t* final_state_indices;  /* [batch] or NULL: in place */
+  const int32_t* num_accepted_tokens;  /* [batch] conv history offset + 1,
+                                          or NULL: 1 */
+  int32_t batch;
+  int32_t spec_query_len;  /* Q: the conv state holds Q + 2 entries */
+  int32_t null_block_id;
+  int32_t conv_dim_first;
+  int32_t use_lower_bound;
+  float lower_bound;
+} kda_decode_args;
+
+/* Arguments of kda_step_tables: the index arrays of one step, from request
+   lengths.  Request b runs q_b = max(query_lens[b], 0) tokens after its
+   c = max(num_computed_tokens[row], 0) computed ones, row =
+   request_indices[b] (or b); one block holds block_size tokens, and block i
+   of a request is block_table[row][i] (its state slot and its cache block).
+   After the step a request holds the block of its next token, that is
+   (c + q_b) / block_size + 1 blocks, at most the table's width; what
+   num_blocks[row] lacks is taken from free_blocks in batch order and written
+   to the row, the null id once the free blocks run out.  Then
+     query_start_loc[b] = q_0 + .. + q_{b-1} (sums are held to max_tokens),
+     state_indices[b]   = block of token c,
+     initial_state_indices[b] = the same when c > 0, else the null id,
+     final_state_indices[b] = block of token c + q_b,
+   (the null id past the width), and for token t of request b, in token order,
+     positions[t]    = c + t - query_start_loc[b],
+     slot_mapping[t] = block * block_size + position % block_size,
+   -1 where the block is null; behind the last token, up to max_tokens,
+   positions are 0 and slots -1.  A request whose row is outside
+   [0, num_request_rows) runs its tokens with null blocks.  Two requests of
+   a launch must not name the same row. */
+typedef struct {
+  const int32_t* query_lens;           /* [batch] */
+  const int32_t* num_computed_tokens;  /* per request row */
+  const int32_t* num_blocks;           /* per request row: blocks held */
+  const int32_t* request_indices;      /* [batch] or NULL: row = b */
+  const int32_t* free_blocks;          /* [num_free] */
+  int32_t* block_table;                /* [num_request_rows, width] */
+  int64_t block_table_strides[2];      /* row, column (elements) */
+  int32_t batch;
+  int32_t num_request_rows;
+  int32_t block_table_width;
+  int32_t block_size;
+  int32_t num_free;
+  int32_t max_tokens;                  /* size of positions, slot_mapping */
+  int32_t null_block_id;
+  int32_t pad_;
+  int32_t* query_start_loc;            /* [batch + 1] outputs from here on */
+  int32_t* new_num_blocks;             /* per request row, written for the
+                                          batch's rows: live blocks held;
+                                          may be num_blocks itself */
+  int32_t* state_indices;              /* [batch] */
+  int32_t* initial_state_indices;      /* [batch] */
+  int32_t* final_state_indices;        /* [batch] */
+  int32_t* positions;                  /* [max_tokens] */
+  int64_t* slot_mapping;               /* [max_tokens] */
+  int32_t* num_allocated;              /* [1] blocks the step asked for; over
+                                          num_free when they ran out */
+} kda_tables_args;
+
 /* Library ABI version (KDA_ABI_VERSION). */
 int kda_abi_version(void);
 
@@ -411,6 +498,17 @@ int kda_recoverssm_commit_step(const kda_commit_args* commit,
                                const kda_plan_args* plan,
                                const kda_compact_args* compact,
                                void* stream);
+
+/* Host-only validation of decode arguments, then the launch (one kernel).  A
+   request's final slot must not be another request's state or final slot. */
+int kda_check_decode(const kda_decode_args* args);
+int kda_conv_update_decode(const kda_decode_args* args, void* stream);
+int kda_check_decode_qkv(const kda_decode_args* args);
+int kda_decode_qkv(const kda_decode_args* args, void* stream);
+
+/* Host-only validation of the step tables' arguments, then the launches. */
+int kda_check_step_tables(const kda_tables_args* args);
+int kda_step_tables(const kda_tables_args* args, void* stream);
 
 /* Launch a one-workgroup kernel that sets counter[0..n) to 0 on `stream`
    (for a counter left non-zero by an aborted launch).  Uses no memset

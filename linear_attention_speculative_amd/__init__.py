@@ -19,3 +19,13 @@ from .ops import (  # noqa: F401
     verify_args,
     verify_qkv,
 )
+from .serving import (  # noqa: F401
+    check_decode,
+    check_decode_qkv,
+    check_step_tables,
+    conv_update_decode,
+    decode_args,
+    decode_qkv,
+    step_tables,
+    tables_args,
+)

@@ -37,6 +37,9 @@ EXPORTED = (
     "kda_check_compact_conv", "kda_compact_conv_state",
     "kda_check_commit_step", "kda_recoverssm_commit_step",
     "kda_reset_counter", "kda_set_launch_events",
+    "kda_check_decode", "kda_conv_update_decode",
+    "kda_check_decode_qkv", "kda_decode_qkv",
+    "kda_check_step_tables", "kda_step_tables",
 )
 
 
@@ -120,6 +123,39 @@ class KdaCompactArgs(Structure):
     ]
 
 
+_LAYER_TENSORS = [(n, KdaTensor) for n in (
+    "mixed_qkv", "raw_gate", "raw_beta", "A_log", "dt_bias", "state", "out",
+    "conv_state", "conv_weight")]
+_LAYER_SCALARS = [
+    ("batch", c_int32), ("spec_query_len", c_int32),
+    ("null_block_id", c_int32), ("conv_dim_first", c_int32),
+    ("use_lower_bound", c_int32), ("lower_bound", c_float)]
+
+
+class KdaDecodeArgs(Structure):
+    _fields_ = _LAYER_TENSORS + [
+        ("state_indices", c_void_p), ("final_state_indices", c_void_p),
+        ("num_accepted_tokens", c_void_p),
+    ] + _LAYER_SCALARS
+
+
+class KdaTablesArgs(Structure):
+    _fields_ = [
+        ("query_lens", c_void_p), ("num_computed_tokens", c_void_p),
+        ("num_blocks", c_void_p), ("request_indices", c_void_p),
+        ("free_blocks", c_void_p), ("block_table", c_void_p),
+        ("block_table_strides", c_int64 * 2),
+        ("batch", c_int32), ("num_request_rows", c_int32),
+        ("block_table_width", c_int32), ("block_size", c_int32),
+        ("num_free", c_int32), ("max_tokens", c_int32),
+        ("null_block_id", c_int32), ("pad_", c_int32),
+        ("query_start_loc", c_void_p), ("new_num_blocks", c_void_p),
+        ("state_indices", c_void_p), ("initial_state_indices", c_void_p),
+        ("final_state_indices", c_void_p), ("positions", c_void_p),
+        ("slot_mapping", c_void_p), ("num_allocated", c_void_p),
+    ]
+
+
 _LIB = None
 
 
@@ -178,5 +214,14 @@ def load() -> ctypes.CDLL:
     lib.kda_set_launch_events.restype = c_int
     lib.kda_set_launch_events.argtypes = [c_void_p, c_void_p, c_int32,
                                           POINTER(c_int32)]
+    for check, launches, args in (
+            ("kda_check_decode", ("kda_conv_update_decode",), KdaDecodeArgs),
+            ("kda_check_decode_qkv", ("kda_decode_qkv",), KdaDecodeArgs),
+            ("kda_check_step_tables", ("kda_step_tables",), KdaTablesArgs)):
+        getattr(lib, check).restype = c_int
+        getattr(lib, check).argtypes = [POINTER(args)]
+        for name in launches:
+            getattr(lib, name).restype = c_int
+            getattr(lib, name).argtypes = [POINTER(args), c_void_p]
     _LIB = lib
     return lib

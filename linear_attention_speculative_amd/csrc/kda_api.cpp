@@ -3,12 +3,9 @@
 // `can_use_cute_recoverssm` and the ops page's `kda_recoverssm_verify` and
 // `KDARecoverSSMCommitContext.create/commit`), translation of the public
 // descriptors into launch parameters, and the exported C entry points.
-#include <stdarg.h>
-#include <stdio.h>
 #include <stdint.h>
 
-#include <string>
-
+#include "kda_host.hpp"
 #include "kda_internal.hpp"
 #include "kda_recoverssm.h"
 
@@ -21,61 +18,9 @@ LaunchTiming& launch_timing() {
 
 }  // namespace kda
 
+using namespace kda::host;
+
 namespace {
-
-thread_local std::string g_err;
-
-int fail(int code, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return code;
-}
-
-int elem_size(int32_t dt) {
-  return dt == KDA_F32 ? 4 : (dt == KDA_BF16 ? 2 : 0);
-}
-
-bool aligned(const void* p, uintptr_t a) {
-  return reinterpret_cast<uintptr_t>(p) % a == 0;
-}
-
-const char* dt_name(int32_t dt) {
-  return dt == KDA_F32 ? "float32" : (dt == KDA_BF16 ? "bfloat16" : "?");
-}
-
-bool supported_head_dim(int64_t d) {
-  return d == 16 || d == 32 || d == 64 || d == 128;
-}
-
-// Checks ndim, non-negative sizes, known dtype and a data pointer.
-int check_desc(const kda_tensor& t, const char* name, int ndim) {
-  if (t.ndim != ndim)
-    return fail(KDA_E_SHAPE, "%s must have %d dimensions (got %d)", name,
-                ndim, t.ndim);
-  for (int i = 0; i < ndim; ++i)
-    if (t.shape[i] < 0)
-      return fail(KDA_E_SHAPE, "%s has a negative size", name);
-  if (elem_size(t.dtype) == 0)
-    return fail(KDA_E_DTYPE, "%s has an unknown dtype code %d", name,
-                t.dtype);
-  int64_t numel = 1;
-  for (int i = 0; i < ndim; ++i) numel *= t.shape[i];
-  if (t.data == nullptr && numel > 0)
-    return fail(KDA_E_ARG, "%s has no data pointer", name);
-  return KDA_OK;
-}
-
-bool shape_is(const kda_tensor& t, int64_t a, int64_t b, int64_t c = -1,
-              int64_t d = -1) {
-  if (t.shape[0] != a || t.shape[1] != b) return false;
-  if (c >= 0 && t.shape[2] != c) return false;
-  if (d >= 0 && t.shape[3] != d) return false;
-  return true;
-}
 
 struct VerifyPlan {
   kda::VerifyParams p;
@@ -92,12 +37,6 @@ struct VerifyPlan {
 int default_vtiles(int64_t items) {
   return items <= 64 ? 8 : items <= 128 ? 4 : 2;
 }
-
-#define KDA_TRY(expr)             \
-  do {                            \
-    int rc_ = (expr);             \
-    if (rc_ != KDA_OK) return rc_; \
-  } while (0)
 
 // conv: the fused conv update (kda_conv_update_verify); otherwise mixed_qkv
 // already holds the convolved q | k | v (kda_recoverssm_verify_qkv) and the
@@ -756,12 +695,6 @@ int plan_step(const kda_commit_args* c, const kda_plan_args* pl,
     plan->p.conv_elem = e;
   }
   return KDA_OK;
-}
-
-int device_status(int hip_rc, const char* what) {
-  if (hip_rc == 0) return KDA_OK;
-  return fail(KDA_E_DEVICE, "%s: HIP error %d (%s)", what, hip_rc,
-              hipGetErrorString(hipError_t(hip_rc)));
 }
 
 }  // namespace

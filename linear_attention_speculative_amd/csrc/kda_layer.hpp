@@ -1,0 +1,91 @@
+// Device pieces shared by the prefill and the decode of a KDA layer: the gate
+// and its decay to fp32 accuracy (a state carries the errors of hundreds of
+// decays, which the verify's few steps do not), and the short convolution.
+#pragma once
+
+#include "kda_device.hpp"
+#include "kda_internal.hpp"
+
+namespace kda {
+
+// e^x to about 1 ulp: the product x log2(e) is carried in two floats, since
+// the hardware exponential alone would turn its rounding into a relative
+// error of |x| ulp.
+__device__ __forceinline__ float exp_(float x) {
+  constexpr float kL = 1.44269502162933349609375f;   // log2(e), high part
+  constexpr float kLlo = 1.92596299112661746887e-8f;  // and the rest
+  constexpr float kLn2 = 0.693147180559945f;
+  const float t = x * kL;
+  const float r = __builtin_fmaf(x, kL, -t) + x * kLlo;
+  const float e = __builtin_amdgcn_exp2f(t);
+  // the correction is meaningless (inf - inf) where e has left the range
+  return e > 0.0f && e < __builtin_inff() ? __builtin_fmaf(e * r, kLn2, e)
+                                          : e;
+}
+
+__device__ __forceinline__ float sigmoid_(float x) {
+  return rcp_(1.0f + exp_(-x));
+}
+
+__device__ __forceinline__ float silu_(float x) {
+  // -inf * 0 would be NaN where the limit is 0
+  return x <= -88.0f ? x * 0.0f : x * sigmoid_(x);
+}
+
+// ln(1 + e) for 0 <= e <= 1, relative to its value: 2 atanh(e / (2 + e)),
+// whose series in z^2 <= 1/9 is below half an ulp after eight terms.
+__device__ __forceinline__ float log1p_(float e) {
+  const float z = e * rcp_(2.0f + e);
+  const float s = z * z;
+  float p = 1.0f / 15.0f;
+  p = __builtin_fmaf(p, s, 1.0f / 13.0f);
+  p = __builtin_fmaf(p, s, 1.0f / 11.0f);
+  p = __builtin_fmaf(p, s, 1.0f / 9.0f);
+  p = __builtin_fmaf(p, s, 1.0f / 7.0f);
+  p = __builtin_fmaf(p, s, 1.0f / 5.0f);
+  p = __builtin_fmaf(p, s, 1.0f / 3.0f);
+  p = __builtin_fmaf(p, s, 1.0f);
+  return 2.0f * z * p;
+}
+
+// Log-decay of one channel (the verify's kda_gate): bounded, or -A softplus,
+// with softplus the identity above 20 and max(x, 0) + ln(1 + e^-|x|) below,
+// which keeps its relative accuracy where it is small.
+__device__ __forceinline__ float layer_gate(float x, float A, bool use_lb,
+                                            float lb) {
+  if (use_lb) return lb * sigmoid_(A * x);
+  const float sp =
+      x > 20.0f ? x : fmaxf(x, 0.0f) + log1p_(exp_(-fabsf(x)));
+  return -A * sp;
+}
+
+// Inputs, parameters and pools of one layer.  Strides in elements.
+struct LayerParams {
+  const void* mixed_qkv;    // [T, 3HD]
+  const void* raw_gate;     // [T, HD]
+  const void* raw_beta;     // [T, H]
+  const float* A_log;       // [H]
+  const float* dt_bias;     // [H, D]
+  float* state;             // [N, H, D, D]
+  void* out;                // [T, HD]
+  void* conv_state;         // conv: [N, 3HD, Lc] seen dim-first
+  const void* conv_weight;  // conv: [3HD, W]
+  int64_t s_x, s_g, s_beta, s_out, s_slot;
+  int64_t s_cs_slot, s_cs_chan, s_cs_tok, s_w_chan, s_w_tap;
+  const int32_t* slots;     // [B]
+  const int32_t* accepted;  // [B] or null (1)
+  int32_t B, H, N, Q, null_id;
+  int32_t flags;            // kOutBf16 | kWBf16 | kLowerBound | kNoConv
+  float lb;
+};
+
+__device__ __forceinline__ bool live_slot(const LayerParams& p, int slot) {
+  return slot > p.null_id && slot >= 0 && slot < p.N;
+}
+
+// Offset of the oldest of the three history inputs in a slot's conv rows.
+__device__ __forceinline__ int history_at(const LayerParams& p, int b) {
+  return (p.accepted ? min(max(p.accepted[b], 1), p.Q) : 1) - 1;
+}
+
+}  // namespace kda

@@ -1,0 +1,183 @@
+"""Python binding of the operators around the verify in a serving step:
+single-token decode and the step's index tables.
+
+Argument marshalling only, as in `ops`; every computation runs in the HIP
+library.  Beyond the library's own checks these functions check what the C
+ABI cannot see: that every tensor lives on one GPU (the launch is made with
+that device current, on its current stream unless one is given) and that
+index arrays are int32, contiguous and long enough.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from . import _abi
+from .ops import (_pack_format, _ptr, _raise, _tensor_values)
+
+
+def _on_device(tensors) -> torch.device:
+    """The GPU that holds all of `tensors` (None entries are skipped)."""
+    device = None
+    for t in tensors:
+        if t is None:
+            continue
+        if device is None:
+            device = t.device
+        if t.device != device:
+            raise ValueError(f"tensors on {device} and {t.device}")
+    if device is None or device.type != "cuda":
+        raise ValueError("the tensors must be on a GPU")
+    return device
+
+
+def _launch(entry, args, tensors, stream) -> None:
+    device = _on_device(tensors)
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
+        raise ValueError(f"a stream of {stream.device} for tensors on "
+                         f"{device}")
+    with torch.cuda.device(device):
+        if stream is None:
+            stream = torch.cuda.current_stream(device)
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) \
+            else int(stream)
+        rc = entry(ctypes.byref(args), handle)
+    if rc != _abi.KDA_OK:
+        _raise(rc)
+
+
+def _ints(t, name: str, size: int, *, exact=False) -> int:
+    """Pointer of an int32 index array of at least `size` entries (0 for
+    None)."""
+    if t is None:
+        return 0
+    if t.dim() != 1 or t.numel() < size or (exact and t.numel() != size):
+        raise ValueError(f"{name} needs {size} entries (got "
+                         f"{list(t.shape)})")
+    return _ptr(t) or 0
+
+
+_LAYER = ("mixed_qkv", "raw_gate", "raw_beta", "A_log", "dt_bias", "state",
+          "out", "conv_state", "conv_weight")
+_DECODE_PACK = struct.Struct("<" + _pack_format(_abi.KdaDecodeArgs))
+
+
+def _layer_values(kw) -> list:
+    return [v for name in _LAYER for v in _tensor_values(kw[name])]
+
+
+def decode_args(*, mixed_qkv, raw_gate, raw_beta, A_log, dt_bias,
+                lower_bound, state, out, state_indices, conv_state=None,
+                conv_weight=None, spec_query_len=1, conv_dim_first=True,
+                final_state_indices=None, num_accepted_tokens=None,
+                null_block_id=0) -> _abi.KdaDecodeArgs:
+    """kda_decode_args for these tensors."""
+    kw = dict(locals())
+    B = state_indices.shape[0]
+    vals = (*_layer_values(kw), _ints(state_indices, "state_indices", B),
+            _ints(final_state_indices, "final_state_indices", B),
+            _ints(num_accepted_tokens, "num_accepted_tokens", B),
+            B, spec_query_len, null_block_id, 1 if conv_dim_first else 0,
+            0 if lower_bound is None else 1,
+            0.0 if lower_bound is None else float(lower_bound))
+    return _abi.KdaDecodeArgs.from_buffer_copy(_DECODE_PACK.pack(*vals))
+
+
+def _tensors(kw):
+    return [v for v in kw.values() if isinstance(v, torch.Tensor)]
+
+
+def check_decode(**kwargs) -> int:
+    """Host-only validation (no launch); returns the kda_status code."""
+    return _abi.load().kda_check_decode(ctypes.byref(decode_args(**kwargs)))
+
+
+def conv_update_decode(*, stream=None, **kwargs) -> None:
+    """One token per request of one KDA layer, with the short convolution
+    fused: row b of the activations advances request b's checkpoint from
+    `state_indices[b]` to `final_state_indices[b]` (default: in place), and
+    its conv history with it.  Arguments follow kda_decode_args in
+    include/kda_recoverssm.h; `lower_bound=None` selects the softplus gate,
+    `num_accepted_tokens=None` reads histories at offset 0."""
+    _launch(_abi.load().kda_conv_update_decode, decode_args(**kwargs),
+            _tensors(kwargs), stream)
+
+
+def _no_conv(kwargs):
+    for name in ("conv_state", "conv_weight", "num_accepted_tokens"):
+        if kwargs.get(name) is not None:
+            raise ValueError(f"{name} is not used on convolved q|k|v")
+
+
+def check_decode_qkv(**kwargs) -> int:
+    """Host-only validation of the unfused decode (no launch)."""
+    _no_conv(kwargs)
+    return _abi.load().kda_check_decode_qkv(
+        ctypes.byref(decode_args(**kwargs)))
+
+
+def decode_qkv(*, stream=None, **kwargs) -> None:
+    """`conv_update_decode` on already convolved q | k | v (no conv state,
+    taps or accepted counts)."""
+    _no_conv(kwargs)
+    _launch(_abi.load().kda_decode_qkv, decode_args(**kwargs),
+            _tensors(kwargs), stream)
+
+
+_TABLES_PACK = struct.Struct("<" + _pack_format(_abi.KdaTablesArgs))
+
+
+def tables_args(*, query_lens, num_computed_tokens, num_blocks, block_table,
+                free_blocks, block_size, query_start_loc, new_num_blocks,
+                state_indices, initial_state_indices, final_state_indices,
+                positions, slot_mapping, num_allocated, request_indices=None,
+                null_block_id=0) -> _abi.KdaTablesArgs:
+    """kda_tables_args for these tensors."""
+    B = query_lens.shape[0]
+    if block_table.dim() != 2 or block_table.dtype != torch.int32:
+        raise ValueError("block_table must be a two-dimensional int32 tensor")
+    rows, width = block_table.shape
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    if not slot_mapping.is_contiguous() or slot_mapping.dim() != 1 or \
+            slot_mapping.shape != positions.shape:
+        raise ValueError("positions and slot_mapping must be contiguous "
+                         "vectors of one size")
+    if request_indices is None and rows < B:
+        raise ValueError("without request_indices the tables need a row per "
+                         "request")
+    vals = (_ints(query_lens, "query_lens", B),
+            _ints(num_computed_tokens, "num_computed_tokens", rows),
+            _ints(num_blocks, "num_blocks", rows),
+            _ints(request_indices, "request_indices", B),
+            _ints(free_blocks, "free_blocks", 0), block_table.data_ptr(),
+            *block_table.stride(), B, rows, width, block_size,
+            free_blocks.shape[0], positions.shape[0], null_block_id, 0,
+            _ints(query_start_loc, "query_start_loc", B + 1),
+            _ints(new_num_blocks, "new_num_blocks", rows),
+            _ints(state_indices, "state_indices", B),
+            _ints(initial_state_indices, "initial_state_indices", B),
+            _ints(final_state_indices, "final_state_indices", B),
+            _ints(positions, "positions", 0), slot_mapping.data_ptr(),
+            _ints(num_allocated, "num_allocated", 1))
+    return _abi.KdaTablesArgs.from_buffer_copy(_TABLES_PACK.pack(*vals))
+
+
+def check_step_tables(**kwargs) -> int:
+    """Host-only validation (no launch); returns the kda_status code."""
+    return _abi.load().kda_check_step_tables(
+        ctypes.byref(tables_args(**kwargs)))
+
+
+def step_tables(*, stream=None, **kwargs) -> None:
+    """The index arrays of one serving step, built on the GPU from request
+    lengths (kda_tables_args in include/kda_recoverssm.h): token offsets, new
+    blocks from `free_blocks` appended to the rows of `block_table`, the
+    state slots that prefill, decode and verify read and write, and each
+    token's position and cache slot.  `num_allocated` receives how many
+    blocks the step asked for; more than `free_blocks` holds means that some
+    requests got null blocks."""
+    _launch(_abi.load().kda_step_tables, tables_args(**kwargs),
+            _tensors(kwargs), stream)

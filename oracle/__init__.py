@@ -36,3 +36,7 @@ from .kda import (  # noqa: F401
     silu,
     verify_qkv,
 )
+from .serving import (  # noqa: F401
+    layer_tokens,
+    step_tables,
+)
