@@ -32,8 +32,10 @@
  *   kda_recoverssm_commit_step -- those three (plan, compaction, commit)
  *       with the same results, in one launch.
  *
- *   kda_conv_update_decode -- the layer on single tokens: one step of the
- *       recurrence on the checkpoints that the verify starts from.
+ *   kda_conv_prefill, kda_conv_update_decode -- the layer on prompts (the
+ *       chunked form, from a zero or given state) and on single tokens (the
+ *       recurrent form), which produce and advance the checkpoints that the
+ *       verify starts from.
  *
  *   kda_step_tables -- a step's index arrays built on the GPU from request
  *       lengths: token offsets, new blocks, state slots, cache slots.
@@ -330,6 +332,52 @@ typedef struct {
   const int32_t* boundary_recovery_lens;
 } kda_compact_args;
 
+/* Arguments of kda_conv_prefill and kda_prefill_qkv: the KDA layer over whole
+   prompts, B requests of any lengths laid end to end in T token rows.  Per
+   request and head, from S_0 (the initial slot's state, or zero), with
+   q, k, v, g, beta formed exactly as in the verify:
+     c_t = beta_t (v_t - S_{t-1} diag(e^g_t) k_hat_t),
+     S_t = S_{t-1} diag(e^g_t) + c_t k_hat_t^T,  out_t = S_t q_t.
+   The last state goes to the request's state slot and, with the fused conv,
+   its last three raw inputs to entries [0, 3) of that slot's conv state (read
+   back with accepted count 1); other entries stay. */
+typedef struct {
+  kda_tensor mixed_qkv;    /* act [T, 3HD]: raw q|k|v (kda_conv_prefill) or
+                              convolved q|k|v (kda_prefill_qkv) */
+  kda_tensor raw_gate;     /* act [T, HD] */
+  kda_tensor raw_beta;     /* act [T, H] */
+  kda_tensor A_log;        /* F32 [H], contiguous */
+  kda_tensor dt_bias;      /* F32 [H, D] (or [H*D]), contiguous */
+  kda_tensor state;        /* F32 [N, H, D(v), D(k)], as for the verify */
+  kda_tensor out;          /* F32 or act [T, HD] */
+  kda_tensor conv_state;   /* act; as for the verify (conv only) */
+  kda_tensor conv_weight;  /* F32 or act [3HD, W] (conv only) */
+  const int32_t* query_start_loc;       /* [batch+1] token offsets, clamped
+                                           to [0, T]; not decreasing */
+  const int32_t* state_indices;         /* [batch] slots that receive the
+                                           states; a request whose slot is
+                                           null gets +0.0 outputs and
+                                           nothing else */
+  const int32_t* initial_state_indices; /* [batch] slots the requests start
+                                           from (state and conv history), a
+                                           null slot meaning zeros; may name
+                                           the request's own slot.  NULL:
+                                           every request starts from zero */
+  const int32_t* num_accepted_tokens;   /* [batch] conv history offset + 1 in
+                                           the initial slot, clamped to
+                                           [1, Q], or NULL: 1 */
+  void* workspace;         /* device, 16-byte aligned, at least
+                              kda_prefill_workspace_size(...) bytes; not
+                              shared by launches in flight together */
+  int64_t workspace_bytes;
+  int32_t batch;
+  int32_t spec_query_len;  /* Q: the conv state holds Q + 2 entries */
+  int32_t null_block_id;
+  int32_t conv_dim_first;
+  int32_t use_lower_bound;
+  float lower_bound;
+} kda_prefill_args;
+
 /* Arguments of kda_conv_update_decode and kda_decode_qkv: one token for each
    of `batch` requests (row b of the activations is request b's), one step of
    the recurrence from the request's state slot, with q, k, v, g, beta formed
@@ -498,6 +546,23 @@ int kda_recoverssm_commit_step(const kda_commit_args* commit,
                                const kda_plan_args* plan,
                                const kda_compact_args* compact,
                                void* stream);
+
+/* Bytes of workspace that a prefill of `tokens` rows and `batch` requests
+   needs (0 for sizes that the checks refuse); the activation dtype is
+   act_dtype, out's is out_dtype (kda_dtype). */
+int64_t kda_prefill_workspace_size(int64_t tokens, int64_t batch,
+                                   int64_t num_heads, int64_t head_dim,
+                                   int32_t act_dtype, int32_t out_dtype);
+
+/* Host-only validation of prefill arguments, then the launches (two kernels
+   on `stream`): with the fused short convolution, or on convolved q|k|v
+   (conv_state, conv_weight and num_accepted_tokens are then not used).  A
+   request's state slot must not be another request's state or initial
+   slot. */
+int kda_check_prefill(const kda_prefill_args* args);
+int kda_conv_prefill(const kda_prefill_args* args, void* stream);
+int kda_check_prefill_qkv(const kda_prefill_args* args);
+int kda_prefill_qkv(const kda_prefill_args* args, void* stream);
 
 /* Host-only validation of decode arguments, then the launch (one kernel).  A
    request's final slot must not be another request's state or final slot. */

@@ -22,10 +22,16 @@ from .ops import (  # noqa: F401
 from .serving import (  # noqa: F401
     check_decode,
     check_decode_qkv,
+    check_prefill,
+    check_prefill_qkv,
     check_step_tables,
+    conv_prefill,
     conv_update_decode,
     decode_args,
     decode_qkv,
+    prefill_args,
+    prefill_qkv,
+    prefill_workspace_size,
     step_tables,
     tables_args,
 )

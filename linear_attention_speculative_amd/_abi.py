@@ -37,6 +37,8 @@ EXPORTED = (
     "kda_check_compact_conv", "kda_compact_conv_state",
     "kda_check_commit_step", "kda_recoverssm_commit_step",
     "kda_reset_counter", "kda_set_launch_events",
+    "kda_prefill_workspace_size", "kda_check_prefill", "kda_conv_prefill",
+    "kda_check_prefill_qkv", "kda_prefill_qkv",
     "kda_check_decode", "kda_conv_update_decode",
     "kda_check_decode_qkv", "kda_decode_qkv",
     "kda_check_step_tables", "kda_step_tables",
@@ -132,6 +134,15 @@ _LAYER_SCALARS = [
     ("use_lower_bound", c_int32), ("lower_bound", c_float)]
 
 
+class KdaPrefillArgs(Structure):
+    _fields_ = _LAYER_TENSORS + [
+        ("query_start_loc", c_void_p), ("state_indices", c_void_p),
+        ("initial_state_indices", c_void_p),
+        ("num_accepted_tokens", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_int64),
+    ] + _LAYER_SCALARS
+
+
 class KdaDecodeArgs(Structure):
     _fields_ = _LAYER_TENSORS + [
         ("state_indices", c_void_p), ("final_state_indices", c_void_p),
@@ -214,7 +225,11 @@ def load() -> ctypes.CDLL:
     lib.kda_set_launch_events.restype = c_int
     lib.kda_set_launch_events.argtypes = [c_void_p, c_void_p, c_int32,
                                           POINTER(c_int32)]
+    lib.kda_prefill_workspace_size.restype = c_int64
+    lib.kda_prefill_workspace_size.argtypes = [c_int64] * 4 + [c_int32] * 2
     for check, launches, args in (
+            ("kda_check_prefill", ("kda_conv_prefill",), KdaPrefillArgs),
+            ("kda_check_prefill_qkv", ("kda_prefill_qkv",), KdaPrefillArgs),
             ("kda_check_decode", ("kda_conv_update_decode",), KdaDecodeArgs),
             ("kda_check_decode_qkv", ("kda_decode_qkv",), KdaDecodeArgs),
             ("kda_check_step_tables", ("kda_step_tables",), KdaTablesArgs)):

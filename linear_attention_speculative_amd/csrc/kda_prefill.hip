@@ -1,0 +1,746 @@
+// KDA layer over prompts for gfx950, in the chunked form: chunks of C = 32
+// tokens turn the token-by-token recurrence into matrix products.
+//
+// Inside a chunk, with G_t the sum of the log-decays up to token t (per
+// channel), k_t and q_t normalised, and S_0 the state before the chunk:
+//   A_tj = sum_k k_tk k_jk e^(G_tk - G_jk)  (j < t)
+//   B_tj = sum_k q_tk k_jk e^(G_tk - G_jk)  (j <= t)
+//   T    = (I + diag(beta) A)^-1 diag(beta)
+//   c    = T (V - (k e^G) S_0^T)            corrections of all 32 tokens
+//   O    = (q e^G) S_0^T + B c
+//   S_C  = S_0 diag(e^G_C) + c^T (k e^(G_C - G))
+// Only the last three lines need S_0.  So two kernels:
+//
+//   kda_prefill_chunk_kernel: one workgroup per (chunk, head), all chunks at
+//   once: convolution, norms, gates, A, B, T and the scaled k and q, written
+//   to the workspace in the order in which the second kernel's lanes hold
+//   matrix operands (one 16-byte load per lane and operand).
+//
+//   kda_prefill_state_kernel: one wave per (request, head, 16 state rows),
+//   chunk after chunk.  The rows v of the state never mix, so a wave keeps
+//   its 16 rows for all channels in 4 D/16 registers per lane and needs
+//   neither LDS nor barriers: the result layout of one product (column on
+//   lane % 16, four rows per lane group) serves as the right operand of the
+//   next one if the summed index is taken in the order
+//   4 g + e (e < 4), 16 + 4 g + e - 4, g = lane / 16, on both sides.
+//
+// Decays never divide: every exponent above is a sum over tokens between j
+// and t, so each factor is at most 1, however strong the gates.  Within 16
+// tokens products e^(G_t - G_j) are carried from j to t by multiplication;
+// the block of later rows and earlier columns splits at its border into two
+// factors of at most 1 each, which a matrix product takes.
+//
+// Rounding: states, sums and the triangular inverse are fp32.  The operands
+// of the second kernel's products are pairs of fp16 (x = hi + lo, 22 bits)
+// under a power-of-two scale, three products each, which loses 2^-22 of a
+// term: fp32-like, at a third of the fp16 matrix rate instead of the
+// sixteenth that fp32 operands have.  k e^G and the like are at most 1 and
+// take the fixed scale 2^12; columns of S, V - ... and c take the scale that
+// puts their largest element near 2^13.  Products that only feed bf16
+// outputs take hi alone (2^-11 against the output's own 2^-9).
+#include "kda_serving.hpp"
+
+namespace kda {
+namespace {
+
+typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+typedef _Float16 h4 __attribute__((ext_vector_type(4)));
+
+constexpr int C = kChunk;
+constexpr int kSub = 16;             // tokens of a sub-block
+constexpr float kUnit = 4096.0f;     // scale of operands of at most 1
+constexpr int kFrag = 1024;          // bytes of one operand (64 lanes x 16)
+
+// Workspace of one (chunk slot, head): byte offsets of its operands.
+template <int D>
+struct Work {
+  static constexpr int KS = D >= 32 ? D / 32 : 1;  // channel steps of 32
+  static constexpr int MT = D / 16;                // state row tiles
+  static constexpr int kd = 0;                     // [2][KS] hi, lo
+  static constexpr int ke = kd + 2 * KS * 2 * kFrag;   // [MT] hi, lo
+  static constexpr int t = ke + MT * 2 * kFrag;        // [2] hi, lo
+  static constexpr int v = t + 2 * 2 * kFrag;          // [2][MT] fp32
+  static constexpr int gam = v + 2 * MT * kFrag;       // [D] fp32
+  static constexpr int qd = gam + (D * 4 + kFrag - 1) / kFrag * kFrag;
+  // q e^G [2][KS] and B [2]: hi, and lo for fp32 outputs
+  static constexpr int b(bool o32) { return qd + 2 * KS * kFrag * (o32 + 1); }
+  static constexpr int size(bool o32) { return b(o32) + 2 * kFrag * (o32 + 1); }
+};
+
+struct Split {
+  h8 hi, lo;
+};
+
+// Both halves are taken from one fp32 value.  It is made opaque first: where
+// the compiler sees the product that x comes from, it may round that product
+// to fp16 once, without the fp32 step, for one half and not for the other,
+// and in a tie hi + lo is then a whole fp16 step off.
+__device__ __forceinline__ Split split8(float (&x)[8]) {
+  Split s;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    asm("" : "+v"(x[e]));
+    s.hi[e] = _Float16(x[e]);
+    s.lo[e] = _Float16(x[e] - float(s.hi[e]));
+  }
+  return s;
+}
+
+__device__ __forceinline__ void store_frag(char* at, int lane, h8 v) {
+  *reinterpret_cast<h8*>(at + lane * 16) = v;
+}
+
+template <int D, bool BF16>
+struct Pair;   // two neighbouring channels of an activation row
+template <int D>
+struct Pair<D, true> {
+  typedef uint32_t T;
+  static __device__ __forceinline__ float lo(T x) {
+    return __uint_as_float(x << 16);
+  }
+  static __device__ __forceinline__ float hi(T x) {
+    return __uint_as_float(x & 0xffff0000u);
+  }
+};
+template <int D>
+struct Pair<D, false> {
+  typedef float2 T;
+  static __device__ __forceinline__ float lo(T x) { return x.x; }
+  static __device__ __forceinline__ float hi(T x) { return x.y; }
+};
+
+constexpr int kThreads = 256;
+
+template <int D>
+struct ChunkCfg {
+  static constexpr int CP = D / 2;               // channel pairs
+  static constexpr int TG = kThreads / CP;       // token groups
+  static constexpr int NTK = C / TG;             // tokens per thread
+  static constexpr int RS = D + 4;               // padded row, floats
+  static constexpr int AS = C + 4;
+};
+
+template <int D>
+struct ChunkSmem {
+  using F = ChunkCfg<D>;
+  float k[C][F::RS];
+  float q[C][F::RS];
+  float p[C][F::RS];    // decays, then their products from the sub-block's
+                        // first token
+  float s[C][F::RS];    // products of the later decays of the sub-block
+  float a[C][F::AS];
+  float b[C][F::AS];
+  float t[C][F::AS];
+  float beta[C];
+  int req;
+};
+
+// Bounds of request b in the token rows, whatever the offsets hold.
+__device__ __forceinline__ int2 token_range(const PrefillParams& p, int b) {
+  const int bos = min(max(p.qsl[b], 0), p.T);
+  return make_int2(bos, min(max(p.qsl[b + 1], bos), p.T));
+}
+
+// First chunk slot of request b.  Slots of different requests are disjoint:
+// the next request starts at least ceil(length / C) later.
+__device__ __forceinline__ int first_slot(int bos, int b) {
+  return bos / C + b;
+}
+
+template <int D, bool BF16, bool O32>
+__global__ void __launch_bounds__(kThreads)
+    kda_prefill_chunk_kernel(PrefillParams p) {
+  using F = ChunkCfg<D>;
+  using W = Work<D>;
+  using P2 = Pair<D, BF16>;
+  typedef typename Act<BF16>::T T;
+  extern __shared__ __align__(16) char smem[];
+  ChunkSmem<D>& m = *reinterpret_cast<ChunkSmem<D>*>(smem);
+  const LayerParams& y = p.y;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int slot = blockIdx.x / y.H, h = blockIdx.x - slot * y.H;
+
+  // the request of this chunk slot
+  if (tid == 0) m.req = -1;
+  for (int i = tid; i < 2 * C * F::AS; i += kThreads) (&m.a[0][0])[i] = 0.0f;
+  __syncthreads();
+  for (int b = tid; b < y.B; b += kThreads) {
+    const int2 r = token_range(p, b);
+    const int f = first_slot(r.x, b);
+    if (slot >= f && slot < f + (r.y - r.x + C - 1) / C) m.req = b;
+  }
+  __syncthreads();
+  const int b = m.req;
+  if (b < 0 || !live_slot(y, y.slots[b])) return;
+  const int2 range = token_range(p, b);
+  const int first = (slot - first_slot(range.x, b)) * C;   // in the request
+  const int t0 = range.x + first, n = min(C, range.y - t0);
+  char* work = p.work + (int64_t(slot) * y.H + h) * W::size(O32);
+
+  // ---- activations: convolution, norms, gates ----
+  const int cp = tid % F::CP, tg = tid / F::CP;
+  const int64_t HD = int64_t(y.H) * D, ch = int64_t(h) * D + 2 * cp;
+  const bool conv = !(y.flags & kNoConv);
+  float val[3][F::NTK][2];
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+    const int64_t c0 = part * HD + ch;
+    const T* col = static_cast<const T*>(y.mixed_qkv) + c0;
+    float x[F::NTK + 3][2];
+#pragma unroll
+    for (int i = 0; i < F::NTK + 3; ++i) {
+      const int t = tg * F::NTK + i - 3;      // token in the chunk
+      x[i][0] = x[i][1] = 0.0f;
+      if ((i >= 3 || conv) && first + t >= 0 && t < n) {
+        const typename P2::T r = *reinterpret_cast<const typename P2::T*>(
+            col + int64_t(t0 + t) * y.s_x);
+        x[i][0] = P2::lo(r);
+        x[i][1] = P2::hi(r);
+      }
+    }
+    if (conv) {
+      if (first == 0 && tg * F::NTK < 3 && p.initial &&
+          live_slot(y, p.initial[b])) {
+        const T* cs = static_cast<const T*>(y.conv_state) +
+                      p.initial[b] * y.s_cs_slot + c0 * y.s_cs_chan;
+        const int at = history_at(y, b);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int t = tg * F::NTK + i - 3;
+          if (t < 0) {
+            x[i][0] = Act<BF16>::f(cs[(at + t + 3) * y.s_cs_tok]);
+            x[i][1] = Act<BF16>::f(cs[y.s_cs_chan + (at + t + 3) * y.s_cs_tok]);
+          }
+        }
+      }
+      float w[2][kConvWidth];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int i = 0; i < kConvWidth; ++i)
+          w[e][i] = ld_elem(y.conv_weight,
+                            (c0 + e) * y.s_w_chan + i * y.s_w_tap,
+                            y.flags & kWBf16);
+#pragma unroll
+      for (int i = 0; i < F::NTK; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float acc = w[e][0] * x[i][e];
+          acc = __builtin_fmaf(w[e][1], x[i + 1][e], acc);
+          acc = __builtin_fmaf(w[e][2], x[i + 2][e], acc);
+          acc = __builtin_fmaf(w[e][3], x[i + 3][e], acc);
+          val[part][i][e] = silu_(acc);
+        }
+    } else {
+#pragma unroll
+      for (int i = 0; i < F::NTK; ++i)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) val[part][i][e] = x[i + 3][e];
+    }
+  }
+  const float A = exp_(y.A_log[h]);
+  const float2 bias = *reinterpret_cast<const float2*>(y.dt_bias + ch);
+  const T* gcol = static_cast<const T*>(y.raw_gate) + ch;
+#pragma unroll
+  for (int i = 0; i < F::NTK; ++i) {
+    const int t = tg * F::NTK + i;
+    const bool in = t < n;
+    float a0 = 1.0f, a1 = 1.0f;
+    if (in) {
+      const typename P2::T r = *reinterpret_cast<const typename P2::T*>(
+          gcol + int64_t(t0 + t) * y.s_g);
+      a0 = exp_(layer_gate(P2::lo(r) + bias.x, A, y.flags & kLowerBound,
+                           y.lb));
+      a1 = exp_(layer_gate(P2::hi(r) + bias.y, A, y.flags & kLowerBound,
+                           y.lb));
+    }
+    float q0 = val[0][i][0], q1 = val[0][i][1];
+    float k0 = val[1][i][0], k1 = val[1][i][1];
+    float qq = q0 * q0 + q1 * q1, kk = k0 * k0 + k1 * k1;
+    if constexpr (F::CP == 64) {
+      qq = wave_sum(qq);
+      kk = wave_sum(kk);
+    } else {
+      qq = group_sum<F::CP>(qq);
+      kk = group_sum<F::CP>(kk);
+    }
+    const float nq = in ? 1.0f / (sqrtf(qq + kNormEps) * sqrtf(float(D))) : 0;
+    const float nk = in ? 1.0f / sqrtf(kk + kNormEps) : 0;
+    *reinterpret_cast<float2*>(&m.q[t][2 * cp]) =
+        in ? make_float2(q0 * nq, q1 * nq) : make_float2(0, 0);
+    *reinterpret_cast<float2*>(&m.k[t][2 * cp]) =
+        in ? make_float2(k0 * nk, k1 * nk) : make_float2(0, 0);
+    *reinterpret_cast<float2*>(&m.p[t][2 * cp]) = make_float2(a0, a1);
+    // V as the second kernel's accumulators hold it
+    float* vf = reinterpret_cast<float*>(work + W::v);
+    const int r = t / kSub, g = (t % kSub) / 4;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int d = 2 * cp + e;
+      vf[((r * W::MT + d / 16) * 64 + g * 16 + d % 16) * 4 + t % 4] =
+          in ? val[2][i][e] : 0.0f;
+    }
+  }
+  if (tid < C)
+    m.beta[tid] =
+        tid < n ? sigmoid_(Act<BF16>::f(static_cast<const T*>(
+                      y.raw_beta)[int64_t(t0 + tid) * y.s_beta + h]))
+                : 0.0f;
+  __syncthreads();
+
+  // ---- A and B inside each sub-block: waves 2 sb + half; a lane takes four
+  // columns j and D/32 channels, and carries k_j e^(G_i - G_j) from row to
+  // row ----
+  {
+    constexpr int CH = D >= 32 ? D / 32 : 1;
+    const int sb = wave >> 1, cl = lane & 31;
+    const int jg = (wave & 1) ? 1 + (lane >> 5) : 3 * (lane >> 5);
+    const int r0 = sb * kSub;
+    const bool on = cl * CH < D;
+    const int c0 = on ? cl * CH : 0;
+    float kd[4][CH] = {};
+#pragma unroll 2
+    for (int i = (wave & 1) ? 4 : 0; i < kSub; ++i) {
+      float ai[CH], ki[CH], qi[CH];
+#pragma unroll
+      for (int e = 0; e < CH; ++e) {
+        ai[e] = m.p[r0 + i][c0 + e];
+        ki[e] = on ? m.k[r0 + i][c0 + e] : 0.0f;
+        qi[e] = on ? m.q[r0 + i][c0 + e] : 0.0f;
+      }
+      float sum[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        sum[j] = sum[4 + j] = 0.0f;
+#pragma unroll
+        for (int e = 0; e < CH; ++e) {
+          kd[j][e] = i == 4 * jg + j ? ki[e] : kd[j][e] * ai[e];
+          sum[j] = __builtin_fmaf(ki[e], kd[j][e], sum[j]);
+          sum[4 + j] = __builtin_fmaf(qi[e], kd[j][e], sum[4 + j]);
+        }
+      }
+      float tot = transpose_sum<16, 8>(sum, lane & 15);
+      tot += __int_as_float(
+          __builtin_amdgcn_ds_swizzle(__float_as_int(tot), 0x401F));
+      const int v = (lane & 15) >> 1, j = 4 * jg + (v & 3);
+      if ((lane & 17) == 0) {
+        if (v >= 4)
+          m.b[r0 + i][r0 + j] = tot;
+        else
+          m.a[r0 + i][r0 + j] = i > j ? tot : 0.0f;
+      }
+    }
+  }
+  // products of decays from the sub-block's start, and to its end
+  float pre[kSub], suf[kSub];
+  const int pc = tid % D, pb = tid / D;       // channel, sub-block
+  if (pb < 2) {
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) pre[i] = m.p[pb * kSub + i][pc];
+    suf[kSub - 1] = 1.0f;
+#pragma unroll
+    for (int i = kSub - 2; i >= 0; --i) suf[i] = suf[i + 1] * pre[i + 1];
+#pragma unroll
+    for (int i = 1; i < kSub; ++i) pre[i] *= pre[i - 1];
+  }
+  __syncthreads();
+  if (pb < 2) {
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+      m.p[pb * kSub + i][pc] = pre[i];
+      m.s[pb * kSub + i][pc] = suf[i];
+    }
+  }
+  __syncthreads();
+
+  const int col = lane & 15, g = lane >> 4;
+  if (wave < 2) {
+    // the block of rows 16.. and columns ..15, of A (wave 0) or B (wave 1)
+    float (*rows)[F::RS] = wave == 0 ? m.k : m.q;
+    f4 acc = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int s = 0; s < D / 4; ++s) {
+      const int c = 4 * s + g;
+      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
+          rows[kSub + col][c] * m.p[kSub + col][c], m.k[col][c] * m.s[col][c],
+          acc, 0, 0, 0);
+    }
+    float (*dst)[F::AS] = wave == 0 ? m.a : m.b;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dst[kSub + 4 * g + i][col] = acc[i];
+  }
+  __syncthreads();
+
+  if (wave == 0) {
+    // T: the two diagonal inverses by substitution (lane = column), then the
+    // block below them, -X2 (beta A21) X1, by products
+    const int blk = (lane >> 4) & 1, r0 = blk * kSub;
+    float x[kSub];
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) {
+      float acc = 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j)
+        acc = __builtin_fmaf(m.a[r0 + i][r0 + j], x[j], acc);
+      x[i] = (i == col ? 1.0f : 0.0f) - m.beta[r0 + i] * acc;
+    }
+    if (lane < 32) {
+#pragma unroll
+      for (int i = 0; i < kSub; ++i)
+        m.t[r0 + i][r0 + col] = blk ? x[i] : x[i] * m.beta[col];
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local");
+    f4 yv = {0, 0, 0, 0}, z = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+      yv = __builtin_amdgcn_mfma_f32_16x16x4f32(
+          m.beta[kSub + col] * m.a[kSub + col][4 * s + g], m.t[4 * s + g][col],
+          yv, 0, 0, 0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)       // summed index 4 g + s on both sides
+      z = __builtin_amdgcn_mfma_f32_16x16x4f32(
+          m.t[kSub + col][kSub + 4 * g + s], yv[s], z, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m.t[kSub + 4 * g + i][col] = -z[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local");
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = kUnit * m.t[r * kSub + col][4 * g + e];
+        v[4 + e] = r == 0 ? 0.0f
+                          : kUnit * m.t[kSub + col][kSub + 4 * g + e] *
+                                m.beta[kSub + 4 * g + e];
+      }
+      const Split s = split8(v);
+      store_frag(work + W::t + 2 * r * kFrag, lane, s.hi);
+      store_frag(work + W::t + (2 * r + 1) * kFrag, lane, s.lo);
+    }
+  } else if (wave == 1) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = kUnit * m.b[r * kSub + col][4 * g + e];
+        v[4 + e] = r == 0 ? 0.0f : kUnit * m.b[kSub + col][kSub + 4 * g + e];
+      }
+      const Split s = split8(v);
+      store_frag(work + W::b(O32) + r * (O32 + 1) * kFrag, lane, s.hi);
+      if (O32)
+        store_frag(work + W::b(O32) + (r * 2 + 1) * kFrag, lane, s.lo);
+    }
+  }
+  // scaled k and q: waves 2 and 3 alone, as long as the others have the
+  // inverse and the causal block
+  constexpr int NKD = 2 * W::KS;
+  for (int task = wave - 2; task >= 0 && task < NKD + W::MT; task += 2) {
+    float x[8], z[8];
+    if (task < NKD) {
+      const int r = task / W::KS, s = task - r * W::KS, t = r * kSub + col;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = 32 * s + (e < 4 ? 4 * g + e : 16 + 4 * g + e - 4);
+        x[e] = z[e] = 0.0f;
+        if (c < D) {
+          const float d =
+              kUnit * m.p[t][c] * (r ? m.p[kSub - 1][c] : 1.0f);
+          x[e] = m.k[t][c] * d;
+          z[e] = m.q[t][c] * d;
+        }
+      }
+      const Split a = split8(x), q = split8(z);
+      store_frag(work + W::kd + 2 * task * kFrag, lane, a.hi);
+      store_frag(work + W::kd + (2 * task + 1) * kFrag, lane, a.lo);
+      store_frag(work + W::qd + task * (O32 + 1) * kFrag, lane, q.hi);
+      if (O32) store_frag(work + W::qd + (2 * task + 1) * kFrag, lane, q.lo);
+    } else {
+      const int mt = task - NKD, c = 16 * mt + col;
+      const float late = m.p[C - 1][c];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int t = e < 4 ? 4 * g + e : kSub + 4 * g + e - 4;
+        x[e] = kUnit * m.k[t][c] * m.s[t][c] * (e < 4 ? late : 1.0f);
+      }
+      const Split a = split8(x);
+      store_frag(work + W::ke + 2 * mt * kFrag, lane, a.hi);
+      store_frag(work + W::ke + (2 * mt + 1) * kFrag, lane, a.lo);
+    }
+  }
+  if (tid < D)
+    reinterpret_cast<float*>(work + W::gam)[tid] =
+        m.p[kSub - 1][tid] * m.p[C - 1][tid];
+}
+
+// ---- second kernel ----------------------------------------------------------
+
+__device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ h8 frag(const char* at, int lane) {
+  return *reinterpret_cast<const h8*>(at + lane * 16);
+}
+
+// Largest value over the four lanes that share a column.
+__device__ __forceinline__ float column_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16));
+  return fmaxf(v, __shfl_xor(v, 32));
+}
+
+// The power of two that puts m (>= 0) into [2^13, 2^14), and its inverse; 1
+// where m is 0 or not finite.
+__device__ __forceinline__ void scale_of(float m, float& up, float& down) {
+  const int e = int(__float_as_uint(m) >> 23);        // biased exponent
+  const int s = e == 0 || e == 255 ? 0 : min(max(127 + 13 - e, -110), 110);
+  up = __uint_as_float(uint32_t(127 + s) << 23);
+  down = __uint_as_float(uint32_t(127 - s) << 23);
+}
+
+template <int D, bool O32, int WAVES>
+__global__ void __launch_bounds__(64 * WAVES)
+    kda_prefill_state_kernel(PrefillParams p, int act_bf16) {
+  using W = Work<D>;
+  const LayerParams& y = p.y;
+  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  // wave -> (request, head, tile): the tiles of a head on one XCD (blocks
+  // i, i + 8, ..), whose L2 then serves the head's operands to all of them
+  constexpr int TB = W::MT / WAVES;            // workgroups of a head
+  const int grp = blockIdx.x / (8 * TB), in = blockIdx.x - grp * (8 * TB);
+  const int item = grp * 8 + in % 8;
+  const int vt = (in / 8) * WAVES + (threadIdx.x >> 6);
+  if (item >= y.B * y.H) return;
+  const int b = item / y.H, h = item - b * y.H;
+  const int2 range = token_range(p, b);
+  const int L = range.y - range.x;
+  if (L == 0) return;
+  const int dst = y.slots[b];
+  const int64_t oc = int64_t(h) * D + vt * 16 + col;
+  if (!live_slot(y, dst)) {
+    for (int t = g; t < L; t += 4)
+      st_elem(y.out, (range.x + t) * y.s_out + oc, 0.0f, y.flags & kOutBf16);
+    return;
+  }
+  const int src = p.initial ? p.initial[b] : -1;
+  const bool from = live_slot(y, src);
+
+  f4 S[W::MT];      // S[m][i]: row v = col, channel 16 m + 4 g + i
+  const int64_t so = (int64_t(h) * D + vt * 16 + col) * D + 4 * g;
+#pragma unroll
+  for (int m = 0; m < W::MT; ++m) {
+    S[m] = f4{0, 0, 0, 0};
+    if (from)
+      S[m] = *reinterpret_cast<const f4*>(y.state + src * y.s_slot + so +
+                                          16 * m);
+  }
+  const int64_t step = int64_t(y.H) * W::size(O32);
+  const char* work =
+      p.work +
+      (int64_t(first_slot(range.x, b)) * y.H + h) * W::size(O32);
+  for (int t0 = 0; t0 < L; t0 += C, work += step) {
+    // S as the right operand: two 16-channel tiles make one step of 32
+    float top = 0.0f;
+#pragma unroll
+    for (int m = 0; m < W::MT; ++m)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(S[m][i]));
+    float up, down;
+    scale_of(column_max(top), up, down);
+    Split s[W::KS];
+#pragma unroll
+    for (int k = 0; k < W::KS; ++k) {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int m = 2 * k + (e >> 2);
+        x[e] = m < W::MT ? S[m < W::MT ? m : 0][e & 3] * up : 0.0f;
+      }
+      s[k] = split8(x);
+    }
+    down *= 1.0f / kUnit;
+    f4 r[2], o[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      f4 acc = {0, 0, 0, 0}, out = {0, 0, 0, 0};
+#pragma unroll
+      for (int k = 0; k < W::KS; ++k) {
+        const char* at = work + W::kd + 2 * (i * W::KS + k) * kFrag;
+        const h8 hi = frag(at, lane), lo = frag(at + kFrag, lane);
+        acc = mfma(hi, s[k].hi, acc);
+        acc = mfma(lo, s[k].hi, acc);
+        acc = mfma(hi, s[k].lo, acc);
+        const char* qa = work + W::qd + (i * W::KS + k) * (O32 + 1) * kFrag;
+        const h8 qh = frag(qa, lane);
+        out = mfma(qh, s[k].hi, out);
+        if (O32) {
+          out = mfma(frag(qa + kFrag, lane), s[k].hi, out);
+          out = mfma(qh, s[k].lo, out);
+        }
+      }
+      const f4 v = *reinterpret_cast<const f4*>(
+          work + W::v + (i * W::MT + vt) * kFrag + lane * 16);
+      r[i] = v - acc * down;
+      o[i] = out * down;
+    }
+    // c = T r
+    float top_r = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top_r = fmaxf(top_r, fabsf(r[i][e]));
+    scale_of(column_max(top_r), up, down);
+    down *= 1.0f / kUnit;
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = r[e >> 2][e & 3] * up;
+    const Split rs = split8(x);
+    float top_c = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const char* at = work + W::t + 2 * i * kFrag;
+      const h8 hi = frag(at, lane), lo = frag(at + kFrag, lane);
+      f4 acc = {0, 0, 0, 0};
+      acc = mfma(hi, rs.hi, acc);
+      acc = mfma(lo, rs.hi, acc);
+      acc = mfma(hi, rs.lo, acc);
+      r[i] = acc * down;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) top_c = fmaxf(top_c, fabsf(r[i][e]));
+    }
+    scale_of(column_max(top_c), up, down);
+    down *= 1.0f / kUnit;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = r[e >> 2][e & 3] * up;
+    const Split cs = split8(x);
+    // outputs
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const char* at = work + W::b(O32) + i * (O32 + 1) * kFrag;
+      const h8 hi = frag(at, lane);
+      f4 acc = {0, 0, 0, 0};
+      acc = mfma(hi, cs.hi, acc);
+      if (O32) {
+        acc = mfma(frag(at + kFrag, lane), cs.hi, acc);
+        acc = mfma(hi, cs.lo, acc);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = t0 + 16 * i + 4 * g + e;
+        if (t < L)
+          st_elem(y.out, (range.x + t) * y.s_out + oc,
+                  o[i][e] + acc[e] * down, y.flags & kOutBf16);
+      }
+    }
+    // the state behind the chunk
+#pragma unroll
+    for (int m = 0; m < W::MT; ++m) {
+      const char* at = work + W::ke + 2 * m * kFrag;
+      const h8 hi = frag(at, lane), lo = frag(at + kFrag, lane);
+      f4 acc = {0, 0, 0, 0};
+      acc = mfma(hi, cs.hi, acc);
+      acc = mfma(lo, cs.hi, acc);
+      acc = mfma(hi, cs.lo, acc);
+      const f4 gam = *reinterpret_cast<const f4*>(work + W::gam +
+                                                  (16 * m + 4 * g) * 4);
+      S[m] = S[m] * gam + acc * down;
+    }
+  }
+  float* to = y.state + dst * y.s_slot + so;
+#pragma unroll
+  for (int m = 0; m < W::MT; ++m) *reinterpret_cast<f4*>(to + 16 * m) = S[m];
+
+  if (vt == 0 && !(y.flags & kNoConv)) {
+    // the newest three raw inputs of the head's channels; each lane reads a
+    // channel's history before it writes the channel (the slots may be one)
+    const int at = history_at(y, b);
+    for (int j = lane; j < 3 * D; j += 64) {
+      const int part = j / D;
+      const int64_t c = part * (int64_t(y.H) * D) + int64_t(h) * D +
+                        (j - part * D);
+      uint32_t v[3];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int t = L - 3 + i;
+        v[i] = 0;
+        if (t >= 0) {
+          const int64_t e = int64_t(range.x + t) * y.s_x + c;
+          v[i] = act_bf16 ? static_cast<const uint16_t*>(y.mixed_qkv)[e]
+                          : static_cast<const uint32_t*>(y.mixed_qkv)[e];
+        } else if (from) {
+          const int64_t e = src * y.s_cs_slot + c * y.s_cs_chan +
+                            (at + t + 3) * y.s_cs_tok;
+          v[i] = act_bf16 ? static_cast<const uint16_t*>(y.conv_state)[e]
+                          : static_cast<const uint32_t*>(y.conv_state)[e];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int64_t e = dst * y.s_cs_slot + c * y.s_cs_chan +
+                          i * y.s_cs_tok;
+        if (act_bf16)
+          static_cast<uint16_t*>(y.conv_state)[e] = uint16_t(v[i]);
+        else
+          static_cast<uint32_t*>(y.conv_state)[e] = v[i];
+      }
+    }
+  }
+}
+
+template <int D, bool BF16, bool O32>
+int launch_prefill_dim(const PrefillParams& p, hipStream_t stream) {
+  const int64_t wgs = int64_t(p.n_slots) * p.y.H;
+  if (wgs > 0x7fffffff) return int(hipErrorInvalidValue);
+  const size_t lds = sizeof(ChunkSmem<D>);
+  auto chunk = kda_prefill_chunk_kernel<D, BF16, O32>;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(chunk),
+        hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+    if (e != hipSuccess) return int(e);
+  }
+  launch_kernel(chunk, dim3(uint32_t(wgs)), dim3(kThreads), lds, stream, p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return int(e);
+  const int64_t groups = (int64_t(p.y.B) * p.y.H + 7) / 8;
+  const int64_t blocks = groups * 8 * Work<D>::MT;
+  if (blocks > 0x7fffffff) return int(hipErrorInvalidValue);
+  launch_kernel(kda_prefill_state_kernel<D, O32, 1>, dim3(uint32_t(blocks)),
+                dim3(64), 0, stream, p, int(BF16));
+  return int(hipGetLastError());
+}
+
+template <int D>
+int launch_prefill_types(const PrefillParams& p, bool act_bf16,
+                         hipStream_t stream) {
+  const bool o32 = !(p.y.flags & kOutBf16);
+  if (act_bf16)
+    return o32 ? launch_prefill_dim<D, true, true>(p, stream)
+               : launch_prefill_dim<D, true, false>(p, stream);
+  return launch_prefill_dim<D, false, true>(p, stream);
+}
+
+}  // namespace
+
+int64_t prefill_slot_bytes(int D, bool out_f32) {
+  switch (D) {
+    case 16: return Work<16>::size(out_f32);
+    case 32: return Work<32>::size(out_f32);
+    case 64: return Work<64>::size(out_f32);
+    case 128: return Work<128>::size(out_f32);
+    default: return 0;
+  }
+}
+
+int launch_prefill(const PrefillParams& p, int D, bool act_bf16,
+                   hipStream_t stream) {
+  switch (D) {
+    case 16: return launch_prefill_types<16>(p, act_bf16, stream);
+    case 32: return launch_prefill_types<32>(p, act_bf16, stream);
+    case 64: return launch_prefill_types<64>(p, act_bf16, stream);
+    case 128: return launch_prefill_types<128>(p, act_bf16, stream);
+    default: return int(hipErrorInvalidValue);
+  }
+}
+
+}  // namespace kda

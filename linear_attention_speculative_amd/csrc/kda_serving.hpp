@@ -1,5 +1,5 @@
 // Launch descriptors of the serving-step operators around the verify:
-// decode and step tables.  Not part of the public ABI.
+// prefill, decode and step tables.  Not part of the public ABI.
 #pragma once
 
 #include "kda_layer.hpp"
@@ -12,6 +12,24 @@ struct DecodeParams {
 };
 int launch_decode(const DecodeParams& p, int D, bool act_bf16,
                   hipStream_t stream);
+
+struct PrefillParams {
+  LayerParams y;
+  const int32_t* qsl;        // [B + 1]
+  const int32_t* initial;    // [B] or null (zeros)
+  char* work;
+  int32_t T;
+  int32_t n_slots;           // chunk slots in the workspace
+};
+// Tokens per chunk, chunk slots of T tokens in B requests, and workspace
+// bytes of one (chunk slot, head).
+constexpr int kChunk = 32;
+constexpr int64_t prefill_slots(int64_t T, int64_t B) {
+  return T / kChunk + B + 1;
+}
+int64_t prefill_slot_bytes(int D, bool out_f32);
+int launch_prefill(const PrefillParams& p, int D, bool act_bf16,
+                   hipStream_t stream);
 
 struct TablesParams {
   const int32_t* query_lens;

@@ -1,4 +1,5 @@
-// Host side of the serving-step operators (decode, step tables): argument checks, translation of the public descriptors into
+// Host side of the serving-step operators (prefill, decode, step
+// tables): argument checks, translation of the public descriptors into
 // launch parameters, and the exported C entry points.
 #include <stdint.h>
 
@@ -209,6 +210,72 @@ int plan_layer(const LayerView& a, bool conv, kda::LayerParams* p, int* D_out,
   return KDA_OK;
 }
 
+struct PrefillPlan {
+  kda::PrefillParams p;
+  int D = 0;
+  bool act_bf16 = false;
+  bool noop = false;
+};
+
+// Bytes of workspace, or 0 for sizes that no launch takes.
+int64_t prefill_bytes(int64_t T, int64_t B, int64_t H, int64_t D,
+                      bool out_f32) {
+  if (T < 0 || B < 0 || H < 1 || !supported_head_dim(D) || T > kI32Max ||
+      B > kI32Max || H > kI32Max || B * H > kI32Max)
+    return 0;
+  const int64_t slots = kda::prefill_slots(T, B);
+  if (slots > kI32Max / H) return 0;
+  return slots * H * kda::prefill_slot_bytes(int(D), out_f32);
+}
+
+int plan_prefill(const kda_prefill_args* a, bool conv, PrefillPlan* plan) {
+  if (a == nullptr) return fail(KDA_E_ARG, "prefill arguments are NULL");
+  kda::PrefillParams& p = plan->p;
+  int64_t T = 0;
+  KDA_TRY(plan_layer(view_of(a), conv, &p.y, &plan->D, &plan->act_bf16, &T));
+  plan->noop = a->batch == 0 || T == 0;
+  const int64_t need = prefill_bytes(T, a->batch, p.y.H, plan->D,
+                                     a->out.dtype == KDA_F32);
+  // the second kernel's grid: a wave per (request, head, 16 rows)
+  if (need == 0 ||
+      (int64_t(a->batch) * p.y.H + 7) / 8 * 8 * (plan->D / 16) > kI32Max)
+    return fail(KDA_E_CAPACITY, "tokens, requests and heads exceed the grid");
+  if (!plan->noop) {
+    if (!a->query_start_loc)
+      return fail(KDA_E_ARG, "query_start_loc is required");
+    if (!a->workspace) return fail(KDA_E_ARG, "the workspace is required");
+    if (a->workspace_bytes < need)
+      return fail(KDA_E_CAPACITY,
+                  "the workspace holds %lld bytes; %lld tokens of %d requests "
+                  "need %lld",
+                  (long long)a->workspace_bytes, (long long)T, a->batch,
+                  (long long)need);
+    if (!aligned(a->workspace, 16))
+      return fail(KDA_E_UNALIGNED, "the workspace must be 16-byte aligned");
+    if (!aligned(a->query_start_loc, 4) ||
+        (a->initial_state_indices && !aligned(a->initial_state_indices, 4)))
+      return fail(KDA_E_UNALIGNED, "metadata pointers must be 4-byte aligned");
+  }
+  p.qsl = a->query_start_loc;
+  p.initial = a->initial_state_indices;
+  p.work = static_cast<char*>(a->workspace);
+  p.T = int32_t(T);
+  p.n_slots = int32_t(kda::prefill_slots(T, a->batch));
+  return KDA_OK;
+}
+
+int run_prefill(const kda_prefill_args* a, bool conv, void* stream,
+                const char* what) {
+  g_err.clear();
+  PrefillPlan plan;
+  KDA_TRY(plan_prefill(a, conv, &plan));
+  if (plan.noop) return KDA_OK;
+  return device_status(
+      kda::launch_prefill(plan.p, plan.D, plan.act_bf16,
+                          static_cast<hipStream_t>(stream)),
+      what);
+}
+
 struct DecodePlan {
   kda::DecodeParams p;
   int D = 0;
@@ -321,6 +388,36 @@ int plan_tables(const kda_tables_args* a, kda::TablesParams* p) {
 }  // namespace
 
 extern "C" {
+
+int64_t kda_prefill_workspace_size(int64_t tokens, int64_t batch,
+                                   int64_t num_heads, int64_t head_dim,
+                                   int32_t act_dtype, int32_t out_dtype) {
+  if (elem_size(act_dtype) == 0 ||
+      (out_dtype != KDA_F32 && out_dtype != act_dtype))
+    return 0;
+  return prefill_bytes(tokens, batch, num_heads, head_dim,
+                       out_dtype == KDA_F32);
+}
+
+int kda_check_prefill(const kda_prefill_args* args) {
+  g_err.clear();
+  PrefillPlan plan;
+  return plan_prefill(args, true, &plan);
+}
+
+int kda_conv_prefill(const kda_prefill_args* args, void* stream) {
+  return run_prefill(args, true, stream, "kda_conv_prefill launch");
+}
+
+int kda_check_prefill_qkv(const kda_prefill_args* args) {
+  g_err.clear();
+  PrefillPlan plan;
+  return plan_prefill(args, false, &plan);
+}
+
+int kda_prefill_qkv(const kda_prefill_args* args, void* stream) {
+  return run_prefill(args, false, stream, "kda_prefill_qkv launch");
+}
 
 int kda_check_decode(const kda_decode_args* args) {
   g_err.clear();

@@ -1,5 +1,5 @@
 """Python binding of the operators around the verify in a serving step:
-single-token decode and the step's index tables.
+prefill of prompts, single-token decode and the step's index tables.
 
 Argument marshalling only, as in `ops`; every computation runs in the HIP
 library.  Beyond the library's own checks these functions check what the C
@@ -15,7 +15,7 @@ import struct
 import torch
 
 from . import _abi
-from .ops import (_pack_format, _ptr, _raise, _tensor_values)
+from .ops import (_DT, _pack_format, _ptr, _raise, _tensor_values)
 
 
 def _on_device(tensors) -> torch.device:
@@ -61,11 +61,82 @@ def _ints(t, name: str, size: int, *, exact=False) -> int:
 
 _LAYER = ("mixed_qkv", "raw_gate", "raw_beta", "A_log", "dt_bias", "state",
           "out", "conv_state", "conv_weight")
+_PREFILL_PACK = struct.Struct("<" + _pack_format(_abi.KdaPrefillArgs))
 _DECODE_PACK = struct.Struct("<" + _pack_format(_abi.KdaDecodeArgs))
 
 
 def _layer_values(kw) -> list:
     return [v for name in _LAYER for v in _tensor_values(kw[name])]
+
+
+def prefill_workspace_size(tokens: int, batch: int, num_heads: int,
+                           head_dim: int, act_dtype: torch.dtype,
+                           out_dtype: torch.dtype = None) -> int:
+    """Bytes of workspace for a prefill of up to `tokens` rows and `batch`
+    requests (outputs in `out_dtype`, default the activations' dtype)."""
+    n = _abi.load().kda_prefill_workspace_size(
+        tokens, batch, num_heads, head_dim, _DT.get(act_dtype, -1),
+        _DT.get(out_dtype or act_dtype, -1))
+    if n <= 0:
+        raise ValueError("no prefill has these sizes and dtypes")
+    return n
+
+
+def prefill_args(*, mixed_qkv, raw_gate, raw_beta, A_log, dt_bias,
+                 lower_bound, state, out, query_start_loc, state_indices,
+                 workspace, conv_state=None, conv_weight=None,
+                 spec_query_len=1, conv_dim_first=True,
+                 initial_state_indices=None, num_accepted_tokens=None,
+                 null_block_id=0) -> _abi.KdaPrefillArgs:
+    """kda_prefill_args for these tensors."""
+    kw = dict(locals())
+    B = state_indices.shape[0]
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    vals = (*_layer_values(kw),
+            _ints(query_start_loc, "query_start_loc", B + 1),
+            _ints(state_indices, "state_indices", B),
+            _ints(initial_state_indices, "initial_state_indices", B),
+            _ints(num_accepted_tokens, "num_accepted_tokens", B),
+            workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(),
+            B, spec_query_len, null_block_id, 1 if conv_dim_first else 0,
+            0 if lower_bound is None else 1,
+            0.0 if lower_bound is None else float(lower_bound))
+    return _abi.KdaPrefillArgs.from_buffer_copy(_PREFILL_PACK.pack(*vals))
+
+
+def check_prefill(**kwargs) -> int:
+    """Host-only validation (no launch); returns the kda_status code."""
+    return _abi.load().kda_check_prefill(ctypes.byref(prefill_args(**kwargs)))
+
+
+def conv_prefill(*, stream=None, **kwargs) -> None:
+    """One KDA layer over whole prompts, with the short convolution fused:
+    request b's tokens are rows query_start_loc[b] .. query_start_loc[b + 1]
+    of the activations, it starts from slot `initial_state_indices[b]` (zeros
+    where null or not given) and leaves its checkpoint and conv history in
+    slot `state_indices[b]`, ready for the verify or the decode with accepted
+    count 1.  Arguments follow kda_prefill_args in
+    include/kda_recoverssm.h; `workspace` is scratch memory of
+    `prefill_workspace_size` bytes."""
+    _launch(_abi.load().kda_conv_prefill, prefill_args(**kwargs),
+            _tensors(kwargs), stream)
+
+
+def check_prefill_qkv(**kwargs) -> int:
+    """Host-only validation of the unfused prefill (no launch)."""
+    _no_conv(kwargs)
+    return _abi.load().kda_check_prefill_qkv(
+        ctypes.byref(prefill_args(**kwargs)))
+
+
+def prefill_qkv(*, stream=None, **kwargs) -> None:
+    """`conv_prefill` on already convolved q | k | v (no conv state, taps or
+    accepted counts)."""
+    _no_conv(kwargs)
+    _launch(_abi.load().kda_prefill_qkv, prefill_args(**kwargs),
+            _tensors(kwargs), stream)
 
 
 def decode_args(*, mixed_qkv, raw_gate, raw_beta, A_log, dt_bias,
