@@ -10,27 +10,27 @@ namespace kda {
 
 // e^x to about 1 ulp: the product x log2(e) is carried in two floats, since
 // the hardware exponential alone would turn its rounding into a relative
-// error of |x| ulp.
+// error of |x| ulp.  Below -104 the result is 0 in fp32 (and an infinite x
+// would make the second float a NaN); a NaN passes.
 __device__ __forceinline__ float exp_(float x) {
   constexpr float kL = 1.44269502162933349609375f;   // log2(e), high part
   constexpr float kLlo = 1.92596299112661746887e-8f;  // and the rest
   constexpr float kLn2 = 0.693147180559945f;
+  x = x < -104.0f ? -104.0f : x;
   const float t = x * kL;
-  const float r = __builtin_fmaf(x, kL, -t) + x * kLlo;
+  const float r = __builtin_fmaf(x, kLlo, __builtin_fmaf(x, kL, -t));
   const float e = __builtin_amdgcn_exp2f(t);
-  // the correction is meaningless (inf - inf) where e has left the range
-  return e > 0.0f && e < __builtin_inff() ? __builtin_fmaf(e * r, kLn2, e)
-                                          : e;
+  return __builtin_fmaf(e * r, kLn2, e);
 }
 
+// From e^-|x|, which cannot overflow: 1 / (1 + e) for x >= 0, else e / (1 + e).
 __device__ __forceinline__ float sigmoid_(float x) {
-  return rcp_(1.0f + exp_(-x));
+  const float e = exp_(-fabsf(x));
+  const float r = rcp_(1.0f + e);
+  return x < 0.0f ? e * r : r;
 }
 
-__device__ __forceinline__ float silu_(float x) {
-  // -inf * 0 would be NaN where the limit is 0
-  return x <= -88.0f ? x * 0.0f : x * sigmoid_(x);
-}
+__device__ __forceinline__ float silu_(float x) { return x * sigmoid_(x); }
 
 // ln(1 + e) for 0 <= e <= 1, relative to its value: 2 atanh(e / (2 + e)),
 // whose series in z^2 <= 1/9 is below half an ulp after eight terms.

@@ -147,6 +147,42 @@ __device__ __forceinline__ int first_slot(int bos, int b) {
   return bos / C + b;
 }
 
+// 1 / sqrt(sum + eps) of N tokens' q and k rows, each spread in pairs over
+// CP consecutive lanes.  The 2 N sums are reduced together, each lane ending
+// with one of them, so that the root is taken once per row and handed back.
+template <int CP, int N>
+__device__ __forceinline__ void row_norms(const float (&q)[N][2],
+                                          const float (&k)[N][2],
+                                          float (&nq)[N], float (&nk)[N]) {
+  float s[2 * N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    s[i] = q[i][0] * q[i][0] + q[i][1] * q[i][1];
+    s[N + i] = k[i][0] * k[i][0] + k[i][1] * k[i][1];
+  }
+  if constexpr (CP >= 16) {
+    constexpr int E = 16 / (2 * N);      // lanes that end with one sum
+    float v = transpose_sum<16, 2 * N>(s, threadIdx.x & 15);
+    if constexpr (CP >= 32)
+      v += __int_as_float(
+          __builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F));
+    if constexpr (CP >= 64) v += __shfl_xor(v, 32);
+    v = __builtin_amdgcn_rsqf(v + kNormEps);
+    const int base = threadIdx.x & 48;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      nq[i] = __shfl(v, base + i * E);
+      nk[i] = __shfl(v, base + (N + i) * E);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      nq[i] = __builtin_amdgcn_rsqf(group_sum<CP>(s[i]) + kNormEps);
+      nk[i] = __builtin_amdgcn_rsqf(group_sum<CP>(s[N + i]) + kNormEps);
+    }
+  }
+}
+
 template <int D, bool BF16, bool O32>
 __global__ void __launch_bounds__(kThreads)
     kda_prefill_chunk_kernel(PrefillParams p) {
@@ -181,54 +217,94 @@ __global__ void __launch_bounds__(kThreads)
   const int cp = tid % F::CP, tg = tid / F::CP;
   const int64_t HD = int64_t(y.H) * D, ch = int64_t(h) * D + 2 * cp;
   const bool conv = !(y.flags & kNoConv);
+  // Every row index is clamped into the request and the value dropped
+  // afterwards: the loads then stand in one block, all in flight together.
+  const int tk = tg * F::NTK;
+  typename P2::T raw[3][F::NTK + 3], rawg[F::NTK];
+  const T* xcol = static_cast<const T*>(y.mixed_qkv) + ch;
+  const T* gcol = static_cast<const T*>(y.raw_gate) + ch;
+#pragma unroll
+  for (int i = 0; i < F::NTK + 3; ++i) {
+    const int64_t row = t0 + min(max(tk + i - 3, -first), n - 1);
+#pragma unroll
+    for (int part = 0; part < 3; ++part)
+      raw[part][i] = *reinterpret_cast<const typename P2::T*>(
+          xcol + row * y.s_x + part * HD);
+    if (i >= 3)
+      rawg[i - 3] = *reinterpret_cast<const typename P2::T*>(gcol +
+                                                             row * y.s_g);
+  }
+  float w[3][2][kConvWidth];
+  if (conv) {
+    if (y.flags & kWRow) {
+      // four taps of a channel in one load
+#pragma unroll
+      for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int64_t o = (part * HD + ch + e) * kConvWidth;
+          if (y.flags & kWBf16) {
+            const uint2 u = *reinterpret_cast<const uint2*>(
+                static_cast<const uint16_t*>(y.conv_weight) + o);
+            w[part][e][0] = __uint_as_float(u.x << 16);
+            w[part][e][1] = __uint_as_float(u.x & 0xffff0000u);
+            w[part][e][2] = __uint_as_float(u.y << 16);
+            w[part][e][3] = __uint_as_float(u.y & 0xffff0000u);
+          } else {
+            const f4 u = *reinterpret_cast<const f4*>(
+                static_cast<const float*>(y.conv_weight) + o);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[part][e][i] = u[i];
+          }
+        }
+    } else {
+#pragma unroll
+      for (int part = 0; part < 3; ++part)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int i = 0; i < kConvWidth; ++i)
+            w[part][e][i] = ld_elem(
+                y.conv_weight,
+                (part * HD + ch + e) * y.s_w_chan + i * y.s_w_tap,
+                y.flags & kWBf16);
+    }
+  }
   float val[3][F::NTK][2];
+  const bool head = first == 0 && tk < 3;   // the window reaches the history
+  const int src = p.initial ? p.initial[b] : -1;
 #pragma unroll
   for (int part = 0; part < 3; ++part) {
-    const int64_t c0 = part * HD + ch;
-    const T* col = static_cast<const T*>(y.mixed_qkv) + c0;
     float x[F::NTK + 3][2];
 #pragma unroll
     for (int i = 0; i < F::NTK + 3; ++i) {
-      const int t = tg * F::NTK + i - 3;      // token in the chunk
-      x[i][0] = x[i][1] = 0.0f;
-      if ((i >= 3 || conv) && first + t >= 0 && t < n) {
-        const typename P2::T r = *reinterpret_cast<const typename P2::T*>(
-            col + int64_t(t0 + t) * y.s_x);
-        x[i][0] = P2::lo(r);
-        x[i][1] = P2::hi(r);
-      }
+      const bool in = tk + i - 3 < n;
+      x[i][0] = in ? P2::lo(raw[part][i]) : 0.0f;
+      x[i][1] = in ? P2::hi(raw[part][i]) : 0.0f;
     }
     if (conv) {
-      if (first == 0 && tg * F::NTK < 3 && p.initial &&
-          live_slot(y, p.initial[b])) {
+      if (head) {
+        const bool from = live_slot(y, src);
         const T* cs = static_cast<const T*>(y.conv_state) +
-                      p.initial[b] * y.s_cs_slot + c0 * y.s_cs_chan;
-        const int at = history_at(y, b);
+                      (part * HD + ch) * y.s_cs_chan;
+        if (from) cs += src * y.s_cs_slot + history_at(y, b) * y.s_cs_tok;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int t = tg * F::NTK + i - 3;
-          if (t < 0) {
-            x[i][0] = Act<BF16>::f(cs[(at + t + 3) * y.s_cs_tok]);
-            x[i][1] = Act<BF16>::f(cs[y.s_cs_chan + (at + t + 3) * y.s_cs_tok]);
+        for (int i = 0; i < 3; ++i)
+          if (tk + i < 3) {
+            x[i][0] = from ? Act<BF16>::f(cs[(tk + i) * y.s_cs_tok]) : 0.0f;
+            x[i][1] = from ? Act<BF16>::f(cs[y.s_cs_chan +
+                                             (tk + i) * y.s_cs_tok])
+                           : 0.0f;
           }
-        }
       }
-      float w[2][kConvWidth];
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < kConvWidth; ++i)
-          w[e][i] = ld_elem(y.conv_weight,
-                            (c0 + e) * y.s_w_chan + i * y.s_w_tap,
-                            y.flags & kWBf16);
 #pragma unroll
       for (int i = 0; i < F::NTK; ++i)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float acc = w[e][0] * x[i][e];
-          acc = __builtin_fmaf(w[e][1], x[i + 1][e], acc);
-          acc = __builtin_fmaf(w[e][2], x[i + 2][e], acc);
-          acc = __builtin_fmaf(w[e][3], x[i + 3][e], acc);
+          float acc = w[part][e][0] * x[i][e];
+          acc = __builtin_fmaf(w[part][e][1], x[i + 1][e], acc);
+          acc = __builtin_fmaf(w[part][e][2], x[i + 2][e], acc);
+          acc = __builtin_fmaf(w[part][e][3], x[i + 3][e], acc);
           val[part][i][e] = silu_(acc);
         }
     } else {
@@ -240,46 +316,53 @@ __global__ void __launch_bounds__(kThreads)
   }
   const float A = exp_(y.A_log[h]);
   const float2 bias = *reinterpret_cast<const float2*>(y.dt_bias + ch);
-  const T* gcol = static_cast<const T*>(y.raw_gate) + ch;
+  // |q|^2 and |k|^2 of the thread's tokens over the lanes of their row
+  float nq[F::NTK], nk[F::NTK];
+  row_norms<F::CP, F::NTK>(val[0], val[1], nq, nk);
 #pragma unroll
   for (int i = 0; i < F::NTK; ++i) {
-    const int t = tg * F::NTK + i;
+    const int t = tk + i;
     const bool in = t < n;
-    float a0 = 1.0f, a1 = 1.0f;
-    if (in) {
-      const typename P2::T r = *reinterpret_cast<const typename P2::T*>(
-          gcol + int64_t(t0 + t) * y.s_g);
-      a0 = exp_(layer_gate(P2::lo(r) + bias.x, A, y.flags & kLowerBound,
-                           y.lb));
-      a1 = exp_(layer_gate(P2::hi(r) + bias.y, A, y.flags & kLowerBound,
-                           y.lb));
-    }
-    float q0 = val[0][i][0], q1 = val[0][i][1];
-    float k0 = val[1][i][0], k1 = val[1][i][1];
-    float qq = q0 * q0 + q1 * q1, kk = k0 * k0 + k1 * k1;
-    if constexpr (F::CP == 64) {
-      qq = wave_sum(qq);
-      kk = wave_sum(kk);
-    } else {
-      qq = group_sum<F::CP>(qq);
-      kk = group_sum<F::CP>(kk);
-    }
-    const float nq = in ? 1.0f / (sqrtf(qq + kNormEps) * sqrtf(float(D))) : 0;
-    const float nk = in ? 1.0f / sqrtf(kk + kNormEps) : 0;
+    const float g0 = layer_gate(P2::lo(rawg[i]) + bias.x, A,
+                                y.flags & kLowerBound, y.lb);
+    const float g1 = layer_gate(P2::hi(rawg[i]) + bias.y, A,
+                                y.flags & kLowerBound, y.lb);
+    const float fq = nq[i] * (1.0f / sqrtf(float(D)));
+    // rows behind the request vanish: k = q = v = 0, decay 1
     *reinterpret_cast<float2*>(&m.q[t][2 * cp]) =
-        in ? make_float2(q0 * nq, q1 * nq) : make_float2(0, 0);
+        in ? make_float2(val[0][i][0] * fq, val[0][i][1] * fq)
+           : make_float2(0, 0);
     *reinterpret_cast<float2*>(&m.k[t][2 * cp]) =
-        in ? make_float2(k0 * nk, k1 * nk) : make_float2(0, 0);
-    *reinterpret_cast<float2*>(&m.p[t][2 * cp]) = make_float2(a0, a1);
-    // V as the second kernel's accumulators hold it
-    float* vf = reinterpret_cast<float*>(work + W::v);
-    const int r = t / kSub, g = (t % kSub) / 4;
+        in ? make_float2(val[1][i][0] * nk[i], val[1][i][1] * nk[i])
+           : make_float2(0, 0);
+    *reinterpret_cast<float2*>(&m.p[t][2 * cp]) =
+        in ? make_float2(exp_(g0), exp_(g1)) : make_float2(1, 1);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int d = 2 * cp + e;
-      vf[((r * W::MT + d / 16) * 64 + g * 16 + d % 16) * 4 + t % 4] =
-          in ? val[2][i][e] : 0.0f;
-    }
+    for (int e = 0; e < 2; ++e) val[2][i][e] = in ? val[2][i][e] : 0.0f;
+  }
+  // V as the second kernel's accumulators hold it
+  char* vf = work + W::v;
+  if constexpr (F::NTK >= 4) {
+#pragma unroll
+    for (int i = 0; i < F::NTK; i += 4)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = tk + i, d = 2 * cp + e;
+        *reinterpret_cast<f4*>(
+            vf + ((t / kSub * W::MT + d / 16) * 64 + (t % kSub) / 4 * 16 +
+                  d % 16) * 16) = f4{val[2][i][e], val[2][i + 1][e],
+                                     val[2][i + 2][e], val[2][i + 3][e]};
+      }
+  } else {
+#pragma unroll
+    for (int i = 0; i < F::NTK; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = tk + i, d = 2 * cp + e;
+        reinterpret_cast<float*>(
+            vf)[((t / kSub * W::MT + d / 16) * 64 + (t % kSub) / 4 * 16 +
+                 d % 16) * 4 + t % 4] = val[2][i][e];
+      }
   }
   if (tid < C)
     m.beta[tid] =
@@ -498,8 +581,54 @@ __device__ __forceinline__ void scale_of(float m, float& up, float& down) {
   down = __uint_as_float(uint32_t(127 - s) << 23);
 }
 
+// Operands of one chunk that meet the state (Front), and those that meet the
+// corrections (Back), in registers.
+template <int D, bool O32>
+struct Front {
+  using W = Work<D>;
+  h8 kh[2 * W::KS], kl[2 * W::KS], qh[2 * W::KS], ql[O32 ? 2 * W::KS : 1];
+  f4 v[2];
+  __device__ __forceinline__ void load(const char* work, int vt, int lane) {
+#pragma unroll
+    for (int i = 0; i < 2 * W::KS; ++i) {
+      kh[i] = frag(work + W::kd + 2 * i * kFrag, lane);
+      kl[i] = frag(work + W::kd + (2 * i + 1) * kFrag, lane);
+      qh[i] = frag(work + W::qd + i * (O32 + 1) * kFrag, lane);
+      if (O32) ql[i] = frag(work + W::qd + (2 * i + 1) * kFrag, lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      v[i] = *reinterpret_cast<const f4*>(
+          work + W::v + (i * W::MT + vt) * kFrag + lane * 16);
+  }
+};
+
+template <int D, bool O32>
+struct Back {
+  using W = Work<D>;
+  h8 th[2], tl[2], bh[2], bl[O32 ? 2 : 1], eh[W::MT], el[W::MT];
+  f4 gam[W::MT];
+  __device__ __forceinline__ void load(const char* work, int lane, int g) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      th[i] = frag(work + W::t + 2 * i * kFrag, lane);
+      tl[i] = frag(work + W::t + (2 * i + 1) * kFrag, lane);
+      bh[i] = frag(work + W::b(O32) + i * (O32 + 1) * kFrag, lane);
+      if (O32) bl[i] = frag(work + W::b(O32) + (2 * i + 1) * kFrag, lane);
+    }
+#pragma unroll
+    for (int m = 0; m < W::MT; ++m) {
+      eh[m] = frag(work + W::ke + 2 * m * kFrag, lane);
+      el[m] = frag(work + W::ke + (2 * m + 1) * kFrag, lane);
+      gam[m] = *reinterpret_cast<const f4*>(work + W::gam +
+                                            (16 * m + 4 * g) * 4);
+    }
+  }
+};
+
 template <int D, bool O32, int WAVES>
 __global__ void __launch_bounds__(64 * WAVES)
+    __attribute__((amdgpu_waves_per_eu(1, 1)))
     kda_prefill_state_kernel(PrefillParams p, int act_bf16) {
   using W = Work<D>;
   const LayerParams& y = p.y;
@@ -525,6 +654,15 @@ __global__ void __launch_bounds__(64 * WAVES)
   const int src = p.initial ? p.initial[b] : -1;
   const bool from = live_slot(y, src);
 
+  const int64_t step = int64_t(y.H) * W::size(O32);
+  const char* work =
+      p.work +
+      (int64_t(first_slot(range.x, b)) * y.H + h) * W::size(O32);
+  Front<D, O32> f;
+  Back<D, O32> k;
+  f.load(work, vt, lane);
+  k.load(work, lane, g);
+
   f4 S[W::MT];      // S[m][i]: row v = col, channel 16 m + 4 g + i
   const int64_t so = (int64_t(h) * D + vt * 16 + col) * D + 4 * g;
 #pragma unroll
@@ -534,11 +672,9 @@ __global__ void __launch_bounds__(64 * WAVES)
       S[m] = *reinterpret_cast<const f4*>(y.state + src * y.s_slot + so +
                                           16 * m);
   }
-  const int64_t step = int64_t(y.H) * W::size(O32);
-  const char* work =
-      p.work +
-      (int64_t(first_slot(range.x, b)) * y.H + h) * W::size(O32);
-  for (int t0 = 0; t0 < L; t0 += C, work += step) {
+  for (int t0 = 0; t0 < L; t0 += C) {
+    // the last chunk loads its own operands again: in bounds, not used
+    if (t0 + C < L) work += step;
     // S as the right operand: two 16-channel tiles make one step of 32
     float top = 0.0f;
 #pragma unroll
@@ -549,40 +685,39 @@ __global__ void __launch_bounds__(64 * WAVES)
     scale_of(column_max(top), up, down);
     Split s[W::KS];
 #pragma unroll
-    for (int k = 0; k < W::KS; ++k) {
+    for (int n = 0; n < W::KS; ++n) {
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int m = 2 * k + (e >> 2);
+        const int m = 2 * n + (e >> 2);
         x[e] = m < W::MT ? S[m < W::MT ? m : 0][e & 3] * up : 0.0f;
       }
-      s[k] = split8(x);
+      s[n] = split8(x);
     }
     down *= 1.0f / kUnit;
     f4 r[2], o[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      f4 acc = {0, 0, 0, 0}, out = {0, 0, 0, 0};
+      r[i] = o[i] = f4{0, 0, 0, 0};
 #pragma unroll
-      for (int k = 0; k < W::KS; ++k) {
-        const char* at = work + W::kd + 2 * (i * W::KS + k) * kFrag;
-        const h8 hi = frag(at, lane), lo = frag(at + kFrag, lane);
-        acc = mfma(hi, s[k].hi, acc);
-        acc = mfma(lo, s[k].hi, acc);
-        acc = mfma(hi, s[k].lo, acc);
-        const char* qa = work + W::qd + (i * W::KS + k) * (O32 + 1) * kFrag;
-        const h8 qh = frag(qa, lane);
-        out = mfma(qh, s[k].hi, out);
+      for (int n = 0; n < W::KS; ++n) {
+        const int j = i * W::KS + n;
+        r[i] = mfma(f.kh[j], s[n].hi, r[i]);
+        r[i] = mfma(f.kl[j], s[n].hi, r[i]);
+        r[i] = mfma(f.kh[j], s[n].lo, r[i]);
+        o[i] = mfma(f.qh[j], s[n].hi, o[i]);
         if (O32) {
-          out = mfma(frag(qa + kFrag, lane), s[k].hi, out);
-          out = mfma(qh, s[k].lo, out);
+          o[i] = mfma(f.ql[j], s[n].hi, o[i]);
+          o[i] = mfma(f.qh[j], s[n].lo, o[i]);
         }
       }
-      const f4 v = *reinterpret_cast<const f4*>(
-          work + W::v + (i * W::MT + vt) * kFrag + lane * 16);
-      r[i] = v - acc * down;
-      o[i] = out * down;
+      r[i] = f.v[i] - r[i] * down;
+      o[i] = o[i] * down;
     }
+    // the next chunk's operands travel during the rest of this one
+    __builtin_amdgcn_sched_barrier(0);
+    f.load(work, vt, lane);
+    __builtin_amdgcn_sched_barrier(0);
     // c = T r
     float top_r = 0.0f;
 #pragma unroll
@@ -598,12 +733,10 @@ __global__ void __launch_bounds__(64 * WAVES)
     float top_c = 0.0f;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const char* at = work + W::t + 2 * i * kFrag;
-      const h8 hi = frag(at, lane), lo = frag(at + kFrag, lane);
       f4 acc = {0, 0, 0, 0};
-      acc = mfma(hi, rs.hi, acc);
-      acc = mfma(lo, rs.hi, acc);
-      acc = mfma(hi, rs.lo, acc);
+      acc = mfma(k.th[i], rs.hi, acc);
+      acc = mfma(k.tl[i], rs.hi, acc);
+      acc = mfma(k.th[i], rs.lo, acc);
       r[i] = acc * down;
 #pragma unroll
       for (int e = 0; e < 4; ++e) top_c = fmaxf(top_c, fabsf(r[i][e]));
@@ -616,13 +749,11 @@ __global__ void __launch_bounds__(64 * WAVES)
     // outputs
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const char* at = work + W::b(O32) + i * (O32 + 1) * kFrag;
-      const h8 hi = frag(at, lane);
       f4 acc = {0, 0, 0, 0};
-      acc = mfma(hi, cs.hi, acc);
+      acc = mfma(k.bh[i], cs.hi, acc);
       if (O32) {
-        acc = mfma(frag(at + kFrag, lane), cs.hi, acc);
-        acc = mfma(hi, cs.lo, acc);
+        acc = mfma(k.bl[i], cs.hi, acc);
+        acc = mfma(k.bh[i], cs.lo, acc);
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -635,16 +766,15 @@ __global__ void __launch_bounds__(64 * WAVES)
     // the state behind the chunk
 #pragma unroll
     for (int m = 0; m < W::MT; ++m) {
-      const char* at = work + W::ke + 2 * m * kFrag;
-      const h8 hi = frag(at, lane), lo = frag(at + kFrag, lane);
       f4 acc = {0, 0, 0, 0};
-      acc = mfma(hi, cs.hi, acc);
-      acc = mfma(lo, cs.hi, acc);
-      acc = mfma(hi, cs.lo, acc);
-      const f4 gam = *reinterpret_cast<const f4*>(work + W::gam +
-                                                  (16 * m + 4 * g) * 4);
-      S[m] = S[m] * gam + acc * down;
+      acc = mfma(k.eh[m], cs.hi, acc);
+      acc = mfma(k.el[m], cs.hi, acc);
+      acc = mfma(k.eh[m], cs.lo, acc);
+      S[m] = S[m] * k.gam[m] + acc * down;
     }
+    __builtin_amdgcn_sched_barrier(0);
+    k.load(work, lane, g);
+    __builtin_amdgcn_sched_barrier(0);
   }
   float* to = y.state + dst * y.s_slot + so;
 #pragma unroll

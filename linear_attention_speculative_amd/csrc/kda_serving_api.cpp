@@ -203,6 +203,10 @@ int plan_layer(const LayerView& a, bool conv, kda::LayerParams* p, int* D_out,
   p->flags = (a.out.dtype == KDA_BF16 ? kda::kOutBf16 : 0) |
              (conv && cw.dtype == KDA_BF16 ? kda::kWBf16 : 0) |
              (conv ? 0 : kda::kNoConv) | (a.use_lb ? kda::kLowerBound : 0);
+  // each channel's four taps contiguous and aligned to their size
+  if (conv && cw.stride[1] == 1 && cw.stride[0] == kda::kConvWidth &&
+      aligned(cw.data, uintptr_t(kda::kConvWidth) * elem_size(cw.dtype)))
+    p->flags |= kda::kWRow;
   p->lb = a.lb;
   *D_out = int(D);
   *act_bf16 = act == KDA_BF16;
