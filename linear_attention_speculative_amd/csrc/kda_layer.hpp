@@ -1,6 +1,7 @@
-// Device pieces shared by the prefill and the decode of a KDA layer: the gate
-// and its decay to fp32 accuracy (a state carries the errors of hundreds of
-// decays, which the verify's few steps do not), and the short convolution.
+// Device pieces shared by the prefill and the decode of a KDA layer: the
+// gate, with a softplus that keeps its relative accuracy where it is small (a
+// state carries the errors of hundreds of decays near 1, which the verify's
+// few steps do not), and the parameters.
 #pragma once
 
 #include "kda_device.hpp"
@@ -8,26 +9,14 @@
 
 namespace kda {
 
-// e^x to about 1 ulp: the product x log2(e) is carried in two floats, since
-// the hardware exponential alone would turn its rounding into a relative
-// error of |x| ulp.  Below -104 the result is 0 in fp32 (and an infinite x
-// would make the second float a NaN); a NaN passes.
-__device__ __forceinline__ float exp_(float x) {
-  constexpr float kL = 1.44269502162933349609375f;   // log2(e), high part
-  constexpr float kLlo = 1.92596299112661746887e-8f;  // and the rest
-  constexpr float kLn2 = 0.693147180559945f;
-  x = x < -104.0f ? -104.0f : x;
-  const float t = x * kL;
-  const float r = __builtin_fmaf(x, kLlo, __builtin_fmaf(x, kL, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  return __builtin_fmaf(e * r, kLn2, e);
-}
+// e^x by the hardware exponential of x log2(e): the product's rounding makes
+// a relative error of up to (|x| + 1) 2^-23.  That is an ulp where it counts:
+// a sigmoid or softplus at a large |x| is 1, x, or too small to matter, and a
+// decay e^g at a large |g| leaves nothing to be wrong about.
+__device__ __forceinline__ float exp_(float x) { return __expf(x); }
 
-// From e^-|x|, which cannot overflow: 1 / (1 + e) for x >= 0, else e / (1 + e).
 __device__ __forceinline__ float sigmoid_(float x) {
-  const float e = exp_(-fabsf(x));
-  const float r = rcp_(1.0f + e);
-  return x < 0.0f ? e * r : r;
+  return rcp_(1.0f + exp_(-x));
 }
 
 __device__ __forceinline__ float silu_(float x) { return x * sigmoid_(x); }

@@ -35,8 +35,8 @@
 // under a power-of-two scale, three products each, which loses 2^-22 of a
 // term: fp32-like, at a third of the fp16 matrix rate instead of the
 // sixteenth that fp32 operands have.  k e^G and the like are at most 1 and
-// take the fixed scale 2^12; columns of S, V - ... and c take the scale that
-// puts their largest element near 2^13.  Products that only feed bf16
+// take fixed scales; each column of S, with its V, r and c, has a scale of
+// its own that follows its largest element.  Products that only feed bf16
 // outputs take hi alone (2^-11 against the output's own 2^-9).
 #include "kda_serving.hpp"
 
@@ -49,6 +49,7 @@ typedef _Float16 h4 __attribute__((ext_vector_type(4)));
 constexpr int C = kChunk;
 constexpr int kSub = 16;             // tokens of a sub-block
 constexpr float kUnit = 4096.0f;     // scale of operands of at most 1
+constexpr float kLate = 32.0f;       // scale of k e^(G_C - G)
 constexpr int kFrag = 1024;          // bytes of one operand (64 lanes x 16)
 
 // Workspace of one (chunk slot, head): byte offsets of its operands.
@@ -132,7 +133,7 @@ struct ChunkSmem {
   float b[C][F::AS];
   float t[C][F::AS];
   float beta[C];
-  int req;
+  int req, before, all, task;
 };
 
 // Bounds of request b in the token rows, whatever the offsets hold.
@@ -183,6 +184,31 @@ __device__ __forceinline__ void row_norms(const float (&q)[N][2],
   }
 }
 
+// Place of request b in the order of falling lengths (ties by number), written
+// to the order that the state kernel takes its requests in: its workgroups
+// then start with the longest ones, and the short ones fill the gaps.  Empty
+// requests have no place; order[-1] counts the others.
+template <int D>
+__device__ __forceinline__ void rank_request(const PrefillParams& p, int b,
+                                             ChunkSmem<D>& m) {
+  const int2 mine = token_range(p, b);
+  const int len = mine.y - mine.x;
+  int before = 0, all = 0;
+  for (int i = threadIdx.x; i < p.y.B; i += kThreads) {
+    const int2 r = token_range(p, i);
+    const int n = r.y - r.x;
+    before += n > len || (n == len && i < b);
+    all += n > 0;
+  }
+  atomicAdd(&m.before, before);
+  atomicAdd(&m.all, all);
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    p.order[m.before] = b;
+    p.order[-1] = m.all;
+  }
+}
+
 template <int D, bool BF16, bool O32>
 __global__ void __launch_bounds__(kThreads)
     kda_prefill_chunk_kernel(PrefillParams p) {
@@ -197,7 +223,10 @@ __global__ void __launch_bounds__(kThreads)
   const int slot = blockIdx.x / y.H, h = blockIdx.x - slot * y.H;
 
   // the request of this chunk slot
-  if (tid == 0) m.req = -1;
+  if (tid == 0) {
+    m.req = -1;
+    m.before = m.all = m.task = 0;
+  }
   for (int i = tid; i < 2 * C * F::AS; i += kThreads) (&m.a[0][0])[i] = 0.0f;
   __syncthreads();
   for (int b = tid; b < y.B; b += kThreads) {
@@ -207,14 +236,18 @@ __global__ void __launch_bounds__(kThreads)
   }
   __syncthreads();
   const int b = m.req;
-  if (b < 0 || !live_slot(y, y.slots[b])) return;
+  if (b < 0) return;
   const int2 range = token_range(p, b);
   const int first = (slot - first_slot(range.x, b)) * C;   // in the request
+  if (first == 0 && h == 0) rank_request<D>(p, b, m);
+  if (!live_slot(y, y.slots[b])) return;
   const int t0 = range.x + first, n = min(C, range.y - t0);
   char* work = p.work + (int64_t(slot) * y.H + h) * W::size(O32);
 
   // ---- activations: convolution, norms, gates ----
-  const int cp = tid % F::CP, tg = tid / F::CP;
+  // a wave holds whole rows at D = 128: its token rows are scalar addresses
+  const int cp = tid % F::CP;
+  const int tg = F::CP == 64 ? uniform(tid / F::CP) : tid / F::CP;
   const int64_t HD = int64_t(y.H) * D, ch = int64_t(h) * D + 2 * cp;
   const bool conv = !(y.flags & kNoConv);
   // Every row index is clamped into the request and the value dropped
@@ -371,10 +404,29 @@ __global__ void __launch_bounds__(kThreads)
                 : 0.0f;
   __syncthreads();
 
-  // ---- A and B inside each sub-block: waves 2 sb + half; a lane takes four
-  // columns j and D/32 channels, and carries k_j e^(G_i - G_j) from row to
-  // row ----
-  {
+  // ---- products of decays from the sub-block's start, and to its end ----
+  float pre[kSub], suf[kSub];
+  const int pc = tid % D, pb = tid / D;       // channel, sub-block
+  bool deep = false;
+  if (pb < 2) {
+#pragma unroll
+    for (int i = 0; i < kSub; ++i) pre[i] = m.p[pb * kSub + i][pc];
+    suf[kSub - 1] = 1.0f;
+#pragma unroll
+    for (int i = kSub - 2; i >= 0; --i) suf[i] = suf[i + 1] * pre[i + 1];
+#pragma unroll
+    for (int i = 1; i < kSub; ++i) pre[i] *= pre[i - 1];
+    deep = !(pre[kSub - 1] >= 1e-37f);
+  }
+  // Within a sub-block, e^(G_i - G_j) = P_i (1 / P_j) with P the products
+  // from its start, as long as no P leaves the fp32 range (down to 1e-37: 16
+  // tokens of log-decay -5 each stay inside): A and B are then fp32 matrix
+  // products.  Where a channel decays further, the sub-blocks are done by
+  // carrying k_j e^(G_i - G_j) from row to row, which takes any decay (and
+  // 4.5 times as long).
+  deep = __syncthreads_or(deep);
+  if (deep) {
+    // waves 2 sb + half; a lane takes four columns j and D/32 channels
     constexpr int CH = D >= 32 ? D / 32 : 1;
     const int sb = wave >> 1, cl = lane & 31;
     const int jg = (wave & 1) ? 1 + (lane >> 5) : 3 * (lane >> 5);
@@ -382,7 +434,7 @@ __global__ void __launch_bounds__(kThreads)
     const bool on = cl * CH < D;
     const int c0 = on ? cl * CH : 0;
     float kd[4][CH] = {};
-#pragma unroll 2
+#pragma unroll 1
     for (int i = (wave & 1) ? 4 : 0; i < kSub; ++i) {
       float ai[CH], ki[CH], qi[CH];
 #pragma unroll
@@ -413,20 +465,8 @@ __global__ void __launch_bounds__(kThreads)
           m.a[r0 + i][r0 + j] = i > j ? tot : 0.0f;
       }
     }
+    __syncthreads();
   }
-  // products of decays from the sub-block's start, and to its end
-  float pre[kSub], suf[kSub];
-  const int pc = tid % D, pb = tid / D;       // channel, sub-block
-  if (pb < 2) {
-#pragma unroll
-    for (int i = 0; i < kSub; ++i) pre[i] = m.p[pb * kSub + i][pc];
-    suf[kSub - 1] = 1.0f;
-#pragma unroll
-    for (int i = kSub - 2; i >= 0; --i) suf[i] = suf[i + 1] * pre[i + 1];
-#pragma unroll
-    for (int i = 1; i < kSub; ++i) pre[i] *= pre[i - 1];
-  }
-  __syncthreads();
   if (pb < 2) {
 #pragma unroll
     for (int i = 0; i < kSub; ++i) {
@@ -437,20 +477,39 @@ __global__ void __launch_bounds__(kThreads)
   __syncthreads();
 
   const int col = lane & 15, g = lane >> 4;
-  if (wave < 2) {
-    // the block of rows 16.. and columns ..15, of A (wave 0) or B (wave 1)
-    float (*rows)[F::RS] = wave == 0 ? m.k : m.q;
+  // One 16 x 16 block of A (rows k) or B (rows q) as a matrix product: a
+  // diagonal block, or the one of rows 16.. and columns ..15, whose decays
+  // split at its border into two factors of at most 1.  Lanes take the
+  // summed channels in the order 16 u + 4 g + i.
+  auto block = [&](const float (*rows)[F::RS], float (*dst)[F::AS], int r0,
+                   int c0, bool strict) {
+    const bool diag = r0 == c0;
     f4 acc = {0, 0, 0, 0};
-#pragma unroll 8
-    for (int s = 0; s < D / 4; ++s) {
-      const int c = 4 * s + g;
-      acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
-          rows[kSub + col][c] * m.p[kSub + col][c], m.k[col][c] * m.s[col][c],
-          acc, 0, 0, 0);
-    }
-    float (*dst)[F::AS] = wave == 0 ? m.a : m.b;
+#pragma unroll 2
+    for (int u = 0; u < D / 16; ++u) {
+      const int c = 16 * u + 4 * g;
+      const f4 x = *reinterpret_cast<const f4*>(&rows[r0 + col][c]);
+      const f4 xp = *reinterpret_cast<const f4*>(&m.p[r0 + col][c]);
+      const f4 z = *reinterpret_cast<const f4*>(&m.k[c0 + col][c]);
+      const f4 zp = *reinterpret_cast<const f4*>(
+          diag ? &m.p[c0 + col][c] : &m.s[c0 + col][c]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) dst[kSub + 4 * g + i][col] = acc[i];
+      for (int i = 0; i < 4; ++i)
+        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
+            x[i] * xp[i], z[i] * (diag ? rcp_(zp[i]) : zp[i]), acc, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = 4 * g + i;
+      const bool in = !diag || (strict ? r > col : r >= col);
+      dst[r0 + r][c0 + col] = in ? acc[i] : 0.0f;
+    }
+  };
+  // what T needs, and one block of B
+  if (wave == 2) block(m.k, m.a, kSub, 0, true);
+  if (!deep) {
+    if (wave < 2) block(m.k, m.a, wave * kSub, wave * kSub, true);
+    if (wave == 3) block(m.q, m.b, 0, 0, false);
   }
   __syncthreads();
 
@@ -501,6 +560,9 @@ __global__ void __launch_bounds__(kThreads)
       store_frag(work + W::t + (2 * r + 1) * kFrag, lane, s.lo);
     }
   } else if (wave == 1) {
+    block(m.q, m.b, kSub, 0, false);
+    if (!deep) block(m.q, m.b, kSub, kSub, false);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "workgroup", "local");
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float v[8];
@@ -515,10 +577,13 @@ __global__ void __launch_bounds__(kThreads)
         store_frag(work + W::b(O32) + (r * 2 + 1) * kFrag, lane, s.lo);
     }
   }
-  // scaled k and q: waves 2 and 3 alone, as long as the others have the
-  // inverse and the causal block
+  // scaled k and q, handed out as the waves become free
   constexpr int NKD = 2 * W::KS;
-  for (int task = wave - 2; task >= 0 && task < NKD + W::MT; task += 2) {
+  for (;;) {
+    int task = 0;
+    if (lane == 0) task = atomicAdd(&m.task, 1);
+    task = uniform(task);
+    if (task >= NKD + W::MT) break;
     float x[8], z[8];
     if (task < NKD) {
       const int r = task / W::KS, s = task - r * W::KS, t = r * kSub + col;
@@ -544,7 +609,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int t = e < 4 ? 4 * g + e : kSub + 4 * g + e - 4;
-        x[e] = kUnit * m.k[t][c] * m.s[t][c] * (e < 4 ? late : 1.0f);
+        x[e] = kLate * m.k[t][c] * m.s[t][c] * (e < 4 ? late : 1.0f);
       }
       const Split a = split8(x);
       store_frag(work + W::ke + 2 * mt * kFrag, lane, a.hi);
@@ -562,107 +627,161 @@ __device__ __forceinline__ f4 mfma(h8 a, h8 b, f4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
 
-__device__ __forceinline__ h8 frag(const char* at, int lane) {
-  return *reinterpret_cast<const h8*>(at + lane * 16);
-}
-
 // Largest value over the four lanes that share a column.
 __device__ __forceinline__ float column_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16));
-  return fmaxf(v, __shfl_xor(v, 32));
+  const uint32_t u = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  const float w = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const uint32_t x = __float_as_uint(w);
+  const auto b = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
-// The power of two that puts m (>= 0) into [2^13, 2^14), and its inverse; 1
-// where m is 0 or not finite.
-__device__ __forceinline__ void scale_of(float m, float& up, float& down) {
-  const int e = int(__float_as_uint(m) >> 23);        // biased exponent
-  const int s = e == 0 || e == 255 ? 0 : min(max(127 + 13 - e, -110), 110);
-  up = __uint_as_float(uint32_t(127 + s) << 23);
-  down = __uint_as_float(uint32_t(127 - s) << 23);
+// hi and lo of eight scaled values.  hi is made opaque before it is widened
+// again: left visible, the compiler recomputes it with a fused instruction of
+// half the rate.
+__device__ __forceinline__ Split split_wide(const float (&x)[8]) {
+  typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+  typedef _Float16 h2 __attribute__((ext_vector_type(2)));
+  u4 hi, lo;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const h2 h = {_Float16(x[2 * e]), _Float16(x[2 * e + 1])};
+    uint32_t u = __builtin_bit_cast(uint32_t, h);
+    asm("" : "+v"(u));
+    hi[e] = u;
+    const h2 k = __builtin_bit_cast(h2, u);
+    const h2 l = {_Float16(x[2 * e] - float(k[0])),
+                  _Float16(x[2 * e + 1] - float(k[1]))};
+    lo[e] = __builtin_bit_cast(uint32_t, l);
+  }
+  return Split{__builtin_bit_cast(h8, hi), __builtin_bit_cast(h8, lo)};
 }
 
-// Operands of one chunk that meet the state (Front), and those that meet the
-// corrections (Back), in registers.
-template <int D, bool O32>
-struct Front {
+__device__ __forceinline__ float max_abs(const f4& a, float m) {
+  return fmaxf(fmaxf(fmaxf(fabsf(a[0]), fabsf(a[1])),
+                     fmaxf(fabsf(a[2]), fabsf(a[3]))), m);
+}
+
+// One wave's load of 64 x 16 bytes from global memory straight into LDS, in
+// lane order (no register holds the data, so any number may be in flight).
+// The completion is waited for by hand (wait_vm): the compiler does not see
+// these loads and keeps no count of them.
+__device__ __forceinline__ void load_lds(const char* base, uint32_t off,
+                                         uint32_t lds) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %1, %2"
+      :
+      : "s"(lds), "v"(off), "s"(base)
+      : "memory");
+}
+
+// Wait until at most N of this wave's global memory operations are under way
+// (they end in the order in which they began).
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  static_assert(N >= 0 && N < 64, "count");
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// LDS of the state kernel: BUFS buffers of one chunk's operands (in workspace
+// order without V, then each wave's two V operands, whose place takes the
+
+template <int D, bool O32, int WAVES, int PROD, int BUFS>
+struct Stage {
   using W = Work<D>;
-  h8 kh[2 * W::KS], kl[2 * W::KS], qh[2 * W::KS], ql[O32 ? 2 * W::KS : 1];
-  f4 v[2];
-  __device__ __forceinline__ void load(const char* work, int vt, int lane) {
-#pragma unroll
-    for (int i = 0; i < 2 * W::KS; ++i) {
-      kh[i] = frag(work + W::kd + 2 * i * kFrag, lane);
-      kl[i] = frag(work + W::kd + (2 * i + 1) * kFrag, lane);
-      qh[i] = frag(work + W::qd + i * (O32 + 1) * kFrag, lane);
-      if (O32) ql[i] = frag(work + W::qd + (2 * i + 1) * kFrag, lane);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      v[i] = *reinterpret_cast<const f4*>(
-          work + W::v + (i * W::MT + vt) * kFrag + lane * 16);
-  }
+  static constexpr int shared_frags = (W::size(O32) - 2 * W::MT * kFrag) /
+                                      kFrag;
+  static constexpr int frags = shared_frags + 2 * WAVES;
+  static constexpr int per_loader = (frags + PROD - 1) / PROD;
+  static constexpr int bytes = frags * kFrag;
+  static constexpr int out_row = O32 ? 64 : 48;   // bytes of 16 outputs
+  static constexpr int lds = BUFS * bytes;
+  static_assert(C * out_row <= 2 * kFrag, "outputs in V's place");
+  // LDS offset of a workspace offset behind V
+  static constexpr int behind(int off) { return off - 2 * W::MT * kFrag; }
 };
 
-template <int D, bool O32>
-struct Back {
-  using W = Work<D>;
-  h8 th[2], tl[2], bh[2], bl[O32 ? 2 : 1], eh[W::MT], el[W::MT];
-  f4 gam[W::MT];
-  __device__ __forceinline__ void load(const char* work, int lane, int g) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      th[i] = frag(work + W::t + 2 * i * kFrag, lane);
-      tl[i] = frag(work + W::t + (2 * i + 1) * kFrag, lane);
-      bh[i] = frag(work + W::b(O32) + i * (O32 + 1) * kFrag, lane);
-      if (O32) bl[i] = frag(work + W::b(O32) + (2 * i + 1) * kFrag, lane);
-    }
-#pragma unroll
-    for (int m = 0; m < W::MT; ++m) {
-      eh[m] = frag(work + W::ke + 2 * m * kFrag, lane);
-      el[m] = frag(work + W::ke + (2 * m + 1) * kFrag, lane);
-      gam[m] = *reinterpret_cast<const f4*>(work + W::gam +
-                                            (16 * m + 4 * g) * 4);
-    }
-  }
-};
-
-template <int D, bool O32, int WAVES>
-__global__ void __launch_bounds__(64 * WAVES)
-    __attribute__((amdgpu_waves_per_eu(1, 1)))
+template <int D, bool O32, int WAVES, int PROD, int BUFS>
+__global__ void __launch_bounds__(64 * (WAVES + PROD))
     kda_prefill_state_kernel(PrefillParams p, int act_bf16) {
   using W = Work<D>;
+  using G = Stage<D, O32, WAVES, PROD, BUFS>;
+  constexpr bool kLean = WAVES + PROD > 8;
+  constexpr int kStores = O32 ? 2 : 1;         // output stores of a chunk
+  extern __shared__ __align__(16) char smem[];
   const LayerParams& y = p.y;
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
-  // wave -> (request, head, tile): the tiles of a head on one XCD (blocks
-  // i, i + 8, ..), whose L2 then serves the head's operands to all of them
+  const int wave = uniform(threadIdx.x >> 6);
+  // workgroup -> (request, longest first, head, tiles): the workgroups of a head on one XCD
+  // (blocks i, i + 8, ..), whose L2 then serves its operands to all of them
   constexpr int TB = W::MT / WAVES;            // workgroups of a head
   const int grp = blockIdx.x / (8 * TB), in = blockIdx.x - grp * (8 * TB);
   const int item = grp * 8 + in % 8;
-  const int vt = (in / 8) * WAVES + (threadIdx.x >> 6);
-  if (item >= y.B * y.H) return;
-  const int b = item / y.H, h = item - b * y.H;
+  const int vt0 = in / 8 * WAVES, vt = vt0 + wave;
+  const int rank = item / y.H, h = item - rank * y.H;
+  if (rank >= p.order[-1]) return;
+  const int b = p.order[rank];
   const int2 range = token_range(p, b);
   const int L = range.y - range.x;
-  if (L == 0) return;
   const int dst = y.slots[b];
-  const int64_t oc = int64_t(h) * D + vt * 16 + col;
   if (!live_slot(y, dst)) {
-    for (int t = g; t < L; t += 4)
-      st_elem(y.out, (range.x + t) * y.s_out + oc, 0.0f, y.flags & kOutBf16);
+    if (wave < WAVES)
+      for (int t = g; t < L; t += 4)
+        st_elem(y.out,
+                (range.x + t) * y.s_out + int64_t(h) * D + vt * 16 + col, 0.0f,
+                !O32);
     return;
   }
-  const int src = p.initial ? p.initial[b] : -1;
-  const bool from = live_slot(y, src);
-
   const int64_t step = int64_t(y.H) * W::size(O32);
   const char* work =
       p.work +
       (int64_t(first_slot(range.x, b)) * y.H + h) * W::size(O32);
-  Front<D, O32> f;
-  Back<D, O32> k;
-  f.load(work, vt, lane);
-  k.load(work, lane, g);
+  const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>(
+      (__attribute__((address_space(3))) char*)smem));
+  const int chunks = (L + C - 1) / C;
+  // One loader's share of a chunk's operands: every loader issues the same
+  // number of loads (the last ones again where they do not divide), and
+  // chunks behind the last one are the last one again, so that the number of
+  // loads under way is known at every wait.
+  auto stage = [&](int chunk) {
+    const char* from_work = work + min(chunk, chunks - 1) * step;
+    const int buf = chunk % BUFS, id = wave - WAVES;
+#pragma unroll
+    for (int i = 0; i < G::per_loader; ++i) {
+      const int f = min(i * PROD + id, G::frags - 1);
+      int off;
+      if (f < G::shared_frags) {
+        off = f * kFrag;
+        if (off >= W::v) off += 2 * W::MT * kFrag;
+      } else {
+        const int v = f - G::shared_frags;     // [wave][row tile]
+        off = W::v + ((v & 1) * W::MT + vt0 + (v >> 1)) * kFrag;
+      }
+      load_lds(from_work, off + lane * 16,
+               lds0 + buf * G::bytes + f * kFrag);
+    }
+  };
 
+  // Barrier n of the loop: chunk n's operands are in LDS, and chunk n - 1's
+  // buffer has been read.  After it, chunk n + BUFS - 1 is loaded there.
+  if (wave >= WAVES) {
+#pragma unroll 1
+    for (int n = 0; n < BUFS - 1; ++n) stage(n);
+#pragma unroll 1
+    for (int n = 0; n < chunks; ++n) {
+      wait_vm<(BUFS - 2) * G::per_loader>();
+      __builtin_amdgcn_s_barrier();
+      stage(n + BUFS - 1);
+    }
+    wait_vm<0>();     // no load may land after the workgroup's end
+    return;
+  }
+
+  const int src = p.initial ? p.initial[b] : -1;
+  const bool from = live_slot(y, src);
   f4 S[W::MT];      // S[m][i]: row v = col, channel 16 m + 4 g + i
   const int64_t so = (int64_t(h) * D + vt * 16 + col) * D + 4 * g;
 #pragma unroll
@@ -672,113 +791,189 @@ __global__ void __launch_bounds__(64 * WAVES)
       S[m] = *reinterpret_cast<const f4*>(y.state + src * y.s_slot + so +
                                           16 * m);
   }
-  for (int t0 = 0; t0 < L; t0 += C) {
-    // the last chunk loads its own operands again: in bounds, not used
-    if (t0 + C < L) work += step;
-    // S as the right operand: two 16-channel tiles make one step of 32
+  // a wave's outputs pass through its tile in LDS: 16 bytes a lane go out,
+  // in place of single elements of eight rows
+  constexpr int EO = O32 ? 4 : 2, LPR = EO;    // lanes per row of 16 bytes
+  char* tile = smem + (G::shared_frags + 2 * wave) * kFrag;
+  const int orow = lane / LPR, ocol = lane % LPR;
+  char* oat = static_cast<char*>(y.out) +
+              ((range.x + orow) * y.s_out + int64_t(h) * D + vt * 16) * EO +
+              ocol * 16;
+
+  // S, V, r and c of a column share a power-of-two scale sig, chosen so that
+  // the largest of S and V lies in [2^9, 2^10) and left alone while it stays
+  // in [2^4, 2^10]: |r| <= |V| + |S column| <= 2^10 (1 + sqrt 128) < 65504,
+  // and what the low halves cannot hold is under 2^-28 of the largest.
+  float sig = 1.0f, inv = 1.0f;
+#pragma unroll 1
+  for (int n = 0; n < chunks; ++n) {
+    const int t0 = n * C;
+    lds_barrier();
+    const int buf = n % BUFS;
+    const char* sm = smem + buf * G::bytes + lane * 16;
+    auto op = [&](int off) {
+      return *reinterpret_cast<const h8*>(sm + off);
+    };
+
+    h8 kh[2 * W::KS], kl[2 * W::KS], qh[2 * W::KS], ql[O32 ? 2 * W::KS : 1];
+    f4 r[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      r[i] = *reinterpret_cast<const f4*>(
+          sm + (G::shared_frags + 2 * wave + i) * kFrag);
+#pragma unroll
+    for (int j = 0; j < W::KS; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int a = i * W::KS + j;
+        kh[a] = op(W::kd + 2 * a * kFrag);
+        kl[a] = op(W::kd + (2 * a + 1) * kFrag);
+        qh[a] = op(G::behind(W::qd + a * (O32 + 1) * kFrag));
+        if (O32) ql[a] = op(G::behind(W::qd + (2 * a + 1) * kFrag));
+      }
+    if constexpr (!kLean) __builtin_amdgcn_sched_barrier(0);
+    // scale
     float top = 0.0f;
 #pragma unroll
-    for (int m = 0; m < W::MT; ++m)
+    for (int m = 0; m < W::MT; ++m) top = max_abs(S[m], top);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = fmaxf(top, fabsf(S[m][i]));
-    float up, down;
-    scale_of(column_max(top), up, down);
-    Split s[W::KS];
+    for (int i = 0; i < 2; ++i) {
+      r[i] *= sig;
+      top = max_abs(r[i], top);
+    }
+    uint64_t low = __ballot(top < 16.0f);
+    low &= low >> 32;
+    low &= low >> 16;                     // all four lanes of a column
+    if (__ballot(top > 1024.0f) | (low & 0xffff)) {
+      top = column_max(top);
+      const int e = int(__float_as_uint(top) >> 23);       // biased
+      const int es = int(__float_as_uint(sig) >> 23);
+      int d = 127 + 9 - e;
+      if ((top >= 16.0f && top <= 1024.0f) || e == 0 || e == 255) d = 0;
+      d = min(max(d, 17 - es), 237 - es);     // sig stays in 2^+-110
+      const float f = __uint_as_float(uint32_t(127 + d) << 23);
+      sig *= f;
+      inv = __uint_as_float(uint32_t(254 - es - d) << 23);
 #pragma unroll
-    for (int n = 0; n < W::KS; ++n) {
+      for (int m = 0; m < W::MT; ++m) S[m] *= f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) r[i] *= f;
+    }
+    // S as the right operand: two 16-channel tiles make one step of 32
+    f4 pr[2] = {}, pl[2] = {}, o[2] = {};
+#pragma unroll
+    for (int j = 0; j < W::KS; ++j) {
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int m = 2 * n + (e >> 2);
-        x[e] = m < W::MT ? S[m < W::MT ? m : 0][e & 3] * up : 0.0f;
+        const int m = 2 * j + (e >> 2);
+        x[e] = m < W::MT ? S[m < W::MT ? m : 0][e & 3] : 0.0f;
       }
-      s[n] = split8(x);
-    }
-    down *= 1.0f / kUnit;
-    f4 r[2], o[2];
+      const Split s = split_wide(x);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      r[i] = o[i] = f4{0, 0, 0, 0};
-#pragma unroll
-      for (int n = 0; n < W::KS; ++n) {
-        const int j = i * W::KS + n;
-        r[i] = mfma(f.kh[j], s[n].hi, r[i]);
-        r[i] = mfma(f.kl[j], s[n].hi, r[i]);
-        r[i] = mfma(f.kh[j], s[n].lo, r[i]);
-        o[i] = mfma(f.qh[j], s[n].hi, o[i]);
+      for (int i = 0; i < 2; ++i) {
+        const int a = i * W::KS + j;
+        pr[i] = mfma(kh[a], s.hi, pr[i]);
+        pl[i] = mfma(kl[a], s.hi, pl[i]);
+        o[i] = mfma(qh[a], s.hi, o[i]);
+        pl[i] = mfma(kh[a], s.lo, pl[i]);
         if (O32) {
-          o[i] = mfma(f.ql[j], s[n].hi, o[i]);
-          o[i] = mfma(f.qh[j], s[n].lo, o[i]);
+          o[i] = mfma(ql[a], s.hi, o[i]);
+          o[i] = mfma(qh[a], s.lo, o[i]);
         }
       }
-      r[i] = f.v[i] - r[i] * down;
-      o[i] = o[i] * down;
     }
-    // the next chunk's operands travel during the rest of this one
-    __builtin_amdgcn_sched_barrier(0);
-    f.load(work, vt, lane);
-    __builtin_amdgcn_sched_barrier(0);
-    // c = T r
-    float top_r = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top_r = fmaxf(top_r, fabsf(r[i][e]));
-    scale_of(column_max(top_r), up, down);
-    down *= 1.0f / kUnit;
-    float x[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = r[e >> 2][e & 3] * up;
-    const Split rs = split8(x);
-    float top_c = 0.0f;
+    // operands of the second half, on their way during the next products
+    h8 th[2], tl[2], bh[2], bl[O32 ? 2 : 1], eh[W::MT], el[W::MT];
+    f4 gam[W::MT];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      f4 acc = {0, 0, 0, 0};
-      acc = mfma(k.th[i], rs.hi, acc);
-      acc = mfma(k.tl[i], rs.hi, acc);
-      acc = mfma(k.th[i], rs.lo, acc);
-      r[i] = acc * down;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) top_c = fmaxf(top_c, fabsf(r[i][e]));
+      th[i] = op(W::t + 2 * i * kFrag);
+      tl[i] = op(W::t + (2 * i + 1) * kFrag);
     }
-    scale_of(column_max(top_c), up, down);
-    down *= 1.0f / kUnit;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = r[e >> 2][e & 3] * up;
-    const Split cs = split8(x);
+    for (int m = 0; m < W::MT; ++m)
+      gam[m] = *reinterpret_cast<const f4*>(
+          smem + buf * G::bytes + G::behind(W::gam) + (16 * m + 4 * g) * 4);
+#pragma unroll
+    for (int m = 0; m < W::MT; ++m) {
+      eh[m] = op(W::ke + 2 * m * kFrag);
+      el[m] = op(W::ke + (2 * m + 1) * kFrag);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      bh[i] = op(G::behind(W::b(O32) + i * (O32 + 1) * kFrag));
+      if (O32) bl[i] = op(G::behind(W::b(O32) + (2 * i + 1) * kFrag));
+    }
+    if constexpr (!kLean) __builtin_amdgcn_sched_barrier(0);
+    // r = V - (k e^G) S, c = T r; c is kept at sig / kLate, so that the update
+    // (k e^(G_C - G) carries kLate) adds up at sig: a split that leaves both
+    // operands' low halves above fp16's smallest steps
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      x[e] = r[e >> 2][e & 3] -
+             (pr[e >> 2][e & 3] + pl[e >> 2][e & 3]) * (1.0f / kUnit);
+    const Split rs = split_wide(x);
+    f4 cr[2], cl[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      cr[i] = mfma(th[i], rs.hi, f4{0, 0, 0, 0});
+      cl[i] = mfma(tl[i], rs.hi, f4{0, 0, 0, 0});
+      cl[i] = mfma(th[i], rs.lo, cl[i]);
+    }
+#pragma unroll
+    for (int m = 0; m < W::MT; ++m) S[m] *= gam[m];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      x[e] = (cr[e >> 2][e & 3] + cl[e >> 2][e & 3]) *
+             (1.0f / (kUnit * kLate));
+    const Split cs = split_wide(x);
     // outputs
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      f4 acc = {0, 0, 0, 0};
-      acc = mfma(k.bh[i], cs.hi, acc);
+      o[i] *= 1.0f / kLate;                 // from kUnit sig, as B c is
+      o[i] = mfma(bh[i], cs.hi, o[i]);
       if (O32) {
-        acc = mfma(k.bl[i], cs.hi, acc);
-        acc = mfma(k.bh[i], cs.lo, acc);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = t0 + 16 * i + 4 * g + e;
-        if (t < L)
-          st_elem(y.out, (range.x + t) * y.s_out + oc,
-                  o[i][e] + acc[e] * down, y.flags & kOutBf16);
+        o[i] = mfma(bl[i], cs.hi, o[i]);
+        o[i] = mfma(bh[i], cs.lo, o[i]);
       }
     }
     // the state behind the chunk
 #pragma unroll
     for (int m = 0; m < W::MT; ++m) {
-      f4 acc = {0, 0, 0, 0};
-      acc = mfma(k.eh[m], cs.hi, acc);
-      acc = mfma(k.el[m], cs.hi, acc);
-      acc = mfma(k.eh[m], cs.lo, acc);
-      S[m] = S[m] * k.gam[m] + acc * down;
+      S[m] = mfma(eh[m], cs.hi, S[m]);
+      S[m] = mfma(el[m], cs.hi, S[m]);
+      S[m] = mfma(eh[m], cs.lo, S[m]);
     }
-    __builtin_amdgcn_sched_barrier(0);
-    k.load(work, lane, g);
-    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float v = o[i][e] * (inv * (kLate / kUnit));
+        char* at = tile + buf * G::bytes + (16 * i + 4 * g + e) * G::out_row +
+                   col * EO;
+        if constexpr (O32)
+          *reinterpret_cast<float*>(at) = v;
+        else
+          *reinterpret_cast<__bf16*>(at) = __bf16(v);
+      }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+#pragma unroll
+    for (int i = 0; i < kStores; ++i) {
+      const int row = orow + i * (64 / LPR);
+      const f4 v = *reinterpret_cast<const f4*>(
+          tile + buf * G::bytes + row * G::out_row + ocol * 16);
+      if (t0 + row < L)
+        *reinterpret_cast<f4*>(oat + int64_t(i) * (64 / LPR) * y.s_out * EO) =
+            v;
+    }
+    oat += C * y.s_out * EO;
   }
   float* to = y.state + dst * y.s_slot + so;
 #pragma unroll
-  for (int m = 0; m < W::MT; ++m) *reinterpret_cast<f4*>(to + 16 * m) = S[m];
+  for (int m = 0; m < W::MT; ++m)
+    *reinterpret_cast<f4*>(to + 16 * m) = S[m] * inv;
 
   if (vt == 0 && !(y.flags & kNoConv)) {
     // the newest three raw inputs of the head's channels; each lane reads a
@@ -817,6 +1012,25 @@ __global__ void __launch_bounds__(64 * WAVES)
   }
 }
 
+template <int D, bool O32, int WAVES, int PROD, int BUFS>
+int launch_state(const PrefillParams& p, bool act_bf16, hipStream_t stream) {
+  const size_t lds = Stage<D, O32, WAVES, PROD, BUFS>::lds;
+  static_assert(Stage<D, O32, WAVES, PROD, BUFS>::lds <= 160 * 1024, "LDS");
+  auto kernel = kda_prefill_state_kernel<D, O32, WAVES, PROD, BUFS>;
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(kernel),
+        hipFuncAttributeMaxDynamicSharedMemorySize, int(lds));
+    if (e != hipSuccess) return int(e);
+  }
+  const int64_t groups = (int64_t(p.y.B) * p.y.H + 7) / 8;
+  const int64_t blocks = groups * 8 * (Work<D>::MT / WAVES);
+  if (blocks > 0x7fffffff) return int(hipErrorInvalidValue);
+  launch_kernel(kernel, dim3(uint32_t(blocks)), dim3(64 * (WAVES + PROD)),
+                lds, stream, p, int(act_bf16));
+  return int(hipGetLastError());
+}
+
 template <int D, bool BF16, bool O32>
 int launch_prefill_dim(const PrefillParams& p, hipStream_t stream) {
   const int64_t wgs = int64_t(p.n_slots) * p.y.H;
@@ -832,12 +1046,20 @@ int launch_prefill_dim(const PrefillParams& p, hipStream_t stream) {
   launch_kernel(chunk, dim3(uint32_t(wgs)), dim3(kThreads), lds, stream, p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return int(e);
-  const int64_t groups = (int64_t(p.y.B) * p.y.H + 7) / 8;
-  const int64_t blocks = groups * 8 * Work<D>::MT;
-  if (blocks > 0x7fffffff) return int(hipErrorInvalidValue);
-  launch_kernel(kda_prefill_state_kernel<D, O32, 1>, dim3(uint32_t(blocks)),
-                dim3(64), 0, stream, p, int(BF16));
-  return int(hipGetLastError());
+  constexpr int MT = Work<D>::MT;
+  // Waves that share a workgroup's operands: as few as keep all workgroups
+  // resident at once (a chunk of D = 128 takes 1.45 us with two waves, 1.6
+  // with four, 2.3 with eight), else as many as there are, which load and
+  // hold each operand once.  Eight waves with fp32 outputs would spill.
+  const int64_t items = int64_t(p.y.B) * p.y.H;
+  if constexpr (MT > 4 && !O32)
+    if (items * (MT / 4) > 256)
+      return launch_state<D, O32, 8, 4, 2>(p, BF16, stream);
+  if constexpr (MT > 2)
+    if (items * (MT / 2) > 256)
+      return launch_state<D, O32, 4, 4, 2>(p, BF16, stream);
+  return launch_state<D, O32, (MT < 2 ? MT : 2), 4, (D == 128 && O32 ? 2 : 3)>(
+      p, BF16, stream);
 }
 
 template <int D>

@@ -18,6 +18,8 @@ struct PrefillParams {
   const int32_t* qsl;        // [B + 1]
   const int32_t* initial;    // [B] or null (zeros)
   char* work;
+  int32_t* order;            // [B] requests by falling length; [-1]: how many
+                             // are not empty
   int32_t T;
   int32_t n_slots;           // chunk slots in the workspace
 };

@@ -229,7 +229,8 @@ int64_t prefill_bytes(int64_t T, int64_t B, int64_t H, int64_t D,
     return 0;
   const int64_t slots = kda::prefill_slots(T, B);
   if (slots > kI32Max / H) return 0;
-  return slots * H * kda::prefill_slot_bytes(int(D), out_f32);
+  return slots * H * kda::prefill_slot_bytes(int(D), out_f32) +
+         (B + 4) / 4 * 16;     // the order of the requests, behind the slots
 }
 
 int plan_prefill(const kda_prefill_args* a, bool conv, PrefillPlan* plan) {
@@ -265,6 +266,8 @@ int plan_prefill(const kda_prefill_args* a, bool conv, PrefillPlan* plan) {
   p.work = static_cast<char*>(a->workspace);
   p.T = int32_t(T);
   p.n_slots = int32_t(kda::prefill_slots(T, a->batch));
+  p.order = reinterpret_cast<int32_t*>(
+                p.work + need - (int64_t(a->batch) + 4) / 4 * 16) + 1;
   return KDA_OK;
 }
 
