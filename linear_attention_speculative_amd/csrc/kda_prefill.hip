@@ -126,16 +126,18 @@ struct ChunkCfg {
 template <int D>
 struct ChunkSmem {
   using F = ChunkCfg<D>;
-  float k[C][F::RS];
-  float q[C][F::RS];
-  float p[C][F::RS];    // decays, then their products from the sub-block's
-                        // first token
-  float s[C][F::RS];    // products of the later decays of the sub-block
+  // With P_t and Q_t the products of a sub-block's decays up to token t and
+  // behind it, P_end those of the whole sub-block:
+  float k[C][F::RS];    // k, then k P
+  float q[C][F::RS];    // q, then q P
+  float z[C][F::RS];    // decays, then k Q
+  float end[2][D];      // P_end
+  float rend[2][D];     // 1 / P_end
   float a[C][F::AS];
   float b[C][F::AS];
   float t[C][F::AS];
   float beta[C];
-  int req, before, all, task;
+  int before, all, task;
 };
 
 // Bounds of request b in the token rows, whatever the offsets hold.
@@ -186,6 +188,26 @@ __device__ __forceinline__ void row_norms(const float (&q)[N][2],
   }
 }
 
+// The request that holds a chunk slot, or -1: the last one whose first slot is
+// not behind it, found by every wave for itself, 64 candidates at a time.
+__device__ __forceinline__ int request_of_slot(const PrefillParams& p,
+                                               int slot, int lane) {
+  int lo = 0, n = p.y.B;       // candidates lo .. lo + n - 1
+  while (n > 1) {
+    const int step = (n + 63) / 64;
+    const int i = lane * step;
+    const bool in = i < n && first_slot(token_range(p, lo + i).x, lo + i) <=
+                                 slot;
+    // (offsets that run backwards give some candidate, checked below)
+    const int k = max(int(__popcll(__ballot(in))) - 1, 0) * step;
+    lo += k;
+    n = min(step, n - k);
+  }
+  const int2 r = token_range(p, lo);
+  const int f = first_slot(r.x, lo);
+  return slot >= f && slot < f + (r.y - r.x + C - 1) / C ? uniform(lo) : -1;
+}
+
 // Place of request b in the order of falling lengths (ties by number), written
 // to the order that the state kernel takes its requests in: its workgroups
 // then start with the longest ones, and the short ones fill the gaps.  Empty
@@ -202,6 +224,7 @@ __device__ __forceinline__ void rank_request(const PrefillParams& p, int b,
     before += n > len || (n == len && i < b);
     all += n > 0;
   }
+  __syncthreads();           // the counters are cleared
   atomicAdd(&m.before, before);
   atomicAdd(&m.all, all);
   __syncthreads();
@@ -225,20 +248,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int slot = blockIdx.x / y.H, h = blockIdx.x - slot * y.H;
 
-  // the request of this chunk slot
-  if (tid == 0) {
-    m.req = -1;
-    m.before = m.all = m.task = 0;
-  }
-  for (int i = tid; i < 2 * C * F::AS; i += ChunkCfg<D>::NT) (&m.a[0][0])[i] = 0.0f;
-  __syncthreads();
-  for (int b = tid; b < y.B; b += F::NT) {
-    const int2 r = token_range(p, b);
-    const int f = first_slot(r.x, b);
-    if (slot >= f && slot < f + (r.y - r.x + C - 1) / C) m.req = b;
-  }
-  __syncthreads();
-  const int b = m.req;
+  if (tid == 0) m.before = m.all = m.task = 0;
+  const int b = request_of_slot(p, slot, lane);
   if (b < 0) return;
   const int2 range = token_range(p, b);
   const int first = (slot - first_slot(range.x, b)) * C;   // in the request
@@ -387,7 +398,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
     *reinterpret_cast<float2*>(&m.k[t][2 * cp]) =
         in ? make_float2(val[1][i][0] * nk[i], val[1][i][1] * nk[i])
            : make_float2(0, 0);
-    *reinterpret_cast<float2*>(&m.p[t][2 * cp]) =
+    *reinterpret_cast<float2*>(&m.z[t][2 * cp]) =
         in ? make_float2(exp_(g0), exp_(g1)) : make_float2(1, 1);
 #pragma unroll
     for (int e = 0; e < 2; ++e) val[2][i][e] = in ? val[2][i][e] : 0.0f;
@@ -424,106 +435,129 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
   __syncthreads();
 
   // ---- products of decays from the sub-block's start, and to its end ----
-  float pre[kSub], suf[kSub];
-  const int pc = tid % D, pb = tid / D;       // channel, sub-block
-  bool deep = false;
-  if (pb < 2) {
+  // a thread's channel, sub-block and, at 512 threads, half of its tokens
+  constexpr int HV = F::NT >= 4 * D ? 2 : 1;
+  constexpr int TK = kSub / HV;
+  const int pc = tid % D, pb = tid / D % 2, t1 = tid / (2 * D) * TK;
+  const bool scans = tid < 2 * D * HV;
+  float pre[TK], suf[TK], full = 1.0f;
+  if (scans) {
+    float d[kSub];
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) pre[i] = m.p[pb * kSub + i][pc];
-    suf[kSub - 1] = 1.0f;
+    for (int i = 0; i < kSub; ++i) d[i] = m.z[pb * kSub + i][pc];
+    float f = 1.0f, l = 1.0f;
+    // (selected with constant indexes, so that d stays in registers)
 #pragma unroll
-    for (int i = kSub - 2; i >= 0; --i) suf[i] = suf[i + 1] * pre[i + 1];
+    for (int i = 0; i < kSub; ++i) {
+      f *= d[i];
 #pragma unroll
-    for (int i = 1; i < kSub; ++i) pre[i] *= pre[i - 1];
-    deep = !(pre[kSub - 1] >= 1e-37f);
+      for (int v = 0; v < HV; ++v)
+        if (i / TK == v && t1 == v * TK) pre[i % TK] = f;
+    }
+#pragma unroll
+    for (int i = kSub - 1; i >= 0; --i) {
+#pragma unroll
+      for (int v = 0; v < HV; ++v)
+        if (i / TK == v && t1 == v * TK) suf[i % TK] = l;
+      l *= d[i];
+    }
+    full = f;
   }
-  // Within a sub-block, e^(G_i - G_j) = P_i (1 / P_j) with P the products
-  // from its start, as long as no P leaves the fp32 range (down to 1e-37: 16
-  // tokens of log-decay -5 each stay inside): A and B are then fp32 matrix
-  // products.  Where a channel decays further, the sub-blocks are done by
-  // carrying k_j e^(G_i - G_j) from row to row, which takes any decay (and
-  // 4.5 times as long).
-  deep = __syncthreads_or(deep);
+  // Within a sub-block, e^(G_i - G_j) = (P_i / P_end) Q_j as long as no P
+  // leaves the fp32 range (down to 1e-37: 16 tokens of log-decay -5 each stay
+  // inside): A and B are then fp32 matrix products.  Where a channel decays
+  // further, the sub-blocks are done by carrying k_j e^(G_i - G_j) from row to
+  // row, which takes any decay (and about five times as long).
+  const bool deep = __syncthreads_or(!(full >= 1e-37f));
   if (deep) {
     // waves 2 sb + half; a lane takes four columns j and D/32 channels
     if (wave < 4) {
-    constexpr int CH = D >= 32 ? D / 32 : 1;
-    const int sb = wave >> 1, cl = lane & 31;
-    const int jg = (wave & 1) ? 1 + (lane >> 5) : 3 * (lane >> 5);
-    const int r0 = sb * kSub;
-    const bool on = cl * CH < D;
-    const int c0 = on ? cl * CH : 0;
-    float kd[4][CH] = {};
+      constexpr int CH = D >= 32 ? D / 32 : 1;
+      const int sb = wave >> 1, cl = lane & 31;
+      const int jg = (wave & 1) ? 1 + (lane >> 5) : 3 * (lane >> 5);
+      const int r0 = sb * kSub;
+      const bool on = cl * CH < D;
+      const int c0 = on ? cl * CH : 0;
+      float kd[4][CH] = {};
 #pragma unroll 1
-    for (int i = (wave & 1) ? 4 : 0; i < kSub; ++i) {
-      float ai[CH], ki[CH], qi[CH];
-#pragma unroll
-      for (int e = 0; e < CH; ++e) {
-        ai[e] = m.p[r0 + i][c0 + e];
-        ki[e] = on ? m.k[r0 + i][c0 + e] : 0.0f;
-        qi[e] = on ? m.q[r0 + i][c0 + e] : 0.0f;
-      }
-      float sum[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        sum[j] = sum[4 + j] = 0.0f;
+      for (int i = 0; i < kSub; ++i) {
+        float ai[CH], ki[CH], qi[CH];
 #pragma unroll
         for (int e = 0; e < CH; ++e) {
-          kd[j][e] = i == 4 * jg + j ? ki[e] : kd[j][e] * ai[e];
-          sum[j] = __builtin_fmaf(ki[e], kd[j][e], sum[j]);
-          sum[4 + j] = __builtin_fmaf(qi[e], kd[j][e], sum[4 + j]);
+          ai[e] = m.z[r0 + i][c0 + e];
+          ki[e] = on ? m.k[r0 + i][c0 + e] : 0.0f;
+          qi[e] = on ? m.q[r0 + i][c0 + e] : 0.0f;
+        }
+        float sum[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          sum[j] = sum[4 + j] = 0.0f;
+#pragma unroll
+          for (int e = 0; e < CH; ++e) {
+            kd[j][e] = i == 4 * jg + j ? ki[e] : kd[j][e] * ai[e];
+            sum[j] = __builtin_fmaf(ki[e], kd[j][e], sum[j]);
+            sum[4 + j] = __builtin_fmaf(qi[e], kd[j][e], sum[4 + j]);
+          }
+        }
+        float tot = transpose_sum<16, 8>(sum, lane & 15);
+        tot += __int_as_float(
+            __builtin_amdgcn_ds_swizzle(__float_as_int(tot), 0x401F));
+        const int v = (lane & 15) >> 1, j = 4 * jg + (v & 3);
+        if ((lane & 17) == 0) {
+          if (v >= 4)
+            m.b[r0 + i][r0 + j] = tot;
+          else
+            m.a[r0 + i][r0 + j] = i > j ? tot : 0.0f;
         }
       }
-      float tot = transpose_sum<16, 8>(sum, lane & 15);
-      tot += __int_as_float(
-          __builtin_amdgcn_ds_swizzle(__float_as_int(tot), 0x401F));
-      const int v = (lane & 15) >> 1, j = 4 * jg + (v & 3);
-      if ((lane & 17) == 0) {
-        if (v >= 4)
-          m.b[r0 + i][r0 + j] = tot;
-        else
-          m.a[r0 + i][r0 + j] = i > j ? tot : 0.0f;
-      }
-    }
     }
     __syncthreads();
   }
-  if (pb < 2) {
+  if (scans) {
+    // the column's k, q and decays make way for k P, q P and k Q
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) {
-      m.p[pb * kSub + i][pc] = pre[i];
-      m.s[pb * kSub + i][pc] = suf[i];
+    for (int i = 0; i < TK; ++i) {
+      const int t = pb * kSub + t1 + i;
+      const float kv = m.k[t][pc];
+      m.k[t][pc] = kv * pre[i];
+      m.q[t][pc] *= pre[i];
+      m.z[t][pc] = kv * suf[i];
+    }
+    if (t1 == 0) {
+      m.end[pb][pc] = full;
+      m.rend[pb][pc] = rcp_(full);
     }
   }
   __syncthreads();
 
   const int col = lane & 15, g = lane >> 4;
-  // One 16 x 16 block of A (rows k) or B (rows q) as a matrix product: a
-  // diagonal block, or the one of rows 16.. and columns ..15, whose decays
-  // split at its border into two factors of at most 1.  Lanes take the
-  // summed channels in the order 16 u + 4 g + i.
+  // One 16 x 16 block of A (rows k P) or B (rows q P) as a matrix product: a
+  // diagonal block (divided by P_end), or the one of rows 16.. and columns
+  // ..15, whose decays split at its border into two factors of at most 1.
+  // Lanes take the summed channels in the order 16 u + 4 g + i.
   auto block = [&](const float (*rows)[F::RS], float (*dst)[F::AS], int r0,
                    int c0, bool strict) {
     const bool diag = r0 == c0;
-    f4 acc = {0, 0, 0, 0};
-#pragma unroll 2
+    f4 acc = {0, 0, 0, 0}, acc2 = {0, 0, 0, 0};
+#pragma unroll
     for (int u = 0; u < D / 16; ++u) {
       const int c = 16 * u + 4 * g;
-      const f4 x = *reinterpret_cast<const f4*>(&rows[r0 + col][c]);
-      const f4 xp = *reinterpret_cast<const f4*>(&m.p[r0 + col][c]);
-      const f4 z = *reinterpret_cast<const f4*>(&m.k[c0 + col][c]);
-      const f4 zp = *reinterpret_cast<const f4*>(
-          diag ? &m.p[c0 + col][c] : &m.s[c0 + col][c]);
+      f4 x = *reinterpret_cast<const f4*>(&rows[r0 + col][c]);
+      const f4 z = *reinterpret_cast<const f4*>(&m.z[c0 + col][c]);
+      if (diag)
+        x *= *reinterpret_cast<const f4*>(&m.rend[r0 / kSub][c]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(
-            x[i] * xp[i], z[i] * (diag ? rcp_(zp[i]) : zp[i]), acc, 0, 0, 0);
+      for (int i = 0; i < 4; i += 2) {
+        acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i], z[i], acc, 0, 0, 0);
+        acc2 = __builtin_amdgcn_mfma_f32_16x16x4f32(x[i + 1], z[i + 1], acc2,
+                                                    0, 0, 0);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = 4 * g + i;
       const bool in = !diag || (strict ? r > col : r >= col);
-      dst[r0 + r][c0 + col] = in ? acc[i] : 0.0f;
+      dst[r0 + r][c0 + col] = in ? acc[i] + acc2[i] : 0.0f;
     }
   };
 #pragma unroll 1
@@ -541,16 +575,29 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
     // block below them, -X2 (beta A21) X1, by products
     const int blk = (lane >> 4) & 1, r0 = blk * kSub;
     float x[kSub];
+    f4 row[4] = {}, next[4];
+    float bt = m.beta[r0];
 #pragma unroll
     for (int i = 0; i < kSub; ++i) {
-      float acc = 0.0f;
+      // the next row travels while this one is used
+      const float bn = i + 1 < kSub ? m.beta[r0 + i + 1] : 0.0f;
 #pragma unroll
-      for (int j = 0; j < i; ++j)
-        acc = __builtin_fmaf(m.a[r0 + i][r0 + j], x[j], acc);
-      x[i] = (i == col ? 1.0f : 0.0f) - m.beta[r0 + i] * acc;
+      for (int j = 0; j < (i + 4) / 4; ++j)
+        if (i + 1 < kSub)
+          next[j] = *reinterpret_cast<const f4*>(&m.a[r0 + i + 1][r0 + 4 * j]);
+      float acc = 0.0f, acc2 = 0.0f;
+#pragma unroll
+      for (int j = 0; j < i; ++j) {
+        float& s = j % 2 ? acc2 : acc;
+        s = __builtin_fmaf(row[j / 4][j % 4], x[j], s);
+      }
+      x[i] = (i == col ? 1.0f : 0.0f) - bt * (acc + acc2);
       // finish this row here: otherwise every row of A is loaded up front,
       // into 120 registers
       asm volatile("" : "+v"(x[i]) : : "memory");
+      bt = bn;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) row[j] = next[j];
     }
     // lanes 32.. repeat lanes ..31 and write the same values
     const float scale = blk ? 1.0f : m.beta[col];
@@ -614,8 +661,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
         const int c = 32 * s + (e < 4 ? 4 * g + e : 16 + 4 * g + e - 4);
         x[e] = z[e] = 0.0f;
         if (c < D) {
-          const float d =
-              kUnit * m.p[t][c] * (r ? m.p[kSub - 1][c] : 1.0f);
+          const float d = r ? kUnit * m.end[0][c] : kUnit;
           x[e] = m.k[t][c] * d;
           z[e] = m.q[t][c] * d;
         }
@@ -627,11 +673,11 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
       if (O32) store_frag(work + W::qd + (2 * task + 1) * kFrag, lane, q.lo);
     } else {
       const int mt = task - NKD, c = 16 * mt + col;
-      const float late = m.p[C - 1][c];
+      const float late = m.end[1][c];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int t = e < 4 ? 4 * g + e : kSub + 4 * g + e - 4;
-        x[e] = kLate * m.k[t][c] * m.s[t][c] * (e < 4 ? late : 1.0f);
+        x[e] = kLate * m.z[t][c] * (e < 4 ? late : 1.0f);
       }
       const Split a = split8(x);
       store_frag(work + W::ke + 2 * mt * kFrag, lane, a.hi);
@@ -640,7 +686,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
   }
   if (tid < D)
     reinterpret_cast<float*>(work + W::gam)[tid] =
-        m.p[kSub - 1][tid] * m.p[C - 1][tid];
+        m.end[0][tid] * m.end[1][tid];
 }
 
 // ---- second kernel ----------------------------------------------------------
