@@ -40,6 +40,9 @@
  *   kda_step_tables -- a step's index arrays built on the GPU from request
  *       lengths: token offsets, new blocks, state slots, cache slots.
  *
+ *   kda_sample -- tokens from logits and given random numbers, and the
+ *       accepted counts of draft windows that the commit plan reads.
+ *
  * plus host-only argument checks mirroring the pages' validation
  * (kernels page `_check_layouts`, `can_use_cute_recoverssm`; ops page
  * `kda_recoverssm_verify`, `KDARecoverSSMCommitContext.create/commit`).
@@ -459,6 +462,48 @@ typedef struct {
                                           num_free when they ran out */
 } kda_tables_args;
 
+/* Arguments of kda_sample.  For each row x of logits (V values), with the
+   parameters of its request (row m belongs to the request b with
+   query_start_loc[b] <= m < query_start_loc[b+1]; without query_start_loc,
+   b = m), over the order of falling x, ties by rising index:
+     w_i = exp((x_i - max x) / temperature);
+     the longest prefix with every w_i >= min_p and at most top_k tokens is
+     kept, then its shortest prefix with at least top_p of its mass;
+     token = the lowest kept i with sum of w_j over kept j <= i  >  u * mass,
+   u = uniform[m].  temperature <= 0: the lowest index of the maximum.
+   top_k <= 0, top_p >= 1, min_p <= 0, NaN parameters and NULL arrays leave
+   their filter (or temperature 1) out; top_p <= 0 keeps one token; u is
+   held to [0, 1).  NaN logits count as -inf; a row without any value above
+   -inf gives token -1.  Each w is rounded
+   to 46 binary places (62 - ceil(log2 V) where that is fewer) and summed as
+   an integer: no order of additions changes a token.  V up to 2^20.
+   Rows before query_start_loc[0] or from query_start_loc[batch] on are not
+   touched.
+   Acceptance (draft_tokens given): request b's window holds the tokens
+   draft_tokens[s .. e) (s, e from query_start_loc); row m's token is checked
+   against draft_tokens[m + 1], and num_accepted[b] = 1 + the number of
+   leading matches, in [1, e - s] (0 for an empty window): what
+   kda_commit_plan takes as num_accepted_tokens.  next_tokens[b] is the
+   token of row s + num_accepted[b] - 1 (-1 for an empty window). */
+typedef struct {
+  kda_tensor logits;              /* F32 or BF16 [M, V], rows contiguous */
+  const float* uniform;           /* [M] */
+  const float* temperature;       /* [batch] each, or NULL */
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const int32_t* query_start_loc; /* [batch + 1], or NULL: batch = M */
+  const int32_t* draft_tokens;    /* [M] or NULL */
+  int32_t* tokens;                /* [M] output */
+  int32_t* num_accepted;          /* [batch] outputs, given iff draft_tokens */
+  int32_t* next_tokens;
+  void* workspace;                /* device, 16-byte aligned, at least
+                                     kda_sample_workspace_size(M, V) bytes */
+  int64_t workspace_bytes;
+  int32_t batch;
+  int32_t pad_;
+} kda_sample_args;
+
 /* Library ABI version (KDA_ABI_VERSION). */
 int kda_abi_version(void);
 
@@ -574,6 +619,14 @@ int kda_decode_qkv(const kda_decode_args* args, void* stream);
 /* Host-only validation of the step tables' arguments, then the launches. */
 int kda_check_step_tables(const kda_tables_args* args);
 int kda_step_tables(const kda_tables_args* args, void* stream);
+
+/* Bytes of workspace that sampling `rows` rows of `vocab` logits needs (0
+   for sizes that the checks refuse). */
+int64_t kda_sample_workspace_size(int64_t rows, int64_t vocab);
+
+/* Host-only validation of the sampling arguments, then the launches. */
+int kda_check_sample(const kda_sample_args* args);
+int kda_sample(const kda_sample_args* args, void* stream);
 
 /* Launch a one-workgroup kernel that sets counter[0..n) to 0 on `stream`
    (for a counter left non-zero by an aborted launch).  Uses no memset

@@ -24,6 +24,7 @@ from .serving import (  # noqa: F401
     check_decode_qkv,
     check_prefill,
     check_prefill_qkv,
+    check_sample,
     check_step_tables,
     conv_prefill,
     conv_update_decode,
@@ -32,6 +33,9 @@ from .serving import (  # noqa: F401
     prefill_args,
     prefill_qkv,
     prefill_workspace_size,
+    sample,
+    sample_args,
+    sample_workspace_size,
     step_tables,
     tables_args,
 )

@@ -42,6 +42,7 @@ EXPORTED = (
     "kda_check_decode", "kda_conv_update_decode",
     "kda_check_decode_qkv", "kda_decode_qkv",
     "kda_check_step_tables", "kda_step_tables",
+    "kda_sample_workspace_size", "kda_check_sample", "kda_sample",
 )
 
 
@@ -167,6 +168,18 @@ class KdaTablesArgs(Structure):
     ]
 
 
+class KdaSampleArgs(Structure):
+    _fields_ = [
+        ("logits", KdaTensor), ("uniform", c_void_p),
+        ("temperature", c_void_p), ("top_k", c_void_p), ("top_p", c_void_p),
+        ("min_p", c_void_p), ("query_start_loc", c_void_p),
+        ("draft_tokens", c_void_p), ("tokens", c_void_p),
+        ("num_accepted", c_void_p), ("next_tokens", c_void_p),
+        ("workspace", c_void_p), ("workspace_bytes", c_int64),
+        ("batch", c_int32), ("pad_", c_int32),
+    ]
+
+
 _LIB = None
 
 
@@ -227,12 +240,15 @@ def load() -> ctypes.CDLL:
                                           POINTER(c_int32)]
     lib.kda_prefill_workspace_size.restype = c_int64
     lib.kda_prefill_workspace_size.argtypes = [c_int64] * 4 + [c_int32] * 2
+    lib.kda_sample_workspace_size.restype = c_int64
+    lib.kda_sample_workspace_size.argtypes = [c_int64] * 2
     for check, launches, args in (
             ("kda_check_prefill", ("kda_conv_prefill",), KdaPrefillArgs),
             ("kda_check_prefill_qkv", ("kda_prefill_qkv",), KdaPrefillArgs),
             ("kda_check_decode", ("kda_conv_update_decode",), KdaDecodeArgs),
             ("kda_check_decode_qkv", ("kda_decode_qkv",), KdaDecodeArgs),
-            ("kda_check_step_tables", ("kda_step_tables",), KdaTablesArgs)):
+            ("kda_check_step_tables", ("kda_step_tables",), KdaTablesArgs),
+            ("kda_check_sample", ("kda_sample",), KdaSampleArgs)):
         getattr(lib, check).restype = c_int
         getattr(lib, check).argtypes = [POINTER(args)]
         for name in launches:

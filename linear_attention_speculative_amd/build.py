@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = ["kda_verify_d128.hip", "kda_verify_d64.hip", "kda_verify_d32.hip",
            "kda_verify_d16.hip", "kda_verify.hip", "kda_commit.hip",
            "kda_plan.hip", "kda_prefill.hip", "kda_decode.hip",
-           "kda_tables.hip", "kda_api.cpp", "kda_serving_api.cpp"]
+           "kda_tables.hip", "kda_sample.hip", "kda_api.cpp",
+           "kda_serving_api.cpp"]
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
 # Packed fp32 VALU ops are disabled for all device code.

@@ -1,0 +1,756 @@
+// Sampling from logits on gfx950: temperature, top-k, min-p and top-p, the
+// token from a given uniform number, and the acceptance of draft windows.
+//
+// For a row x with maximum m: w_i = 2^-d_i, d_i = (m - x_i) log2(e) / T, held
+// as integers round(w 2^s) with s <= 46 and sums below 2^62.  All three
+// filters keep a prefix of the order (x falling, index rising), so the kept
+// set is one threshold pair (value, index); the token is the lowest kept index
+// whose running weight passes u times the whole.  Integer sums make the result
+// independent of the order in which lanes add; the weights come from fp64
+// arithmetic (a cubic share of the time of an fp32 exponential, and a token at
+// the border of two sums of 10^5 terms needs it).
+//
+// A full sort is avoided.  Two kernels:
+//
+//   kda_group_max_kernel reads the logits once (the floor: HBM) and leaves the
+//   maximum of every group of 512.
+//   kda_sample_kernel, one workgroup a row, reads only what it still needs.
+//   Greedy rows read one group.  With top-k <= groups, the k-th largest group
+//   maximum bounds the k-th largest value from below: only groups at or above
+//   it are read again, and the few values there go to a list in LDS.  Larger
+//   k and top-p alone first take a histogram over 2048 bins of 1/16 octave in
+//   d (of counts, or of weights), whose bin at the border bounds the list.  The
+//   list is sorted, cut, and summed.  Rows that keep more than the list holds
+//   find the threshold by a radix search instead (any size, more passes), and
+//   rows without top-k and top-p sum their groups in order.
+#include "kda_serving.hpp"
+
+namespace kda {
+namespace {
+
+constexpr int kGroup = 512;          // logits of a group
+constexpr int kMaxGroups = 2048;     // V up to 2^20
+constexpr int kMaxThreads = 256;     // group maximum kernel
+constexpr int kPerWg = 4 * 4;        // its groups per workgroup
+constexpr int kRowThreads = 1024;    // row kernel
+constexpr int kWaves = kRowThreads / 64;
+constexpr int kList = 4096;          // entries of the sorted list
+constexpr int kBins = 2048;
+
+__device__ __forceinline__ float logit(const SampleParams& p, const char* row,
+                                       int i, bool bf16) {
+  return bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(row)[i])
+              : reinterpret_cast<const float*>(row)[i];
+}
+
+// The request of row m, or -1 for a row outside every request.
+__device__ __forceinline__ int request_of_row(const SampleParams& p, int m,
+                                              int lane) {
+  if (p.qsl == nullptr) return m < p.B ? m : -1;
+  if (p.B == 0) return -1;
+  int lo = 0, n = p.B;
+  while (n > 1) {      // last b with qsl[b] <= m, 64 candidates at a time
+    const int step = (n + 63) / 64;
+    const int i = lane * step;
+    const bool in = i < n && p.qsl[lo + i] <= m;
+    const int k = max(int(__popcll(__ballot(in))) - 1, 0) * step;
+    lo += k;
+    n = min(step, n - k);
+  }
+  lo = uniform(lo);
+  return p.qsl[lo] <= m && m < p.qsl[lo + 1] ? lo : -1;
+}
+
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) v = fmaxf(v, __shfl_xor(v, s));
+  return v;
+}
+
+// Eight consecutive logits of an aligned row as one or two 16-byte loads.
+template <bool BF16>
+__device__ __forceinline__ void load8(const char* row, int i, float (&x)[8]) {
+  if constexpr (BF16) {
+    const uint4 u = *reinterpret_cast<const uint4*>(row + 2 * int64_t(i));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      x[2 * e] = __uint_as_float(w[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const f4 v = *reinterpret_cast<const f4*>(row + 4 * int64_t(i) + 16 * h);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * h + e] = v[e];
+    }
+  }
+}
+
+// A group's logits over the lanes of a wave: element e of lane l is logit
+// first + 8 l + e (aligned rows) or first + 64 e + l; index(e) tells which.
+// Behind the row's end -inf, and -inf for NaN.
+template <bool BF16, bool VEC>
+struct Group {
+  float x[8];
+  int first;
+  __device__ __forceinline__ int index(int e) const {
+    const int lane = threadIdx.x & 63;
+    return VEC ? first + 8 * lane + e : first + 64 * e + lane;
+  }
+  __device__ __forceinline__ void load(const char* row, int g, int V) {
+    typedef typename Act<BF16>::T T;
+    first = g * kGroup;
+    const int lane = threadIdx.x & 63;
+    if (VEC && first + kGroup <= V) {
+      load8<BF16>(row, first + 8 * lane, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = min(index(e), V - 1);
+        x[e] = Act<BF16>::f(reinterpret_cast<const T*>(row)[i]);
+        if (index(e) >= V) x[e] = -__builtin_inff();
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (!(x[e] == x[e])) x[e] = -__builtin_inff();
+  }
+};
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads)
+    kda_group_max_kernel(SampleParams p, int G, int per_row) {
+  const int m = blockIdx.x / per_row, part = blockIdx.x - m * per_row;
+  if (p.qsl && (m < p.qsl[0] || m >= p.qsl[p.B])) return;
+  const char* row = static_cast<const char*>(p.logits) +
+                    m * p.s_row * (BF16 ? 2 : 4);
+  float* out = reinterpret_cast<float*>(p.work) + int64_t(m) * G;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int g0 = part * kPerWg + wave * (kPerWg / 4);
+  Group<BF16, VEC> v[kPerWg / 4];
+#pragma unroll
+  for (int i = 0; i < kPerWg / 4; ++i) v[i].load(row, min(g0 + i, G - 1), p.V);
+#pragma unroll
+  for (int i = 0; i < kPerWg / 4; ++i) {
+    float t = v[i].x[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) t = fmaxf(t, v[i].x[e]);
+    t = wave_max(t);
+    if (lane == 0 && g0 + i < G) out[g0 + i] = t;
+  }
+}
+
+// ---- row kernel -----------------------------------------------------------
+
+// fp32 as an unsigned number of the same order, and back.
+__device__ __forceinline__ uint32_t ordered(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);      // -0 counts as 0
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float unordered(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
+struct RowSmem {
+  union {
+    struct {
+      uint64_t key[kList];      // ordered(x) << 32 | ~index
+      uint64_t w[kList];
+    } list;
+    struct {
+      uint32_t count[kBins];
+      uint64_t mass[kBins];
+    } hist;
+    uint64_t group[kMaxGroups];
+  };
+  float gmax[kMaxGroups];
+  double table[16];             // 2^(-j/16)
+  uint64_t red[kWaves + 1];
+  uint32_t n;
+  int found, pick;
+  uint64_t before, value;
+};
+
+// Weight of a logit: 2^-d as a real number and as an integer.
+struct Weights {
+  const double* table;
+  double c;                     // log2(e) / T
+  float m, c16;                 // maximum; 16 c, for the bins
+  int s;                        // binary places
+  double min_p;
+  // 0 for -inf and whatever lies 2^128 below the maximum
+  __device__ __forceinline__ double real(float x) const {
+    const double d = x == m ? 0.0 : (double(m) - double(x)) * c;
+    if (!(d < 128.0) || x == -__builtin_inff()) return 0.0;
+    const int e = int(d * 16.0);
+    const double z = (double(e) * 0.0625 - d) * 0.6931471805599453094;
+    double q = 1.0 / 5040.0;    // e^z, |z| < 0.0434, to 2^-52
+    q = fma(q, z, 1.0 / 720.0);
+    q = fma(q, z, 1.0 / 120.0);
+    q = fma(q, z, 1.0 / 24.0);
+    q = fma(q, z, 1.0 / 6.0);
+    q = fma(q, z, 0.5);
+    q = fma(q, z, 1.0);
+    q = fma(q, z, 1.0);
+    return ldexp(q * table[e & 15], -(e >> 4));
+  }
+  // rounded by an addition whose last binary place is 1
+  __device__ __forceinline__ uint64_t whole(double w) const {
+    return uint64_t(__double_as_longlong(ldexp(w, s) + 0x1p52)) &
+           ((uint64_t(1) << 52) - 1);
+  }
+  __device__ __forceinline__ bool above_min(double w) const {
+    return w >= min_p && w > 0.0;
+  }
+  // 1/16 octave bins of d: never falls as x falls
+  __device__ __forceinline__ int bin(float x) const {
+    if (x == m) return 0;
+    const float b = (m - x) * c16;
+    return b < float(kBins - 1) ? int(b) : kBins - 1;
+  }
+};
+
+// Threshold pair: a logit is kept if it is larger than `key`, or equal and at
+// an index of at most `index`.
+struct Threshold {
+  uint32_t key;
+  int index;
+  __device__ __forceinline__ bool keeps(float x, int i) const {
+    const uint32_t k = ordered(x);
+    return k > key || (k == key && i <= index);
+  }
+};
+
+template <bool BF16, bool VEC>
+struct Row {
+  const char* at;
+  int V, G;
+  RowSmem& sm;
+  // f(x, index) for the logits of the groups that `use(g)` takes, a group to
+  // a wave; -inf is left out.
+  template <class Use, class F>
+  __device__ __forceinline__ void each(Use use, F f) const {
+    const int wave = uniform(threadIdx.x >> 6);
+#pragma unroll 1
+    for (int g = wave; g < G; g += kWaves) {
+      if (!use(g)) continue;
+      Group<BF16, VEC> v;
+      v.load(at, g, V);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (v.x[e] > -__builtin_inff()) f(v.x[e], v.index(e));
+    }
+  }
+};
+
+__device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) v += __shfl_xor((unsigned long long)v, s);
+  return v;
+}
+
+// Inclusive prefix sum over the workgroup; red[kWaves] is the total until the
+// next call.
+__device__ __forceinline__ uint64_t row_scan(uint64_t v, uint64_t* red) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const uint64_t o = __shfl_up((unsigned long long)v, s);
+    if (lane >= s) v += o;
+  }
+  __syncthreads();
+  if (lane == 63) red[w] = v;
+  __syncthreads();
+  uint64_t base = 0, total = 0;
+#pragma unroll 1
+  for (int j = 0; j < kWaves; ++j) {
+    if (j < w) base += red[j];
+    total += red[j];
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) red[kWaves] = total;
+  __syncthreads();
+  return base + v;
+}
+
+// First index i of a[0 .. n) (n <= kPer * kRowThreads) whose inclusive prefix
+// sum reaches `target`; sm.found = i (or -1), sm.before = the sum before it,
+// sm.value = a[i].  Returns the total of a.
+template <int kPer, class T>
+__device__ __forceinline__ uint64_t find_prefix(RowSmem& sm, const T* a, int n,
+                                                uint64_t target) {
+  uint64_t v[kPer], own = 0;
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = threadIdx.x * kPer + j;
+    v[j] = i < n ? uint64_t(a[i]) : 0;
+    own += v[j];
+  }
+  if (threadIdx.x == 0) sm.found = -1;
+  uint64_t sum = row_scan(own, sm.red) - own;
+  const uint64_t total = sm.red[kWaves];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int i = threadIdx.x * kPer + j;
+    if (i < n && sum < target && sum + v[j] >= target) {
+      sm.found = i;
+      sm.before = sum;
+      sm.value = v[j];
+    }
+    sum += v[j];
+  }
+  __syncthreads();
+  return total;
+}
+
+// Sort of the list's first n keys, falling; n is padded to a power of two with
+// zeros.
+__device__ __forceinline__ void sort_list(uint64_t* key, int n) {
+  int size = 64;
+  while (size < n) size <<= 1;
+  for (int i = n + threadIdx.x; i < size; i += kRowThreads) key[i] = 0;
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 2; k <= size; k <<= 1) {
+#pragma unroll 1
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int t = threadIdx.x; t < size / 2; t += kRowThreads) {
+        const int i = 2 * t - (t & (j - 1));      // bit j clear
+        const uint64_t a = key[i], b = key[i + j];
+        if ((a < b) == ((i & k) == 0)) {
+          key[i] = b;
+          key[i + j] = a;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// Target of a share of a whole: the least integer >= share * mass, at least 1
+// and at most mass.
+__device__ __forceinline__ uint64_t share_of(double share, uint64_t mass) {
+  const double t = ceil(share * double(mass));
+  const uint64_t v = t >= 1.0 ? uint64_t(t) : 1;
+  return v < mass ? v : mass;
+}
+
+// Sums of v before each element of a wave's group, in the order of indexes.
+template <bool VEC>
+__device__ __forceinline__ void group_prefix(const uint64_t (&v)[8],
+                                             uint64_t (&pre)[8]) {
+  const int lane = threadIdx.x & 63;
+  const auto scan = [&](uint64_t x) {
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const uint64_t o = __shfl_up((unsigned long long)x, s);
+      if (lane >= s) x += o;
+    }
+    return x;
+  };
+  if constexpr (VEC) {            // a lane's elements are neighbours
+    uint64_t own = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      pre[e] = own;
+      own += v[e];
+    }
+    const uint64_t base = scan(own) - own;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) pre[e] += base;
+  } else {                        // neighbours are in neighbouring lanes
+    uint64_t base = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint64_t upto = scan(v[e]);
+      pre[e] = base + upto - v[e];
+      base += __shfl((unsigned long long)upto, 63);
+    }
+  }
+}
+
+// The threshold of the first `target` in count or weight (what(x) each) among
+// the logits that `thr` keeps and that pass min-p: radix search over the
+// ordered keys, 11, 11 and 10 bits a pass, then the last tie's index.
+template <bool BF16, bool VEC, class What>
+__device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
+                                            const Weights& wt, Threshold thr,
+                                            uint64_t target, What what) {
+  RowSmem& sm = row.sm;
+  const auto all = [](int) { return true; };
+  uint32_t prefix = 0, mask = 0;
+  uint64_t before = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const int bins = pass == 2 ? 1024 : 2048;
+    for (int i = threadIdx.x; i < bins; i += kRowThreads) sm.hist.mass[i] = 0;
+    __syncthreads();
+    row.each(all, [&](float x, int i) {
+      const uint32_t k = ordered(x);
+      if ((k & mask) != prefix || !thr.keeps(x, i)) return;
+      const double w = wt.real(x);
+      if (!wt.above_min(w)) return;
+      // bins in falling order
+      atomicAdd((unsigned long long*)&sm.hist
+                    .mass[bins - 1 - ((k >> shift) & (bins - 1))],
+                (unsigned long long)what(w));
+    });
+    __syncthreads();
+    find_prefix<2>(sm, sm.hist.mass, bins, target - before);
+    const int f = max(sm.found, 0);
+    before += sm.before;
+    prefix |= uint32_t(bins - 1 - f) << shift;
+    mask |= uint32_t(bins - 1) << shift;
+    __syncthreads();
+  }
+  // ties: each counts the same; the index of the last one kept
+  const uint64_t one = what(wt.real(unordered(prefix)));
+  const uint64_t left = target - before;
+  const uint64_t rank = one > 0 ? (left + one - 1) / one : 1;
+  for (int i = threadIdx.x; i < row.G; i += kRowThreads) sm.group[i] = 0;
+  __syncthreads();
+  row.each(all, [&](float x, int i) {
+    if (ordered(x) == prefix && thr.keeps(x, i))
+      atomicAdd((unsigned long long*)&sm.group[i / kGroup], 1ull);
+  });
+  __syncthreads();
+  find_prefix<2>(sm, sm.group, row.G, rank);
+  const int g = sm.found;
+  const uint64_t seen = sm.before;
+  if (threadIdx.x == 0) sm.pick = row.V - 1;
+  __syncthreads();
+  if (g >= 0 && threadIdx.x < 64) {
+    Group<BF16, VEC> v;
+    v.load(row.at, g, row.V);
+    uint64_t tie[8], pre[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      tie[e] = v.x[e] > -__builtin_inff() && ordered(v.x[e]) == prefix &&
+               thr.keeps(v.x[e], v.index(e));
+    group_prefix<VEC>(tie, pre);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (tie[e] && seen + pre[e] + 1 == rank) sm.pick = v.index(e);
+  }
+  __syncthreads();
+  const Threshold t{prefix, sm.pick};
+  __syncthreads();
+  return t;
+}
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kRowThreads)
+    kda_sample_kernel(SampleParams p, int G, int places) {
+  extern __shared__ __align__(16) char smem[];
+  RowSmem& sm = *reinterpret_cast<RowSmem*>(smem);
+  const int m = blockIdx.x, tid = threadIdx.x;
+  const int b = request_of_row(p, m, tid & 63);
+  if (b < 0) return;
+  const float T = p.temperature && p.temperature[b] == p.temperature[b]
+                      ? p.temperature[b] : 1.0f;
+  const int k = p.top_k ? p.top_k[b] : 0;
+  // (comparisons written so that NaN switches a filter off)
+  const float top_p = p.top_p && p.top_p[b] < 1.0f ? p.top_p[b] : 1.0f;
+  const float min_p = p.min_p && p.min_p[b] > 0.0f ? p.min_p[b] : 0.0f;
+  const float u = p.uniform[m] > 0.0f ? p.uniform[m] : 0.0f;
+
+  const float* gm = reinterpret_cast<const float*>(p.work) + int64_t(m) * G;
+  const Row<BF16, VEC> row{static_cast<const char*>(p.logits) +
+                               m * p.s_row * (BF16 ? 2 : 4),
+                           p.V, G, sm};
+  float top = -__builtin_inff();
+  for (int g = tid; g < G; g += kRowThreads) {
+    const float v = gm[g];
+    sm.gmax[g] = v;
+    top = fmaxf(top, v);
+  }
+  if (tid < 16) sm.table[tid] = exp2(-0.0625 * tid);
+  top = wave_max(top);
+  if ((tid & 63) == 0) sm.red[tid >> 6] = __float_as_uint(top);
+  if (tid == 0) {
+    sm.found = G;
+    sm.pick = p.V;
+    sm.n = 0;
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int j = 0; j < kWaves; ++j)
+    top = fmaxf(top, __uint_as_float(uint32_t(sm.red[j])));
+  if (top == -__builtin_inff()) {
+    if (tid == 0) p.tokens[m] = -1;
+    return;
+  }
+
+  if (T <= 0.0f || k == 1 || top_p <= 0.0f) {
+    // the lowest index of the maximum
+    for (int g = tid; g < G; g += kRowThreads)
+      if (sm.gmax[g] == top) atomicMin(&sm.found, g);
+    __syncthreads();
+    if (tid < 64) {
+      Group<BF16, VEC> v;
+      v.load(row.at, min(sm.found, G - 1), p.V);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (v.x[e] == top) atomicMin(&sm.pick, v.index(e));
+    }
+    __syncthreads();
+    if (tid == 0) p.tokens[m] = sm.pick;
+    return;
+  }
+
+  const double c = 1.4426950408889634074 / double(T);
+  const Weights wt{sm.table, c, top, float(16.0 * c), places,
+                   double(fminf(min_p, 1.0f))};
+  const bool need_k = k > 0 && k < p.V, need_p = top_p < 1.0f;
+  // groups without a logit that passes min-p are not read again
+  int live = 0;
+  for (int g = tid; g < G; g += kRowThreads) {
+    if (!wt.above_min(wt.real(sm.gmax[g])))
+      sm.gmax[g] = -__builtin_inff();
+    else
+      ++live;
+  }
+  row_scan(uint64_t(live), sm.red);
+  live = int(sm.red[kWaves]);
+  float floor_x = -__builtin_inff();
+  const auto used = [&](int g) {
+    return sm.gmax[g] > -__builtin_inff() && sm.gmax[g] >= floor_x;
+  };
+
+  // ---- which logits go to the list: x >= floor_x and bin <= last_bin ----
+  bool listed = false;
+  int last_bin = kBins - 1;
+  uint64_t mass = 0;                 // of all that pass min-p (top-p alone)
+  if (need_k && k <= live) {
+    // the k-th largest group maximum: at least k logits lie at or above it
+    for (int g = tid; g < G; g += kRowThreads) {
+      const float v = sm.gmax[g];
+      int rank = 0;
+      for (int j = 0; j < G; ++j)
+        rank += sm.gmax[j] > v || (sm.gmax[j] == v && j < g);
+      if (rank == k - 1) sm.value = __float_as_uint(v);
+    }
+    __syncthreads();
+    floor_x = __uint_as_float(uint32_t(sm.value));
+    listed = true;
+  } else if (need_k || need_p) {
+    for (int i = tid; i < kBins; i += kRowThreads) {
+      sm.hist.count[i] = 0;
+      sm.hist.mass[i] = 0;
+    }
+    __syncthreads();
+    row.each(used, [&](float x, int) {
+      const int bin = wt.bin(x);
+      if (!need_k) {
+        const double w = wt.real(x);
+        if (!wt.above_min(w)) return;
+        atomicAdd((unsigned long long*)&sm.hist.mass[bin],
+                  (unsigned long long)wt.whole(w));
+      }
+      atomicAdd(&sm.hist.count[bin], 1u);
+    });
+    __syncthreads();
+    if (need_k) {
+      find_prefix<2>(sm, sm.hist.count, kBins, uint64_t(k));
+    } else {
+      mass = find_prefix<2>(sm, sm.hist.mass, kBins, 0);
+      find_prefix<2>(sm, sm.hist.mass, kBins, share_of(top_p, mass));
+    }
+    // (fewer than k logits pass: all of them)
+    last_bin = sm.found < 0 ? kBins - 1 : sm.found;
+    uint64_t upto = 0;
+    for (int i = tid; i <= last_bin; i += kRowThreads)
+      upto += sm.hist.count[i];
+    row_scan(upto, sm.red);
+    listed = sm.red[kWaves] <= kList;
+  }
+  if (listed) {
+    __syncthreads();
+    row.each(used, [&](float x, int i) {
+      if (x < floor_x || wt.bin(x) > last_bin) return;
+      if (!wt.above_min(wt.real(x))) return;
+      const uint32_t at = atomicAdd(&sm.n, 1u);
+      if (at < kList)
+        sm.list.key[at] = uint64_t(ordered(x)) << 32 | (0xffffffffu - i);
+    });
+    __syncthreads();
+    listed = sm.n <= kList;          // ties at the floor may be many
+  }
+
+  if (listed) {
+    const int n = sm.n;
+    sort_list(sm.list.key, n);
+    int kept = need_k ? min(n, k) : n;
+    for (int i = tid; i < kept; i += kRowThreads)
+      sm.list.w[i] =
+          wt.whole(wt.real(unordered(uint32_t(sm.list.key[i] >> 32))));
+    __syncthreads();
+    if (need_p) {
+      if (need_k) mass = find_prefix<4>(sm, sm.list.w, kept, 0);
+      find_prefix<4>(sm, sm.list.w, kept, share_of(top_p, mass));
+      if (sm.found >= 0) kept = sm.found + 1;
+      __syncthreads();
+    }
+    // the kept ones in the order of their indexes
+    for (int i = tid; i < kept; i += kRowThreads)
+      sm.list.key[i] = sm.list.key[i] << 32 | uint32_t(i);
+    __syncthreads();
+    sort_list(sm.list.key, kept);
+    uint64_t w[kList / kRowThreads];
+#pragma unroll
+    for (int j = 0; j < kList / kRowThreads; ++j) {
+      const int i = tid + j * kRowThreads;
+      w[j] = i < kept ? sm.list.w[uint32_t(sm.list.key[i])] : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kList / kRowThreads; ++j) {
+      const int i = tid + j * kRowThreads;
+      if (i < kept) sm.list.w[i] = w[j];
+    }
+    __syncthreads();
+    mass = find_prefix<4>(sm, sm.list.w, kept, 0);
+    const uint64_t past = uint64_t(double(u) * double(mass)) + 1;
+    find_prefix<4>(sm, sm.list.w, kept, past < mass ? past : mass);
+    if (tid == 0)
+      p.tokens[m] = int(0xffffffffu -
+                        uint32_t(sm.list.key[max(sm.found, 0)] >> 32));
+    return;
+  }
+
+  // ---- any number of kept logits: thresholds, then sums by group ----
+  __syncthreads();
+  Threshold thr{0, p.V};
+  const auto passes = [&](float x, int i, double& w) {
+    if (!thr.keeps(x, i)) return false;
+    w = wt.real(x);
+    return wt.above_min(w);
+  };
+  if (need_k) {
+    uint64_t n = 0;
+    row.each(used, [&](float x, int i) {
+      double w;
+      n += passes(x, i, w);
+    });
+    row_scan(n, sm.red);
+    if (sm.red[kWaves] > uint64_t(k))
+      thr = search<BF16, VEC>(row, wt, thr, uint64_t(k),
+                              [](double) { return uint64_t(1); });
+  }
+#pragma unroll 1
+  for (int step = need_p ? 0 : 1; step < 2; ++step) {
+    for (int g = tid; g < G; g += kRowThreads) sm.group[g] = 0;
+    __syncthreads();
+    const int wave = uniform(tid >> 6);
+#pragma unroll 1
+    for (int g = wave; g < G; g += kWaves) {
+      if (!used(g)) continue;
+      Group<BF16, VEC> v;
+      v.load(row.at, g, p.V);
+      uint64_t sum = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        double w;
+        if (v.x[e] > -__builtin_inff() && passes(v.x[e], v.index(e), w))
+          sum += wt.whole(w);
+      }
+      sum = wave_sum64(sum);
+      if ((tid & 63) == 0) sm.group[g] = sum;
+    }
+    __syncthreads();
+    mass = find_prefix<2>(sm, sm.group, G, 0);
+    if (step == 0)
+      thr = search<BF16, VEC>(row, wt, thr, share_of(top_p, mass),
+                              [&](double w) { return wt.whole(w); });
+  }
+  const uint64_t past = uint64_t(double(u) * double(mass)) + 1;
+  const uint64_t target = past < mass ? past : mass;
+  find_prefix<2>(sm, sm.group, G, target);
+  const uint64_t before = sm.before;
+  if (tid < 64) {
+    Group<BF16, VEC> v;
+    v.load(row.at, min(max(sm.found, 0), G - 1), p.V);
+    uint64_t w[8], pre[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      double r = 0.0;
+      w[e] = v.x[e] > -__builtin_inff() && passes(v.x[e], v.index(e), r)
+                 ? wt.whole(r) : 0;
+    }
+    group_prefix<VEC>(w, pre);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (before + pre[e] < target && before + pre[e] + w[e] >= target)
+        p.tokens[m] = v.index(e);
+  }
+}
+
+// One thread per request: leading rows whose token is the window's next one.
+__global__ void __launch_bounds__(256) kda_accept_kernel(SampleParams p) {
+  const int b = blockIdx.x * 256 + threadIdx.x;
+  if (b >= p.B) return;
+  const int s = min(max(p.qsl[b], 0), p.M);
+  const int e = min(max(p.qsl[b + 1], s), p.M);
+  int t = s;
+  while (t + 1 < e && p.tokens[t] == p.draft[t + 1]) ++t;
+  p.accepted[b] = s < e ? t - s + 1 : 0;
+  p.next[b] = s < e ? p.tokens[t] : -1;
+}
+
+template <bool BF16, bool VEC>
+int launch_rows(const SampleParams& p, int G, int places,
+                hipStream_t stream) {
+  const int per_row = (G + kPerWg - 1) / kPerWg;
+  launch_kernel(kda_group_max_kernel<BF16, VEC>,
+                dim3(uint32_t(p.M) * uint32_t(per_row)), dim3(kMaxThreads), 0,
+                stream, p, G, per_row);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return int(e);
+  auto kernel = kda_sample_kernel<BF16, VEC>;
+  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                          hipFuncAttributeMaxDynamicSharedMemorySize,
+                          int(sizeof(RowSmem)));
+  if (e != hipSuccess) return int(e);
+  launch_kernel(kernel, dim3(p.M), dim3(kRowThreads), sizeof(RowSmem), stream,
+                p, G, places);
+  return int(hipGetLastError());
+}
+
+}  // namespace
+
+int64_t sample_work_bytes(int64_t M, int64_t V) {
+  if (M < 0 || V < 1 || M > 0x7fffffff || V > int64_t(kMaxGroups) * kGroup)
+    return 0;
+  const int64_t G = (V + kGroup - 1) / kGroup;
+  if (M * ((G + kPerWg - 1) / kPerWg) > 0x7fffffff) return 0;
+  return (M * G * 4 + 255) / 256 * 256 + 256;
+}
+
+int launch_sample(const SampleParams& p, bool bf16, hipStream_t stream) {
+  const int G = (p.V + kGroup - 1) / kGroup;
+  // binary places of a weight: sums of V of them stay below 2^62, and one
+  // below 2^51, where adding 2^52 still rounds to whole numbers
+  int bits = 0;
+  while ((int64_t(1) << bits) < p.V) ++bits;
+  const int places = bits < 16 ? 46 : 62 - bits;
+  const int elem = bf16 ? 2 : 4;
+  const bool vec = reinterpret_cast<uintptr_t>(p.logits) % 16 == 0 &&
+                   p.s_row * elem % 16 == 0;
+  if (p.M > 0) {
+    const int e = bf16 ? (vec ? launch_rows<true, true>(p, G, places, stream)
+                              : launch_rows<true, false>(p, G, places, stream))
+                       : (vec ? launch_rows<false, true>(p, G, places, stream)
+                              : launch_rows<false, false>(p, G, places,
+                                                          stream));
+    if (e != 0) return e;
+  }
+  if (p.draft && p.B > 0)
+    launch_kernel(kda_accept_kernel, dim3((p.B - 1) / 256 + 1), dim3(256), 0,
+                  stream, p);
+  return int(hipGetLastError());
+}
+
+}  // namespace kda

@@ -1,5 +1,5 @@
 // Launch descriptors of the serving-step operators around the verify:
-// prefill, decode and step tables.  Not part of the public ABI.
+// prefill, decode, step tables and sampling.  Not part of the public ABI.
 #pragma once
 
 #include "kda_layer.hpp"
@@ -52,5 +52,24 @@ struct TablesParams {
   int32_t B, rows, width, block, num_free, cap, null_id;
 };
 int launch_step_tables(const TablesParams& p, hipStream_t stream);
+
+struct SampleParams {
+  const void* logits;
+  int64_t s_row;
+  const float* uniform;
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const int32_t* qsl;         // or null
+  const int32_t* draft;       // or null
+  int32_t* tokens;
+  int32_t* accepted;
+  int32_t* next;
+  char* work;
+  int32_t M, V, B;
+};
+int64_t sample_work_bytes(int64_t M, int64_t V);
+int launch_sample(const SampleParams& p, bool bf16, hipStream_t stream);
 
 }  // namespace kda

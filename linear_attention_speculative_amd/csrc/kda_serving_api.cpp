@@ -1,5 +1,5 @@
-// Host side of the serving-step operators (prefill, decode, step
-// tables): argument checks, translation of the public descriptors into
+// Host side of the serving-step operators (prefill, decode, step tables,
+// sampling): argument checks, translation of the public descriptors into
 // launch parameters, and the exported C entry points.
 #include <stdint.h>
 
@@ -392,6 +392,76 @@ int plan_tables(const kda_tables_args* a, kda::TablesParams* p) {
   return KDA_OK;
 }
 
+int plan_sample(const kda_sample_args* a, kda::SampleParams* p, bool* bf16) {
+  if (a == nullptr) return fail(KDA_E_ARG, "sampling arguments are NULL");
+  if (a->batch < 0) return fail(KDA_E_ARG, "batch is negative");
+  const kda_tensor& x = a->logits;
+  KDA_TRY(check_desc(x, "logits", 2));
+  const int64_t M = x.shape[0], V = x.shape[1];
+  if (V < 1) return fail(KDA_E_SHAPE, "the logits have no vocabulary");
+  if (V > (1 << 20))
+    return fail(KDA_E_UNSUPPORTED, "vocabularies of up to 2^20 are supported");
+  const int64_t need = kda::sample_work_bytes(M, V);
+  if (need == 0) return fail(KDA_E_CAPACITY, "too many rows");
+  if ((V > 1 && x.stride[1] != 1) || x.stride[0] < 0)
+    return fail(KDA_E_LAYOUT, "logit rows must be contiguous");
+  if (!aligned(x.data, elem_size(x.dtype)))
+    return fail(KDA_E_UNALIGNED, "the logits are not element aligned");
+  if (!a->query_start_loc && a->batch != M)
+    return fail(KDA_E_SHAPE,
+                "without query_start_loc there is one request per row (%lld "
+                "rows, %d requests)",
+                (long long)M, a->batch);
+  if (a->draft_tokens) {
+    if (!a->query_start_loc)
+      return fail(KDA_E_ARG, "draft_tokens need query_start_loc");
+    if (a->batch > 0 && (!a->num_accepted || !a->next_tokens))
+      return fail(KDA_E_ARG,
+                  "draft_tokens need num_accepted and next_tokens");
+  } else if (a->num_accepted || a->next_tokens) {
+    return fail(KDA_E_ARG,
+                "num_accepted and next_tokens need draft_tokens");
+  }
+  if (M > 0) {
+    if (!a->uniform || !a->tokens)
+      return fail(KDA_E_ARG, "uniform and tokens are required");
+    if (!a->workspace) return fail(KDA_E_ARG, "the workspace is required");
+    if (a->workspace_bytes < need)
+      return fail(KDA_E_CAPACITY,
+                  "the workspace holds %lld bytes; %lld rows of %lld logits "
+                  "need %lld",
+                  (long long)a->workspace_bytes, (long long)M, (long long)V,
+                  (long long)need);
+    if (!aligned(a->workspace, 16))
+      return fail(KDA_E_UNALIGNED, "the workspace must be 16-byte aligned");
+  }
+  const void* all[] = {a->uniform, a->temperature, a->top_k, a->top_p,
+                       a->min_p, a->query_start_loc, a->draft_tokens,
+                       a->tokens, a->num_accepted, a->next_tokens};
+  for (const void* q : all)
+    if (q && !aligned(q, 4))
+      return fail(KDA_E_UNALIGNED, "arrays must be 4-byte aligned");
+  *p = kda::SampleParams{};
+  p->logits = x.data;
+  p->s_row = x.stride[0];
+  p->uniform = a->uniform;
+  p->temperature = a->temperature;
+  p->top_k = a->top_k;
+  p->top_p = a->top_p;
+  p->min_p = a->min_p;
+  p->qsl = a->query_start_loc;
+  p->draft = a->draft_tokens;
+  p->tokens = a->tokens;
+  p->accepted = a->num_accepted;
+  p->next = a->next_tokens;
+  p->work = static_cast<char*>(a->workspace);
+  p->M = int32_t(M);
+  p->V = int32_t(V);
+  p->B = a->batch;
+  *bf16 = x.dtype == KDA_BF16;
+  return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -459,6 +529,27 @@ int kda_step_tables(const kda_tables_args* args, void* stream) {
   return device_status(
       kda::launch_step_tables(p, static_cast<hipStream_t>(stream)),
       "kda_step_tables launch");
+}
+
+int64_t kda_sample_workspace_size(int64_t rows, int64_t vocab) {
+  return kda::sample_work_bytes(rows, vocab);
+}
+
+int kda_check_sample(const kda_sample_args* args) {
+  g_err.clear();
+  kda::SampleParams p;
+  bool bf16 = false;
+  return plan_sample(args, &p, &bf16);
+}
+
+int kda_sample(const kda_sample_args* args, void* stream) {
+  g_err.clear();
+  kda::SampleParams p;
+  bool bf16 = false;
+  KDA_TRY(plan_sample(args, &p, &bf16));
+  return device_status(
+      kda::launch_sample(p, bf16, static_cast<hipStream_t>(stream)),
+      "kda_sample launch");
 }
 
 }  // extern "C"

@@ -1,5 +1,6 @@
 """Python binding of the operators around the verify in a serving step:
-prefill of prompts, single-token decode and the step's index tables.
+prefill of prompts, single-token decode, the step's index tables, and sampling
+with draft acceptance.
 
 Argument marshalling only, as in `ops`; every computation runs in the HIP
 library.  Beyond the library's own checks these functions check what the C
@@ -252,3 +253,69 @@ def step_tables(*, stream=None, **kwargs) -> None:
     requests got null blocks."""
     _launch(_abi.load().kda_step_tables, tables_args(**kwargs),
             _tensors(kwargs), stream)
+
+
+_SAMPLE_PACK = struct.Struct("<" + _pack_format(_abi.KdaSampleArgs))
+
+
+def _floats(t, name: str, size: int) -> int:
+    """Pointer of a float32 array of at least `size` entries (0 for None)."""
+    if t is None:
+        return 0
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32")
+    if t.dim() != 1 or t.numel() < size or not t.is_contiguous():
+        raise ValueError(f"{name} needs {size} contiguous entries (got "
+                         f"{list(t.shape)})")
+    return t.data_ptr()
+
+
+def sample_workspace_size(rows: int, vocab: int) -> int:
+    """Bytes of workspace for sampling up to `rows` rows of `vocab` logits."""
+    n = _abi.load().kda_sample_workspace_size(rows, vocab)
+    if n <= 0:
+        raise ValueError("no sampling has these sizes")
+    return n
+
+
+def sample_args(*, logits, uniform, tokens, workspace, temperature=None,
+                top_k=None, top_p=None, min_p=None, query_start_loc=None,
+                draft_tokens=None, num_accepted=None,
+                next_tokens=None) -> _abi.KdaSampleArgs:
+    """kda_sample_args for these tensors."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocabulary]")
+    M = logits.shape[0]
+    B = M if query_start_loc is None else query_start_loc.numel() - 1
+    if B < 0:
+        raise ValueError("query_start_loc needs batch + 1 entries")
+    if not workspace.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    vals = (*_tensor_values(logits), _floats(uniform, "uniform", M),
+            _floats(temperature, "temperature", B),
+            _ints(top_k, "top_k", B), _floats(top_p, "top_p", B),
+            _floats(min_p, "min_p", B),
+            _ints(query_start_loc, "query_start_loc", B + 1),
+            _ints(draft_tokens, "draft_tokens", M),
+            _ints(tokens, "tokens", M),
+            _ints(num_accepted, "num_accepted", B),
+            _ints(next_tokens, "next_tokens", B), workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), B, 0)
+    return _abi.KdaSampleArgs.from_buffer_copy(_SAMPLE_PACK.pack(*vals))
+
+
+def check_sample(**kwargs) -> int:
+    """Host-only validation (no launch); returns the kda_status code."""
+    return _abi.load().kda_check_sample(ctypes.byref(sample_args(**kwargs)))
+
+
+def sample(*, stream=None, **kwargs) -> None:
+    """A token for every row of `logits` from the given `uniform` numbers,
+    under the temperature, top-k, top-p and min-p of the row's request
+    (kda_sample_args in include/kda_recoverssm.h).  With `draft_tokens` (the
+    windows' tokens, rows as in the verify) also each request's accepted
+    count, as `CommitContext.plan` and `commit_step` take it, and the token
+    that follows the accepted ones.  `workspace` is scratch memory of
+    `sample_workspace_size` bytes."""
+    _launch(_abi.load().kda_sample, sample_args(**kwargs), _tensors(kwargs),
+            stream)

@@ -37,6 +37,8 @@ from .kda import (  # noqa: F401
     verify_qkv,
 )
 from .serving import (  # noqa: F401
+    accept_drafts,
     layer_tokens,
+    sample_row,
     step_tables,
 )

@@ -121,3 +121,58 @@ def step_tables(*, query_lens, num_computed_tokens, num_blocks, block_table,
     r.update(block_table=table, new_num_blocks=held,
              num_allocated=np.array([used]))
     return r
+
+
+def sample_row(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
+    """Token of one row of logits [V] (float64), from the definition: weights
+    e^((x - max) / T) rounded to the documented binary places and summed as
+    Python integers, the order by falling value and rising index, the three
+    prefixes, and the running sum by index."""
+    x = np.where(np.isnan(x), -np.inf, np.asarray(x, np.float64))
+    V, top = len(x), np.max(x)
+    if top == -np.inf:
+        return -1
+    T = 1.0 if np.isnan(temperature) else float(temperature)
+    if T <= 0:
+        return int(np.argmax(x))
+    places = min(46, 62 - max(0, (V - 1).bit_length()))
+    with np.errstate(invalid="ignore", over="ignore"):
+        w = np.where(x == top, 1.0, np.exp((x - top) / T))
+    w[(x == -np.inf) | np.isnan(w)] = 0.0
+    order = np.argsort(-x, kind="stable")
+    kept = [i for i in order if x[i] > -np.inf and w[i] > 0]
+    if min_p > 0:
+        kept = [i for i in kept if w[i] >= min(min_p, 1.0)]
+    if top_k > 0:
+        kept = kept[:top_k]
+    whole = {i: int(np.rint(np.ldexp(w[i], places))) for i in kept}
+    if top_p < 1:
+        need, have, n = float(top_p) * float(sum(whole.values())), 0, 0
+        while n == 0 or have < need:
+            have += whole[kept[n]]
+            n += 1
+        kept = kept[:n]
+    kept = sorted(kept)
+    limit = float(max(u, 0.0)) * float(sum(whole[i] for i in kept))
+    have = 0
+    for i in kept:
+        have += whole[i]
+        if have > limit:
+            return int(i)
+    return int(kept[-1])
+
+
+def accept_drafts(tokens, draft_tokens, query_start_loc):
+    """(accepted counts, next tokens) of draft windows, row by row."""
+    accepted, following = [], []
+    for s, e in zip(query_start_loc[:-1], query_start_loc[1:]):
+        if e <= s:
+            accepted.append(0)
+            following.append(-1)
+            continue
+        t = s
+        while t + 1 < e and tokens[t] == draft_tokens[t + 1]:
+            t += 1
+        accepted.append(t - s + 1)
+        following.append(tokens[t])
+    return np.array(accepted), np.array(following)
