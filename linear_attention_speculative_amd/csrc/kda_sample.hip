@@ -7,22 +7,26 @@
 // set is one threshold pair (value, index); the token is the lowest kept index
 // whose running weight passes u times the whole.  Integer sums make the result
 // independent of the order in which lanes add; the weights come from fp64
-// arithmetic (a cubic share of the time of an fp32 exponential, and a token at
-// the border of two sums of 10^5 terms needs it).
+// arithmetic, which a token at the border of two sums of 10^5 terms needs.
 //
-// A full sort is avoided.  Two kernels:
+// A full sort is avoided; what needs every logit of a row is split over many
+// workgroups, what needs one order over the row is one workgroup's:
 //
 //   kda_group_max_kernel reads the logits once (the floor: HBM) and leaves the
 //   maximum of every group of 512.
+//   kda_row_sums_kernel, only for rows without top-k: with top-p the weights
+//   by bins of 1/32 octave of d, without it the weights of each group.
 //   kda_sample_kernel, one workgroup a row, reads only what it still needs.
 //   Greedy rows read one group.  With top-k <= groups, the k-th largest group
 //   maximum bounds the k-th largest value from below: only groups at or above
-//   it are read again, and the few values there go to a list in LDS.  Larger
-//   k and top-p alone first take a histogram over 2048 bins of 1/16 octave in
-//   d (of counts, or of weights), whose bin at the border bounds the list.  The
-//   list is sorted, cut, and summed.  Rows that keep more than the list holds
-//   find the threshold by a radix search instead (any size, more passes), and
-//   rows without top-k and top-p sum their groups in order.
+//   it are read again, and the few values there go to a list in LDS, which is
+//   sorted, cut and summed.  Larger k takes a histogram of counts first, whose
+//   bin at the border bounds the list.  Top-p alone lists only the bin that
+//   holds its border, and so finds the threshold pair however many logits are
+//   kept.  What no list holds (thousands of ties, or of top-k) is left to a
+//   radix search of any size.
+//   kda_kept_sums_kernel and kda_pick_kernel, only for rows that kept more
+//   than a list: the kept weights of each group, and the token from them.
 #include "kda_serving.hpp"
 
 namespace kda {
@@ -36,6 +40,7 @@ constexpr int kRowThreads = 1024;    // row kernel
 constexpr int kWaves = kRowThreads / 64;
 constexpr int kList = 4096;          // entries of the sorted list
 constexpr int kBins = 2048;
+constexpr int kSteps = 256;          // of an octave, in the table of weights
 
 __device__ __forceinline__ float logit(const SampleParams& p, const char* row,
                                        int i, bool bf16) {
@@ -119,31 +124,6 @@ struct Group {
   }
 };
 
-template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads)
-    kda_group_max_kernel(SampleParams p, int G, int per_row) {
-  const int m = blockIdx.x / per_row, part = blockIdx.x - m * per_row;
-  if (p.qsl && (m < p.qsl[0] || m >= p.qsl[p.B])) return;
-  const char* row = static_cast<const char*>(p.logits) +
-                    m * p.s_row * (BF16 ? 2 : 4);
-  float* out = reinterpret_cast<float*>(p.work) + int64_t(m) * G;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int g0 = part * kPerWg + wave * (kPerWg / 4);
-  Group<BF16, VEC> v[kPerWg / 4];
-#pragma unroll
-  for (int i = 0; i < kPerWg / 4; ++i) v[i].load(row, min(g0 + i, G - 1), p.V);
-#pragma unroll
-  for (int i = 0; i < kPerWg / 4; ++i) {
-    float t = v[i].x[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) t = fmaxf(t, v[i].x[e]);
-    t = wave_max(t);
-    if (lane == 0 && g0 + i < G) out[g0 + i] = t;
-  }
-}
-
-// ---- row kernel -----------------------------------------------------------
-
 // fp32 as an unsigned number of the same order, and back.
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t u = __float_as_uint(x + 0.0f);      // -0 counts as 0
@@ -159,58 +139,139 @@ struct RowSmem {
       uint64_t key[kList];      // ordered(x) << 32 | ~index
       uint64_t w[kList];
     } list;
-    struct {
-      uint32_t count[kBins];
-      uint64_t mass[kBins];
-    } hist;
+    uint32_t count[kBins];
+    uint64_t mass[kBins];
     uint64_t group[kMaxGroups];
   };
   float gmax[kMaxGroups];
-  double table[16];             // 2^(-j/16)
+  double table[kSteps];         // 2^(-j/256)
   uint64_t red[kWaves + 1];
   uint32_t n;
   int found, pick;
   uint64_t before, value;
 };
 
-// Weight of a logit: 2^-d as a real number and as an integer.
+__device__ __forceinline__ void fill_table(double* table) {
+  for (int i = threadIdx.x; i < kSteps; i += blockDim.x)
+    table[i] = exp2(double(i) * (-1.0 / kSteps));
+}
+
+// Weight of a logit as an integer, from its distance to the maximum in steps
+// of 1/256 octave: a table for the whole step, a cubic for the rest (2^-38 of
+// the weight), the octave by the exponent field, and an addition whose last
+// binary place is 1 to round.
 struct Weights {
   const double* table;
-  double c;                     // log2(e) / T
-  float m, c16;                 // maximum; 16 c, for the bins
+  double c, most, d_min_p;      // steps per unit; clamps; steps that min-p allows
+  float m;
   int s;                        // binary places
-  double min_p;
-  // 0 for -inf and whatever lies 2^128 below the maximum
-  __device__ __forceinline__ double real(float x) const {
-    const double d = x == m ? 0.0 : (double(m) - double(x)) * c;
-    if (!(d < 128.0) || x == -__builtin_inff()) return 0.0;
-    const int e = int(d * 16.0);
-    const double z = (double(e) * 0.0625 - d) * 0.6931471805599453094;
-    double q = 1.0 / 5040.0;    // e^z, |z| < 0.0434, to 2^-52
-    q = fma(q, z, 1.0 / 720.0);
-    q = fma(q, z, 1.0 / 120.0);
-    q = fma(q, z, 1.0 / 24.0);
-    q = fma(q, z, 1.0 / 6.0);
-    q = fma(q, z, 0.5);
-    q = fma(q, z, 1.0);
-    q = fma(q, z, 1.0);
-    return ldexp(q * table[e & 15], -(e >> 4));
+  __device__ __forceinline__ void init(const double* tab, float top, float T,
+                                       float min_p, int places) {
+    table = tab;
+    m = top;
+    s = places;
+    c = kSteps * 1.4426950408889634074 / double(T);
+    most = double((places + 2) * kSteps);           // weighs 2^-2 places: 0
+    d_min_p = min_p > 0.0f ? -kSteps * log2(double(fminf(min_p, 1.0f)))
+                           : __builtin_inf();
   }
-  // rounded by an addition whose last binary place is 1
-  __device__ __forceinline__ uint64_t whole(double w) const {
-    return uint64_t(__double_as_longlong(ldexp(w, s) + 0x1p52)) &
+  // Steps below the maximum (0 for a maximum of +inf itself; `most` for -inf
+  // and whatever the weights cannot tell from 0).
+  __device__ __forceinline__ double steps(float x) const {
+    const double d = fmin((double(m) - double(x)) * c, most);
+    return x == m ? 0.0 : d;
+  }
+  __device__ __forceinline__ uint64_t whole(double d) const {
+    const int e = int(d);
+    const double f = d - double(e);
+    constexpr double l = -0.6931471805599453094 / kSteps;
+    double q = fma(f, l * l * l / 6.0, l * l / 2.0);
+    q = fma(f, q, l);
+    q = fma(f, q, 1.0) * table[e & (kSteps - 1)];
+    const int64_t u = __double_as_longlong(q) +
+                      (int64_t(s - e / kSteps) << 52);
+    return uint64_t(__double_as_longlong(__longlong_as_double(u) + 0x1p52)) &
            ((uint64_t(1) << 52) - 1);
   }
-  __device__ __forceinline__ bool above_min(double w) const {
-    return w >= min_p && w > 0.0;
+  __device__ __forceinline__ uint64_t of(float x) const {
+    return whole(steps(x));
   }
-  // 1/16 octave bins of d: never falls as x falls
-  __device__ __forceinline__ int bin(float x) const {
-    if (x == m) return 0;
-    const float b = (m - x) * c16;
-    return b < float(kBins - 1) ? int(b) : kBins - 1;
+  // within min-p (a -inf never is)
+  __device__ __forceinline__ bool allows(float x, double d) const {
+    return d <= d_min_p && x > -__builtin_inff();
+  }
+  // 1/32 octave bins
+  __device__ __forceinline__ int bin(double d) const {
+    return min(int(d) >> 3, kBins - 1);
   }
 };
+
+// The parameters of a row's request, NaN and absent ones off.
+struct Params {
+  float T, top_p, min_p, u;
+  int k;
+  bool greedy, need_k, need_p;
+  __device__ __forceinline__ Params(const SampleParams& p, int b, int m) {
+    T = p.temperature && p.temperature[b] == p.temperature[b]
+            ? p.temperature[b] : 1.0f;
+    k = p.top_k ? p.top_k[b] : 0;
+    top_p = p.top_p && p.top_p[b] < 1.0f ? p.top_p[b] : 1.0f;
+    min_p = p.min_p && p.min_p[b] > 0.0f ? p.min_p[b] : 0.0f;
+    u = p.uniform[m] > 0.0f ? p.uniform[m] : 0.0f;
+    greedy = T <= 0.0f || k == 1 || top_p <= 0.0f;
+    need_k = k > 0 && k < p.V;
+    need_p = top_p < 1.0f;
+  }
+};
+
+// Workspace of a row: maxima of its groups, sums (bins or groups), and what
+// the row kernel leaves to the last two.
+struct Work {
+  float* gmax;
+  uint64_t* sums;         // [kBins]: bins, or weights of groups
+  int32_t* key;           // threshold pair; index -1: the token is decided
+  int32_t* index;
+  __device__ __host__ static int64_t maxima(int64_t M, int64_t G) {
+    return (M * G * 4 + 255) / 256 * 256;
+  }
+  __device__ __host__ static int64_t bytes(int64_t M, int64_t G) {
+    return maxima(M, G) + M * kBins * 8 + (M * 8 + 255) / 256 * 256;
+  }
+  __device__ __forceinline__ Work(const SampleParams& p, int m, int G) {
+    char* sum = p.work + maxima(p.M, G);
+    gmax = reinterpret_cast<float*>(p.work) + int64_t(m) * G;
+    sums = reinterpret_cast<uint64_t*>(sum) + int64_t(m) * kBins;
+    key = reinterpret_cast<int32_t*>(sum + int64_t(p.M) * kBins * 8) + 2 * m;
+    index = key + 1;
+  }
+};
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads)
+    kda_group_max_kernel(SampleParams p, int G, int per_row) {
+  const int m = blockIdx.x / per_row, part = blockIdx.x - m * per_row;
+  if (p.qsl && (m < p.qsl[0] || m >= p.qsl[p.B])) return;
+  const char* row = static_cast<const char*>(p.logits) +
+                    m * p.s_row * (BF16 ? 2 : 4);
+  const Work out(p, m, G);
+  // the row's bins, cleared for the next kernel
+  for (int i = part * kMaxThreads + threadIdx.x; i < kBins;
+       i += per_row * kMaxThreads)
+    out.sums[i] = 0;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int g0 = part * kPerWg + wave * (kPerWg / 4);
+  Group<BF16, VEC> v[kPerWg / 4];
+#pragma unroll
+  for (int i = 0; i < kPerWg / 4; ++i) v[i].load(row, min(g0 + i, G - 1), p.V);
+#pragma unroll
+  for (int i = 0; i < kPerWg / 4; ++i) {
+    float t = v[i].x[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) t = fmaxf(t, v[i].x[e]);
+    t = wave_max(t);
+    if (lane == 0 && g0 + i < G) out.gmax[g0 + i] = t;
+  }
+}
 
 // Threshold pair: a logit is kept if it is larger than `key`, or equal and at
 // an index of at most `index`.
@@ -386,20 +447,20 @@ __device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int bins = pass == 2 ? 1024 : 2048;
-    for (int i = threadIdx.x; i < bins; i += kRowThreads) sm.hist.mass[i] = 0;
+    for (int i = threadIdx.x; i < bins; i += kRowThreads) sm.mass[i] = 0;
     __syncthreads();
     row.each(all, [&](float x, int i) {
       const uint32_t k = ordered(x);
       if ((k & mask) != prefix || !thr.keeps(x, i)) return;
-      const double w = wt.real(x);
-      if (!wt.above_min(w)) return;
+      const double d = wt.steps(x);
+      if (!wt.allows(x, d)) return;
       // bins in falling order
-      atomicAdd((unsigned long long*)&sm.hist
+      atomicAdd((unsigned long long*)&sm
                     .mass[bins - 1 - ((k >> shift) & (bins - 1))],
-                (unsigned long long)what(w));
+                (unsigned long long)what(d));
     });
     __syncthreads();
-    find_prefix<2>(sm, sm.hist.mass, bins, target - before);
+    find_prefix<2>(sm, sm.mass, bins, target - before);
     const int f = max(sm.found, 0);
     before += sm.before;
     prefix |= uint32_t(bins - 1 - f) << shift;
@@ -407,7 +468,7 @@ __device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
     __syncthreads();
   }
   // ties: each counts the same; the index of the last one kept
-  const uint64_t one = what(wt.real(unordered(prefix)));
+  const uint64_t one = what(wt.steps(unordered(prefix)));
   const uint64_t left = target - before;
   const uint64_t rank = one > 0 ? (left + one - 1) / one : 1;
   for (int i = threadIdx.x; i < row.G; i += kRowThreads) sm.group[i] = 0;
@@ -441,50 +502,131 @@ __device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
   return t;
 }
 
+// Row maximum from the groups' maxima, by every wave for itself.
+__device__ __forceinline__ float row_max(const float* gmax, int G) {
+  float top = -__builtin_inff();
+  for (int g = threadIdx.x & 63; g < G; g += 64) top = fmaxf(top, gmax[g]);
+  return wave_max(top);
+}
+
+// Rows without top-k, kPerWg groups a workgroup: with top-p the weights by
+// bins, added to the row's bins, otherwise the weight of each group.
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads)
+    kda_row_sums_kernel(SampleParams p, int G, int per_row, int places) {
+  __shared__ double table[kSteps];
+  __shared__ unsigned long long mass[kBins];
+  const int m = blockIdx.x / per_row, part = blockIdx.x - m * per_row;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int b = request_of_row(p, m, lane);
+  if (b < 0) return;
+  const Params q(p, b, m);
+  if (q.greedy || q.need_k) return;
+  const Work work(p, m, G);
+  const float top = row_max(work.gmax, G);
+  if (top == -__builtin_inff()) return;
+  fill_table(table);
+  if (q.need_p)
+    for (int i = threadIdx.x; i < kBins; i += kMaxThreads) mass[i] = 0;
+  __syncthreads();
+  Weights wt;
+  wt.init(table, top, q.T, q.min_p, places);
+  const char* row = static_cast<const char*>(p.logits) +
+                    m * p.s_row * (BF16 ? 2 : 4);
+#pragma unroll 1
+  for (int i = 0; i < kPerWg / 4; ++i) {
+    const int g = part * kPerWg + wave * (kPerWg / 4) + i;
+    if (g >= G) break;
+    // a group whose largest logit min-p drops has nothing to add
+    if (!wt.allows(work.gmax[g], wt.steps(work.gmax[g]))) {
+      if (!q.need_p && lane == 0) work.sums[g] = 0;
+      continue;
+    }
+    Group<BF16, VEC> v;
+    v.load(row, g, p.V);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double d = wt.steps(v.x[e]);
+      const uint64_t w = wt.allows(v.x[e], d) ? wt.whole(d) : 0;
+      if (!q.need_p)
+        sum += w;
+      else if (w > 0)
+        atomicAdd(&mass[wt.bin(d)], (unsigned long long)w);
+    }
+    if (!q.need_p) {
+      sum = wave_sum64(sum);
+      if (lane == 0) work.sums[g] = sum;
+    }
+  }
+  if (!q.need_p) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kMaxThreads)
+    if (mass[i] > 0)
+      atomicAdd((unsigned long long*)&work.sums[i], mass[i]);
+}
+
+// The token whose running weight passes u: from the weights of the groups
+// (sm.group) and the group that the border falls into.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void pick_token(const SampleParams& p,
+                                           const Row<BF16, VEC>& row,
+                                           const Weights& wt, Threshold thr,
+                                           float u, int m) {
+  RowSmem& sm = row.sm;
+  const uint64_t mass = find_prefix<2>(sm, sm.group, row.G, 0);
+  const uint64_t past = uint64_t(double(u) * double(mass)) + 1;
+  const uint64_t target = past < mass ? past : mass;
+  find_prefix<2>(sm, sm.group, row.G, target);
+  const uint64_t before = sm.before;
+  if (threadIdx.x < 64) {
+    Group<BF16, VEC> v;
+    v.load(row.at, min(max(sm.found, 0), row.G - 1), p.V);
+    uint64_t w[8], pre[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double d = wt.steps(v.x[e]);
+      w[e] = wt.allows(v.x[e], d) && thr.keeps(v.x[e], v.index(e))
+                 ? wt.whole(d) : 0;
+    }
+    group_prefix<VEC>(w, pre);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (before + pre[e] < target && before + pre[e] + w[e] >= target)
+        p.tokens[m] = v.index(e);
+  }
+}
+
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kRowThreads)
     kda_sample_kernel(SampleParams p, int G, int places) {
   extern __shared__ __align__(16) char smem[];
   RowSmem& sm = *reinterpret_cast<RowSmem*>(smem);
   const int m = blockIdx.x, tid = threadIdx.x;
+  const Work work(p, m, G);
   const int b = request_of_row(p, m, tid & 63);
+  if (tid == 0) *work.index = -1;
   if (b < 0) return;
-  const float T = p.temperature && p.temperature[b] == p.temperature[b]
-                      ? p.temperature[b] : 1.0f;
-  const int k = p.top_k ? p.top_k[b] : 0;
-  // (comparisons written so that NaN switches a filter off)
-  const float top_p = p.top_p && p.top_p[b] < 1.0f ? p.top_p[b] : 1.0f;
-  const float min_p = p.min_p && p.min_p[b] > 0.0f ? p.min_p[b] : 0.0f;
-  const float u = p.uniform[m] > 0.0f ? p.uniform[m] : 0.0f;
-
-  const float* gm = reinterpret_cast<const float*>(p.work) + int64_t(m) * G;
+  const Params q(p, b, m);
+  const int k = q.k;
   const Row<BF16, VEC> row{static_cast<const char*>(p.logits) +
                                m * p.s_row * (BF16 ? 2 : 4),
                            p.V, G, sm};
-  float top = -__builtin_inff();
-  for (int g = tid; g < G; g += kRowThreads) {
-    const float v = gm[g];
-    sm.gmax[g] = v;
-    top = fmaxf(top, v);
-  }
-  if (tid < 16) sm.table[tid] = exp2(-0.0625 * tid);
-  top = wave_max(top);
-  if ((tid & 63) == 0) sm.red[tid >> 6] = __float_as_uint(top);
+  for (int g = tid; g < G; g += kRowThreads) sm.gmax[g] = work.gmax[g];
+  fill_table(sm.table);
   if (tid == 0) {
     sm.found = G;
     sm.pick = p.V;
     sm.n = 0;
   }
   __syncthreads();
-#pragma unroll 1
-  for (int j = 0; j < kWaves; ++j)
-    top = fmaxf(top, __uint_as_float(uint32_t(sm.red[j])));
+  const float top = row_max(sm.gmax, G);
   if (top == -__builtin_inff()) {
     if (tid == 0) p.tokens[m] = -1;
     return;
   }
 
-  if (T <= 0.0f || k == 1 || top_p <= 0.0f) {
+  if (q.greedy) {
     // the lowest index of the maximum
     for (int g = tid; g < G; g += kRowThreads)
       if (sm.gmax[g] == top) atomicMin(&sm.found, g);
@@ -501,30 +643,42 @@ __global__ void __launch_bounds__(kRowThreads)
     return;
   }
 
-  const double c = 1.4426950408889634074 / double(T);
-  const Weights wt{sm.table, c, top, float(16.0 * c), places,
-                   double(fminf(min_p, 1.0f))};
-  const bool need_k = k > 0 && k < p.V, need_p = top_p < 1.0f;
+  Weights wt;
+  wt.init(sm.table, top, q.T, q.min_p, places);
+  Threshold thr{0, p.V};
+  if (!q.need_k && !q.need_p) {
+    for (int g = tid; g < G; g += kRowThreads) sm.group[g] = work.sums[g];
+    __syncthreads();
+    pick_token<BF16, VEC>(p, row, wt, thr, q.u, m);
+    return;
+  }
   // groups without a logit that passes min-p are not read again
   int live = 0;
   for (int g = tid; g < G; g += kRowThreads) {
-    if (!wt.above_min(wt.real(sm.gmax[g])))
+    if (!wt.allows(sm.gmax[g], wt.steps(sm.gmax[g])))
       sm.gmax[g] = -__builtin_inff();
     else
       ++live;
   }
   row_scan(uint64_t(live), sm.red);
   live = int(sm.red[kWaves]);
-  float floor_x = -__builtin_inff();
+
+  // ---- which logits go to the list ----
+  enum { kAll, kCount, kMass } by = kAll;      // what bins_of means
+  float floor_x = -__builtin_inff();           // x >= floor_x
+  float scale = 0.0f;                          // count bins of m - x
+  int lo_bin = 0, hi_bin = kBins - 1;          // lo_bin <= bin <= hi_bin
+  uint64_t mass = 0, before = 0;
+  bool listed = true;
   const auto used = [&](int g) {
     return sm.gmax[g] > -__builtin_inff() && sm.gmax[g] >= floor_x;
   };
-
-  // ---- which logits go to the list: x >= floor_x and bin <= last_bin ----
-  bool listed = false;
-  int last_bin = kBins - 1;
-  uint64_t mass = 0;                 // of all that pass min-p (top-p alone)
-  if (need_k && k <= live) {
+  const auto count_bin = [&](float x) {        // never falls as x falls
+    if (x == top) return 0;
+    const float f = (top - x) * scale;
+    return f < float(kBins - 1) ? int(f) : kBins - 1;
+  };
+  if (q.need_k && k <= live) {
     // the k-th largest group maximum: at least k logits lie at or above it
     for (int g = tid; g < G; g += kRowThreads) {
       const float v = sm.gmax[g];
@@ -535,157 +689,193 @@ __global__ void __launch_bounds__(kRowThreads)
     }
     __syncthreads();
     floor_x = __uint_as_float(uint32_t(sm.value));
-    listed = true;
-  } else if (need_k || need_p) {
-    for (int i = tid; i < kBins; i += kRowThreads) {
-      sm.hist.count[i] = 0;
-      sm.hist.mass[i] = 0;
-    }
+  } else if (q.need_k) {
+    // counts, in bins that put the lowest group maximum a quarter of the way
+    float low = top;
+    for (int g = tid & 63; g < G; g += 64)
+      if (sm.gmax[g] > -__builtin_inff()) low = fminf(low, sm.gmax[g]);
+    low = -wave_max(-low);
+    scale = float(kBins / 4) / fmaxf(top - low, 1e-3f);
+    by = kCount;
+    for (int i = tid; i < kBins; i += kRowThreads) sm.count[i] = 0;
     __syncthreads();
     row.each(used, [&](float x, int) {
-      const int bin = wt.bin(x);
-      if (!need_k) {
-        const double w = wt.real(x);
-        if (!wt.above_min(w)) return;
-        atomicAdd((unsigned long long*)&sm.hist.mass[bin],
-                  (unsigned long long)wt.whole(w));
-      }
-      atomicAdd(&sm.hist.count[bin], 1u);
+      atomicAdd(&sm.count[count_bin(x)], 1u);
     });
     __syncthreads();
-    if (need_k) {
-      find_prefix<2>(sm, sm.hist.count, kBins, uint64_t(k));
-    } else {
-      mass = find_prefix<2>(sm, sm.hist.mass, kBins, 0);
-      find_prefix<2>(sm, sm.hist.mass, kBins, share_of(top_p, mass));
-    }
-    // (fewer than k logits pass: all of them)
-    last_bin = sm.found < 0 ? kBins - 1 : sm.found;
-    uint64_t upto = 0;
-    for (int i = tid; i <= last_bin; i += kRowThreads)
-      upto += sm.hist.count[i];
-    row_scan(upto, sm.red);
-    listed = sm.red[kWaves] <= kList;
+    find_prefix<2>(sm, sm.count, kBins, uint64_t(k));
+    // (fewer than k logits: all of them)
+    if (sm.found >= 0) hi_bin = sm.found;
+    listed = sm.found < 0 || sm.before + sm.value <= kList;
+  } else {
+    by = kMass;
+    for (int i = tid; i < kBins; i += kRowThreads) sm.mass[i] = work.sums[i];
+    __syncthreads();
+    mass = find_prefix<2>(sm, sm.mass, kBins, 0);
+    find_prefix<2>(sm, sm.mass, kBins, share_of(q.top_p, mass));
+    lo_bin = hi_bin = sm.found;
+    before = sm.before;
   }
   if (listed) {
     __syncthreads();
-    row.each(used, [&](float x, int i) {
-      if (x < floor_x || wt.bin(x) > last_bin) return;
-      if (!wt.above_min(wt.real(x))) return;
-      const uint32_t at = atomicAdd(&sm.n, 1u);
-      if (at < kList)
-        sm.list.key[at] = uint64_t(ordered(x)) << 32 | (0xffffffffu - i);
-    });
+    row.each(
+        [&](int g) {
+          return used(g) &&
+                 (by != kMass || wt.bin(wt.steps(sm.gmax[g])) <= hi_bin);
+        },
+        [&](float x, int i) {
+          if (x < floor_x || (by == kCount && count_bin(x) > hi_bin)) return;
+          const double d = wt.steps(x);
+          if (!wt.allows(x, d)) return;
+          if (by == kMass) {
+            const int bin = wt.bin(d);
+            if (bin < lo_bin || bin > hi_bin) return;
+          }
+          const uint32_t at = atomicAdd(&sm.n, 1u);
+          if (at < kList)
+            sm.list.key[at] = uint64_t(ordered(x)) << 32 | (0xffffffffu - i);
+        });
     __syncthreads();
-    listed = sm.n <= kList;          // ties at the floor may be many
+    listed = sm.n <= kList;          // (ties may be many)
   }
 
   if (listed) {
     const int n = sm.n;
     sort_list(sm.list.key, n);
-    int kept = need_k ? min(n, k) : n;
+    int kept = q.need_k ? min(n, k) : n;
     for (int i = tid; i < kept; i += kRowThreads)
-      sm.list.w[i] =
-          wt.whole(wt.real(unordered(uint32_t(sm.list.key[i] >> 32))));
+      sm.list.w[i] = wt.of(unordered(uint32_t(sm.list.key[i] >> 32)));
     __syncthreads();
-    if (need_p) {
-      if (need_k) mass = find_prefix<4>(sm, sm.list.w, kept, 0);
-      find_prefix<4>(sm, sm.list.w, kept, share_of(top_p, mass));
+    if (q.need_p) {
+      if (q.need_k) mass = find_prefix<4>(sm, sm.list.w, kept, 0);
+      find_prefix<4>(sm, sm.list.w, kept, share_of(q.top_p, mass) - before);
       if (sm.found >= 0) kept = sm.found + 1;
       __syncthreads();
     }
-    // the kept ones in the order of their indexes
-    for (int i = tid; i < kept; i += kRowThreads)
-      sm.list.key[i] = sm.list.key[i] << 32 | uint32_t(i);
-    __syncthreads();
-    sort_list(sm.list.key, kept);
-    uint64_t w[kList / kRowThreads];
+    if (by == kMass) {
+      // the last kept one is the threshold pair
+      const uint64_t last = sm.list.key[kept - 1];
+      thr = Threshold{uint32_t(last >> 32),
+                      int(0xffffffffu - uint32_t(last))};
+    } else {
+      // the kept ones in the order of their indexes
+      for (int i = tid; i < kept; i += kRowThreads)
+        sm.list.key[i] = sm.list.key[i] << 32 | uint32_t(i);
+      __syncthreads();
+      sort_list(sm.list.key, kept);
+      uint64_t w[kList / kRowThreads];
 #pragma unroll
-    for (int j = 0; j < kList / kRowThreads; ++j) {
-      const int i = tid + j * kRowThreads;
-      w[j] = i < kept ? sm.list.w[uint32_t(sm.list.key[i])] : 0;
-    }
-    __syncthreads();
+      for (int j = 0; j < kList / kRowThreads; ++j) {
+        const int i = tid + j * kRowThreads;
+        w[j] = i < kept ? sm.list.w[uint32_t(sm.list.key[i])] : 0;
+      }
+      __syncthreads();
 #pragma unroll
-    for (int j = 0; j < kList / kRowThreads; ++j) {
-      const int i = tid + j * kRowThreads;
-      if (i < kept) sm.list.w[i] = w[j];
+      for (int j = 0; j < kList / kRowThreads; ++j) {
+        const int i = tid + j * kRowThreads;
+        if (i < kept) sm.list.w[i] = w[j];
+      }
+      __syncthreads();
+      mass = find_prefix<4>(sm, sm.list.w, kept, 0);
+      const uint64_t past = uint64_t(double(q.u) * double(mass)) + 1;
+      find_prefix<4>(sm, sm.list.w, kept, past < mass ? past : mass);
+      if (tid == 0)
+        p.tokens[m] = int(0xffffffffu -
+                          uint32_t(sm.list.key[max(sm.found, 0)] >> 32));
+      return;
     }
+  } else {
+    // ---- no list holds them: thresholds by radix search ----
     __syncthreads();
-    mass = find_prefix<4>(sm, sm.list.w, kept, 0);
-    const uint64_t past = uint64_t(double(u) * double(mass)) + 1;
-    find_prefix<4>(sm, sm.list.w, kept, past < mass ? past : mass);
-    if (tid == 0)
-      p.tokens[m] = int(0xffffffffu -
-                        uint32_t(sm.list.key[max(sm.found, 0)] >> 32));
-    return;
+    if (q.need_k) {
+      uint64_t n = 0;
+      row.each(used, [&](float x, int) { n += wt.allows(x, wt.steps(x)); });
+      row_scan(n, sm.red);
+      if (sm.red[kWaves] > uint64_t(k))
+        thr = search<BF16, VEC>(row, wt, thr, uint64_t(k),
+                                [](double) { return uint64_t(1); });
+      if (q.need_p) {
+        uint64_t sum = 0;
+        row.each(used, [&](float x, int i) {
+          const double d = wt.steps(x);
+          if (wt.allows(x, d) && thr.keeps(x, i)) sum += wt.whole(d);
+        });
+        row_scan(sum, sm.red);
+        mass = sm.red[kWaves];
+      }
+    }
+    if (q.need_p)
+      thr = search<BF16, VEC>(row, wt, thr, share_of(q.top_p, mass),
+                              [&](double d) { return wt.whole(d); });
   }
+  // the kept weights of each group are left to many workgroups
+  if (tid == 0) {
+    *work.key = int32_t(thr.key);
+    *work.index = thr.index;
+  }
+}
 
-  // ---- any number of kept logits: thresholds, then sums by group ----
+// Kept weights of each group of the rows with a threshold pair.
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads)
+    kda_kept_sums_kernel(SampleParams p, int G, int per_row, int places) {
+  __shared__ double table[kSteps];
+  const int m = blockIdx.x / per_row, part = blockIdx.x - m * per_row;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const Work work(p, m, G);
+  const Threshold thr{uint32_t(*work.key), *work.index};
+  if (thr.index < 0) return;
+  const int b = request_of_row(p, m, lane);
+  if (b < 0) return;
+  const Params q(p, b, m);
+  fill_table(table);
   __syncthreads();
-  Threshold thr{0, p.V};
-  const auto passes = [&](float x, int i, double& w) {
-    if (!thr.keeps(x, i)) return false;
-    w = wt.real(x);
-    return wt.above_min(w);
-  };
-  if (need_k) {
-    uint64_t n = 0;
-    row.each(used, [&](float x, int i) {
-      double w;
-      n += passes(x, i, w);
-    });
-    row_scan(n, sm.red);
-    if (sm.red[kWaves] > uint64_t(k))
-      thr = search<BF16, VEC>(row, wt, thr, uint64_t(k),
-                              [](double) { return uint64_t(1); });
-  }
+  Weights wt;
+  wt.init(table, row_max(work.gmax, G), q.T, q.min_p, places);
+  const char* row = static_cast<const char*>(p.logits) +
+                    m * p.s_row * (BF16 ? 2 : 4);
 #pragma unroll 1
-  for (int step = need_p ? 0 : 1; step < 2; ++step) {
-    for (int g = tid; g < G; g += kRowThreads) sm.group[g] = 0;
-    __syncthreads();
-    const int wave = uniform(tid >> 6);
-#pragma unroll 1
-    for (int g = wave; g < G; g += kWaves) {
-      if (!used(g)) continue;
+  for (int i = 0; i < kPerWg / 4; ++i) {
+    const int g = part * kPerWg + wave * (kPerWg / 4) + i;
+    if (g >= G) break;
+    uint64_t sum = 0;
+    const float x = work.gmax[g];
+    if (wt.allows(x, wt.steps(x)) && ordered(x) >= thr.key) {
       Group<BF16, VEC> v;
-      v.load(row.at, g, p.V);
-      uint64_t sum = 0;
+      v.load(row, g, p.V);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        double w;
-        if (v.x[e] > -__builtin_inff() && passes(v.x[e], v.index(e), w))
-          sum += wt.whole(w);
+        const double d = wt.steps(v.x[e]);
+        if (wt.allows(v.x[e], d) && thr.keeps(v.x[e], v.index(e)))
+          sum += wt.whole(d);
       }
       sum = wave_sum64(sum);
-      if ((tid & 63) == 0) sm.group[g] = sum;
     }
-    __syncthreads();
-    mass = find_prefix<2>(sm, sm.group, G, 0);
-    if (step == 0)
-      thr = search<BF16, VEC>(row, wt, thr, share_of(top_p, mass),
-                              [&](double w) { return wt.whole(w); });
+    if (lane == 0) work.sums[g] = sum;
   }
-  const uint64_t past = uint64_t(double(u) * double(mass)) + 1;
-  const uint64_t target = past < mass ? past : mass;
-  find_prefix<2>(sm, sm.group, G, target);
-  const uint64_t before = sm.before;
-  if (tid < 64) {
-    Group<BF16, VEC> v;
-    v.load(row.at, min(max(sm.found, 0), G - 1), p.V);
-    uint64_t w[8], pre[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      double r = 0.0;
-      w[e] = v.x[e] > -__builtin_inff() && passes(v.x[e], v.index(e), r)
-                 ? wt.whole(r) : 0;
-    }
-    group_prefix<VEC>(w, pre);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (before + pre[e] < target && before + pre[e] + w[e] >= target)
-        p.tokens[m] = v.index(e);
-  }
+}
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kRowThreads)
+    kda_pick_kernel(SampleParams p, int G, int places) {
+  extern __shared__ __align__(16) char smem[];
+  RowSmem& sm = *reinterpret_cast<RowSmem*>(smem);
+  const int m = blockIdx.x, tid = threadIdx.x;
+  const Work work(p, m, G);
+  const Threshold thr{uint32_t(*work.key), *work.index};
+  if (thr.index < 0) return;
+  const int b = request_of_row(p, m, tid & 63);
+  if (b < 0) return;
+  const Params q(p, b, m);
+  for (int g = tid; g < G; g += kRowThreads) sm.group[g] = work.sums[g];
+  fill_table(sm.table);
+  __syncthreads();
+  Weights wt;
+  wt.init(sm.table, row_max(work.gmax, G), q.T, q.min_p, places);
+  const Row<BF16, VEC> row{static_cast<const char*>(p.logits) +
+                               m * p.s_row * (BF16 ? 2 : 4),
+                           p.V, G, sm};
+  pick_token<BF16, VEC>(p, row, wt, thr, q.u, m);
 }
 
 // One thread per request: leading rows whose token is the window's next one.
@@ -707,15 +897,24 @@ int launch_rows(const SampleParams& p, int G, int places,
   launch_kernel(kda_group_max_kernel<BF16, VEC>,
                 dim3(uint32_t(p.M) * uint32_t(per_row)), dim3(kMaxThreads), 0,
                 stream, p, G, per_row);
+  const dim3 parts(uint32_t(p.M) * uint32_t(per_row));
+  launch_kernel(kda_row_sums_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
+                stream, p, G, per_row, places);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return int(e);
-  auto kernel = kda_sample_kernel<BF16, VEC>;
-  e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                          hipFuncAttributeMaxDynamicSharedMemorySize,
-                          int(sizeof(RowSmem)));
-  if (e != hipSuccess) return int(e);
-  launch_kernel(kernel, dim3(p.M), dim3(kRowThreads), sizeof(RowSmem), stream,
-                p, G, places);
+  for (auto kernel : {kda_sample_kernel<BF16, VEC>,
+                      kda_pick_kernel<BF16, VEC>}) {
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                            hipFuncAttributeMaxDynamicSharedMemorySize,
+                            int(sizeof(RowSmem)));
+    if (e != hipSuccess) return int(e);
+  }
+  launch_kernel(kda_sample_kernel<BF16, VEC>, dim3(p.M), dim3(kRowThreads),
+                sizeof(RowSmem), stream, p, G, places);
+  launch_kernel(kda_kept_sums_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
+                stream, p, G, per_row, places);
+  launch_kernel(kda_pick_kernel<BF16, VEC>, dim3(p.M), dim3(kRowThreads),
+                sizeof(RowSmem), stream, p, G, places);
   return int(hipGetLastError());
 }
 
@@ -726,7 +925,7 @@ int64_t sample_work_bytes(int64_t M, int64_t V) {
     return 0;
   const int64_t G = (V + kGroup - 1) / kGroup;
   if (M * ((G + kPerWg - 1) / kPerWg) > 0x7fffffff) return 0;
-  return (M * G * 4 + 255) / 256 * 256 + 256;
+  return Work::bytes(M, G) + 256;
 }
 
 int launch_sample(const SampleParams& p, bool bf16, hipStream_t stream) {
