@@ -108,8 +108,14 @@ struct Group {
     typedef typename Act<BF16>::T T;
     first = g * kGroup;
     const int lane = threadIdx.x & 63;
-    if (VEC && first + kGroup <= V) {
-      load8<BF16>(row, first + 8 * lane, x);
+    if (first + kGroup <= V) {
+      if constexpr (VEC) {
+        load8<BF16>(row, first + 8 * lane, x);
+      } else {
+        const T* at = reinterpret_cast<const T*>(row) + first + lane;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = Act<BF16>::f(at[64 * e]);
+      }
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -132,6 +138,27 @@ __device__ __forceinline__ uint32_t ordered(float x) {
 __device__ __forceinline__ float unordered(uint32_t k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
+constexpr uint32_t kLowestKey = 0x00800000u;       // the least above -inf's
+
+// The least key from kLowestKey to `top` whose value satisfies `test`, which
+// `top` does and every value above one that does: by every wave for itself,
+// 64 candidates at a time.
+template <class Test>
+__device__ __forceinline__ uint32_t least_key(uint32_t top, Test test) {
+  uint32_t lo = kLowestKey, hi = top;
+  while (lo < hi) {
+    const uint32_t step = (hi - lo) / 64 + 1;
+    const uint64_t at = uint64_t(lo) + uint64_t(threadIdx.x & 63) * step;
+    const uint64_t in =
+        __ballot(at >= hi || test(unordered(uint32_t(at < hi ? at : hi))));
+    // some candidate is at or past hi, or test holds from none of them to hi
+    const int f = in ? int(__ffsll((unsigned long long)in)) - 1 : 64;
+    const uint64_t first = uint64_t(lo) + uint64_t(f) * step;
+    if (f > 0) lo += uint32_t(f - 1) * step + 1;
+    hi = first < hi ? uint32_t(first) : hi;
+  }
+  return uint32_t(uniform(int(hi)));
+}
 
 struct RowSmem {
   union {
@@ -145,7 +172,7 @@ struct RowSmem {
   };
   float gmax[kMaxGroups];
   double table[kSteps];         // 2^(-j/256)
-  uint64_t red[kWaves + 1];
+  uint64_t red[kWaves];
   uint32_t n;
   int found, pick;
   uint64_t before, value;
@@ -289,19 +316,40 @@ struct Row {
   const char* at;
   int V, G;
   RowSmem& sm;
-  // f(x, index) for the logits of the groups that `use(g)` takes, a group to
-  // a wave; -inf is left out.
+  // f(x, index) for the logits of the groups that `use(g)` takes; -inf is left
+  // out.
   template <class Use, class F>
   __device__ __forceinline__ void each(Use use, F f) const {
-    const int wave = uniform(threadIdx.x >> 6);
-#pragma unroll 1
-    for (int g = wave; g < G; g += kWaves) {
-      if (!use(g)) continue;
-      Group<BF16, VEC> v;
-      v.load(at, g, V);
+    each_group(use, [&](const Group<BF16, VEC>& v) {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (v.x[e] > -__builtin_inff()) f(v.x[e], v.index(e));
+    });
+  }
+  // f(group), a group to a wave, the loads of kAhead groups at once.
+  template <class Use, class F>
+  __device__ __forceinline__ void each_group(Use use, F f) const {
+    constexpr int kAhead = VEC ? 4 : 2;
+    int g = uniform(threadIdx.x >> 6);
+#pragma unroll 1
+    while (true) {
+      int id[kAhead], n = 0;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        while (g < G && !use(g)) g += kWaves;
+        id[j] = g;
+        n += g < G;
+        g += kWaves;
+      }
+      if (n == 0) return;
+      Group<BF16, VEC> v[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) v[j].load(at, min(id[j], G - 1), V);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        if (j >= n) break;
+        f(v[j]);
+      }
     }
   }
 };
@@ -312,9 +360,9 @@ __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
   return v;
 }
 
-// Inclusive prefix sum over the workgroup; red[kWaves] is the total until the
-// next call.
-__device__ __forceinline__ uint64_t row_scan(uint64_t v, uint64_t* red) {
+// Inclusive prefix sum over the workgroup, and the total.
+__device__ __forceinline__ uint64_t row_scan(uint64_t v, uint64_t* red,
+                                             uint64_t* total) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) {
@@ -324,24 +372,22 @@ __device__ __forceinline__ uint64_t row_scan(uint64_t v, uint64_t* red) {
   __syncthreads();
   if (lane == 63) red[w] = v;
   __syncthreads();
-  uint64_t base = 0, total = 0;
-#pragma unroll 1
+  uint64_t base = 0, sum = 0;
+#pragma unroll
   for (int j = 0; j < kWaves; ++j) {
-    if (j < w) base += red[j];
-    total += red[j];
+    base = j == w ? sum : base;
+    sum += red[j];
   }
-  __syncthreads();
-  if (threadIdx.x == 0) red[kWaves] = total;
-  __syncthreads();
+  *total = sum;
   return base + v;
 }
 
 // First index i of a[0 .. n) (n <= kPer * kRowThreads) whose inclusive prefix
-// sum reaches `target`; sm.found = i (or -1), sm.before = the sum before it,
-// sm.value = a[i].  Returns the total of a.
-template <int kPer, class T>
+// sum reaches goal(total of a); sm.found = i (or -1), sm.before = the sum
+// before it, sm.value = a[i].  Returns the total.
+template <int kPer, class T, class Goal>
 __device__ __forceinline__ uint64_t find_prefix(RowSmem& sm, const T* a, int n,
-                                                uint64_t target) {
+                                                Goal goal) {
   uint64_t v[kPer], own = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
@@ -349,9 +395,11 @@ __device__ __forceinline__ uint64_t find_prefix(RowSmem& sm, const T* a, int n,
     v[j] = i < n ? uint64_t(a[i]) : 0;
     own += v[j];
   }
+  __syncthreads();                    // the last result has been read
   if (threadIdx.x == 0) sm.found = -1;
-  uint64_t sum = row_scan(own, sm.red) - own;
-  const uint64_t total = sm.red[kWaves];
+  uint64_t total;
+  uint64_t sum = row_scan(own, sm.red, &total) - own;
+  const uint64_t target = goal(total);
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = threadIdx.x * kPer + j;
@@ -366,28 +414,118 @@ __device__ __forceinline__ uint64_t find_prefix(RowSmem& sm, const T* a, int n,
   return total;
 }
 
-// Sort of the list's first n keys, falling; n is padded to a power of two with
-// zeros.
-__device__ __forceinline__ void sort_list(uint64_t* key, int n) {
-  int size = 64;
-  while (size < n) size <<= 1;
-  for (int i = n + threadIdx.x; i < size; i += kRowThreads) key[i] = 0;
-  __syncthreads();
+// The value of lane l ^ J, without a trip through LDS.
+template <int J>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t u) {
+  const auto mov = [](uint32_t x, auto ctrl) {
+    return uint32_t(__builtin_amdgcn_mov_dpp(int(x), decltype(ctrl)::value,
+                                             0xF, 0xF, true));
+  };
+  if constexpr (J == 1) return mov(u, std::integral_constant<int, kQuadXor1>{});
+  if constexpr (J == 2) return mov(u, std::integral_constant<int, kQuadXor2>{});
+  if constexpr (J == 4)        // l ^ 7, then l ^ 3
+    return mov(mov(u, std::integral_constant<int, kRowHalfMirror>{}),
+               std::integral_constant<int, 0x1B>{});
+  if constexpr (J == 8)        // l ^ 15, then l ^ 7
+    return mov(mov(u, std::integral_constant<int, kRowMirror>{}),
+               std::integral_constant<int, kRowHalfMirror>{});
+  if constexpr (J == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    return threadIdx.x & 16 ? r[0] : r[1];
+  }
+  if constexpr (J == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return threadIdx.x & 32 ? r[0] : r[1];
+  }
+}
+
+// One step of the bitonic network on key i: the larger of the pair goes to
+// the lower index in blocks of k whose bit k is clear.
+__device__ __forceinline__ uint64_t keep_of(uint64_t own, uint64_t other,
+                                            int i, int k, int j) {
+  const bool larger = ((i & k) == 0) == ((i & j) == 0);
+  return (own > other) == larger ? own : other;
+}
+
+template <int J, int P>
+__device__ __forceinline__ void lane_step(uint64_t (&v)[P], int k) {
+  if (J >= k) return;
+#pragma unroll
+  for (int r = 0; r < P; ++r) {
+    const uint64_t o = uint64_t(lane_xor<J>(uint32_t(v[r] >> 32))) << 32 |
+                       lane_xor<J>(uint32_t(v[r]));
+    v[r] = keep_of(v[r], o, r * kRowThreads + threadIdx.x, k, J);
+  }
+}
+
+// Sort of `size` keys (a power of two, at most P * kRowThreads), falling: key
+// r * kRowThreads + tid in register r of a thread.  Pairs inside a wave are
+// exchanged between lanes, pairs of registers in place, the others through two
+// buffers in turn, at one barrier each.
+template <int P>
+__device__ __forceinline__ void sort_keys(uint64_t* a, uint64_t* b, int size) {
+  const int tid = threadIdx.x;
+  uint64_t v[P];
+#pragma unroll
+  for (int r = 0; r < P; ++r) {
+    const int i = r * kRowThreads + tid;
+    v[r] = i < size ? a[i] : 0;
+  }
+  uint64_t* buf = b;
 #pragma unroll 1
   for (int k = 2; k <= size; k <<= 1) {
-#pragma unroll 1
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      for (int t = threadIdx.x; t < size / 2; t += kRowThreads) {
-        const int i = 2 * t - (t & (j - 1));      // bit j clear
-        const uint64_t a = key[i], b = key[i + j];
-        if ((a < b) == ((i & k) == 0)) {
-          key[i] = b;
-          key[i + j] = a;
-        }
+#pragma unroll
+    for (int s = P / 2; s >= 1; s >>= 1)
+      if (s * kRowThreads < k) {
+#pragma unroll
+        for (int r = 0; r < P; ++r)
+          if ((r & s) == 0) {
+            const int i = r * kRowThreads + tid;
+            const uint64_t x = v[r], z = v[r + s];
+            const bool larger = (i & k) == 0;
+            v[r] = (x > z) == larger ? x : z;
+            v[r + s] = (x > z) == larger ? z : x;
+          }
       }
+#pragma unroll 1
+    for (int j = min(k >> 1, kRowThreads / 2); j >= 64; j >>= 1) {
+#pragma unroll
+      for (int r = 0; r < P; ++r) buf[r * kRowThreads + tid] = v[r];
       __syncthreads();
+#pragma unroll
+      for (int r = 0; r < P; ++r) {
+        const int i = r * kRowThreads + tid;
+        v[r] = keep_of(v[r], buf[i ^ j], i, k, j);
+      }
+      buf = buf == a ? b : a;
     }
+    lane_step<32>(v, k);
+    lane_step<16>(v, k);
+    lane_step<8>(v, k);
+    lane_step<4>(v, k);
+    lane_step<2>(v, k);
+    lane_step<1>(v, k);
   }
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < P; ++r) a[r * kRowThreads + tid] = v[r];
+  __syncthreads();
+}
+
+// Sort of the list's first n keys, falling; zeros follow them.  The weights'
+// place is the second buffer.
+__device__ __forceinline__ void sort_list(RowSmem& sm, int n) {
+  int size = 2;
+  while (size < n) size <<= 1;
+  for (int i = n + threadIdx.x; i < size; i += kRowThreads)
+    sm.list.key[i] = 0;
+  __syncthreads();
+  if (size <= kRowThreads)
+    sort_keys<1>(sm.list.key, sm.list.w, size);
+  else if (size <= 2 * kRowThreads)
+    sort_keys<2>(sm.list.key, sm.list.w, size);
+  else
+    sort_keys<4>(sm.list.key, sm.list.w, size);
 }
 
 // Target of a share of a whole: the least integer >= share * mass, at least 1
@@ -432,53 +570,58 @@ __device__ __forceinline__ void group_prefix(const uint64_t (&v)[8],
   }
 }
 
-// The threshold of the first `target` in count or weight (what(x) each) among
-// the logits that `thr` keeps and that pass min-p: radix search over the
-// ordered keys, 11, 11 and 10 bits a pass, then the last tie's index.
+// The least integer > u * mass, at most mass.
+__device__ __forceinline__ uint64_t past_share(float u, uint64_t mass) {
+  const uint64_t past = uint64_t(double(u) * double(mass)) + 1;
+  return past < mass ? past : mass;
+}
+
+// The threshold of the first `target` in what(x) among the logits that `thr`
+// keeps and whose keys are at least `least`: radix search over the ordered
+// keys, 11, 11 and 10 bits a pass, then the last tie's index.
 template <bool BF16, bool VEC, class What>
 __device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
-                                            const Weights& wt, Threshold thr,
+                                            uint32_t least, Threshold thr,
                                             uint64_t target, What what) {
   RowSmem& sm = row.sm;
-  const auto all = [](int) { return true; };
+  const auto used = [&](int g) { return ordered(sm.gmax[g]) >= least; };
   uint32_t prefix = 0, mask = 0;
   uint64_t before = 0;
 #pragma unroll 1
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
     const int bins = pass == 2 ? 1024 : 2048;
+    __syncthreads();
     for (int i = threadIdx.x; i < bins; i += kRowThreads) sm.mass[i] = 0;
     __syncthreads();
-    row.each(all, [&](float x, int i) {
+    row.each(used, [&](float x, int i) {
       const uint32_t k = ordered(x);
-      if ((k & mask) != prefix || !thr.keeps(x, i)) return;
-      const double d = wt.steps(x);
-      if (!wt.allows(x, d)) return;
-      // bins in falling order
-      atomicAdd((unsigned long long*)&sm
-                    .mass[bins - 1 - ((k >> shift) & (bins - 1))],
-                (unsigned long long)what(d));
+      if ((k & mask) == prefix && k >= least && thr.keeps(x, i))
+        // bins in falling order
+        atomicAdd((unsigned long long*)&sm
+                      .mass[bins - 1 - ((k >> shift) & (bins - 1))],
+                  (unsigned long long)what(x));
     });
     __syncthreads();
-    find_prefix<2>(sm, sm.mass, bins, target - before);
-    const int f = max(sm.found, 0);
+    find_prefix<2>(sm, sm.mass, bins,
+                   [&](uint64_t) { return target - before; });
     before += sm.before;
-    prefix |= uint32_t(bins - 1 - f) << shift;
+    prefix |= uint32_t(bins - 1 - max(sm.found, 0)) << shift;
     mask |= uint32_t(bins - 1) << shift;
-    __syncthreads();
   }
   // ties: each counts the same; the index of the last one kept
-  const uint64_t one = what(wt.steps(unordered(prefix)));
+  const uint64_t one = what(unordered(prefix));
   const uint64_t left = target - before;
   const uint64_t rank = one > 0 ? (left + one - 1) / one : 1;
+  __syncthreads();
   for (int i = threadIdx.x; i < row.G; i += kRowThreads) sm.group[i] = 0;
   __syncthreads();
-  row.each(all, [&](float x, int i) {
+  row.each(used, [&](float x, int i) {
     if (ordered(x) == prefix && thr.keeps(x, i))
       atomicAdd((unsigned long long*)&sm.group[i / kGroup], 1ull);
   });
   __syncthreads();
-  find_prefix<2>(sm, sm.group, row.G, rank);
+  find_prefix<2>(sm, sm.group, row.G, [&](uint64_t) { return rank; });
   const int g = sm.found;
   const uint64_t seen = sm.before;
   if (threadIdx.x == 0) sm.pick = row.V - 1;
@@ -489,8 +632,7 @@ __device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
     uint64_t tie[8], pre[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      tie[e] = v.x[e] > -__builtin_inff() && ordered(v.x[e]) == prefix &&
-               thr.keeps(v.x[e], v.index(e));
+      tie[e] = ordered(v.x[e]) == prefix && thr.keeps(v.x[e], v.index(e));
     group_prefix<VEC>(tie, pre);
 #pragma unroll
     for (int e = 0; e < 8; ++e)
@@ -574,10 +716,9 @@ __device__ __forceinline__ void pick_token(const SampleParams& p,
                                            const Weights& wt, Threshold thr,
                                            float u, int m) {
   RowSmem& sm = row.sm;
-  const uint64_t mass = find_prefix<2>(sm, sm.group, row.G, 0);
-  const uint64_t past = uint64_t(double(u) * double(mass)) + 1;
-  const uint64_t target = past < mass ? past : mass;
-  find_prefix<2>(sm, sm.group, row.G, target);
+  const uint64_t mass = find_prefix<2>(
+      sm, sm.group, row.G, [&](uint64_t w) { return past_share(u, w); });
+  const uint64_t target = past_share(u, mass);
   const uint64_t before = sm.before;
   if (threadIdx.x < 64) {
     Group<BF16, VEC> v;
@@ -652,88 +793,110 @@ __global__ void __launch_bounds__(kRowThreads)
     pick_token<BF16, VEC>(p, row, wt, thr, q.u, m);
     return;
   }
-  // groups without a logit that passes min-p are not read again
-  int live = 0;
-  for (int g = tid; g < G; g += kRowThreads) {
-    if (!wt.allows(sm.gmax[g], wt.steps(sm.gmax[g])))
-      sm.gmax[g] = -__builtin_inff();
-    else
-      ++live;
-  }
-  row_scan(uint64_t(live), sm.red);
-  live = int(sm.red[kWaves]);
+  // Every condition on a logit's weight is one on its key.
+  const uint32_t top_key = ordered(top);
+  const uint32_t min_key =
+      q.min_p > 0.0f ? least_key(top_key,
+                                 [&](float x) {
+                                   return wt.allows(x, wt.steps(x));
+                                 })
+                     : kLowestKey;
+  uint64_t live = 0;                 // groups that hold a logit min-p allows
+  for (int g = tid; g < G; g += kRowThreads)
+    live += ordered(sm.gmax[g]) >= min_key;
+  row_scan(live, sm.red, &live);
 
-  // ---- which logits go to the list ----
-  enum { kAll, kCount, kMass } by = kAll;      // what bins_of means
-  float floor_x = -__builtin_inff();           // x >= floor_x
-  float scale = 0.0f;                          // count bins of m - x
-  int lo_bin = 0, hi_bin = kBins - 1;          // lo_bin <= bin <= hi_bin
-  uint64_t mass = 0, before = 0;
+  // ---- which keys go to the list: first <= key < last ----
+  uint32_t first = min_key, last = 0xffffffffu;
+  uint64_t mass = 0, before = 0;     // top-p alone: weights of all, and in front
   bool listed = true;
-  const auto used = [&](int g) {
-    return sm.gmax[g] > -__builtin_inff() && sm.gmax[g] >= floor_x;
-  };
-  const auto count_bin = [&](float x) {        // never falls as x falls
-    if (x == top) return 0;
-    const float f = (top - x) * scale;
-    return f < float(kBins - 1) ? int(f) : kBins - 1;
-  };
-  if (q.need_k && k <= live) {
+  if (q.need_k && uint64_t(k) <= live) {
     // the k-th largest group maximum: at least k logits lie at or above it
     for (int g = tid; g < G; g += kRowThreads) {
       const float v = sm.gmax[g];
       int rank = 0;
       for (int j = 0; j < G; ++j)
         rank += sm.gmax[j] > v || (sm.gmax[j] == v && j < g);
-      if (rank == k - 1) sm.value = __float_as_uint(v);
+      if (rank == k - 1) sm.value = ordered(v);
     }
     __syncthreads();
-    floor_x = __uint_as_float(uint32_t(sm.value));
+    first = uint32_t(sm.value);
   } else if (q.need_k) {
-    // counts, in bins that put the lowest group maximum a quarter of the way
+    // counts, in bins of m - x that put the lowest group maximum at three
+    // quarters; kBins for whatever lies behind the last bin
     float low = top;
     for (int g = tid & 63; g < G; g += 64)
-      if (sm.gmax[g] > -__builtin_inff()) low = fminf(low, sm.gmax[g]);
+      if (ordered(sm.gmax[g]) >= min_key) low = fminf(low, sm.gmax[g]);
     low = -wave_max(-low);
-    scale = float(kBins / 4) / fmaxf(top - low, 1e-3f);
-    by = kCount;
+    const float scale = float(kBins / 4 * 3) / fmaxf(top - low, 1e-3f);
+    const auto bin_of = [&](float x) {         // never falls as x falls
+      if (x == top) return 0;
+      const float f = (top - x) * scale;
+      return f < float(kBins) ? int(f) : kBins;
+    };
     for (int i = tid; i < kBins; i += kRowThreads) sm.count[i] = 0;
     __syncthreads();
-    row.each(used, [&](float x, int) {
-      atomicAdd(&sm.count[count_bin(x)], 1u);
-    });
-    __syncthreads();
-    find_prefix<2>(sm, sm.count, kBins, uint64_t(k));
-    // (fewer than k logits: all of them)
-    if (sm.found >= 0) hi_bin = sm.found;
-    listed = sm.found < 0 || sm.before + sm.value <= kList;
+    uint64_t rest = 0;
+    row.each([&](int g) { return ordered(sm.gmax[g]) >= min_key; },
+             [&](float x, int) {
+               const int bin = bin_of(x);
+               if (bin < kBins)
+                 atomicAdd(&sm.count[bin], 1u);
+               else
+                 ++rest;
+             });
+    row_scan(rest, sm.red, &rest);
+    const uint64_t counted = find_prefix<2>(
+        sm, sm.count, kBins, [&](uint64_t) { return uint64_t(k); });
+    // (fewer than k in the bins: all there are, if the list takes them)
+    const int border = sm.found;
+    listed = (border >= 0 ? sm.before + sm.value : counted + rest) <= kList;
+    if (border >= 0)
+      first = max(first, least_key(top_key, [&](float x) {
+                    return bin_of(x) <= border;
+                  }));
   } else {
-    by = kMass;
     for (int i = tid; i < kBins; i += kRowThreads) sm.mass[i] = work.sums[i];
     __syncthreads();
-    mass = find_prefix<2>(sm, sm.mass, kBins, 0);
-    find_prefix<2>(sm, sm.mass, kBins, share_of(q.top_p, mass));
-    lo_bin = hi_bin = sm.found;
+    mass = find_prefix<2>(sm, sm.mass, kBins, [&](uint64_t w) {
+      return share_of(q.top_p, w);
+    });
     before = sm.before;
+    const int border = sm.found;
+    first = max(first, least_key(top_key, [&](float x) {
+                  return wt.bin(wt.steps(x)) <= border;
+                }));
+    if (border > 0)
+      last = least_key(top_key, [&](float x) {
+        return wt.bin(wt.steps(x)) < border;
+      });
   }
   if (listed) {
     __syncthreads();
-    row.each(
-        [&](int g) {
-          return used(g) &&
-                 (by != kMass || wt.bin(wt.steps(sm.gmax[g])) <= hi_bin);
-        },
-        [&](float x, int i) {
-          if (x < floor_x || (by == kCount && count_bin(x) > hi_bin)) return;
-          const double d = wt.steps(x);
-          if (!wt.allows(x, d)) return;
-          if (by == kMass) {
-            const int bin = wt.bin(d);
-            if (bin < lo_bin || bin > hi_bin) return;
+    row.each_group(
+        [&](int g) { return ordered(sm.gmax[g]) >= first; },
+        [&](const Group<BF16, VEC>& v) {
+          uint64_t in[8];
+          int n = 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t key = ordered(v.x[e]);
+            in[e] = __ballot(key >= first && key < last);
+            n += __popcll(in[e]);
           }
-          const uint32_t at = atomicAdd(&sm.n, 1u);
-          if (at < kList)
-            sm.list.key[at] = uint64_t(ordered(x)) << 32 | (0xffffffffu - i);
+          if (n == 0) return;
+          int at = 0;                  // one place for the whole group's
+          if ((tid & 63) == 0) at = atomicAdd(&sm.n, uint32_t(n));
+          at = uniform(at);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int mine =
+                at + __popcll(in[e] & ((uint64_t(1) << (tid & 63)) - 1));
+            if ((in[e] >> (tid & 63) & 1) && mine < kList)
+              sm.list.key[mine] = uint64_t(ordered(v.x[e])) << 32 |
+                                  (0xffffffffu - uint32_t(v.index(e)));
+            at += __popcll(in[e]);
+          }
         });
     __syncthreads();
     listed = sm.n <= kList;          // (ties may be many)
@@ -741,72 +904,74 @@ __global__ void __launch_bounds__(kRowThreads)
 
   if (listed) {
     const int n = sm.n;
-    sort_list(sm.list.key, n);
+    sort_list(sm, n);
     int kept = q.need_k ? min(n, k) : n;
     for (int i = tid; i < kept; i += kRowThreads)
       sm.list.w[i] = wt.of(unordered(uint32_t(sm.list.key[i] >> 32)));
     __syncthreads();
     if (q.need_p) {
-      if (q.need_k) mass = find_prefix<4>(sm, sm.list.w, kept, 0);
-      find_prefix<4>(sm, sm.list.w, kept, share_of(q.top_p, mass) - before);
+      find_prefix<4>(sm, sm.list.w, kept, [&](uint64_t w) {
+        return share_of(q.top_p, q.need_k ? w : mass) - before;
+      });
       if (sm.found >= 0) kept = sm.found + 1;
-      __syncthreads();
     }
-    if (by == kMass) {
+    if (!q.need_k) {
       // the last kept one is the threshold pair
-      const uint64_t last = sm.list.key[kept - 1];
-      thr = Threshold{uint32_t(last >> 32),
-                      int(0xffffffffu - uint32_t(last))};
+      const uint64_t end = sm.list.key[kept - 1];
+      thr = Threshold{uint32_t(end >> 32), int(0xffffffffu - uint32_t(end))};
     } else {
-      // the kept ones in the order of their indexes
-      for (int i = tid; i < kept; i += kRowThreads)
-        sm.list.key[i] = sm.list.key[i] << 32 | uint32_t(i);
-      __syncthreads();
-      sort_list(sm.list.key, kept);
-      uint64_t w[kList / kRowThreads];
-#pragma unroll
-      for (int j = 0; j < kList / kRowThreads; ++j) {
-        const int i = tid + j * kRowThreads;
-        w[j] = i < kept ? sm.list.w[uint32_t(sm.list.key[i])] : 0;
+      // the index whose running weight passes u: by its upper ten bits, then
+      // by its lower ten
+      uint64_t* bins = reinterpret_cast<uint64_t*>(sm.gmax);
+      static_assert(kMaxGroups * kGroup <= 1 << 20 &&
+                    sizeof(sm.gmax) >= 1024 * sizeof(uint64_t), "index bits");
+      uint64_t target = 0;
+      int high = 0;
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        __syncthreads();
+        for (int i = tid; i < 1024; i += kRowThreads) bins[i] = 0;
+        __syncthreads();
+        for (int i = tid; i < kept; i += kRowThreads) {
+          const int at = int(0xffffffffu - uint32_t(sm.list.key[i]));
+          if (pass == 0 || at >> 10 == high)
+            atomicAdd((unsigned long long*)&bins[pass == 0 ? at >> 10
+                                                           : at & 1023],
+                      (unsigned long long)sm.list.w[i]);
+        }
+        __syncthreads();
+        find_prefix<1>(sm, bins, 1024, [&](uint64_t w) {
+          if (pass == 0) target = past_share(q.u, w);
+          return target;
+        });
+        target -= sm.before;
+        if (pass == 0) high = max(sm.found, 0);
       }
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < kList / kRowThreads; ++j) {
-        const int i = tid + j * kRowThreads;
-        if (i < kept) sm.list.w[i] = w[j];
-      }
-      __syncthreads();
-      mass = find_prefix<4>(sm, sm.list.w, kept, 0);
-      const uint64_t past = uint64_t(double(q.u) * double(mass)) + 1;
-      find_prefix<4>(sm, sm.list.w, kept, past < mass ? past : mass);
-      if (tid == 0)
-        p.tokens[m] = int(0xffffffffu -
-                          uint32_t(sm.list.key[max(sm.found, 0)] >> 32));
+      if (tid == 0) p.tokens[m] = high << 10 | max(sm.found, 0);
       return;
     }
   } else {
     // ---- no list holds them: thresholds by radix search ----
+    const auto used = [&](int g) { return ordered(sm.gmax[g]) >= min_key; };
     __syncthreads();
     if (q.need_k) {
       uint64_t n = 0;
-      row.each(used, [&](float x, int) { n += wt.allows(x, wt.steps(x)); });
-      row_scan(n, sm.red);
-      if (sm.red[kWaves] > uint64_t(k))
-        thr = search<BF16, VEC>(row, wt, thr, uint64_t(k),
-                                [](double) { return uint64_t(1); });
+      row.each(used, [&](float x, int) { n += ordered(x) >= min_key; });
+      row_scan(n, sm.red, &n);
+      if (n > uint64_t(k))
+        thr = search<BF16, VEC>(row, min_key, thr, uint64_t(k),
+                                [](float) { return uint64_t(1); });
       if (q.need_p) {
         uint64_t sum = 0;
         row.each(used, [&](float x, int i) {
-          const double d = wt.steps(x);
-          if (wt.allows(x, d) && thr.keeps(x, i)) sum += wt.whole(d);
+          if (ordered(x) >= min_key && thr.keeps(x, i)) sum += wt.of(x);
         });
-        row_scan(sum, sm.red);
-        mass = sm.red[kWaves];
+        row_scan(sum, sm.red, &mass);
       }
     }
     if (q.need_p)
-      thr = search<BF16, VEC>(row, wt, thr, share_of(q.top_p, mass),
-                              [&](double d) { return wt.whole(d); });
+      thr = search<BF16, VEC>(row, min_key, thr, share_of(q.top_p, mass),
+                              [&](float x) { return wt.of(x); });
   }
   // the kept weights of each group are left to many workgroups
   if (tid == 0) {
