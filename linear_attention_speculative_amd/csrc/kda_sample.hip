@@ -14,8 +14,9 @@
 //
 //   kda_group_max_kernel reads the logits once (the floor: HBM) and leaves the
 //   maximum of every group of 512.
-//   kda_row_sums_kernel, only for rows without top-k: with top-p the weights
-//   by bins of 1/32 octave of d, without it the weights of each group.
+//   kda_row_sums_kernel, only for rows that need it: with top-p alone the
+//   weights by bins of 1/32 octave of d, with top-k > groups counts by bins,
+//   without either the weights of each group.
 //   kda_sample_kernel, one workgroup a row, reads only what it still needs.
 //   Greedy rows read one group.  With top-k <= groups, the k-th largest group
 //   maximum bounds the k-th largest value from below: only groups at or above
@@ -651,8 +652,40 @@ __device__ __forceinline__ float row_max(const float* gmax, int G) {
   return wave_max(top);
 }
 
-// Rows without top-k, kPerWg groups a workgroup: with top-p the weights by
-// bins, added to the row's bins, otherwise the weight of each group.
+// Bins of m - x for counts, with the lowest maximum among the groups that
+// hold a key of at least min_key at three quarters; kBins for whatever lies
+// behind the last bin (or cannot be told, below a maximum of +inf).
+struct CountBins {
+  float top, scale;
+  __device__ __forceinline__ CountBins(const float* gmax, int G, float top_,
+                                       uint32_t min_key)
+      : top(top_) {
+    float low = top;
+    for (int g = threadIdx.x & 63; g < G; g += 64)
+      if (ordered(gmax[g]) >= min_key) low = fminf(low, gmax[g]);
+    low = -wave_max(-low);
+    scale = float(kBins / 4 * 3) / fmaxf(top - low, 1e-3f);
+  }
+  // never falls as x falls
+  __device__ __forceinline__ int operator()(float x) const {
+    const float f = (top - x) * scale;
+    return f < float(kBins) ? int(f) : kBins;
+  }
+};
+
+// Least key that min-p allows.
+__device__ __forceinline__ uint32_t least_allowed(const Params& q,
+                                                  const Weights& wt,
+                                                  float top) {
+  if (!(q.min_p > 0.0f)) return kLowestKey;
+  return least_key(ordered(top),
+                   [&](float x) { return wt.allows(x, wt.steps(x)); });
+}
+
+// kPerWg groups a workgroup, of the rows that need more than their group
+// maxima: top-k beyond the number of groups, counts by bins; top-p alone,
+// weights by bins (both added to the row's bins); neither, the weight of each
+// group.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads)
     kda_row_sums_kernel(SampleParams p, int G, int per_row, int places) {
@@ -663,16 +696,20 @@ __global__ void __launch_bounds__(kMaxThreads)
   const int b = request_of_row(p, m, lane);
   if (b < 0) return;
   const Params q(p, b, m);
-  if (q.greedy || q.need_k) return;
+  const bool counts = q.need_k;
+  if (q.greedy || (counts && q.k <= G)) return;
   const Work work(p, m, G);
   const float top = row_max(work.gmax, G);
   if (top == -__builtin_inff()) return;
   fill_table(table);
-  if (q.need_p)
+  const bool binned = counts || q.need_p;
+  if (binned)
     for (int i = threadIdx.x; i < kBins; i += kMaxThreads) mass[i] = 0;
   __syncthreads();
   Weights wt;
   wt.init(table, top, q.T, q.min_p, places);
+  const uint32_t min_key = least_allowed(q, wt, top);
+  const CountBins bins(work.gmax, G, top, min_key);
   const char* row = static_cast<const char*>(p.logits) +
                     m * p.s_row * (BF16 ? 2 : 4);
 #pragma unroll 1
@@ -680,28 +717,36 @@ __global__ void __launch_bounds__(kMaxThreads)
     const int g = part * kPerWg + wave * (kPerWg / 4) + i;
     if (g >= G) break;
     // a group whose largest logit min-p drops has nothing to add
-    if (!wt.allows(work.gmax[g], wt.steps(work.gmax[g]))) {
-      if (!q.need_p && lane == 0) work.sums[g] = 0;
+    if (ordered(work.gmax[g]) < min_key) {
+      if (!binned && lane == 0) work.sums[g] = 0;
       continue;
     }
     Group<BF16, VEC> v;
     v.load(row, g, p.V);
+    if (counts) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int bin = bins(v.x[e]);
+        if (bin < kBins) atomicAdd(&mass[bin], 1ull);
+      }
+      continue;
+    }
     uint64_t sum = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const double d = wt.steps(v.x[e]);
-      const uint64_t w = wt.allows(v.x[e], d) ? wt.whole(d) : 0;
-      if (!q.need_p)
+      const uint64_t w = ordered(v.x[e]) >= min_key ? wt.whole(d) : 0;
+      if (!binned)
         sum += w;
       else if (w > 0)
         atomicAdd(&mass[wt.bin(d)], (unsigned long long)w);
     }
-    if (!q.need_p) {
+    if (!binned) {
       sum = wave_sum64(sum);
       if (lane == 0) work.sums[g] = sum;
     }
   }
-  if (!q.need_p) return;
+  if (!binned) return;
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += kMaxThreads)
     if (mass[i] > 0)
@@ -795,12 +840,7 @@ __global__ void __launch_bounds__(kRowThreads)
   }
   // Every condition on a logit's weight is one on its key.
   const uint32_t top_key = ordered(top);
-  const uint32_t min_key =
-      q.min_p > 0.0f ? least_key(top_key,
-                                 [&](float x) {
-                                   return wt.allows(x, wt.steps(x));
-                                 })
-                     : kLowestKey;
+  const uint32_t min_key = least_allowed(q, wt, top);
   uint64_t live = 0;                 // groups that hold a logit min-p allows
   for (int g = tid; g < G; g += kRowThreads)
     live += ordered(sm.gmax[g]) >= min_key;
@@ -822,38 +862,28 @@ __global__ void __launch_bounds__(kRowThreads)
     __syncthreads();
     first = uint32_t(sm.value);
   } else if (q.need_k) {
-    // counts, in bins of m - x that put the lowest group maximum at three
-    // quarters; kBins for whatever lies behind the last bin
-    float low = top;
-    for (int g = tid & 63; g < G; g += 64)
-      if (ordered(sm.gmax[g]) >= min_key) low = fminf(low, sm.gmax[g]);
-    low = -wave_max(-low);
-    const float scale = float(kBins / 4 * 3) / fmaxf(top - low, 1e-3f);
-    const auto bin_of = [&](float x) {         // never falls as x falls
-      if (x == top) return 0;
-      const float f = (top - x) * scale;
-      return f < float(kBins) ? int(f) : kBins;
-    };
-    for (int i = tid; i < kBins; i += kRowThreads) sm.count[i] = 0;
+    const CountBins bins(sm.gmax, G, top, min_key);
+    if (k > G) {                     // counted by the kernel before
+      for (int i = tid; i < kBins; i += kRowThreads)
+        sm.count[i] = uint32_t(work.sums[i]);
+    } else {
+      for (int i = tid; i < kBins; i += kRowThreads) sm.count[i] = 0;
+      __syncthreads();
+      row.each([&](int g) { return ordered(sm.gmax[g]) >= min_key; },
+               [&](float x, int) {
+                 const int bin = bins(x);
+                 if (bin < kBins) atomicAdd(&sm.count[bin], 1u);
+               });
+    }
     __syncthreads();
-    uint64_t rest = 0;
-    row.each([&](int g) { return ordered(sm.gmax[g]) >= min_key; },
-             [&](float x, int) {
-               const int bin = bin_of(x);
-               if (bin < kBins)
-                 atomicAdd(&sm.count[bin], 1u);
-               else
-                 ++rest;
-             });
-    row_scan(rest, sm.red, &rest);
-    const uint64_t counted = find_prefix<2>(
-        sm, sm.count, kBins, [&](uint64_t) { return uint64_t(k); });
-    // (fewer than k in the bins: all there are, if the list takes them)
+    find_prefix<2>(sm, sm.count, kBins,
+                   [&](uint64_t) { return uint64_t(k); });
     const int border = sm.found;
-    listed = (border >= 0 ? sm.before + sm.value : counted + rest) <= kList;
+    // (fewer than k in the bins: all there are, if the list surely takes them)
+    listed = border >= 0 ? sm.before + sm.value <= kList : p.V <= kList;
     if (border >= 0)
       first = max(first, least_key(top_key, [&](float x) {
-                    return bin_of(x) <= border;
+                    return bins(x) <= border;
                   }));
   } else {
     for (int i = tid; i < kBins; i += kRowThreads) sm.mass[i] = work.sums[i];
@@ -873,6 +903,10 @@ __global__ void __launch_bounds__(kRowThreads)
   }
   if (listed) {
     __syncthreads();
+    // as floats; without a last key, one that nothing compares with
+    const float x_first = unordered(first);
+    const float x_last = last == 0xffffffffu ? __builtin_nanf("")
+                                             : unordered(last);
     row.each_group(
         [&](int g) { return ordered(sm.gmax[g]) >= first; },
         [&](const Group<BF16, VEC>& v) {
@@ -880,19 +914,20 @@ __global__ void __launch_bounds__(kRowThreads)
           int n = 0;
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const uint32_t key = ordered(v.x[e]);
-            in[e] = __ballot(key >= first && key < last);
+            in[e] = __ballot(v.x[e] >= x_first && !(v.x[e] >= x_last));
             n += __popcll(in[e]);
           }
           if (n == 0) return;
-          int at = 0;                  // one place for the whole group's
+          uint32_t at = 0;             // one place for the whole group's
           if ((tid & 63) == 0) at = atomicAdd(&sm.n, uint32_t(n));
-          at = uniform(at);
+          at = uint32_t(uniform(int(at)));
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int mine =
-                at + __popcll(in[e] & ((uint64_t(1) << (tid & 63)) - 1));
-            if ((in[e] >> (tid & 63) & 1) && mine < kList)
+            if (in[e] == 0) continue;
+            const uint32_t mine = __builtin_amdgcn_mbcnt_hi(
+                uint32_t(in[e] >> 32),
+                __builtin_amdgcn_mbcnt_lo(uint32_t(in[e]), at));
+            if (v.x[e] >= x_first && !(v.x[e] >= x_last) && mine < kList)
               sm.list.key[mine] = uint64_t(ordered(v.x[e])) << 32 |
                                   (0xffffffffu - uint32_t(v.index(e)));
             at += __popcll(in[e]);
