@@ -37,10 +37,17 @@ constexpr int kGroup = 512;          // logits of a group
 constexpr int kMaxGroups = 2048;     // V up to 2^20
 constexpr int kMaxThreads = 256;     // group maximum kernel
 constexpr int kPerWg = 4 * 4;        // its groups per workgroup
-constexpr int kRowThreads = 1024;    // row kernel
+constexpr int kRowThreads = 512;     // row kernel: two rows a CU, whose waits
+                                     // overlap (1024 window rows: 76 us against 98
+                                     // with 1024 threads; one row alone 43, 35)
 constexpr int kWaves = kRowThreads / 64;
 constexpr int kList = 4096;          // entries of the sorted list
 constexpr int kBins = 2048;
+// items per thread of the row kernel: bins and groups, list entries, half bins
+constexpr int kPer2k = kBins / kRowThreads;
+constexpr int kPerList = kList / kRowThreads;
+constexpr int kPer1k = 1024 / kRowThreads;
+static_assert(kBins == kMaxGroups && kPer1k >= 1, "sizes");
 constexpr int kSteps = 256;          // of an octave, in the table of weights
 
 __device__ __forceinline__ float logit(const SampleParams& p, const char* row,
@@ -525,8 +532,11 @@ __device__ __forceinline__ void sort_list(RowSmem& sm, int n) {
     sort_keys<1>(sm.list.key, sm.list.w, size);
   else if (size <= 2 * kRowThreads)
     sort_keys<2>(sm.list.key, sm.list.w, size);
-  else
+  else if (size <= 4 * kRowThreads)
     sort_keys<4>(sm.list.key, sm.list.w, size);
+  else
+    sort_keys<8>(sm.list.key, sm.list.w, size);
+  static_assert(kList <= 8 * kRowThreads, "sort");
 }
 
 // Target of a share of a whole: the least integer >= share * mass, at least 1
@@ -604,7 +614,7 @@ __device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
                   (unsigned long long)what(x));
     });
     __syncthreads();
-    find_prefix<2>(sm, sm.mass, bins,
+    find_prefix<kPer2k>(sm, sm.mass, bins,
                    [&](uint64_t) { return target - before; });
     before += sm.before;
     prefix |= uint32_t(bins - 1 - max(sm.found, 0)) << shift;
@@ -622,7 +632,7 @@ __device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
       atomicAdd((unsigned long long*)&sm.group[i / kGroup], 1ull);
   });
   __syncthreads();
-  find_prefix<2>(sm, sm.group, row.G, [&](uint64_t) { return rank; });
+  find_prefix<kPer2k>(sm, sm.group, row.G, [&](uint64_t) { return rank; });
   const int g = sm.found;
   const uint64_t seen = sm.before;
   if (threadIdx.x == 0) sm.pick = row.V - 1;
@@ -761,7 +771,7 @@ __device__ __forceinline__ void pick_token(const SampleParams& p,
                                            const Weights& wt, Threshold thr,
                                            float u, int m) {
   RowSmem& sm = row.sm;
-  const uint64_t mass = find_prefix<2>(
+  const uint64_t mass = find_prefix<kPer2k>(
       sm, sm.group, row.G, [&](uint64_t w) { return past_share(u, w); });
   const uint64_t target = past_share(u, mass);
   const uint64_t before = sm.before;
@@ -803,7 +813,6 @@ __global__ void __launch_bounds__(kRowThreads)
   if (tid == 0) {
     sm.found = G;
     sm.pick = p.V;
-    sm.n = 0;
   }
   __syncthreads();
   const float top = row_max(sm.gmax, G);
@@ -850,58 +859,10 @@ __global__ void __launch_bounds__(kRowThreads)
   uint32_t first = min_key, last = 0xffffffffu;
   uint64_t mass = 0, before = 0;     // top-p alone: weights of all, and in front
   bool listed = true;
-  if (q.need_k && uint64_t(k) <= live) {
-    // the k-th largest group maximum: at least k logits lie at or above it
-    for (int g = tid; g < G; g += kRowThreads) {
-      const float v = sm.gmax[g];
-      int rank = 0;
-      for (int j = 0; j < G; ++j)
-        rank += sm.gmax[j] > v || (sm.gmax[j] == v && j < g);
-      if (rank == k - 1) sm.value = ordered(v);
-    }
-    __syncthreads();
-    first = uint32_t(sm.value);
-  } else if (q.need_k) {
-    const CountBins bins(sm.gmax, G, top, min_key);
-    if (k > G) {                     // counted by the kernel before
-      for (int i = tid; i < kBins; i += kRowThreads)
-        sm.count[i] = uint32_t(work.sums[i]);
-    } else {
-      for (int i = tid; i < kBins; i += kRowThreads) sm.count[i] = 0;
-      __syncthreads();
-      row.each([&](int g) { return ordered(sm.gmax[g]) >= min_key; },
-               [&](float x, int) {
-                 const int bin = bins(x);
-                 if (bin < kBins) atomicAdd(&sm.count[bin], 1u);
-               });
-    }
-    __syncthreads();
-    find_prefix<2>(sm, sm.count, kBins,
-                   [&](uint64_t) { return uint64_t(k); });
-    const int border = sm.found;
-    // (fewer than k in the bins: all there are, if the list surely takes them)
-    listed = border >= 0 ? sm.before + sm.value <= kList : p.V <= kList;
-    if (border >= 0)
-      first = max(first, least_key(top_key, [&](float x) {
-                    return bins(x) <= border;
-                  }));
-  } else {
-    for (int i = tid; i < kBins; i += kRowThreads) sm.mass[i] = work.sums[i];
-    __syncthreads();
-    mass = find_prefix<2>(sm, sm.mass, kBins, [&](uint64_t w) {
-      return share_of(q.top_p, w);
-    });
-    before = sm.before;
-    const int border = sm.found;
-    first = max(first, least_key(top_key, [&](float x) {
-                  return wt.bin(wt.steps(x)) <= border;
-                }));
-    if (border > 0)
-      last = least_key(top_key, [&](float x) {
-        return wt.bin(wt.steps(x)) < border;
-      });
-  }
-  if (listed) {
+  // Puts the keys first <= key < last into the list, in any order; whether it
+  // took all of them (ties may be many).
+  const auto gather = [&]() {
+    if (tid == 0) sm.n = 0;
     __syncthreads();
     // as floats; without a last key, one that nothing compares with
     const float x_first = unordered(first);
@@ -934,8 +895,73 @@ __global__ void __launch_bounds__(kRowThreads)
           }
         });
     __syncthreads();
-    listed = sm.n <= kList;          // (ties may be many)
+    return sm.n <= kList;
+  };
+  // Fewer groups than k hold what min-p allows: likely few logits in all.
+  bool have_list = q.need_k && q.min_p > 0.0f && uint64_t(k) > live && gather();
+  if (have_list) {
+    // (cut at k below)
+  } else if (q.need_k && uint64_t(k) <= live) {
+    // the k-th largest group maximum: at least k logits lie at or above it
+    // (ranks by counting, several threads to a group where there are few)
+    int parts = 1;
+    while (2 * parts * G <= kRowThreads) parts *= 2;
+    for (int g = tid; g < G; g += kRowThreads) sm.count[g] = 0;
+    __syncthreads();
+    for (int i = tid; i < G * parts; i += kRowThreads) {
+      const int g = i / parts;
+      const float v = sm.gmax[g];
+      int rank = 0;
+      for (int j = i & (parts - 1); j < G; j += parts)
+        rank += sm.gmax[j] > v || (sm.gmax[j] == v && j < g);
+      atomicAdd(&sm.count[g], uint32_t(rank));
+    }
+    __syncthreads();
+    for (int g = tid; g < G; g += kRowThreads)
+      if (sm.count[g] == uint32_t(k - 1)) sm.value = ordered(sm.gmax[g]);
+    __syncthreads();
+    first = uint32_t(sm.value);
+  } else if (q.need_k) {
+    const CountBins bins(sm.gmax, G, top, min_key);
+    if (k > G) {                     // counted by the kernel before
+      for (int i = tid; i < kBins; i += kRowThreads)
+        sm.count[i] = uint32_t(work.sums[i]);
+    } else {
+      for (int i = tid; i < kBins; i += kRowThreads) sm.count[i] = 0;
+      __syncthreads();
+      row.each([&](int g) { return ordered(sm.gmax[g]) >= min_key; },
+               [&](float x, int) {
+                 const int bin = bins(x);
+                 if (bin < kBins) atomicAdd(&sm.count[bin], 1u);
+               });
+    }
+    __syncthreads();
+    find_prefix<kPer2k>(sm, sm.count, kBins,
+                   [&](uint64_t) { return uint64_t(k); });
+    const int border = sm.found;
+    // (fewer than k in the bins: all there are, if the list surely takes them)
+    listed = border >= 0 ? sm.before + sm.value <= kList : p.V <= kList;
+    if (border >= 0)
+      first = max(first, least_key(top_key, [&](float x) {
+                    return bins(x) <= border;
+                  }));
+  } else {
+    for (int i = tid; i < kBins; i += kRowThreads) sm.mass[i] = work.sums[i];
+    __syncthreads();
+    mass = find_prefix<kPer2k>(sm, sm.mass, kBins, [&](uint64_t w) {
+      return share_of(q.top_p, w);
+    });
+    before = sm.before;
+    const int border = sm.found;
+    first = max(first, least_key(top_key, [&](float x) {
+                  return wt.bin(wt.steps(x)) <= border;
+                }));
+    if (border > 0)
+      last = least_key(top_key, [&](float x) {
+        return wt.bin(wt.steps(x)) < border;
+      });
   }
+  if (listed && !have_list) listed = gather();
 
   if (listed) {
     const int n = sm.n;
@@ -945,7 +971,7 @@ __global__ void __launch_bounds__(kRowThreads)
       sm.list.w[i] = wt.of(unordered(uint32_t(sm.list.key[i] >> 32)));
     __syncthreads();
     if (q.need_p) {
-      find_prefix<4>(sm, sm.list.w, kept, [&](uint64_t w) {
+      find_prefix<kPerList>(sm, sm.list.w, kept, [&](uint64_t w) {
         return share_of(q.top_p, q.need_k ? w : mass) - before;
       });
       if (sm.found >= 0) kept = sm.found + 1;
@@ -975,7 +1001,7 @@ __global__ void __launch_bounds__(kRowThreads)
                       (unsigned long long)sm.list.w[i]);
         }
         __syncthreads();
-        find_prefix<1>(sm, bins, 1024, [&](uint64_t w) {
+        find_prefix<kPer1k>(sm, bins, 1024, [&](uint64_t w) {
           if (pass == 0) target = past_share(q.u, w);
           return target;
         });
