@@ -211,11 +211,13 @@ __device__ __forceinline__ int request_of_slot(const PrefillParams& p,
 // Place of request b in the order of falling lengths (ties by number), written
 // to the order that the state kernel takes its requests in: its workgroups
 // then start with the longest ones, and the short ones fill the gaps.  Empty
-// requests have no place; order[-1] counts the others.
+// requests have no place; order[-1] counts the others.  The first workgroup
+// writes the count even where it holds no request (b = -1), so that a batch
+// of empty requests leaves 0 there and not what the workspace held.
 template <int D>
 __device__ __forceinline__ void rank_request(const PrefillParams& p, int b,
                                              ChunkSmem<D>& m) {
-  const int2 mine = token_range(p, b);
+  const int2 mine = b < 0 ? make_int2(0, 0) : token_range(p, b);
   const int len = mine.y - mine.x;
   int before = 0, all = 0;
   for (int i = threadIdx.x; i < p.y.B; i += ChunkCfg<D>::NT) {
@@ -229,8 +231,8 @@ __device__ __forceinline__ void rank_request(const PrefillParams& p, int b,
   atomicAdd(&m.all, all);
   __syncthreads();
   if (threadIdx.x == 0) {
-    p.order[m.before] = b;
-    p.order[-1] = m.all;
+    if (b >= 0) p.order[m.before] = b;
+    if (blockIdx.x == 0) p.order[-1] = m.all;
   }
 }
 
@@ -250,10 +252,15 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
 
   if (tid == 0) m.before = m.all = m.task = 0;
   const int b = request_of_slot(p, slot, lane);
-  if (b < 0) return;
+  if (b < 0) {
+    if (blockIdx.x == 0) rank_request<D>(p, -1, m);
+    return;
+  }
   const int2 range = token_range(p, b);
   const int first = (slot - first_slot(range.x, b)) * C;   // in the request
-  if (first == 0 && h == 0) rank_request<D>(p, b, m);
+  // (offsets that run backwards can give slot 0 to a later chunk)
+  if (h == 0 && (first == 0 || slot == 0))
+    rank_request<D>(p, first == 0 ? b : -1, m);
   if (!live_slot(y, y.slots[b])) return;
   const int t0 = range.x + first, n = min(C, range.y - t0);
   char* work = p.work + (int64_t(slot) * y.H + h) * W::size(O32);
@@ -743,7 +750,7 @@ __device__ __forceinline__ void load_lds(const char* base, uint32_t off,
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(lds), "v"(off), "s"(base)
-      : "memory");
+      : "memory", "m0");
 }
 
 // Wait until at most N of this wave's global memory operations are under way
@@ -756,7 +763,7 @@ __device__ __forceinline__ void wait_vm() {
 
 // LDS of the state kernel: BUFS buffers of one chunk's operands (in workspace
 // order without V, then each wave's two V operands, whose place takes the
-
+// chunk's outputs on their way to memory).
 template <int D, bool O32, int WAVES, int PROD, int BUFS>
 struct Stage {
   using W = Work<D>;
@@ -790,8 +797,10 @@ __global__ void __launch_bounds__(64 * (WAVES + PROD))
   const int item = grp * 8 + in % 8;
   const int vt0 = in / 8 * WAVES, vt = vt0 + wave;
   const int rank = item / y.H, h = item - rank * y.H;
-  if (rank >= p.order[-1]) return;
+  if (rank >= y.B || rank >= p.order[-1]) return;
   const int b = p.order[rank];
+  // offsets that run backwards leave places of the order unwritten
+  if (b < 0 || b >= y.B) return;
   const int2 range = token_range(p, b);
   const int L = range.y - range.x;
   const int dst = y.slots[b];

@@ -186,6 +186,32 @@ def test_unordered_offsets_stay_inside():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("qsl", [[0, 0, 0, 0], [40, 40, 40, 40],
+                                 [33, 0, 70, 0], [40, 5, 5, 39]])
+def test_workspace_content_is_never_an_index(qsl):
+    """A batch of rows without any request's token (as a padded launch has
+    them) changes nothing, and no batch takes an index from what an earlier
+    call left in the workspace."""
+    kw = make_layer(40, 4, 3, 64, 3, act="f32", seed=17)
+    before = {n: kw[n].clone() for n in ("out", "state", "conv_state")}
+    work = workspace(kw, 3)
+    work.view(torch.int32).fill_(2)
+    args = dict(kw, query_start_loc=i32(qsl, DEV),
+                state_indices=i32([1, 2, 3], DEV), workspace=work)
+    kda.conv_prefill(**args)
+    torch.cuda.synchronize()
+    if len(set(qsl)) == 1:
+        for name, old in before.items():
+            assert torch.equal(kw[name], old), name
+        # the same rows as one request, over the same workspace
+        args["query_start_loc"] = i32([0, 40, 40, 40], DEV)
+        ref = reference(kw, [0, 40, 40, 40], [1, 2, 3], None)
+        kda.conv_prefill(**args)
+        torch.cuda.synchronize()
+        compare(kw, ref, [1], pairs=True)
+
+
+@pytest.mark.gpu
 def test_graph_replays_and_streams():
     """A captured prefill replayed over new inputs, with eager work between
     the replays, against eager calls; the call runs on the stream given."""
