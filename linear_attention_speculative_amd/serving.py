@@ -19,55 +19,50 @@ from . import _abi
 from .ops import (_DT, _pack_format, _ptr, _raise, _tensor_values)
 
 
-def _on_device(tensors) -> torch.device:
-    """The GPU that holds all of `tensors` (None entries are skipped)."""
-    device = None
-    for t in tensors:
-        if t is None:
-            continue
-        if device is None:
-            device = t.device
-        if t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
-    if device is None or device.type != "cuda":
+def _launch(entry, args, kwargs, stream) -> None:
+    """Calls `entry` with the tensors' GPU current, on that GPU's current
+    stream or the one given."""
+    index = None
+    for t in kwargs.values():
+        if isinstance(t, torch.Tensor) and t.get_device() != index:
+            if index is not None:
+                raise ValueError("tensors on different devices (the index "
+                                 f"of one is {index}, of another "
+                                 f"{t.get_device()})")
+            index = t.get_device()
+    if index is None or index < 0:
         raise ValueError("the tensors must be on a GPU")
-    return device
-
-
-def _launch(entry, args, tensors, stream) -> None:
-    device = _on_device(tensors)
-    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
-        raise ValueError(f"a stream of {stream.device} for tensors on "
-                         f"{device}")
-    with torch.cuda.device(device):
-        if stream is None:
-            stream = torch.cuda.current_stream(device)
-        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) \
-            else int(stream)
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(index)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device.index != index:
+            raise ValueError(f"a stream of {stream.device} for tensors on "
+                             f"GPU {index}")
+        handle = stream.cuda_stream
+    else:
+        handle = int(stream)
+    if torch.cuda.current_device() == index:
         rc = entry(ctypes.byref(args), handle)
+    else:
+        with torch.cuda.device(index):
+            rc = entry(ctypes.byref(args), handle)
     if rc != _abi.KDA_OK:
         _raise(rc)
 
 
-def _ints(t, name: str, size: int, *, exact=False) -> int:
+def _ints(t, name: str, size: int) -> int:
     """Pointer of an int32 index array of at least `size` entries (0 for
     None)."""
     if t is None:
         return 0
-    if t.dim() != 1 or t.numel() < size or (exact and t.numel() != size):
+    if t.dim() != 1 or t.numel() < size:
         raise ValueError(f"{name} needs {size} entries (got "
                          f"{list(t.shape)})")
     return _ptr(t) or 0
 
 
-_LAYER = ("mixed_qkv", "raw_gate", "raw_beta", "A_log", "dt_bias", "state",
-          "out", "conv_state", "conv_weight")
 _PREFILL_PACK = struct.Struct("<" + _pack_format(_abi.KdaPrefillArgs))
 _DECODE_PACK = struct.Struct("<" + _pack_format(_abi.KdaDecodeArgs))
-
-
-def _layer_values(kw) -> list:
-    return [v for name in _LAYER for v in _tensor_values(kw[name])]
 
 
 def prefill_workspace_size(tokens: int, batch: int, num_heads: int,
@@ -90,11 +85,14 @@ def prefill_args(*, mixed_qkv, raw_gate, raw_beta, A_log, dt_bias,
                  initial_state_indices=None, num_accepted_tokens=None,
                  null_block_id=0) -> _abi.KdaPrefillArgs:
     """kda_prefill_args for these tensors."""
-    kw = dict(locals())
     B = state_indices.shape[0]
     if not workspace.is_contiguous():
         raise ValueError("the workspace must be contiguous")
-    vals = (*_layer_values(kw),
+    vals = (*_tensor_values(mixed_qkv), *_tensor_values(raw_gate),
+            *_tensor_values(raw_beta), *_tensor_values(A_log),
+            *_tensor_values(dt_bias), *_tensor_values(state),
+            *_tensor_values(out), *_tensor_values(conv_state),
+            *_tensor_values(conv_weight),
             _ints(query_start_loc, "query_start_loc", B + 1),
             _ints(state_indices, "state_indices", B),
             _ints(initial_state_indices, "initial_state_indices", B),
@@ -122,7 +120,7 @@ def conv_prefill(*, stream=None, **kwargs) -> None:
     include/kda_recoverssm.h; `workspace` is scratch memory of
     `prefill_workspace_size` bytes."""
     _launch(_abi.load().kda_conv_prefill, prefill_args(**kwargs),
-            _tensors(kwargs), stream)
+            kwargs, stream)
 
 
 def check_prefill_qkv(**kwargs) -> int:
@@ -137,7 +135,7 @@ def prefill_qkv(*, stream=None, **kwargs) -> None:
     accepted counts)."""
     _no_conv(kwargs)
     _launch(_abi.load().kda_prefill_qkv, prefill_args(**kwargs),
-            _tensors(kwargs), stream)
+            kwargs, stream)
 
 
 def decode_args(*, mixed_qkv, raw_gate, raw_beta, A_log, dt_bias,
@@ -146,19 +144,19 @@ def decode_args(*, mixed_qkv, raw_gate, raw_beta, A_log, dt_bias,
                 final_state_indices=None, num_accepted_tokens=None,
                 null_block_id=0) -> _abi.KdaDecodeArgs:
     """kda_decode_args for these tensors."""
-    kw = dict(locals())
     B = state_indices.shape[0]
-    vals = (*_layer_values(kw), _ints(state_indices, "state_indices", B),
+    vals = (*_tensor_values(mixed_qkv), *_tensor_values(raw_gate),
+            *_tensor_values(raw_beta), *_tensor_values(A_log),
+            *_tensor_values(dt_bias), *_tensor_values(state),
+            *_tensor_values(out), *_tensor_values(conv_state),
+            *_tensor_values(conv_weight),
+            _ints(state_indices, "state_indices", B),
             _ints(final_state_indices, "final_state_indices", B),
             _ints(num_accepted_tokens, "num_accepted_tokens", B),
             B, spec_query_len, null_block_id, 1 if conv_dim_first else 0,
             0 if lower_bound is None else 1,
             0.0 if lower_bound is None else float(lower_bound))
     return _abi.KdaDecodeArgs.from_buffer_copy(_DECODE_PACK.pack(*vals))
-
-
-def _tensors(kw):
-    return [v for v in kw.values() if isinstance(v, torch.Tensor)]
 
 
 def check_decode(**kwargs) -> int:
@@ -174,7 +172,7 @@ def conv_update_decode(*, stream=None, **kwargs) -> None:
     include/kda_recoverssm.h; `lower_bound=None` selects the softplus gate,
     `num_accepted_tokens=None` reads histories at offset 0."""
     _launch(_abi.load().kda_conv_update_decode, decode_args(**kwargs),
-            _tensors(kwargs), stream)
+            kwargs, stream)
 
 
 def _no_conv(kwargs):
@@ -195,7 +193,7 @@ def decode_qkv(*, stream=None, **kwargs) -> None:
     taps or accepted counts)."""
     _no_conv(kwargs)
     _launch(_abi.load().kda_decode_qkv, decode_args(**kwargs),
-            _tensors(kwargs), stream)
+            kwargs, stream)
 
 
 _TABLES_PACK = struct.Struct("<" + _pack_format(_abi.KdaTablesArgs))
@@ -252,7 +250,7 @@ def step_tables(*, stream=None, **kwargs) -> None:
     blocks the step asked for; more than `free_blocks` holds means that some
     requests got null blocks."""
     _launch(_abi.load().kda_step_tables, tables_args(**kwargs),
-            _tensors(kwargs), stream)
+            kwargs, stream)
 
 
 _SAMPLE_PACK = struct.Struct("<" + _pack_format(_abi.KdaSampleArgs))
@@ -317,5 +315,4 @@ def sample(*, stream=None, **kwargs) -> None:
     count, as `CommitContext.plan` and `commit_step` take it, and the token
     that follows the accepted ones.  `workspace` is scratch memory of
     `sample_workspace_size` bytes."""
-    _launch(_abi.load().kda_sample, sample_args(**kwargs), _tensors(kwargs),
-            stream)
+    _launch(_abi.load().kda_sample, sample_args(**kwargs), kwargs, stream)
