@@ -86,6 +86,20 @@ def test_step_tables_match_oracle(ci):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("free", [None, 1500])
+@pytest.mark.parametrize("B", [255, 256, 257, 511, 2047, 2048, 2049, 4097])
+def test_batches_around_the_tiles(B, free):
+    """Batches at the borders of the request kernel's variants and tiles,
+    with many new blocks a request, some requests without any."""
+    kw, host = make(B=B, rows=B + 3, width=7, block=5, qmax=33, seed=B,
+                    free=free)
+    ref = oracle.step_tables(**host)
+    kda.step_tables(**kw)
+    torch.cuda.synchronize()
+    check(kw, ref)
+
+
+@pytest.mark.gpu
 def test_empty_batch():
     kw, host = make(1, 2, 2, 4, 3, cap=6)
     for n in ("query_lens", "request_indices", "state_indices",
