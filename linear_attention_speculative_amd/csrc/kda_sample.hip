@@ -9,22 +9,24 @@
 // independent of the order in which lanes add; the weights come from fp64
 // arithmetic, which a token at the border of two sums of 10^5 terms needs.
 //
-// A full sort is avoided; what needs every logit of a row is split over many
-// workgroups, what needs one order over the row is one workgroup's:
+// A full sort is avoided.  What reads the logits is split over many workgroups
+// (one alone gets some 40 GB/s of a row); what orders a row is one wave's or
+// one workgroup's:
 //
 //   kda_group_max_kernel reads the logits once (the floor: HBM) and leaves the
 //   maximum of every group of 512.
 //   kda_row_sums_kernel, only for rows that need it: with top-p alone the
-//   weights by bins of 1/32 octave of d, with top-k > groups counts by bins,
-//   without either the weights of each group.
-//   kda_sample_kernel, one workgroup a row, reads only what it still needs.
-//   Greedy rows read one group.  With top-k <= groups, the k-th largest group
-//   maximum bounds the k-th largest value from below: only groups at or above
-//   it are read again, and the few values there go to a list in LDS, which is
-//   sorted, cut and summed.  Larger k takes a histogram of counts first, whose
-//   bin at the border bounds the list.  Top-p alone lists only the bin that
-//   holds its border, and so finds the threshold pair however many logits are
-//   kept.  What no list holds (thousands of ties, or of top-k) is left to a
+//   weights by bins of 1/32 octave of d, with more for top-k than groups that
+//   hold any logit counts by bins, without either the weights of each group.
+//   kda_plan_kernel, one wave a row, decides which logits matter.  Greedy rows
+//   end here.  With top-k <= groups, the k-th largest group maximum bounds the
+//   k-th largest value from below; with larger k the bin at the border of the
+//   counts does.  Top-p alone needs only the bin that holds its border, and so
+//   finds the threshold pair however many logits are kept.
+//   kda_gather_kernel lists those logits, reading again only groups whose
+//   maximum reaches the bound.
+//   kda_list_kernel, one workgroup a row, sorts the list, cuts it and takes the
+//   token.  What no list holds (thousands of ties, or of top-k) it leaves to a
 //   radix search of any size.
 //   kda_kept_sums_kernel and kda_pick_kernel, only for rows that kept more
 //   than a list: the kept weights of each group, and the token from them.
@@ -35,11 +37,9 @@ namespace {
 
 constexpr int kGroup = 512;          // logits of a group
 constexpr int kMaxGroups = 2048;     // V up to 2^20
-constexpr int kMaxThreads = 256;     // group maximum kernel
-constexpr int kPerWg = 4 * 4;        // its groups per workgroup
-constexpr int kRowThreads = 512;     // row kernel: two rows a CU, whose waits
-                                     // overlap (1024 window rows: 76 us against 98
-                                     // with 1024 threads; one row alone 43, 35)
+constexpr int kMaxThreads = 256;     // split kernels
+constexpr int kPerWg = 4 * 4;        // groups per workgroup of the split kernels
+constexpr int kRowThreads = 512;     // list and pick kernels
 constexpr int kWaves = kRowThreads / 64;
 constexpr int kList = 4096;          // entries of the sorted list
 constexpr int kBins = 2048;
@@ -50,17 +50,11 @@ constexpr int kPer1k = 1024 / kRowThreads;
 static_assert(kBins == kMaxGroups && kPer1k >= 1, "sizes");
 constexpr int kSteps = 256;          // of an octave, in the table of weights
 
-__device__ __forceinline__ float logit(const SampleParams& p, const char* row,
-                                       int i, bool bf16) {
-  return bf16 ? bf16_to_f32(reinterpret_cast<const uint16_t*>(row)[i])
-              : reinterpret_cast<const float*>(row)[i];
-}
-
 // The request of row m, or -1 for a row outside every request.
 __device__ __forceinline__ int request_of_row(const SampleParams& p, int m,
                                               int lane) {
   if (p.qsl == nullptr) return m < p.B ? m : -1;
-  if (p.B == 0) return -1;
+  if (p.B == 0 || m < p.qsl[0] || m >= p.qsl[p.B]) return -1;
   int lo = 0, n = p.B;
   while (n > 1) {      // last b with qsl[b] <= m, 64 candidates at a time
     const int step = (n + 63) / 64;
@@ -170,10 +164,9 @@ __device__ __forceinline__ uint32_t least_key(uint32_t top, Test test) {
 
 struct RowSmem {
   union {
-    struct {
-      uint64_t key[kList];      // ordered(x) << 32 | ~index
-      uint64_t w[kList];
-    } list;
+    // ordered(x) << 32 | ~index.  A sort of at most half of them uses the
+    // upper half as its second buffer, which then holds their weights.
+    uint64_t key[kList];
     uint32_t count[kBins];
     uint64_t mass[kBins];
     uint64_t group[kMaxGroups];
@@ -181,7 +174,6 @@ struct RowSmem {
   float gmax[kMaxGroups];
   double table[kSteps];         // 2^(-j/256)
   uint64_t red[kWaves];
-  uint32_t n;
   int found, pick;
   uint64_t before, value;
 };
@@ -191,14 +183,18 @@ __device__ __forceinline__ void fill_table(double* table) {
     table[i] = exp2(double(i) * (-1.0 / kSteps));
 }
 
+__device__ __forceinline__ double uniform_double(double v) {
+  return __hiloint2double(uniform(__double2hiint(v)),
+                          uniform(__double2loint(v)));
+}
+
 // Weight of a logit as an integer, from its distance to the maximum in steps
-// of 1/256 octave: a table for the whole step, a cubic for the rest (2^-38 of
-// the weight), the octave by the exponent field, and an addition whose last
-// binary place is 1 to round.
+// of 1/256 octave: a table for the nearest whole step, a cubic for the rest
+// (2^-42 of the weight), the octave by the exponent field, and an addition
+// whose last binary place is 1 to round.
 struct Weights {
   const double* table;
-  double c, most, d_min_p;      // steps per unit; clamps; steps that min-p allows
-  float m;
+  double m, c, most, d_min_p;   // steps per unit; clamp; steps that min-p allows
   int s;                        // binary places
   __device__ __forceinline__ void init(const double* tab, float top, float T,
                                        float min_p, int places) {
@@ -206,19 +202,32 @@ struct Weights {
     m = top;
     s = places;
     c = kSteps * 1.4426950408889634074 / double(T);
+    if (top == __builtin_inff()) {      // itself: 0 steps; all others: `most`
+      m = 0x1p128;
+      c = 0x1p900;
+    }
     most = double((places + 2) * kSteps);           // weighs 2^-2 places: 0
     d_min_p = min_p > 0.0f ? -kSteps * log2(double(fminf(min_p, 1.0f)))
                            : __builtin_inf();
+    // one value for all lanes: in scalar registers
+    m = uniform_double(m);
+    c = uniform_double(c);
+    most = uniform_double(most);
+    d_min_p = uniform_double(d_min_p);
   }
-  // Steps below the maximum (0 for a maximum of +inf itself; `most` for -inf
-  // and whatever the weights cannot tell from 0).
+  // Steps below the maximum (`most` for -inf and whatever the weights cannot
+  // tell from 0).
   __device__ __forceinline__ double steps(float x) const {
-    const double d = fmin((double(m) - double(x)) * c, most);
-    return x == m ? 0.0 : d;
+    return fmax(fmin((m - double(x)) * c, most), 0.0);
+  }
+  // the nearest whole step
+  __device__ __forceinline__ int nearest(double d) const {
+    return __double2loint(d + 0x1.8p52);
   }
   __device__ __forceinline__ uint64_t whole(double d) const {
-    const int e = int(d);
-    const double f = d - double(e);
+    const double r = d + 0x1.8p52;
+    const int e = __double2loint(r);
+    const double f = d - (r - 0x1.8p52);
     constexpr double l = -0.6931471805599453094 / kSteps;
     double q = fma(f, l * l * l / 6.0, l * l / 2.0);
     q = fma(f, q, l);
@@ -237,7 +246,7 @@ struct Weights {
   }
   // 1/32 octave bins
   __device__ __forceinline__ int bin(double d) const {
-    return min(int(d) >> 3, kBins - 1);
+    return min(nearest(d) >> 3, kBins - 1);
   }
 };
 
@@ -259,42 +268,75 @@ struct Params {
   }
 };
 
-// Workspace of a row: maxima of its groups, sums (bins or groups), and what
-// the row kernel leaves to the last two.
+// What is left to do for a row, and what the kernels tell each other.
+enum Mode : int32_t {
+  kDecided,      // nothing
+  kGather,       // list the keys first <= key < last, then take it from there
+  kSearch,       // too many for a list
+  kKept,         // sum the weights that the threshold pair keeps, then pick
+  kSummed        // pick; the sums are there
+};
+struct Plan {
+  Mode mode;
+  float top;                 // the row's maximum
+  uint32_t min_key;          // least key that min-p allows
+  uint32_t first, last;
+  uint32_t n;                // keys found; kList at most are in the list
+  uint64_t mass, before;     // top-p alone: weights of all, and above `last`
+  uint32_t key;              // threshold pair
+  int32_t index;
+};
+
+// Workspace of a row: maxima of its groups, sums (bins or groups), the list,
+// and its plan.
 struct Work {
   float* gmax;
   uint64_t* sums;         // [kBins]: bins, or weights of groups
-  int32_t* key;           // threshold pair; index -1: the token is decided
-  int32_t* index;
+  uint64_t* list;         // [kList]: ordered(x) << 32 | ~index
+  Plan* plan;
   __device__ __host__ static int64_t maxima(int64_t M, int64_t G) {
     return (M * G * 4 + 255) / 256 * 256;
   }
   __device__ __host__ static int64_t bytes(int64_t M, int64_t G) {
-    return maxima(M, G) + M * kBins * 8 + (M * 8 + 255) / 256 * 256;
+    return maxima(M, G) + M * int64_t(kBins + kList) * 8 +
+           (M * int64_t(sizeof(Plan)) + 255) / 256 * 256;
   }
   __device__ __forceinline__ Work(const SampleParams& p, int m, int G) {
-    char* sum = p.work + maxima(p.M, G);
+    char* at = p.work + maxima(p.M, G);
     gmax = reinterpret_cast<float*>(p.work) + int64_t(m) * G;
-    sums = reinterpret_cast<uint64_t*>(sum) + int64_t(m) * kBins;
-    key = reinterpret_cast<int32_t*>(sum + int64_t(p.M) * kBins * 8) + 2 * m;
-    index = key + 1;
+    sums = reinterpret_cast<uint64_t*>(at) + int64_t(m) * kBins;
+    at += int64_t(p.M) * kBins * 8;
+    list = reinterpret_cast<uint64_t*>(at) + int64_t(m) * kList;
+    at += int64_t(p.M) * kList * 8;
+    plan = reinterpret_cast<Plan*>(at) + m;
+  }
+};
+
+// The groups of a row that a workgroup of the split kernels takes.
+struct Part {
+  int m, first, end;
+  __device__ __forceinline__ Part(int G, int per_row, int per_wg = kPerWg) {
+    m = blockIdx.x / per_row;
+    first = (blockIdx.x - m * per_row) * per_wg;
+    end = min(first + per_wg, G);
   }
 };
 
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads)
     kda_group_max_kernel(SampleParams p, int G, int per_row) {
-  const int m = blockIdx.x / per_row, part = blockIdx.x - m * per_row;
+  const Part part(G, per_row);
+  const int m = part.m;
   if (p.qsl && (m < p.qsl[0] || m >= p.qsl[p.B])) return;
   const char* row = static_cast<const char*>(p.logits) +
                     m * p.s_row * (BF16 ? 2 : 4);
   const Work out(p, m, G);
   // the row's bins, cleared for the next kernel
-  for (int i = part * kMaxThreads + threadIdx.x; i < kBins;
-       i += per_row * kMaxThreads)
+  for (int i = (blockIdx.x - m * per_row) * kMaxThreads + threadIdx.x;
+       i < kBins; i += per_row * kMaxThreads)
     out.sums[i] = 0;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int g0 = part * kPerWg + wave * (kPerWg / 4);
+  const int g0 = part.first + wave * (kPerWg / 4);
   Group<BF16, VEC> v[kPerWg / 4];
 #pragma unroll
   for (int i = 0; i < kPerWg / 4; ++i) v[i].load(row, min(g0 + i, G - 1), p.V);
@@ -304,18 +346,52 @@ __global__ void __launch_bounds__(kMaxThreads)
 #pragma unroll
     for (int e = 1; e < 8; ++e) t = fmaxf(t, v[i].x[e]);
     t = wave_max(t);
-    if (lane == 0 && g0 + i < G) out.gmax[g0 + i] = t;
+    if (lane == 0 && g0 + i < part.end) out.gmax[g0 + i] = t;
   }
 }
 
-// Threshold pair: a logit is kept if it is larger than `key`, or equal and at
-// an index of at most `index`.
+// f(x) for the logits of a wave's group that keep(x, index) takes.  The lanes
+// first gather them in `buf` (512 floats of the wave's own): with few kept,
+// one dense pass in place of eight sparse ones through f's fp64 arithmetic.
+template <bool BF16, bool VEC, class Keep, class F>
+__device__ __forceinline__ void each_kept(const Group<BF16, VEC>& v,
+                                          float* buf, Keep keep, F f) {
+  const int lane = threadIdx.x & 63;
+  uint64_t in[8];
+  int n = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    in[e] = __ballot(keep(v.x[e], v.index(e)));
+    n += __popcll(in[e]);
+  }
+  if (n > kGroup / 4 * 3) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (keep(v.x[e], v.index(e))) f(v.x[e]);
+    return;
+  }
+  uint32_t at = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t mine = __builtin_amdgcn_mbcnt_hi(
+        uint32_t(in[e] >> 32),
+        __builtin_amdgcn_mbcnt_lo(uint32_t(in[e]), at));
+    if (keep(v.x[e], v.index(e))) buf[mine] = v.x[e];
+    at += __popcll(in[e]);
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+  for (int i = lane; i < n; i += 64) f(buf[i]);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+}
+
+// Threshold pair: a logit is kept if it is larger than `key`'s value, or equal
+// and at an index of at most `index`.
 struct Threshold {
   uint32_t key;
   int index;
   __device__ __forceinline__ bool keeps(float x, int i) const {
-    const uint32_t k = ordered(x);
-    return k > key || (k == key && i <= index);
+    const float at = unordered(key);
+    return x > at || (x == at && i <= index);
   }
 };
 
@@ -334,29 +410,42 @@ struct Row {
         if (v.x[e] > -__builtin_inff()) f(v.x[e], v.index(e));
     });
   }
-  // f(group), a group to a wave, the loads of kAhead groups at once.
+  // f(group), a group to a wave.
   template <class Use, class F>
   __device__ __forceinline__ void each_group(Use use, F f) const {
-    constexpr int kAhead = VEC ? 4 : 2;
-    int g = uniform(threadIdx.x >> 6);
-#pragma unroll 1
-    while (true) {
-      int id[kAhead], n = 0;
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) {
-        while (g < G && !use(g)) g += kWaves;
-        id[j] = g;
-        n += g < G;
-        g += kWaves;
-      }
-      if (n == 0) return;
-      Group<BF16, VEC> v[kAhead];
-#pragma unroll
-      for (int j = 0; j < kAhead; ++j) v[j].load(at, min(id[j], G - 1), V);
+    each_batch(use, [&](const Group<BF16, VEC>(&v)[kAhead], int n) {
 #pragma unroll
       for (int j = 0; j < kAhead; ++j) {
         if (j >= n) break;
         f(v[j]);
+      }
+    });
+  }
+  // f(groups, count): the loads of up to kAhead groups at once.
+  static constexpr int kAhead = 2;
+  template <class Use, class F>
+  __device__ __forceinline__ void each_batch(Use use, F f) const {
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+#pragma unroll 1
+    for (int base = wave; base < G; base += 64 * kWaves) {
+      const int mine = base + lane * kWaves;
+      uint64_t left = __ballot(mine < G && use(min(mine, G - 1)));
+#pragma unroll 1
+      while (left) {
+        int id[kAhead], n = 0;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          id[j] = j > 0 ? id[j - 1] : 0;
+          if (left) {
+            id[j] = base + (__ffsll((unsigned long long)left) - 1) * kWaves;
+            left &= left - 1;
+            ++n;
+          }
+        }
+        Group<BF16, VEC> v[kAhead];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) v[j].load(at, id[j], V);
+        f(v, n);
       }
     }
   }
@@ -368,15 +457,56 @@ __device__ __forceinline__ uint64_t wave_sum64(uint64_t v) {
   return v;
 }
 
-// Inclusive prefix sum over the workgroup, and the total.
-__device__ __forceinline__ uint64_t row_scan(uint64_t v, uint64_t* red,
-                                             uint64_t* total) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+// Inclusive prefix sum over a wave.
+__device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
+  const int lane = threadIdx.x & 63;
 #pragma unroll
   for (int s = 1; s < 64; s <<= 1) {
     const uint64_t o = __shfl_up((unsigned long long)v, s);
     if (lane >= s) v += o;
   }
+  return v;
+}
+
+// First bin of a row's kBins whose inclusive prefix sum reaches goal(total),
+// or -1, by one wave: the 32 bins of a lane, then those of the lane found.
+struct BinFound {
+  int at;
+  uint64_t before, value, total;
+};
+template <class Goal>
+__device__ __forceinline__ BinFound find_bin(const uint64_t* bins, Goal goal) {
+  constexpr int kOwn = kBins / 64;
+  const int lane = threadIdx.x & 63;
+  uint64_t own = 0;
+#pragma unroll
+  for (int j = 0; j < kOwn / 2; ++j) {
+    const ulonglong2 v =
+        reinterpret_cast<const ulonglong2*>(bins)[lane * (kOwn / 2) + j];
+    own += v.x + v.y;
+  }
+  BinFound f{-1, 0, 0, 0};
+  const uint64_t upto = wave_scan(own);
+  f.total = __shfl((unsigned long long)upto, 63);
+  const uint64_t target = goal(f.total);
+  const uint64_t in = __ballot(upto >= target);
+  if (in == 0) return f;
+  const int l = __ffsll((unsigned long long)in) - 1;
+  const uint64_t base = __shfl((unsigned long long)(upto - own), l);
+  const uint64_t v = lane < kOwn ? bins[l * kOwn + lane] : 0;
+  const uint64_t u = base + wave_scan(v);
+  const int i = __ffsll((unsigned long long)__ballot(u >= target)) - 1;
+  f.at = l * kOwn + i;
+  f.before = __shfl((unsigned long long)(u - v), i);
+  f.value = __shfl((unsigned long long)v, i);
+  return f;
+}
+
+// Inclusive prefix sum over the workgroup, and the total.
+__device__ __forceinline__ uint64_t row_scan(uint64_t v, uint64_t* red,
+                                             uint64_t* total) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  v = wave_scan(v);
   __syncthreads();
   if (lane == 63) red[w] = v;
   __syncthreads();
@@ -390,17 +520,17 @@ __device__ __forceinline__ uint64_t row_scan(uint64_t v, uint64_t* red,
   return base + v;
 }
 
-// First index i of a[0 .. n) (n <= kPer * kRowThreads) whose inclusive prefix
+// First index i of a(0 .. n - 1) (n <= kPer * kRowThreads) whose inclusive prefix
 // sum reaches goal(total of a); sm.found = i (or -1), sm.before = the sum
-// before it, sm.value = a[i].  Returns the total.
-template <int kPer, class T, class Goal>
-__device__ __forceinline__ uint64_t find_prefix(RowSmem& sm, const T* a, int n,
+// before it, sm.value = a(i).  Returns the total.
+template <int kPer, class A, class Goal>
+__device__ __forceinline__ uint64_t find_prefix(RowSmem& sm, A a, int n,
                                                 Goal goal) {
   uint64_t v[kPer], own = 0;
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int i = threadIdx.x * kPer + j;
-    v[j] = i < n ? uint64_t(a[i]) : 0;
+    v[j] = i < n ? uint64_t(a(i)) : 0;
     own += v[j];
   }
   __syncthreads();                    // the last result has been read
@@ -469,7 +599,7 @@ __device__ __forceinline__ void lane_step(uint64_t (&v)[P], int k) {
 // Sort of `size` keys (a power of two, at most P * kRowThreads), falling: key
 // r * kRowThreads + tid in register r of a thread.  Pairs inside a wave are
 // exchanged between lanes, pairs of registers in place, the others through two
-// buffers in turn, at one barrier each.
+// buffers in turn, at one barrier each, or through a alone (b = a) at two.
 template <int P>
 __device__ __forceinline__ void sort_keys(uint64_t* a, uint64_t* b, int size) {
   const int tid = threadIdx.x;
@@ -505,6 +635,7 @@ __device__ __forceinline__ void sort_keys(uint64_t* a, uint64_t* b, int size) {
         const int i = r * kRowThreads + tid;
         v[r] = keep_of(v[r], buf[i ^ j], i, k, j);
       }
+      if (a == b) __syncthreads();
       buf = buf == a ? b : a;
     }
     lane_step<32>(v, k);
@@ -520,23 +651,22 @@ __device__ __forceinline__ void sort_keys(uint64_t* a, uint64_t* b, int size) {
   __syncthreads();
 }
 
-// Sort of the list's first n keys, falling; zeros follow them.  The weights'
-// place is the second buffer.
+// Sort of the list's first n keys, falling; zeros follow them.
 __device__ __forceinline__ void sort_list(RowSmem& sm, int n) {
   int size = 2;
   while (size < n) size <<= 1;
-  for (int i = n + threadIdx.x; i < size; i += kRowThreads)
-    sm.list.key[i] = 0;
+  for (int i = n + threadIdx.x; i < size; i += kRowThreads) sm.key[i] = 0;
   __syncthreads();
+  uint64_t* const upper = sm.key + kList / 2;
   if (size <= kRowThreads)
-    sort_keys<1>(sm.list.key, sm.list.w, size);
+    sort_keys<1>(sm.key, upper, size);
   else if (size <= 2 * kRowThreads)
-    sort_keys<2>(sm.list.key, sm.list.w, size);
+    sort_keys<2>(sm.key, upper, size);
   else if (size <= 4 * kRowThreads)
-    sort_keys<4>(sm.list.key, sm.list.w, size);
+    sort_keys<4>(sm.key, upper, size);
   else
-    sort_keys<8>(sm.list.key, sm.list.w, size);
-  static_assert(kList <= 8 * kRowThreads, "sort");
+    sort_keys<8>(sm.key, sm.key, size);
+  static_assert(kList == 8 * kRowThreads, "sort");
 }
 
 // Target of a share of a whole: the least integer >= share * mass, at least 1
@@ -551,15 +681,6 @@ __device__ __forceinline__ uint64_t share_of(double share, uint64_t mass) {
 template <bool VEC>
 __device__ __forceinline__ void group_prefix(const uint64_t (&v)[8],
                                              uint64_t (&pre)[8]) {
-  const int lane = threadIdx.x & 63;
-  const auto scan = [&](uint64_t x) {
-#pragma unroll
-    for (int s = 1; s < 64; s <<= 1) {
-      const uint64_t o = __shfl_up((unsigned long long)x, s);
-      if (lane >= s) x += o;
-    }
-    return x;
-  };
   if constexpr (VEC) {            // a lane's elements are neighbours
     uint64_t own = 0;
 #pragma unroll
@@ -567,14 +688,14 @@ __device__ __forceinline__ void group_prefix(const uint64_t (&v)[8],
       pre[e] = own;
       own += v[e];
     }
-    const uint64_t base = scan(own) - own;
+    const uint64_t base = wave_scan(own) - own;
 #pragma unroll
     for (int e = 0; e < 8; ++e) pre[e] += base;
   } else {                        // neighbours are in neighbouring lanes
     uint64_t base = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint64_t upto = scan(v[e]);
+      const uint64_t upto = wave_scan(v[e]);
       pre[e] = base + upto - v[e];
       base += __shfl((unsigned long long)upto, 63);
     }
@@ -614,7 +735,7 @@ __device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
                   (unsigned long long)what(x));
     });
     __syncthreads();
-    find_prefix<kPer2k>(sm, sm.mass, bins,
+    find_prefix<kPer2k>(sm, [&](int i) { return sm.mass[i]; }, bins,
                    [&](uint64_t) { return target - before; });
     before += sm.before;
     prefix |= uint32_t(bins - 1 - max(sm.found, 0)) << shift;
@@ -632,7 +753,7 @@ __device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
       atomicAdd((unsigned long long*)&sm.group[i / kGroup], 1ull);
   });
   __syncthreads();
-  find_prefix<kPer2k>(sm, sm.group, row.G, [&](uint64_t) { return rank; });
+  find_prefix<kPer2k>(sm, [&](int i) { return sm.group[i]; }, row.G, [&](uint64_t) { return rank; });
   const int g = sm.found;
   const uint64_t seen = sm.before;
   if (threadIdx.x == 0) sm.pick = row.V - 1;
@@ -662,19 +783,67 @@ __device__ __forceinline__ float row_max(const float* gmax, int G) {
   return wave_max(top);
 }
 
-// Bins of m - x for counts, with the lowest maximum among the groups that
-// hold a key of at least min_key at three quarters; kBins for whatever lies
-// behind the last bin (or cannot be told, below a maximum of +inf).
+// Groups whose maximum has a key of at least `least`.
+__device__ __forceinline__ int live_groups(const float* gmax, int G,
+                                           uint32_t least) {
+  const int lane = threadIdx.x & 63;
+  int n = 0;
+  for (int g = lane; g - lane < G; g += 64)
+    n += __popcll(__ballot(g < G && ordered(gmax[min(g, G - 1)]) >= least));
+  return n;
+}
+
+// Key of the k-th largest group maximum (k <= G), bit by bit, by every wave
+// for itself.
+__device__ __forceinline__ uint32_t kth_key(const float* gmax, int G, int k) {
+  constexpr int kRegs = kMaxGroups / 64, kStep = 4;
+  const int lane = threadIdx.x & 63;
+  uint32_t key[kRegs];
+#pragma unroll
+  for (int r = 0; r < kRegs; r += kStep) {
+    if (r * 64 >= G) break;
+#pragma unroll
+    for (int i = r; i < r + kStep; ++i) {
+      const int g = i * 64 + lane;
+      key[i] = g < G ? ordered(gmax[min(g, G - 1)]) : 0;
+    }
+  }
+  uint32_t at = 0;       // the largest key that k maxima reach, two bits a step
+#pragma unroll 1
+  for (int bit = 30; bit >= 0; bit -= 2) {
+    int n[3] = {0, 0, 0};
+#pragma unroll
+    for (int r = 0; r < kRegs; r += kStep) {
+      if (r * 64 >= G) break;
+#pragma unroll
+      for (int i = r; i < r + kStep; ++i)
+#pragma unroll
+        for (int d = 0; d < 3; ++d)
+          n[d] += __popcll(__ballot(key[i] >= (at | uint32_t(d + 1) << bit)));
+    }
+    at |= uint32_t((n[0] >= k) + (n[1] >= k) + (n[2] >= k)) << bit;
+  }
+  return at;
+}
+
+// Bins of m - x for counts; kBins for whatever lies behind the last one (or
+// cannot be told, below a maximum of +inf).  Those down to `low`, the least
+// maximum among the groups that hold a key of at least min_key, take 7/8 of
+// them for few and 3/8 for many: of G groups of any 512 independent values
+// some G ln G lie at or above it.  Fewer logits to count, and finer bins.
 struct CountBins {
   float top, scale;
+  static __device__ __forceinline__ bool few(int k, int G) {
+    return 2.0f * float(k) <= float(G) * __log2f(float(G));
+  }
   __device__ __forceinline__ CountBins(const float* gmax, int G, float top_,
-                                       uint32_t min_key)
+                                       uint32_t min_key, bool few)
       : top(top_) {
     float low = top;
     for (int g = threadIdx.x & 63; g < G; g += 64)
       if (ordered(gmax[g]) >= min_key) low = fminf(low, gmax[g]);
     low = -wave_max(-low);
-    scale = float(kBins / 4 * 3) / fmaxf(top - low, 1e-3f);
+    scale = float(kBins / 8) * (few ? 7.0f : 3.0f) / fmaxf(top - low, 1e-3f);
   }
   // never falls as x falls
   __device__ __forceinline__ int operator()(float x) const {
@@ -698,36 +867,43 @@ __device__ __forceinline__ uint32_t least_allowed(const Params& q,
 // group.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads)
-    kda_row_sums_kernel(SampleParams p, int G, int per_row, int places) {
+    kda_row_sums_kernel(SampleParams p, int G, int per_row, int per_wg,
+                        int places) {
   __shared__ double table[kSteps];
   __shared__ unsigned long long mass[kBins];
-  const int m = blockIdx.x / per_row, part = blockIdx.x - m * per_row;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float kept[kMaxThreads / 64][kGroup];
+  const Part part(G, per_row, per_wg);
+  const int m = part.m;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int b = request_of_row(p, m, lane);
   if (b < 0) return;
   const Params q(p, b, m);
+  if (q.greedy) return;
   const bool counts = q.need_k;
-  if (q.greedy || (counts && q.k <= G)) return;
   const Work work(p, m, G);
+  const int live = counts ? live_groups(work.gmax, G, kLowestKey) : G;
+  if (counts && q.k <= live) return;
   const float top = row_max(work.gmax, G);
   if (top == -__builtin_inff()) return;
-  fill_table(table);
+  if (!counts) fill_table(table);
   const bool binned = counts || q.need_p;
+  uint32_t* count = reinterpret_cast<uint32_t*>(mass);
   if (binned)
-    for (int i = threadIdx.x; i < kBins; i += kMaxThreads) mass[i] = 0;
+    for (int i = threadIdx.x; i < (counts ? kBins / 2 : kBins);
+         i += kMaxThreads)
+      mass[i] = 0;
   __syncthreads();
   Weights wt;
   wt.init(table, top, q.T, q.min_p, places);
   const uint32_t min_key = least_allowed(q, wt, top);
-  const CountBins bins(work.gmax, G, top, min_key);
+  const float least = unordered(min_key);
+  const CountBins bins(work.gmax, G, top, min_key, CountBins::few(q.k, live));
   const char* row = static_cast<const char*>(p.logits) +
                     m * p.s_row * (BF16 ? 2 : 4);
 #pragma unroll 1
-  for (int i = 0; i < kPerWg / 4; ++i) {
-    const int g = part * kPerWg + wave * (kPerWg / 4) + i;
-    if (g >= G) break;
+  for (int g = part.first + wave; g < part.end; g += kMaxThreads / 64) {
     // a group whose largest logit min-p drops has nothing to add
-    if (ordered(work.gmax[g]) < min_key) {
+    if (work.gmax[g] < least) {
       if (!binned && lane == 0) work.sums[g] = 0;
       continue;
     }
@@ -737,30 +913,32 @@ __global__ void __launch_bounds__(kMaxThreads)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int bin = bins(v.x[e]);
-        if (bin < kBins) atomicAdd(&mass[bin], 1ull);
+        if (bin < kBins) atomicAdd(&count[bin], 1u);
       }
       continue;
     }
     uint64_t sum = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const double d = wt.steps(v.x[e]);
-      const uint64_t w = ordered(v.x[e]) >= min_key ? wt.whole(d) : 0;
-      if (!binned)
-        sum += w;
-      else if (w > 0)
-        atomicAdd(&mass[wt.bin(d)], (unsigned long long)w);
-    }
-    if (!binned) {
+    const auto in = [&](float x, int) { return x >= least; };
+    if (binned) {
+      each_kept<BF16, VEC>(v, kept[wave], in, [&](float x) {
+        const double d = wt.steps(x);
+        const uint64_t w = wt.whole(d);
+        if (w > 0) atomicAdd(&mass[wt.bin(d)], (unsigned long long)w);
+      });
+    } else {
+      each_kept<BF16, VEC>(v, kept[wave], in,
+                           [&](float x) { sum += wt.of(x); });
       sum = wave_sum64(sum);
       if (lane == 0) work.sums[g] = sum;
     }
   }
   if (!binned) return;
   __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += kMaxThreads)
-    if (mass[i] > 0)
-      atomicAdd((unsigned long long*)&work.sums[i], mass[i]);
+  for (int i = threadIdx.x; i < kBins; i += kMaxThreads) {
+    const uint64_t add = counts ? count[i] : mass[i];
+    if (add > 0)
+      atomicAdd((unsigned long long*)&work.sums[i], (unsigned long long)add);
+  }
 }
 
 // The token whose running weight passes u: from the weights of the groups
@@ -772,7 +950,7 @@ __device__ __forceinline__ void pick_token(const SampleParams& p,
                                            float u, int m) {
   RowSmem& sm = row.sm;
   const uint64_t mass = find_prefix<kPer2k>(
-      sm, sm.group, row.G, [&](uint64_t w) { return past_share(u, w); });
+      sm, [&](int i) { return sm.group[i]; }, row.G, [&](uint64_t w) { return past_share(u, w); });
   const uint64_t target = past_share(u, mass);
   const uint64_t before = sm.before;
   if (threadIdx.x < 64) {
@@ -793,192 +971,212 @@ __device__ __forceinline__ void pick_token(const SampleParams& p,
   }
 }
 
+// What a row needs, by one wave; greedy rows get their token.
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(64)
+    kda_plan_kernel(SampleParams p, int G, int places) {
+  const int m = blockIdx.x, lane = threadIdx.x;
+  const Work work(p, m, G);
+  const int b = request_of_row(p, m, lane);
+  if (b < 0) {
+    if (lane == 0) work.plan->mode = kDecided;
+    return;
+  }
+  const Params q(p, b, m);
+  const int k = q.k;
+  const float* gmax = work.gmax;
+  const float top = row_max(gmax, G);
+  Plan plan{};
+  plan.top = top;
+  plan.last = 0xffffffffu;
+  plan.index = p.V;
+  if (top == -__builtin_inff() || q.greedy) {
+    int token = -1;
+    if (top > -__builtin_inff()) {
+      // the lowest index of the maximum
+      int g = lane;
+      while (!__any(g < G && gmax[min(g, G - 1)] == top) && g - lane < G)
+        g += 64;
+      const uint64_t in = __ballot(g < G && gmax[min(g, G - 1)] == top);
+      g = g - lane + __ffsll((unsigned long long)in) - 1;
+      Group<BF16, VEC> v;
+      v.load(static_cast<const char*>(p.logits) +
+                 m * p.s_row * (BF16 ? 2 : 4),
+             min(max(g, 0), G - 1), p.V);
+      int at = p.V - 1;
+#pragma unroll
+      for (int e = 7; e >= 0; --e)
+        if (v.x[e] == top) at = min(at, v.index(e));
+#pragma unroll
+      for (int s = 1; s < 64; s <<= 1) at = min(at, __shfl_xor(at, s));
+      token = at;
+    }
+    if (lane == 0) {
+      p.tokens[m] = token;
+      work.plan->mode = kDecided;
+    }
+    return;
+  }
+  // Every condition on a logit's weight is one on its key.
+  Weights wt;
+  wt.init(nullptr, top, q.T, q.min_p, places);
+  const uint32_t min_key = least_allowed(q, wt, top);
+  const uint32_t top_key = ordered(top);
+  plan.min_key = plan.first = plan.key = min_key;
+  plan.mode = kGather;
+  if (!q.need_k && !q.need_p) {
+    plan.mode = kSummed;
+  } else if (!q.need_k) {
+    const BinFound f = find_bin(
+        work.sums, [&](uint64_t w) { return share_of(q.top_p, w); });
+    plan.mass = f.total;
+    plan.before = f.before;
+    plan.first = max(min_key, least_key(top_key, [&](float x) {
+                       return wt.bin(wt.steps(x)) <= f.at;
+                     }));
+    if (f.at > 0)
+      plan.last = least_key(top_key, [&](float x) {
+        return wt.bin(wt.steps(x)) < f.at;
+      });
+  } else {
+    // groups that hold any logit, and one that min-p allows
+    const int live = live_groups(gmax, G, kLowestKey);
+    const int allowed = live_groups(gmax, G, min_key);
+    if (k <= allowed) {
+      // at least k logits lie at or above the k-th largest group maximum
+      plan.first = kth_key(gmax, G, k);
+    } else if (k > live) {           // counted by the kernel before
+      const CountBins bins(gmax, G, top, min_key, CountBins::few(k, live));
+      const BinFound f =
+          find_bin(work.sums, [&](uint64_t) { return uint64_t(k); });
+      if (f.at >= 0)
+        plan.first = max(min_key, least_key(top_key, [&](float x) {
+                           return bins(x) <= f.at;
+                         }));
+      // (below the last bin may lie any number; min-p may leave few of it)
+      const bool many = f.at >= 0 ? f.before + f.value > kList
+                                  : allowed * kGroup > kList;
+      if (many && !(q.min_p > 0.0f)) plan.mode = kSearch;
+    }
+    // between the two, min-p likely leaves few: all it allows
+  }
+  if (lane == 0) *work.plan = plan;
+}
+
+// The keys first <= key < last of the rows that list them, in any order.
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads)
+    kda_gather_kernel(SampleParams p, int G, int per_row) {
+  const Part part(G, per_row);
+  const int m = part.m;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const Work work(p, m, G);
+  if (work.plan->mode != kGather) return;
+  // as floats; without a last key, one that nothing compares with
+  const uint32_t last = work.plan->last;
+  const float x_first = unordered(work.plan->first);
+  const float x_last = last == 0xffffffffu ? __builtin_nanf("")
+                                           : unordered(last);
+  const auto in = [&](float x) { return x >= x_first && !(x >= x_last); };
+  constexpr int kOwn = kPerWg / 4;           // groups of a wave
+  const int g0 = part.first + wave * kOwn;
+  int id[kOwn], groups = 0;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    id[i] = 0;
+    const bool use = g0 + i < G && work.gmax[min(g0 + i, G - 1)] >= x_first;
+#pragma unroll
+    for (int j = 0; j < kOwn; ++j)
+      if (use && j == groups) id[j] = g0 + i;
+    groups += use;
+  }
+  if (groups == 0) return;
+  const char* row = static_cast<const char*>(p.logits) +
+                    m * p.s_row * (BF16 ? 2 : 4);
+  Group<BF16, VEC> v[kOwn];
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j)
+    if (j < groups) v[j].load(row, id[j], p.V);
+  int own = 0;
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j) {
+    if (j >= groups) break;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) own += in(v[j].x[e]);
+  }
+  // places: one addition for the wave, and the lanes' own by the binary
+  // digits of their numbers
+  static_assert(8 * kOwn < 64, "digits");
+  uint32_t all = 0, at = 0;
+#pragma unroll
+  for (int i = 0; i < 6; ++i) {
+    const uint64_t has = __ballot(own >> i & 1);
+    all += uint32_t(__popcll(has)) << i;
+    at += __builtin_amdgcn_mbcnt_hi(
+              uint32_t(has >> 32),
+              __builtin_amdgcn_mbcnt_lo(uint32_t(has), 0))
+          << i;
+  }
+  if (all == 0) return;
+  uint32_t base = 0;
+  if (lane == 0) base = atomicAdd(&work.plan->n, all);
+  at += uint32_t(uniform(int(base)));
+#pragma unroll
+  for (int j = 0; j < kOwn; ++j) {
+    if (j >= groups) break;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (in(v[j].x[e])) {
+        if (at < kList)
+          work.list[at] = uint64_t(ordered(v[j].x[e])) << 32 |
+                          (0xffffffffu - uint32_t(v[j].index(e)));
+        ++at;
+      }
+  }
+}
+
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kRowThreads)
-    kda_sample_kernel(SampleParams p, int G, int places) {
+    __attribute__((amdgpu_waves_per_eu(6)))
+    kda_list_kernel(SampleParams p, int G, int places) {
   extern __shared__ __align__(16) char smem[];
   RowSmem& sm = *reinterpret_cast<RowSmem*>(smem);
   const int m = blockIdx.x, tid = threadIdx.x;
   const Work work(p, m, G);
+  const Plan plan = *work.plan;
+  if (plan.mode != kGather && plan.mode != kSearch) return;
   const int b = request_of_row(p, m, tid & 63);
-  if (tid == 0) *work.index = -1;
   if (b < 0) return;
   const Params q(p, b, m);
   const int k = q.k;
-  const Row<BF16, VEC> row{static_cast<const char*>(p.logits) +
-                               m * p.s_row * (BF16 ? 2 : 4),
-                           p.V, G, sm};
-  for (int g = tid; g < G; g += kRowThreads) sm.gmax[g] = work.gmax[g];
   fill_table(sm.table);
-  if (tid == 0) {
-    sm.found = G;
-    sm.pick = p.V;
-  }
-  __syncthreads();
-  const float top = row_max(sm.gmax, G);
-  if (top == -__builtin_inff()) {
-    if (tid == 0) p.tokens[m] = -1;
-    return;
-  }
-
-  if (q.greedy) {
-    // the lowest index of the maximum
-    for (int g = tid; g < G; g += kRowThreads)
-      if (sm.gmax[g] == top) atomicMin(&sm.found, g);
-    __syncthreads();
-    if (tid < 64) {
-      Group<BF16, VEC> v;
-      v.load(row.at, min(sm.found, G - 1), p.V);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (v.x[e] == top) atomicMin(&sm.pick, v.index(e));
-    }
-    __syncthreads();
-    if (tid == 0) p.tokens[m] = sm.pick;
-    return;
-  }
-
   Weights wt;
-  wt.init(sm.table, top, q.T, q.min_p, places);
-  Threshold thr{0, p.V};
-  if (!q.need_k && !q.need_p) {
-    for (int g = tid; g < G; g += kRowThreads) sm.group[g] = work.sums[g];
-    __syncthreads();
-    pick_token<BF16, VEC>(p, row, wt, thr, q.u, m);
-    return;
-  }
-  // Every condition on a logit's weight is one on its key.
-  const uint32_t top_key = ordered(top);
-  const uint32_t min_key = least_allowed(q, wt, top);
-  uint64_t live = 0;                 // groups that hold a logit min-p allows
-  for (int g = tid; g < G; g += kRowThreads)
-    live += ordered(sm.gmax[g]) >= min_key;
-  row_scan(live, sm.red, &live);
-
-  // ---- which keys go to the list: first <= key < last ----
-  uint32_t first = min_key, last = 0xffffffffu;
-  uint64_t mass = 0, before = 0;     // top-p alone: weights of all, and in front
-  bool listed = true;
-  // Puts the keys first <= key < last into the list, in any order; whether it
-  // took all of them (ties may be many).
-  const auto gather = [&]() {
-    if (tid == 0) sm.n = 0;
-    __syncthreads();
-    // as floats; without a last key, one that nothing compares with
-    const float x_first = unordered(first);
-    const float x_last = last == 0xffffffffu ? __builtin_nanf("")
-                                             : unordered(last);
-    row.each_group(
-        [&](int g) { return ordered(sm.gmax[g]) >= first; },
-        [&](const Group<BF16, VEC>& v) {
-          uint64_t in[8];
-          int n = 0;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            in[e] = __ballot(v.x[e] >= x_first && !(v.x[e] >= x_last));
-            n += __popcll(in[e]);
-          }
-          if (n == 0) return;
-          uint32_t at = 0;             // one place for the whole group's
-          if ((tid & 63) == 0) at = atomicAdd(&sm.n, uint32_t(n));
-          at = uint32_t(uniform(int(at)));
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if (in[e] == 0) continue;
-            const uint32_t mine = __builtin_amdgcn_mbcnt_hi(
-                uint32_t(in[e] >> 32),
-                __builtin_amdgcn_mbcnt_lo(uint32_t(in[e]), at));
-            if (v.x[e] >= x_first && !(v.x[e] >= x_last) && mine < kList)
-              sm.list.key[mine] = uint64_t(ordered(v.x[e])) << 32 |
-                                  (0xffffffffu - uint32_t(v.index(e)));
-            at += __popcll(in[e]);
-          }
-        });
-    __syncthreads();
-    return sm.n <= kList;
-  };
-  // Fewer groups than k hold what min-p allows: likely few logits in all.
-  bool have_list = q.need_k && q.min_p > 0.0f && uint64_t(k) > live && gather();
-  if (have_list) {
-    // (cut at k below)
-  } else if (q.need_k && uint64_t(k) <= live) {
-    // the k-th largest group maximum: at least k logits lie at or above it
-    // (ranks by counting, several threads to a group where there are few)
-    int parts = 1;
-    while (2 * parts * G <= kRowThreads) parts *= 2;
-    for (int g = tid; g < G; g += kRowThreads) sm.count[g] = 0;
-    __syncthreads();
-    for (int i = tid; i < G * parts; i += kRowThreads) {
-      const int g = i / parts;
-      const float v = sm.gmax[g];
-      int rank = 0;
-      for (int j = i & (parts - 1); j < G; j += parts)
-        rank += sm.gmax[j] > v || (sm.gmax[j] == v && j < g);
-      atomicAdd(&sm.count[g], uint32_t(rank));
-    }
-    __syncthreads();
-    for (int g = tid; g < G; g += kRowThreads)
-      if (sm.count[g] == uint32_t(k - 1)) sm.value = ordered(sm.gmax[g]);
-    __syncthreads();
-    first = uint32_t(sm.value);
-  } else if (q.need_k) {
-    const CountBins bins(sm.gmax, G, top, min_key);
-    if (k > G) {                     // counted by the kernel before
-      for (int i = tid; i < kBins; i += kRowThreads)
-        sm.count[i] = uint32_t(work.sums[i]);
-    } else {
-      for (int i = tid; i < kBins; i += kRowThreads) sm.count[i] = 0;
-      __syncthreads();
-      row.each([&](int g) { return ordered(sm.gmax[g]) >= min_key; },
-               [&](float x, int) {
-                 const int bin = bins(x);
-                 if (bin < kBins) atomicAdd(&sm.count[bin], 1u);
-               });
-    }
-    __syncthreads();
-    find_prefix<kPer2k>(sm, sm.count, kBins,
-                   [&](uint64_t) { return uint64_t(k); });
-    const int border = sm.found;
-    // (fewer than k in the bins: all there are, if the list surely takes them)
-    listed = border >= 0 ? sm.before + sm.value <= kList : p.V <= kList;
-    if (border >= 0)
-      first = max(first, least_key(top_key, [&](float x) {
-                    return bins(x) <= border;
-                  }));
-  } else {
-    for (int i = tid; i < kBins; i += kRowThreads) sm.mass[i] = work.sums[i];
-    __syncthreads();
-    mass = find_prefix<kPer2k>(sm, sm.mass, kBins, [&](uint64_t w) {
-      return share_of(q.top_p, w);
-    });
-    before = sm.before;
-    const int border = sm.found;
-    first = max(first, least_key(top_key, [&](float x) {
-                  return wt.bin(wt.steps(x)) <= border;
-                }));
-    if (border > 0)
-      last = least_key(top_key, [&](float x) {
-        return wt.bin(wt.steps(x)) < border;
-      });
-  }
-  if (listed && !have_list) listed = gather();
-
-  if (listed) {
-    const int n = sm.n;
+  wt.init(sm.table, plan.top, q.T, q.min_p, places);
+  Threshold thr{plan.min_key, p.V};
+  if (plan.mode == kGather && plan.n >= 1 && plan.n <= kList) {
+    const int n = int(plan.n);
+    for (int i = tid; i < n; i += kRowThreads) sm.key[i] = work.list[i];
     sort_list(sm, n);
     int kept = q.need_k ? min(n, k) : n;
-    for (int i = tid; i < kept; i += kRowThreads)
-      sm.list.w[i] = wt.of(unordered(uint32_t(sm.list.key[i] >> 32)));
+    // weights: kept beside a short list, computed at each use for a long one
+    const bool stored = n <= kList / 2;
+    uint64_t* const w = sm.key + kList / 2;
+    if (stored)
+      for (int i = tid; i < kept; i += kRowThreads)
+        w[i] = wt.of(unordered(uint32_t(sm.key[i] >> 32)));
+    const auto weight = [&](int i) {
+      return stored ? w[i] : wt.of(unordered(uint32_t(sm.key[i] >> 32)));
+    };
     __syncthreads();
     if (q.need_p) {
-      find_prefix<kPerList>(sm, sm.list.w, kept, [&](uint64_t w) {
-        return share_of(q.top_p, q.need_k ? w : mass) - before;
+      find_prefix<kPerList>(sm, weight, kept, [&](uint64_t all) {
+        return share_of(q.top_p, q.need_k ? all : plan.mass) - plan.before;
       });
       if (sm.found >= 0) kept = sm.found + 1;
     }
     if (!q.need_k) {
       // the last kept one is the threshold pair
-      const uint64_t end = sm.list.key[kept - 1];
+      const uint64_t end = sm.key[kept - 1];
       thr = Threshold{uint32_t(end >> 32), int(0xffffffffu - uint32_t(end))};
     } else {
       // the index whose running weight passes u: by its upper ten bits, then
@@ -994,25 +1192,35 @@ __global__ void __launch_bounds__(kRowThreads)
         for (int i = tid; i < 1024; i += kRowThreads) bins[i] = 0;
         __syncthreads();
         for (int i = tid; i < kept; i += kRowThreads) {
-          const int at = int(0xffffffffu - uint32_t(sm.list.key[i]));
+          const int at = int(0xffffffffu - uint32_t(sm.key[i]));
           if (pass == 0 || at >> 10 == high)
             atomicAdd((unsigned long long*)&bins[pass == 0 ? at >> 10
                                                            : at & 1023],
-                      (unsigned long long)sm.list.w[i]);
+                      (unsigned long long)weight(i));
         }
         __syncthreads();
-        find_prefix<kPer1k>(sm, bins, 1024, [&](uint64_t w) {
-          if (pass == 0) target = past_share(q.u, w);
-          return target;
-        });
+        find_prefix<kPer1k>(sm, [&](int i) { return bins[i]; }, 1024,
+                            [&](uint64_t all) {
+                              if (pass == 0) target = past_share(q.u, all);
+                              return target;
+                            });
         target -= sm.before;
         if (pass == 0) high = max(sm.found, 0);
       }
-      if (tid == 0) p.tokens[m] = high << 10 | max(sm.found, 0);
+      if (tid == 0) {
+        p.tokens[m] = high << 10 | max(sm.found, 0);
+        work.plan->mode = kDecided;
+      }
       return;
     }
   } else {
     // ---- no list holds them: thresholds by radix search ----
+    const uint32_t min_key = plan.min_key;
+    const Row<BF16, VEC> row{static_cast<const char*>(p.logits) +
+                                 m * p.s_row * (BF16 ? 2 : 4),
+                             p.V, G, sm};
+    uint64_t mass = plan.mass;
+    for (int g = tid; g < G; g += kRowThreads) sm.gmax[g] = work.gmax[g];
     const auto used = [&](int g) { return ordered(sm.gmax[g]) >= min_key; };
     __syncthreads();
     if (q.need_k) {
@@ -1036,45 +1244,45 @@ __global__ void __launch_bounds__(kRowThreads)
   }
   // the kept weights of each group are left to many workgroups
   if (tid == 0) {
-    *work.key = int32_t(thr.key);
-    *work.index = thr.index;
+    work.plan->key = thr.key;
+    work.plan->index = thr.index;
+    work.plan->mode = kKept;
   }
 }
 
 // Kept weights of each group of the rows with a threshold pair.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads)
-    kda_kept_sums_kernel(SampleParams p, int G, int per_row, int places) {
+    kda_kept_sums_kernel(SampleParams p, int G, int per_row,
+                         int places) {
   __shared__ double table[kSteps];
-  const int m = blockIdx.x / per_row, part = blockIdx.x - m * per_row;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ float kept[kMaxThreads / 64][kGroup];
+  const Part part(G, per_row);
+  const int m = part.m;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const Work work(p, m, G);
-  const Threshold thr{uint32_t(*work.key), *work.index};
-  if (thr.index < 0) return;
+  if (work.plan->mode != kKept) return;
+  const Threshold thr{work.plan->key, work.plan->index};
   const int b = request_of_row(p, m, lane);
   if (b < 0) return;
   const Params q(p, b, m);
   fill_table(table);
   __syncthreads();
   Weights wt;
-  wt.init(table, row_max(work.gmax, G), q.T, q.min_p, places);
+  wt.init(table, work.plan->top, q.T, q.min_p, places);
+  // (the threshold is never below what min-p allows)
+  const float least = unordered(thr.key);
   const char* row = static_cast<const char*>(p.logits) +
                     m * p.s_row * (BF16 ? 2 : 4);
 #pragma unroll 1
-  for (int i = 0; i < kPerWg / 4; ++i) {
-    const int g = part * kPerWg + wave * (kPerWg / 4) + i;
-    if (g >= G) break;
+  for (int g = part.first + wave; g < part.end; g += kMaxThreads / 64) {
     uint64_t sum = 0;
-    const float x = work.gmax[g];
-    if (wt.allows(x, wt.steps(x)) && ordered(x) >= thr.key) {
+    if (work.gmax[g] >= least) {
       Group<BF16, VEC> v;
       v.load(row, g, p.V);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const double d = wt.steps(v.x[e]);
-        if (wt.allows(v.x[e], d) && thr.keeps(v.x[e], v.index(e)))
-          sum += wt.whole(d);
-      }
+      each_kept<BF16, VEC>(
+          v, kept[wave], [&](float x, int i) { return thr.keeps(x, i); },
+          [&](float x) { sum += wt.of(x); });
       sum = wave_sum64(sum);
     }
     if (lane == 0) work.sums[g] = sum;
@@ -1088,8 +1296,8 @@ __global__ void __launch_bounds__(kRowThreads)
   RowSmem& sm = *reinterpret_cast<RowSmem*>(smem);
   const int m = blockIdx.x, tid = threadIdx.x;
   const Work work(p, m, G);
-  const Threshold thr{uint32_t(*work.key), *work.index};
-  if (thr.index < 0) return;
+  if (work.plan->mode != kKept && work.plan->mode != kSummed) return;
+  const Threshold thr{work.plan->key, work.plan->index};
   const int b = request_of_row(p, m, tid & 63);
   if (b < 0) return;
   const Params q(p, b, m);
@@ -1097,7 +1305,7 @@ __global__ void __launch_bounds__(kRowThreads)
   fill_table(sm.table);
   __syncthreads();
   Weights wt;
-  wt.init(sm.table, row_max(work.gmax, G), q.T, q.min_p, places);
+  wt.init(sm.table, work.plan->top, q.T, q.min_p, places);
   const Row<BF16, VEC> row{static_cast<const char*>(p.logits) +
                                m * p.s_row * (BF16 ? 2 : 4),
                            p.V, G, sm};
@@ -1116,26 +1324,28 @@ __global__ void __launch_bounds__(256) kda_accept_kernel(SampleParams p) {
   p.next[b] = s < e ? p.tokens[t] : -1;
 }
 
+static_assert(sizeof(RowSmem) <= 64 * 1024, "LDS of a launch");
+
 template <bool BF16, bool VEC>
 int launch_rows(const SampleParams& p, int G, int places,
                 hipStream_t stream) {
   const int per_row = (G + kPerWg - 1) / kPerWg;
-  launch_kernel(kda_group_max_kernel<BF16, VEC>,
-                dim3(uint32_t(p.M) * uint32_t(per_row)), dim3(kMaxThreads), 0,
-                stream, p, G, per_row);
   const dim3 parts(uint32_t(p.M) * uint32_t(per_row));
-  launch_kernel(kda_row_sums_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
-                stream, p, G, per_row, places);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return int(e);
-  for (auto kernel : {kda_sample_kernel<BF16, VEC>,
-                      kda_pick_kernel<BF16, VEC>}) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                            hipFuncAttributeMaxDynamicSharedMemorySize,
-                            int(sizeof(RowSmem)));
-    if (e != hipSuccess) return int(e);
-  }
-  launch_kernel(kda_sample_kernel<BF16, VEC>, dim3(p.M), dim3(kRowThreads),
+  launch_kernel(kda_group_max_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
+                stream, p, G, per_row);
+  // half as many workgroups, each with bins of its own, for many rows (640
+  // rows with top-k 1000 of 131072: 64 us against 97; one row with top-p: 12
+  // as it is, 17 with half)
+  const int sums_wg = p.M >= 128 ? 2 * kPerWg : kPerWg;
+  const int sums_row = (G + sums_wg - 1) / sums_wg;
+  launch_kernel(kda_row_sums_kernel<BF16, VEC>,
+                dim3(uint32_t(p.M) * uint32_t(sums_row)), dim3(kMaxThreads), 0,
+                stream, p, G, sums_row, sums_wg, places);
+  launch_kernel(kda_plan_kernel<BF16, VEC>, dim3(p.M), dim3(64), 0, stream, p,
+                G, places);
+  launch_kernel(kda_gather_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
+                stream, p, G, per_row);
+  launch_kernel(kda_list_kernel<BF16, VEC>, dim3(p.M), dim3(kRowThreads),
                 sizeof(RowSmem), stream, p, G, places);
   launch_kernel(kda_kept_sums_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
                 stream, p, G, per_row, places);

@@ -197,6 +197,85 @@ def test_large_vocabulary_and_many_requests():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("k", [1, 3, 4, 5, 60, 700, 2500])
+@pytest.mark.parametrize("mp", [0.0, 1e-9, 0.3])
+def test_few_groups_hold_logits(k, mp):
+    """A masked vocabulary (as a grammar leaves it): only some stretches hold
+    logits above -inf, more or fewer than k of them."""
+    V = 20000
+    rows = []
+    for seed, spans in enumerate([[(7000, 7003)], [(0, 40), (9000, 9100)],
+                                  [(100, 2000)], [(i, i + 1) for i in
+                                                  range(5, V, 600)],
+                                  [(512, 6200), (19999, 20000)]]):
+        x = logits(1, V, seed=40 + seed)[0].cpu()
+        keep = torch.zeros(V, dtype=torch.bool)
+        for s, e in spans:
+            keep[s:e] = True
+        rows.append(torch.where(keep, x, torch.tensor(-float("inf"))))
+    x = torch.stack(rows).to(DEV)
+    M = len(rows)
+    u = np.linspace(0.05, 0.95, M)
+    for p in (1.0, 0.7):
+        full = [np.full(M, v) for v in (0.9, k, p, mp)]
+        got = run(x, u, *full)["tokens"]
+        assert np.array_equal(got, expect(x, u, *full)), p
+
+
+@pytest.mark.gpu
+def test_counts_that_end_before_k():
+    """Every group's maximum far above its other logits: the counted bins hold
+    fewer than k, and the rest lies behind them."""
+    V, M = 131072, 4
+    x = logits(M, V, seed=50) - 60.0
+    x[:, ::512] = 10.0 + logits(M, V // 512, seed=51, std=0.1)
+    u = np.array([0.1, 0.5, 0.9, 0.999])
+    k = np.array([900, 1000, 257, 300])
+    for T, mp in ((1.0, None), (30.0, None), (30.0, np.full(M, 0.05))):
+        full = [np.full(M, T), k, np.full(M, 0.99), mp]
+        got = run(x, u, *full)["tokens"]
+        assert np.array_equal(got, expect(x, u, *full)), T
+
+
+@pytest.mark.gpu
+def test_top_k_among_two_thousand_groups():
+    """The k-th of up to 2048 group maxima, and k just past them."""
+    V, M = 1 << 20, 5
+    x = logits(M, V, "bf16", seed=52)
+    u = np.array([0.2, 0.4, 0.6, 0.8, 0.95])
+    k = np.array([2, 64, 1500, 2048, 2049])
+    got = run(x, u, None, k)["tokens"]
+    assert np.array_equal(got, expect(x, u, None, k))
+
+
+@pytest.mark.gpu
+def test_many_rows_share_the_sums_differently():
+    """From 128 rows on a workgroup takes more groups: the same tokens."""
+    V, M = 9000, 130
+    x = logits(M, V, seed=53)
+    rng = np.random.RandomState(5)
+    u, T = rng.rand(M), rng.choice([0.7, 1.0], size=M)
+    k = rng.choice([0, 30, 400], size=M)
+    p, mp = rng.choice([1.0, 0.8], size=M), rng.choice([0.0, 0.05], size=M)
+    got = run(x, u, T, k, p, mp)["tokens"]
+    assert np.array_equal(got, expect(x, u, T, k, p, mp))
+    few = run(x[:5], u[:5], T[:5], k[:5], p[:5], mp[:5])["tokens"]
+    assert np.array_equal(few, got[:5])
+
+
+@pytest.mark.gpu
+def test_backward_offsets_stay_inside():
+    """Offsets that run backwards: nothing outside the outputs is touched, no
+    token leaves the vocabulary."""
+    x = logits(12, 3000, seed=54)
+    out = run(x, np.full(12, 0.5), np.full(4, 1.0), np.array([0, 5, 300, 40]),
+              np.array([0.9, 1.0, 0.9, 1.0]), None, qsl=[8, 3, 20, 5, 10],
+              draft=np.zeros(12))
+    assert np.all((out["tokens"] == -9) |
+                  ((out["tokens"] >= 0) & (out["tokens"] < 3000)))
+
+
+@pytest.mark.gpu
 def test_no_rows():
     got = run(torch.zeros((0, 50), device=DEV), np.zeros(0))
     assert got["tokens"].size == 0
