@@ -18,18 +18,26 @@
 //   kda_row_sums_kernel, only for rows that need it: with top-p alone the
 //   weights by bins of 1/32 octave of d, with more for top-k than groups that
 //   hold any logit counts by bins, without either the weights of each group.
-//   kda_plan_kernel, one wave a row, decides which logits matter.  Greedy rows
-//   end here.  With top-k <= groups, the k-th largest group maximum bounds the
-//   k-th largest value from below; with larger k the bin at the border of the
-//   counts does.  Top-p alone needs only the bin that holds its border, and so
-//   finds the threshold pair however many logits are kept.
+//   One wave of the last workgroup of a row then decides which logits matter.
+//   Greedy rows end here.  With top-k <= groups, the k-th largest group maximum
+//   bounds the k-th largest value from below; with larger k the bin at the
+//   border of the counts does.  Top-p alone needs only the bin that holds its
+//   border, and so finds the threshold pair however many logits are kept.
 //   kda_gather_kernel lists those logits, reading again only groups whose
 //   maximum reaches the bound.
 //   kda_list_kernel, one workgroup a row, sorts the list, cuts it and takes the
 //   token.  What no list holds (thousands of ties, or of top-k) it leaves to a
 //   radix search of any size.
-//   kda_kept_sums_kernel and kda_pick_kernel, only for rows that kept more
-//   than a list: the kept weights of each group, and the token from them.
+//   kda_kept_sums_kernel, only for rows that kept more than a list: the kept
+//   weights of each group, and by one wave of the row's last workgroup the
+//   token from them.
+//
+// The last workgroups' work stands in place of two kernels of its own: 33 rows
+// take 57 us a call against 62.
+//
+// In all, 640 of 1024 window rows of 131072 bf16 logits with mixed parameters:
+// 28 us for the maxima (6 TB/s), 57 sums and plans (fp64 weights of the rows
+// with top-p alone), 17 lists, 34 sorts, 24 kept sums, 5 acceptance.
 #include "kda_serving.hpp"
 
 namespace kda {
@@ -39,7 +47,7 @@ constexpr int kGroup = 512;          // logits of a group
 constexpr int kMaxGroups = 2048;     // V up to 2^20
 constexpr int kMaxThreads = 256;     // split kernels
 constexpr int kPerWg = 4 * 4;        // groups per workgroup of the split kernels
-constexpr int kRowThreads = 512;     // list and pick kernels
+constexpr int kRowThreads = 512;     // list kernel
 constexpr int kWaves = kRowThreads / 64;
 constexpr int kList = 4096;          // entries of the sorted list
 constexpr int kBins = 2048;
@@ -285,6 +293,8 @@ struct Plan {
   uint64_t mass, before;     // top-p alone: weights of all, and above `last`
   uint32_t key;              // threshold pair
   int32_t index;
+  uint32_t arrived[2];       // workgroups that have done the row's sums, and
+                             // its kept sums
 };
 
 // Workspace of a row: maxima of its groups, sums (bins or groups), the list,
@@ -312,13 +322,37 @@ struct Work {
   }
 };
 
+// Whether this workgroup is the last of `parts` of a row to get here.  It then
+// may read (with shared_load) what the others wrote with device-scope atomics
+// and shared_store before they got here.  Those go through to where all XCDs
+// see them, so that waiting for their end is enough: a release fence would
+// write back the whole L2 (640 rows with top-k 1000: the sums kernel 750 us
+// in place of 104).
+__device__ __forceinline__ bool last_of(uint32_t* arrived, int parts) {
+  __shared__ int last;
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(arrived, 1u) + 1 == uint32_t(parts);
+  __syncthreads();
+  return last != 0;
+}
+__device__ __forceinline__ void shared_store(uint64_t* at, uint64_t v) {
+  __hip_atomic_store(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t shared_load(const uint64_t* at) {
+  return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
 // The groups of a row that a workgroup of the split kernels takes.
 struct Part {
   int m, first, end;
+  bool chosen;     // one of them, not always on the same XCD
   __device__ __forceinline__ Part(int G, int per_row, int per_wg = kPerWg) {
     m = blockIdx.x / per_row;
-    first = (blockIdx.x - m * per_row) * per_wg;
+    const int part = blockIdx.x - m * per_row;
+    first = part * per_wg;
     end = min(first + per_wg, G);
+    chosen = part == m % per_row;
   }
 };
 
@@ -331,6 +365,8 @@ __global__ void __launch_bounds__(kMaxThreads)
   const char* row = static_cast<const char*>(p.logits) +
                     m * p.s_row * (BF16 ? 2 : 4);
   const Work out(p, m, G);
+  if (part.chosen && threadIdx.x == 0)
+    out.plan->arrived[0] = out.plan->arrived[1] = 0;
   // the row's bins, cleared for the next kernel
   for (int i = (blockIdx.x - m * per_row) * kMaxThreads + threadIdx.x;
        i < kBins; i += per_row * kMaxThreads)
@@ -468,39 +504,43 @@ __device__ __forceinline__ uint64_t wave_scan(uint64_t v) {
   return v;
 }
 
-// First bin of a row's kBins whose inclusive prefix sum reaches goal(total),
-// or -1, by one wave: the 32 bins of a lane, then those of the lane found.
-struct BinFound {
+// First of n numbers (at most 64 * 64) whose inclusive prefix sum reaches
+// goal(total), or -1, by one wave: by the `own` numbers of each lane, then
+// among those of the lane found.
+struct Found {
   int at;
   uint64_t before, value, total;
 };
 template <class Goal>
-__device__ __forceinline__ BinFound find_bin(const uint64_t* bins, Goal goal) {
-  constexpr int kOwn = kBins / 64;
+__device__ __forceinline__ Found find_first(const uint64_t* a, int n,
+                                            Goal goal) {
+  const int own = (n + 63) / 64;
   const int lane = threadIdx.x & 63;
-  uint64_t own = 0;
-#pragma unroll
-  for (int j = 0; j < kOwn / 2; ++j) {
-    const ulonglong2 v =
-        reinterpret_cast<const ulonglong2*>(bins)[lane * (kOwn / 2) + j];
-    own += v.x + v.y;
+  uint64_t sum = 0;
+#pragma unroll 4
+  for (int j = 0; j < own; ++j) {
+    const int i = lane * own + j;
+    const uint64_t v = shared_load(a + min(i, n - 1));
+    sum += i < n ? v : 0;
   }
-  BinFound f{-1, 0, 0, 0};
-  const uint64_t upto = wave_scan(own);
+  Found f{-1, 0, 0, 0};
+  const uint64_t upto = wave_scan(sum);
   f.total = __shfl((unsigned long long)upto, 63);
   const uint64_t target = goal(f.total);
   const uint64_t in = __ballot(upto >= target);
   if (in == 0) return f;
   const int l = __ffsll((unsigned long long)in) - 1;
-  const uint64_t base = __shfl((unsigned long long)(upto - own), l);
-  const uint64_t v = lane < kOwn ? bins[l * kOwn + lane] : 0;
+  const uint64_t base = __shfl((unsigned long long)(upto - sum), l);
+  const int first = l * own;
+  const uint64_t v = lane < own && first + lane < n ? shared_load(a + first + lane) : 0;
   const uint64_t u = base + wave_scan(v);
   const int i = __ffsll((unsigned long long)__ballot(u >= target)) - 1;
-  f.at = l * kOwn + i;
+  f.at = first + i;
   f.before = __shfl((unsigned long long)(u - v), i);
   f.value = __shfl((unsigned long long)v, i);
   return f;
 }
+static_assert(kMaxGroups <= 64 * 64 && kBins <= 64 * 64, "find_first");
 
 // Inclusive prefix sum over the workgroup, and the total.
 __device__ __forceinline__ uint64_t row_scan(uint64_t v, uint64_t* red,
@@ -861,128 +901,12 @@ __device__ __forceinline__ uint32_t least_allowed(const Params& q,
                    [&](float x) { return wt.allows(x, wt.steps(x)); });
 }
 
-// kPerWg groups a workgroup, of the rows that need more than their group
-// maxima: top-k beyond the number of groups, counts by bins; top-p alone,
-// weights by bins (both added to the row's bins); neither, the weight of each
-// group.
-template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads)
-    kda_row_sums_kernel(SampleParams p, int G, int per_row, int per_wg,
-                        int places) {
-  __shared__ double table[kSteps];
-  __shared__ unsigned long long mass[kBins];
-  __shared__ float kept[kMaxThreads / 64][kGroup];
-  const Part part(G, per_row, per_wg);
-  const int m = part.m;
-  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int b = request_of_row(p, m, lane);
-  if (b < 0) return;
-  const Params q(p, b, m);
-  if (q.greedy) return;
-  const bool counts = q.need_k;
-  const Work work(p, m, G);
-  const int live = counts ? live_groups(work.gmax, G, kLowestKey) : G;
-  if (counts && q.k <= live) return;
-  const float top = row_max(work.gmax, G);
-  if (top == -__builtin_inff()) return;
-  if (!counts) fill_table(table);
-  const bool binned = counts || q.need_p;
-  uint32_t* count = reinterpret_cast<uint32_t*>(mass);
-  if (binned)
-    for (int i = threadIdx.x; i < (counts ? kBins / 2 : kBins);
-         i += kMaxThreads)
-      mass[i] = 0;
-  __syncthreads();
-  Weights wt;
-  wt.init(table, top, q.T, q.min_p, places);
-  const uint32_t min_key = least_allowed(q, wt, top);
-  const float least = unordered(min_key);
-  const CountBins bins(work.gmax, G, top, min_key, CountBins::few(q.k, live));
-  const char* row = static_cast<const char*>(p.logits) +
-                    m * p.s_row * (BF16 ? 2 : 4);
-#pragma unroll 1
-  for (int g = part.first + wave; g < part.end; g += kMaxThreads / 64) {
-    // a group whose largest logit min-p drops has nothing to add
-    if (work.gmax[g] < least) {
-      if (!binned && lane == 0) work.sums[g] = 0;
-      continue;
-    }
-    Group<BF16, VEC> v;
-    v.load(row, g, p.V);
-    if (counts) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int bin = bins(v.x[e]);
-        if (bin < kBins) atomicAdd(&count[bin], 1u);
-      }
-      continue;
-    }
-    uint64_t sum = 0;
-    const auto in = [&](float x, int) { return x >= least; };
-    if (binned) {
-      each_kept<BF16, VEC>(v, kept[wave], in, [&](float x) {
-        const double d = wt.steps(x);
-        const uint64_t w = wt.whole(d);
-        if (w > 0) atomicAdd(&mass[wt.bin(d)], (unsigned long long)w);
-      });
-    } else {
-      each_kept<BF16, VEC>(v, kept[wave], in,
-                           [&](float x) { sum += wt.of(x); });
-      sum = wave_sum64(sum);
-      if (lane == 0) work.sums[g] = sum;
-    }
-  }
-  if (!binned) return;
-  __syncthreads();
-  for (int i = threadIdx.x; i < kBins; i += kMaxThreads) {
-    const uint64_t add = counts ? count[i] : mass[i];
-    if (add > 0)
-      atomicAdd((unsigned long long*)&work.sums[i], (unsigned long long)add);
-  }
-}
-
-// The token whose running weight passes u: from the weights of the groups
-// (sm.group) and the group that the border falls into.
-template <bool BF16, bool VEC>
-__device__ __forceinline__ void pick_token(const SampleParams& p,
-                                           const Row<BF16, VEC>& row,
-                                           const Weights& wt, Threshold thr,
-                                           float u, int m) {
-  RowSmem& sm = row.sm;
-  const uint64_t mass = find_prefix<kPer2k>(
-      sm, [&](int i) { return sm.group[i]; }, row.G, [&](uint64_t w) { return past_share(u, w); });
-  const uint64_t target = past_share(u, mass);
-  const uint64_t before = sm.before;
-  if (threadIdx.x < 64) {
-    Group<BF16, VEC> v;
-    v.load(row.at, min(max(sm.found, 0), row.G - 1), p.V);
-    uint64_t w[8], pre[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const double d = wt.steps(v.x[e]);
-      w[e] = wt.allows(v.x[e], d) && thr.keeps(v.x[e], v.index(e))
-                 ? wt.whole(d) : 0;
-    }
-    group_prefix<VEC>(w, pre);
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (before + pre[e] < target && before + pre[e] + w[e] >= target)
-        p.tokens[m] = v.index(e);
-  }
-}
-
 // What a row needs, by one wave; greedy rows get their token.
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(64)
-    kda_plan_kernel(SampleParams p, int G, int places) {
-  const int m = blockIdx.x, lane = threadIdx.x;
-  const Work work(p, m, G);
-  const int b = request_of_row(p, m, lane);
-  if (b < 0) {
-    if (lane == 0) work.plan->mode = kDecided;
-    return;
-  }
-  const Params q(p, b, m);
+__device__ __forceinline__ void plan_row(const SampleParams& p,
+                                         const Work& work, const Params& q,
+                                         int m, int G, int places) {
+  const int lane = threadIdx.x & 63;
   const int k = q.k;
   const float* gmax = work.gmax;
   const float top = row_max(gmax, G);
@@ -1027,8 +951,8 @@ __global__ void __launch_bounds__(64)
   if (!q.need_k && !q.need_p) {
     plan.mode = kSummed;
   } else if (!q.need_k) {
-    const BinFound f = find_bin(
-        work.sums, [&](uint64_t w) { return share_of(q.top_p, w); });
+    const Found f = find_first(
+        work.sums, kBins, [&](uint64_t w) { return share_of(q.top_p, w); });
     plan.mass = f.total;
     plan.before = f.before;
     plan.first = max(min_key, least_key(top_key, [&](float x) {
@@ -1045,10 +969,10 @@ __global__ void __launch_bounds__(64)
     if (k <= allowed) {
       // at least k logits lie at or above the k-th largest group maximum
       plan.first = kth_key(gmax, G, k);
-    } else if (k > live) {           // counted by the kernel before
+    } else if (k > live) {           // counted before
       const CountBins bins(gmax, G, top, min_key, CountBins::few(k, live));
-      const BinFound f =
-          find_bin(work.sums, [&](uint64_t) { return uint64_t(k); });
+      const Found f = find_first(work.sums, kBins,
+                                 [&](uint64_t) { return uint64_t(k); });
       if (f.at >= 0)
         plan.first = max(min_key, least_key(top_key, [&](float x) {
                            return bins(x) <= f.at;
@@ -1061,6 +985,118 @@ __global__ void __launch_bounds__(64)
     // between the two, min-p likely leaves few: all it allows
   }
   if (lane == 0) *work.plan = plan;
+}
+
+// per_wg groups a workgroup, of the rows that need more than their group
+// maxima: top-k beyond the number of groups, counts by bins; top-p alone,
+// weights by bins (both added to the row's bins); neither, the weight of each
+// group.
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kMaxThreads)
+    kda_row_sums_kernel(SampleParams p, int G, int per_row, int per_wg,
+                        int places) {
+  __shared__ double table[kSteps];
+  __shared__ unsigned long long mass[kBins];
+  __shared__ float kept[kMaxThreads / 64][kGroup];
+  const Part part(G, per_row, per_wg);
+  const int m = part.m;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int b = request_of_row(p, m, lane);
+  const Work work(p, m, G);
+  if (b < 0) {
+    if (part.chosen && threadIdx.x == 0) work.plan->mode = kDecided;
+    return;
+  }
+  const Params q(p, b, m);
+  const bool counts = q.need_k;
+  const int live = counts ? live_groups(work.gmax, G, kLowestKey) : G;
+  const float top = row_max(work.gmax, G);
+  if (q.greedy || (counts && q.k <= live) || top == -__builtin_inff()) {
+    if (part.chosen && wave == 0)
+      plan_row<BF16, VEC>(p, work, q, m, G, places);
+    return;
+  }
+  if (!counts) fill_table(table);
+  const bool binned = counts || q.need_p;
+  uint32_t* count = reinterpret_cast<uint32_t*>(mass);
+  if (binned)
+    for (int i = threadIdx.x; i < (counts ? kBins / 2 : kBins);
+         i += kMaxThreads)
+      mass[i] = 0;
+  __syncthreads();
+  Weights wt;
+  wt.init(table, top, q.T, q.min_p, places);
+  const uint32_t min_key = least_allowed(q, wt, top);
+  const float least = unordered(min_key);
+  const CountBins bins(work.gmax, G, top, min_key, CountBins::few(q.k, live));
+  const char* row = static_cast<const char*>(p.logits) +
+                    m * p.s_row * (BF16 ? 2 : 4);
+#pragma unroll 1
+  for (int g = part.first + wave; g < part.end; g += kMaxThreads / 64) {
+    // a group whose largest logit min-p drops has nothing to add
+    if (work.gmax[g] < least) {
+      if (!binned && lane == 0) shared_store(&work.sums[g], 0);
+      continue;
+    }
+    Group<BF16, VEC> v;
+    v.load(row, g, p.V);
+    if (counts) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int bin = bins(v.x[e]);
+        if (bin < kBins) atomicAdd(&count[bin], 1u);
+      }
+      continue;
+    }
+    uint64_t sum = 0;
+    const auto in = [&](float x, int) { return x >= least; };
+    if (binned) {
+      each_kept<BF16, VEC>(v, kept[wave], in, [&](float x) {
+        const double d = wt.steps(x);
+        const uint64_t w = wt.whole(d);
+        if (w > 0) atomicAdd(&mass[wt.bin(d)], (unsigned long long)w);
+      });
+    } else {
+      each_kept<BF16, VEC>(v, kept[wave], in,
+                           [&](float x) { sum += wt.of(x); });
+      sum = wave_sum64(sum);
+      if (lane == 0) shared_store(&work.sums[g], sum);
+    }
+  }
+  if (binned) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kMaxThreads) {
+      const uint64_t add = counts ? count[i] : mass[i];
+      if (add > 0)
+        atomicAdd((unsigned long long*)&work.sums[i], (unsigned long long)add);
+    }
+  }
+  if (last_of(&work.plan->arrived[0], per_row) && wave == 0)
+    plan_row<BF16, VEC>(p, work, q, m, G, places);
+}
+
+// The token whose running weight passes u, by one wave: from the weights of
+// the groups and the group that the border falls into.
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void pick_token(const SampleParams& p,
+                                           const Work& work,
+                                           const Weights& wt, Threshold thr,
+                                           float u, int m, int G) {
+  const Found f = find_first(work.sums, G,
+                             [&](uint64_t w) { return past_share(u, w); });
+  const uint64_t target = past_share(u, f.total);
+  Group<BF16, VEC> v;
+  v.load(static_cast<const char*>(p.logits) + m * p.s_row * (BF16 ? 2 : 4),
+         max(f.at, 0), p.V);
+  uint64_t w[8], pre[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    w[e] = thr.keeps(v.x[e], v.index(e)) ? wt.of(v.x[e]) : 0;
+  group_prefix<VEC>(w, pre);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (f.before + pre[e] < target && f.before + pre[e] + w[e] >= target)
+      p.tokens[m] = v.index(e);
 }
 
 // The keys first <= key < last of the rows that list them, in any order.
@@ -1250,7 +1286,8 @@ __global__ void __launch_bounds__(kRowThreads)
   }
 }
 
-// Kept weights of each group of the rows with a threshold pair.
+// Kept weights of each group of the rows with a threshold pair, and their
+// token, or that of a row whose sums are there.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads)
     kda_kept_sums_kernel(SampleParams p, int G, int per_row,
@@ -1261,7 +1298,8 @@ __global__ void __launch_bounds__(kMaxThreads)
   const int m = part.m;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const Work work(p, m, G);
-  if (work.plan->mode != kKept) return;
+  const Mode mode = work.plan->mode;
+  if (mode != kKept && (mode != kSummed || !part.chosen)) return;
   const Threshold thr{work.plan->key, work.plan->index};
   const int b = request_of_row(p, m, lane);
   if (b < 0) return;
@@ -1274,6 +1312,10 @@ __global__ void __launch_bounds__(kMaxThreads)
   const float least = unordered(thr.key);
   const char* row = static_cast<const char*>(p.logits) +
                     m * p.s_row * (BF16 ? 2 : 4);
+  if (mode == kSummed) {
+    if (wave == 0) pick_token<BF16, VEC>(p, work, wt, thr, q.u, m, G);
+    return;
+  }
 #pragma unroll 1
   for (int g = part.first + wave; g < part.end; g += kMaxThreads / 64) {
     uint64_t sum = 0;
@@ -1285,31 +1327,10 @@ __global__ void __launch_bounds__(kMaxThreads)
           [&](float x) { sum += wt.of(x); });
       sum = wave_sum64(sum);
     }
-    if (lane == 0) work.sums[g] = sum;
+    if (lane == 0) shared_store(&work.sums[g], sum);
   }
-}
-
-template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kRowThreads)
-    kda_pick_kernel(SampleParams p, int G, int places) {
-  extern __shared__ __align__(16) char smem[];
-  RowSmem& sm = *reinterpret_cast<RowSmem*>(smem);
-  const int m = blockIdx.x, tid = threadIdx.x;
-  const Work work(p, m, G);
-  if (work.plan->mode != kKept && work.plan->mode != kSummed) return;
-  const Threshold thr{work.plan->key, work.plan->index};
-  const int b = request_of_row(p, m, tid & 63);
-  if (b < 0) return;
-  const Params q(p, b, m);
-  for (int g = tid; g < G; g += kRowThreads) sm.group[g] = work.sums[g];
-  fill_table(sm.table);
-  __syncthreads();
-  Weights wt;
-  wt.init(sm.table, work.plan->top, q.T, q.min_p, places);
-  const Row<BF16, VEC> row{static_cast<const char*>(p.logits) +
-                               m * p.s_row * (BF16 ? 2 : 4),
-                           p.V, G, sm};
-  pick_token<BF16, VEC>(p, row, wt, thr, q.u, m);
+  if (last_of(&work.plan->arrived[1], per_row) && wave == 0)
+    pick_token<BF16, VEC>(p, work, wt, thr, q.u, m, G);
 }
 
 // One thread per request: leading rows whose token is the window's next one.
@@ -1341,16 +1362,14 @@ int launch_rows(const SampleParams& p, int G, int places,
   launch_kernel(kda_row_sums_kernel<BF16, VEC>,
                 dim3(uint32_t(p.M) * uint32_t(sums_row)), dim3(kMaxThreads), 0,
                 stream, p, G, sums_row, sums_wg, places);
-  launch_kernel(kda_plan_kernel<BF16, VEC>, dim3(p.M), dim3(64), 0, stream, p,
-                G, places);
-  launch_kernel(kda_gather_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
-                stream, p, G, per_row);
-  launch_kernel(kda_list_kernel<BF16, VEC>, dim3(p.M), dim3(kRowThreads),
-                sizeof(RowSmem), stream, p, G, places);
+  if (p.top_k || p.top_p) {
+    launch_kernel(kda_gather_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
+                  stream, p, G, per_row);
+    launch_kernel(kda_list_kernel<BF16, VEC>, dim3(p.M), dim3(kRowThreads),
+                  sizeof(RowSmem), stream, p, G, places);
+  }
   launch_kernel(kda_kept_sums_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
                 stream, p, G, per_row, places);
-  launch_kernel(kda_pick_kernel<BF16, VEC>, dim3(p.M), dim3(kRowThreads),
-                sizeof(RowSmem), stream, p, G, places);
   return int(hipGetLastError());
 }
 
