@@ -271,8 +271,9 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
   const int tg = F::CP == 64 ? uniform(tid / F::CP) : tid / F::CP;
   const int64_t HD = int64_t(y.H) * D, ch = int64_t(h) * D + 2 * cp;
   const bool conv = !(y.flags & kNoConv);
-  // Every row index is clamped into the request and the value dropped
-  // afterwards: the loads then stand in one block, all in flight together.
+  // Every row index is clamped into the request: the loads then stand in one
+  // block, all in flight together.  What comes of rows behind the request is
+  // dropped at the end (no row before them uses it).
   const int tk = tg * F::NTK;
   typename P2::T raw[3][F::NTK + 3], rawg[F::NTK];
   const T* xcol = static_cast<const T*>(y.mixed_qkv) + ch;
@@ -332,9 +333,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
     float x[F::NTK + 3][2];
 #pragma unroll
     for (int i = 0; i < F::NTK + 3; ++i) {
-      const bool in = tk + i - 3 < n;
-      x[i][0] = in ? P2::lo(raw[part][i]) : 0.0f;
-      x[i][1] = in ? P2::hi(raw[part][i]) : 0.0f;
+      x[i][0] = P2::lo(raw[part][i]);
+      x[i][1] = P2::hi(raw[part][i]);
     }
     if (conv) {
       if (head) {
@@ -392,23 +392,27 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
   // |q|^2 and |k|^2 of the thread's tokens over the lanes of their row
   float nq[F::NTK], nk[F::NTK];
   row_norms<F::CP, F::NTK>(val[0], val[1], nq, nk);
+  // rows behind the request vanish: k = q = v = 0, decay 1
+  if (n < C) {
+#pragma unroll
+    for (int i = 0; i < F::NTK; ++i)
+      if (tk + i >= n) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          val[0][i][e] = val[1][i][e] = val[2][i][e] = gate[i][e] = 0.0f;
+        nq[i] = nk[i] = 0.0f;
+      }
+  }
 #pragma unroll
   for (int i = 0; i < F::NTK; ++i) {
     const int t = tk + i;
-    const bool in = t < n;
-    const float g0 = gate[i][0], g1 = gate[i][1];
     const float fq = nq[i] * (1.0f / sqrtf(float(D)));
-    // rows behind the request vanish: k = q = v = 0, decay 1
     *reinterpret_cast<float2*>(&m.q[t][2 * cp]) =
-        in ? make_float2(val[0][i][0] * fq, val[0][i][1] * fq)
-           : make_float2(0, 0);
+        make_float2(val[0][i][0] * fq, val[0][i][1] * fq);
     *reinterpret_cast<float2*>(&m.k[t][2 * cp]) =
-        in ? make_float2(val[1][i][0] * nk[i], val[1][i][1] * nk[i])
-           : make_float2(0, 0);
+        make_float2(val[1][i][0] * nk[i], val[1][i][1] * nk[i]);
     *reinterpret_cast<float2*>(&m.z[t][2 * cp]) =
-        in ? make_float2(exp_(g0), exp_(g1)) : make_float2(1, 1);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) val[2][i][e] = in ? val[2][i][e] : 0.0f;
+        make_float2(exp_(gate[i][0]), exp_(gate[i][1]));
   }
   // V as the second kernel's accumulators hold it
   char* vf = work + W::v;
@@ -443,32 +447,38 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
 
   // ---- products of decays from the sub-block's start, and to its end ----
   // a thread's channel, sub-block and, at 512 threads, half of its tokens
-  constexpr int HV = F::NT >= 4 * D ? 2 : 1;
+  constexpr int HV = F::NT >= 4 * D && 2 * D % 64 == 0 ? 2 : 1;
   constexpr int TK = kSub / HV;
-  const int pc = tid % D, pb = tid / D % 2, t1 = tid / (2 * D) * TK;
+  const int pc = tid % D, pb = tid / D % 2;
+  const int half = HV == 2 ? uniform(tid / (2 * D)) : 0;   // of whole waves
+  const int t1 = half * TK;
   const bool scans = tid < 2 * D * HV;
   float pre[TK], suf[TK], full = 1.0f;
   if (scans) {
     float d[kSub];
 #pragma unroll
     for (int i = 0; i < kSub; ++i) d[i] = m.z[pb * kSub + i][pc];
-    float f = 1.0f, l = 1.0f;
-    // (selected with constant indexes, so that d stays in registers)
+    // products over the thread's tokens and, from there on, over the others
+    const auto scan = [&](auto first) {
+      constexpr int t0 = decltype(first)::value;
+      float f = 1.0f, l = 1.0f;
 #pragma unroll
-    for (int i = 0; i < kSub; ++i) {
-      f *= d[i];
+      for (int i = 0; i < t0; ++i) f *= d[i];
 #pragma unroll
-      for (int v = 0; v < HV; ++v)
-        if (i / TK == v && t1 == v * TK) pre[i % TK] = f;
-    }
+      for (int i = 0; i < TK; ++i) pre[i] = f *= d[t0 + i];
 #pragma unroll
-    for (int i = kSub - 1; i >= 0; --i) {
+      for (int i = kSub - 1; i >= t0 + TK; --i) l *= d[i];
+      full = f * l;
 #pragma unroll
-      for (int v = 0; v < HV; ++v)
-        if (i / TK == v && t1 == v * TK) suf[i % TK] = l;
-      l *= d[i];
-    }
-    full = f;
+      for (int i = TK - 1; i >= 0; --i) {
+        suf[i] = l;
+        l *= d[t0 + i];
+      }
+    };
+    if (half == 0)
+      scan(std::integral_constant<int, 0>{});
+    else
+      scan(std::integral_constant<int, HV == 2 ? TK : 0>{});
   }
   // Within a sub-block, e^(G_i - G_j) = (P_i / P_end) Q_j as long as no P
   // leaves the fp32 range (down to 1e-37: 16 tokens of log-decay -5 each stay
@@ -741,7 +751,8 @@ __device__ __forceinline__ float max_abs(const f4& a, float m) {
 // One wave's load of 64 x 16 bytes from global memory straight into LDS, in
 // lane order (no register holds the data, so any number may be in flight).
 // The completion is waited for by hand (wait_vm): the compiler does not see
-// these loads and keeps no count of them.
+// these loads and keeps no count of them.  (m0 is a reserved register, which
+// the compiler sets anew before each use of its own.)
 __device__ __forceinline__ void load_lds(const char* base, uint32_t off,
                                          uint32_t lds) {
   asm volatile(
@@ -750,7 +761,7 @@ __device__ __forceinline__ void load_lds(const char* base, uint32_t off,
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(lds), "v"(off), "s"(base)
-      : "memory", "m0");
+      : "memory");
 }
 
 // Wait until at most N of this wave's global memory operations are under way
