@@ -387,9 +387,9 @@ typedef struct {
    exactly as in the verify:
      c = beta (v - S diag(e^g) k_hat),  S' = S diag(e^g) + c k_hat^T,
      out = S' q.
-   The new state goes to the final slot (NULL: in place); with the fused conv, the newest three raw
-   inputs go to entries [0, 3) of the final slot's conv state, other entries
-   stay.  A request whose state slot is null gets +0.0 outputs and nothing
+   The new state goes to the final slot (NULL: in place); with the fused conv,
+   the newest three raw inputs go to entries [0, 3) of the final slot's conv
+   state, other entries stay.  A request whose state slot is null gets +0.0 outputs and nothing
    else; one whose final slot alone is null gets its output and no state. */
 typedef struct {
   kda_tensor mixed_qkv;    /* act [B, 3HD] */
@@ -483,7 +483,8 @@ typedef struct {
    draft_tokens[s .. e) (s, e from query_start_loc); row m's token is checked
    against draft_tokens[m + 1], and num_accepted[b] = 1 + the number of
    leading matches, in [1, e - s] (0 for an empty window): what
-   kda_commit_plan takes as num_accepted_tokens.  next_tokens[b] is the
+   kda_commit_plan takes as num_accepted_tokens (with request_indices it reads
+   that array by request row, this one is in batch order).  next_tokens[b] is the
    token of row s + num_accepted[b] - 1 (-1 for an empty window). */
 typedef struct {
   kda_tensor logits;              /* F32 or BF16 [M, V], rows contiguous */
@@ -498,7 +499,9 @@ typedef struct {
   int32_t* num_accepted;          /* [batch] outputs, given iff draft_tokens */
   int32_t* next_tokens;
   void* workspace;                /* device, 16-byte aligned, at least
-                                     kda_sample_workspace_size(M, V) bytes */
+                                     kda_sample_workspace_size(M, V) bytes;
+                                     not shared by launches in flight
+                                     together */
   int64_t workspace_bytes;
   int32_t batch;
   int32_t pad_;
@@ -636,8 +639,9 @@ int kda_reset_counter(int32_t* counter, int32_t n, void* stream);
 /* Kernel timing without a profiler, for callers that measure each kernel's
    own duration (an event recorded on the stream around a launch also counts
    the gap the event's own marker adds before the next dispatch).  Arms the
-   calling thread: the next `launches` verify, commit, plan or compaction
-   kernels that library calls on this thread launch are dispatched with
+   calling thread: the next `launches` kernels that library calls on this
+   thread launch (a prefill takes two, the step tables two or, without
+   tokens, one, sampling three to six) are dispatched with
    hipExtLaunchKernel, `start_event` (a hipEvent_t, may be NULL) recording
    the start of the first of them and `stop_event` (may be NULL) the end of
    the last.  The counter-clearing kernels (kda_reset_counter, the first

@@ -18,7 +18,7 @@ struct LaunchTiming {
 };
 LaunchTiming& launch_timing();
 
-// Launch of a verify, commit, plan or compaction kernel.
+// Launch of a kernel (all but the counter resets).
 template <typename... Args, typename F>
 inline void launch_kernel(F kernel, dim3 grid, dim3 block, uint32_t shmem,
                           hipStream_t stream, Args... args) {

@@ -46,7 +46,7 @@ namespace {
 constexpr int kGroup = 512;          // logits of a group
 constexpr int kMaxGroups = 2048;     // V up to 2^20
 constexpr int kMaxThreads = 256;     // split kernels
-constexpr int kPerWg = 4 * 4;        // groups per workgroup of the split kernels
+constexpr int kPerWg = 4 * 4;        // their groups per workgroup
 constexpr int kRowThreads = 512;     // list kernel
 constexpr int kWaves = kRowThreads / 64;
 constexpr int kList = 4096;          // entries of the sorted list
@@ -202,7 +202,8 @@ __device__ __forceinline__ double uniform_double(double v) {
 // whose last binary place is 1 to round.
 struct Weights {
   const double* table;
-  double m, c, most, d_min_p;   // steps per unit; clamp; steps that min-p allows
+  double m, c;                  // maximum; steps per unit
+  double most, d_min_p;         // clamp; steps that min-p allows
   int s;                        // binary places
   __device__ __forceinline__ void init(const double* tab, float top, float T,
                                        float min_p, int places) {
@@ -532,7 +533,8 @@ __device__ __forceinline__ Found find_first(const uint64_t* a, int n,
   const int l = __ffsll((unsigned long long)in) - 1;
   const uint64_t base = __shfl((unsigned long long)(upto - sum), l);
   const int first = l * own;
-  const uint64_t v = lane < own && first + lane < n ? shared_load(a + first + lane) : 0;
+  const uint64_t v =
+      lane < own && first + lane < n ? shared_load(a + first + lane) : 0;
   const uint64_t u = base + wave_scan(v);
   const int i = __ffsll((unsigned long long)__ballot(u >= target)) - 1;
   f.at = first + i;
@@ -560,9 +562,9 @@ __device__ __forceinline__ uint64_t row_scan(uint64_t v, uint64_t* red,
   return base + v;
 }
 
-// First index i of a(0 .. n - 1) (n <= kPer * kRowThreads) whose inclusive prefix
-// sum reaches goal(total of a); sm.found = i (or -1), sm.before = the sum
-// before it, sm.value = a(i).  Returns the total.
+// First index i of a(0 .. n - 1) (n <= kPer * kRowThreads) whose inclusive
+// prefix sum reaches goal(total of a); sm.found = i (or -1), sm.before = the
+// sum before it, sm.value = a(i).  Returns the total.
 template <int kPer, class A, class Goal>
 __device__ __forceinline__ uint64_t find_prefix(RowSmem& sm, A a, int n,
                                                 Goal goal) {
@@ -793,7 +795,8 @@ __device__ __forceinline__ Threshold search(const Row<BF16, VEC>& row,
       atomicAdd((unsigned long long*)&sm.group[i / kGroup], 1ull);
   });
   __syncthreads();
-  find_prefix<kPer2k>(sm, [&](int i) { return sm.group[i]; }, row.G, [&](uint64_t) { return rank; });
+  find_prefix<kPer2k>(sm, [&](int i) { return sm.group[i]; }, row.G,
+                      [&](uint64_t) { return rank; });
   const int g = sm.found;
   const uint64_t seen = sm.before;
   if (threadIdx.x == 0) sm.pick = row.V - 1;
