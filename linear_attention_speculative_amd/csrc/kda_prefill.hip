@@ -27,9 +27,9 @@
 //   to LDS takes a wave some 50 cycles, which the others then do not spend.
 //
 // What bounds them, on 8192 tokens of 32 heads of D = 128 (bf16): the chunk
-// kernel, 232 us, its vector arithmetic (busy 67% of the time; 0.13 GB read
-// beyond the caches and 0.5 GB written are 125 us of HBM); the state kernel,
-// 370 us, the length of one chunk's chain of products, 1.45 us times 256
+// kernel, 230 us, its vector arithmetic (busy 67% of the time) and memory (0.27
+// GB read and 0.52 GB written: 160 us at a copy's rate); the state kernel, 370
+// us, the length of one chunk's chain of products, 1.45 us times 256
 // chunks, with one wave to each SIMD that has any.  16 prompts of 16000
 // tokens together: 430 and 268 us.
 //
