@@ -1382,7 +1382,10 @@ int64_t sample_work_bytes(int64_t M, int64_t V) {
   if (M < 0 || V < 1 || M > 0x7fffffff || V > int64_t(kMaxGroups) * kGroup)
     return 0;
   const int64_t G = (V + kGroup - 1) / kGroup;
-  if (M * ((G + kPerWg - 1) / kPerWg) > 0x7fffffff) return 0;
+  // work items of the launches: 256 per kPerWg groups, 512 per row
+  if (M * ((G + kPerWg - 1) / kPerWg) > 0xffffffff / kMaxThreads ||
+      M > 0xffffffff / kRowThreads)
+    return 0;
   return Work::bytes(M, G) + 256;
 }
 

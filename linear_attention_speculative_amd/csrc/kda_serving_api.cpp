@@ -12,6 +12,7 @@ using namespace kda::host;
 namespace {
 
 constexpr int64_t kI32Max = 0x7fffffff;
+constexpr int64_t kMaxThreads = 0xffffffff;   // work items of a launch
 
 // The fields that the two layer argument blocks share.
 struct LayerView {
@@ -163,6 +164,8 @@ int plan_layer(const LayerView& a, bool conv, kda::LayerParams* p, int* D_out,
     if (st < 0 || st > kI32Max)
       return fail(KDA_E_LAYOUT, "a tensor stride is negative or exceeds 2^31");
   // Rows that writes would share (a broadcast view) cannot hold results.
+  if (conv && ((N > 1 && cs.stride[0] == 0) || s_chan == 0 || s_tok == 0))
+    return fail(KDA_E_LAYOUT, "the conv state's entries overlap");
   if (T > 1 && a.out.stride[0] < HD)
     return fail(KDA_E_LAYOUT, "out's rows overlap");
   if (N > 1 && S.stride[0] < H * D * D)
@@ -228,7 +231,11 @@ int64_t prefill_bytes(int64_t T, int64_t B, int64_t H, int64_t D,
       B > kI32Max || H > kI32Max || B * H > kI32Max)
     return 0;
   const int64_t slots = kda::prefill_slots(T, B);
-  if (slots > kI32Max / H) return 0;
+  // launches of up to 512 threads per (chunk slot, head), and of up to 320
+  // per (request, head, 16 rows)
+  if (slots > kMaxThreads / 512 / H ||
+      (B * H + 7) / 8 * 8 * (D / 16) > kMaxThreads / 320)
+    return 0;
   return slots * H * kda::prefill_slot_bytes(int(D), out_f32) +
          (B + 4) / 4 * 16;     // the order of the requests, behind the slots
 }
@@ -241,9 +248,7 @@ int plan_prefill(const kda_prefill_args* a, bool conv, PrefillPlan* plan) {
   plan->noop = a->batch == 0 || T == 0;
   const int64_t need = prefill_bytes(T, a->batch, p.y.H, plan->D,
                                      a->out.dtype == KDA_F32);
-  // the second kernel's grid: a wave per (request, head, 16 rows)
-  if (need == 0 ||
-      (int64_t(a->batch) * p.y.H + 7) / 8 * 8 * (plan->D / 16) > kI32Max)
+  if (need == 0)
     return fail(KDA_E_CAPACITY, "tokens, requests and heads exceed the grid");
   if (!plan->noop) {
     if (!a->query_start_loc)
@@ -299,6 +304,9 @@ int plan_decode(const kda_decode_args* a, bool conv, DecodePlan* plan) {
                 "a decode step takes one row per request (%lld rows, %d "
                 "requests)",
                 (long long)T, a->batch);
+  // up to 512 threads per (request, head)
+  if (T * plan->p.y.H > kMaxThreads / 512)
+    return fail(KDA_E_CAPACITY, "requests and heads exceed the grid");
   if (a->final_state_indices && !aligned(a->final_state_indices, 4))
     return fail(KDA_E_UNALIGNED, "metadata pointers must be 4-byte aligned");
   plan->p.final_slots = a->final_state_indices;

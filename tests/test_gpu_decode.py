@@ -167,6 +167,8 @@ def test_decode_checks():
         (dict(out=ok["out"][:1].expand(3, -1)), _abi.KDA_E_LAYOUT),
         (dict(conv_state=ok["conv_state"][:, :, :5]),
          _abi.KDA_E_UNSUPPORTED),
+        (dict(conv_state=ok["conv_state"][:1].expand(6, -1, -1)),
+         _abi.KDA_E_LAYOUT),
         (dict(conv_weight=ok["conv_weight"][:, :3]), _abi.KDA_E_SHAPE),
         (dict(spec_query_len=17), _abi.KDA_E_UNSUPPORTED),
         (dict(dt_bias=ok["dt_bias"][:, :8]), _abi.KDA_E_SHAPE),
@@ -184,6 +186,11 @@ def test_decode_checks():
     assert lib.kda_check_decode(a) == _abi.KDA_E_ARG
     a.batch = -1
     assert lib.kda_check_decode(a) == _abi.KDA_E_ARG
+    a = kda.decode_args(**ok)               # work items of a launch past 2^32
+    a.batch = (1 << 23) // 2
+    for t in (a.mixed_qkv, a.raw_gate, a.raw_beta, a.out):
+        t.shape[0] = a.batch
+    assert lib.kda_check_decode(a) == _abi.KDA_E_CAPACITY
 
 
 def test_decode_binding_refusals():

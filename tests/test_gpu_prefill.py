@@ -136,6 +136,30 @@ def test_null_slots_and_rows_behind():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_non_finite_inputs_stay_in_their_request(act):
+    """A NaN or infinite input spoils its own request from its chunk on: the
+    chunks before it and the other requests stay as without it."""
+    lens, slots = [40, 100, 70], [1, 2, 3]
+    qsl = np.concatenate([[0], np.cumsum(lens)])
+    a = make_layer(210, 5, 2, 64, 3, act=act, seed=61)
+    b = {k: v.clone() if isinstance(v, torch.Tensor) else v
+         for k, v in a.items()}
+    t = 40 + 70                           # token 70 of the second request
+    b["mixed_qkv"][t, :128] = float("nan")
+    b["raw_gate"][t + 3, 5] = float("nan")
+    b["mixed_qkv"][t + 9, -3] = float("inf")
+    run(a, qsl, slots, None)
+    run(b, qsl, slots, None)
+    whole = np.r_[0:40 + 64, 140:210]     # chunks of 32 before token 70
+    assert torch.equal(a["out"][whole], b["out"][whole])
+    for s in (1, 3):
+        assert torch.equal(a["state"][s], b["state"][s])
+        assert torch.equal(a["conv_state"][s], b["conv_state"][s])
+    assert bool(torch.isnan(b["out"][t:140]).any())
+
+
+@pytest.mark.gpu
 def test_in_place_continuation_in_pieces():
     """A prompt in pieces through one slot, the pieces continuing in place,
     equals the whole prompt."""
@@ -288,6 +312,10 @@ def test_prefill_checks():
         (dict(conv_state=ok["conv_state"].bfloat16()), _abi.KDA_E_DTYPE),
         (dict(conv_state=ok["conv_state"][:5]), _abi.KDA_E_SHAPE),
         (dict(spec_query_len=0), _abi.KDA_E_UNSUPPORTED),
+        (dict(conv_state=ok["conv_state"][:1].expand(6, -1, -1)),
+         _abi.KDA_E_LAYOUT),
+        (dict(conv_state=ok["conv_state"][:, :, :1].expand(-1, -1, 6)),
+         _abi.KDA_E_LAYOUT),
     ]
     for over, code in bad:
         assert kda.check_prefill(**dict(ok, **over)) == code, over.keys()
@@ -317,6 +345,10 @@ def test_prefill_binding_refusals():
         kda.prefill_workspace_size(10, 1, 2, 48, torch.bfloat16)
     with pytest.raises(ValueError):
         kda.prefill_workspace_size(-1, 1, 2, 64, torch.bfloat16)
+    with pytest.raises(ValueError):       # work items of a launch past 2^32
+        kda.prefill_workspace_size(1 << 24, 1, 32, 64, torch.bfloat16)
+    with pytest.raises(ValueError):
+        kda.prefill_workspace_size(1 << 20, 1 << 20, 32, 128, torch.bfloat16)
     with pytest.raises(ValueError):
         kda.prefill_workspace_size(10, 1, 2, 64, torch.float16)
     with pytest.raises(ValueError, match="conv_weight|conv_state"):

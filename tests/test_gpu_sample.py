@@ -363,6 +363,8 @@ def test_sample_binding_refusals():
         kda.check_sample(**dict(ok, top_p=torch.zeros(1)))
     with pytest.raises(ValueError):
         kda.sample_workspace_size(4, (1 << 20) + 1)
+    with pytest.raises(ValueError):       # work items of a launch past 2^32
+        kda.sample_workspace_size(1 << 23, 40)
 
 
 def test_oracle_sampling_closed_forms():
