@@ -22,15 +22,13 @@ from .ops import (_DT, _pack_format, _ptr, _raise, _tensor_values)
 def _launch(entry, args, kwargs, stream) -> None:
     """Calls `entry` with the tensors' GPU current, on that GPU's current
     stream or the one given."""
-    index = None
-    for t in kwargs.values():
-        if isinstance(t, torch.Tensor) and t.get_device() != index:
-            if index is not None:
-                raise ValueError("tensors on different devices (the index "
-                                 f"of one is {index}, of another "
-                                 f"{t.get_device()})")
-            index = t.get_device()
-    if index is None or index < 0:
+    on = {t.get_device() for t in kwargs.values()
+          if isinstance(t, torch.Tensor)}
+    if len(on) > 1:
+        raise ValueError(f"tensors on different devices (indexes {on}, -1 "
+                         "being the host)")
+    index = on.pop() if on else -1
+    if index < 0:
         raise ValueError("the tensors must be on a GPU")
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(index)
