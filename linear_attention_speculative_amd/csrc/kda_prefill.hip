@@ -228,16 +228,22 @@ __device__ __forceinline__ void rank_request(const PrefillParams& p, int b,
                                              ChunkSmem<D>& m) {
   const int2 mine = b < 0 ? make_int2(0, 0) : token_range(p, b);
   const int len = mine.y - mine.x;
+  // counted by waves: one LDS atomic each (by lanes, all on one address, they
+  // took 5 us)
   int before = 0, all = 0;
-  for (int i = threadIdx.x; i < p.y.B; i += ChunkCfg<D>::NT) {
-    const int2 r = token_range(p, i);
+  for (int i0 = threadIdx.x & ~63; i0 < p.y.B; i0 += ChunkCfg<D>::NT) {
+    const int i = i0 + int(threadIdx.x & 63);
+    const bool in = i < p.y.B;
+    const int2 r = token_range(p, in ? i : 0);
     const int n = r.y - r.x;
-    before += n > len || (n == len && i < b);
-    all += n > 0;
+    before += __popcll(__ballot(in && (n > len || (n == len && i < b))));
+    all += __popcll(__ballot(in && n > 0));
   }
   __syncthreads();           // the counters are cleared
-  atomicAdd(&m.before, before);
-  atomicAdd(&m.all, all);
+  if ((threadIdx.x & 63) == 0) {
+    atomicAdd(&m.before, before);
+    atomicAdd(&m.all, all);
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
     if (b >= 0) p.order[m.before] = b;
