@@ -643,7 +643,7 @@ int kda_reset_counter(int32_t* counter, int32_t n, void* stream);
    the gap the event's own marker adds before the next dispatch).  Arms the
    calling thread: the next `launches` kernels that library calls on this
    thread launch (a prefill takes two, the step tables two or, without
-   tokens, one, sampling three to six) are dispatched with
+   tokens, one, sampling three to eight) are dispatched with
    hipExtLaunchKernel, `start_event` (a hipEvent_t, may be NULL) recording
    the start of the first of them and `stop_event` (may be NULL) the end of
    the last.  The counter-clearing kernels (kda_reset_counter, the first

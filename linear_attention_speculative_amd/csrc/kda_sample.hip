@@ -18,26 +18,28 @@
 //   kda_row_sums_kernel, only for rows that need it: with top-p alone the
 //   weights by bins of 1/32 octave of d, with more for top-k than groups that
 //   hold any logit counts by bins, without either the weights of each group.
-//   One wave of the last workgroup of a row then decides which logits matter.
-//   Greedy rows end here.  With top-k <= groups, the k-th largest group maximum
-//   bounds the k-th largest value from below; with larger k the bin at the
-//   border of the counts does.  Top-p alone needs only the bin that holds its
-//   border, and so finds the threshold pair however many logits are kept.
+//   plan_row, one wave a row, then decides which logits matter.  Greedy rows
+//   end here.  With top-k <= groups, the k-th largest group maximum bounds the
+//   k-th largest value from below; with larger k the bin at the border of the
+//   counts does.  Top-p alone needs only the bin that holds its border, and so
+//   finds the threshold pair however many logits are kept.
 //   kda_gather_kernel lists those logits, reading again only groups whose
 //   maximum reaches the bound.
 //   kda_list_kernel, one workgroup a row, sorts the list, cuts it and takes the
 //   token.  What no list holds (thousands of ties, or of top-k) it leaves to a
 //   radix search of any size.
 //   kda_kept_sums_kernel, only for rows that kept more than a list: the kept
-//   weights of each group, and by one wave of the row's last workgroup the
-//   token from them.
+//   weights of each group; pick_token, one wave a row, the token from them.
 //
-// The last workgroups' work stands in place of two kernels of its own: 33 rows
-// take 57 us a call against 62.
+// plan_row and pick_token have kernels of their own where there are many rows.
+// With few, whose launches count, one wave of the last workgroup to finish a
+// row's sums does their work (33 rows: 57 us a call against 62; 640 rows with
+// top-k 1000: 104 us for sums and plans against 73, the workgroups' places
+// being held meanwhile).
 //
 // In all, 640 of 1024 window rows of 131072 bf16 logits with mixed parameters:
-// 28 us for the maxima (6 TB/s), 57 sums and plans (fp64 weights of the rows
-// with top-p alone), 17 lists, 34 sorts, 24 kept sums, 5 acceptance.
+// 28 us for the maxima (6 TB/s), 56 sums and plans (fp64 weights of the rows
+// with top-p alone), 16 lists, 33 sorts, 26 kept sums and picks, 5 acceptance.
 #include "kda_serving.hpp"
 
 namespace kda {
@@ -265,12 +267,18 @@ struct Params {
   int k;
   bool greedy, need_k, need_p;
   __device__ __forceinline__ Params(const SampleParams& p, int b, int m) {
-    T = p.temperature && p.temperature[b] == p.temperature[b]
-            ? p.temperature[b] : 1.0f;
-    k = p.top_k ? p.top_k[b] : 0;
-    top_p = p.top_p && p.top_p[b] < 1.0f ? p.top_p[b] : 1.0f;
-    min_p = p.min_p && p.min_p[b] > 0.0f ? p.min_p[b] : 0.0f;
-    u = p.uniform[m] > 0.0f ? p.uniform[m] : 0.0f;
+    // five loads under way together, of some valid place for what is absent
+    const float* any = p.uniform + m;
+    const float t = *(p.temperature ? p.temperature + b : any);
+    const int n = *(p.top_k ? p.top_k + b : reinterpret_cast<const int*>(any));
+    const float tp = *(p.top_p ? p.top_p + b : any);
+    const float mp = *(p.min_p ? p.min_p + b : any);
+    const float uu = *any;
+    T = p.temperature && t == t ? t : 1.0f;
+    k = p.top_k ? n : 0;
+    top_p = p.top_p && tp < 1.0f ? tp : 1.0f;
+    min_p = p.min_p && mp > 0.0f ? mp : 0.0f;
+    u = uu > 0.0f ? uu : 0.0f;
     greedy = T <= 0.0f || k == 1 || top_p <= 0.0f;
     need_k = k > 0 && k < p.V;
     need_p = top_p < 1.0f;
@@ -997,7 +1005,7 @@ __device__ __forceinline__ void plan_row(const SampleParams& p,
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads)
     kda_row_sums_kernel(SampleParams p, int G, int per_row, int per_wg,
-                        int places) {
+                        int places, bool plans) {
   __shared__ double table[kSteps];
   __shared__ unsigned long long mass[kBins];
   __shared__ float kept[kMaxThreads / 64][kGroup];
@@ -1007,15 +1015,16 @@ __global__ void __launch_bounds__(kMaxThreads)
   const int b = request_of_row(p, m, lane);
   const Work work(p, m, G);
   if (b < 0) {
-    if (part.chosen && threadIdx.x == 0) work.plan->mode = kDecided;
+    if (plans && part.chosen && threadIdx.x == 0) work.plan->mode = kDecided;
     return;
   }
   const Params q(p, b, m);
+  if (q.greedy && !plans) return;
   const bool counts = q.need_k;
   const int live = counts ? live_groups(work.gmax, G, kLowestKey) : G;
   const float top = row_max(work.gmax, G);
   if (q.greedy || (counts && q.k <= live) || top == -__builtin_inff()) {
-    if (part.chosen && wave == 0)
+    if (plans && part.chosen && wave == 0)
       plan_row<BF16, VEC>(p, work, q, m, G, places);
     return;
   }
@@ -1074,8 +1083,21 @@ __global__ void __launch_bounds__(kMaxThreads)
         atomicAdd((unsigned long long*)&work.sums[i], (unsigned long long)add);
     }
   }
-  if (last_of(&work.plan->arrived[0], per_row) && wave == 0)
+  if (plans && last_of(&work.plan->arrived[0], per_row) && wave == 0)
     plan_row<BF16, VEC>(p, work, q, m, G, places);
+}
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(64)
+    kda_plan_kernel(SampleParams p, int G, int places) {
+  const int m = blockIdx.x;
+  const Work work(p, m, G);
+  const int b = request_of_row(p, m, threadIdx.x);
+  if (b < 0) {
+    if (threadIdx.x == 0) work.plan->mode = kDecided;
+    return;
+  }
+  plan_row<BF16, VEC>(p, work, Params(p, b, m), m, G, places);
 }
 
 // The token whose running weight passes u, by one wave: from the weights of
@@ -1110,10 +1132,11 @@ __global__ void __launch_bounds__(kMaxThreads)
   const int m = part.m;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const Work work(p, m, G);
-  if (work.plan->mode != kGather) return;
+  const Plan plan = *work.plan;
+  if (plan.mode != kGather) return;
   // as floats; without a last key, one that nothing compares with
-  const uint32_t last = work.plan->last;
-  const float x_first = unordered(work.plan->first);
+  const uint32_t last = plan.last;
+  const float x_first = unordered(plan.first);
   const float x_last = last == 0xffffffffu ? __builtin_nanf("")
                                            : unordered(last);
   const auto in = [&](float x) { return x >= x_first && !(x >= x_last); };
@@ -1293,8 +1316,8 @@ __global__ void __launch_bounds__(kRowThreads)
 // token, or that of a row whose sums are there.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kMaxThreads)
-    kda_kept_sums_kernel(SampleParams p, int G, int per_row,
-                         int places) {
+    kda_kept_sums_kernel(SampleParams p, int G, int per_row, int places,
+                         bool picks) {
   __shared__ double table[kSteps];
   __shared__ float kept[kMaxThreads / 64][kGroup];
   const Part part(G, per_row);
@@ -1302,15 +1325,16 @@ __global__ void __launch_bounds__(kMaxThreads)
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const Work work(p, m, G);
   const Mode mode = work.plan->mode;
-  if (mode != kKept && (mode != kSummed || !part.chosen)) return;
-  const Threshold thr{work.plan->key, work.plan->index};
+  if (mode != kKept && !(picks && mode == kSummed && part.chosen)) return;
+  const Plan plan = *work.plan;
+  const Threshold thr{plan.key, plan.index};
   const int b = request_of_row(p, m, lane);
   if (b < 0) return;
   const Params q(p, b, m);
   fill_table(table);
   __syncthreads();
   Weights wt;
-  wt.init(table, work.plan->top, q.T, q.min_p, places);
+  wt.init(table, plan.top, q.T, q.min_p, places);
   // (the threshold is never below what min-p allows)
   const float least = unordered(thr.key);
   const char* row = static_cast<const char*>(p.logits) +
@@ -1332,8 +1356,27 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
     if (lane == 0) shared_store(&work.sums[g], sum);
   }
-  if (last_of(&work.plan->arrived[1], per_row) && wave == 0)
+  if (picks && last_of(&work.plan->arrived[1], per_row) && wave == 0)
     pick_token<BF16, VEC>(p, work, wt, thr, q.u, m, G);
+}
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(64)
+    kda_pick_kernel(SampleParams p, int G, int places) {
+  __shared__ double table[kSteps];
+  const int m = blockIdx.x;
+  const Work work(p, m, G);
+  const Plan plan = *work.plan;
+  if (plan.mode != kKept && plan.mode != kSummed) return;
+  const int b = request_of_row(p, m, threadIdx.x);
+  if (b < 0) return;
+  const Params q(p, b, m);
+  fill_table(table);
+  __syncthreads();
+  Weights wt;
+  wt.init(table, plan.top, q.T, q.min_p, places);
+  pick_token<BF16, VEC>(p, work, wt, Threshold{plan.key, plan.index}, q.u, m,
+                        G);
 }
 
 // One thread per request: leading rows whose token is the window's next one.
@@ -1360,11 +1403,15 @@ int launch_rows(const SampleParams& p, int G, int places,
   // half as many workgroups, each with bins of its own, for many rows (640
   // rows with top-k 1000 of 131072: 64 us against 97; one row with top-p: 12
   // as it is, 17 with half)
-  const int sums_wg = p.M >= 128 ? 2 * kPerWg : kPerWg;
+  const bool many = p.M >= 128;
+  const int sums_wg = many ? 2 * kPerWg : kPerWg;
   const int sums_row = (G + sums_wg - 1) / sums_wg;
   launch_kernel(kda_row_sums_kernel<BF16, VEC>,
                 dim3(uint32_t(p.M) * uint32_t(sums_row)), dim3(kMaxThreads), 0,
-                stream, p, G, sums_row, sums_wg, places);
+                stream, p, G, sums_row, sums_wg, places, !many);
+  if (many)
+    launch_kernel(kda_plan_kernel<BF16, VEC>, dim3(p.M), dim3(64), 0, stream,
+                  p, G, places);
   if (p.top_k || p.top_p) {
     launch_kernel(kda_gather_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
                   stream, p, G, per_row);
@@ -1372,7 +1419,10 @@ int launch_rows(const SampleParams& p, int G, int places,
                   sizeof(RowSmem), stream, p, G, places);
   }
   launch_kernel(kda_kept_sums_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
-                stream, p, G, per_row, places);
+                stream, p, G, per_row, places, !many);
+  if (many)
+    launch_kernel(kda_pick_kernel<BF16, VEC>, dim3(p.M), dim3(64), 0, stream,
+                  p, G, places);
   return int(hipGetLastError());
 }
 
