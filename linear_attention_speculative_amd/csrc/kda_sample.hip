@@ -34,11 +34,11 @@
 // plan_row and pick_token have kernels of their own where there are many rows.
 // With few, whose launches count, one wave of the last workgroup to finish a
 // row's sums does their work (33 rows: 57 us a call against 62; 640 rows with
-// top-k 1000: 104 us for sums and plans against 73, the workgroups' places
+// top-k 1000: 104 us for sums and plans against 74, the workgroups' places
 // being held meanwhile).
 //
 // In all, 640 of 1024 window rows of 131072 bf16 logits with mixed parameters:
-// 28 us for the maxima (6 TB/s), 56 sums and plans (fp64 weights of the rows
+// 28 us for the maxima (6 TB/s), 54 sums and plans (fp64 weights of the rows
 // with top-p alone), 16 lists, 33 sorts, 26 kept sums and picks, 5 acceptance.
 #include "kda_serving.hpp"
 
@@ -520,17 +520,28 @@ struct Found {
   int at;
   uint64_t before, value, total;
 };
-template <class Goal>
+// kOwn = n / 64: numbers that an earlier launch left; kOwn = 0: any n, written
+// by others of this launch.
+template <int kOwn, class Goal>
 __device__ __forceinline__ Found find_first(const uint64_t* a, int n,
                                             Goal goal) {
-  const int own = (n + 63) / 64;
+  const int own = kOwn > 0 ? kOwn : (n + 63) / 64;
   const int lane = threadIdx.x & 63;
   uint64_t sum = 0;
+  if constexpr (kOwn > 0) {
+#pragma unroll
+    for (int j = 0; j < kOwn / 2; ++j) {
+      const ulonglong2 v =
+          reinterpret_cast<const ulonglong2*>(a)[lane * (kOwn / 2) + j];
+      sum += v.x + v.y;
+    }
+  } else {
 #pragma unroll 4
-  for (int j = 0; j < own; ++j) {
-    const int i = lane * own + j;
-    const uint64_t v = shared_load(a + min(i, n - 1));
-    sum += i < n ? v : 0;
+    for (int j = 0; j < own; ++j) {
+      const int i = lane * own + j;
+      const uint64_t v = shared_load(a + min(i, n - 1));
+      sum += i < n ? v : 0;
+    }
   }
   Found f{-1, 0, 0, 0};
   const uint64_t upto = wave_scan(sum);
@@ -913,7 +924,7 @@ __device__ __forceinline__ uint32_t least_allowed(const Params& q,
 }
 
 // What a row needs, by one wave; greedy rows get their token.
-template <bool BF16, bool VEC>
+template <bool BF16, bool VEC, bool kShared>
 __device__ __forceinline__ void plan_row(const SampleParams& p,
                                          const Work& work, const Params& q,
                                          int m, int G, int places) {
@@ -962,7 +973,7 @@ __device__ __forceinline__ void plan_row(const SampleParams& p,
   if (!q.need_k && !q.need_p) {
     plan.mode = kSummed;
   } else if (!q.need_k) {
-    const Found f = find_first(
+    const Found f = find_first<kShared ? 0 : kBins / 64>(
         work.sums, kBins, [&](uint64_t w) { return share_of(q.top_p, w); });
     plan.mass = f.total;
     plan.before = f.before;
@@ -982,8 +993,8 @@ __device__ __forceinline__ void plan_row(const SampleParams& p,
       plan.first = kth_key(gmax, G, k);
     } else if (k > live) {           // counted before
       const CountBins bins(gmax, G, top, min_key, CountBins::few(k, live));
-      const Found f = find_first(work.sums, kBins,
-                                 [&](uint64_t) { return uint64_t(k); });
+      const Found f = find_first<kShared ? 0 : kBins / 64>(
+          work.sums, kBins, [&](uint64_t) { return uint64_t(k); });
       if (f.at >= 0)
         plan.first = max(min_key, least_key(top_key, [&](float x) {
                            return bins(x) <= f.at;
@@ -1025,7 +1036,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   const float top = row_max(work.gmax, G);
   if (q.greedy || (counts && q.k <= live) || top == -__builtin_inff()) {
     if (plans && part.chosen && wave == 0)
-      plan_row<BF16, VEC>(p, work, q, m, G, places);
+      plan_row<BF16, VEC, true>(p, work, q, m, G, places);
     return;
   }
   if (!counts) fill_table(table);
@@ -1084,7 +1095,7 @@ __global__ void __launch_bounds__(kMaxThreads)
     }
   }
   if (plans && last_of(&work.plan->arrived[0], per_row) && wave == 0)
-    plan_row<BF16, VEC>(p, work, q, m, G, places);
+    plan_row<BF16, VEC, true>(p, work, q, m, G, places);
 }
 
 template <bool BF16, bool VEC>
@@ -1097,7 +1108,7 @@ __global__ void __launch_bounds__(64)
     if (threadIdx.x == 0) work.plan->mode = kDecided;
     return;
   }
-  plan_row<BF16, VEC>(p, work, Params(p, b, m), m, G, places);
+  plan_row<BF16, VEC, false>(p, work, Params(p, b, m), m, G, places);
 }
 
 // The token whose running weight passes u, by one wave: from the weights of
@@ -1107,8 +1118,8 @@ __device__ __forceinline__ void pick_token(const SampleParams& p,
                                            const Work& work,
                                            const Weights& wt, Threshold thr,
                                            float u, int m, int G) {
-  const Found f = find_first(work.sums, G,
-                             [&](uint64_t w) { return past_share(u, w); });
+  const Found f = find_first<0>(
+      work.sums, G, [&](uint64_t w) { return past_share(u, w); });
   const uint64_t target = past_share(u, f.total);
   Group<BF16, VEC> v;
   v.load(static_cast<const char*>(p.logits) + m * p.s_row * (BF16 ? 2 : 4),
