@@ -391,8 +391,9 @@ typedef struct {
      out = S' q.
    The new state goes to the final slot (NULL: in place); with the fused conv,
    the newest three raw inputs go to entries [0, 3) of the final slot's conv
-   state, other entries stay.  A request whose state slot is null gets +0.0 outputs and nothing
-   else; one whose final slot alone is null gets its output and no state. */
+   state, other entries stay.  A request whose state slot is null gets +0.0
+   outputs and nothing else; one whose final slot alone is null gets its output
+   and no state. */
 typedef struct {
   kda_tensor mixed_qkv;    /* act [B, 3HD] */
   kda_tensor raw_gate;     /* act [B, HD] */
@@ -486,8 +487,8 @@ typedef struct {
    against draft_tokens[m + 1], and num_accepted[b] = 1 + the number of
    leading matches, in [1, e - s] (0 for an empty window): what
    kda_commit_plan takes as num_accepted_tokens (with request_indices it reads
-   that array by request row, this one is in batch order).  next_tokens[b] is the
-   token of row s + num_accepted[b] - 1 (-1 for an empty window). */
+   that array by request row, this one is in batch order).  next_tokens[b] is
+   the token of row s + num_accepted[b] - 1 (-1 for an empty window). */
 typedef struct {
   kda_tensor logits;              /* F32 or BF16 [M, V], rows contiguous */
   const float* uniform;           /* [M] */
