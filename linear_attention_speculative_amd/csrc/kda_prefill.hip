@@ -27,11 +27,10 @@
 //   to LDS takes a wave some 50 cycles, which the others then do not spend.
 //
 // What bounds them, on 8192 tokens of 32 heads of D = 128 (bf16): the chunk
-// kernel, 230 us, its vector arithmetic (busy 67% of the time) and memory (0.27
-// GB read and 0.52 GB written: 160 us at a copy's rate); the state kernel, 370
-// us, the length of one chunk's chain of products, 1.45 us times 256
-// chunks, with one wave to each SIMD that has any.  16 prompts of 16000
-// tokens together: 430 and 268 us.
+// kernel, 230 us, its vector arithmetic and memory (0.27 GB read and 0.6 GB
+// written: 175 us at a copy's rate); the state kernel, 417 us, the length of
+// one chunk's chain of products, 1.6 us times 256 chunks, with one wave to
+// each SIMD that has any.  16 prompts of 16000 tokens together: 433 and 305 us.
 //
 // Decays never divide: every exponent above is a sum over tokens between j
 // and t, so each factor is at most 1, however strong the gates.  Within 16
@@ -45,8 +44,11 @@
 // term: fp32-like, at a third of the fp16 matrix rate instead of the
 // sixteenth that fp32 operands have.  k e^G and the like are at most 1 and
 // take fixed scales; each column of S, with its V, r and c, has a scale of
-// its own that follows its largest element.  Products that only feed bf16
-// outputs take hi alone (2^-11 against the output's own 2^-9).
+// its own that follows its largest element.  The products behind bf16 outputs
+// are as exact: an output is what two terms leave, and where the delta rule
+// replaces what the state held, it can be far smaller than they are.  (With
+// the high halves alone, 2^-11 of each term, the two kernels took 223 and 364
+// us, and outputs were off by many bf16 steps there.)
 #include "kda_serving.hpp"
 
 namespace kda {
@@ -72,9 +74,8 @@ struct Work {
   static constexpr int v = t + 2 * 2 * kFrag;          // [2][MT] fp32
   static constexpr int gam = v + 2 * MT * kFrag;       // [D] fp32
   static constexpr int qd = gam + (D * 4 + kFrag - 1) / kFrag * kFrag;
-  // q e^G [2][KS] and B [2]: hi, and lo for fp32 outputs
-  static constexpr int b(bool o32) { return qd + 2 * KS * kFrag * (o32 + 1); }
-  static constexpr int size(bool o32) { return b(o32) + 2 * kFrag * (o32 + 1); }
+  static constexpr int b = qd + 2 * KS * 2 * kFrag;    // q e^G, then B: [2]
+  static constexpr int size = b + 2 * 2 * kFrag;       // hi, lo
 };
 
 struct Split {
@@ -251,7 +252,7 @@ __device__ __forceinline__ void rank_request(const PrefillParams& p, int b,
   }
 }
 
-template <int D, bool BF16, bool O32>
+template <int D, bool BF16>
 __global__ void __launch_bounds__(ChunkCfg<D>::NT)
     __attribute__((amdgpu_waves_per_eu(4, 4)))
     kda_prefill_chunk_kernel(PrefillParams p) {
@@ -278,7 +279,7 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
     rank_request<D>(p, first == 0 ? b : -1, m);
   if (!live_slot(y, y.slots[b])) return;
   const int t0 = range.x + first, n = min(C, range.y - t0);
-  char* work = p.work + (int64_t(slot) * y.H + h) * W::size(O32);
+  char* work = p.work + (int64_t(slot) * y.H + h) * W::size;
 
   // ---- activations: convolution, norms, gates ----
   // a wave holds whole rows at D = 128: its token rows are scalar addresses
@@ -674,9 +675,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
         v[4 + e] = r == 0 ? 0.0f : kUnit * m.b[kSub + col][kSub + 4 * g + e];
       }
       const Split s = split8(v);
-      store_frag(work + W::b(O32) + r * (O32 + 1) * kFrag, lane, s.hi);
-      if (O32)
-        store_frag(work + W::b(O32) + (r * 2 + 1) * kFrag, lane, s.lo);
+      store_frag(work + W::b + 2 * r * kFrag, lane, s.hi);
+      store_frag(work + W::b + (2 * r + 1) * kFrag, lane, s.lo);
     }
   }
   // scaled k and q, handed out as the waves become free
@@ -702,8 +702,8 @@ __global__ void __launch_bounds__(ChunkCfg<D>::NT)
       const Split a = split8(x), q = split8(z);
       store_frag(work + W::kd + 2 * task * kFrag, lane, a.hi);
       store_frag(work + W::kd + (2 * task + 1) * kFrag, lane, a.lo);
-      store_frag(work + W::qd + task * (O32 + 1) * kFrag, lane, q.hi);
-      if (O32) store_frag(work + W::qd + (2 * task + 1) * kFrag, lane, q.lo);
+      store_frag(work + W::qd + 2 * task * kFrag, lane, q.hi);
+      store_frag(work + W::qd + (2 * task + 1) * kFrag, lane, q.lo);
     } else {
       const int mt = task - NKD, c = 16 * mt + col;
       const float late = m.end[1][c];
@@ -794,7 +794,7 @@ __device__ __forceinline__ void wait_vm() {
 template <int D, bool O32, int WAVES, int PROD, int BUFS>
 struct Stage {
   using W = Work<D>;
-  static constexpr int shared_frags = (W::size(O32) - 2 * W::MT * kFrag) /
+  static constexpr int shared_frags = (W::size - 2 * W::MT * kFrag) /
                                       kFrag;
   static constexpr int frags = shared_frags + 2 * WAVES;
   static constexpr int per_loader = (frags + PROD - 1) / PROD;
@@ -840,10 +840,10 @@ __global__ void __launch_bounds__(64 * (WAVES + PROD))
                 !O32);
     return;
   }
-  const int64_t step = int64_t(y.H) * W::size(O32);
+  const int64_t step = int64_t(y.H) * W::size;
   const char* work =
       p.work +
-      (int64_t(first_slot(range.x, b)) * y.H + h) * W::size(O32);
+      (int64_t(first_slot(range.x, b)) * y.H + h) * W::size;
   const uint32_t lds0 = uint32_t(reinterpret_cast<uintptr_t>(
       (__attribute__((address_space(3))) char*)smem));
   const int chunks = (L + C - 1) / C;
@@ -920,23 +920,29 @@ __global__ void __launch_bounds__(64 * (WAVES + PROD))
       return *reinterpret_cast<const h8*>(sm + off);
     };
 
-    h8 kh[2 * W::KS], kl[2 * W::KS], qh[2 * W::KS], ql[O32 ? 2 * W::KS : 1];
+    h8 kh[2 * W::KS], kl[2 * W::KS], qh[2 * W::KS], ql[2 * W::KS];
     f4 r[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       r[i] = *reinterpret_cast<const f4*>(
           sm + (G::shared_frags + 2 * wave + i) * kFrag);
-#pragma unroll
-    for (int j = 0; j < W::KS; ++j)
+    const auto load_kq = [&](int j) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int a = i * W::KS + j;
         kh[a] = op(W::kd + 2 * a * kFrag);
         kl[a] = op(W::kd + (2 * a + 1) * kFrag);
-        qh[a] = op(G::behind(W::qd + a * (O32 + 1) * kFrag));
-        if (O32) ql[a] = op(G::behind(W::qd + (2 * a + 1) * kFrag));
+        qh[a] = op(G::behind(W::qd + 2 * a * kFrag));
+        ql[a] = op(G::behind(W::qd + (2 * a + 1) * kFrag));
       }
-    if constexpr (!kLean) __builtin_amdgcn_sched_barrier(0);
+    };
+    // many waves to a SIMD cover each other's loads and have no registers to
+    // hold operands ahead of their use
+    if constexpr (!kLean) {
+#pragma unroll
+      for (int j = 0; j < W::KS; ++j) load_kq(j);
+      __builtin_amdgcn_sched_barrier(0);
+    }
     // scale
     float top = 0.0f;
 #pragma unroll
@@ -968,6 +974,7 @@ __global__ void __launch_bounds__(64 * (WAVES + PROD))
     f4 pr[2] = {}, pl[2] = {}, o[2] = {};
 #pragma unroll
     for (int j = 0; j < W::KS; ++j) {
+      if constexpr (kLean) load_kq(j);
       float x[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
@@ -982,14 +989,13 @@ __global__ void __launch_bounds__(64 * (WAVES + PROD))
         pl[i] = mfma(kl[a], s.hi, pl[i]);
         o[i] = mfma(qh[a], s.hi, o[i]);
         pl[i] = mfma(kh[a], s.lo, pl[i]);
-        if (O32) {
-          o[i] = mfma(ql[a], s.hi, o[i]);
-          o[i] = mfma(qh[a], s.lo, o[i]);
-        }
+        o[i] = mfma(ql[a], s.hi, o[i]);
+        o[i] = mfma(qh[a], s.lo, o[i]);
       }
+      if constexpr (kLean) __builtin_amdgcn_sched_barrier(0);
     }
     // operands of the second half, on their way during the next products
-    h8 th[2], tl[2], bh[2], bl[O32 ? 2 : 1], eh[W::MT], el[W::MT];
+    h8 th[2], tl[2], bh[2], bl[2], eh[W::MT], el[W::MT];
     f4 gam[W::MT];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -1000,15 +1006,18 @@ __global__ void __launch_bounds__(64 * (WAVES + PROD))
     for (int m = 0; m < W::MT; ++m)
       gam[m] = *reinterpret_cast<const f4*>(
           smem + buf * G::bytes + G::behind(W::gam) + (16 * m + 4 * g) * 4);
-#pragma unroll
-    for (int m = 0; m < W::MT; ++m) {
+    const auto load_ke = [&](int m) {
       eh[m] = op(W::ke + 2 * m * kFrag);
       el[m] = op(W::ke + (2 * m + 1) * kFrag);
+    };
+    if constexpr (!kLean) {
+#pragma unroll
+      for (int m = 0; m < W::MT; ++m) load_ke(m);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      bh[i] = op(G::behind(W::b(O32) + i * (O32 + 1) * kFrag));
-      if (O32) bl[i] = op(G::behind(W::b(O32) + (2 * i + 1) * kFrag));
+      bh[i] = op(G::behind(W::b + 2 * i * kFrag));
+      bl[i] = op(G::behind(W::b + (2 * i + 1) * kFrag));
     }
     if constexpr (!kLean) __builtin_amdgcn_sched_barrier(0);
     // r = V - (k e^G) S, c = T r; c is kept at sig / kLate, so that the update
@@ -1039,14 +1048,13 @@ __global__ void __launch_bounds__(64 * (WAVES + PROD))
     for (int i = 0; i < 2; ++i) {
       o[i] *= 1.0f / kLate;                 // from kUnit sig, as B c is
       o[i] = mfma(bh[i], cs.hi, o[i]);
-      if (O32) {
-        o[i] = mfma(bl[i], cs.hi, o[i]);
-        o[i] = mfma(bh[i], cs.lo, o[i]);
-      }
+      o[i] = mfma(bl[i], cs.hi, o[i]);
+      o[i] = mfma(bh[i], cs.lo, o[i]);
     }
     // the state behind the chunk
 #pragma unroll
     for (int m = 0; m < W::MT; ++m) {
+      if constexpr (kLean) load_ke(m);
       S[m] = mfma(eh[m], cs.hi, S[m]);
       S[m] = mfma(el[m], cs.hi, S[m]);
       S[m] = mfma(eh[m], cs.lo, S[m]);
@@ -1141,7 +1149,7 @@ int launch_prefill_dim(const PrefillParams& p, hipStream_t stream) {
   const int64_t wgs = int64_t(p.n_slots) * p.y.H;
   if (wgs > 0x7fffffff) return int(hipErrorInvalidValue);
   const size_t lds = sizeof(ChunkSmem<D>);
-  auto chunk = kda_prefill_chunk_kernel<D, BF16, O32>;
+  auto chunk = kda_prefill_chunk_kernel<D, BF16>;
   if (lds > 65536) {
     const hipError_t e = hipFuncSetAttribute(
         reinterpret_cast<const void*>(chunk),
@@ -1154,9 +1162,10 @@ int launch_prefill_dim(const PrefillParams& p, hipStream_t stream) {
   if (e != hipSuccess) return int(e);
   constexpr int MT = Work<D>::MT;
   // Waves that share a workgroup's operands: as few as keep all workgroups
-  // resident at once (a chunk of D = 128 takes 1.45 us with two waves, 1.6
-  // with four, 2.3 with eight), else as many as there are, which load and
-  // hold each operand once.  Eight waves with fp32 outputs would spill.
+  // resident at once (a chunk of D = 128 takes 2.1 us with two waves on every
+  // CU, 2.4 to 2.7 with four, 3.4 to 4.8 with eight), else as many as there
+  // are, which load and hold each operand once.  (fp32 outputs have no variant
+  // of eight.)
   const int64_t items = int64_t(p.y.B) * p.y.H;
   if constexpr (MT > 4 && !O32)
     if (items * (MT / 4) > 256)
@@ -1164,7 +1173,7 @@ int launch_prefill_dim(const PrefillParams& p, hipStream_t stream) {
   if constexpr (MT > 2)
     if (items * (MT / 2) > 256)
       return launch_state<D, O32, 4, 4, 2>(p, BF16, stream);
-  return launch_state<D, O32, (MT < 2 ? MT : 2), 4, (D == 128 && O32 ? 2 : 3)>(
+  return launch_state<D, O32, (MT < 2 ? MT : 2), 4, (D == 128 ? 2 : 3)>(
       p, BF16, stream);
 }
 
@@ -1180,12 +1189,12 @@ int launch_prefill_types(const PrefillParams& p, bool act_bf16,
 
 }  // namespace
 
-int64_t prefill_slot_bytes(int D, bool out_f32) {
+int64_t prefill_slot_bytes(int D) {
   switch (D) {
-    case 16: return Work<16>::size(out_f32);
-    case 32: return Work<32>::size(out_f32);
-    case 64: return Work<64>::size(out_f32);
-    case 128: return Work<128>::size(out_f32);
+    case 16: return Work<16>::size;
+    case 32: return Work<32>::size;
+    case 64: return Work<64>::size;
+    case 128: return Work<128>::size;
     default: return 0;
   }
 }

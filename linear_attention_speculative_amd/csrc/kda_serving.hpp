@@ -29,7 +29,7 @@ constexpr int kChunk = 32;
 constexpr int64_t prefill_slots(int64_t T, int64_t B) {
   return T / kChunk + B + 1;
 }
-int64_t prefill_slot_bytes(int D, bool out_f32);
+int64_t prefill_slot_bytes(int D);
 int launch_prefill(const PrefillParams& p, int D, bool act_bf16,
                    hipStream_t stream);
 

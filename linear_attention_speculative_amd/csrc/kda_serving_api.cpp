@@ -225,8 +225,7 @@ struct PrefillPlan {
 };
 
 // Bytes of workspace, or 0 for sizes that no launch takes.
-int64_t prefill_bytes(int64_t T, int64_t B, int64_t H, int64_t D,
-                      bool out_f32) {
+int64_t prefill_bytes(int64_t T, int64_t B, int64_t H, int64_t D) {
   if (T < 0 || B < 0 || H < 1 || !supported_head_dim(D) || T > kI32Max ||
       B > kI32Max || H > kI32Max || B * H > kI32Max)
     return 0;
@@ -236,7 +235,7 @@ int64_t prefill_bytes(int64_t T, int64_t B, int64_t H, int64_t D,
   if (slots > kMaxThreads / 512 / H ||
       (B * H + 7) / 8 * 8 * (D / 16) > kMaxThreads / 320)
     return 0;
-  return slots * H * kda::prefill_slot_bytes(int(D), out_f32) +
+  return slots * H * kda::prefill_slot_bytes(int(D)) +
          (B + 4) / 4 * 16;     // the order of the requests, behind the slots
 }
 
@@ -246,8 +245,7 @@ int plan_prefill(const kda_prefill_args* a, bool conv, PrefillPlan* plan) {
   int64_t T = 0;
   KDA_TRY(plan_layer(view_of(a), conv, &p.y, &plan->D, &plan->act_bf16, &T));
   plan->noop = a->batch == 0 || T == 0;
-  const int64_t need = prefill_bytes(T, a->batch, p.y.H, plan->D,
-                                     a->out.dtype == KDA_F32);
+  const int64_t need = prefill_bytes(T, a->batch, p.y.H, plan->D);
   if (need == 0)
     return fail(KDA_E_CAPACITY, "tokens, requests and heads exceed the grid");
   if (!plan->noop) {
@@ -480,8 +478,7 @@ int64_t kda_prefill_workspace_size(int64_t tokens, int64_t batch,
   if (elem_size(act_dtype) == 0 ||
       (out_dtype != KDA_F32 && out_dtype != act_dtype))
     return 0;
-  return prefill_bytes(tokens, batch, num_heads, head_dim,
-                       out_dtype == KDA_F32);
+  return prefill_bytes(tokens, batch, num_heads, head_dim);
 }
 
 int kda_check_prefill(const kda_prefill_args* args) {
