@@ -343,9 +343,12 @@ typedef struct {
      S_t = S_{t-1} diag(e^g_t) + c_t k_hat_t^T,  out_t = S_t q_t.
    The last state goes to the request's state slot and, with the fused conv,
    its last three raw inputs to entries [0, 3) of that slot's conv state (read
-   back with accepted count 1); other entries stay.  Tokens are taken 32 at a
-   time: an input that is not finite spoils its request's outputs from up to 31
-   tokens before it on, and no other request's. */
+   back with accepted count 1); other entries stay.  A request without tokens
+   changes nothing, its state slot included.  Tokens are taken 32 at a time: an
+   input that is not finite spoils its request's outputs from up to 31 tokens
+   before it on, and no other request's.  Arithmetic is fp32-like, its errors
+   going by the largest value that a row v of the state, or that v, has within
+   the 32 tokens. */
 typedef struct {
   kda_tensor mixed_qkv;    /* act [T, 3HD]: raw q|k|v (kda_conv_prefill) or
                               convolved q|k|v (kda_prefill_qkv) */

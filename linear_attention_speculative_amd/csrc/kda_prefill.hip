@@ -44,11 +44,14 @@
 // term: fp32-like, at a third of the fp16 matrix rate instead of the
 // sixteenth that fp32 operands have.  k e^G and the like are at most 1 and
 // take fixed scales; each column of S, with its V, r and c, has a scale of
-// its own that follows its largest element.  The products behind bf16 outputs
-// are as exact: an output is what two terms leave, and where the delta rule
-// replaces what the state held, it can be far smaller than they are.  (With
-// the high halves alone, 2^-11 of each term, the two kernels took 223 and 364
-// us, and outputs were off by many bf16 steps there.)
+// its own that follows its largest element: errors go by the largest value
+// that a column of S, or its V, has within a chunk.  Of a column that a chunk
+// decays to e^G of itself, with G below some -20, and that no V joins, the
+// corrections that remain (e^G or less each) keep fewer bits, down to none.
+// The products behind bf16 outputs are as exact: an output is what two terms
+// leave, and where the delta rule replaces what the state held, it can be far
+// smaller than they are.  (With the high halves alone, 2^-11 of each term, the
+// two kernels took 223 and 364 us, and outputs were off by many bf16 steps.)
 #include "kda_serving.hpp"
 
 namespace kda {
@@ -956,19 +959,42 @@ __global__ void __launch_bounds__(64 * (WAVES + PROD))
     low &= low >> 32;
     low &= low >> 16;                     // all four lanes of a column
     if (__ballot(top > 1024.0f) | (low & 0xffff)) {
-      top = column_max(top);
-      const int e = int(__float_as_uint(top) >> 23);       // biased
+      // V once more, unscaled: under the scale of a column that had vanished
+      // it may be infinite
+      float ts = 0.0f, tv = 0.0f;
+#pragma unroll
+      for (int m = 0; m < W::MT; ++m) ts = max_abs(S[m], ts);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        r[i] = *reinterpret_cast<const f4*>(
+            sm + (G::shared_frags + 2 * wave + i) * kFrag);
+        tv = max_abs(r[i], tv);
+      }
+      ts = column_max(ts);
+      tv = column_max(tv);
+      // biased exponents under the scale of now
       const int es = int(__float_as_uint(sig) >> 23);
+      const int e_s = max(int(__float_as_uint(ts) >> 23), 1);
+      const int e_v = max(int(__float_as_uint(tv) >> 23), 1);
+      const int e = max(ts > 0.0f ? e_s : -999,
+                        tv > 0.0f ? e_v + es - 127 : -999);
       int d = 127 + 9 - e;
-      if ((top >= 16.0f && top <= 1024.0f) || e == 0 || e == 255) d = 0;
-      d = min(max(d, 17 - es), 237 - es);     // sig stays in 2^+-110
-      const float f = __uint_as_float(uint32_t(127 + d) << 23);
-      sig *= f;
+      if ((e >= 127 + 4 && e < 127 + 10) || e == -999 || e_s == 255 ||
+          e_v == 255)
+        d = 0;
+      // sig stays in 2^-125 .. 2^110 (below 2^-118 only for a state past the
+      // largest fp32 number), so d is in -235 .. 235: up in two factors, and
+      // far down to where S is nothing beside V
+      d = min(max(d, 2 - es), 237 - es);
+      const float f =
+          __uint_as_float(uint32_t(max(127 + min(d, 127), 0)) << 23);
+      const float f2 = __uint_as_float(uint32_t(max(d, 127)) << 23);
+      sig = __uint_as_float(uint32_t(es + d) << 23);
       inv = __uint_as_float(uint32_t(254 - es - d) << 23);
 #pragma unroll
-      for (int m = 0; m < W::MT; ++m) S[m] *= f;
+      for (int m = 0; m < W::MT; ++m) S[m] = S[m] * f * f2;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) r[i] *= f;
+      for (int i = 0; i < 2; ++i) r[i] *= sig;
     }
     // S as the right operand: two 16-channel tiles make one step of 32
     f4 pr[2] = {}, pl[2] = {}, o[2] = {};
