@@ -383,7 +383,9 @@ typedef struct {
   int32_t null_block_id;
   int32_t conv_dim_first;
   int32_t use_lower_bound;
-  float lower_bound;
+  float lower_bound;       /* at most 0 (a bound above 0 lets states grow past
+                              the operands' range and is refused here, not by
+                              the decode) */
 } kda_prefill_args;
 
 /* Arguments of kda_conv_update_decode and kda_decode_qkv: one token for each

@@ -244,6 +244,11 @@ int plan_prefill(const kda_prefill_args* a, bool conv, PrefillPlan* plan) {
   kda::PrefillParams& p = plan->p;
   int64_t T = 0;
   KDA_TRY(plan_layer(view_of(a), conv, &p.y, &plan->D, &plan->act_bf16, &T));
+  // The chunked form's operands are products of decays of at most 1 each.
+  if (a->use_lower_bound && !(a->lower_bound <= 0.0f))
+    return fail(KDA_E_UNSUPPORTED,
+                "the prefill needs a lower_bound of at most 0 (got %g)",
+                double(a->lower_bound));
   plan->noop = a->batch == 0 || T == 0;
   const int64_t need = prefill_bytes(T, a->batch, p.y.H, plan->D);
   if (need == 0)

@@ -115,8 +115,9 @@ def conv_prefill(*, stream=None, **kwargs) -> None:
     where null or not given) and leaves its checkpoint and conv history in
     slot `state_indices[b]`, ready for the verify or the decode with accepted
     count 1.  Arguments follow kda_prefill_args in
-    include/kda_recoverssm.h; `workspace` is scratch memory of
-    `prefill_workspace_size` bytes."""
+    include/kda_recoverssm.h; `lower_bound` is None (softplus gate) or at
+    most 0; `workspace` is scratch memory of `prefill_workspace_size`
+    bytes."""
     _launch(_abi.load().kda_conv_prefill, prefill_args(**kwargs),
             kwargs, stream)
 
