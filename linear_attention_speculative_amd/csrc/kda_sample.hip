@@ -31,11 +31,9 @@
 //   kda_kept_sums_kernel, only for rows that kept more than a list: the kept
 //   weights of each group; pick_token, one wave a row, the token from them.
 //
-// plan_row and pick_token have kernels of their own where there are many rows.
-// With few, whose launches count, one wave of the last workgroup to finish a
-// row's sums does their work (33 rows: 57 us a call against 62; 640 rows with
-// top-k 1000: 104 us for sums and plans against 74, the workgroups' places
-// being held meanwhile).
+// plan_row and pick_token have kernels of their own, except where a batch has
+// so few workgroups that launches count: there one wave of the last workgroup
+// to finish a row's sums does their work (launch_rows).
 //
 // In all, 640 of 1024 window rows of 131072 bf16 logits with mixed parameters:
 // 28 us for the maxima (6 TB/s), 54 sums and plans (fp64 weights of the rows
@@ -334,24 +332,19 @@ struct Work {
 };
 
 // Whether this workgroup is the last of `parts` of a row to get here.  It then
-// may read (with shared_load) what the others wrote with device-scope atomics
-// and shared_store before they got here.  Those go through to where all XCDs
-// see them, so that waiting for their end is enough: a release fence would
-// write back the whole L2 (640 rows with top-k 1000: the sums kernel 750 us
-// in place of 104).
+// may read what the others wrote before: each counts itself with a release of
+// what its threads wrote (the barrier hands that to the first thread), and the
+// count it finds acquires what the others released.  A release writes back an
+// XCD's L2, so this is for few workgroups (launch_rows).
 __device__ __forceinline__ bool last_of(uint32_t* arrived, int parts) {
   __shared__ int last;
-  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(arrived, 1u) + 1 == uint32_t(parts);
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_ACQ_REL,
+                                  __HIP_MEMORY_SCOPE_AGENT) ==
+           uint32_t(parts - 1);
   __syncthreads();
   return last != 0;
-}
-__device__ __forceinline__ void shared_store(uint64_t* at, uint64_t v) {
-  __hip_atomic_store(at, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ uint64_t shared_load(const uint64_t* at) {
-  return __hip_atomic_load(at, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 // The groups of a row that a workgroup of the split kernels takes.
@@ -541,7 +534,7 @@ __device__ __forceinline__ Found find_first(const uint64_t* a, int n,
 #pragma unroll 4
     for (int j = 0; j < own; ++j) {
       const int i = lane * own + j;
-      const uint64_t v = shared_load(a + min(i, n - 1));
+      const uint64_t v = a[min(i, n - 1)];
       sum += i < n ? v : 0;
     }
   }
@@ -555,7 +548,7 @@ __device__ __forceinline__ Found find_first(const uint64_t* a, int n,
   const uint64_t base = __shfl((unsigned long long)(upto - sum), l);
   const int first = l * own;
   const uint64_t v =
-      lane < own && first + lane < n ? shared_load(a + first + lane) : 0;
+      lane < own && first + lane < n ? a[first + lane] : 0;
   const uint64_t u = base + wave_scan(v);
   const int i = __ffsll((unsigned long long)__ballot(u >= target)) - 1;
   f.at = first + i;
@@ -1060,7 +1053,7 @@ __global__ void __launch_bounds__(kMaxThreads)
   for (int g = part.first + wave; g < part.end; g += kMaxThreads / 64) {
     // a group whose largest logit min-p drops has nothing to add
     if (work.gmax[g] < least) {
-      if (!binned && lane == 0) shared_store(&work.sums[g], 0);
+      if (!binned && lane == 0) work.sums[g] = 0;
       continue;
     }
     Group<BF16, VEC> v;
@@ -1085,7 +1078,7 @@ __global__ void __launch_bounds__(kMaxThreads)
       each_kept<BF16, VEC>(v, kept[wave], in,
                            [&](float x) { sum += wt.of(x); });
       sum = wave_sum64(sum);
-      if (lane == 0) shared_store(&work.sums[g], sum);
+      if (lane == 0) work.sums[g] = sum;
     }
   }
   if (binned) {
@@ -1367,7 +1360,7 @@ __global__ void __launch_bounds__(kMaxThreads)
           [&](float x) { sum += wt.of(x); });
       sum = wave_sum64(sum);
     }
-    if (lane == 0) shared_store(&work.sums[g], sum);
+    if (lane == 0) work.sums[g] = sum;
   }
   if (picks && last_of(&work.plan->arrived[1], per_row) && wave == 0)
     pick_token<BF16, VEC>(p, work, wt, thr, q.u, m, G);
@@ -1417,12 +1410,18 @@ int launch_rows(const SampleParams& p, int G, int places,
   // rows with top-k 1000 of 131072: 64 us against 97; one row with top-p: 12
   // as it is, 17 with half)
   const bool many = p.M >= 128;
+  // Up to 128 workgroups, a row's last one plans and picks (4 rows of 131072:
+  // 22 us a call against 26 without filters, 49 against 51 with top-p; 32 of
+  // 32000: 22 against 25, 49 against 48).  More of them wait for each other's
+  // releases (16 rows of 131072 with top-p: 55 against 53; 127: 199 against
+  // 105).
+  const bool last = int64_t(p.M) * per_row <= 128;
   const int sums_wg = many ? 2 * kPerWg : kPerWg;
   const int sums_row = (G + sums_wg - 1) / sums_wg;
   launch_kernel(kda_row_sums_kernel<BF16, VEC>,
                 dim3(uint32_t(p.M) * uint32_t(sums_row)), dim3(kMaxThreads), 0,
-                stream, p, G, sums_row, sums_wg, places, !many);
-  if (many)
+                stream, p, G, sums_row, sums_wg, places, last);
+  if (!last)
     launch_kernel(kda_plan_kernel<BF16, VEC>, dim3(p.M), dim3(64), 0, stream,
                   p, G, places);
   if (p.top_k || p.top_p) {
@@ -1432,8 +1431,8 @@ int launch_rows(const SampleParams& p, int G, int places,
                   sizeof(RowSmem), stream, p, G, places);
   }
   launch_kernel(kda_kept_sums_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
-                stream, p, G, per_row, places, !many);
-  if (many)
+                stream, p, G, per_row, places, last);
+  if (!last)
     launch_kernel(kda_pick_kernel<BF16, VEC>, dim3(p.M), dim3(64), 0, stream,
                   p, G, places);
   return int(hipGetLastError());
