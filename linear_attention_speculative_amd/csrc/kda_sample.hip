@@ -1406,10 +1406,12 @@ int launch_rows(const SampleParams& p, int G, int places,
   const dim3 parts(uint32_t(p.M) * uint32_t(per_row));
   launch_kernel(kda_group_max_kernel<BF16, VEC>, parts, dim3(kMaxThreads), 0,
                 stream, p, G, per_row);
-  // half as many workgroups, each with bins of its own, for many rows (640
-  // rows with top-k 1000 of 131072: 64 us against 97; one row with top-p: 12
-  // as it is, 17 with half)
-  const bool many = p.M >= 128;
+  // Half as many workgroups, each with bins of its own, for the sums of eight
+  // a CU and more (times of a call: 640 rows of 131072 with top-k 1000 261 us
+  // against 285, 640 of 32000 98 against 106, 128 of 131072 77 against 83; 96
+  // of 131072 69 both; with fewer the whole number is quicker: 256 rows of
+  // 32000 without filters 33 against 38, 32 of 131072 27 against 35).
+  const bool many = int64_t(p.M) * per_row >= 2048;
   // Up to 128 workgroups, a row's last one plans and picks (4 rows of 131072:
   // 22 us a call against 26 without filters, 49 against 51 with top-p; 32 of
   // 32000: 22 against 25, 49 against 48).  More of them wait for each other's

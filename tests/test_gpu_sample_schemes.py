@@ -27,3 +27,19 @@ def test_few_workgroups_and_more(M, V):
     want = expect(*args)
     for _ in range(3):
         assert np.array_equal(run(*args)["tokens"], want)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,V", [(682, 17500), (683, 17500), (2047, 900),
+                                 (2048, 900)])
+def test_thousands_of_workgroups(M, V):
+    """From 2048 workgroups on each takes twice the groups of a row's sums
+    (2046 and 2049 of them here, 2047 and 2048): the tokens of the same rows
+    in small batches, and the oracle's on every tenth."""
+    args = batch(M, V, M)
+    got = run(*args)["tokens"]
+    parts = [run(*(a[s:s + 42] for a in args))["tokens"]
+             for s in range(0, M, 42)]
+    assert np.array_equal(got, np.concatenate(parts))
+    some = [a[::10] for a in args]
+    assert np.array_equal(got[::10], expect(*some))
