@@ -481,10 +481,10 @@ typedef struct {
    u = uniform[m].  temperature <= 0: the lowest index of the maximum.
    top_k <= 0, top_p >= 1, min_p <= 0, NaN parameters and NULL arrays leave
    their filter (or temperature 1) out; top_p <= 0 keeps one token; u is
-   held to [0, 1).  NaN logits count as -inf; a row without any value above
-   -inf gives token -1.  Each w is rounded to 46 binary places (62 -
-   ceil(log2 V) where that is fewer; formed in fp64, so that one next to the
-   middle of two may go to either) and summed as an integer: no order of
+   held to [0, 1 - 2^-24] (NaN: 0).  NaN logits count as -inf; a row without
+   any value above -inf gives token -1.  Each w is rounded to 46 binary places
+   (62 - ceil(log2 V) where that is fewer; formed in fp64, so that one next to
+   the middle of two may go to either) and summed as an integer: no order of
    additions changes a token.  V up to 2^20.
    Rows before query_start_loc[0] or from query_start_loc[batch] on are not
    touched.

@@ -278,7 +278,7 @@ struct Params {
     k = p.top_k ? n : 0;
     top_p = p.top_p && tp < 1.0f ? tp : 1.0f;
     min_p = p.min_p && mp > 0.0f ? mp : 0.0f;
-    u = uu > 0.0f ? uu : 0.0f;
+    u = uu > 0.0f ? fminf(uu, 0x1.fffffep-1f) : 0.0f;
     greedy = T <= 0.0f || k == 1 || top_p <= 0.0f;
     need_k = k > 0 && k < p.V;
     need_p = top_p < 1.0f;

@@ -90,3 +90,18 @@ def test_top_p_of_one_half(k):
     ks = None if k is None else np.full(n, k)
     got = run(f32(x), np.full(n, 0.999), k=ks, p=np.full(n, 0.5))["tokens"]
     assert np.array_equal(got > 0, [over > 0 for _, over in CASES])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k,p", [(None, None), (6, None), (None, 0.999999),
+                                 (6, 0.99)])
+def test_uniform_numbers_from_one_on(k, p):
+    """u is held to [0, 1): to the largest number below 1, so that a number
+    that was rounded up to 1 does not take the last token with any weight."""
+    u = np.array([1.0, 1.5, 4.0, 1e20, 3e38, np.inf, 1 - 2.0 ** -24])
+    x = np.full((len(u), 9), -25.0, np.float32)
+    x[:, 1] = 0.0
+    n = len(u)
+    got = run(f32(x), u, k=None if k is None else np.full(n, k),
+              p=None if p is None else np.full(n, p))["tokens"]
+    assert got.tolist() == [1] * n
