@@ -3,6 +3,8 @@
 // launch parameters, and the exported C entry points.
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "kda_host.hpp"
 #include "kda_recoverssm.h"
 #include "kda_serving.hpp"
@@ -32,6 +34,21 @@ LayerView view_of(const Args* a) {
                    a->batch,          a->spec_query_len,  a->null_block_id,
                    a->conv_dim_first, a->use_lower_bound, a->lower_bound,
                    a->state_indices,  a->num_accepted_tokens};
+}
+
+// Whether a tensor of three dimensions has its elements in places of their own,
+// each dimension's stride past the extent of those of smaller stride.
+bool nested(const kda_tensor& t) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3,
+            [&](int i, int j) { return t.stride[i] < t.stride[j]; });
+  int64_t extent = 0;          // from the first element to the last
+  for (int i : order) {
+    if (t.shape[i] <= 1) continue;
+    if (t.stride[i] <= extent) return false;
+    extent += (t.shape[i] - 1) * t.stride[i];
+  }
+  return true;
 }
 
 // Checks of one layer's tensors (the verify's rules where they apply), and
@@ -163,8 +180,9 @@ int plan_layer(const LayerView& a, bool conv, kda::LayerParams* p, int* D_out,
   for (int64_t st : strides)
     if (st < 0 || st > kI32Max)
       return fail(KDA_E_LAYOUT, "a tensor stride is negative or exceeds 2^31");
-  // Rows that writes would share (a broadcast view) cannot hold results.
-  if (conv && ((N > 1 && cs.stride[0] == 0) || s_chan == 0 || s_tok == 0))
+  // Elements that writes would share (a broadcast or sliding view) cannot hold
+  // results.
+  if (conv && !nested(cs))
     return fail(KDA_E_LAYOUT, "the conv state's entries overlap");
   if (T > 1 && a.out.stride[0] < HD)
     return fail(KDA_E_LAYOUT, "out's rows overlap");
