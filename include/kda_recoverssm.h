@@ -604,6 +604,10 @@ int kda_recoverssm_commit_step(const kda_commit_args* commit,
                                const kda_compact_args* compact,
                                void* stream);
 
+/* Of the calls below, no output may share memory with an input, except where
+   an argument says so (states and conv states of one slot, num_blocks).  The
+   squares of a head's q and k are summed in fp32. */
+
 /* Bytes of workspace that a prefill of `tokens` rows and `batch` requests
    needs (0 for sizes that the checks refuse); the activation dtype is
    act_dtype, out's is out_dtype (kda_dtype). */

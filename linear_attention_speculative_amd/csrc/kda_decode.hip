@@ -17,8 +17,8 @@
 // bytes.  One workgroup takes one tile, held in registers; its loads are
 // issued first, so that the convolution and the gates run under them.
 // Workgroups follow the XCD-aware order of the commit: each XCD streams one
-// contiguous eighth of the items.  256 requests of 32 heads (1.08 GB read and
-// written): 196 us, 5.5 TB/s; one request: 6.2 us, the latency of its loads.
+// contiguous eighth of the items.  251 requests of 32 heads (1.05 GB read and
+// written): 196 us, 5.4 TB/s; one request: 6.2 us, the latency of its loads.
 #include "kda_layer.hpp"
 #include "kda_serving.hpp"
 

@@ -28,9 +28,9 @@
 //
 // What bounds them, on 8192 tokens of 32 heads of D = 128 (bf16): the chunk
 // kernel, 230 us, its vector arithmetic and memory (0.27 GB read and 0.6 GB
-// written: 175 us at a copy's rate); the state kernel, 417 us, the length of
+// written: 175 us at a copy's rate); the state kernel, 415 us, the length of
 // one chunk's chain of products, 1.6 us times 256 chunks, with one wave to
-// each SIMD that has any.  16 prompts of 16000 tokens together: 433 and 305 us.
+// each SIMD that has any.  16 prompts of 16000 tokens together: 439 and 308 us.
 //
 // Decays never divide: every exponent above is a sum over tokens between j
 // and t, so each factor is at most 1, however strong the gates.  Within 16

@@ -36,7 +36,7 @@
 // to finish a row's sums does their work (launch_rows).
 //
 // In all, 640 of 1024 window rows of 131072 bf16 logits with mixed parameters:
-// 28 us for the maxima (6 TB/s), 54 sums and plans (fp64 weights of the rows
+// 28 us for the maxima (6 TB/s), 55 sums and plans (fp64 weights of the rows
 // with top-p alone), 16 lists, 33 sorts, 26 kept sums and picks, 5 acceptance.
 #include "kda_serving.hpp"
 
