@@ -334,10 +334,13 @@ struct Work {
 // Whether this workgroup is the last of `parts` of a row to get here.  It then
 // may read what the others wrote before: each counts itself with a release of
 // what its threads wrote (the barrier hands that to the first thread), and the
-// count it finds acquires what the others released.  A release writes back an
-// XCD's L2, so this is for few workgroups (launch_rows).
+// count it finds acquires what the others released.  Every wave also waits for
+// its stores to end before the barrier, so that the release finds them in the
+// L2 whatever the order in which a CU's waves reach it.  A release writes back
+// an XCD's L2, so this is for few workgroups (launch_rows).
 __device__ __forceinline__ bool last_of(uint32_t* arrived, int parts) {
   __shared__ int last;
+  asm volatile("s_waitcnt vmcnt(0)" : : : "memory");
   __syncthreads();
   if (threadIdx.x == 0)
     last = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_ACQ_REL,
