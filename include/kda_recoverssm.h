@@ -43,6 +43,10 @@
  *   kda_sample -- tokens from logits and given random numbers, and the
  *       accepted counts of draft windows that the commit plan reads.
  *
+ *   kda_latent_write, kda_latent_attention -- the attention layers between
+ *       KDA layers, over a paged cache of one latent vector a token, for
+ *       single tokens and draft windows.
+ *
  * plus host-only argument checks mirroring the pages' validation
  * (kernels page `_check_layouts`, `can_use_cute_recoverssm`; ops page
  * `kda_recoverssm_verify`, `KDARecoverSSMCommitContext.create/commit`).
@@ -516,6 +520,61 @@ typedef struct {
   int32_t pad_;
 } kda_sample_args;
 
+/* Arguments of kda_latent_write: token t's latent and rope key go to place
+   slot_mapping[t] of a paged cache (block slot / block_size, token slot %
+   block_size of it, as kda_step_tables numbers them), bit for bit.  R = latent
+   dim, P = rope dim.  A slot in a block <= null_block_id or past the cache
+   writes nothing.  Two tokens must not name the same slot. */
+typedef struct {
+  kda_tensor latent;             /* act [T, R] */
+  kda_tensor rope_key;           /* act [T, P]; empty for P = 0 */
+  kda_tensor cache;              /* act [N, block_size, R + P] */
+  const int64_t* slot_mapping;   /* [T] */
+  int32_t null_block_id;
+  int32_t pad_;
+} kda_latent_write_args;
+
+/* Arguments of kda_latent_attention: attention in latent space (the absorbed
+   form) over a paged cache.  Token t of request b (its rows follow
+   query_start_loc, clamped to [0, T]) stands at position c + i, c =
+   max(num_computed_tokens[row], 0), i = t - query_start_loc[b], row =
+   request_indices[b] (or b), and sees the cache entries e_j = (c_j | r_j) of
+   positions j = 0 .. c + i, its own included (kda_latent_write comes first):
+     s_j = softmax_scale * q_th . e_j,   p = softmax over j,
+     out_th = sum_j p_j c_j,             lse_th = ln sum_j e^(s_j).
+   Position j lies in block block_table[row][j / block_size]; positions of a
+   null block (<= null_block_id or >= N) or past the table's width are not
+   seen.  A query that sees nothing, or whose row is outside
+   [0, num_request_rows), gets +0.0 outputs and lse -inf.  Places of the cache
+   that no query of the tile sees are never read into a product; an entry that
+   is not finite spoils the outputs of all tokens of its request's window (of
+   its tiles of rows), also of those before it.  Arithmetic is fp32; with bf16
+   the weights p are rounded to bf16 before they weigh the latents.  Token rows
+   outside all requests are not touched. */
+typedef struct {
+  kda_tensor q;                  /* act [T, H, R + P] */
+  kda_tensor cache;              /* act [N, block_size, R + P]; R is 128, 256
+                                    or 512, P is 0 or 64 */
+  kda_tensor out;                /* act [T, H, R] */
+  kda_tensor lse;                /* F32 [T, H], or empty */
+  const int32_t* query_start_loc;      /* [batch + 1], not decreasing */
+  const int32_t* num_computed_tokens;  /* per request row */
+  const int32_t* request_indices;      /* [batch] or NULL: row = b */
+  const int32_t* block_table;          /* [num_request_rows, width] */
+  int64_t block_table_strides[2];      /* row, column (elements) */
+  void* workspace;               /* device, 16-byte aligned, at least
+                                    kda_latent_attention_workspace_size(...)
+                                    bytes; not shared by launches in flight
+                                    together */
+  int64_t workspace_bytes;
+  int32_t batch;
+  int32_t num_request_rows;
+  int32_t block_table_width;
+  int32_t null_block_id;
+  float softmax_scale;
+  int32_t pad_;
+} kda_latent_args;
+
 /* Library ABI version (KDA_ABI_VERSION). */
 int kda_abi_version(void);
 
@@ -644,6 +703,23 @@ int64_t kda_sample_workspace_size(int64_t rows, int64_t vocab);
 int kda_check_sample(const kda_sample_args* args);
 int kda_sample(const kda_sample_args* args, void* stream);
 
+/* Host-only validation of the cache write's arguments, then its launch. */
+int kda_check_latent_write(const kda_latent_write_args* args);
+int kda_latent_write(const kda_latent_write_args* args, void* stream);
+
+/* Bytes of workspace of a latent attention over `tokens` rows of `batch`
+   requests (0 for sizes that the checks refuse); act_dtype a kda_dtype. */
+int64_t kda_latent_attention_workspace_size(int64_t tokens, int64_t batch,
+                                            int64_t num_heads,
+                                            int64_t latent_dim,
+                                            int64_t rope_dim,
+                                            int32_t act_dtype);
+
+/* Host-only validation of the latent attention's arguments, then the
+   launches (two kernels). */
+int kda_check_latent_attention(const kda_latent_args* args);
+int kda_latent_attention(const kda_latent_args* args, void* stream);
+
 /* Launch a one-workgroup kernel that sets counter[0..n) to 0 on `stream`
    (for a counter left non-zero by an aborted launch).  Uses no memset
    node, so it may be captured in a graph. */
@@ -654,7 +730,7 @@ int kda_reset_counter(int32_t* counter, int32_t n, void* stream);
    the gap the event's own marker adds before the next dispatch).  Arms the
    calling thread: the next `launches` kernels that library calls on this
    thread launch (a prefill takes two, the step tables two or, without
-   tokens, one, sampling three to eight) are dispatched with
+   tokens, one, sampling three to eight, the latent attention two) are dispatched with
    hipExtLaunchKernel, `start_event` (a hipEvent_t, may be NULL) recording
    the start of the first of them and `stop_event` (may be NULL) the end of
    the last.  The counter-clearing kernels (kda_reset_counter, the first

@@ -4,6 +4,15 @@ The compute path is the HIP library `libkda_recoverssm.so` (C ABI in
 include/kda_recoverssm.h); this package is its thin torch binding.
 """
 from ._abi import LIB_PATH, load  # noqa: F401
+from .cache import (  # noqa: F401
+    check_latent_attention,
+    check_latent_write,
+    latent_args,
+    latent_attention,
+    latent_attention_workspace_size,
+    latent_write,
+    latent_write_args,
+)
 from .ops import (  # noqa: F401
     CommitContext,
     KdaError,

@@ -43,6 +43,9 @@ EXPORTED = (
     "kda_check_decode_qkv", "kda_decode_qkv",
     "kda_check_step_tables", "kda_step_tables",
     "kda_sample_workspace_size", "kda_check_sample", "kda_sample",
+    "kda_check_latent_write", "kda_latent_write",
+    "kda_latent_attention_workspace_size", "kda_check_latent_attention",
+    "kda_latent_attention",
 )
 
 
@@ -180,6 +183,28 @@ class KdaSampleArgs(Structure):
     ]
 
 
+class KdaLatentWriteArgs(Structure):
+    _fields_ = [
+        ("latent", KdaTensor), ("rope_key", KdaTensor), ("cache", KdaTensor),
+        ("slot_mapping", c_void_p), ("null_block_id", c_int32),
+        ("pad_", c_int32),
+    ]
+
+
+class KdaLatentArgs(Structure):
+    _fields_ = [
+        ("q", KdaTensor), ("cache", KdaTensor), ("out", KdaTensor),
+        ("lse", KdaTensor),
+        ("query_start_loc", c_void_p), ("num_computed_tokens", c_void_p),
+        ("request_indices", c_void_p), ("block_table", c_void_p),
+        ("block_table_strides", c_int64 * 2),
+        ("workspace", c_void_p), ("workspace_bytes", c_int64),
+        ("batch", c_int32), ("num_request_rows", c_int32),
+        ("block_table_width", c_int32), ("null_block_id", c_int32),
+        ("softmax_scale", c_float), ("pad_", c_int32),
+    ]
+
+
 _LIB = None
 
 
@@ -242,13 +267,20 @@ def load() -> ctypes.CDLL:
     lib.kda_prefill_workspace_size.argtypes = [c_int64] * 4 + [c_int32] * 2
     lib.kda_sample_workspace_size.restype = c_int64
     lib.kda_sample_workspace_size.argtypes = [c_int64] * 2
+    lib.kda_latent_attention_workspace_size.restype = c_int64
+    lib.kda_latent_attention_workspace_size.argtypes = ([c_int64] * 5 +
+                                                        [c_int32])
     for check, launches, args in (
             ("kda_check_prefill", ("kda_conv_prefill",), KdaPrefillArgs),
             ("kda_check_prefill_qkv", ("kda_prefill_qkv",), KdaPrefillArgs),
             ("kda_check_decode", ("kda_conv_update_decode",), KdaDecodeArgs),
             ("kda_check_decode_qkv", ("kda_decode_qkv",), KdaDecodeArgs),
             ("kda_check_step_tables", ("kda_step_tables",), KdaTablesArgs),
-            ("kda_check_sample", ("kda_sample",), KdaSampleArgs)):
+            ("kda_check_sample", ("kda_sample",), KdaSampleArgs),
+            ("kda_check_latent_write", ("kda_latent_write",),
+             KdaLatentWriteArgs),
+            ("kda_check_latent_attention", ("kda_latent_attention",),
+             KdaLatentArgs)):
         getattr(lib, check).restype = c_int
         getattr(lib, check).argtypes = [POINTER(args)]
         for name in launches:

@@ -1,0 +1,117 @@
+"""Python binding of the operators on token caches: the attention layers over
+paged latent caches.
+
+Argument marshalling and the checks that the C ABI cannot make, as in
+`serving`; every computation runs in the HIP library.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+import torch
+
+from . import _abi
+from .ops import _DT, _pack_format, _tensor_values
+from .serving import _ints, _launch
+
+_WRITE_PACK = struct.Struct("<" + _pack_format(_abi.KdaLatentWriteArgs))
+
+
+def latent_write_args(*, latent, cache, slot_mapping, rope_key=None,
+                      null_block_id=0) -> _abi.KdaLatentWriteArgs:
+    """kda_latent_write_args for these tensors."""
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    if slot_mapping.dim() != 1 or not slot_mapping.is_contiguous() or \
+            slot_mapping.shape[0] < latent.shape[0]:
+        raise ValueError("slot_mapping needs a contiguous entry per token")
+    vals = (*_tensor_values(latent), *_tensor_values(rope_key),
+            *_tensor_values(cache), slot_mapping.data_ptr(), null_block_id, 0)
+    return _abi.KdaLatentWriteArgs.from_buffer_copy(_WRITE_PACK.pack(*vals))
+
+
+def check_latent_write(**kwargs) -> int:
+    """Host-only validation (no launch); returns the kda_status code."""
+    return _abi.load().kda_check_latent_write(
+        ctypes.byref(latent_write_args(**kwargs)))
+
+
+def latent_write(*, stream=None, **kwargs) -> None:
+    """Each token's `latent` (and `rope_key`) into its place of a paged cache
+    (kda_latent_write_args in include/kda_recoverssm.h); `slot_mapping` as
+    `step_tables` gives it, of which the first entry per row of `latent` is
+    read, -1 writing nothing."""
+    _launch(_abi.load().kda_latent_write, latent_write_args(**kwargs), kwargs,
+            stream)
+
+
+def _table(block_table, request_indices, batch):
+    """(pointer, strides, rows, width) of a block table."""
+    if block_table.dim() != 2 or block_table.dtype != torch.int32:
+        raise ValueError("block_table must be a two-dimensional int32 tensor")
+    rows, width = block_table.shape
+    if request_indices is None and rows < batch:
+        raise ValueError("without request_indices the table needs a row per "
+                         "request")
+    return block_table.data_ptr(), block_table.stride(), rows, width
+
+
+def _workspace(t):
+    if not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def latent_attention_workspace_size(tokens: int, batch: int, num_heads: int,
+                                    latent_dim: int, rope_dim: int,
+                                    act_dtype: torch.dtype) -> int:
+    """Bytes of workspace for a latent attention over `tokens` rows of `batch`
+    requests.  Batches of other sizes may need more or less: a workspace for
+    several takes the largest."""
+    n = _abi.load().kda_latent_attention_workspace_size(
+        tokens, batch, num_heads, latent_dim, rope_dim,
+        _DT.get(act_dtype, -1))
+    if n <= 0:
+        raise ValueError("no latent attention has these sizes and dtype")
+    return n
+
+
+_LATENT_PACK = struct.Struct("<" + _pack_format(_abi.KdaLatentArgs))
+
+
+def latent_args(*, q, cache, out, query_start_loc, num_computed_tokens,
+                block_table, softmax_scale, workspace, lse=None,
+                request_indices=None, null_block_id=0) -> _abi.KdaLatentArgs:
+    """kda_latent_args for these tensors."""
+    B = query_start_loc.numel() - 1
+    if B < 0:
+        raise ValueError("query_start_loc needs batch + 1 entries")
+    table, strides, rows, width = _table(block_table, request_indices, B)
+    work, size = _workspace(workspace)
+    vals = (*_tensor_values(q), *_tensor_values(cache), *_tensor_values(out),
+            *_tensor_values(lse),
+            _ints(query_start_loc, "query_start_loc", B + 1),
+            _ints(num_computed_tokens, "num_computed_tokens", rows),
+            _ints(request_indices, "request_indices", B), table, *strides,
+            work, size, B, rows, width, null_block_id, float(softmax_scale),
+            0)
+    return _abi.KdaLatentArgs.from_buffer_copy(_LATENT_PACK.pack(*vals))
+
+
+def check_latent_attention(**kwargs) -> int:
+    """Host-only validation (no launch); returns the kda_status code."""
+    return _abi.load().kda_check_latent_attention(
+        ctypes.byref(latent_args(**kwargs)))
+
+
+def latent_attention(*, stream=None, **kwargs) -> None:
+    """Attention of single tokens, draft windows or short prompt pieces in
+    latent space, over a paged cache that holds their own entries already
+    (`latent_write`): each query sees its request's positions up to its own.
+    Arguments follow kda_latent_args in include/kda_recoverssm.h; `q` and
+    `out` are [tokens, heads, ..], `lse` (optional) receives the log of each
+    softmax's sum, `workspace` is scratch memory of
+    `latent_attention_workspace_size` bytes."""
+    _launch(_abi.load().kda_latent_attention, latent_args(**kwargs), kwargs,
+            stream)

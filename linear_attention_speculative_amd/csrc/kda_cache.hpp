@@ -1,0 +1,58 @@
+// Launch descriptors of the operators on token caches, blocks and logits
+// (latent attention, block life, changes of logits).  Not part of the public
+// ABI.
+#pragma once
+
+#include "kda_internal.hpp"
+
+namespace kda {
+
+// Where a request's tokens lie: offsets, computed tokens, block table.
+struct PagedParams {
+  const int32_t* qsl;        // [B + 1]
+  const int32_t* computed;   // per request row
+  const int32_t* req_idx;    // [B] or null (row = b)
+  const int32_t* table;      // [rows, width]
+  int64_t s_tab_row, s_tab_col;
+  const char* cache;
+  int64_t s_blk, s_tok;      // bytes
+  int32_t B, rows, width, block, null_id;
+  int64_t N;                 // blocks of the cache
+};
+
+struct LatentWriteParams {
+  const char* latent;
+  const char* rope;          // or null
+  int64_t s_lat, s_rope;     // bytes
+  char* cache;
+  int64_t s_blk, s_tok;      // bytes
+  const int64_t* slots;
+  int64_t total_slots;       // N * block
+  int32_t T, block, first_slot;  // (slots below first_slot are null)
+  int32_t lat_chunks, chunks;    // 16-byte chunks of the latent, of a row
+};
+int launch_latent_write(const LatentWriteParams& p, hipStream_t stream);
+
+struct LatentParams {
+  PagedParams c;
+  const char* q;
+  int64_t s_q_tok, s_q_head;     // bytes
+  char* out;
+  int64_t s_out_tok, s_out_head; // bytes
+  float* lse;                    // or null
+  int64_t s_lse_tok, s_lse_head;
+  char* work;
+  float scale;                   // softmax scale times log2 e
+  int32_t T, H;
+  int32_t group;                 // rows of a workgroup / 32: 1 or 2
+  int32_t workers;
+};
+// Row groups for these sizes, and workspace bytes.
+constexpr int kLatentWorkers = 256;
+int latent_groups(int64_t T, int64_t B, int64_t H, int R,
+                  bool bf16);
+int64_t latent_work_bytes(int group, int R);
+int launch_latent(const LatentParams& p, int R, int P, bool bf16,
+                  hipStream_t stream);
+
+}  // namespace kda

@@ -1,0 +1,300 @@
+// Host side of the operators on token caches: argument checks, translation of
+// the public descriptors into launch parameters, and the exported C entry
+// points.
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "kda_cache.hpp"
+#include "kda_host.hpp"
+#include "kda_recoverssm.h"
+
+using namespace kda::host;
+
+namespace {
+
+constexpr int64_t kI32Max = 0x7fffffff;
+constexpr int64_t kMaxThreads = 0xffffffff;   // work items of a launch
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// Strides of a tensor of 16-byte aligned rows (its last dimension).
+int check_rows(const kda_tensor& t, const char* name) {
+  const int last = t.ndim - 1, es = elem_size(t.dtype);
+  if (t.shape[last] > 1 && t.stride[last] != 1)
+    return fail(KDA_E_LAYOUT, "%s must have contiguous rows", name);
+  bool rows = true;
+  for (int i = 0; i < last; ++i) {
+    if (t.shape[i] <= 1) continue;
+    if (t.stride[i] < 0)
+      return fail(KDA_E_LAYOUT, "%s has a negative stride", name);
+    rows &= t.stride[i] * es % 16 == 0;
+  }
+  if (!rows || !aligned(t.data, 16))
+    return fail(KDA_E_UNALIGNED, "a row of %s does not start on a 16-byte "
+                "boundary", name);
+  return KDA_OK;
+}
+
+// Whether every element has a place of its own: each dimension's stride past
+// the extent of those of smaller stride.
+bool apart(const kda_tensor& t) {
+  int order[4] = {0, 1, 2, 3};
+  std::sort(order, order + t.ndim,
+            [&](int i, int j) { return t.stride[i] < t.stride[j]; });
+  int64_t extent = 0;          // from the first element to the last
+  for (int k = 0; k < t.ndim; ++k) {
+    const int i = order[k];
+    if (t.shape[i] == 0) return true;
+    if (t.shape[i] == 1) continue;
+    if (t.stride[i] <= extent) return false;
+    extent += (t.shape[i] - 1) * t.stride[i];
+  }
+  return true;
+}
+
+int check_cache(const kda_tensor& t) {
+  KDA_TRY(check_desc(t, "cache", 3));
+  if (t.shape[0] < 1 || t.shape[1] < 1)
+    return fail(KDA_E_SHAPE, "the cache must be [blocks, block_size, dims]");
+  if (t.shape[0] > kI32Max || t.shape[1] > kI32Max)
+    return fail(KDA_E_CAPACITY, "the cache's blocks exceed 2^31");
+  return check_rows(t, "cache");
+}
+
+bool latent_dims(int64_t R, int64_t P) {
+  return (R == 128 || R == 256 || R == 512) && (P == 0 || P == 64);
+}
+
+int plan_latent_write(const kda_latent_write_args* a,
+                      kda::LatentWriteParams* p) {
+  if (a == nullptr) return fail(KDA_E_ARG, "cache write arguments are NULL");
+  KDA_TRY(check_cache(a->cache));
+  KDA_TRY(check_desc(a->latent, "latent", 2));
+  const kda_tensor &lat = a->latent, &rope = a->rope_key, &cache = a->cache;
+  const int64_t T = lat.shape[0], W = cache.shape[2];
+  const bool has_rope = rope.ndim != 0;
+  const int es = elem_size(cache.dtype);
+  if (has_rope) KDA_TRY(check_desc(rope, "rope_key", 2));
+  if (lat.dtype != cache.dtype || (has_rope && rope.dtype != cache.dtype))
+    return fail(KDA_E_DTYPE,
+                "latent, rope_key and cache must share one dtype");
+  const int64_t P = has_rope ? rope.shape[1] : 0;
+  if ((has_rope && rope.shape[0] != T) || lat.shape[1] + P != W ||
+      lat.shape[1] < 1)
+    return fail(KDA_E_SHAPE,
+                "latent [T, R] and rope_key [T, P] must fill the cache's "
+                "R + P = %lld values",
+                (long long)W);
+  if (lat.shape[1] * es % 16 != 0 || P * es % 16 != 0)
+    return fail(KDA_E_UNSUPPORTED,
+                "latent and rope key take multiples of 16 bytes");
+  KDA_TRY(check_rows(lat, "latent"));
+  if (has_rope) KDA_TRY(check_rows(rope, "rope_key"));
+  if (!apart(cache)) return fail(KDA_E_LAYOUT, "the cache's entries overlap");
+  if (a->null_block_id < 0)
+    return fail(KDA_E_ARG, "null_block_id must not be negative");
+  if (T > kI32Max || T * (W * es / 16) > kMaxThreads - 256)
+    return fail(KDA_E_CAPACITY, "too many tokens");
+  if (T > 0 && !a->slot_mapping)
+    return fail(KDA_E_ARG, "slot_mapping is required");
+  if (!aligned(a->slot_mapping, 8))
+    return fail(KDA_E_UNALIGNED, "slot_mapping must be 8-byte aligned");
+  *p = kda::LatentWriteParams{};
+  p->latent = static_cast<const char*>(lat.data);
+  p->rope = static_cast<const char*>(rope.data);
+  p->s_lat = lat.stride[0] * es;
+  p->s_rope = has_rope ? rope.stride[0] * es : 0;
+  p->cache = static_cast<char*>(cache.data);
+  p->s_blk = cache.stride[0] * es;
+  p->s_tok = cache.stride[1] * es;
+  p->slots = a->slot_mapping;
+  p->total_slots = cache.shape[0] * cache.shape[1];
+  p->first_slot = (int64_t(a->null_block_id) + 1) * cache.shape[1];
+  p->T = int32_t(T);
+  p->block = int32_t(cache.shape[1]);
+  p->lat_chunks = int32_t(lat.shape[1] * es / 16);
+  p->chunks = int32_t(W * es / 16);
+  return KDA_OK;
+}
+
+// A cache seen through request rows and a block table.
+template <class Args>
+int plan_paged(const Args* a, const kda_tensor& cache, kda::PagedParams* p) {
+  if (a->batch < 0 || a->num_request_rows < 0 || a->block_table_width < 0)
+    return fail(KDA_E_ARG, "a count is negative");
+  if (a->null_block_id < 0)
+    return fail(KDA_E_ARG, "null_block_id must not be negative");
+  const int64_t sr = a->block_table_strides[0], sc = a->block_table_strides[1];
+  if (sr < 0 || sc < 0 || sr > kI32Max || sc > kI32Max)
+    return fail(KDA_E_LAYOUT, "a table stride is negative or exceeds 2^31");
+  if (a->num_request_rows > 0 && a->block_table_width > 0 && !a->block_table)
+    return fail(KDA_E_ARG, "block_table is required");
+  if (!aligned(a->block_table, 4) || !aligned(a->request_indices, 4))
+    return fail(KDA_E_UNALIGNED, "metadata pointers must be 4-byte aligned");
+  const int es = elem_size(cache.dtype);
+  *p = kda::PagedParams{};
+  p->req_idx = a->request_indices;
+  p->table = a->block_table;
+  p->s_tab_row = sr;
+  p->s_tab_col = sc;
+  p->cache = static_cast<const char*>(cache.data);
+  p->s_blk = cache.stride[0] * es;
+  p->s_tok = cache.stride[1] * es;
+  p->B = a->batch;
+  p->rows = a->num_request_rows;
+  p->width = a->block_table_width;
+  p->block = int32_t(cache.shape[1]);
+  p->null_id = a->null_block_id;
+  p->N = cache.shape[0];
+  return KDA_OK;
+}
+
+int64_t latent_bytes(int64_t T, int64_t B, int64_t H, int64_t R, int64_t P,
+                     bool bf16) {
+  if (T < 0 || B < 0 || H < 1 || B > kI32Max || T > kI32Max ||
+      H > kI32Max || T * H > kI32Max - 256 || !latent_dims(R, P))
+    return 0;
+  return kda::latent_work_bytes(kda::latent_groups(T, B, H, int(R), bf16),
+                                int(R));
+}
+
+struct LatentPlan {
+  kda::LatentParams p;
+  int R = 0, P = 0;
+  bool bf16 = false, noop = false;
+};
+
+// lse: F32 [T, H] in any strides, or empty.
+int check_lse(const kda_tensor& lse, int64_t T, int64_t H) {
+  if (lse.ndim == 0) return KDA_OK;
+  KDA_TRY(check_desc(lse, "lse", 2));
+  if (lse.dtype != KDA_F32)
+    return fail(KDA_E_DTYPE, "lse must be float32");
+  if (!shape_is(lse, T, H))
+    return fail(KDA_E_SHAPE, "lse must be [T, H]");
+  if (lse.stride[0] < 0 || lse.stride[1] < 0 || !apart(lse))
+    return fail(KDA_E_LAYOUT, "lse's entries overlap");
+  if (!aligned(lse.data, 4))
+    return fail(KDA_E_UNALIGNED, "lse must be 4-byte aligned");
+  return KDA_OK;
+}
+
+int plan_latent(const kda_latent_args* a, LatentPlan* plan) {
+  if (a == nullptr) return fail(KDA_E_ARG, "attention arguments are NULL");
+  kda::LatentParams& p = plan->p;
+  KDA_TRY(check_cache(a->cache));
+  KDA_TRY(check_desc(a->q, "q", 3));
+  KDA_TRY(check_desc(a->out, "out", 3));
+  const int32_t act = a->q.dtype;
+  if (a->cache.dtype != act || a->out.dtype != act)
+    return fail(KDA_E_DTYPE, "q, cache and out must share one dtype");
+  const int64_t T = a->q.shape[0], H = a->q.shape[1], W = a->q.shape[2];
+  const int64_t R = a->out.shape[2], P = W - R;
+  if (H < 1) return fail(KDA_E_SHAPE, "q must be [T, heads, R + P]");
+  if (a->out.shape[0] != T || a->out.shape[1] != H || a->cache.shape[2] != W)
+    return fail(KDA_E_SHAPE,
+                "q [T, H, R + P], out [T, H, R] and cache [N, block, R + P] "
+                "do not fit each other");
+  if (!latent_dims(R, P))
+    return fail(KDA_E_UNSUPPORTED,
+                "latent dims 128, 256 and 512 and rope dims 0 and 64 are "
+                "supported (got %lld and %lld)",
+                (long long)R, (long long)P);
+  KDA_TRY(check_rows(a->q, "q"));
+  KDA_TRY(check_rows(a->out, "out"));
+  if (!apart(a->out)) return fail(KDA_E_LAYOUT, "out's rows overlap");
+  KDA_TRY(check_lse(a->lse, T, H));
+  KDA_TRY(plan_paged(a, a->cache, &p.c));
+  const bool bf16 = act == KDA_BF16;
+  const int64_t need = latent_bytes(T, a->batch, H, R, P, bf16);
+  if (need == 0)
+    return fail(KDA_E_CAPACITY, "tokens and heads exceed 2^31 rows");
+  plan->noop = a->batch == 0 || T == 0;
+  if (!plan->noop) {
+    if (!a->query_start_loc ||
+        (a->num_request_rows > 0 && !a->num_computed_tokens))
+      return fail(KDA_E_ARG,
+                  "query_start_loc and num_computed_tokens are required");
+    if (!aligned(a->query_start_loc, 4) ||
+        !aligned(a->num_computed_tokens, 4))
+      return fail(KDA_E_UNALIGNED,
+                  "metadata pointers must be 4-byte aligned");
+    if (!a->workspace) return fail(KDA_E_ARG, "the workspace is required");
+    if (a->workspace_bytes < need)
+      return fail(KDA_E_CAPACITY,
+                  "the workspace holds %lld bytes; this attention needs %lld",
+                  (long long)a->workspace_bytes, (long long)need);
+    if (!aligned(a->workspace, 16))
+      return fail(KDA_E_UNALIGNED, "the workspace must be 16-byte aligned");
+  }
+  const int es = elem_size(act);
+  p.c.qsl = a->query_start_loc;
+  p.c.computed = a->num_computed_tokens;
+  p.q = static_cast<const char*>(a->q.data);
+  p.s_q_tok = a->q.stride[0] * es;
+  p.s_q_head = a->q.stride[1] * es;
+  p.out = static_cast<char*>(a->out.data);
+  p.s_out_tok = a->out.stride[0] * es;
+  p.s_out_head = a->out.stride[1] * es;
+  p.lse = a->lse.ndim ? static_cast<float*>(a->lse.data) : nullptr;
+  p.s_lse_tok = a->lse.stride[0];
+  p.s_lse_head = a->lse.stride[1];
+  p.work = static_cast<char*>(a->workspace);
+  p.scale = a->softmax_scale * kLog2e;
+  p.T = int32_t(T);
+  p.H = int32_t(H);
+  p.group = kda::latent_groups(T, a->batch, H, int(R), bf16);
+  p.workers = kda::kLatentWorkers;
+  plan->R = int(R);
+  plan->P = int(P);
+  plan->bf16 = bf16;
+  return KDA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int kda_check_latent_write(const kda_latent_write_args* args) {
+  g_err.clear();
+  kda::LatentWriteParams p;
+  return plan_latent_write(args, &p);
+}
+
+int kda_latent_write(const kda_latent_write_args* args, void* stream) {
+  g_err.clear();
+  kda::LatentWriteParams p;
+  KDA_TRY(plan_latent_write(args, &p));
+  if (p.T == 0) return KDA_OK;
+  return device_status(
+      kda::launch_latent_write(p, static_cast<hipStream_t>(stream)),
+      "kda_latent_write launch");
+}
+
+int64_t kda_latent_attention_workspace_size(int64_t tokens, int64_t batch,
+                                            int64_t num_heads,
+                                            int64_t latent_dim,
+                                            int64_t rope_dim,
+                                            int32_t act_dtype) {
+  if (elem_size(act_dtype) == 0) return 0;
+  return latent_bytes(tokens, batch, num_heads, latent_dim, rope_dim,
+                      act_dtype == KDA_BF16);
+}
+
+int kda_check_latent_attention(const kda_latent_args* args) {
+  g_err.clear();
+  LatentPlan plan;
+  return plan_latent(args, &plan);
+}
+
+int kda_latent_attention(const kda_latent_args* args, void* stream) {
+  g_err.clear();
+  LatentPlan plan;
+  KDA_TRY(plan_latent(args, &plan));
+  if (plan.noop) return KDA_OK;
+  return device_status(kda::launch_latent(plan.p, plan.R, plan.P, plan.bf16,
+                                          static_cast<hipStream_t>(stream)),
+                       "kda_latent_attention launch");
+}
+
+}  // extern "C"

@@ -18,6 +18,10 @@ the algebraic identity between the verify recurrence and the commit fold).
 The commit plan, the boundary fold and the conv compaction are pinned by
 multi-step simulations against a fresh recurrence over the accepted stream.
 """
+from .cache import (  # noqa: F401
+    latent_attention,
+    latent_write,
+)
 from .kda import (  # noqa: F401
     EPS,
     SOFTPLUS_THRESHOLD,

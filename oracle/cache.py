@@ -1,0 +1,83 @@
+"""fp64 reference for the operators on token caches.  TEST INFRASTRUCTURE ONLY
+(see the package docstring); written request by request from the definitions.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+
+def latent_write(*, latent, rope_key, cache, slot_mapping, null_block_id=0):
+    """Updated copy of the cache [N, block_size, R + P] (any dtype)."""
+    new = np.array(cache)
+    N, bs = new.shape[:2]
+    for t in range(len(latent)):
+        blk, at = divmod(int(slot_mapping[t]), bs)
+        if null_block_id < blk < N:
+            row = [latent[t]] if rope_key is None else [latent[t],
+                                                        rope_key[t]]
+            new[blk, at] = np.concatenate(row)
+    return new
+
+
+def places(*, row, length, block_table, block_size, num_blocks,
+           null_block_id=0):
+    """(block, slot) of a request row's first `length` positions, None for
+    those of null blocks or past the table."""
+    rows, width = block_table.shape
+    got = []
+    for j in range(length):
+        e, at = divmod(j, block_size)
+        blk = int(block_table[row, e]) if 0 <= row < rows and e < width \
+            else null_block_id
+        got.append((blk, at) if null_block_id < blk < num_blocks else None)
+    return got
+
+
+def softmax_sum(q, k, v, see, scale):
+    """One head: q [t, w], k [n, w], v [n, d], see [t, n].  Returns out [t, d],
+    lse [t], the weighted magnitudes sum_j p_j |v_j| [t, d], and the largest
+    sum of magnitudes behind a score, scale * sum_k |q_k k_jk| [t]."""
+    s = np.where(see, (q @ k.T) * scale, -np.inf)
+    top = s.max(axis=1, initial=-np.inf)
+    safe = np.where(np.isfinite(top), top, 0.0)
+    p = np.where(see, np.exp(s - safe[:, None]), 0.0)
+    total = p.sum(axis=1)
+    p /= np.where(total > 0, total, 1.0)[:, None]
+    with np.errstate(divide="ignore"):
+        lse = np.log(total) + safe
+    size = np.where(see, (np.abs(q) @ np.abs(k).T) * abs(scale), 0.0)
+    return p @ v, lse, p @ np.abs(v), size.max(axis=1, initial=0.0)
+
+
+def latent_attention(*, q, cache, out, lse, query_start_loc,
+                     num_computed_tokens, block_table, softmax_scale,
+                     latent_dim, request_indices=None, null_block_id=0):
+    """Absorbed attention over the paged cache.  Returns dict(out, lse) of
+    updated copies, and for bounds on errors `weight` (like out), `size` and
+    `keys` (like lse)."""
+    T, H, _ = q.shape
+    R, (N, bs) = latent_dim, cache.shape[:2]
+    out, lse = np.array(out, np.float64), np.array(lse, np.float64)
+    weight, size, keys = (np.zeros_like(out), np.zeros_like(lse),
+                          np.zeros_like(lse))
+    rows = block_table.shape[0]
+    for b in range(len(query_start_loc) - 1):
+        bos = min(max(int(query_start_loc[b]), 0), T)
+        eos = min(max(int(query_start_loc[b + 1]), bos), T)
+        row = b if request_indices is None else int(request_indices[b])
+        ok = 0 <= row < rows
+        c = max(int(num_computed_tokens[row]), 0) if ok else 0
+        at = places(row=row, length=c + eos - bos, block_table=block_table,
+                    block_size=bs, num_blocks=N,
+                    null_block_id=null_block_id) if ok else []
+        pos = np.array([j for j, p in enumerate(at) if p], np.int64)
+        e = np.array([cache[at[j]] for j in pos], np.float64).reshape(
+            len(pos), cache.shape[2])
+        see = pos[None] <= (c + np.arange(eos - bos))[:, None]
+        for h in range(H):
+            r = softmax_sum(q[bos:eos, h].astype(np.float64), e, e[:, :R],
+                            see, softmax_scale)
+            out[bos:eos, h], lse[bos:eos, h] = r[0], r[1]
+            weight[bos:eos, h], size[bos:eos, h] = r[2], r[3]
+            keys[bos:eos, h] = see.sum(axis=1)
+    return dict(out=out, lse=lse, weight=weight, size=size, keys=keys)
