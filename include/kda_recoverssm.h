@@ -47,6 +47,10 @@
  *       KDA layers, over a paged cache of one latent vector a token, for
  *       single tokens and draft windows.
  *
+ *   kda_latent_expand, kda_latent_prefill -- the same layers on prompts: keys
+ *       and values of every head from the cached latents, and the causal
+ *       attention over them.
+ *
  * plus host-only argument checks mirroring the pages' validation
  * (kernels page `_check_layouts`, `can_use_cute_recoverssm`; ops page
  * `kda_recoverssm_verify`, `KDARecoverSSMCommitContext.create/commit`).
@@ -575,6 +579,58 @@ typedef struct {
   int32_t pad_;
 } kda_latent_args;
 
+/* Arguments of kda_latent_expand: keys and values of every head from cached
+   latents.  Request b's key rows key_start_loc[b] .. key_start_loc[b + 1]
+   (clamped to [0, S]; not decreasing) are its positions 0, 1, ..; for the
+   entry (c_j | r_j) of such a position,
+     key[s, h] = W_h[0 .. D) c_j,  value[s, h] = W_h[D .. 2D) c_j,
+     rope_key[s] = r_j,
+   with fp32 sums, rounded once.  Positions of null blocks, past the block
+   table or of rows outside [0, num_request_rows) give +0.0.  Rows outside all
+   requests are not touched. */
+typedef struct {
+  kda_tensor cache;              /* act [N, block_size, R + P]; R a multiple
+                                    of 64, P of 8 values (fp32: 32, 4) */
+  kda_tensor weight;             /* act [H, 2 D, R] */
+  kda_tensor key;                /* act [S, H, D]; D is 64 or 128 */
+  kda_tensor rope_key;           /* act [S, P], or empty: not gathered */
+  kda_tensor value;              /* act [S, H, D] */
+  const int32_t* key_start_loc;  /* [batch + 1] */
+  const int32_t* request_indices;      /* [batch] or NULL: row = b */
+  const int32_t* block_table;          /* [num_request_rows, width] */
+  int64_t block_table_strides[2];      /* row, column (elements) */
+  int32_t batch;
+  int32_t num_request_rows;
+  int32_t block_table_width;
+  int32_t null_block_id;
+} kda_latent_expand_args;
+
+/* Arguments of kda_latent_prefill: causal attention with a key and a value
+   for every head and one rope key for all of them.  Request b has the queries
+   query_start_loc[b] .. query_start_loc[b + 1] (clamped to [0, T]) and the
+   keys key_start_loc[b] .. key_start_loc[b + 1] (clamped to [0, S]); the
+   queries stand at its last positions: query i of n_q sees the keys j <= n_k -
+   n_q + i,
+     s_j = softmax_scale * (q_th[0 .. D) . key[j, h] + q_th[D ..) . rope[j]),
+     out_th = sum_j softmax(s)_j value[j, h],  lse_th = ln sum_j e^(s_j).
+   A query without keys (n_k < n_q) gets +0.0 outputs and lse -inf.  A key or
+   value that is not finite spoils outputs of its head and request, also from
+   up to 255 tokens before it on.  Arithmetic is fp32; with bf16 the weights
+   are rounded to bf16 before they weigh the values.  Token rows outside all
+   requests are not touched. */
+typedef struct {
+  kda_tensor q;                  /* act [T, H, D + P]; D 64 or 128, P 0 or 64 */
+  kda_tensor key;                /* act [S, H, D] */
+  kda_tensor rope_key;           /* act [S, P]; empty for P = 0 */
+  kda_tensor value;              /* act [S, H, D] */
+  kda_tensor out;                /* act [T, H, D] */
+  kda_tensor lse;                /* F32 [T, H], or empty */
+  const int32_t* query_start_loc;  /* [batch + 1], not decreasing, both */
+  const int32_t* key_start_loc;
+  int32_t batch;
+  float softmax_scale;
+} kda_latent_prefill_args;
+
 /* Library ABI version (KDA_ABI_VERSION). */
 int kda_abi_version(void);
 
@@ -719,6 +775,15 @@ int64_t kda_latent_attention_workspace_size(int64_t tokens, int64_t batch,
    launches (two kernels). */
 int kda_check_latent_attention(const kda_latent_args* args);
 int kda_latent_attention(const kda_latent_args* args, void* stream);
+
+/* Host-only validation of the expansion's arguments, then its launch. */
+int kda_check_latent_expand(const kda_latent_expand_args* args);
+int kda_latent_expand(const kda_latent_expand_args* args, void* stream);
+
+/* Host-only validation of the prompt attention's arguments, then its
+   launch. */
+int kda_check_latent_prefill(const kda_latent_prefill_args* args);
+int kda_latent_prefill(const kda_latent_prefill_args* args, void* stream);
 
 /* Launch a one-workgroup kernel that sets counter[0..n) to 0 on `stream`
    (for a counter left non-zero by an aborted launch).  Uses no memset

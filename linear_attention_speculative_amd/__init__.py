@@ -6,10 +6,16 @@ include/kda_recoverssm.h); this package is its thin torch binding.
 from ._abi import LIB_PATH, load  # noqa: F401
 from .cache import (  # noqa: F401
     check_latent_attention,
+    check_latent_expand,
+    check_latent_prefill,
     check_latent_write,
     latent_args,
     latent_attention,
     latent_attention_workspace_size,
+    latent_expand,
+    latent_expand_args,
+    latent_prefill,
+    latent_prefill_args,
     latent_write,
     latent_write_args,
 )

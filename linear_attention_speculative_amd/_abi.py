@@ -46,6 +46,8 @@ EXPORTED = (
     "kda_check_latent_write", "kda_latent_write",
     "kda_latent_attention_workspace_size", "kda_check_latent_attention",
     "kda_latent_attention",
+    "kda_check_latent_expand", "kda_latent_expand",
+    "kda_check_latent_prefill", "kda_latent_prefill",
 )
 
 
@@ -205,6 +207,26 @@ class KdaLatentArgs(Structure):
     ]
 
 
+class KdaLatentExpandArgs(Structure):
+    _fields_ = [
+        ("cache", KdaTensor), ("weight", KdaTensor), ("key", KdaTensor),
+        ("rope_key", KdaTensor), ("value", KdaTensor),
+        ("key_start_loc", c_void_p), ("request_indices", c_void_p),
+        ("block_table", c_void_p), ("block_table_strides", c_int64 * 2),
+        ("batch", c_int32), ("num_request_rows", c_int32),
+        ("block_table_width", c_int32), ("null_block_id", c_int32),
+    ]
+
+
+class KdaLatentPrefillArgs(Structure):
+    _fields_ = [
+        ("q", KdaTensor), ("key", KdaTensor), ("rope_key", KdaTensor),
+        ("value", KdaTensor), ("out", KdaTensor), ("lse", KdaTensor),
+        ("query_start_loc", c_void_p), ("key_start_loc", c_void_p),
+        ("batch", c_int32), ("softmax_scale", c_float),
+    ]
+
+
 _LIB = None
 
 
@@ -280,7 +302,11 @@ def load() -> ctypes.CDLL:
             ("kda_check_latent_write", ("kda_latent_write",),
              KdaLatentWriteArgs),
             ("kda_check_latent_attention", ("kda_latent_attention",),
-             KdaLatentArgs)):
+             KdaLatentArgs),
+            ("kda_check_latent_expand", ("kda_latent_expand",),
+             KdaLatentExpandArgs),
+            ("kda_check_latent_prefill", ("kda_latent_prefill",),
+             KdaLatentPrefillArgs)):
         getattr(lib, check).restype = c_int
         getattr(lib, check).argtypes = [POINTER(args)]
         for name in launches:

@@ -115,3 +115,75 @@ def latent_attention(*, stream=None, **kwargs) -> None:
     `latent_attention_workspace_size` bytes."""
     _launch(_abi.load().kda_latent_attention, latent_args(**kwargs), kwargs,
             stream)
+
+
+_EXPAND_PACK = struct.Struct("<" + _pack_format(_abi.KdaLatentExpandArgs))
+
+
+def latent_expand_args(*, cache, weight, key, value, key_start_loc,
+                       block_table, rope_key=None, request_indices=None,
+                       null_block_id=0) -> _abi.KdaLatentExpandArgs:
+    """kda_latent_expand_args for these tensors."""
+    B = key_start_loc.numel() - 1
+    if B < 0:
+        raise ValueError("key_start_loc needs batch + 1 entries")
+    table, strides, rows, width = _table(block_table, request_indices, B)
+    vals = (*_tensor_values(cache), *_tensor_values(weight),
+            *_tensor_values(key), *_tensor_values(rope_key),
+            *_tensor_values(value),
+            _ints(key_start_loc, "key_start_loc", B + 1),
+            _ints(request_indices, "request_indices", B), table, *strides, B,
+            rows, width, null_block_id)
+    return _abi.KdaLatentExpandArgs.from_buffer_copy(_EXPAND_PACK.pack(*vals))
+
+
+def check_latent_expand(**kwargs) -> int:
+    """Host-only validation (no launch); returns the kda_status code."""
+    return _abi.load().kda_check_latent_expand(
+        ctypes.byref(latent_expand_args(**kwargs)))
+
+
+def latent_expand(*, stream=None, **kwargs) -> None:
+    """Keys and values of every head from the cached latents of whole requests
+    (kda_latent_expand_args in include/kda_recoverssm.h): rows
+    key_start_loc[b] .. key_start_loc[b + 1] of `key`, `value` and `rope_key`
+    (optional: the cached rope keys) are request b's positions from 0 on.
+    `weight` is [heads, 2 * head_dim, latent], keys' rows before values'."""
+    _launch(_abi.load().kda_latent_expand, latent_expand_args(**kwargs),
+            kwargs, stream)
+
+
+_PROMPT_PACK = struct.Struct("<" + _pack_format(_abi.KdaLatentPrefillArgs))
+
+
+def latent_prefill_args(*, q, key, value, out, query_start_loc, key_start_loc,
+                        softmax_scale, rope_key=None,
+                        lse=None) -> _abi.KdaLatentPrefillArgs:
+    """kda_latent_prefill_args for these tensors."""
+    B = query_start_loc.numel() - 1
+    if B < 0:
+        raise ValueError("query_start_loc needs batch + 1 entries")
+    vals = (*_tensor_values(q), *_tensor_values(key),
+            *_tensor_values(rope_key), *_tensor_values(value),
+            *_tensor_values(out), *_tensor_values(lse),
+            _ints(query_start_loc, "query_start_loc", B + 1),
+            _ints(key_start_loc, "key_start_loc", B + 1), B,
+            float(softmax_scale))
+    return _abi.KdaLatentPrefillArgs.from_buffer_copy(
+        _PROMPT_PACK.pack(*vals))
+
+
+def check_latent_prefill(**kwargs) -> int:
+    """Host-only validation (no launch); returns the kda_status code."""
+    return _abi.load().kda_check_latent_prefill(
+        ctypes.byref(latent_prefill_args(**kwargs)))
+
+
+def latent_prefill(*, stream=None, **kwargs) -> None:
+    """Causal attention of prompts, or pieces of prompts behind computed
+    tokens, over expanded keys and values (`latent_expand`): request b's
+    queries are its last positions among its keys.  Arguments follow
+    kda_latent_prefill_args in include/kda_recoverssm.h; the last values of a
+    query go with `rope_key`, which all heads share."""
+    _launch(_abi.load().kda_latent_prefill, latent_prefill_args(**kwargs),
+            kwargs, stream)

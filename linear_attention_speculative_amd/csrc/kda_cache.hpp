@@ -55,4 +55,42 @@ int64_t latent_work_bytes(int group, int R);
 int launch_latent(const LatentParams& p, int R, int P, bool bf16,
                   hipStream_t stream);
 
+struct ExpandParams {
+  PagedParams c;                 // qsl: the key rows' offsets; no lengths
+  const char* w;                 // [H, 2 D, R]
+  int64_t s_w_head, s_w_row;     // bytes, from here on
+  char* key;
+  int64_t s_k_tok, s_k_head;
+  char* value;
+  int64_t s_v_tok, s_v_head;
+  char* rope;                    // or null
+  int64_t s_rope;
+  int32_t S, H, D, R;
+  int32_t rope_chunks;           // of 16 bytes
+};
+int launch_latent_expand(const ExpandParams& p, bool bf16,
+                         hipStream_t stream);
+
+struct PromptParams {
+  const char* q;
+  int64_t s_q_tok, s_q_head;     // bytes
+  const char* key;
+  int64_t s_k_tok, s_k_head;
+  const char* value;
+  int64_t s_v_tok, s_v_head;
+  const char* rope;
+  int64_t s_rope;
+  char* out;
+  int64_t s_out_tok, s_out_head;
+  float* lse;                    // or null
+  int64_t s_lse_tok, s_lse_head;
+  const int32_t* qsl;
+  const int32_t* ksl;
+  float scale;                   // softmax scale times log2 e
+  int32_t T, S, H, B;
+};
+int64_t prompt_tiles(int64_t T, int64_t B);
+int launch_latent_prefill(const PromptParams& p, int D, int P, bool bf16,
+                          hipStream_t stream);
+
 }  // namespace kda

@@ -251,6 +251,162 @@ int plan_latent(const kda_latent_args* a, LatentPlan* plan) {
   return KDA_OK;
 }
 
+// key and value [S, H, D] of one dtype, rope_key [S, P] or empty.
+int check_keys(const kda_tensor& key, const kda_tensor& value,
+               const kda_tensor& rope, int64_t P) {
+  KDA_TRY(check_desc(key, "key", 3));
+  KDA_TRY(check_desc(value, "value", 3));
+  const int64_t S = key.shape[0], H = key.shape[1], D = key.shape[2];
+  if (value.dtype != key.dtype)
+    return fail(KDA_E_DTYPE, "key and value must share one dtype");
+  if (H < 1 || !shape_is(value, S, H, D))
+    return fail(KDA_E_SHAPE, "key and value must be [S, heads, D]");
+  if (D != 64 && D != 128)
+    return fail(KDA_E_UNSUPPORTED, "head dims 64 and 128 are supported "
+                "(got %lld)", (long long)D);
+  KDA_TRY(check_rows(key, "key"));
+  KDA_TRY(check_rows(value, "value"));
+  if (rope.ndim == 0) return KDA_OK;
+  KDA_TRY(check_desc(rope, "rope_key", 2));
+  if (rope.dtype != key.dtype)
+    return fail(KDA_E_DTYPE, "key and rope_key must share one dtype");
+  if (!shape_is(rope, S, P))
+    return fail(KDA_E_SHAPE, "rope_key must be [S, P] = [%lld, %lld]",
+                (long long)S, (long long)P);
+  return P > 0 ? check_rows(rope, "rope_key") : KDA_OK;
+}
+
+int plan_expand(const kda_latent_expand_args* a, kda::ExpandParams* p,
+                bool* bf16) {
+  if (a == nullptr) return fail(KDA_E_ARG, "expansion arguments are NULL");
+  KDA_TRY(check_cache(a->cache));
+  KDA_TRY(check_desc(a->weight, "weight", 3));
+  const kda_tensor& w = a->weight;
+  const int64_t R = w.shape[2], P = a->cache.shape[2] - R;
+  KDA_TRY(check_keys(a->key, a->value, a->rope_key, P));
+  const int64_t S = a->key.shape[0], H = a->key.shape[1], D = a->key.shape[2];
+  if (a->cache.dtype != a->key.dtype || w.dtype != a->key.dtype)
+    return fail(KDA_E_DTYPE,
+                "cache, weight, key and value must share one dtype");
+  if (!shape_is(w, H, 2 * D, R) || P < 0)
+    return fail(KDA_E_SHAPE,
+                "weight must be [H, 2 D, R] = [%lld, %lld, R <= %lld]",
+                (long long)H, (long long)(2 * D),
+                (long long)a->cache.shape[2]);
+  const int es = elem_size(w.dtype);
+  if (R < 1 || R * es % 128 != 0 || P * es % 16 != 0)
+    return fail(KDA_E_UNSUPPORTED,
+                "latents take multiples of 128 bytes, rope keys of 16");
+  KDA_TRY(check_rows(w, "weight"));
+  if (!apart(a->key) || !apart(a->value) ||
+      (a->rope_key.ndim && !apart(a->rope_key)))
+    return fail(KDA_E_LAYOUT, "rows of key, value or rope_key overlap");
+  KDA_TRY(plan_paged(a, a->cache, &p->c));
+  if (S > kI32Max - 256 || H > kI32Max / 256 ||
+      (H * 2 * D + 127) / 128 > 65535 ||
+      (S + 127) / 128 * ((H * 2 * D + 127) / 128) > kMaxThreads / 256)
+    return fail(KDA_E_CAPACITY, "key rows and heads exceed the grid");
+  if (a->batch > 0 && S > 0 && !a->key_start_loc)
+    return fail(KDA_E_ARG, "key_start_loc is required");
+  if (!aligned(a->key_start_loc, 4))
+    return fail(KDA_E_UNALIGNED, "metadata pointers must be 4-byte aligned");
+  p->c.qsl = a->key_start_loc;
+  p->w = static_cast<const char*>(w.data);
+  p->s_w_head = w.stride[0] * es;
+  p->s_w_row = w.stride[1] * es;
+  p->key = static_cast<char*>(a->key.data);
+  p->s_k_tok = a->key.stride[0] * es;
+  p->s_k_head = a->key.stride[1] * es;
+  p->value = static_cast<char*>(a->value.data);
+  p->s_v_tok = a->value.stride[0] * es;
+  p->s_v_head = a->value.stride[1] * es;
+  p->rope = static_cast<char*>(a->rope_key.data);
+  p->s_rope = a->rope_key.stride[0] * es;
+  p->S = int32_t(S);
+  p->H = int32_t(H);
+  p->D = int32_t(D);
+  p->R = int32_t(R);
+  p->rope_chunks = a->rope_key.ndim ? int32_t(P * es / 16) : 0;
+  *bf16 = w.dtype == KDA_BF16;
+  return KDA_OK;
+}
+
+struct PromptPlan {
+  kda::PromptParams p;
+  int D = 0, P = 0;
+  bool bf16 = false, noop = false;
+};
+
+int plan_prompt(const kda_latent_prefill_args* a, PromptPlan* plan) {
+  if (a == nullptr)
+    return fail(KDA_E_ARG, "prompt attention arguments are NULL");
+  KDA_TRY(check_desc(a->q, "q", 3));
+  KDA_TRY(check_desc(a->out, "out", 3));
+  const int64_t T = a->q.shape[0], H = a->q.shape[1];
+  const int64_t D = a->out.shape[2], P = a->q.shape[2] - D;
+  const int32_t act = a->q.dtype;
+  KDA_TRY(check_keys(a->key, a->value, a->rope_key, P));
+  if (a->key.dtype != act || a->out.dtype != act)
+    return fail(KDA_E_DTYPE, "q, key, value and out must share one dtype");
+  if (H < 1 || !shape_is(a->out, T, H) || a->key.shape[1] != H ||
+      a->key.shape[2] != D)
+    return fail(KDA_E_SHAPE,
+                "q [T, H, D + P], out [T, H, D] and key [S, H, D] do not fit "
+                "each other");
+  if (P != 0 && P != 64)
+    return fail(KDA_E_UNSUPPORTED, "rope dims 0 and 64 are supported (got "
+                "%lld)", (long long)P);
+  if ((P > 0) != (a->rope_key.ndim != 0))
+    return fail(KDA_E_SHAPE, "rope_key goes with q's last %lld values",
+                (long long)P);
+  KDA_TRY(check_rows(a->q, "q"));
+  KDA_TRY(check_rows(a->out, "out"));
+  if (!apart(a->out)) return fail(KDA_E_LAYOUT, "out's rows overlap");
+  KDA_TRY(check_lse(a->lse, T, H));
+  if (a->batch < 0) return fail(KDA_E_ARG, "batch is negative");
+  const int64_t S = a->key.shape[0];
+  if (T > kI32Max - 512 || S > kI32Max - 512 || H > kI32Max ||
+      kda::prompt_tiles(T, a->batch) > kMaxThreads / 512 / H)
+    return fail(KDA_E_CAPACITY, "tokens, requests and heads exceed the grid");
+  plan->noop = T == 0 || a->batch == 0;
+  if (!plan->noop && (!a->query_start_loc || !a->key_start_loc))
+    return fail(KDA_E_ARG,
+                "query_start_loc and key_start_loc are required");
+  if (!aligned(a->query_start_loc, 4) || !aligned(a->key_start_loc, 4))
+    return fail(KDA_E_UNALIGNED, "metadata pointers must be 4-byte aligned");
+  const int es = elem_size(act);
+  kda::PromptParams& p = plan->p;
+  p = kda::PromptParams{};
+  p.q = static_cast<const char*>(a->q.data);
+  p.s_q_tok = a->q.stride[0] * es;
+  p.s_q_head = a->q.stride[1] * es;
+  p.key = static_cast<const char*>(a->key.data);
+  p.s_k_tok = a->key.stride[0] * es;
+  p.s_k_head = a->key.stride[1] * es;
+  p.value = static_cast<const char*>(a->value.data);
+  p.s_v_tok = a->value.stride[0] * es;
+  p.s_v_head = a->value.stride[1] * es;
+  p.rope = static_cast<const char*>(a->rope_key.data);
+  p.s_rope = a->rope_key.stride[0] * es;
+  p.out = static_cast<char*>(a->out.data);
+  p.s_out_tok = a->out.stride[0] * es;
+  p.s_out_head = a->out.stride[1] * es;
+  p.lse = a->lse.ndim ? static_cast<float*>(a->lse.data) : nullptr;
+  p.s_lse_tok = a->lse.stride[0];
+  p.s_lse_head = a->lse.stride[1];
+  p.qsl = a->query_start_loc;
+  p.ksl = a->key_start_loc;
+  p.scale = a->softmax_scale * kLog2e;
+  p.T = int32_t(T);
+  p.S = int32_t(S);
+  p.H = int32_t(H);
+  p.B = a->batch;
+  plan->D = int(D);
+  plan->P = int(P);
+  plan->bf16 = act == KDA_BF16;
+  return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -295,6 +451,41 @@ int kda_latent_attention(const kda_latent_args* args, void* stream) {
   return device_status(kda::launch_latent(plan.p, plan.R, plan.P, plan.bf16,
                                           static_cast<hipStream_t>(stream)),
                        "kda_latent_attention launch");
+}
+
+int kda_check_latent_expand(const kda_latent_expand_args* args) {
+  g_err.clear();
+  kda::ExpandParams p{};
+  bool bf16 = false;
+  return plan_expand(args, &p, &bf16);
+}
+
+int kda_latent_expand(const kda_latent_expand_args* args, void* stream) {
+  g_err.clear();
+  kda::ExpandParams p{};
+  bool bf16 = false;
+  KDA_TRY(plan_expand(args, &p, &bf16));
+  if (p.S == 0 || p.c.B == 0) return KDA_OK;
+  return device_status(
+      kda::launch_latent_expand(p, bf16, static_cast<hipStream_t>(stream)),
+      "kda_latent_expand launch");
+}
+
+int kda_check_latent_prefill(const kda_latent_prefill_args* args) {
+  g_err.clear();
+  PromptPlan plan;
+  return plan_prompt(args, &plan);
+}
+
+int kda_latent_prefill(const kda_latent_prefill_args* args, void* stream) {
+  g_err.clear();
+  PromptPlan plan;
+  KDA_TRY(plan_prompt(args, &plan));
+  if (plan.noop) return KDA_OK;
+  return device_status(
+      kda::launch_latent_prefill(plan.p, plan.D, plan.P, plan.bf16,
+                                 static_cast<hipStream_t>(stream)),
+      "kda_latent_prefill launch");
 }
 
 }  // extern "C"

@@ -128,4 +128,137 @@ __device__ __forceinline__ u4 load_transposed(const char* tile, int t,
   return u4{x[0], x[1], y[0], y[1]};
 }
 
+// The running maximum is only moved when it is passed by more than this (in
+// powers of two): weights of up to 2^kSlack cost nothing in fp32 or bf16, and
+// moving it costs a pass over O.
+constexpr float kSlack = 8.0f;
+
+// What places without a token read (static: a copy for each source file).
+static __device__ const char kZeros[4096] = {};
+
+// Wait for the oldest of the steps under way: `left` steps remain, of which up
+// to AHEAD + 1 are under way, with MINE loads each.
+template <int AHEAD, int MINE>
+__device__ __forceinline__ void wait_tile(int left,
+                                          std::integral_constant<int, MINE>) {
+  if constexpr (AHEAD * MINE < 64 && AHEAD > 0) {
+    if (left > AHEAD) return wait_vm<AHEAD * MINE>();
+    wait_tile<AHEAD - 1>(left, std::integral_constant<int, MINE>());
+  } else {
+    wait_vm<0>();
+  }
+}
+
+// 32 tokens against a wave's 32 queries, one a lane: S^T = K q^T, the softmax's
+// running maximum (`top`, in powers of two) and sum, O^T += V^T P^T.  Keys are
+// two tiles side by side (CH and CHP chunks a row), values NB blocks of 32 of a
+// tile's rows from block `blk` on.  `live`: which tokens are there; the lane's
+// query sees the first `left` of them.
+template <bool BF16, int CH, int CHP, int CHV, int KF, int NB>
+__device__ __forceinline__ void attend(const char* keys, const char* ropes,
+                                       const char* values, int blk,
+                                       const u4 (&q)[KF], f16v (&o)[NB],
+                                       float& top, float& sum, uint32_t live,
+                                       int left, float scale) {
+  constexpr int kTile = 32;
+  // (operands are read a few ahead of their products; without the borders
+  // the compiler reads them all at once and has no registers left)
+  constexpr int G = 3;
+  const int lane = fresh_tid() & 63, half = lane >> 5;
+  auto key = [&](int k) -> u4 {
+    const int ch = 2 * k + half;
+    const char* a =
+        2 * k < CH ? keys + place<CH>(lane & 31, ch) * 16
+                   : ropes + place<(CHP > 0 ? CHP : 8)>(lane & 31, ch - CH) *
+                                 16;
+    return *reinterpret_cast<const u4*>(a);
+  };
+  f16v x0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x0[i] = 0.0f;
+  u4 kk[2][G];
+#pragma unroll
+  for (int j = 0; j < G && j < KF; ++j) kk[0][j] = key(j);
+#pragma unroll
+  for (int k = 0; k < KF; k += G) {
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+      if (k + G + j < KF) kk[(k / G + 1) & 1][j] = key(k + G + j);
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+      if (k + j < KF) x0 = mma<BF16>(kk[(k / G) & 1][j], q[k + j], x0);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  float x[16], m = -INFINITY;
+  if (__all(left == kTile) && live == 0xffffffffu) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = x0[i] * scale;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int t = acc_row(i, half);
+      const bool see = t < left && ((live >> t) & 1);
+      x[i] = see ? x0[i] * scale : -INFINITY;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) m = fmaxf(m, x[i]);
+  m = halves_max(m);
+  if (__any(m > top + kSlack)) {
+    const float to = fmaxf(top, m);
+    const float by = top == -INFINITY ? 0.0f : exp2f(top - to);
+    top = to;
+    sum *= by;
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) o[k][i] *= by;
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    x[i] = __builtin_amdgcn_exp2f(x[i] - base);
+    sum += x[i];
+  }
+  if constexpr (BF16) {
+    u4 pr[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      pr[t] = u4{pack_bf16(x[8 * t], x[8 * t + 1]),
+                 pack_bf16(x[8 * t + 2], x[8 * t + 3]),
+                 pack_bf16(x[8 * t + 4], x[8 * t + 5]),
+                 pack_bf16(x[8 * t + 6], x[8 * t + 7])};
+    u4 v[2][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      v[0][t] = load_transposed<CHV>(values, 16 * t, blk);
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (k + 1 < NB)
+          v[(k + 1) & 1][t] =
+              load_transposed<CHV>(values, 16 * t, blk + k + 1);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) o[k] = mma<true>(v[k & 1][t], pr[t], o[k]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const int t = acc_row(i, half);
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int e = 32 * (blk + k) + (lane & 31);
+        const float v = *reinterpret_cast<const float*>(
+            values + place<CHV>(t, e / 4) * 16 + e % 4 * 4);
+        o[k] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, x[i], o[k], 0, 0, 0);
+      }
+      if (i & 1) __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
 }  // namespace kda

@@ -1,0 +1,394 @@
+// Attention over prompts in the expanded form: keys and values of every head
+// from the cached latents, and the causal attention that reads them.
+//
+//   k_j,h = W_k,h c_j,  v_j,h = W_v,h c_j            kda_latent_expand_kernel
+//   s_j = scale (q_h . (k_j,h | r_j)),  out_h = softmax(s) v_.,h
+//                                                   kda_latent_prefill_kernel
+//
+// Per pair of a query and a key this costs 2 (2 D + P) operations a head, where
+// the absorbed form has 2 (2 R + P): for prompts it is worth the one product
+// with W.
+//
+// The attention takes both products transposed, with a query a lane (see
+// attend() in kda_mma.hpp): a wave has 32 queries of one head, a workgroup
+// eight waves, which share 64 keys and values at a time in LDS.  The expansion
+// is a matrix product of gathered cache rows with W, 128 x 128 a workgroup.
+#include "kda_cache.hpp"
+#include "kda_mma.hpp"
+
+namespace kda {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+
+// ---- expansion ---------------------------------------------------------------
+
+constexpr int kExpand = 128;       // tokens and columns of a workgroup
+
+// Number of the request of row t: the last b with start[b] <= t.
+__device__ __forceinline__ int request_of(const int32_t* start, int B, int t) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int m = (lo + hi) >> 1;
+    if (start[m] <= t)
+      lo = m;
+    else
+      hi = m;
+  }
+  return lo;
+}
+
+// Cache entry of key row s, null where nothing is written, kZeros where its
+// block is null.
+__device__ __forceinline__ const char* key_entry(const ExpandParams& p,
+                                                 int s) {
+  const PagedParams& c = p.c;
+  if (s >= p.S || s < c.qsl[0] || s >= c.qsl[c.B]) return nullptr;
+  const int b = request_of(c.qsl, c.B, s);
+  const int row = c.req_idx ? c.req_idx[b] : b;
+  const int pos = s - c.qsl[b];
+  const int e = pos / c.block;
+  if (row < 0 || row >= c.rows || e >= c.width || pos < 0) return kZeros;
+  const int id = c.table[row * c.s_tab_row + e * c.s_tab_col];
+  if (id <= c.null_id || id >= c.N) return kZeros;
+  return c.cache + id * c.s_blk + int64_t(pos - e * c.block) * c.s_tok;
+}
+
+// 128 tokens x 128 columns, four waves of 64 x 64; the summed index 128 bytes
+// at a time.  The product is taken transposed (columns of W as rows), so that a
+// lane ends with four neighbouring values of one token.
+template <bool BF16>
+__global__ void __launch_bounds__(256, 2)
+    kda_latent_expand_kernel(ExpandParams p) {
+  constexpr int ES = BF16 ? 2 : 4;
+  constexpr int kPart = kExpand * 128;         // bytes of one operand's tile
+  extern __shared__ __align__(16) char smem[];
+  __shared__ const char* entry[kExpand];
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = uniform(tid >> 6);
+  const int cols = p.H * 2 * p.D;
+  const int s0 = blockIdx.x * kExpand, n0 = blockIdx.y * kExpand;
+  if (tid < kExpand) entry[tid] = key_entry(p, s0 + tid);
+  __syncthreads();
+  // the rope keys, by the first column of workgroups
+  if (blockIdx.y == 0 && p.rope_chunks > 0) {
+    for (int i = tid; i < kExpand * p.rope_chunks; i += 256) {
+      const int t = i / p.rope_chunks, ch = i - t * p.rope_chunks;
+      const char* e = entry[t];
+      if (e)
+        *reinterpret_cast<u4*>(p.rope + (s0 + t) * p.s_rope + ch * 16) =
+            *reinterpret_cast<const u4*>(
+                e == kZeros ? e : e + int64_t(p.R) * ES + ch * 16);
+    }
+  }
+  // a wave's loads: 8 rows of 128 bytes each, four of tokens, four of W
+  const char* src[8];
+  const int ch = lane & 7;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int rw = (wave * 4 + j) * 8 + (lane >> 3);
+    const char* e = entry[rw];
+    // (zeros' row is shorter than R: its loads stay at its start)
+    src[j] = e == nullptr || e == kZeros ? nullptr
+                                         : e + (ch ^ swizzle<8>(rw)) * 16;
+    const int n = n0 + rw;
+    const int h = n / (2 * p.D), d = n - h * 2 * p.D;
+    src[4 + j] = n < cols ? p.w + h * p.s_w_head + d * p.s_w_row +
+                                (ch ^ swizzle<8>(rw)) * 16
+                          : nullptr;
+  }
+  const uint32_t lds0 = lds_addr(smem);
+  auto stage = [&](int k, int buf) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      load_lds(src[j] ? src[j] + k * 128 : kZeros,
+               uniform(lds0 + buf * 2 * kPart + (j >> 2) * kPart +
+                       (wave * 4 + (j & 3)) * 1024));
+  };
+  f16v acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  const int wt = (wave & 1) * 64, wn = (wave >> 1) * 64;
+  const int steps = p.R * ES / 128;
+  stage(0, 0);
+#pragma unroll 1
+  for (int k = 0; k < steps; ++k) {
+    wait_vm<0>();
+    lds_barrier();
+    if (k + 1 < steps) stage(k + 1, (k + 1) & 1);
+    const char* tok = smem + (k & 1) * 2 * kPart;
+    const char* w = tok + kPart;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      u4 a[2], b[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        a[i] = *reinterpret_cast<const u4*>(
+            w + place<8>(wn + 32 * i + (lane & 31), 2 * c + half) * 16);
+        b[i] = *reinterpret_cast<const u4*>(
+            tok + place<8>(wt + 32 * i + (lane & 31), 2 * c + half) * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mma<BF16>(a[i], b[j],
+                                                          acc[i][j]);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int t = wt + 32 * j + (lane & 31);
+    const int64_t s = s0 + t;
+    if (entry[t] == nullptr) continue;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const int n = n0 + wn + 32 * i + acc_row(e, half);
+        if (n >= cols) continue;
+        const int h = n / (2 * p.D), d = n - h * 2 * p.D;
+        char* dst = d < p.D ? p.key + s * p.s_k_tok + h * p.s_k_head + d * ES
+                            : p.value + s * p.s_v_tok + h * p.s_v_head +
+                                  (d - p.D) * ES;
+        const f16v& v = acc[i][j];
+        if constexpr (BF16)
+          *reinterpret_cast<u2*>(dst) = u2{pack_bf16(v[e], v[e + 1]),
+                                           pack_bf16(v[e + 2], v[e + 3])};
+        else
+          *reinterpret_cast<f4*>(dst) = f4{v[e], v[e + 1], v[e + 2],
+                                           v[e + 3]};
+      }
+  }
+}
+
+// ---- attention -----------------------------------------------------------------
+
+constexpr int kWaves = 8;
+constexpr int kQueries = 32 * kWaves;
+constexpr int kKeys = 64;          // keys of a step
+
+template <bool BF16, int D, int P>
+struct Prompt {
+  static constexpr int ES = BF16 ? 2 : 4;
+  static constexpr int CH = D * ES / 16, CHP = P * ES / 16;
+  static constexpr int KF = (D + P) * ES / 32;
+  static constexpr int NB = D / 32;
+  static constexpr int LK = kKeys * CH / 64, LP = kKeys * CHP / 64;  // loads
+  static constexpr int MINE = (2 * LK + LP) / kWaves;
+  static constexpr int TILE = kKeys * (2 * CH + CHP) * 16;
+  static constexpr int NBUF = BF16 ? 3 : 1;
+  static constexpr int ROPE = kKeys * CH * 16, VALUE = ROPE + kKeys * CHP * 16;
+  static_assert(LK % kWaves == 0 && LP % kWaves == 0, "loads");
+};
+
+template <bool BF16, int D, int P>
+__global__ void __launch_bounds__(64 * kWaves, 2)
+    kda_latent_prefill_kernel(PromptParams p) {
+  using Z = Prompt<BF16, D, P>;
+  extern __shared__ __align__(16) char smem[];
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = uniform(tid >> 6);
+  // blocks i, i + 8, .. are on one XCD: a head's query tiles, which read the
+  // same keys, where H is a multiple of 8.  The last tiles, which have the
+  // most keys, come first.
+  const int h = blockIdx.x % p.H, item = blockIdx.x / p.H;
+  int64_t* red = reinterpret_cast<int64_t*>(smem);
+  int32_t* found = reinterpret_cast<int32_t*>(smem + 64);
+  if (tid == 0) found[0] = -1;
+  int64_t done = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 64 * kWaves) {
+    // requests from the last to the first
+    const int b = p.B - 1 - (b0 + tid);
+    int v = 0;
+    if (b >= 0) {
+      const int bos = min(max(p.qsl[b], 0), p.T);
+      v = (min(max(p.qsl[b + 1], bos), p.T) - bos + kQueries - 1) / kQueries;
+    }
+    int64_t upto = v;
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+      const int64_t o = __shfl_up(upto, s);
+      if (lane >= s) upto += o;
+    }
+    __syncthreads();
+    if (lane == 63) red[wave] = upto;
+    __syncthreads();
+    int64_t before = done;
+    for (int k = 0; k < wave; ++k) before += red[k];
+    const int64_t at = before + upto - v;
+    if (v > 0 && at <= item && item < at + v) {
+      found[0] = b;
+      found[1] = v - 1 - int(item - at);       // its last tiles first
+    }
+    for (int k = 0; k < kWaves; ++k) done += red[k];
+    if (done > item) break;
+  }
+  __syncthreads();
+  const int b = uniform(found[0]), tile = uniform(found[1]);
+  __syncthreads();
+  if (b < 0) return;
+  const int bos = min(max(p.qsl[b], 0), p.T);
+  const int len = min(max(p.qsl[b + 1], bos), p.T) - bos;
+  const int kbos = min(max(p.ksl[b], 0), p.S);
+  const int keys = min(max(p.ksl[b + 1], kbos), p.S) - kbos;
+  const int ahead = keys - len;                // keys in front of the queries
+  const int t0 = tile * kQueries + wave * 32;
+  const int tok = t0 + (lane & 31);
+  // keys of this lane's query, of the wave and of the workgroup
+  const int lim = ahead + min(tok, len - 1) + 1;
+  const int wave_lim = t0 < len ? ahead + min(t0 + 32, len) : 0;
+  const int n = ahead + min((tile + 1) * kQueries, len);
+  const int steps = n > 0 ? (n + kKeys - 1) / kKeys : 0;
+
+  u4 q[Z::KF];
+  {
+    const char* src = p.q + int64_t(bos + min(tok, len - 1)) * p.s_q_tok +
+                      h * p.s_q_head + half * 16;
+#pragma unroll
+    for (int k = 0; k < Z::KF; ++k)
+      q[k] = *reinterpret_cast<const u4*>(src + 32 * k);
+  }
+  f16v o[Z::NB];
+#pragma unroll
+  for (int k = 0; k < Z::NB; ++k)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[k][i] = 0.0f;
+  float top = -INFINITY, sum = 0.0f;
+
+  const char* key = p.key + int64_t(kbos) * p.s_k_tok + h * p.s_k_head;
+  const char* value = p.value + int64_t(kbos) * p.s_v_tok + h * p.s_v_head;
+  const char* rope = p.rope + int64_t(kbos) * p.s_rope;
+  const uint32_t lds0 = lds_addr(smem);
+  auto stage = [&](int step, int buf) {
+    const int l = fresh_tid() & 63;
+#pragma unroll
+    for (int j = 0; j < Z::MINE; ++j) {
+      const int i = uniform(j * kWaves + wave);
+      const char* src;
+      int rw;
+      if (j * kWaves < Z::LK) {
+        rw = i * (64 / Z::CH) + l / Z::CH;
+        src = key + int64_t(step * kKeys + rw) * p.s_k_tok +
+              ((l % Z::CH) ^ swizzle<Z::CH>(rw)) * 16;
+      } else if (j * kWaves < Z::LK + Z::LP) {
+        constexpr int CP = Z::CHP > 0 ? Z::CHP : 8;
+        rw = (i - Z::LK) * (64 / CP) + l / CP;
+        src = rope + int64_t(step * kKeys + rw) * p.s_rope +
+              ((l % CP) ^ swizzle<CP>(rw)) * 16;
+      } else {
+        rw = (i - Z::LK - Z::LP) * (64 / Z::CH) + l / Z::CH;
+        src = value + int64_t(step * kKeys + rw) * p.s_v_tok +
+              ((l % Z::CH) ^ swizzle<Z::CH>(rw)) * 16;
+      }
+      load_lds(step * kKeys + rw < n ? src : kZeros,
+               uniform(lds0 + buf * Z::TILE + i * 1024));
+    }
+  };
+
+  constexpr int kAhead = Z::NBUF > 1 ? Z::NBUF - 1 : 0;
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k)
+    if (k < steps) stage(k, k);
+  int buf = 0;
+#pragma unroll 1
+  for (int s = 0; s < steps; ++s) {
+    if constexpr (kAhead == 0) {
+      lds_barrier();                       // the last step's tile is read
+      stage(s, 0);
+      wait_vm<0>();
+      lds_barrier();
+    } else {
+      wait_tile<kAhead - 1>(steps - s,
+                            std::integral_constant<int, Z::MINE>());
+      lds_barrier();                       // and the last step's tile is read
+      if (s + kAhead < steps) stage(s + kAhead, buf ? buf - 1 : kAhead);
+    }
+    const char* tile = smem + buf * Z::TILE;
+#pragma unroll
+    for (int k = 0; k < kKeys; k += 32) {
+      const int at = s * kKeys + k;
+      if (at < wave_lim)
+        attend<BF16, Z::CH, Z::CHP, Z::CH>(
+            tile + k * Z::CH * 16, tile + Z::ROPE + k * Z::CHP * 16,
+            tile + Z::VALUE + k * Z::CH * 16, 0, q, o, top, sum, 0xffffffffu,
+            min(lim - at, 32), p.scale);
+    }
+    buf = buf + 1 == Z::NBUF ? 0 : buf + 1;
+  }
+  sum = halves_sum(sum);
+  if (tok >= len) return;
+  const float by = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+  char* dst = p.out + int64_t(bos + tok) * p.s_out_tok + h * p.s_out_head;
+#pragma unroll
+  for (int k = 0; k < Z::NB; ++k)
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const int e = 32 * k + acc_row(i, half);
+      if constexpr (BF16)
+        *reinterpret_cast<u2*>(dst + e * 2) =
+            u2{pack_bf16(o[k][i] * by, o[k][i + 1] * by),
+               pack_bf16(o[k][i + 2] * by, o[k][i + 3] * by)};
+      else
+        *reinterpret_cast<f4*>(dst + e * 4) = f4{
+            o[k][i] * by, o[k][i + 1] * by, o[k][i + 2] * by,
+            o[k][i + 3] * by};
+    }
+  if (p.lse && half == 0)
+    p.lse[int64_t(bos + tok) * p.s_lse_tok + h * p.s_lse_head] =
+        sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
+}
+
+template <bool BF16, int D, int P>
+int launch(const PromptParams& p, hipStream_t stream) {
+  using Z = Prompt<BF16, D, P>;
+  constexpr int lds = Z::NBUF * Z::TILE;
+  static_assert(lds <= 160 * 1024, "LDS");
+  const auto kernel = kda_latent_prefill_kernel<BF16, D, P>;
+  const hipError_t e = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(kernel),
+      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return int(e);
+  launch_kernel(kernel, dim3(uint32_t(prompt_tiles(p.T, p.B) * p.H)),
+                dim3(64 * kWaves), lds, stream, p);
+  return int(hipGetLastError());
+}
+
+template <bool BF16>
+int launch_dims(const PromptParams& p, int D, int P, hipStream_t stream) {
+  if (D == 128 && P == 64) return launch<BF16, 128, 64>(p, stream);
+  if (D == 128 && P == 0) return launch<BF16, 128, 0>(p, stream);
+  if (D == 64 && P == 64) return launch<BF16, 64, 64>(p, stream);
+  if (D == 64 && P == 0) return launch<BF16, 64, 0>(p, stream);
+  return int(hipErrorInvalidValue);
+}
+
+}  // namespace
+
+// Query tiles of T tokens in B requests, at most.
+int64_t prompt_tiles(int64_t T, int64_t B) { return T / kQueries + B; }
+
+int launch_latent_prefill(const PromptParams& p, int D, int P, bool bf16,
+                          hipStream_t stream) {
+  return bf16 ? launch_dims<true>(p, D, P, stream)
+              : launch_dims<false>(p, D, P, stream);
+}
+
+int launch_latent_expand(const ExpandParams& p, bool bf16,
+                         hipStream_t stream) {
+  constexpr int lds = 4 * kExpand * 128;
+  const dim3 grid((p.S + kExpand - 1) / kExpand,
+                  (p.H * 2 * p.D + kExpand - 1) / kExpand);
+  if (bf16)
+    launch_kernel(kda_latent_expand_kernel<true>, grid, dim3(256), lds,
+                  stream, p);
+  else
+    launch_kernel(kda_latent_expand_kernel<false>, grid, dim3(256), lds,
+                  stream, p);
+  return int(hipGetLastError());
+}
+
+}  // namespace kda

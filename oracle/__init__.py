@@ -20,6 +20,8 @@ multi-step simulations against a fresh recurrence over the accepted stream.
 """
 from .cache import (  # noqa: F401
     latent_attention,
+    latent_expand,
+    latent_prefill,
     latent_write,
 )
 from .kda import (  # noqa: F401

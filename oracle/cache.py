@@ -81,3 +81,60 @@ def latent_attention(*, q, cache, out, lse, query_start_loc,
             weight[bos:eos, h], size[bos:eos, h] = r[2], r[3]
             keys[bos:eos, h] = see.sum(axis=1)
     return dict(out=out, lse=lse, weight=weight, size=size, keys=keys)
+
+
+def latent_expand(*, cache, weight, key, rope_key, value, key_start_loc,
+                  block_table, request_indices=None, null_block_id=0):
+    """Updated copies of key, value, rope_key (or None), and for bounds the
+    sums of magnitudes behind keys and values (`key_size`, `value_size`)."""
+    key, value = np.array(key, np.float64), np.array(value, np.float64)
+    rope = None if rope_key is None else np.array(rope_key, np.float64)
+    S, H, D = key.shape
+    R = weight.shape[2]
+    N, bs = cache.shape[:2]
+    ks, vs = np.zeros_like(key), np.zeros_like(value)
+    for b in range(len(key_start_loc) - 1):
+        bos = min(max(int(key_start_loc[b]), 0), S)
+        eos = min(max(int(key_start_loc[b + 1]), bos), S)
+        row = b if request_indices is None else int(request_indices[b])
+        at = places(row=row, length=eos - bos, block_table=block_table,
+                    block_size=bs, num_blocks=N, null_block_id=null_block_id)
+        for j, p in enumerate(at):
+            e = np.zeros(cache.shape[2]) if p is None \
+                else np.asarray(cache[p], np.float64)
+            kv = weight @ e[:R]
+            size = np.abs(weight) @ np.abs(e[:R])
+            key[bos + j], value[bos + j] = kv[:, :D], kv[:, D:]
+            ks[bos + j], vs[bos + j] = size[:, :D], size[:, D:]
+            if rope is not None:
+                rope[bos + j] = e[R:]
+    return dict(key=key, value=value, rope_key=rope, key_size=ks,
+                value_size=vs)
+
+
+def latent_prefill(*, q, key, value, out, lse, query_start_loc,
+                   key_start_loc, softmax_scale, rope_key=None):
+    """As `latent_attention`, over expanded keys and values."""
+    T, H, _ = q.shape
+    S = key.shape[0]
+    out, lse = np.array(out, np.float64), np.array(lse, np.float64)
+    weight, size, keys = (np.zeros_like(out), np.zeros_like(lse),
+                          np.zeros_like(lse))
+    for b in range(len(query_start_loc) - 1):
+        bos = min(max(int(query_start_loc[b]), 0), T)
+        eos = min(max(int(query_start_loc[b + 1]), bos), T)
+        ka = min(max(int(key_start_loc[b]), 0), S)
+        ke = min(max(int(key_start_loc[b + 1]), ka), S)
+        n, t = ke - ka, eos - bos
+        see = np.arange(n)[None] <= (n - t + np.arange(t))[:, None]
+        for h in range(H):
+            k = np.asarray(key[ka:ke, h], np.float64)
+            if rope_key is not None:
+                k = np.concatenate([k, rope_key[ka:ke]], axis=1)
+            r = softmax_sum(np.asarray(q[bos:eos, h], np.float64), k,
+                            np.asarray(value[ka:ke, h], np.float64), see,
+                            softmax_scale)
+            out[bos:eos, h], lse[bos:eos, h] = r[0], r[1]
+            weight[bos:eos, h], size[bos:eos, h] = r[2], r[3]
+            keys[bos:eos, h] = see.sum(axis=1)
+    return dict(out=out, lse=lse, weight=weight, size=size, keys=keys)
