@@ -51,6 +51,9 @@
  *       and values of every head from the cached latents, and the causal
  *       attention over them.
  *
+ *   kda_adjust_logits -- biases, penalties for repeated tokens and grammar
+ *       masks on the logits that kda_sample takes.
+ *
  * plus host-only argument checks mirroring the pages' validation
  * (kernels page `_check_layouts`, `can_use_cute_recoverssm`; ops page
  * `kda_recoverssm_verify`, `KDARecoverSSMCommitContext.create/commit`).
@@ -631,6 +634,51 @@ typedef struct {
   float softmax_scale;
 } kda_latent_prefill_args;
 
+/* Arguments of kda_adjust_logits: logits changed in place, before kda_sample.
+   For the entry x of token v in row m, which belongs to request b as in
+   kda_sample:
+     y = x + bias (the last entry of b's list that names v, if one does);
+     v seen:     y = y / r where y > 0, else y * r;
+     count > 0:  y = y - frequency_penalty * count - presence_penalty;
+     v not allowed by m's grammar mask: y = -inf.
+   A history is row request_indices[b] (or b) of token_ids, its first
+   token_lens[row] entries (held to [0, max_len]); the first
+   prompt_lens[row] of them are the prompt.  A token is seen if it is among
+   them, and its count is how often it occurs behind the prompt.  With
+   draft_tokens, row m of the window that starts at s also counts (and has
+   seen) draft_tokens[s + 1 .. m]; draft_tokens[s] is the history's last token.
+   r <= 0, NaN parameters and NULL arrays leave their change out; a request
+   without a row of token_ids (NULL, or outside [0, num_request_rows)) has an
+   empty history.  Tokens outside [0, V) are ignored.  Arithmetic is fp32, rounded once.  Entries that nothing changes keep their bits; rows that
+   belong to no request are not touched.
+   A mask row holds a bit for each token, bit v % 32 of word v / 32, 1 =
+   allowed; row m's is mask_rows[m] (NULL: m), outside [0, num_masks): none. */
+typedef struct {
+  kda_tensor logits;               /* F32 or BF16 [M, V], rows contiguous */
+  const int32_t* query_start_loc;  /* [batch + 1], or NULL: batch = M */
+  const int32_t* draft_tokens;     /* [M] or NULL */
+  const int32_t* request_indices;  /* [batch] or NULL: row = b */
+  const int32_t* token_ids;        /* [num_request_rows, max_len] or NULL */
+  int64_t token_ids_stride;        /* of a row; columns are contiguous */
+  const int32_t* prompt_lens;      /* per request row */
+  const int32_t* token_lens;       /* per request row */
+  const float* repetition_penalty; /* [batch] each, or NULL */
+  const float* frequency_penalty;
+  const float* presence_penalty;
+  const int32_t* bias_start;       /* [batch + 1] or NULL, not decreasing */
+  const int32_t* bias_tokens;      /* [num_biases] */
+  const float* bias_values;        /* [num_biases] */
+  const int32_t* mask;             /* [num_masks, >= ceil(V / 32)] or NULL */
+  int64_t mask_stride;             /* of a row; words are contiguous */
+  const int32_t* mask_rows;        /* [M] or NULL */
+  int32_t batch;
+  int32_t num_request_rows;
+  int32_t max_len;
+  int32_t num_biases;
+  int32_t num_masks;
+  int32_t pad_;
+} kda_logits_args;
+
 /* Library ABI version (KDA_ABI_VERSION). */
 int kda_abi_version(void);
 
@@ -784,6 +832,10 @@ int kda_latent_expand(const kda_latent_expand_args* args, void* stream);
    launch. */
 int kda_check_latent_prefill(const kda_latent_prefill_args* args);
 int kda_latent_prefill(const kda_latent_prefill_args* args, void* stream);
+
+/* Host-only validation of the logits' changes, then their launch. */
+int kda_check_adjust_logits(const kda_logits_args* args);
+int kda_adjust_logits(const kda_logits_args* args, void* stream);
 
 /* Launch a one-workgroup kernel that sets counter[0..n) to 0 on `stream`
    (for a counter left non-zero by an aborted launch).  Uses no memset

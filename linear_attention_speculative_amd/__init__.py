@@ -5,6 +5,8 @@ include/kda_recoverssm.h); this package is its thin torch binding.
 """
 from ._abi import LIB_PATH, load  # noqa: F401
 from .cache import (  # noqa: F401
+    adjust_logits,
+    check_adjust_logits,
     check_latent_attention,
     check_latent_expand,
     check_latent_prefill,
@@ -18,6 +20,7 @@ from .cache import (  # noqa: F401
     latent_prefill_args,
     latent_write,
     latent_write_args,
+    logits_args,
 )
 from .ops import (  # noqa: F401
     CommitContext,

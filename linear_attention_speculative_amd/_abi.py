@@ -48,6 +48,7 @@ EXPORTED = (
     "kda_latent_attention",
     "kda_check_latent_expand", "kda_latent_expand",
     "kda_check_latent_prefill", "kda_latent_prefill",
+    "kda_check_adjust_logits", "kda_adjust_logits",
 )
 
 
@@ -227,6 +228,23 @@ class KdaLatentPrefillArgs(Structure):
     ]
 
 
+class KdaLogitsArgs(Structure):
+    _fields_ = [
+        ("logits", KdaTensor), ("query_start_loc", c_void_p),
+        ("draft_tokens", c_void_p), ("request_indices", c_void_p),
+        ("token_ids", c_void_p), ("token_ids_stride", c_int64),
+        ("prompt_lens", c_void_p), ("token_lens", c_void_p),
+        ("repetition_penalty", c_void_p), ("frequency_penalty", c_void_p),
+        ("presence_penalty", c_void_p), ("bias_start", c_void_p),
+        ("bias_tokens", c_void_p), ("bias_values", c_void_p),
+        ("mask", c_void_p), ("mask_stride", c_int64),
+        ("mask_rows", c_void_p),
+        ("batch", c_int32), ("num_request_rows", c_int32),
+        ("max_len", c_int32), ("num_biases", c_int32),
+        ("num_masks", c_int32), ("pad_", c_int32),
+    ]
+
+
 _LIB = None
 
 
@@ -306,7 +324,9 @@ def load() -> ctypes.CDLL:
             ("kda_check_latent_expand", ("kda_latent_expand",),
              KdaLatentExpandArgs),
             ("kda_check_latent_prefill", ("kda_latent_prefill",),
-             KdaLatentPrefillArgs)):
+             KdaLatentPrefillArgs),
+            ("kda_check_adjust_logits", ("kda_adjust_logits",),
+             KdaLogitsArgs)):
         getattr(lib, check).restype = c_int
         getattr(lib, check).argtypes = [POINTER(args)]
         for name in launches:

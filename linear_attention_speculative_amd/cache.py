@@ -1,5 +1,6 @@
-"""Python binding of the operators on token caches: the attention layers over
-paged latent caches.
+"""Python binding of the operators on token caches and token histories: the
+attention layers over paged latent caches, and the changes of logits in front
+of `sample`.
 
 Argument marshalling and the checks that the C ABI cannot make, as in
 `serving`; every computation runs in the HIP library.
@@ -13,7 +14,7 @@ import torch
 
 from . import _abi
 from .ops import _DT, _pack_format, _tensor_values
-from .serving import _ints, _launch
+from .serving import _floats, _ints, _launch
 
 _WRITE_PACK = struct.Struct("<" + _pack_format(_abi.KdaLatentWriteArgs))
 
@@ -187,3 +188,80 @@ def latent_prefill(*, stream=None, **kwargs) -> None:
     query go with `rope_key`, which all heads share."""
     _launch(_abi.load().kda_latent_prefill, latent_prefill_args(**kwargs),
             kwargs, stream)
+
+
+_LOGITS_PACK = struct.Struct("<" + _pack_format(_abi.KdaLogitsArgs))
+
+
+def _int_rows(t, name):
+    """(pointer, row stride, rows, columns) of a two-dimensional int32 tensor
+    with contiguous rows."""
+    if t is None:
+        return 0, 0, 0, 0
+    if t.dim() != 2 or t.dtype != torch.int32:
+        raise ValueError(f"{name} must be a two-dimensional int32 tensor")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} needs contiguous rows")
+    return t.data_ptr(), t.stride(0), t.shape[0], t.shape[1]
+
+
+def logits_args(*, logits, query_start_loc=None, draft_tokens=None,
+                request_indices=None, token_ids=None, prompt_lens=None,
+                token_lens=None, repetition_penalty=None,
+                frequency_penalty=None, presence_penalty=None,
+                bias_start=None, bias_tokens=None, bias_values=None,
+                mask=None, mask_rows=None) -> _abi.KdaLogitsArgs:
+    """kda_logits_args for these tensors."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, vocabulary]")
+    M, V = logits.shape
+    B = M if query_start_loc is None else query_start_loc.numel() - 1
+    if B < 0:
+        raise ValueError("query_start_loc needs batch + 1 entries")
+    ids, s_ids, rows, length = _int_rows(token_ids, "token_ids")
+    if token_ids is not None:
+        if request_indices is None and rows < B:
+            raise ValueError("without request_indices token_ids needs a row "
+                             "per request")
+        if rows and (prompt_lens is None or token_lens is None):
+            raise ValueError("token_ids need prompt_lens and token_lens")
+    words, s_mask, masks, width = _int_rows(mask, "mask")
+    if mask is not None:
+        if masks and width < (V + 31) // 32:
+            raise ValueError("mask needs a bit for every token")
+        if mask_rows is None and masks < M:
+            raise ValueError("without mask_rows there is a mask per row")
+    n = 0
+    if bias_start is not None:
+        if bias_tokens is None or bias_values is None:
+            raise ValueError("bias_start needs bias_tokens and bias_values")
+        n = min(bias_tokens.numel(), bias_values.numel())
+    vals = (*_tensor_values(logits),
+            _ints(query_start_loc, "query_start_loc", B + 1),
+            _ints(draft_tokens, "draft_tokens", M),
+            _ints(request_indices, "request_indices", B), ids, s_ids,
+            _ints(prompt_lens, "prompt_lens", rows),
+            _ints(token_lens, "token_lens", rows),
+            _floats(repetition_penalty, "repetition_penalty", B),
+            _floats(frequency_penalty, "frequency_penalty", B),
+            _floats(presence_penalty, "presence_penalty", B),
+            _ints(bias_start, "bias_start", B + 1),
+            _ints(bias_tokens, "bias_tokens", n),
+            _floats(bias_values, "bias_values", n), words, s_mask,
+            _ints(mask_rows, "mask_rows", M), B, rows, length, n, masks, 0)
+    return _abi.KdaLogitsArgs.from_buffer_copy(_LOGITS_PACK.pack(*vals))
+
+
+def check_adjust_logits(**kwargs) -> int:
+    """Host-only validation (no launch); returns the kda_status code."""
+    return _abi.load().kda_check_adjust_logits(
+        ctypes.byref(logits_args(**kwargs)))
+
+
+def adjust_logits(*, stream=None, **kwargs) -> None:
+    """Logits changed in place in front of `sample`: biases, repetition,
+    frequency and presence penalties from the token histories (and a window's
+    drafts), grammar masks (kda_logits_args in include/kda_recoverssm.h).
+    Rows belong to requests as in `sample`; every change is optional."""
+    _launch(_abi.load().kda_adjust_logits, logits_args(**kwargs), kwargs,
+            stream)

@@ -93,4 +93,29 @@ int64_t prompt_tiles(int64_t T, int64_t B);
 int launch_latent_prefill(const PromptParams& p, int D, int P, bool bf16,
                           hipStream_t stream);
 
+struct LogitsParams {
+  void* logits;
+  int64_t s_row;
+  const int32_t* qsl;            // or null: a row a request
+  const int32_t* draft;          // or null
+  const int32_t* req_idx;        // or null
+  const int32_t* tokens;         // [rows, L], or null: no history
+  int64_t s_tok;
+  const int32_t* prompt;
+  const int32_t* known;
+  const float* rep;              // [B] each, or null
+  const float* freq;
+  const float* pres;
+  const int32_t* bias_start;     // [B + 1], or null: no biases
+  const int32_t* bias_tokens;
+  const float* bias_values;
+  const int32_t* mask;           // or null
+  int64_t s_mask;
+  const int32_t* mask_rows;      // [M], or null: row m
+  int32_t M, V, B, rows, L, num_bias, num_masks;
+};
+int64_t logits_slices(int64_t V);
+int launch_adjust_logits(const LogitsParams& p, bool bf16,
+                         hipStream_t stream);
+
 }  // namespace kda

@@ -407,6 +407,81 @@ int plan_prompt(const kda_latent_prefill_args* a, PromptPlan* plan) {
   return KDA_OK;
 }
 
+int plan_logits(const kda_logits_args* a, kda::LogitsParams* p, bool* bf16) {
+  if (a == nullptr) return fail(KDA_E_ARG, "logits arguments are NULL");
+  if (a->batch < 0 || a->num_request_rows < 0 || a->max_len < 0 ||
+      a->num_biases < 0 || a->num_masks < 0)
+    return fail(KDA_E_ARG, "a count is negative");
+  const kda_tensor& x = a->logits;
+  KDA_TRY(check_desc(x, "logits", 2));
+  const int64_t M = x.shape[0], V = x.shape[1];
+  if (V < 1) return fail(KDA_E_SHAPE, "the logits have no vocabulary");
+  if (V > (1 << 20))
+    return fail(KDA_E_UNSUPPORTED, "vocabularies of up to 2^20 are supported");
+  if ((V > 1 && x.stride[1] != 1) || x.stride[0] < 0)
+    return fail(KDA_E_LAYOUT, "logit rows must be contiguous");
+  if (M > 1 && x.stride[0] < V)
+    return fail(KDA_E_LAYOUT, "logit rows overlap");
+  if (!aligned(x.data, elem_size(x.dtype)))
+    return fail(KDA_E_UNALIGNED, "the logits are not element aligned");
+  if (!a->query_start_loc && a->batch != M)
+    return fail(KDA_E_SHAPE,
+                "without query_start_loc there is one request per row (%lld "
+                "rows, %d requests)",
+                (long long)M, a->batch);
+  if (M > kI32Max - 64 || a->batch > 65535)
+    return fail(KDA_E_CAPACITY, "at most 65535 requests and 2^31 rows");
+  if (a->draft_tokens && !a->query_start_loc)
+    return fail(KDA_E_ARG, "draft_tokens need query_start_loc");
+  if (a->token_ids && a->num_request_rows > 0 &&
+      (!a->prompt_lens || !a->token_lens))
+    return fail(KDA_E_ARG, "token_ids need prompt_lens and token_lens");
+  if (a->bias_start && a->num_biases > 0 &&
+      (!a->bias_tokens || !a->bias_values))
+    return fail(KDA_E_ARG, "bias_start needs bias_tokens and bias_values");
+  if ((a->token_ids && a->num_request_rows > 1 &&
+       a->token_ids_stride < a->max_len) ||
+      (a->mask && a->num_masks > 1 && a->mask_stride < (V + 31) / 32))
+    return fail(KDA_E_LAYOUT, "rows of token_ids or mask overlap");
+  const void* all[] = {a->query_start_loc, a->draft_tokens,
+                       a->request_indices, a->token_ids, a->prompt_lens,
+                       a->token_lens, a->repetition_penalty,
+                       a->frequency_penalty, a->presence_penalty,
+                       a->bias_start, a->bias_tokens, a->bias_values, a->mask,
+                       a->mask_rows};
+  for (const void* q : all)
+    if (q && !aligned(q, 4))
+      return fail(KDA_E_UNALIGNED, "arrays must be 4-byte aligned");
+  *p = kda::LogitsParams{};
+  p->logits = x.data;
+  p->s_row = x.stride[0];
+  p->qsl = a->query_start_loc;
+  p->draft = a->draft_tokens;
+  p->req_idx = a->request_indices;
+  p->tokens = a->token_ids;
+  p->s_tok = a->token_ids_stride;
+  p->prompt = a->prompt_lens;
+  p->known = a->token_lens;
+  p->rep = a->repetition_penalty;
+  p->freq = a->frequency_penalty;
+  p->pres = a->presence_penalty;
+  p->bias_start = a->bias_start;
+  p->bias_tokens = a->bias_tokens;
+  p->bias_values = a->bias_values;
+  p->mask = a->mask;
+  p->s_mask = a->mask_stride;
+  p->mask_rows = a->mask_rows;
+  p->M = int32_t(M);
+  p->V = int32_t(V);
+  p->B = a->batch;
+  p->rows = a->num_request_rows;
+  p->L = a->max_len;
+  p->num_bias = a->num_biases;
+  p->num_masks = a->num_masks;
+  *bf16 = x.dtype == KDA_BF16;
+  return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -486,6 +561,24 @@ int kda_latent_prefill(const kda_latent_prefill_args* args, void* stream) {
       kda::launch_latent_prefill(plan.p, plan.D, plan.P, plan.bf16,
                                  static_cast<hipStream_t>(stream)),
       "kda_latent_prefill launch");
+}
+
+int kda_check_adjust_logits(const kda_logits_args* args) {
+  g_err.clear();
+  kda::LogitsParams p;
+  bool bf16 = false;
+  return plan_logits(args, &p, &bf16);
+}
+
+int kda_adjust_logits(const kda_logits_args* args, void* stream) {
+  g_err.clear();
+  kda::LogitsParams p;
+  bool bf16 = false;
+  KDA_TRY(plan_logits(args, &p, &bf16));
+  if (p.M == 0 || p.B == 0) return KDA_OK;
+  return device_status(
+      kda::launch_adjust_logits(p, bf16, static_cast<hipStream_t>(stream)),
+      "kda_adjust_logits launch");
 }
 
 }  // extern "C"

@@ -19,6 +19,7 @@ The commit plan, the boundary fold and the conv compaction are pinned by
 multi-step simulations against a fresh recurrence over the accepted stream.
 """
 from .cache import (  # noqa: F401
+    adjust_logits,
     latent_attention,
     latent_expand,
     latent_prefill,

@@ -138,3 +138,69 @@ def latent_prefill(*, q, key, value, out, lse, query_start_loc,
             weight[bos:eos, h], size[bos:eos, h] = r[2], r[3]
             keys[bos:eos, h] = see.sum(axis=1)
     return dict(out=out, lse=lse, weight=weight, size=size, keys=keys)
+
+
+def adjust_logits(*, logits, query_start_loc=None, draft_tokens=None,
+                  request_indices=None, token_ids=None, prompt_lens=None,
+                  token_lens=None, repetition_penalty=None,
+                  frequency_penalty=None, presence_penalty=None,
+                  bias_start=None, bias_tokens=None, bias_values=None,
+                  mask=None, mask_rows=None):
+    """Changed copy of the logits [M, V], and the sums of magnitudes behind
+    its entries (for bounds)."""
+    y = np.array(logits, np.float64)
+    size = np.abs(y)
+    M, V = y.shape
+    B = M if query_start_loc is None else len(query_start_loc) - 1
+
+    def param(a, b, none):
+        return none if a is None or np.isnan(a[b]) else float(a[b])
+
+    for b in range(B):
+        s, e = (b, b + 1) if query_start_loc is None else (
+            min(max(int(query_start_loc[b]), 0), M),
+            min(max(int(query_start_loc[b + 1]), 0), M))
+        r = param(repetition_penalty, b, 1.0)
+        r = r if r > 0 else 1.0
+        f, p = (param(a, b, 0.0) for a in (frequency_penalty,
+                                           presence_penalty))
+        count, seen = np.zeros(V, np.int64), np.zeros(V, bool)
+        if token_ids is not None:
+            row = b if request_indices is None else int(request_indices[b])
+            if 0 <= row < len(token_ids):
+                n = min(max(int(token_lens[row]), 0), token_ids.shape[1])
+                for i in range(n):
+                    t = int(token_ids[row, i])
+                    if 0 <= t < V:
+                        seen[t] = True
+                        count[t] += i >= prompt_lens[row]
+        bias = {}
+        if bias_start is not None:
+            lo = max(int(bias_start[b]), 0)
+            hi = min(int(bias_start[b + 1]), len(bias_tokens))
+            for i in range(lo, hi):
+                bias[int(bias_tokens[i])] = float(bias_values[i])
+        for m in range(s, e):
+            if m > s and draft_tokens is not None:
+                t = int(draft_tokens[m])
+                if 0 <= t < V:
+                    seen[t] = True
+                    count[t] += 1
+            for t, v in bias.items():
+                if 0 <= t < V:
+                    y[m, t] += v
+                    size[m, t] += abs(v)
+            for t in np.flatnonzero(seen):
+                by = 1 / r if y[m, t] > 0 else r
+                y[m, t] *= by
+                size[m, t] *= by
+                if count[t]:
+                    y[m, t] -= f * count[t] + p
+                    size[m, t] += abs(f) * count[t] + abs(p)
+            mr = -1 if mask is None else m if mask_rows is None \
+                else int(mask_rows[m])
+            if mask is not None and 0 <= mr < len(mask):
+                words = np.asarray(mask[mr]).astype(np.int64)
+                bits = (words[np.arange(V) // 32] >> (np.arange(V) % 32)) & 1
+                y[m, bits == 0] = -np.inf
+    return y, size
