@@ -51,6 +51,10 @@
  *       and values of every head from the cached latents, and the causal
  *       attention over them.
  *
+ *   kda_copy_blocks, kda_fork_blocks, kda_free_blocks, kda_compact_blocks --
+ *       blocks shared, copied, given back and moved, over the states, conv
+ *       states and caches that share a block table.
+ *
  *   kda_adjust_logits -- biases, penalties for repeated tokens and grammar
  *       masks on the logits that kda_sample takes.
  *
@@ -679,6 +683,123 @@ typedef struct {
   int32_t pad_;
 } kda_logits_args;
 
+/* Arguments of kda_copy_blocks: for each pair (source, destination) and every
+   pool (a layer's state, conv state or cache; block i lies at base + i *
+   stride), the block's bytes copied bit for bit.  A pair with a null id
+   (<= null_block_id or >= num_blocks) or with source = destination copies
+   nothing.  A destination must not be another pair's source or destination. */
+typedef struct {
+  const int64_t* tables;         /* device int64 [3][num_pools]: base byte
+                                    addresses, block strides and block sizes
+                                    in bytes */
+  const int64_t* host_tables;    /* optional HOST copy, for the checks and the
+                                    launch's size */
+  const int32_t* copy_pairs;     /* device [max_pairs][2] */
+  const int32_t* num_pairs;      /* device [1] or NULL: max_pairs; held to
+                                    [0, max_pairs] */
+  int64_t num_blocks;            /* N of every pool */
+  int32_t num_pools;
+  int32_t max_pairs;
+  int32_t null_block_id;
+  int32_t pad_;
+} kda_copy_args;
+
+/* Arguments of kda_fork_blocks: request rows that continue another row's
+   tokens.  Fork f makes child row b = child_rows[f] hold the first c =
+   max(num_computed_tokens[a], 0) tokens of parent row a = parent_rows[f]:
+     blocks 0 .. k - 1, k = c / block_size, are the parent's (shared),
+     block k, which the next token goes to and which holds the running state,
+     is taken from free_blocks in the order of the forks (the null id once
+     they run out),
+     copy_pairs[f] = (the parent's block k, the new one) for kda_copy_blocks,
+     num_computed_tokens[b] = c, num_blocks[b] = k + 1 (at most the width).
+   A pair is (null, null) where the parent does not hold block k or there is
+   no new block.  A fork with a row outside [0, num_request_rows) or with a =
+   b does nothing and takes no block.  Entries of the child's row behind block
+   k stay.  A child row must not be another fork's row; a parent may have many
+   forks. */
+typedef struct {
+  const int32_t* parent_rows;    /* [num_forks] */
+  const int32_t* child_rows;     /* [num_forks] */
+  int32_t* num_computed_tokens;  /* per request row, read and written */
+  int32_t* num_blocks;           /* per request row, read and written */
+  int32_t* block_table;          /* [num_request_rows, width], as well */
+  int64_t block_table_strides[2];      /* row, column (elements) */
+  const int32_t* free_blocks;    /* [num_free] */
+  int32_t* copy_pairs;           /* [num_forks][2] output */
+  int32_t* num_allocated;        /* [1] output: blocks the forks asked for */
+  int32_t num_forks;
+  int32_t num_request_rows;
+  int32_t block_table_width;
+  int32_t block_size;
+  int32_t num_free;
+  int32_t null_block_id;
+} kda_fork_args;
+
+/* Arguments of kda_free_blocks: rows released, references counted anew, free
+   blocks listed.
+     new_num_blocks[r] = 0 for released rows, else num_blocks[r] held to
+     [0, width] (may be num_blocks itself);
+     ref_counts[i] = pinned[i] (0 where negative; NULL: 0) + how often the rows
+     hold block i (their first new_num_blocks entries; null ids are none);
+     free_blocks = the blocks i > null_block_id with no reference, in rising
+     order, null ids behind them up to N;  num_free = how many they are.
+   Released rows outside [0, num_request_rows) are ignored; one may be named
+   twice. */
+typedef struct {
+  const int32_t* released_rows;  /* [num_released] */
+  const int32_t* block_table;    /* [num_request_rows, width] */
+  int64_t block_table_strides[2];      /* row, column (elements) */
+  const int32_t* num_blocks;     /* per request row: entries held */
+  const int32_t* pinned;         /* [N] references of other holders, or NULL */
+  int32_t* new_num_blocks;       /* per request row; outputs from here on */
+  int32_t* ref_counts;           /* [N] */
+  int32_t* free_blocks;          /* [N] */
+  int32_t* num_free;             /* [1] */
+  void* workspace;               /* kda_blocks_workspace_size(N) bytes, 4-byte
+                                    aligned */
+  int64_t workspace_bytes;
+  int32_t num_released;
+  int32_t num_request_rows;
+  int32_t block_table_width;
+  int32_t total_blocks;          /* N */
+  int32_t null_block_id;
+  int32_t pad_;
+} kda_free_args;
+
+/* Arguments of kda_compact_blocks: live blocks (ref_counts > 0) moved to the
+   lowest ids behind the null one.  With n live blocks, those above
+   null_block_id + n move, in rising order, to the free ids up to there, in
+   rising order:
+     copy_pairs lists the moves (kda_copy_blocks makes them), null pairs
+     behind them;  num_pairs = how many (of more than max_pairs moves the
+     first max_pairs are made; N / 2 are always enough);
+     new_block_table is the block table with the new ids in the first
+     num_blocks[r] entries of each row, other entries as they were (may be
+     block_table itself);
+     new_ref_counts the counts by new id (may be ref_counts itself).
+   With all moves made, the free blocks are null_block_id + n + 1 .. N - 1. */
+typedef struct {
+  const int32_t* ref_counts;     /* [N] */
+  const int32_t* block_table;    /* [num_request_rows, width] */
+  int64_t block_table_strides[2];      /* row, column (elements) */
+  const int32_t* num_blocks;     /* per request row: entries held */
+  int32_t* new_block_table;      /* outputs from here on */
+  int64_t new_block_table_strides[2];
+  int32_t* new_ref_counts;       /* [N] */
+  int32_t* copy_pairs;           /* [max_pairs][2] */
+  int32_t* num_pairs;            /* [1] */
+  void* workspace;               /* kda_blocks_workspace_size(N) bytes, 4-byte
+                                    aligned */
+  int64_t workspace_bytes;
+  int32_t max_pairs;
+  int32_t num_request_rows;
+  int32_t block_table_width;
+  int32_t total_blocks;          /* N */
+  int32_t null_block_id;
+  int32_t pad_;
+} kda_compact_blocks_args;
+
 /* Library ABI version (KDA_ABI_VERSION). */
 int kda_abi_version(void);
 
@@ -836,6 +957,20 @@ int kda_latent_prefill(const kda_latent_prefill_args* args, void* stream);
 /* Host-only validation of the logits' changes, then their launch. */
 int kda_check_adjust_logits(const kda_logits_args* args);
 int kda_adjust_logits(const kda_logits_args* args, void* stream);
+
+/* Host-only validation of the block operators' arguments, then their launches
+   (copies and forks one kernel, the other two several).  The workspace of the
+   last two is scratch memory for `total_blocks` blocks (0 for sizes that the
+   checks refuse), not shared by launches in flight together. */
+int kda_check_copy_blocks(const kda_copy_args* args);
+int kda_copy_blocks(const kda_copy_args* args, void* stream);
+int kda_check_fork_blocks(const kda_fork_args* args);
+int kda_fork_blocks(const kda_fork_args* args, void* stream);
+int64_t kda_blocks_workspace_size(int64_t total_blocks);
+int kda_check_free_blocks(const kda_free_args* args);
+int kda_free_blocks(const kda_free_args* args, void* stream);
+int kda_check_compact_blocks(const kda_compact_blocks_args* args);
+int kda_compact_blocks(const kda_compact_blocks_args* args, void* stream);
 
 /* Launch a one-workgroup kernel that sets counter[0..n) to 0 on `stream`
    (for a counter left non-zero by an aborted launch).  Uses no memset

@@ -4,6 +4,19 @@ The compute path is the HIP library `libkda_recoverssm.so` (C ABI in
 include/kda_recoverssm.h); this package is its thin torch binding.
 """
 from ._abi import LIB_PATH, load  # noqa: F401
+from .blocks import (  # noqa: F401
+    BlockPools,
+    blocks_workspace_size,
+    check_compact_blocks,
+    check_fork_blocks,
+    check_free_blocks,
+    compact_blocks,
+    compact_blocks_args,
+    fork_args,
+    fork_blocks,
+    free_args,
+    free_blocks,
+)
 from .cache import (  # noqa: F401
     adjust_logits,
     check_adjust_logits,

@@ -49,6 +49,10 @@ EXPORTED = (
     "kda_check_latent_expand", "kda_latent_expand",
     "kda_check_latent_prefill", "kda_latent_prefill",
     "kda_check_adjust_logits", "kda_adjust_logits",
+    "kda_check_copy_blocks", "kda_copy_blocks",
+    "kda_check_fork_blocks", "kda_fork_blocks", "kda_blocks_workspace_size",
+    "kda_check_free_blocks", "kda_free_blocks",
+    "kda_check_compact_blocks", "kda_compact_blocks",
 )
 
 
@@ -245,6 +249,58 @@ class KdaLogitsArgs(Structure):
     ]
 
 
+class KdaCopyArgs(Structure):
+    _fields_ = [
+        ("tables", c_void_p), ("host_tables", POINTER(c_int64)),
+        ("copy_pairs", c_void_p), ("num_pairs", c_void_p),
+        ("num_blocks", c_int64), ("num_pools", c_int32),
+        ("max_pairs", c_int32), ("null_block_id", c_int32),
+        ("pad_", c_int32),
+    ]
+
+
+class KdaForkArgs(Structure):
+    _fields_ = [
+        ("parent_rows", c_void_p), ("child_rows", c_void_p),
+        ("num_computed_tokens", c_void_p), ("num_blocks", c_void_p),
+        ("block_table", c_void_p), ("block_table_strides", c_int64 * 2),
+        ("free_blocks", c_void_p), ("copy_pairs", c_void_p),
+        ("num_allocated", c_void_p),
+        ("num_forks", c_int32), ("num_request_rows", c_int32),
+        ("block_table_width", c_int32), ("block_size", c_int32),
+        ("num_free", c_int32), ("null_block_id", c_int32),
+    ]
+
+
+class KdaFreeArgs(Structure):
+    _fields_ = [
+        ("released_rows", c_void_p), ("block_table", c_void_p),
+        ("block_table_strides", c_int64 * 2), ("num_blocks", c_void_p),
+        ("pinned", c_void_p), ("new_num_blocks", c_void_p),
+        ("ref_counts", c_void_p), ("free_blocks", c_void_p),
+        ("num_free", c_void_p), ("workspace", c_void_p),
+        ("workspace_bytes", c_int64),
+        ("num_released", c_int32), ("num_request_rows", c_int32),
+        ("block_table_width", c_int32), ("total_blocks", c_int32),
+        ("null_block_id", c_int32), ("pad_", c_int32),
+    ]
+
+
+class KdaCompactBlocksArgs(Structure):
+    _fields_ = [
+        ("ref_counts", c_void_p), ("block_table", c_void_p),
+        ("block_table_strides", c_int64 * 2), ("num_blocks", c_void_p),
+        ("new_block_table", c_void_p),
+        ("new_block_table_strides", c_int64 * 2),
+        ("new_ref_counts", c_void_p), ("copy_pairs", c_void_p),
+        ("num_pairs", c_void_p), ("workspace", c_void_p),
+        ("workspace_bytes", c_int64),
+        ("max_pairs", c_int32), ("num_request_rows", c_int32),
+        ("block_table_width", c_int32), ("total_blocks", c_int32),
+        ("null_block_id", c_int32), ("pad_", c_int32),
+    ]
+
+
 _LIB = None
 
 
@@ -307,6 +363,8 @@ def load() -> ctypes.CDLL:
     lib.kda_prefill_workspace_size.argtypes = [c_int64] * 4 + [c_int32] * 2
     lib.kda_sample_workspace_size.restype = c_int64
     lib.kda_sample_workspace_size.argtypes = [c_int64] * 2
+    lib.kda_blocks_workspace_size.restype = c_int64
+    lib.kda_blocks_workspace_size.argtypes = [c_int64]
     lib.kda_latent_attention_workspace_size.restype = c_int64
     lib.kda_latent_attention_workspace_size.argtypes = ([c_int64] * 5 +
                                                         [c_int32])
@@ -326,7 +384,12 @@ def load() -> ctypes.CDLL:
             ("kda_check_latent_prefill", ("kda_latent_prefill",),
              KdaLatentPrefillArgs),
             ("kda_check_adjust_logits", ("kda_adjust_logits",),
-             KdaLogitsArgs)):
+             KdaLogitsArgs),
+            ("kda_check_copy_blocks", ("kda_copy_blocks",), KdaCopyArgs),
+            ("kda_check_fork_blocks", ("kda_fork_blocks",), KdaForkArgs),
+            ("kda_check_free_blocks", ("kda_free_blocks",), KdaFreeArgs),
+            ("kda_check_compact_blocks", ("kda_compact_blocks",),
+             KdaCompactBlocksArgs)):
         getattr(lib, check).restype = c_int
         getattr(lib, check).argtypes = [POINTER(args)]
         for name in launches:

@@ -24,7 +24,7 @@ SOURCES = ["kda_verify_d128.hip", "kda_verify_d64.hip", "kda_verify_d32.hip",
            "kda_verify_d16.hip", "kda_verify.hip", "kda_commit.hip",
            "kda_plan.hip", "kda_prefill.hip", "kda_decode.hip",
            "kda_tables.hip", "kda_sample.hip", "kda_latent.hip", "kda_prompt.hip",
-           "kda_logits.hip", "kda_api.cpp", "kda_serving_api.cpp", "kda_cache_api.cpp"]
+           "kda_logits.hip", "kda_blocks.hip", "kda_api.cpp", "kda_serving_api.cpp", "kda_cache_api.cpp"]
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 
 # Packed fp32 VALU ops are disabled for all device code.

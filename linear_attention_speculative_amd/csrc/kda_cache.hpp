@@ -118,4 +118,64 @@ int64_t logits_slices(int64_t V);
 int launch_adjust_logits(const LogitsParams& p, bool bf16,
                          hipStream_t stream);
 
+struct CopyParams {
+  const int64_t* tables;         // [3][L]: bases, block strides and block
+                                 // sizes, in bytes
+  const int32_t* pairs;          // [P][2]: source, destination
+  const int32_t* num_pairs;      // [1] or null: P
+  int64_t N;
+  int32_t L, P, null_id;
+};
+int64_t copy_pieces(int64_t bytes);
+int launch_copy_blocks(const CopyParams& p, int64_t pieces,
+                       hipStream_t stream);
+
+struct ForkParams {
+  const int32_t* parents;        // [F]
+  const int32_t* children;
+  int32_t* computed;             // per request row
+  int32_t* held;
+  int32_t* table;
+  int64_t s_tab_row, s_tab_col;
+  const int32_t* free_blocks;
+  int32_t* pairs;                // [F][2]
+  int32_t* allocated;            // [1]
+  int32_t F, rows, width, block, num_free, null_id;
+};
+int launch_fork_blocks(const ForkParams& p, hipStream_t stream);
+
+constexpr int kBlockChunk = 4096;   // blocks of one count
+struct FreeParams {
+  const int32_t* released;       // [R]
+  const int32_t* held;           // per request row
+  int32_t* new_held;
+  const int32_t* table;
+  int64_t s_tab_row, s_tab_col;
+  const int32_t* pinned;         // [N] or null
+  int32_t* refs;                 // [N]
+  int32_t* free_blocks;          // [N]
+  int32_t* num_free;             // [1]
+  int32_t* counts;               // workspace: one a chunk of blocks
+  int64_t N;
+  int32_t R, rows, width, null_id;
+};
+int launch_free_blocks(const FreeParams& p, hipStream_t stream);
+
+struct CompactBlocksParams {
+  const int32_t* refs;           // [N]
+  int32_t* new_refs;
+  const int32_t* held;
+  const int32_t* table;
+  int64_t s_tab_row, s_tab_col;
+  int32_t* new_table;
+  int64_t s_new_row, s_new_col;
+  int32_t* pairs;                // [max_pairs][2]
+  int32_t* num_pairs;            // [1]
+  int32_t* counts;               // workspace
+  int32_t* moved;                // workspace [N]: a moved block's pair
+  int64_t N;
+  int32_t max_pairs, rows, width, null_id;
+};
+int launch_compact_blocks(const CompactBlocksParams& p, hipStream_t stream);
+
 }  // namespace kda

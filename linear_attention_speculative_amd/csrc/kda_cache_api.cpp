@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <initializer_list>
 
 #include "kda_cache.hpp"
 #include "kda_host.hpp"
@@ -482,6 +483,175 @@ int plan_logits(const kda_logits_args* a, kda::LogitsParams* p, bool* bf16) {
   return KDA_OK;
 }
 
+int check_pointers(std::initializer_list<const void*> needed,
+                   std::initializer_list<const void*> all) {
+  for (const void* q : needed)
+    if (!q) return fail(KDA_E_ARG, "a required array is NULL");
+  for (const void* q : all)
+    if (q && !aligned(q, 4))
+      return fail(KDA_E_UNALIGNED, "arrays must be 4-byte aligned");
+  return KDA_OK;
+}
+
+// A block table of `rows` x `width`; one that is written must have an entry
+// of its own for each element.
+int check_table(const int32_t* t, const int64_t* strides, int64_t rows,
+                int64_t width, bool written) {
+  const int64_t sr = strides[0], sc = strides[1];
+  if (rows > 0 && width > 0 && !t)
+    return fail(KDA_E_ARG, "a block table is NULL");
+  if (sr < 0 || sc < 0 || sr > kI32Max || sc > kI32Max)
+    return fail(KDA_E_LAYOUT, "a table stride is negative or exceeds 2^31");
+  if (written && width > 0 && rows > 0 &&
+      ((width > 1 && sc == 0) ||
+       (rows > 1 && sr < sc * (width - 1) + 1 &&
+        (sr == 0 || sc < sr * (rows - 1) + 1))))
+    return fail(KDA_E_LAYOUT, "the block table's rows overlap");
+  return KDA_OK;
+}
+
+int plan_copy(const kda_copy_args* a, kda::CopyParams* p, int64_t* pieces) {
+  if (a == nullptr) return fail(KDA_E_ARG, "copy arguments are NULL");
+  if (a->num_pools < 1 || a->max_pairs < 0 || a->num_blocks < 0)
+    return fail(KDA_E_ARG, "copies need a pool and no negative counts");
+  if (a->null_block_id < 0)
+    return fail(KDA_E_ARG, "null_block_id must not be negative");
+  if (a->num_pools > 65535 || a->num_blocks > kI32Max)
+    return fail(KDA_E_CAPACITY, "at most 65535 pools and 2^31 blocks");
+  if (!a->tables) return fail(KDA_E_ARG, "the pools' tables are required");
+  if (a->max_pairs > 0 && !a->copy_pairs)
+    return fail(KDA_E_ARG, "copy_pairs is required");
+  if (!aligned(a->tables, 8) || !aligned(a->copy_pairs, 4) ||
+      !aligned(a->num_pairs, 4))
+    return fail(KDA_E_UNALIGNED, "arrays must be aligned to their elements");
+  *pieces = int64_t(1) << 20;
+  if (a->host_tables) {
+    const int64_t L = a->num_pools;
+    int64_t most = 0;
+    for (int64_t i = 0; i < L; ++i) {
+      const int64_t base = a->host_tables[i], st = a->host_tables[L + i],
+                    size = a->host_tables[2 * L + i];
+      if (size < 1 || st < size)
+        return fail(KDA_E_LAYOUT,
+                    "blocks of pool %lld overlap (%lld bytes every %lld)",
+                    (long long)i, (long long)size, (long long)st);
+      if (base == 0) return fail(KDA_E_ARG, "a pool's address is NULL");
+      most = std::max(most, kda::copy_pieces(size));
+    }
+    *pieces = most * std::max(a->max_pairs, 1);
+  }
+  *p = kda::CopyParams{a->tables,     a->copy_pairs, a->num_pairs,
+                       a->num_blocks, a->num_pools,  a->max_pairs,
+                       a->null_block_id};
+  return KDA_OK;
+}
+
+int plan_fork(const kda_fork_args* a, kda::ForkParams* p) {
+  if (a == nullptr) return fail(KDA_E_ARG, "fork arguments are NULL");
+  if (a->num_forks < 0 || a->num_request_rows < 0 ||
+      a->block_table_width < 0 || a->num_free < 0)
+    return fail(KDA_E_ARG, "a count is negative");
+  if (a->block_size < 1)
+    return fail(KDA_E_ARG, "block_size must be at least 1");
+  if (a->null_block_id < 0)
+    return fail(KDA_E_ARG, "null_block_id must not be negative");
+  if (a->num_forks > 0) {
+    KDA_TRY(check_pointers({a->parent_rows, a->child_rows, a->copy_pairs,
+                            a->num_allocated}, {}));
+    if (a->num_request_rows > 0)
+      KDA_TRY(check_pointers({a->num_computed_tokens, a->num_blocks}, {}));
+    if (a->num_free > 0) KDA_TRY(check_pointers({a->free_blocks}, {}));
+  }
+  KDA_TRY(check_pointers({}, {a->parent_rows, a->child_rows,
+                              a->num_computed_tokens, a->num_blocks,
+                              a->block_table, a->free_blocks, a->copy_pairs,
+                              a->num_allocated}));
+  KDA_TRY(check_table(a->block_table, a->block_table_strides,
+                      a->num_request_rows, a->block_table_width, true));
+  *p = kda::ForkParams{a->parent_rows, a->child_rows,
+                       a->num_computed_tokens, a->num_blocks, a->block_table,
+                       a->block_table_strides[0], a->block_table_strides[1],
+                       a->free_blocks, a->copy_pairs, a->num_allocated,
+                       a->num_forks, a->num_request_rows,
+                       a->block_table_width, a->block_size, a->num_free,
+                       a->null_block_id};
+  return KDA_OK;
+}
+
+constexpr int64_t kMaxBlocks = 1 << 28;
+
+// Counts of chunks, then an entry a block.
+int64_t blocks_bytes(int64_t N) {
+  if (N < 0 || N > kMaxBlocks) return 0;
+  return (N / kda::kBlockChunk + 1 + N) * 4;
+}
+
+// What the two operators over all blocks share.
+template <class Args>
+int check_blocks(const Args* a) {
+  if (a->num_request_rows < 0 || a->block_table_width < 0 ||
+      a->total_blocks < 1)
+    return fail(KDA_E_ARG, "a count is negative, or there are no blocks");
+  if (a->null_block_id < 0)
+    return fail(KDA_E_ARG, "null_block_id must not be negative");
+  if (a->total_blocks > kMaxBlocks)
+    return fail(KDA_E_CAPACITY, "at most 2^28 blocks");
+  if (a->num_request_rows > 0)
+    KDA_TRY(check_pointers({a->num_blocks}, {a->num_blocks}));
+  KDA_TRY(check_table(a->block_table, a->block_table_strides,
+                      a->num_request_rows, a->block_table_width, false));
+  KDA_TRY(check_pointers({a->workspace}, {a->workspace, a->block_table}));
+  if (a->workspace_bytes < blocks_bytes(a->total_blocks))
+    return fail(KDA_E_CAPACITY,
+                "the workspace holds %lld bytes; %d blocks need %lld",
+                (long long)a->workspace_bytes, a->total_blocks,
+                (long long)blocks_bytes(a->total_blocks));
+  return KDA_OK;
+}
+
+int plan_free(const kda_free_args* a, kda::FreeParams* p) {
+  if (a == nullptr) return fail(KDA_E_ARG, "free arguments are NULL");
+  if (a->num_released < 0) return fail(KDA_E_ARG, "a count is negative");
+  KDA_TRY(check_blocks(a));
+  KDA_TRY(check_pointers({a->ref_counts, a->free_blocks, a->num_free},
+                         {a->released_rows, a->pinned, a->new_num_blocks,
+                          a->ref_counts, a->free_blocks, a->num_free}));
+  if (a->num_released > 0) KDA_TRY(check_pointers({a->released_rows}, {}));
+  if (a->num_request_rows > 0)
+    KDA_TRY(check_pointers({a->new_num_blocks}, {}));
+  *p = kda::FreeParams{a->released_rows, a->num_blocks, a->new_num_blocks,
+                       a->block_table, a->block_table_strides[0],
+                       a->block_table_strides[1], a->pinned, a->ref_counts,
+                       a->free_blocks, a->num_free,
+                       static_cast<int32_t*>(a->workspace), a->total_blocks,
+                       a->num_released, a->num_request_rows,
+                       a->block_table_width, a->null_block_id};
+  return KDA_OK;
+}
+
+int plan_compact_blocks(const kda_compact_blocks_args* a,
+                        kda::CompactBlocksParams* p) {
+  if (a == nullptr) return fail(KDA_E_ARG, "compaction arguments are NULL");
+  if (a->max_pairs < 0) return fail(KDA_E_ARG, "a count is negative");
+  KDA_TRY(check_blocks(a));
+  KDA_TRY(check_table(a->new_block_table, a->new_block_table_strides,
+                      a->num_request_rows, a->block_table_width, true));
+  KDA_TRY(check_pointers({a->ref_counts, a->new_ref_counts, a->num_pairs},
+                         {a->ref_counts, a->new_ref_counts, a->num_pairs,
+                          a->new_block_table, a->copy_pairs}));
+  if (a->max_pairs > 0) KDA_TRY(check_pointers({a->copy_pairs}, {}));
+  int32_t* work = static_cast<int32_t*>(a->workspace);
+  *p = kda::CompactBlocksParams{
+      a->ref_counts, a->new_ref_counts, a->num_blocks, a->block_table,
+      a->block_table_strides[0], a->block_table_strides[1],
+      a->new_block_table, a->new_block_table_strides[0],
+      a->new_block_table_strides[1], a->copy_pairs, a->num_pairs, work,
+      work + a->total_blocks / kda::kBlockChunk + 1, a->total_blocks,
+      a->max_pairs, a->num_request_rows, a->block_table_width,
+      a->null_block_id};
+  return KDA_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -579,6 +749,74 @@ int kda_adjust_logits(const kda_logits_args* args, void* stream) {
   return device_status(
       kda::launch_adjust_logits(p, bf16, static_cast<hipStream_t>(stream)),
       "kda_adjust_logits launch");
+}
+
+int kda_check_copy_blocks(const kda_copy_args* args) {
+  g_err.clear();
+  kda::CopyParams p;
+  int64_t pieces = 0;
+  return plan_copy(args, &p, &pieces);
+}
+
+int kda_copy_blocks(const kda_copy_args* args, void* stream) {
+  g_err.clear();
+  kda::CopyParams p;
+  int64_t pieces = 0;
+  KDA_TRY(plan_copy(args, &p, &pieces));
+  if (p.P == 0) return KDA_OK;
+  return device_status(
+      kda::launch_copy_blocks(p, pieces, static_cast<hipStream_t>(stream)),
+      "kda_copy_blocks launch");
+}
+
+int kda_check_fork_blocks(const kda_fork_args* args) {
+  g_err.clear();
+  kda::ForkParams p;
+  return plan_fork(args, &p);
+}
+
+int kda_fork_blocks(const kda_fork_args* args, void* stream) {
+  g_err.clear();
+  kda::ForkParams p;
+  KDA_TRY(plan_fork(args, &p));
+  if (p.F == 0) return KDA_OK;
+  return device_status(
+      kda::launch_fork_blocks(p, static_cast<hipStream_t>(stream)),
+      "kda_fork_blocks launch");
+}
+
+int64_t kda_blocks_workspace_size(int64_t total_blocks) {
+  return blocks_bytes(total_blocks);
+}
+
+int kda_check_free_blocks(const kda_free_args* args) {
+  g_err.clear();
+  kda::FreeParams p;
+  return plan_free(args, &p);
+}
+
+int kda_free_blocks(const kda_free_args* args, void* stream) {
+  g_err.clear();
+  kda::FreeParams p;
+  KDA_TRY(plan_free(args, &p));
+  return device_status(
+      kda::launch_free_blocks(p, static_cast<hipStream_t>(stream)),
+      "kda_free_blocks launch");
+}
+
+int kda_check_compact_blocks(const kda_compact_blocks_args* args) {
+  g_err.clear();
+  kda::CompactBlocksParams p;
+  return plan_compact_blocks(args, &p);
+}
+
+int kda_compact_blocks(const kda_compact_blocks_args* args, void* stream) {
+  g_err.clear();
+  kda::CompactBlocksParams p;
+  KDA_TRY(plan_compact_blocks(args, &p));
+  return device_status(
+      kda::launch_compact_blocks(p, static_cast<hipStream_t>(stream)),
+      "kda_compact_blocks launch");
 }
 
 }  // extern "C"

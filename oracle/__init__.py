@@ -20,6 +20,10 @@ multi-step simulations against a fresh recurrence over the accepted stream.
 """
 from .cache import (  # noqa: F401
     adjust_logits,
+    compact_blocks,
+    copy_blocks,
+    fork_blocks,
+    free_blocks,
     latent_attention,
     latent_expand,
     latent_prefill,

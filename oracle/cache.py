@@ -204,3 +204,84 @@ def adjust_logits(*, logits, query_start_loc=None, draft_tokens=None,
                 bits = (words[np.arange(V) // 32] >> (np.arange(V) % 32)) & 1
                 y[m, bits == 0] = -np.inf
     return y, size
+
+
+def copy_blocks(pools, pairs, num_pairs=None, null_block_id=0):
+    """Updated copies of the pools [N, ..]."""
+    new = [np.array(p) for p in pools]
+    n = len(pairs) if num_pairs is None else min(max(int(num_pairs), 0),
+                                                 len(pairs))
+    for src, dst in np.asarray(pairs)[:n]:
+        for old, pool in zip(pools, new):
+            if null_block_id < src < len(old) and \
+                    null_block_id < dst < len(old):
+                pool[dst] = old[src]
+    return new
+
+
+def fork_blocks(*, parent_rows, child_rows, num_computed_tokens, num_blocks,
+                block_table, free_blocks, block_size, null_block_id=0):
+    table, held, comp = (np.array(a) for a in (block_table, num_blocks,
+                                               num_computed_tokens))
+    rows, width = table.shape
+    pairs = np.full((len(parent_rows), 2), null_block_id)
+    free, asked = list(free_blocks), 0
+    for f, (a, b) in enumerate(zip(parent_rows, child_rows)):
+        if not (0 <= a < rows and 0 <= b < rows) or a == b or width == 0:
+            continue
+        c = max(int(num_computed_tokens[a]), 0)
+        k = c // block_size
+        new = int(free[asked]) if asked < len(free) else null_block_id
+        asked += 1
+        table[b, :k] = block_table[a, :k]
+        if k < width:
+            table[b, k] = new
+            if k < num_blocks[a] and new > null_block_id and \
+                    block_table[a, k] > null_block_id:
+                pairs[f] = block_table[a, k], new
+        comp[b], held[b] = c, min(k + 1, width)
+    return dict(block_table=table, num_blocks=held, num_computed_tokens=comp,
+                copy_pairs=pairs, num_allocated=np.array([asked]))
+
+
+def free_blocks(*, released_rows, block_table, num_blocks, total_blocks,
+                pinned=None, null_block_id=0):
+    rows, width = block_table.shape
+    held = np.clip(num_blocks, 0, width)
+    for r in released_rows:
+        if 0 <= r < rows:
+            held[r] = 0
+    refs = np.zeros(total_blocks, np.int64) if pinned is None \
+        else np.maximum(pinned, 0)
+    for r in range(rows):
+        for b in block_table[r, :held[r]]:
+            if null_block_id < b < total_blocks:
+                refs[b] += 1
+    free = [i for i in range(null_block_id + 1, total_blocks) if refs[i] == 0]
+    listed = np.full(total_blocks, null_block_id)
+    listed[:len(free)] = free
+    return dict(new_num_blocks=held, ref_counts=refs, free_blocks=listed,
+                num_free=np.array([len(free)]))
+
+
+def compact_blocks(*, ref_counts, block_table, num_blocks, max_pairs,
+                   null_block_id=0):
+    N = len(ref_counts)
+    live = [i for i in range(null_block_id + 1, N) if ref_counts[i] > 0]
+    end = null_block_id + 1 + len(live)
+    src = [i for i in live if i >= end]
+    dst = [i for i in range(null_block_id + 1, min(end, N))
+           if ref_counts[i] <= 0]
+    moves = list(zip(src, dst))[:max_pairs]
+    to = dict(moves)
+    refs, table = np.array(ref_counts), np.array(block_table)
+    for a, b in moves:
+        refs[b], refs[a] = ref_counts[a], 0
+    for r in range(len(table)):
+        for j in range(min(max(int(num_blocks[r]), 0), table.shape[1])):
+            table[r, j] = to.get(int(table[r, j]), table[r, j])
+    pairs = np.full((max_pairs, 2), null_block_id)
+    if moves:
+        pairs[:len(moves)] = moves
+    return dict(new_ref_counts=refs, new_block_table=table, copy_pairs=pairs,
+                num_pairs=np.array([len(moves)]))
