@@ -123,21 +123,17 @@ __global__ void __launch_bounds__(kThreads) kda_fork_kernel(ForkParams p) {
 __global__ void __launch_bounds__(kThreads) kda_free_start_kernel(FreeParams p) {
   const int i = blockIdx.x * kThreads + threadIdx.x;
   if (i < p.N) p.refs[i] = p.pinned ? max(p.pinned[i], 0) : 0;
-  if (i < p.rows) p.new_held[i] = min(max(p.held[i], 0), p.width);
-}
-
-// (after new_held was written: a row named twice is released once)
-__global__ void __launch_bounds__(kThreads)
-    kda_free_release_kernel(FreeParams p) {
-  const int i = blockIdx.x * kThreads + threadIdx.x;
-  if (i >= p.R) return;
-  const int row = p.released[i];
-  if (row >= 0 && row < p.rows) p.new_held[row] = 0;
 }
 
 __global__ void __launch_bounds__(kThreads) kda_free_count_kernel(FreeParams p) {
   const int row = blockIdx.x;
-  const int n = p.new_held[row];
+  int released = 0;                          // (a row may be named twice)
+  for (int i = threadIdx.x; i < p.R; i += kThreads)
+    released |= p.released[i] == row;
+  released = __syncthreads_or(released);
+  const int n = released ? 0 : min(max(p.held[row], 0), p.width);
+  __syncthreads();                           // (new_held may be held itself)
+  if (threadIdx.x == 0) p.new_held[row] = n;
   const int32_t* t = p.table + row * p.s_tab_row;
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const int id = t[i * p.s_tab_col];
@@ -308,6 +304,150 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
+// ---- the same in one workgroup ---------------------------------------------------
+
+// Pools of up to kSmallBlocks blocks and tables of up to kSmallEntries entries
+// take one launch each in place of five: all counts and lists fit LDS.
+constexpr int kSmallBlocks = 16384;
+constexpr int kSmallRows = 4096;
+constexpr int kSmallEntries = 65536;
+constexpr int kMany = 1024;        // threads
+
+// Exclusive prefix sum over the workgroup's threads, and the total.
+__device__ __forceinline__ int scan_many(int v, int* total, int* red) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int upto = v;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const int o = __shfl_up(upto, s);
+    if (lane >= s) upto += o;
+  }
+  __syncthreads();
+  if (lane == 63) red[w] = upto;
+  __syncthreads();
+  int before = 0, all = 0;
+  for (int k = 0; k < kMany / 64; ++k) {
+    before += k < w ? red[k] : 0;
+    all += red[k];
+  }
+  *total = all;
+  return before + upto - v;
+}
+
+// Every entry of a table, a wave a row, eight rows under way together.
+template <class Load, class Use>
+__device__ __forceinline__ void each_entry(int rows, int width, Load load,
+                                           Use use) {
+  constexpr int U = 8, kWaves = kMany / 64;
+  const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
+  for (int r0 = w; r0 < rows; r0 += U * kWaves)
+    for (int j = lane; j < width; j += 64) {
+      int id[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        id[k] = load(min(r0 + k * kWaves, rows - 1), j);
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+        if (r0 + k * kWaves < rows) use(r0 + k * kWaves, j, id[k]);
+    }
+}
+
+__global__ void __launch_bounds__(kMany) kda_free_small_kernel(FreeParams p) {
+  extern __shared__ __align__(16) int32_t refs[];   // [N], then held [rows]
+  __shared__ int red[kMany / 64];
+  const int tid = threadIdx.x, N = int(p.N);
+  int32_t* held = refs + N;
+  for (int i = tid; i < N; i += kMany)
+    refs[i] = p.pinned ? max(p.pinned[i], 0) : 0;
+  for (int i = tid; i < p.rows; i += kMany)
+    held[i] = min(max(p.held[i], 0), p.width);
+  __syncthreads();
+  for (int i = tid; i < p.R; i += kMany) {
+    const int row = p.released[i];
+    if (row >= 0 && row < p.rows) held[row] = 0;
+  }
+  __syncthreads();
+  for (int i = tid; i < p.rows; i += kMany) p.new_held[i] = held[i];
+  if (p.width > 0)
+    each_entry(
+        p.rows, p.width,
+        [&](int r, int j) {
+          return j < held[r] ? p.table[r * p.s_tab_row + j * p.s_tab_col]
+                             : p.null_id;
+        },
+        [&](int, int, int id) {
+          if (id > p.null_id && id < N) atomicAdd(&refs[id], 1);
+        });
+  __syncthreads();
+  for (int i = tid; i < N; i += kMany) p.refs[i] = refs[i];
+  // each thread lists the free ones among its own run of blocks
+  const int run = (N + kMany - 1) / kMany, lo = min(tid * run, N),
+            hi = min(lo + run, N);
+  int n = 0, total;
+  for (int i = lo; i < hi; ++i) n += i > p.null_id && refs[i] <= 0;
+  int at = scan_many(n, &total, red);
+  for (int i = lo; i < hi; ++i)
+    if (i > p.null_id && refs[i] <= 0) p.free_blocks[at++] = i;
+  for (int i = total + tid; i < N; i += kMany) p.free_blocks[i] = p.null_id;
+  if (tid == 0) p.num_free[0] = total;
+}
+
+__global__ void __launch_bounds__(kMany)
+    kda_compact_small_kernel(CompactBlocksParams p) {
+  extern __shared__ __align__(16) int32_t refs[];   // [N], then lists
+  __shared__ int red[kMany / 64];
+  const int tid = threadIdx.x, N = int(p.N);
+  uint16_t* src = reinterpret_cast<uint16_t*>(refs + N);   // [N / 2 + 1]
+  uint16_t* dst = src + N / 2 + 1;
+  uint16_t* map = dst + N / 2 + 1;                         // [N]
+  int32_t* held = refs + 2 * N + 1;                        // [rows]
+  for (int i = tid; i < p.rows; i += kMany) held[i] = p.held[i];
+  for (int i = tid; i < N; i += kMany) {
+    refs[i] = p.refs[i];
+    map[i] = uint16_t(i);
+  }
+  __syncthreads();
+  const int run = (N + kMany - 1) / kMany, lo = min(tid * run, N),
+            hi = min(lo + run, N);
+  auto live = [&](int i) { return i > p.null_id && refs[i] > 0; };
+  int n = 0, total, moves;
+  for (int i = lo; i < hi; ++i) n += live(i);
+  const int rank = scan_many(n, &total, red);
+  const int first = p.null_id + 1, end = first + total;
+  n = 0;
+  for (int i = max(lo, end); i < hi; ++i) n += live(i);
+  int from = scan_many(n, &moves, red);      // moves: live ones from end on
+  int free = lo > first ? lo - first - rank : 0;
+  for (int i = lo; i < hi; ++i) {
+    if (i >= end && live(i)) src[from++] = uint16_t(i);
+    if (i >= first && i < end && !live(i)) dst[free++] = uint16_t(i);
+  }
+  __syncthreads();
+  moves = min(moves, p.max_pairs);
+  for (int64_t i = tid; i < p.max_pairs; i += kMany) {
+    const bool in = i < moves;
+    const int a = in ? src[i] : p.null_id, b = in ? dst[i] : p.null_id;
+    p.pairs[2 * i] = a;
+    p.pairs[2 * i + 1] = b;
+    if (in) {
+      map[a] = uint16_t(b);
+      refs[b] = refs[a];
+      refs[a] = 0;
+    }
+  }
+  if (tid == 0) p.num_pairs[0] = moves;
+  __syncthreads();
+  for (int i = tid; i < N; i += kMany) p.new_refs[i] = refs[i];
+  if (p.width > 0)
+    each_entry(
+        p.rows, p.width,
+        [&](int r, int j) { return p.table[r * p.s_tab_row + j * p.s_tab_col]; },
+        [&](int r, int j, int id) {
+          if (j < held[r] && id > p.null_id && id < N) id = map[id];
+          p.new_table[r * p.s_new_row + j * p.s_new_col] = id;
+        });
+}
+
 }  // namespace
 
 int launch_copy_blocks(const CopyParams& p, int64_t pieces,
@@ -332,19 +472,32 @@ namespace {
 dim3 grid_of(int64_t n) {
   return dim3(uint32_t((n + kThreads - 1) / kThreads));
 }
+bool is_small(int64_t N, int64_t rows, int64_t width) {
+  return N <= kSmallBlocks && rows <= kSmallRows &&
+         rows * width <= kSmallEntries;
+}
+template <class F>
+hipError_t more_lds(F kernel) {
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             hipFuncAttributeMaxDynamicSharedMemorySize,
+                             (kSmallBlocks * 2 + 1 + kSmallRows) * 4);
+}
 dim3 chunks_of(int64_t N) {
   return dim3(uint32_t((N + kBlockChunk - 1) / kBlockChunk));
 }
 }  // namespace
 
 int launch_free_blocks(const FreeParams& p, hipStream_t stream) {
-  launch_kernel(kda_free_start_kernel,
-                grid_of(p.N > p.rows ? p.N : int64_t(p.rows)), dim3(kThreads),
-                0, stream, p);
-  if (p.R > 0)
-    launch_kernel(kda_free_release_kernel, grid_of(p.R), dim3(kThreads), 0,
-                  stream, p);
-  if (p.rows > 0 && p.width > 0)
+  if (is_small(p.N, p.rows, p.width)) {
+    const hipError_t e = more_lds(kda_free_small_kernel);
+    if (e != hipSuccess) return int(e);
+    launch_kernel(kda_free_small_kernel, dim3(1), dim3(kMany),
+                  uint32_t(p.N + p.rows) * 4, stream, p);
+    return int(hipGetLastError());
+  }
+  launch_kernel(kda_free_start_kernel, grid_of(p.N), dim3(kThreads), 0, stream,
+                p);
+  if (p.rows > 0)
     launch_kernel(kda_free_count_kernel, dim3(p.rows), dim3(kThreads), 0,
                   stream, p);
   launch_kernel(kda_live_count_kernel, chunks_of(p.N), dim3(kThreads), 0,
@@ -356,6 +509,13 @@ int launch_free_blocks(const FreeParams& p, hipStream_t stream) {
 }
 
 int launch_compact_blocks(const CompactBlocksParams& p, hipStream_t stream) {
+  if (is_small(p.N, p.rows, p.width)) {
+    const hipError_t e = more_lds(kda_compact_small_kernel);
+    if (e != hipSuccess) return int(e);
+    launch_kernel(kda_compact_small_kernel, dim3(1), dim3(kMany),
+                  uint32_t(p.N * 2 + 1 + p.rows) * 4, stream, p);
+    return int(hipGetLastError());
+  }
   launch_kernel(kda_live_count_kernel, chunks_of(p.N), dim3(kThreads), 0,
                 stream, p.refs, p.counts, p.N, p.null_id);
   launch_kernel(kda_compact_plan_kernel, chunks_of(p.N), dim3(kThreads), 0,

@@ -113,8 +113,8 @@ struct LogitsParams {
   int64_t s_mask;
   const int32_t* mask_rows;      // [M], or null: row m
   int32_t M, V, B, rows, L, num_bias, num_masks;
+  int32_t mask_from;             // first row of a launch of the masks
 };
-int64_t logits_slices(int64_t V);
 int launch_adjust_logits(const LogitsParams& p, bool bf16,
                          hipStream_t stream);
 

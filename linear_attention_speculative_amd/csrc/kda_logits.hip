@@ -6,24 +6,31 @@
 //
 // `count` is how often a token was produced: the history behind the prompt,
 // and in a draft window the drafts up to the row.  Nothing is kept between
-// calls: one workgroup takes a request and a slice of the vocabulary, counts
-// the slice's tokens of the history in LDS (integer atomics: no order changes
-// a count) and goes through the rows of the request's window, one more draft
-// counted for each.  Only entries that change are read and written: a row
-// without a mask costs the entries of its history, a masked one its writes.
-//
-// One word of LDS a token: a bias, the prompt's tokens and the count.  The
-// bias itself is looked up in the request's list when a token has one, from
-// the end (the last of several counts).
+// calls.  One workgroup takes a request: it counts the tokens of its history
+// in a table in LDS that is addressed by the token (integer atomics: no order
+// changes a count), with each token's last bias, lists the places in use, and
+// changes their entries in all rows of the window, four under way in each
+// thread.  What bounds that is memory: an entry costs a line of it.  Requests
+// with more tokens than the table takes go through the vocabulary in slices,
+// a word of LDS a token, by several workgroups.  The masks are a kernel of
+// their own behind it, 16 bytes at a time (in one kernel with the rest, the
+// rows under a mask held up their workgroup: 640 rows of 131072 bf16, a
+// quarter of them masked, 118 us).
 #include "kda_cache.hpp"
 #include "kda_mma.hpp"
 
 namespace kda {
 namespace {
 
-constexpr int kSlice = 8192;       // tokens of a workgroup
-constexpr int kThreads = 512;
-constexpr uint32_t kSeen = 1u << 31, kBiased = 1u << 30, kCount = kBiased - 1;
+constexpr int kThreads = 1024;
+constexpr int kMaskThreads = 256;
+constexpr int64_t kMaskRows = 65535;
+constexpr int kPlaces = 8192;      // of the table
+constexpr int kMost = 6144;        // tokens that it takes
+constexpr int kSlice = 4096;       // tokens of a pass without it
+constexpr int kRows = 64;          // rows of a window whose data is in LDS
+// a token of the prompt, one that a row's draft may add, and its count
+constexpr uint32_t kSeen = 1u << 31, kListed = 1u << 30, kCount = kListed - 1;
 
 struct Change {
   float r, f, p;
@@ -32,28 +39,76 @@ struct Change {
   int n;
 };
 
-__device__ __forceinline__ float bias_of(const Change& c, int token) {
-  for (int i = c.n - 1; i >= 0; --i)
-    if (c.tokens[i] == token) return c.values[i];
-  return 0.0f;
-}
-
+// `w`: seen and count; `e`: a bias's place in the list, plus one.
 __device__ __forceinline__ float change(const Change& c, float y, uint32_t w,
-                                        int token) {
-  if (w & kBiased) y += bias_of(c, token);
-  if (w & (kSeen | kCount)) y = y > 0.0f ? y / c.r : y * c.r;
+                                        uint32_t e) {
+  if (e) y += c.values[e - 1];
+  if (w) y = y > 0.0f ? y / c.r : y * c.r;
   if (w & kCount) y = y - c.f * float(w & kCount) - c.p;
   return y;
+}
+
+// Mask words of a mask row, or null.
+__device__ __forceinline__ const int32_t* mask_at(const LogitsParams& p,
+                                                  int mr) {
+  return mr >= 0 && mr < p.num_masks ? p.mask + mr * p.s_mask : nullptr;
+}
+
+// Rows [first, m1) of a window, with what the LDS holds of them.
+struct Rows {
+  const int32_t* draft;            // draft[m - first]; null: none
+  const int32_t* mask_row;         // as well, of given mask rows
+  int first, count;
+};
+
+// Changes `touched` listed tokens in all rows: token_of(i) and word_of(i) of
+// the i-th one, bias_of(i) as change() takes it.
+template <bool BF16, class Token, class Word, class Bias>
+__device__ __forceinline__ void change_listed(const LogitsParams& p,
+                                              const Change& c, const Rows& r,
+                                              int touched, Token token_of,
+                                              Word word_of, Bias bias_of) {
+  typedef typename Act<BF16>::T E;
+  constexpr int U = 4;
+  const int64_t items = int64_t(touched) * r.count;
+  for (int64_t i0 = threadIdx.x; i0 < items; i0 += U * kThreads) {
+    E* x[U];
+    float y[U];
+    uint32_t w[U], e[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      x[k] = nullptr;
+      const int64_t i = i0 + k * kThreads;
+      if (i >= items) continue;
+      const int at = int(i / r.count), j = int(i - int64_t(at) * r.count);
+      const int token = token_of(at);
+      const int32_t* mask =
+          p.mask ? mask_at(p, p.mask_rows ? r.mask_row[j] : r.first + j)
+                 : nullptr;
+      // (what a mask hides stays as it is)
+      if (mask && !((uint32_t(mask[token >> 5]) >> (token & 31)) & 1))
+        continue;
+      w[k] = word_of(at) & ~kListed;
+      if (r.draft)
+        for (int d = 1; d <= j; ++d) w[k] += r.draft[d] == token;
+      e[k] = bias_of(at);
+      if (!(w[k] | e[k])) continue;          // (a later row's draft)
+      x[k] = static_cast<E*>(p.logits) + (r.first + j) * p.s_row + token;
+      y[k] = ld_elem(x[k], 0, BF16);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+      if (x[k]) st_elem(x[k], 0, change(c, y[k], w[k], e[k]), BF16);
+  }
 }
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
     kda_adjust_logits_kernel(LogitsParams p) {
-  constexpr int G = BF16 ? 8 : 4;            // entries of 16 bytes
-  typedef typename Act<BF16>::T E;
-  __shared__ __align__(16) uint32_t words[kSlice];
+  extern __shared__ __align__(16) uint32_t lds[];
+  __shared__ int touched;
+  __shared__ int32_t row_draft[kRows], row_mask[kRows];
   const int tid = threadIdx.x, b = blockIdx.y;
-  const int v0 = blockIdx.x * kSlice, nv = min(p.V - v0, kSlice);
   int m0 = b, m1 = b + 1;
   if (p.qsl) {
     m0 = min(max(p.qsl[b], 0), p.M);
@@ -67,6 +122,16 @@ __global__ void __launch_bounds__(kThreads)
   if (first >= m1) return;
 
   Change c{1.0f, 0.0f, 0.0f, nullptr, nullptr, 0};
+  const int32_t* history = nullptr;
+  int known = 0, prompt = 0;
+  if (p.tokens) {
+    const int row = p.req_idx ? p.req_idx[b] : b;
+    if (row >= 0 && row < p.rows) {
+      history = p.tokens + row * p.s_tok;
+      known = min(max(p.known[row], 0), p.L);
+      prompt = p.prompt[row];
+    }
+  }
   if (p.rep) c.r = p.rep[b];
   if (p.freq) c.f = p.freq[b];
   if (p.pres) c.p = p.pres[b];
@@ -80,126 +145,213 @@ __global__ void __launch_bounds__(kThreads)
     c.values = p.bias_values + lo;
   }
   const bool counts = c.r != 1.0f || c.f != 0.0f || c.p != 0.0f;
-  const bool any = counts || c.n > 0;
-  if (!any && !p.mask) return;
+  if (!counts) known = 0;
+  const bool drafts = counts && p.draft;
+  if (!counts && c.n == 0) return;
+  const bool table = int64_t(known) + c.n + (drafts ? m1 - start : 0) <= kMost;
+  if (table && blockIdx.x > 0) return;       // (one workgroup does it all)
 
-  if (any) {
-    for (int i = tid; i < kSlice / 4; i += kThreads)
-      reinterpret_cast<u4*>(words)[i] = u4{0, 0, 0, 0};
-    __syncthreads();
-    if (counts && p.tokens) {
-      const int row = p.req_idx ? p.req_idx[b] : b;
-      if (row >= 0 && row < p.rows) {
-        const int32_t* t = p.tokens + row * p.s_tok;
-        const int known = min(max(p.known[row], 0), p.L);
-        const int prompt = p.prompt[row];
-        for (int i = tid; i < known; i += kThreads) {
-          const uint32_t at = uint32_t(t[i]) - uint32_t(v0);
-          if (at < uint32_t(nv)) {
-            if (i < prompt)
-              atomicOr(&words[at], kSeen);
-            else
-              atomicAdd(&words[at], 1u);
-          }
-        }
-      }
+  Rows r{drafts ? p.draft + first : nullptr, nullptr, first, m1 - first};
+  if (p.mask && p.mask_rows) {
+    r.mask_row = p.mask_rows + first;
+    if (r.count <= kRows) {
+      if (tid < r.count) row_mask[tid] = r.mask_row[tid];
+      r.mask_row = row_mask;
     }
-    for (int i = tid; i < c.n; i += kThreads) {
-      const uint32_t at = uint32_t(c.tokens[i]) - uint32_t(v0);
-      if (at < uint32_t(nv)) atomicOr(&words[at], kBiased);
-    }
-    if (counts && p.draft)
-      for (int i = start + 1 + tid; i <= first; i += kThreads) {
-        const uint32_t at = uint32_t(p.draft[i]) - uint32_t(v0);
-        if (at < uint32_t(nv)) atomicAdd(&words[at], 1u);
-      }
-    __syncthreads();
+  }
+  if (drafts && r.count <= kRows) {
+    if (tid < r.count) row_draft[tid] = p.draft[first + tid];
+    r.draft = row_draft;
   }
 
-  for (int m = first; m < m1; ++m) {
-    if (m > first && counts && p.draft) {
-      __syncthreads();
-      const uint32_t at = uint32_t(p.draft[m]) - uint32_t(v0);
-      if (tid == 0 && at < uint32_t(nv)) ++words[at];
-      __syncthreads();
+  if (table) {
+    uint32_t* key = lds;                     // a token plus one; 0: free
+    uint32_t* word = lds + kPlaces;
+    uint16_t* list = reinterpret_cast<uint16_t*>(lds + 2 * kPlaces);
+    uint32_t* biased = lds + 2 * kPlaces + kPlaces / 2;
+    for (int i = tid; i < kPlaces / 4; i += kThreads) {
+      reinterpret_cast<u4*>(key)[i] = u4{0, 0, 0, 0};
+      reinterpret_cast<u4*>(word)[i] = u4{0, 0, 0, 0};
+      if (p.bias_start) reinterpret_cast<u4*>(biased)[i] = u4{0, 0, 0, 0};
     }
-    E* x = static_cast<E*>(p.logits) + m * p.s_row + v0;
-    const int32_t* mask = nullptr;
-    if (p.mask) {
-      const int mr = p.mask_rows ? p.mask_rows[m] : m;
-      if (mr >= 0 && mr < p.num_masks)
-        mask = p.mask + mr * p.s_mask + v0 / 32;
+    if (tid == 0) touched = 0;
+    __syncthreads();
+    // the place of a token, taken for it if it is new; at most kMost tokens
+    // come, so there is always a free one
+    auto place_of = [&](int token) -> int {
+      if (uint32_t(token) >= uint32_t(p.V)) return -1;
+      const uint32_t k = uint32_t(token) + 1;
+      uint32_t at = (k * 2654435761u) >> 19;
+      while (true) {
+        const uint32_t had = atomicCAS(&key[at], 0u, k);
+        if (had == 0) list[atomicAdd(&touched, 1)] = uint16_t(at);
+        if (had == 0 || had == k) return int(at);
+        at = (at + 1) % kPlaces;
+      }
+    };
+    for (int i = tid; i < known; i += kThreads) {
+      const int at = place_of(history[i]);
+      if (at < 0) continue;
+      if (i < prompt)
+        atomicOr(&word[at], kSeen);
+      else
+        atomicAdd(&word[at], 1u);
     }
-    if (!any && !mask) continue;
-    const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0;
-    for (int i = tid * G; i < nv; i += kThreads * G) {
-      uint32_t w[G], changed = 0;
-#pragma unroll
-      for (int k = 0; k < G; ++k) w[k] = 0;
-      if (any) {
-#pragma unroll
-        for (int k = 0; k < G; k += 4) {
-          const u4 q = *reinterpret_cast<const u4*>(words + i + k);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[k + j] = q[j];
-        }
-#pragma unroll
-        for (int k = 0; k < G; ++k) changed |= w[k] ? 1u << k : 0u;
+    if (drafts)
+      for (int i = start + 1 + tid; i < m1; i += kThreads) {
+        const int at = place_of(p.draft[i]);
+        if (at >= 0 && i <= first) atomicAdd(&word[at], 1u);
       }
-      constexpr uint32_t all = (1u << G) - 1;
-      uint32_t out = 0;                      // entries that are masked
-      if (mask) out = ~(uint32_t(mask[i >> 5]) >> (i & 31)) & all;
-      if (!(changed | out)) continue;
-      changed &= ~out;
-      if (wide && i + G <= nv) {
-        u4 v = {0, 0, 0, 0};
-        if (out != all) v = *reinterpret_cast<const u4*>(x + i);
+    for (int i = tid; i < c.n; i += kThreads) {
+      const int at = place_of(c.tokens[i]);
+      if (at >= 0) atomicMax(&biased[at], uint32_t(i) + 1);
+    }
+    __syncthreads();
+    change_listed<BF16>(
+        p, c, r, touched, [&](int i) { return int(key[list[i]]) - 1; },
+        [&](int i) { return word[list[i]]; },
+        [&](int i) { return c.n > 0 ? biased[list[i]] : 0u; });
+    return;
+  }
+
+  uint32_t* words = lds;
+  uint32_t* biased = lds + kSlice;
+  uint16_t* list = reinterpret_cast<uint16_t*>(lds + 2 * kSlice);
+  for (int v0 = int(blockIdx.x) * kSlice; v0 < p.V;
+       v0 += int(gridDim.x) * kSlice) {
+    const int nv = min(p.V - v0, kSlice);
+    __syncthreads();                         // the last slice is done
+    for (int i = tid; i < kSlice / 2; i += kThreads)
+      reinterpret_cast<u4*>(lds)[i] = u4{0, 0, 0, 0};
+    if (tid == 0) touched = 0;
+    __syncthreads();
+    for (int i = tid; i < known; i += kThreads) {
+      const uint32_t at = uint32_t(history[i]) - uint32_t(v0);
+      if (at >= uint32_t(nv)) continue;
+      if (i < prompt)
+        atomicOr(&words[at], kSeen);
+      else
+        atomicAdd(&words[at], 1u);
+    }
+    if (drafts)
+      for (int i = start + 1 + tid; i < m1; i += kThreads) {
+        const uint32_t at = uint32_t(p.draft[i]) - uint32_t(v0);
+        if (at >= uint32_t(nv)) continue;
+        if (i <= first)
+          atomicAdd(&words[at], 1u);
+        else
+          atomicOr(&words[at], kListed);
+      }
+    for (int i = tid; i < c.n; i += kThreads) {
+      const uint32_t at = uint32_t(c.tokens[i]) - uint32_t(v0);
+      if (at < uint32_t(nv)) atomicMax(&biased[at], uint32_t(i) + 1);
+    }
+    __syncthreads();
+    for (int i = tid; i < nv; i += kThreads)
+      if (words[i] | biased[i]) list[atomicAdd(&touched, 1)] = uint16_t(i);
+    __syncthreads();
+    change_listed<BF16>(
+        p, c, r, touched, [&](int i) { return v0 + list[i]; },
+        [&](int i) { return words[list[i]]; },
+        [&](int i) { return biased[list[i]]; });
+  }
+}
+
+// Entries that a row's mask does not allow, after the changes.
+template <bool BF16>
+__global__ void __launch_bounds__(kMaskThreads)
+    kda_mask_logits_kernel(LogitsParams p) {
+  constexpr int G = BF16 ? 8 : 4;            // entries of 16 bytes
+  constexpr int U = 4, kMaskChunk = U * kMaskThreads * G;
+  constexpr uint32_t all = (1u << G) - 1;
+  typedef typename Act<BF16>::T E;
+  const int m = p.mask_from + blockIdx.y, v0 = blockIdx.x * kMaskChunk;
+  if (p.qsl && (m < p.qsl[0] || m >= p.qsl[p.B])) return;
+  const int32_t* mask = mask_at(p, p.mask_rows ? p.mask_rows[m] : m);
+  if (!mask) return;
+  E* x = static_cast<E*>(p.logits) + m * p.s_row;
+  const bool wide = reinterpret_cast<uintptr_t>(x) % 16 == 0;
+  uint32_t out[U];
+  u4 v[U];
 #pragma unroll
-        for (int k = 0; k < G; ++k) {
-          float y = BF16 ? bf16_to_f32(uint16_t(v[k / 2] >> (k % 2 * 16)))
-                         : __uint_as_float(v[BF16 ? 0 : k]);
-          if ((changed >> k) & 1) y = change(c, y, w[k], v0 + i + k);
-          if ((out >> k) & 1) y = -INFINITY;
-          if (!(((changed | out) >> k) & 1)) continue;
-          if constexpr (BF16)
-            v[k / 2] = (v[k / 2] & (0xffff0000u >> (k % 2 * 16))) |
-                       (uint32_t(f32_to_bf16(y)) << (k % 2 * 16));
-          else
-            v[k] = __float_as_uint(y);
-        }
-        *reinterpret_cast<u4*>(x + i) = v;
-      } else {
-        for (int k = 0; k < G && i + k < nv; ++k) {
-          if ((out >> k) & 1)
-            st_elem(x, i + k, -INFINITY, BF16);
-          else if ((changed >> k) & 1)
-            st_elem(x, i + k,
-                    change(c, ld_elem(x, i + k, BF16), words[i + k],
-                           v0 + i + k),
-                    BF16);
+  for (int k = 0; k < U; ++k) {
+    const int i = v0 + (k * kMaskThreads + int(threadIdx.x)) * G;
+    out[k] = i < p.V ? ~(uint32_t(mask[i >> 5]) >> (i & 31)) & all : 0u;
+  }
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const int i = v0 + (k * kMaskThreads + int(threadIdx.x)) * G;
+    v[k] = u4{0, 0, 0, 0};
+    if (out[k] && out[k] != all && wide && i + G <= p.V)
+      v[k] = *reinterpret_cast<const u4*>(x + i);
+  }
+#pragma unroll
+  for (int k = 0; k < U; ++k) {
+    const int i = v0 + (k * kMaskThreads + int(threadIdx.x)) * G;
+    if (!out[k]) continue;
+    if (wide && i + G <= p.V) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (BF16) {
+          const uint32_t lo = (out[k] >> (2 * j)) & 1,
+                         hi = (out[k] >> (2 * j + 1)) & 1;
+          const uint32_t part = ((0u - lo) & 0xffffu) | (0u - hi) << 16;
+          v[k][j] = (v[k][j] & ~part) | (0xff80ff80u & part);
+        } else {
+          if ((out[k] >> j) & 1) v[k][j] = 0xff800000u;
         }
       }
+      *reinterpret_cast<u4*>(x + i) = v[k];
+    } else {
+      for (int j = 0; j < G && i + j < p.V; ++j)
+        if ((out[k] >> j) & 1) st_elem(x, i + j, -INFINITY, BF16);
     }
   }
 }
 
 }  // namespace
 
-int64_t logits_slices(int64_t V) { return (V + kSlice - 1) / kSlice; }
+namespace {
+template <bool BF16>
+int launch(const LogitsParams& p, hipStream_t stream) {
+  if (p.rep || p.freq || p.pres || p.bias_start) {
+    // a workgroup takes some 16 rows of an average window; the slices of
+    // requests that the table does not take are shared by up to 32 (where the
+    // longest history fits, there are none)
+    const int64_t rows = (int64_t(p.M) / p.B + 15) / 16;
+    const int64_t z = rows < 1 ? 1 : rows > 64 ? 64 : rows;
+    const int64_t most = int64_t(p.L) + p.num_bias + p.M;
+    const int64_t slices = (int64_t(p.V) + kSlice - 1) / kSlice;
+    const int64_t x = most <= kMost ? 1 : slices > 32 ? 32 : slices;
+    constexpr int lds = (3 * kPlaces + kPlaces / 2) * 4;
+    static_assert(lds >= (2 * kSlice + kSlice / 2) * 4, "LDS");
+    const auto kernel = kda_adjust_logits_kernel<BF16>;
+    const hipError_t e = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(kernel),
+        hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return int(e);
+    launch_kernel(kernel, dim3(uint32_t(x), p.B, uint32_t(z)), dim3(kThreads),
+                  p.bias_start ? lds : lds - kPlaces * 4, stream, p);
+  }
+  if (p.mask) {
+    constexpr int kMaskChunk = 4 * kMaskThreads * (BF16 ? 8 : 4);
+    LogitsParams q = p;
+    // (rows in launches of what a grid takes)
+    for (int64_t m = 0; m < p.M; m += kMaskRows) {
+      q.mask_from = int32_t(m);
+      const int64_t n = p.M - m < kMaskRows ? p.M - m : kMaskRows;
+      launch_kernel(kda_mask_logits_kernel<BF16>,
+                    dim3((p.V - 1) / kMaskChunk + 1, uint32_t(n)),
+                    dim3(kMaskThreads), 0, stream, q);
+    }
+  }
+  return int(hipGetLastError());
+}
+}  // namespace
 
 int launch_adjust_logits(const LogitsParams& p, bool bf16,
                          hipStream_t stream) {
-  // a workgroup takes some 16 rows of an average window
-  const int64_t z = (int64_t(p.M) / p.B + 15) / 16;
-  const dim3 grid(uint32_t(logits_slices(p.V)), p.B,
-                  uint32_t(z < 1 ? 1 : z > 64 ? 64 : z));
-  if (bf16)
-    launch_kernel(kda_adjust_logits_kernel<true>, grid, dim3(kThreads), 0,
-                  stream, p);
-  else
-    launch_kernel(kda_adjust_logits_kernel<false>, grid, dim3(kThreads), 0,
-                  stream, p);
-  return int(hipGetLastError());
+  return bf16 ? launch<true>(p, stream) : launch<false>(p, stream);
 }
 
 }  // namespace kda

@@ -205,6 +205,12 @@ HELD = [
     dict(rows=30, width=7, N=9000, released=1.0),
     dict(rows=30, width=7, N=40, released=0.0, fill=1.0),
     dict(rows=600, width=40, N=100000, fill=0.9),
+    # around what one workgroup takes
+    dict(rows=40, width=9, N=16384, fill=0.02),
+    dict(rows=40, width=9, N=16385, fill=0.02, null=3),
+    dict(rows=4097, width=2, N=300, pinned=True),
+    dict(rows=256, width=256, N=5000),
+    dict(rows=257, width=256, N=5000, released=0.9),
 ]
 
 

@@ -91,6 +91,11 @@ CASES = [
     dict(lens=[100, 3], V=500, act="f32", hist=90),     # windows shared
     dict(lens=[0, 0], V=100, act="f32", tail=2),
     dict(lens=[2, 1], V=131072, act="bf16", hist=5000),
+    # histories around what the table takes, and longer
+    dict(lens=[3, 0, 1, 2], V=20001, act="bf16", hist=6130, pad=1),
+    dict(lens=[80, 5], V=9001, act="f32", hist=7000),
+    dict(lens=[70, 66], V=400, act="bf16", hist=40),
+    dict(lens=[2] * 9, V=140000, act="f32", hist=9000),
 ]
 
 
