@@ -150,13 +150,11 @@ int plan_paged(const Args* a, const kda_tensor& cache, kda::PagedParams* p) {
   return KDA_OK;
 }
 
-int64_t latent_bytes(int64_t T, int64_t B, int64_t H, int64_t R, int64_t P,
-                     bool bf16) {
+int64_t latent_bytes(int64_t T, int64_t B, int64_t H, int64_t R, int64_t P) {
   if (T < 0 || B < 0 || H < 1 || B > kI32Max || T > kI32Max ||
       H > kI32Max || T * H > kI32Max - 256 || !latent_dims(R, P))
     return 0;
-  return kda::latent_work_bytes(kda::latent_groups(T, B, H, int(R), bf16),
-                                int(R));
+  return kda::latent_work_bytes(kda::latent_groups(T, B, H), int(R));
 }
 
 struct LatentPlan {
@@ -207,7 +205,7 @@ int plan_latent(const kda_latent_args* a, LatentPlan* plan) {
   KDA_TRY(check_lse(a->lse, T, H));
   KDA_TRY(plan_paged(a, a->cache, &p.c));
   const bool bf16 = act == KDA_BF16;
-  const int64_t need = latent_bytes(T, a->batch, H, R, P, bf16);
+  const int64_t need = latent_bytes(T, a->batch, H, R, P);
   if (need == 0)
     return fail(KDA_E_CAPACITY, "tokens and heads exceed 2^31 rows");
   plan->noop = a->batch == 0 || T == 0;
@@ -244,7 +242,7 @@ int plan_latent(const kda_latent_args* a, LatentPlan* plan) {
   p.scale = a->softmax_scale * kLog2e;
   p.T = int32_t(T);
   p.H = int32_t(H);
-  p.group = kda::latent_groups(T, a->batch, H, int(R), bf16);
+  p.group = kda::latent_groups(T, a->batch, H);
   p.workers = kda::kLatentWorkers;
   plan->R = int(R);
   plan->P = int(P);
@@ -678,8 +676,7 @@ int64_t kda_latent_attention_workspace_size(int64_t tokens, int64_t batch,
                                             int64_t rope_dim,
                                             int32_t act_dtype) {
   if (elem_size(act_dtype) == 0) return 0;
-  return latent_bytes(tokens, batch, num_heads, latent_dim, rope_dim,
-                      act_dtype == KDA_BF16);
+  return latent_bytes(tokens, batch, num_heads, latent_dim, rope_dim);
 }
 
 int kda_check_latent_attention(const kda_latent_args* args) {

@@ -15,10 +15,11 @@
 // and O (R values) in registers.  The values are the keys' tile in LDS, read
 // transposed.
 //
-// A workgroup of four waves takes `RG` groups of 32 rows; the waves that are
-// left over divide the tokens of a step (TG token groups of 32), each with a
-// softmax of its own, joined through LDS at the end.  (fp32: DS = 2 waves
-// share the dimensions of O, which with q would not fit the registers.)
+// A workgroup takes RG groups of 32 rows (1 or 2) and 32 tokens a step, with
+// DS = 4 waves to each group: one with all of q and O has no registers left.
+// Each sums a quarter of the R + P products of all scores, gets the others'
+// parts of the scores of 8 tokens through LDS, takes their weights, gives
+// those to the others, and sums a quarter of the dimensions of O.
 //
 // Work is divided by tokens, not by requests: `workers` workgroups take equal
 // runs of the steps of all requests laid end to end, so that one long request
@@ -35,10 +36,10 @@
 namespace kda {
 namespace {
 
-constexpr int kTile = 32;          // tokens of a wave's step
+constexpr int kTile = 32;          // tokens of a step
 constexpr int kTab = 512;          // block table entries kept in LDS
-constexpr int kThreads = 256;
 constexpr float kLog2e = 1.44269504088896340736f;
+
 // A run's piece of a request that another workgroup continues.
 struct Piece {
   int32_t b, row_tile, last, pad;   // b < 0: none
@@ -68,68 +69,79 @@ __device__ __forceinline__ Request load_request(const PagedParams& p, int T,
 template <bool BF16, int R, int P, int RG>
 struct Shape {
   static constexpr int ES = BF16 ? 2 : 4;
-  // waves that share the values' dimensions: q and O have to fit a wave's
-  // registers (each of them forms the same scores)
-  static constexpr int DS = R == 512 ? (BF16 ? 2 : 4) : R == 256 && !BF16 ? 2 : 1;
-  static constexpr int TG = 4 / (RG * DS);     // token groups
-  static constexpr int SHARE = RG * DS;        // waves that share a tile
+  static constexpr int DS = 4;                 // waves of a row group
+  static constexpr int WAVES = RG * DS, THREADS = 64 * WAVES;
   static constexpr int CH = R * ES / 16;       // chunks of a latent
   static constexpr int CHP = P * ES / 16;      // and of a rope key
-  static constexpr int KF = (R + P) * ES / 32; // operands of a row
+  static constexpr int KL = CH / 2 / DS, KP = CHP / 2 / DS;  // operands of a
+  static constexpr int KF = KL + KP;                         // row, a wave's
   static constexpr int NB = R / 32 / DS;       // blocks of O of a wave
   static constexpr int TILE = kTile * (CH + CHP) * 16;
-  static constexpr int NBUF = 147456 / TILE / TG > 4 ? 4 : 147456 / TILE / TG;
   static constexpr int ROPE = kTile * CH * 16; // the rope part of a tile
-  static constexpr int LOADS = kTile * (CH + CHP) / 64;
-  static constexpr int MINE = LOADS / SHARE;   // loads of a wave
+  static constexpr int LL = kTile * CH / 64, LP = kTile * CHP / 64;  // loads
+  static constexpr int NL = LL / WAVES;        // of a wave
+  static constexpr int NP = (LP + WAVES - 1) / WAVES;
+  static constexpr int MINE = NL + NP;
   static constexpr int ROWS = 32 * RG;
-  static constexpr int STEP = kTile * TG;      // tokens of a step
-  static constexpr int BUFS = TG * NBUF * TILE;
-  static constexpr int LDS = BUFS + kTab * 4;
-  static_assert(kTile * CH / 64 % SHARE == 0 && kTile * CHP / 64 % SHARE == 0 &&
-                    TG >= 1 && NBUF >= 1,
-                "shape");
+  // what a wave gets of the others: three parts of its scores; then its own
+  // weights, maxima and, at the end, sums, for the others
+  static constexpr int BOX = 3 * 1024;
+  static constexpr int EXCH = WAVES * BOX;
+  static constexpr int REST = EXCH + kTab * 4;
+  static constexpr int FIT = (160 * 1024 - 256 - REST) / TILE;
+  static constexpr int NBUF = FIT > 4 ? 4 : FIT;
+  static constexpr int LDS = NBUF * TILE + REST;
+  static_assert(LL % WAVES == 0 && NBUF >= 1, "shape");
 };
 
+// Row tiles of a request, and steps of each.
 __device__ __forceinline__ int steps_of(const Request& r, int H, int rows,
-                                            int step, int* tiles) {
+                                        int* tiles) {
   *tiles = int((int64_t(r.q) * H + rows - 1) / rows);
-  return max((r.n + step - 1) / step, 1);
+  return max((r.n + kTile - 1) / kTile, 1);
 }
 
 template <bool BF16, int R, int P, int RG>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(256 * RG, RG)
     kda_latent_attention_kernel(LatentParams p) {
   using Z = Shape<BF16, R, P, RG>;
+  constexpr int kThreads = Z::THREADS;
   extern __shared__ __align__(16) char smem[];
-  int32_t* tab = reinterpret_cast<int32_t*>(smem + Z::BUFS);
+  char* exch = smem + Z::NBUF * Z::TILE;
+  int32_t* tab = reinterpret_cast<int32_t*>(exch + Z::EXCH);
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
   const int wave = uniform(tid >> 6);
-  const int tg = wave / Z::SHARE, share = wave % Z::SHARE;
-  const int ds = share % Z::DS, rg = share / Z::DS;
+  const int ds = wave % Z::DS, rg = wave / Z::DS;
   const PagedParams& c = p.c;
   const int W = p.workers, w = blockIdx.x;
 
   // -- this workgroup's run: steps [first, last) of all requests ------------
   Piece* plan = reinterpret_cast<Piece*>(p.work);
-  __shared__ int64_t red[4];
+  __shared__ int64_t red[Z::WAVES];
   __shared__ int32_t found_b;
   __shared__ int64_t found_at;
+  __shared__ int32_t flag[Z::WAVES];
+  auto steps_at = [&](int b) -> int64_t {
+    if (b >= c.B) return 0;
+    const Request r = load_request(c, p.T, b);
+    int tiles;
+    const int steps = steps_of(r, p.H, Z::ROWS, &tiles);
+    return int64_t(steps) * tiles;
+  };
+  auto wave_sums = [&](int64_t v) {            // of all waves, in order
+    if (lane == 63) red[wave] = v;
+    __syncthreads();
+    int64_t all = 0;
+    for (int k = 0; k < Z::WAVES; ++k) all += red[k];
+    return all;
+  };
   int64_t total = 0;
+  const int64_t mine0 = steps_at(tid);         // (of most batches, all)
   for (int b0 = 0; b0 < c.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    int64_t v = 0;
-    if (b < c.B) {
-      const Request r = load_request(c, p.T, b);
-      int tiles;
-      const int steps = steps_of(r, p.H, Z::ROWS, Z::STEP, &tiles);
-      v = int64_t(steps) * tiles;
-    }
+    int64_t v = b0 == 0 ? mine0 : steps_at(b0 + tid);
 #pragma unroll
     for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
-    if (lane == 0) red[wave] = v;
-    __syncthreads();
-    total += red[0] + red[1] + red[2] + red[3];
+    total += wave_sums(v);
     __syncthreads();
   }
   const int64_t per = max((total + W - 1) / W, int64_t(1));
@@ -138,30 +150,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (first >= last) return;
   int64_t done = 0;
   for (int b0 = 0; b0 < c.B; b0 += kThreads) {
-    const int b = b0 + tid;
-    int64_t v = 0;
-    if (b < c.B) {
-      const Request r = load_request(c, p.T, b);
-      int tiles;
-      const int steps = steps_of(r, p.H, Z::ROWS, Z::STEP, &tiles);
-      v = int64_t(steps) * tiles;
-    }
+    const int64_t v = b0 == 0 ? mine0 : steps_at(b0 + tid);
     int64_t upto = v;
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) {
       const int64_t o = __shfl_up(upto, s);
       if (lane >= s) upto += o;
     }
-    if (lane == 63) red[wave] = upto;
-    __syncthreads();
-    int64_t before = done;
-    for (int k = 0; k < wave; ++k) before += red[k];
-    const int64_t at = before + upto - v;
+    const int64_t all = wave_sums(upto);
+    int64_t at = done + upto - v;
+    for (int k = 0; k < wave; ++k) at += red[k];
     if (v > 0 && at <= first && first < at + v) {
-      found_b = b;
+      found_b = b0 + tid;
       found_at = at;
     }
-    done += red[0] + red[1] + red[2] + red[3];
+    done += all;
     __syncthreads();
     if (done > first) break;
   }
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t item0 = found_at;      // the request's first step
   Request r = load_request(c, p.T, b);
   int tiles;
-  int steps = steps_of(r, p.H, Z::ROWS, Z::STEP, &tiles);
+  int steps = steps_of(r, p.H, Z::ROWS, &tiles);
   int rt = int((first - item0) / steps);
   // the run: from step s0 of row tile rt of request b, `left` steps
   int s0 = int(first - item0 - int64_t(rt) * steps);
@@ -181,20 +184,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s1 = int(min(int64_t(steps), s0 + left));
     const int rows = r.q * p.H;
     const int last_tok = min((rt + 1) * Z::ROWS, rows) - 1;
-    // keys of the row tile, and of this lane's query
+    // keys of the row tile, and of this lane's query; steps that have any
     const int n = int(min(int64_t(r.c) + last_tok / p.H + 1, int64_t(r.n)));
-    int lim;
-    u4 q[Z::KF];
-    {
-      const int mine = min(rt * Z::ROWS + rg * 32 + (lane & 31), rows - 1);
-      const int tok = mine / p.H, head = mine - tok * p.H;
-      lim = int(min(int64_t(r.c) + tok + 1, int64_t(r.n)));
-      const char* src = p.q + int64_t(r.bos + tok) * p.s_q_tok +
-                        head * p.s_q_head + half * 16;
-#pragma unroll
-      for (int k = 0; k < Z::KF; ++k)
-        q[k] = *reinterpret_cast<const u4*>(src + 32 * k);
-    }
+    const int mine = min(rt * Z::ROWS + rg * 32 + (lane & 31), rows - 1);
+    const int lim = int(min(int64_t(r.c) + mine / p.H + 1, int64_t(r.n)));
+    const int end = min(s1, (n + kTile - 1) / kTile);
     f16v o[Z::NB];
 #pragma unroll
     for (int k = 0; k < Z::NB; ++k)
@@ -204,12 +198,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     int tab0 = -1;                      // first table entry in LDS
     const int32_t* table = c.table + int64_t(max(r.row, 0)) * c.s_tab_row;
-    // A step's tokens: where they are, for the lanes 0..31 of token group tg.
-    uint32_t live[Z::NBUF];
+    // Loads a step's tile; returns which of its tokens are there.
     auto stage = [&](int step, int buf) -> uint32_t {
-      const int e_lo = step * Z::STEP / c.block;
-      const int e_hi = (step * Z::STEP + Z::STEP - 1) / c.block;
-      if (tab0 < 0 || e_lo < tab0 || e_hi >= tab0 + kTab) {
+      const int e_lo = step * kTile / c.block;
+      const int e_hi = (step * kTile + kTile - 1) / c.block;
+      if (tab0 < 0 || e_hi >= tab0 + kTab) {
         __syncthreads();
         tab0 = e_lo;
         for (int i = tid; i < kTab; i += kThreads)
@@ -218,9 +211,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                        : c.null_id;
         __syncthreads();
       }
-      const int t0 = step * Z::STEP + tg * kTile;
-      if (t0 >= n) return 0u;
-      const int pos = t0 + (lane & 31);
+      // lanes l and l + 32: token l
+      const int pos = step * kTile + (lane & 31);
       const int e = pos / c.block;
       const int id = tab[e - tab0];
       const bool ok = pos < n && id > c.null_id && id < c.N;
@@ -229,128 +221,194 @@ __global__ void __launch_bounds__(kThreads, 1)
                             : kZeros;
       const uint64_t a = reinterpret_cast<uint64_t>(addr);
       const uint32_t lo = uint32_t(a), hi = uint32_t(a >> 32);
-      const uint32_t lds =
-          uniform(lds_addr(smem) + (tg * Z::NBUF + buf) * Z::TILE);
+      const uint32_t lds = uniform(lds_addr(smem) + buf * Z::TILE);
       const int l = fresh_tid() & 63;
 #pragma unroll
-      for (int j = 0; j < Z::MINE; ++j) {
-        const int i = uniform(j * Z::SHARE + share);   // of 64 chunks each
-        // (the latents' loads come first, for each wave)
-        if (j < Z::MINE * Z::CH / (Z::CH + Z::CHP)) {
-          if constexpr (Z::CH >= 64) {             // part of one row
-            const int rw = i * 64 / Z::CH;
-            const uint64_t base =
-                (uint64_t(uint32_t(__builtin_amdgcn_readlane(int(hi), rw)))
-                 << 32) |
-                uint32_t(__builtin_amdgcn_readlane(int(lo), rw));
-            load_lds(base,
-                     uint32_t(((i * 64 % Z::CH + l) ^ swizzle<Z::CH>(rw)) *
-                              16),
-                     lds + i * 1024);
-          } else {                                 // a few rows
-            const int rw = i * (64 / Z::CH) + l / Z::CH;
-            const uint32_t alo = __shfl(int(lo), rw),
-                           ahi = __shfl(int(hi), rw);
-            load_lds(reinterpret_cast<const char*>(
-                         (uint64_t(ahi) << 32) | alo) +
-                         ((l % Z::CH) ^ swizzle<Z::CH>(rw)) * 16,
-                     lds + i * 1024);
-          }
-        } else if constexpr (Z::CHP > 0) {
-          const int rw = (i - kTile * Z::CH / 64) * (64 / Z::CHP) +
-                         l / Z::CHP;
+      for (int j = 0; j < Z::NL; ++j) {
+        const int i = uniform(j * Z::WAVES + wave);    // of 64 chunks each
+        if constexpr (Z::CH >= 64) {                 // part of one row
+          const int rw = i * 64 / Z::CH;
+          const uint64_t base =
+              (uint64_t(uint32_t(__builtin_amdgcn_readlane(int(hi), rw)))
+               << 32) |
+              uint32_t(__builtin_amdgcn_readlane(int(lo), rw));
+          load_lds(base,
+                   uint32_t(((i * 64 % Z::CH + l) ^ swizzle<Z::CH>(rw)) * 16),
+                   lds + i * 1024);
+        } else {                                     // a few rows
+          const int rw = i * (64 / Z::CH) + l / Z::CH;
+          const uint32_t alo = __shfl(int(lo), rw), ahi = __shfl(int(hi), rw);
+          load_lds(reinterpret_cast<const char*>((uint64_t(ahi) << 32) | alo) +
+                       ((l % Z::CH) ^ swizzle<Z::CH>(rw)) * 16,
+                   lds + i * 1024);
+        }
+      }
+      if constexpr (Z::CHP > 0) {
+#pragma unroll
+        for (int j = 0; j < Z::NP; ++j) {
+          // (with fewer loads than waves some are made twice, which keeps
+          // the number of every wave's loads the same)
+          const int i = uniform((j * Z::WAVES + wave) % Z::LP);
+          const int rw = i * (64 / Z::CHP) + l / Z::CHP;
           const uint32_t alo = __shfl(int(lo), rw), ahi = __shfl(int(hi), rw);
           load_lds(reinterpret_cast<const char*>((uint64_t(ahi) << 32) | alo) +
                        (Z::CH + ((l % Z::CHP) ^ swizzle<Z::CHP>(rw))) * 16,
-                   lds + i * 1024);
+                   lds + Z::ROPE + i * 1024);
         }
       }
       return uint32_t(__ballot(ok));
     };
 
-    // live[k]: which tokens of the step k ahead are there
+    constexpr int kAhead = Z::NBUF - 1;
+    uint32_t live[Z::NBUF];             // live[k]: of the step k ahead
 #pragma unroll
-    for (int k = 0; k < Z::NBUF - 1; ++k)
-      live[k] = s0 + k < s1 ? stage(s0 + k, k) : 0u;
+    for (int k = 0; k < kAhead; ++k)
+      live[k] = s0 + k < end ? stage(s0 + k, k) : 0u;
+    // The queries, after the first tiles' loads and waited for here: a wait
+    // in the loop would wait for the tiles under way, too.
+    u4 q[Z::KF];
+    {
+      const int tok = mine / p.H, head = mine - tok * p.H;
+      const char* src = p.q + int64_t(r.bos + tok) * p.s_q_tok +
+                        head * p.s_q_head + (2 * ds + half) * 16;
+#pragma unroll
+      for (int k = 0; k < Z::KF; ++k)
+        q[k] = *reinterpret_cast<const u4*>(src + 32 * Z::DS * k);
+#pragma unroll
+      for (int k = 0; k < Z::KF; ++k) asm volatile("" : "+v"(q[k]));
+    }
     int buf = 0;
-    // steps of the run in which this token group has tokens
-    const int mine = min(s1, (n - tg * kTile + Z::STEP - 1) / Z::STEP);
 #pragma unroll 1
-    for (int s = s0; s < s1; ++s) {
-      constexpr int kAhead = Z::NBUF - 1;
-      // the buffer that the last step has read takes the next loads
-      if (Z::SHARE > 1) lds_barrier();
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      const int nb = buf == 0 ? kAhead : buf - 1;
-      live[kAhead] = s + kAhead < s1 ? stage(s + kAhead, nb) : 0u;
-      wait_tile<kAhead>(mine - s, std::integral_constant<int, Z::MINE>());
-      if (Z::SHARE > 1) lds_barrier();
-      const int t0 = s * Z::STEP + tg * kTile;
-      const char* tile = smem + (tg * Z::NBUF + buf) * Z::TILE;
-      if (t0 < n)
-        attend<BF16, Z::CH, Z::CHP, Z::CH>(tile, tile + Z::ROPE, tile,
-                                           ds * Z::NB, q, o, top, sum,
-                                           live[0], min(lim - t0, kTile),
-                                           p.scale);
+    for (int s = s0; s < end; ++s) {
+      if constexpr (kAhead == 0) {
+        lds_barrier();                  // the last step's tile is read
+        live[0] = stage(s, 0);
+        wait_vm<0>();
+        lds_barrier();
+      } else {
+        wait_tile<kAhead - 1>(end - s,
+                              std::integral_constant<int, Z::MINE>());
+        lds_barrier();                  // and the last step's tile is read
+        live[kAhead] = s + kAhead < end ? stage(s + kAhead, buf ? buf - 1
+                                                                : kAhead)
+                                        : 0u;
+      }
+      const char* tile = smem + buf * Z::TILE;
+      const int l = fresh_tid() & 63;
+      const f4* box = reinterpret_cast<const f4*>(exch + wave * Z::BOX) + l;
+      // this wave's part of the scores; the others' registers to them
+      f4 own;
+      {
+        const RowReader<Z::CH, Z::DS> latents(tile, l, ds);
+        const RowReader<(Z::CHP > 0 ? Z::CHP : 8), Z::DS> ropes(
+            tile + Z::ROPE, l, ds);
+        const f16v part = score<BF16>(
+            [&](int k) { return k < Z::KL ? latents(k) : ropes(k - Z::KL); },
+            q);
+#pragma unroll
+        for (int d = 0; d < Z::DS; ++d) {
+          const f4 v = {part[4 * d], part[4 * d + 1], part[4 * d + 2],
+                        part[4 * d + 3]};
+          if (d == ds)
+            own = v;
+          else
+            reinterpret_cast<f4*>(exch + (rg * Z::DS + d) * Z::BOX)
+                [(ds > d ? ds - 1 : ds) * 64 + l] = v;
+        }
+      }
+      lds_barrier();
+      // scores of its own eight tokens, their maximum and weights
+      float x[4], m = -INFINITY;
+#pragma unroll
+      for (int d = 0; d < 3; ++d) {
+        const f4 v = box[d * 64];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) own[e] += v[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 8 * ds + 4 * (l >> 5) + e;
+        const bool see = t < lim - s * kTile && ((live[0] >> t) & 1);
+        x[e] = see ? own[e] * p.scale : -INFINITY;
+        m = fmaxf(m, x[e]);
+      }
+      m = halves_max(m);
+      const bool high = __any(m > top + kSlack);
+      auto weights = [&](float (&y)[4]) {
+        const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = __builtin_amdgcn_exp2f(x[e] - base);
+        char* to = exch + wave * Z::BOX;
+        if constexpr (BF16)
+          reinterpret_cast<u2*>(to)[l] = u2{pack_bf16(y[0], y[1]),
+                                            pack_bf16(y[2], y[3])};
+        else
+          reinterpret_cast<f4*>(to)[l] = f4{y[0], y[1], y[2], y[3]};
+      };
+      float y[4];
+      weights(y);
+      reinterpret_cast<float*>(exch + wave * Z::BOX + 2048)[l] = m;
+      if (l == 0) flag[wave] = high;
+      lds_barrier();
+      int any = 0;
+#pragma unroll
+      for (int k = 0; k < Z::WAVES; ++k) any |= flag[k];
+      if (uniform(any)) {
+        // the running maximum moves: weights anew, O and the sum scaled
+        float to = top;
+#pragma unroll
+        for (int d = 0; d < Z::DS; ++d)
+          to = fmaxf(to, reinterpret_cast<const float*>(
+                             exch + (rg * Z::DS + d) * Z::BOX + 2048)[l]);
+        const float by = top == -INFINITY ? 0.0f : exp2f(top - to);
+        top = to;
+        sum *= by;
+#pragma unroll
+        for (int k = 0; k < Z::NB; ++k)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[k][i] *= by;
+        lds_barrier();
+        weights(y);
+        lds_barrier();
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum += y[e];
+      const char* all = exch + rg * Z::DS * Z::BOX;
+      if constexpr (BF16) {
+        u4 pr[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const u2 a = reinterpret_cast<const u2*>(all + 2 * t * Z::BOX)[l];
+          const u2 b = reinterpret_cast<const u2*>(all + (2 * t + 1) *
+                                                   Z::BOX)[l];
+          pr[t] = u4{a[0], a[1], b[0], b[1]};
+        }
+        weigh_bf16<Z::CH>(tile, ds * Z::NB, l, pr, o);
+      } else {
+        float z[16];
+#pragma unroll
+        for (int d = 0; d < Z::DS; ++d) {
+          const f4 a = reinterpret_cast<const f4*>(all + d * Z::BOX)[l];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[4 * d + e] = a[e];
+        }
+        weigh_f32<Z::CH>(tile, ds * Z::NB, l, z, o);
+      }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) live[k] = live[k + 1];
       buf = buf + 1 == Z::NBUF ? 0 : buf + 1;
     }
-    sum = halves_sum(sum);
-
-    // -- the token groups' sums joined: the first of them ends with them ----
-    if constexpr (Z::TG > 1) {
-      float* box = reinterpret_cast<float*>(smem);
-      constexpr int kBlocks = 8;           // blocks of O that move at a time
-      static_assert(Z::TG * Z::SHARE * 64 * 2 * 4 <= Z::BUFS, "statistics");
-      __syncthreads();
-      box[(wave * 64 + lane) * 2] = top;
-      box[(wave * 64 + lane) * 2 + 1] = sum;
-      __syncthreads();
-      float to = top;
+    {
+      // the waves' sums over their own tokens, joined
+      sum = halves_sum(sum);
+      lds_barrier();
+      reinterpret_cast<float*>(exch + wave * Z::BOX)[lane] = sum;
+      lds_barrier();
+      sum = 0.0f;
 #pragma unroll
-      for (int g = 0; g < Z::TG; ++g)
-        to = fmaxf(to, box[((g * Z::SHARE + share) * 64 + lane) * 2]);
-      float all = 0.0f;
-#pragma unroll
-      for (int g = 0; g < Z::TG; ++g) {
-        const float* e = box + ((g * Z::SHARE + share) * 64 + lane) * 2;
-        all += e[0] == -INFINITY ? 0.0f : exp2f(e[0] - to) * e[1];
-      }
-      const float by = top == -INFINITY ? 0.0f : exp2f(top - to);
-      top = to;
-      sum = all;
-#pragma unroll
-      for (int k = 0; k < Z::NB; ++k)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[k][i] *= by;
-#pragma unroll
-      for (int k0 = 0; k0 < Z::NB; k0 += kBlocks)
-#pragma unroll
-        for (int g = 1; g < Z::TG; ++g) {
-          __syncthreads();
-          if (tg == g)
-#pragma unroll
-            for (int k = k0; k < k0 + kBlocks && k < Z::NB; ++k)
-#pragma unroll
-              for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<f4*>(
-                    box + (((share * kBlocks + k - k0) * 4 + i / 4) * 64 +
-                           lane) * 4) =
-                    f4{o[k][i], o[k][i + 1], o[k][i + 2], o[k][i + 3]};
-          __syncthreads();
-          if (tg == 0)
-#pragma unroll
-            for (int k = k0; k < k0 + kBlocks && k < Z::NB; ++k)
-#pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                const f4 v = *reinterpret_cast<const f4*>(
-                    box + (((share * kBlocks + k - k0) * 4 + i / 4) * 64 +
-                           lane) * 4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[k][i + e] += v[e];
-              }
-        }
+      for (int d = 0; d < Z::DS; ++d)
+        sum += reinterpret_cast<const float*>(
+            exch + (rg * Z::DS + d) * Z::BOX)[lane];
     }
 
     // -- the whole of it: outputs; a piece: to the workspace ------------------
@@ -359,52 +417,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int lane = fresh_tid() & 63, half = lane >> 5;
     const int row = rt * Z::ROWS + rg * 32 + (lane & 31);
     const int tok = row / p.H, head = row - tok * p.H;
-    if (tg == 0) {
-      if (whole) {
-        if (row < rows) {
-          const float by = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-          char* dst = p.out + int64_t(r.bos + tok) * p.s_out_tok +
-                      head * p.s_out_head;
-#pragma unroll
-          for (int k = 0; k < Z::NB; ++k)
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-              const int e = 32 * (ds * Z::NB + k) + acc_row(i, half);
-              if constexpr (BF16)
-                *reinterpret_cast<u2*>(dst + e * 2) =
-                    u2{pack_bf16(o[k][i] * by, o[k][i + 1] * by),
-                       pack_bf16(o[k][i + 2] * by, o[k][i + 3] * by)};
-              else
-                *reinterpret_cast<f4*>(dst + e * 4) =
-                    f4{o[k][i] * by, o[k][i + 1] * by, o[k][i + 2] * by,
-                       o[k][i + 3] * by};
-            }
-          if (p.lse && half == 0 && ds == 0)
-            p.lse[int64_t(r.bos + tok) * p.s_lse_tok + head * p.s_lse_head] =
-                sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
-        }
-      } else {
-        const int slot = s0 == 0 ? 2 * w + 1 : 2 * w;
-        float* ml = reinterpret_cast<float*>(p.work + W * sizeof(Piece)) +
-                    int64_t(slot) * Z::ROWS * 2;
-        float* to = reinterpret_cast<float*>(
-                        p.work + W * sizeof(Piece) +
-                        int64_t(2) * W * Z::ROWS * 8) +
-                    (int64_t(slot) * RG + rg) * 32 * R;
-        if (half == 0 && ds == 0) {
-          ml[(rg * 32 + lane) * 2] = top;
-          ml[(rg * 32 + lane) * 2 + 1] = sum;
-        }
+    if (whole) {
+      if (row < rows) {
+        const float by = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+        char* dst = p.out + int64_t(r.bos + tok) * p.s_out_tok +
+                    head * p.s_out_head;
 #pragma unroll
         for (int k = 0; k < Z::NB; ++k)
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<f4*>(
-                to + (((ds * Z::NB + k) * 4 + i / 4) * 64 + lane) * 4) =
-                f4{o[k][i], o[k][i + 1], o[k][i + 2], o[k][i + 3]};
-        if (s0 == 0 && tid == 0)
-          plan[w] = Piece{b, rt, w + int((steps - left + per - 1) / per), 0};
+          for (int i = 0; i < 16; i += 4) {
+            const int e = 32 * (ds * Z::NB + k) + acc_row(i, half);
+            if constexpr (BF16)
+              *reinterpret_cast<u2*>(dst + e * 2) =
+                  u2{pack_bf16(o[k][i] * by, o[k][i + 1] * by),
+                     pack_bf16(o[k][i + 2] * by, o[k][i + 3] * by)};
+            else
+              *reinterpret_cast<f4*>(dst + e * 4) =
+                  f4{o[k][i] * by, o[k][i + 1] * by, o[k][i + 2] * by,
+                     o[k][i + 3] * by};
+          }
+        if (p.lse && half == 0 && ds == 0)
+          p.lse[int64_t(r.bos + tok) * p.s_lse_tok + head * p.s_lse_head] =
+              sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
       }
+    } else {
+      const int slot = s0 == 0 ? 2 * w + 1 : 2 * w;
+      float* ml = reinterpret_cast<float*>(p.work + W * sizeof(Piece)) +
+                  int64_t(slot) * Z::ROWS * 2;
+      float* to = reinterpret_cast<float*>(p.work + W * sizeof(Piece) +
+                                           int64_t(2) * W * Z::ROWS * 8) +
+                  (int64_t(slot) * RG + rg) * 32 * R;
+      if (half == 0 && ds == 0) {
+        ml[(rg * 32 + lane) * 2] = top;
+        ml[(rg * 32 + lane) * 2 + 1] = sum;
+      }
+#pragma unroll
+      for (int k = 0; k < Z::NB; ++k)
+#pragma unroll
+        for (int i = 0; i < 16; i += 4)
+          *reinterpret_cast<f4*>(
+              to + (((ds * Z::NB + k) * 4 + i / 4) * 64 + lane) * 4) =
+              f4{o[k][i], o[k][i + 1], o[k][i + 2], o[k][i + 3]};
+      if (s0 == 0 && tid == 0)
+        plan[w] = Piece{b, rt, w + int((steps - left + per - 1) / per), 0};
     }
     left -= s1 - s0;
     if (left <= 0) return;
@@ -415,60 +470,100 @@ __global__ void __launch_bounds__(kThreads, 1)
       do {
         r = load_request(c, p.T, ++b);
       } while (r.q == 0);
-      steps = steps_of(r, p.H, Z::ROWS, Z::STEP, &tiles);
+      steps = steps_of(r, p.H, Z::ROWS, &tiles);
     }
   }
 }
 
-// Joins the pieces of row tiles that several workgroups shared: a wave takes
-// four registers' worth of one 32-row group at a time, in the order in which
-// the lanes of the first kernel had them.
+// Joins the pieces of row tiles that several workgroups shared: a workgroup
+// takes 32 dimensions of a 32-row group, in the order in which the lanes of the
+// first kernel had them, its waves every fourth piece.
+constexpr int kJoinWaves = 4;
 template <bool BF16, int R, int RG>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(64 * kJoinWaves)
     kda_latent_join_kernel(LatentParams p) {
-  constexpr int kUnits = R / 8;            // of 4 values for each lane
-  const int w = blockIdx.x, rg = blockIdx.z, W = p.workers;
+  __shared__ float tops[8][32], sums[kJoinWaves][64];
+  __shared__ f4 box[kJoinWaves][4][64];
+  const int w = blockIdx.x, u = blockIdx.y, rg = blockIdx.z, W = p.workers;
   const Piece piece = reinterpret_cast<const Piece*>(p.work)[w];
   if (piece.b < 0) return;
-  const int lane = threadIdx.x & 63, half = lane >> 5;
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = uniform(tid >> 6);
   const float* ml = reinterpret_cast<const float*>(p.work +
-                                                   W * sizeof(Piece));
-  const float* parts = ml + int64_t(2) * W * 32 * RG * 2;
+                                                   W * sizeof(Piece)) +
+                    rg * 64;
+  const f4* parts = reinterpret_cast<const f4*>(
+                        p.work + W * sizeof(Piece) +
+                        int64_t(2) * W * 32 * RG * 8) +
+                    rg * (8 * R) + u * 256 + lane;
+  const int count = piece.last - w + 1;
+  auto slot = [&](int i) {
+    return int64_t(i == 0 ? 2 * w + 1 : 2 * (w + i));
+  };
+  // (the first pieces are under way while the maximum is found)
+  constexpr int U = 4;
+  f4 acc[4], v[U][4];
+  f2 e[U];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const int64_t at = slot(min(i0 + k * kJoinWaves, count - 1)) * RG;
+      e[k] = *reinterpret_cast<const f2*>(ml + at * 64 + (lane & 31) * 2);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[k][j] = parts[at * (8 * R) + j * 64];
+    }
+  };
+  fetch(wave);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = f4{0, 0, 0, 0};
+  float top = -INFINITY, sum = 0.0f;
+  for (int i = tid >> 5; i < count; i += 8)
+    top = fmaxf(top, ml[slot(i) * RG * 64 + (tid & 31) * 2]);
+  tops[tid >> 5][tid & 31] = top;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) top = fmaxf(top, tops[k][lane & 31]);
+  for (int i0 = wave; i0 < count; i0 += U * kJoinWaves) {
+    if (i0 != wave) fetch(i0);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (i0 + k * kJoinWaves >= count) break;
+      const float by = e[k][0] == -INFINITY ? 0.0f : exp2f(e[k][0] - top);
+      sum += by * e[k][1];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) acc[j][d] += by * v[k][j][d];
+    }
+  }
+  sums[wave][lane] = sum;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) box[wave][j][lane] = acc[j];
+  __syncthreads();
+  // wave j: four dimensions of each half
+  f4 o = box[0][wave][lane];
+#pragma unroll
+  for (int k = 1; k < kJoinWaves; ++k)
+#pragma unroll
+    for (int d = 0; d < 4; ++d) o[d] += box[k][wave][lane][d];
+  sum = 0.0f;
+#pragma unroll
+  for (int k = 0; k < kJoinWaves; ++k) sum += sums[k][lane];
   const Request r = load_request(p.c, p.T, piece.b);
   const int row = piece.row_tile * 32 * RG + rg * 32 + (lane & 31);
-  const int count = piece.last - w + 1;
-  auto slot = [&](int i) { return i == 0 ? 2 * w + 1 : 2 * (w + i); };
-  float top = -INFINITY;
-  for (int i = 0; i < count; ++i)
-    top = fmaxf(top, ml[(int64_t(slot(i)) * 32 * RG + rg * 32 +
-                         (lane & 31)) * 2]);
-  const int u = blockIdx.y * (kThreads / 64) + (threadIdx.x >> 6);
-  float sum = 0.0f;
-  f4 acc = {0, 0, 0, 0};
-  for (int i = 0; i < count; ++i) {
-    const float* e =
-        ml + (int64_t(slot(i)) * 32 * RG + rg * 32 + (lane & 31)) * 2;
-    const float by = e[0] == -INFINITY ? 0.0f : exp2f(e[0] - top);
-    sum += by * e[1];
-    const f4 v = *reinterpret_cast<const f4*>(
-        parts + (int64_t(slot(i)) * RG + rg) * 32 * R + (u * 64 + lane) * 4);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) acc[k] += by * v[k];
-  }
-  if (row >= r.q * p.H || u >= kUnits) return;
+  if (row >= r.q * p.H) return;
   const int tok = row / p.H, head = row - tok * p.H;
   const float by = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-  const int at = 32 * (u / 4) + acc_row(u % 4 * 4, half);
+  const int at = 32 * u + acc_row(wave * 4, half);
   char* dst = p.out + int64_t(r.bos + tok) * p.s_out_tok +
               head * p.s_out_head;
   if constexpr (BF16)
     *reinterpret_cast<u2*>(dst + at * 2) =
-        u2{pack_bf16(acc[0] * by, acc[1] * by),
-           pack_bf16(acc[2] * by, acc[3] * by)};
+        u2{pack_bf16(o[0] * by, o[1] * by), pack_bf16(o[2] * by, o[3] * by)};
   else
     *reinterpret_cast<f4*>(dst + at * 4) =
-        f4{acc[0] * by, acc[1] * by, acc[2] * by, acc[3] * by};
-  if (p.lse && half == 0 && u == 0)
+        f4{o[0] * by, o[1] * by, o[2] * by, o[3] * by};
+  if (p.lse && half == 0 && u == 0 && wave == 0)
     p.lse[int64_t(r.bos + tok) * p.s_lse_tok + head * p.s_lse_head] =
         sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
@@ -476,24 +571,24 @@ __global__ void __launch_bounds__(kThreads)
 template <bool BF16, int R, int P, int RG>
 int launch(const LatentParams& p, hipStream_t stream) {
   using Z = Shape<BF16, R, P, RG>;
-  static_assert(Z::LDS + 64 <= 160 * 1024, "LDS");
+  static_assert(Z::LDS + 256 <= 160 * 1024, "LDS");
   const hipError_t e = hipFuncSetAttribute(
       reinterpret_cast<const void*>(
           &kda_latent_attention_kernel<BF16, R, P, RG>),
       hipFuncAttributeMaxDynamicSharedMemorySize, Z::LDS);
   if (e != hipSuccess) return int(e);
   launch_kernel(kda_latent_attention_kernel<BF16, R, P, RG>, dim3(p.workers),
-                dim3(kThreads), Z::LDS, stream, p);
+                dim3(Z::THREADS), Z::LDS, stream, p);
   launch_kernel(kda_latent_join_kernel<BF16, R, RG>,
-                dim3(p.workers, R / 32, RG), dim3(kThreads), 0, stream, p);
+                dim3(p.workers, R / 32, RG), dim3(64 * kJoinWaves), 0, stream,
+                p);
   return int(hipGetLastError());
 }
 
 template <bool BF16, int R, int P>
 int launch_groups(const LatentParams& p, hipStream_t stream) {
   if (p.group == 1) return launch<BF16, R, P, 1>(p, stream);
-  if constexpr (BF16 || R < 512)
-    if (p.group == 2) return launch<BF16, R, P, 2>(p, stream);
+  if (p.group == 2) return launch<BF16, R, P, 2>(p, stream);
   return int(hipErrorInvalidValue);
 }
 
@@ -528,12 +623,11 @@ __global__ void __launch_bounds__(256)
 
 }  // namespace
 
-int latent_groups(int64_t T, int64_t B, int64_t H, int R,
-                  bool bf16) {
+int latent_groups(int64_t T, int64_t B, int64_t H) {
   // as many rows as an average request has, so that its tokens are read once
   const int64_t rows = B > 0 ? (T + B - 1) / B * H : H;
   if (rows <= 32) return 1;
-  return R == 512 && !bf16 ? 1 : 2;
+  return 2;
 }
 
 int64_t latent_work_bytes(int group, int R) {

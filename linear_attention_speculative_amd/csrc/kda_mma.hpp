@@ -10,6 +10,7 @@
 
 namespace kda {
 
+typedef float f2 __attribute__((ext_vector_type(2)));
 typedef float f16v __attribute__((ext_vector_type(16)));
 typedef __bf16 b8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u2 __attribute__((ext_vector_type(2)));
@@ -38,7 +39,6 @@ __device__ __forceinline__ f16v mma(u4 a, u4 b, f16v c) {
 // Two floats as bf16, rounded to nearest even; the first in the low half.
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   typedef __bf16 b2 __attribute__((ext_vector_type(2)));
-  typedef float f2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f2{a, b}, b2));
 }
 
@@ -108,25 +108,59 @@ __device__ __forceinline__ constexpr int place(int r, int c) {
   return r * CH + (c ^ swizzle<CH>(r));
 }
 
+// The operands of row l % 32 that share `part` of PARTS reads: its k-th is
+// chunk 2 (PARTS k + part) + l / 32.  The swizzle repeats every 16 chunks (8 in
+// rows of 8), so a few addresses and immediate offsets serve a whole row.
+template <int CH, int PARTS>
+struct RowReader {
+  static constexpr int PERIOD = CH >= 16 ? 16 : 8;
+  static constexpr int N = PERIOD / (2 * PARTS);   // operands of a period
+  static_assert(N >= 1, "parts");
+  const char* at[N];
+  __device__ __forceinline__ RowReader(const char* tile, int lane, int part) {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      at[k] = tile + place<CH>(lane & 31,
+                               2 * (PARTS * k + part) + (lane >> 5)) * 16;
+  }
+  __device__ __forceinline__ u4 operator()(int k) const {
+    return *reinterpret_cast<const u4*>(at[k % N] + k / N * (PERIOD * 16));
+  }
+};
+
 // The left operand of a product with the transpose of rows [t, t + 16) of a
-// bf16 tile: result row m = l % 32 is element 32 blk + m of the tile's rows;
-// lane half h sums over rows t + 4 h + {0..3} and t + 8 + 4 h + {0..3}, the
-// order in which a product's result has its own rows.
+// bf16 tile, t = 0 or 16: result row m = l % 32 is element 32 blk + m of the
+// tile's rows; lane half h sums over rows t + 4 h + {0..3} and t + 8 + 4 h +
+// {0..3}, the order in which a product's result has its own rows.
 template <int CH>
-__device__ __forceinline__ u4 load_transposed(const char* tile, int t,
-                                              int blk) {
-  typedef s4 __attribute__((address_space(3))) * lp;
-  const int l = threadIdx.x & 63, i = l & 15;
-  const int row = t + 4 * (l >> 5) + (i >> 2);
-  const int c = 4 * blk + 2 * ((l >> 4) & 1) + ((i & 3) >> 1);
-  const char* a = tile + place<CH>(row, c) * 16 + (i & 1) * 8;
-  const char* b = tile + place<CH>(row + 8, c) * 16 + (i & 1) * 8;
-  const u2 x = __builtin_bit_cast(
-      u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)a));
-  const u2 y = __builtin_bit_cast(
-      u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)b));
-  return u4{x[0], x[1], y[0], y[1]};
-}
+struct ColumnReader {
+  static constexpr int N = CH >= 16 ? 4 : 2;   // blocks of a swizzle's period
+  const char* at[N][2];
+  // blocks are counted from `blk0` on, at any place of a period
+  __device__ __forceinline__ ColumnReader(const char* tile, int blk0,
+                                          int lane) {
+    const int i = lane & 15;
+    const int row = 4 * (lane >> 5) + (i >> 2);
+    const int c = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        at[k][e] = tile + place<CH>(row + 8 * e, 4 * (blk0 + k) + c) * 16 +
+                   (i & 1) * 8;
+  }
+  __device__ __forceinline__ u4 operator()(int t, int blk) const {
+    typedef s4 __attribute__((address_space(3))) * lp;
+    const int off = t * CH * 16 + blk / N * (N * 64);
+    const u2 x = __builtin_bit_cast(
+        u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lp)(at[blk % N][0] + off)));
+    const u2 y = __builtin_bit_cast(
+        u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (lp)(at[blk % N][1] + off)));
+    return u4{x[0], x[1], y[0], y[1]};
+  }
+};
 
 // The running maximum is only moved when it is passed by more than this (in
 // powers of two): weights of up to 2^kSlack cost nothing in fp32 or bf16, and
@@ -149,33 +183,16 @@ __device__ __forceinline__ void wait_tile(int left,
   }
 }
 
-// 32 tokens against a wave's 32 queries, one a lane: S^T = K q^T, the softmax's
-// running maximum (`top`, in powers of two) and sum, O^T += V^T P^T.  Keys are
-// two tiles side by side (CH and CHP chunks a row), values NB blocks of 32 of a
-// tile's rows from block `blk` on.  `live`: which tokens are there; the lane's
-// query sees the first `left` of them.
-template <bool BF16, int CH, int CHP, int CHV, int KF, int NB>
-__device__ __forceinline__ void attend(const char* keys, const char* ropes,
-                                       const char* values, int blk,
-                                       const u4 (&q)[KF], f16v (&o)[NB],
-                                       float& top, float& sum, uint32_t live,
-                                       int left, float scale) {
-  constexpr int kTile = 32;
+// S^T = K q^T of 32 tokens and a wave's 32 queries, one a lane: key(k) is the
+// k-th operand of the lane's token.
+template <bool BF16, int KF, class Key>
+__device__ __forceinline__ f16v score(Key key, const u4 (&q)[KF]) {
   // (operands are read a few ahead of their products; without the borders
   // the compiler reads them all at once and has no registers left)
   constexpr int G = 3;
-  const int lane = fresh_tid() & 63, half = lane >> 5;
-  auto key = [&](int k) -> u4 {
-    const int ch = 2 * k + half;
-    const char* a =
-        2 * k < CH ? keys + place<CH>(lane & 31, ch) * 16
-                   : ropes + place<(CHP > 0 ? CHP : 8)>(lane & 31, ch - CH) *
-                                 16;
-    return *reinterpret_cast<const u4*>(a);
-  };
-  f16v x0;
+  f16v x;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x0[i] = 0.0f;
+  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
   u4 kk[2][G];
 #pragma unroll
   for (int j = 0; j < G && j < KF; ++j) kk[0][j] = key(j);
@@ -186,19 +203,30 @@ __device__ __forceinline__ void attend(const char* keys, const char* ropes,
       if (k + G + j < KF) kk[(k / G + 1) & 1][j] = key(k + G + j);
 #pragma unroll
     for (int j = 0; j < G; ++j)
-      if (k + j < KF) x0 = mma<BF16>(kk[(k / G) & 1][j], q[k + j], x0);
+      if (k + j < KF) x = mma<BF16>(kk[(k / G) & 1][j], q[k + j], x);
     __builtin_amdgcn_sched_barrier(0);
   }
-  float x[16], m = -INFINITY;
-  if (__all(left == kTile) && live == 0xffffffffu) {
+  return x;
+}
+
+// Softmax weights of those scores, in powers of two: the running maximum
+// `top` and sum, O scaled where the maximum moves.  `live`: which tokens are
+// there; the lane's query sees the first `left` of them.
+template <int NB>
+__device__ __forceinline__ void soften(const f16v& s, float scale,
+                                       uint32_t live, int left, int half,
+                                       float& top, float& sum, f16v (&o)[NB],
+                                       float (&x)[16]) {
+  float m = -INFINITY;
+  if (__all(left >= 32) && live == 0xffffffffu) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = x0[i] * scale;
+    for (int i = 0; i < 16; ++i) x[i] = s[i] * scale;
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int t = acc_row(i, half);
       const bool see = t < left && ((live >> t) & 1);
-      x[i] = see ? x0[i] * scale : -INFINITY;
+      x[i] = see ? s[i] * scale : -INFINITY;
     }
   }
 #pragma unroll
@@ -222,6 +250,53 @@ __device__ __forceinline__ void attend(const char* keys, const char* ropes,
     x[i] = __builtin_amdgcn_exp2f(x[i] - base);
     sum += x[i];
   }
+}
+
+// O^T += V^T P^T: NB blocks of 32 of the values' rows, from block `blk` on (a
+// multiple of NB where the rows have more).  bf16: pr[t] holds the weights of
+// tokens 16 t + 4 h + {0..3} and 16 t + 8 + 4 h + {0..3}, h = lane / 32.
+template <int CHV, int NB>
+__device__ __forceinline__ void weigh_bf16(const char* values, int blk,
+                                           int lane, const u4 (&pr)[2],
+                                           f16v (&o)[NB]) {
+  const ColumnReader<CHV> value_at(values, blk, lane);
+  u4 v[2][2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) v[0][t] = value_at(16 * t, 0);
+#pragma unroll
+  for (int k = 0; k < NB; ++k) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (k + 1 < NB) v[(k + 1) & 1][t] = value_at(16 * t, k + 1);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) o[k] = mma<true>(v[k & 1][t], pr[t], o[k]);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// fp32: x[i] is the weight of token acc_row(i, lane / 32).
+template <int CHV, int NB>
+__device__ __forceinline__ void weigh_f32(const char* values, int blk,
+                                          int lane, const float (&x)[16],
+                                          f16v (&o)[NB]) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const int t = acc_row(i, lane >> 5);
+#pragma unroll
+    for (int k = 0; k < NB; ++k) {
+      const int e = 32 * (blk + k) + (lane & 31);
+      const float v = *reinterpret_cast<const float*>(
+          values + place<CHV>(t, e / 4) * 16 + e % 4 * 4);
+      o[k] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, x[i], o[k], 0, 0, 0);
+    }
+    if (i & 1) __builtin_amdgcn_sched_barrier(0);
+  }
+}
+
+// Either, from the weights of a result's registers.
+template <bool BF16, int CHV, int NB>
+__device__ __forceinline__ void weigh(const char* values, int blk, int lane,
+                                      const float (&x)[16], f16v (&o)[NB]) {
   if constexpr (BF16) {
     u4 pr[2];
 #pragma unroll
@@ -230,34 +305,9 @@ __device__ __forceinline__ void attend(const char* keys, const char* ropes,
                  pack_bf16(x[8 * t + 2], x[8 * t + 3]),
                  pack_bf16(x[8 * t + 4], x[8 * t + 5]),
                  pack_bf16(x[8 * t + 6], x[8 * t + 7])};
-    u4 v[2][2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      v[0][t] = load_transposed<CHV>(values, 16 * t, blk);
-#pragma unroll
-    for (int k = 0; k < NB; ++k) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (k + 1 < NB)
-          v[(k + 1) & 1][t] =
-              load_transposed<CHV>(values, 16 * t, blk + k + 1);
-#pragma unroll
-      for (int t = 0; t < 2; ++t) o[k] = mma<true>(v[k & 1][t], pr[t], o[k]);
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    weigh_bf16<CHV>(values, blk, lane, pr, o);
   } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int t = acc_row(i, half);
-#pragma unroll
-      for (int k = 0; k < NB; ++k) {
-        const int e = 32 * (blk + k) + (lane & 31);
-        const float v = *reinterpret_cast<const float*>(
-            values + place<CHV>(t, e / 4) * 16 + e % 4 * 4);
-        o[k] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, x[i], o[k], 0, 0, 0);
-      }
-      if (i & 1) __builtin_amdgcn_sched_barrier(0);
-    }
+    weigh_f32<CHV>(values, blk, lane, x, o);
   }
 }
 

@@ -10,7 +10,7 @@
 // with W.
 //
 // The attention takes both products transposed, with a query a lane (see
-// attend() in kda_mma.hpp): a wave has 32 queries of one head, a workgroup
+// score(), soften() and weigh() in kda_mma.hpp): a wave has 32 queries of one head, a workgroup
 // eight waves, which share 64 keys and values at a time in LDS.  The expansion
 // is a matrix product of gathered cache rows with W, 128 x 128 a workgroup.
 #include "kda_cache.hpp"
@@ -244,14 +244,6 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
   const int n = ahead + min((tile + 1) * kQueries, len);
   const int steps = n > 0 ? (n + kKeys - 1) / kKeys : 0;
 
-  u4 q[Z::KF];
-  {
-    const char* src = p.q + int64_t(bos + min(tok, len - 1)) * p.s_q_tok +
-                      h * p.s_q_head + half * 16;
-#pragma unroll
-    for (int k = 0; k < Z::KF; ++k)
-      q[k] = *reinterpret_cast<const u4*>(src + 32 * k);
-  }
   f16v o[Z::NB];
 #pragma unroll
   for (int k = 0; k < Z::NB; ++k)
@@ -293,6 +285,18 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
 #pragma unroll
   for (int k = 0; k < kAhead; ++k)
     if (k < steps) stage(k, k);
+  // The queries, after the first tiles' loads and waited for here: a wait in
+  // the loop would wait for the tiles under way, too.
+  u4 q[Z::KF];
+  {
+    const char* src = p.q + int64_t(bos + min(tok, len - 1)) * p.s_q_tok +
+                      h * p.s_q_head + half * 16;
+#pragma unroll
+    for (int k = 0; k < Z::KF; ++k)
+      q[k] = *reinterpret_cast<const u4*>(src + 32 * k);
+#pragma unroll
+    for (int k = 0; k < Z::KF; ++k) asm volatile("" : "+v"(q[k]));
+  }
   int buf = 0;
 #pragma unroll 1
   for (int s = 0; s < steps; ++s) {
@@ -311,11 +315,20 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
 #pragma unroll
     for (int k = 0; k < kKeys; k += 32) {
       const int at = s * kKeys + k;
-      if (at < wave_lim)
-        attend<BF16, Z::CH, Z::CHP, Z::CH>(
-            tile + k * Z::CH * 16, tile + Z::ROPE + k * Z::CHP * 16,
-            tile + Z::VALUE + k * Z::CH * 16, 0, q, o, top, sum, 0xffffffffu,
-            min(lim - at, 32), p.scale);
+      if (at < wave_lim) {
+        const int l = fresh_tid() & 63;
+        const RowReader<Z::CH, 1> heads(tile + k * Z::CH * 16, l, 0);
+        const RowReader<(Z::CHP > 0 ? Z::CHP : 8), 1> ropes(
+            tile + Z::ROPE + k * Z::CHP * 16, l, 0);
+        const f16v sc = score<BF16>(
+            [&](int i) {
+              return i < Z::CH / 2 ? heads(i) : ropes(i - Z::CH / 2);
+            },
+            q);
+        float x[16];
+        soften(sc, p.scale, 0xffffffffu, lim - at, l >> 5, top, sum, o, x);
+        weigh<BF16, Z::CH>(tile + Z::VALUE + k * Z::CH * 16, 0, l, x, o);
+      }
     }
     buf = buf + 1 == Z::NBUF ? 0 : buf + 1;
   }
