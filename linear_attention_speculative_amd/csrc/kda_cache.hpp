@@ -18,6 +18,8 @@ struct PagedParams {
   int64_t s_blk, s_tok;      // bytes
   int32_t B, rows, width, block, null_id;
   int64_t N;                 // blocks of the cache
+  uint32_t magic;            // position / block = position * magic >> shift,
+  int32_t shift;             // for positions below 2^31
 };
 
 struct LatentWriteParams {

@@ -147,6 +147,12 @@ int plan_paged(const Args* a, const kda_tensor& cache, kda::PagedParams* p) {
   p->block = int32_t(cache.shape[1]);
   p->null_id = a->null_block_id;
   p->N = cache.shape[0];
+  // magic = ceil(2^(31 + l) / block), 2^l the power of two not below block: at
+  // most 2^32 - 1, and its error, below 1, times a position stays below 2^31
+  int l = 0;
+  while ((int64_t(1) << l) < p->block) ++l;
+  p->shift = 31 + l;
+  p->magic = uint32_t(((uint64_t(1) << p->shift) + p->block - 1) / p->block);
   return KDA_OK;
 }
 

@@ -51,6 +51,11 @@ struct Request {
   int c, n;             // computed tokens; keys, at most the table's
 };
 
+// Block of a position (below 2^31) in its request: position / block.
+__device__ __forceinline__ int block_of(const PagedParams& p, int pos) {
+  return int((uint64_t(uint32_t(pos)) * p.magic) >> p.shift);
+}
+
 __device__ __forceinline__ Request load_request(const PagedParams& p, int T,
                                                 int b) {
   Request r;
@@ -94,7 +99,11 @@ struct Shape {
   static_assert(LL % WAVES == 0 && NBUF >= 1, "shape");
 };
 
-// Row tiles of a request, and steps of each.
+// Row tiles of a request, and steps of each.  A row tile counts kStart steps
+// more when work is divided: what its queries, its first loads and its outputs
+// take (without them, 48 windows of draft tokens with short requests among them
+// took 63 us, the mean workgroup 41).
+constexpr int kStart = 4;
 __device__ __forceinline__ int steps_of(const Request& r, int H, int rows,
                                         int* tiles) {
   *tiles = int((int64_t(r.q) * H + rows - 1) / rows);
@@ -126,7 +135,7 @@ __global__ void __launch_bounds__(256 * RG, RG)
     const Request r = load_request(c, p.T, b);
     int tiles;
     const int steps = steps_of(r, p.H, Z::ROWS, &tiles);
-    return int64_t(steps) * tiles;
+    return int64_t(steps + kStart) * tiles;
   };
   auto wave_sums = [&](int64_t v) {            // of all waves, in order
     if (lane == 63) red[wave] = v;
@@ -173,15 +182,18 @@ __global__ void __launch_bounds__(256 * RG, RG)
   Request r = load_request(c, p.T, b);
   int tiles;
   int steps = steps_of(r, p.H, Z::ROWS, &tiles);
-  int rt = int((first - item0) / steps);
-  // the run: from step s0 of row tile rt of request b, `left` steps
-  int s0 = int(first - item0 - int64_t(rt) * steps);
+  int rt = int((first - item0) / (steps + kStart));
+  // the run: from unit u0 of row tile rt of request b, `left` units, of which
+  // the first kStart of a tile are no steps
+  int u0 = int(first - item0 - int64_t(rt) * (steps + kStart));
   int64_t left = last - first;
 
 #pragma unroll 1
   while (true) {
     // -- one piece: steps [s0, s1) of row tile rt of request b ----------------
-    const int s1 = int(min(int64_t(steps), s0 + left));
+    const int s0 = max(u0 - kStart, 0);
+    const int s1 = int(min(int64_t(steps), u0 + left - kStart));
+    if (s1 <= s0) return;               // (the next workgroup starts it)
     const int rows = r.q * p.H;
     const int last_tok = min((rt + 1) * Z::ROWS, rows) - 1;
     // keys of the row tile, and of this lane's query; steps that have any
@@ -200,11 +212,10 @@ __global__ void __launch_bounds__(256 * RG, RG)
     const int32_t* table = c.table + int64_t(max(r.row, 0)) * c.s_tab_row;
     // Loads a step's tile; returns which of its tokens are there.
     auto stage = [&](int step, int buf) -> uint32_t {
-      const int e_lo = step * kTile / c.block;
-      const int e_hi = (step * kTile + kTile - 1) / c.block;
+      const int e_hi = block_of(c, step * kTile + kTile - 1);
       if (tab0 < 0 || e_hi >= tab0 + kTab) {
         __syncthreads();
-        tab0 = e_lo;
+        tab0 = block_of(c, step * kTile);
         for (int i = tid; i < kTab; i += kThreads)
           tab[i] = int64_t(tab0) + i < c.width && r.row >= 0
                        ? table[int64_t(tab0 + i) * c.s_tab_col]
@@ -213,7 +224,7 @@ __global__ void __launch_bounds__(256 * RG, RG)
       }
       // lanes l and l + 32: token l
       const int pos = step * kTile + (lane & 31);
-      const int e = pos / c.block;
+      const int e = block_of(c, pos);
       const int id = tab[e - tab0];
       const bool ok = pos < n && id > c.null_id && id < c.N;
       const char* addr = ok ? c.cache + id * c.s_blk +
@@ -459,12 +470,12 @@ __global__ void __launch_bounds__(256 * RG, RG)
               to + (((ds * Z::NB + k) * 4 + i / 4) * 64 + lane) * 4) =
               f4{o[k][i], o[k][i + 1], o[k][i + 2], o[k][i + 3]};
       if (s0 == 0 && tid == 0)
-        plan[w] = Piece{b, rt, w + int((steps - left + per - 1) / per), 0};
+        plan[w] = Piece{b, rt, w + int((steps - s1 + per - 1) / per), 0};
     }
-    left -= s1 - s0;
+    left -= s1 + kStart - u0;
     if (left <= 0) return;
     __syncthreads();                       // LDS is free for the next piece
-    s0 = 0;
+    u0 = 0;
     if (++rt == tiles) {
       rt = 0;
       do {
@@ -477,14 +488,15 @@ __global__ void __launch_bounds__(256 * RG, RG)
 
 // Joins the pieces of row tiles that several workgroups shared: a workgroup
 // takes 32 dimensions of a 32-row group, in the order in which the lanes of the
-// first kernel had them, its waves every fourth piece.
+// first kernel had them, its waves every fourth piece.  Of few pieces each wave
+// takes all, for 32 dimensions of its own.
 constexpr int kJoinWaves = 4;
 template <bool BF16, int R, int RG>
 __global__ void __launch_bounds__(64 * kJoinWaves)
     kda_latent_join_kernel(LatentParams p) {
   __shared__ float tops[8][32], sums[kJoinWaves][64];
   __shared__ f4 box[kJoinWaves][4][64];
-  const int w = blockIdx.x, u = blockIdx.y, rg = blockIdx.z, W = p.workers;
+  const int w = blockIdx.x, rg = blockIdx.z, W = p.workers;
   const Piece piece = reinterpret_cast<const Piece*>(p.work)[w];
   if (piece.b < 0) return;
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -492,11 +504,15 @@ __global__ void __launch_bounds__(64 * kJoinWaves)
   const float* ml = reinterpret_cast<const float*>(p.work +
                                                    W * sizeof(Piece)) +
                     rg * 64;
+  const int count = piece.last - w + 1;
+  const bool few = count <= 4;
+  if (few && blockIdx.y % kJoinWaves != 0) return;
+  const int u = few ? blockIdx.y + wave : blockIdx.y;
+  const int start = few ? 0 : wave, stride = few ? 1 : kJoinWaves;
   const f4* parts = reinterpret_cast<const f4*>(
                         p.work + W * sizeof(Piece) +
                         int64_t(2) * W * 32 * RG * 8) +
                     rg * (8 * R) + u * 256 + lane;
-  const int count = piece.last - w + 1;
   auto slot = [&](int i) {
     return int64_t(i == 0 ? 2 * w + 1 : 2 * (w + i));
   };
@@ -507,13 +523,13 @@ __global__ void __launch_bounds__(64 * kJoinWaves)
   auto fetch = [&](int i0) {
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      const int64_t at = slot(min(i0 + k * kJoinWaves, count - 1)) * RG;
+      const int64_t at = slot(min(i0 + k * stride, count - 1)) * RG;
       e[k] = *reinterpret_cast<const f2*>(ml + at * 64 + (lane & 31) * 2);
 #pragma unroll
       for (int j = 0; j < 4; ++j) v[k][j] = parts[at * (8 * R) + j * 64];
     }
   };
-  fetch(wave);
+  fetch(start);
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = f4{0, 0, 0, 0};
   float top = -INFINITY, sum = 0.0f;
@@ -523,11 +539,11 @@ __global__ void __launch_bounds__(64 * kJoinWaves)
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 8; ++k) top = fmaxf(top, tops[k][lane & 31]);
-  for (int i0 = wave; i0 < count; i0 += U * kJoinWaves) {
-    if (i0 != wave) fetch(i0);
+  for (int i0 = start; i0 < count; i0 += U * stride) {
+    if (i0 != start) fetch(i0);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-      if (i0 + k * kJoinWaves >= count) break;
+      if (i0 + k * stride >= count) break;
       const float by = e[k][0] == -INFINITY ? 0.0f : exp2f(e[k][0] - top);
       sum += by * e[k][1];
 #pragma unroll
@@ -536,34 +552,43 @@ __global__ void __launch_bounds__(64 * kJoinWaves)
         for (int d = 0; d < 4; ++d) acc[j][d] += by * v[k][j][d];
     }
   }
-  sums[wave][lane] = sum;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) box[wave][j][lane] = acc[j];
-  __syncthreads();
-  // wave j: four dimensions of each half
-  f4 o = box[0][wave][lane];
-#pragma unroll
-  for (int k = 1; k < kJoinWaves; ++k)
-#pragma unroll
-    for (int d = 0; d < 4; ++d) o[d] += box[k][wave][lane][d];
-  sum = 0.0f;
-#pragma unroll
-  for (int k = 0; k < kJoinWaves; ++k) sum += sums[k][lane];
   const Request r = load_request(p.c, p.T, piece.b);
   const int row = piece.row_tile * 32 * RG + rg * 32 + (lane & 31);
-  if (row >= r.q * p.H) return;
   const int tok = row / p.H, head = row - tok * p.H;
-  const float by = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-  const int at = 32 * u + acc_row(wave * 4, half);
   char* dst = p.out + int64_t(r.bos + tok) * p.s_out_tok +
               head * p.s_out_head;
-  if constexpr (BF16)
-    *reinterpret_cast<u2*>(dst + at * 2) =
-        u2{pack_bf16(o[0] * by, o[1] * by), pack_bf16(o[2] * by, o[3] * by)};
-  else
-    *reinterpret_cast<f4*>(dst + at * 4) =
-        f4{o[0] * by, o[1] * by, o[2] * by, o[3] * by};
-  if (p.lse && half == 0 && u == 0 && wave == 0)
+  // four dimensions of each half from `at` on
+  auto write = [&](const f4& o, int at, float by) {
+    if constexpr (BF16)
+      *reinterpret_cast<u2*>(dst + at * 2) = u2{
+          pack_bf16(o[0] * by, o[1] * by), pack_bf16(o[2] * by, o[3] * by)};
+    else
+      *reinterpret_cast<f4*>(dst + at * 4) =
+          f4{o[0] * by, o[1] * by, o[2] * by, o[3] * by};
+  };
+  if (!few) {
+    sums[wave][lane] = sum;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) box[wave][j][lane] = acc[j];
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kJoinWaves; ++k) sum += sums[k][lane];
+  }
+  if (row >= r.q * p.H) return;
+  const float by = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+  if (few) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) write(acc[j], 32 * u + acc_row(4 * j, half), by);
+  } else {
+    f4 o = box[0][wave][lane];
+#pragma unroll
+    for (int k = 1; k < kJoinWaves; ++k)
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[d] += box[k][wave][lane][d];
+    write(o, 32 * u + acc_row(4 * wave, half), by);
+  }
+  if (p.lse && half == 0 && u == 0 && (few || wave == 0))
     p.lse[int64_t(r.bos + tok) * p.s_lse_tok + head * p.s_lse_head] =
         sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
