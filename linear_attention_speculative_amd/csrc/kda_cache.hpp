@@ -44,7 +44,8 @@ struct LatentParams {
   float* lse;                    // or null
   int64_t s_lse_tok, s_lse_head;
   char* work;
-  float scale;                   // softmax scale times log2 e
+  float scale;                   // softmax scale times log2 e, above 0,
+  int32_t negate;                // and whether that is of negated queries
   int32_t T, H;
   int32_t group;                 // rows of a workgroup / 32: 1 or 2
   int32_t workers;
@@ -87,7 +88,8 @@ struct PromptParams {
   int64_t s_lse_tok, s_lse_head;
   const int32_t* qsl;
   const int32_t* ksl;
-  float scale;                   // softmax scale times log2 e
+  float scale;                   // as in LatentParams
+  int32_t negate;
   int32_t T, S, H, B;
 };
 int64_t prompt_tiles(int64_t T, int64_t B);

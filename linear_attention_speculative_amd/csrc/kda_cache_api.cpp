@@ -62,6 +62,15 @@ int check_cache(const kda_tensor& t) {
   return check_rows(t, "cache");
 }
 
+// The kernels take scales above 0: queries are negated for one below, and a
+// scale of 0 is one that leaves no difference between scores.
+template <class Params>
+void set_scale(float scale, Params* p) {
+  p->negate = scale < 0.0f;
+  p->scale = (scale < 0.0f ? -scale : scale) * kLog2e;
+  if (p->scale == 0.0f) p->scale = 0x1p-126f;
+}
+
 bool latent_dims(int64_t R, int64_t P) {
   return (R == 128 || R == 256 || R == 512) && (P == 0 || P == 64);
 }
@@ -245,7 +254,7 @@ int plan_latent(const kda_latent_args* a, LatentPlan* plan) {
   p.s_lse_tok = a->lse.stride[0];
   p.s_lse_head = a->lse.stride[1];
   p.work = static_cast<char*>(a->workspace);
-  p.scale = a->softmax_scale * kLog2e;
+  set_scale(a->softmax_scale, &p);
   p.T = int32_t(T);
   p.H = int32_t(H);
   p.group = kda::latent_groups(T, a->batch, H);
@@ -401,7 +410,7 @@ int plan_prompt(const kda_latent_prefill_args* a, PromptPlan* plan) {
   p.s_lse_head = a->lse.stride[1];
   p.qsl = a->query_start_loc;
   p.ksl = a->key_start_loc;
-  p.scale = a->softmax_scale * kLog2e;
+  set_scale(a->softmax_scale, &p);
   p.T = int32_t(T);
   p.S = int32_t(S);
   p.H = int32_t(H);

@@ -284,7 +284,8 @@ __global__ void __launch_bounds__(256 * RG, RG)
                         head * p.s_q_head + (2 * ds + half) * 16;
 #pragma unroll
       for (int k = 0; k < Z::KF; ++k)
-        q[k] = *reinterpret_cast<const u4*>(src + 32 * Z::DS * k);
+        q[k] = negated<BF16>(
+            *reinterpret_cast<const u4*>(src + 32 * Z::DS * k), p.negate);
 #pragma unroll
       for (int k = 0; k < Z::KF; ++k) asm volatile("" : "+v"(q[k]));
     }
@@ -304,7 +305,7 @@ __global__ void __launch_bounds__(256 * RG, RG)
                                                                 : kAhead)
                                         : 0u;
       }
-      const char* tile = smem + buf * Z::TILE;
+      const uint32_t tile = uniform(lds_addr(smem) + buf * Z::TILE);
       const int l = fresh_tid() & 63;
       const f4* box = reinterpret_cast<const f4*>(exch + wave * Z::BOX) + l;
       // this wave's part of the scores; the others' registers to them
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(256 * RG, RG)
                                                    Z::BOX)[l];
           pr[t] = u4{a[0], a[1], b[0], b[1]};
         }
-        weigh_bf16<Z::CH>(tile, ds * Z::NB, l, pr, o);
+        weigh_bf16(ColumnReader<Z::CH>(tile, ds * Z::NB, l), 0, pr, o);
       } else {
         float z[16];
 #pragma unroll

@@ -110,35 +110,40 @@ __device__ __forceinline__ constexpr int place(int r, int c) {
 
 // The operands of row l % 32 that share `part` of PARTS reads: its k-th is
 // chunk 2 (PARTS k + part) + l / 32.  The swizzle repeats every 16 chunks (8 in
-// rows of 8), so a few addresses and immediate offsets serve a whole row.
+// rows of 8), so a few addresses and immediate offsets serve a whole row, and
+// rows 32 further on; the addresses move with the tile.
+typedef __attribute__((address_space(3))) const u4* lds_u4;
 template <int CH, int PARTS>
 struct RowReader {
   static constexpr int PERIOD = CH >= 16 ? 16 : 8;
   static constexpr int N = PERIOD / (2 * PARTS);   // operands of a period
   static_assert(N >= 1, "parts");
-  const char* at[N];
-  __device__ __forceinline__ RowReader(const char* tile, int lane, int part) {
+  uint32_t at[N];
+  __device__ __forceinline__ RowReader(uint32_t tile, int lane, int part) {
 #pragma unroll
     for (int k = 0; k < N; ++k)
       at[k] = tile + place<CH>(lane & 31,
                                2 * (PARTS * k + part) + (lane >> 5)) * 16;
   }
-  __device__ __forceinline__ u4 operator()(int k) const {
-    return *reinterpret_cast<const u4*>(at[k % N] + k / N * (PERIOD * 16));
+  __device__ __forceinline__ u4 operator()(int k, int row = 0) const {
+    return *(lds_u4)uintptr_t(at[k % N] + (k / N * PERIOD + row * CH) * 16);
+  }
+  __device__ __forceinline__ void move(int by) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) at[k] += by;
   }
 };
 
 // The left operand of a product with the transpose of rows [t, t + 16) of a
-// bf16 tile, t = 0 or 16: result row m = l % 32 is element 32 blk + m of the
-// tile's rows; lane half h sums over rows t + 4 h + {0..3} and t + 8 + 4 h +
+// bf16 tile, t a multiple of 16: result row m = l % 32 is element 32 blk + m of
+// the tile's rows; lane half h sums over rows t + 4 h + {0..3} and t + 8 + 4 h +
 // {0..3}, the order in which a product's result has its own rows.
 template <int CH>
 struct ColumnReader {
   static constexpr int N = CH >= 16 ? 4 : 2;   // blocks of a swizzle's period
-  const char* at[N][2];
+  uint32_t at[N][2];
   // blocks are counted from `blk0` on, at any place of a period
-  __device__ __forceinline__ ColumnReader(const char* tile, int blk0,
-                                          int lane) {
+  __device__ __forceinline__ ColumnReader(uint32_t tile, int blk0, int lane) {
     const int i = lane & 15;
     const int row = 4 * (lane >> 5) + (i >> 2);
     const int c = 2 * ((lane >> 4) & 1) + ((i & 3) >> 1);
@@ -154,13 +159,30 @@ struct ColumnReader {
     const int off = t * CH * 16 + blk / N * (N * 64);
     const u2 x = __builtin_bit_cast(
         u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lp)(at[blk % N][0] + off)));
+                (lp)uintptr_t(at[blk % N][0] + off)));
     const u2 y = __builtin_bit_cast(
         u2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (lp)(at[blk % N][1] + off)));
+                (lp)uintptr_t(at[blk % N][1] + off)));
     return u4{x[0], x[1], y[0], y[1]};
   }
+  __device__ __forceinline__ void move(int by) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      at[k][0] += by;
+      at[k][1] += by;
+    }
+  }
 };
+
+// The fp32 counterpart: one value, element 32 blk + l % 32 of row t, of a tile
+// at `tile`.
+template <int CH>
+__device__ __forceinline__ float column_value(uint32_t tile, int t, int blk,
+                                              int lane) {
+  const int e = 32 * blk + (lane & 31);
+  return *(__attribute__((address_space(3))) const float*)uintptr_t(
+      tile + place<CH>(t, e / 4) * 16 + e % 4 * 4);
+}
 
 // The running maximum is only moved when it is passed by more than this (in
 // powers of two): weights of up to 2^kSlack cost nothing in fp32 or bf16, and
@@ -210,28 +232,22 @@ __device__ __forceinline__ f16v score(Key key, const u4 (&q)[KF]) {
 }
 
 // Softmax weights of those scores, in powers of two: the running maximum
-// `top` and sum, O scaled where the maximum moves.  `live`: which tokens are
-// there; the lane's query sees the first `left` of them.
+// `top` and sum, O scaled where the maximum moves.  The lane's query sees the
+// first `left` tokens; scale > 0.
 template <int NB>
-__device__ __forceinline__ void soften(const f16v& s, float scale,
-                                       uint32_t live, int left, int half,
-                                       float& top, float& sum, f16v (&o)[NB],
-                                       float (&x)[16]) {
-  float m = -INFINITY;
-  if (__all(left >= 32) && live == 0xffffffffu) {
+__device__ __forceinline__ void soften(f16v& s, float scale, int left,
+                                       int half, float& top, float& sum,
+                                       f16v (&o)[NB], float (&x)[16]) {
+  if (!__all(left >= 32)) {
+    asm volatile("");                  // (a branch of its own)
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = s[i] * scale;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int t = acc_row(i, half);
-      const bool see = t < left && ((live >> t) & 1);
-      x[i] = see ? s[i] * scale : -INFINITY;
-    }
+    for (int i = 0; i < 16; ++i)
+      s[i] = acc_row(i, half) < left ? s[i] : -INFINITY;
   }
+  float m = fmaxf(s[0], s[1]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) m = fmaxf(m, x[i]);
-  m = halves_max(m);
+  for (int i = 2; i < 16; i += 2) m = fmaxf(fmaxf(m, s[i]), s[i + 1]);
+  m = halves_max(m) * scale;
   if (__any(m > top + kSlack)) {
     const float to = fmaxf(top, m);
     const float by = top == -INFINITY ? 0.0f : exp2f(top - to);
@@ -244,71 +260,70 @@ __device__ __forceinline__ void soften(const f16v& s, float scale,
       __builtin_amdgcn_sched_barrier(0);
     }
   }
-  const float base = top == -INFINITY ? 0.0f : top;
+  const float base = top == -INFINITY ? 0.0f : -top;
+  float part[4] = {sum, 0.0f, 0.0f, 0.0f};
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    x[i] = __builtin_amdgcn_exp2f(x[i] - base);
-    sum += x[i];
+    x[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[i], scale, base));
+    part[i & 3] += x[i];
   }
+  sum = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// O^T += V^T P^T: NB blocks of 32 of the values' rows, from block `blk` on (a
-// multiple of NB where the rows have more).  bf16: pr[t] holds the weights of
-// tokens 16 t + 4 h + {0..3} and 16 t + 8 + 4 h + {0..3}, h = lane / 32.
-template <int CHV, int NB>
-__device__ __forceinline__ void weigh_bf16(const char* values, int blk,
-                                           int lane, const u4 (&pr)[2],
-                                           f16v (&o)[NB]) {
-  const ColumnReader<CHV> value_at(values, blk, lane);
+// The weights of a result's registers as operands: pr[t] holds tokens 16 t + 4
+// h + {0..3} and 16 t + 8 + 4 h + {0..3}, h = lane / 32.
+__device__ __forceinline__ void pack_weights(const float (&x)[16],
+                                             u4 (&pr)[2]) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    pr[t] = u4{pack_bf16(x[8 * t], x[8 * t + 1]),
+               pack_bf16(x[8 * t + 2], x[8 * t + 3]),
+               pack_bf16(x[8 * t + 4], x[8 * t + 5]),
+               pack_bf16(x[8 * t + 6], x[8 * t + 7])};
+}
+
+// O^T += V^T P^T: NB blocks of 32 of the values' rows [row, row + 32).
+template <int NB, class Column>
+__device__ __forceinline__ void weigh_bf16(const Column& value_at, int row,
+                                           const u4 (&pr)[2], f16v (&o)[NB]) {
   u4 v[2][2];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) v[0][t] = value_at(16 * t, 0);
+  for (int t = 0; t < 2; ++t) v[0][t] = value_at(row + 16 * t, 0);
 #pragma unroll
   for (int k = 0; k < NB; ++k) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
-      if (k + 1 < NB) v[(k + 1) & 1][t] = value_at(16 * t, k + 1);
+      if (k + 1 < NB) v[(k + 1) & 1][t] = value_at(row + 16 * t, k + 1);
 #pragma unroll
     for (int t = 0; t < 2; ++t) o[k] = mma<true>(v[k & 1][t], pr[t], o[k]);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// fp32: x[i] is the weight of token acc_row(i, lane / 32).
+// fp32: x[i] is the weight of token acc_row(i, lane / 32) of the tile's.
 template <int CHV, int NB>
-__device__ __forceinline__ void weigh_f32(const char* values, int blk,
-                                          int lane, const float (&x)[16],
+__device__ __forceinline__ void weigh_f32(uint32_t values, int blk, int lane,
+                                          const float (&x)[16],
                                           f16v (&o)[NB]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
-    const int t = acc_row(i, lane >> 5);
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
-      const int e = 32 * (blk + k) + (lane & 31);
-      const float v = *reinterpret_cast<const float*>(
-          values + place<CHV>(t, e / 4) * 16 + e % 4 * 4);
-      o[k] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, x[i], o[k], 0, 0, 0);
-    }
+    for (int k = 0; k < NB; ++k)
+      o[k] = __builtin_amdgcn_mfma_f32_32x32x2f32(
+          column_value<CHV>(values, acc_row(i, lane >> 5), blk + k, lane),
+          x[i], o[k], 0, 0, 0);
     if (i & 1) __builtin_amdgcn_sched_barrier(0);
   }
 }
 
-// Either, from the weights of a result's registers.
-template <bool BF16, int CHV, int NB>
-__device__ __forceinline__ void weigh(const char* values, int blk, int lane,
-                                      const float (&x)[16], f16v (&o)[NB]) {
-  if constexpr (BF16) {
-    u4 pr[2];
+// Query operands of a scale below 0 are negated, so that scores rise with their
+// weights.
+template <bool BF16>
+__device__ __forceinline__ u4 negated(u4 q, bool yes) {
+  const uint32_t flip = !yes ? 0u : BF16 ? 0x80008000u : 0x80000000u;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-      pr[t] = u4{pack_bf16(x[8 * t], x[8 * t + 1]),
-                 pack_bf16(x[8 * t + 2], x[8 * t + 3]),
-                 pack_bf16(x[8 * t + 4], x[8 * t + 5]),
-                 pack_bf16(x[8 * t + 6], x[8 * t + 7])};
-    weigh_bf16<CHV>(values, blk, lane, pr, o);
-  } else {
-    weigh_f32<CHV>(values, blk, lane, x, o);
-  }
+  for (int e = 0; e < 4; ++e) q[e] ^= flip;
+  return q;
 }
 
 }  // namespace kda

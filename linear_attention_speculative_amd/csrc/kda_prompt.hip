@@ -10,7 +10,8 @@
 // with W.
 //
 // The attention takes both products transposed, with a query a lane (see
-// score(), soften() and weigh() in kda_mma.hpp): a wave has 32 queries of one head, a workgroup
+// score(), soften() and weigh_bf16() in
+// kda_mma.hpp): a wave has 32 queries of one head, a workgroup
 // eight waves, which share 64 keys and values at a time in LDS.  The expansion
 // is a matrix product of gathered cache rows with W, 128 x 128 a workgroup.
 #include "kda_cache.hpp"
@@ -293,11 +294,15 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
                       h * p.s_q_head + half * 16;
 #pragma unroll
     for (int k = 0; k < Z::KF; ++k)
-      q[k] = *reinterpret_cast<const u4*>(src + 32 * k);
+      q[k] = negated<BF16>(*reinterpret_cast<const u4*>(src + 32 * k),
+                           p.negate);
 #pragma unroll
     for (int k = 0; k < Z::KF; ++k) asm volatile("" : "+v"(q[k]));
   }
   int buf = 0;
+  RowReader<Z::CH, 1> heads(lds0, lane, 0);
+  RowReader<(Z::CHP > 0 ? Z::CHP : 8), 1> ropes(lds0 + Z::ROPE, lane, 0);
+  ColumnReader<Z::CH> values(lds0 + Z::VALUE, 0, lane);
 #pragma unroll 1
   for (int s = 0; s < steps; ++s) {
     if constexpr (kAhead == 0) {
@@ -311,26 +316,33 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
       lds_barrier();                       // and the last step's tile is read
       if (s + kAhead < steps) stage(s + kAhead, buf ? buf - 1 : kAhead);
     }
-    const char* tile = smem + buf * Z::TILE;
 #pragma unroll
     for (int k = 0; k < kKeys; k += 32) {
       const int at = s * kKeys + k;
       if (at < wave_lim) {
-        const int l = fresh_tid() & 63;
-        const RowReader<Z::CH, 1> heads(tile + k * Z::CH * 16, l, 0);
-        const RowReader<(Z::CHP > 0 ? Z::CHP : 8), 1> ropes(
-            tile + Z::ROPE + k * Z::CHP * 16, l, 0);
-        const f16v sc = score<BF16>(
+        f16v sc = score<BF16>(
             [&](int i) {
-              return i < Z::CH / 2 ? heads(i) : ropes(i - Z::CH / 2);
+              return i < Z::CH / 2 ? heads(i, k) : ropes(i - Z::CH / 2, k);
             },
             q);
         float x[16];
-        soften(sc, p.scale, 0xffffffffu, lim - at, l >> 5, top, sum, o, x);
-        weigh<BF16, Z::CH>(tile + Z::VALUE + k * Z::CH * 16, 0, l, x, o);
+        soften(sc, p.scale, lim - at, half, top, sum, o, x);
+        if constexpr (BF16) {
+          u4 pr[2];
+          pack_weights(x, pr);
+          weigh_bf16(values, k, pr, o);
+        } else {
+          weigh_f32<Z::CH>(lds0 + buf * Z::TILE + Z::VALUE + k * Z::CH * 16, 0,
+                           fresh_tid() & 63, x, o);
+        }
       }
     }
-    buf = buf + 1 == Z::NBUF ? 0 : buf + 1;
+    const bool wrap = buf + 1 == Z::NBUF;
+    const int by = uniform(wrap ? -buf * Z::TILE : Z::TILE);
+    buf = wrap ? 0 : buf + 1;
+    heads.move(by);
+    if (Z::CHP > 0) ropes.move(by);
+    if (BF16) values.move(by);
   }
   sum = halves_sum(sum);
   if (tok >= len) return;
