@@ -231,35 +231,44 @@ __device__ __forceinline__ f16v score(Key key, const u4 (&q)[KF]) {
   return x;
 }
 
-// Softmax weights of those scores, in powers of two: the running maximum
-// `top` and sum, O scaled where the maximum moves.  The lane's query sees the
-// first `left` tokens; scale > 0.
-template <int NB>
-__device__ __forceinline__ void soften(f16v& s, float scale, int left,
-                                       int half, float& top, float& sum,
-                                       f16v (&o)[NB], float (&x)[16]) {
-  if (!__all(left >= 32)) {
-    asm volatile("");                  // (a branch of its own)
+// Scores that the lane's query does not see (it sees the first `left` tokens).
+__device__ __forceinline__ void hide(f16v& s, int left, int half) {
+  if (__all(left >= 32)) return;
+  asm volatile("");                    // (a branch of its own)
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-      s[i] = acc_row(i, half) < left ? s[i] : -INFINITY;
-  }
+  for (int i = 0; i < 16; ++i)
+    s[i] = acc_row(i, half) < left ? s[i] : -INFINITY;
+}
+
+// The largest score of the lane's query.
+__device__ __forceinline__ float highest(const f16v& s) {
   float m = fmaxf(s[0], s[1]);
 #pragma unroll
   for (int i = 2; i < 16; i += 2) m = fmaxf(fmaxf(m, s[i]), s[i + 1]);
-  m = halves_max(m) * scale;
-  if (__any(m > top + kSlack)) {
-    const float to = fmaxf(top, m);
-    const float by = top == -INFINITY ? 0.0f : exp2f(top - to);
-    top = to;
-    sum *= by;
+  return halves_max(m);
+}
+
+// Moves the running maximum `top` (in powers of two) to m where it is passed by
+// more than kSlack, and scales the sum and O with it.
+template <int NB>
+__device__ __forceinline__ void raise(float m, float& top, float& sum,
+                                      f16v (&o)[NB]) {
+  if (!__any(m > top + kSlack)) return;
+  const float to = fmaxf(top, m);
+  const float by = top == -INFINITY ? 0.0f : exp2f(top - to);
+  top = to;
+  sum *= by;
 #pragma unroll
-    for (int k = 0; k < NB; ++k) {
+  for (int k = 0; k < NB; ++k) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[k][i] *= by;
-      __builtin_amdgcn_sched_barrier(0);
-    }
+    for (int i = 0; i < 16; ++i) o[k][i] *= by;
+    __builtin_amdgcn_sched_barrier(0);
   }
+}
+
+// Softmax weights of scores under that maximum, and their sum.
+__device__ __forceinline__ void soften(const f16v& s, float scale, float top,
+                                       float& sum, float (&x)[16]) {
   const float base = top == -INFINITY ? 0.0f : -top;
   float part[4] = {sum, 0.0f, 0.0f, 0.0f};
 #pragma unroll

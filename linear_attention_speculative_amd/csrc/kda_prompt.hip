@@ -181,7 +181,7 @@ struct Prompt {
   static constexpr int LK = kKeys * CH / 64, LP = kKeys * CHP / 64;  // loads
   static constexpr int MINE = (2 * LK + LP) / kWaves;
   static constexpr int TILE = kKeys * (2 * CH + CHP) * 16;
-  static constexpr int NBUF = BF16 ? 3 : 1;
+  static constexpr int NBUF = BF16 ? 3 : 1;    // (fp32: one fits)
   static constexpr int ROPE = kKeys * CH * 16, VALUE = ROPE + kKeys * CHP * 16;
   static_assert(LK % kWaves == 0 && LP % kWaves == 0, "loads");
 };
@@ -256,30 +256,54 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
   const char* value = p.value + int64_t(kbos) * p.s_v_tok + h * p.s_v_head;
   const char* rope = p.rope + int64_t(kbos) * p.s_rope;
   const uint32_t lds0 = lds_addr(smem);
-  auto stage = [&](int step, int buf) {
-    const int l = fresh_tid() & 63;
+  // This lane's places of the next step's loads.
+  const char* src[Z::MINE];
+  auto row_of = [&](int j, int l) {
+    const int i = j * kWaves + wave;
+    constexpr int CP = Z::CHP > 0 ? Z::CHP : 8;
+    return j * kWaves < Z::LK ? i * (64 / Z::CH) + l / Z::CH
+           : j * kWaves < Z::LK + Z::LP
+               ? (i - Z::LK) * (64 / CP) + l / CP
+               : (i - Z::LK - Z::LP) * (64 / Z::CH) + l / Z::CH;
+  };
+  auto stride_of = [&](int j) {
+    return j * kWaves < Z::LK            ? p.s_k_tok
+           : j * kWaves < Z::LK + Z::LP ? p.s_rope
+                                        : p.s_v_tok;
+  };
+  auto place_of = [&](int j, int l) {
+    constexpr int CP = Z::CHP > 0 ? Z::CHP : 8;
+    const bool is_rope = j * kWaves >= Z::LK && j * kWaves < Z::LK + Z::LP;
+    const int rw = row_of(j, l);
+    const int ch = is_rope ? (l % CP) ^ swizzle<CP>(rw)
+                           : (l % Z::CH) ^ swizzle<Z::CH>(rw);
+    return (j * kWaves < Z::LK ? key : is_rope ? rope : value) +
+           rw * stride_of(j) + ch * 16;
+  };
+  // (fp32 queries leave no registers for the places: formed for each step)
+  if constexpr (BF16)
 #pragma unroll
-    for (int j = 0; j < Z::MINE; ++j) {
-      const int i = uniform(j * kWaves + wave);
-      const char* src;
-      int rw;
-      if (j * kWaves < Z::LK) {
-        rw = i * (64 / Z::CH) + l / Z::CH;
-        src = key + int64_t(step * kKeys + rw) * p.s_k_tok +
-              ((l % Z::CH) ^ swizzle<Z::CH>(rw)) * 16;
-      } else if (j * kWaves < Z::LK + Z::LP) {
-        constexpr int CP = Z::CHP > 0 ? Z::CHP : 8;
-        rw = (i - Z::LK) * (64 / CP) + l / CP;
-        src = rope + int64_t(step * kKeys + rw) * p.s_rope +
-              ((l % CP) ^ swizzle<CP>(rw)) * 16;
-      } else {
-        rw = (i - Z::LK - Z::LP) * (64 / Z::CH) + l / Z::CH;
-        src = value + int64_t(step * kKeys + rw) * p.s_v_tok +
-              ((l % Z::CH) ^ swizzle<Z::CH>(rw)) * 16;
-      }
-      load_lds(step * kKeys + rw < n ? src : kZeros,
-               uniform(lds0 + buf * Z::TILE + i * 1024));
+    for (int j = 0; j < Z::MINE; ++j) src[j] = place_of(j, lane);
+  auto stage = [&](int step, int buf) {
+    const uint32_t to = uniform(lds0 + buf * Z::TILE + wave * 1024);
+    const int l = fresh_tid() & 63;
+    if constexpr (!BF16)
+#pragma unroll
+      for (int j = 0; j < Z::MINE; ++j)
+        src[j] = place_of(j, l) + int64_t(step) * kKeys * stride_of(j);
+    if ((step + 1) * kKeys <= n) {
+#pragma unroll
+      for (int j = 0; j < Z::MINE; ++j)
+        load_lds(src[j], to + j * kWaves * 1024);
+    } else {
+#pragma unroll
+      for (int j = 0; j < Z::MINE; ++j)
+        load_lds(step * kKeys + row_of(j, l) < n ? src[j] : kZeros,
+                 to + j * kWaves * 1024);
     }
+    if constexpr (BF16)
+#pragma unroll
+      for (int j = 0; j < Z::MINE; ++j) src[j] += kKeys * stride_of(j);
   };
 
   constexpr int kAhead = Z::NBUF > 1 ? Z::NBUF - 1 : 0;
@@ -299,50 +323,106 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
 #pragma unroll
     for (int k = 0; k < Z::KF; ++k) asm volatile("" : "+v"(q[k]));
   }
-  int buf = 0;
   RowReader<Z::CH, 1> heads(lds0, lane, 0);
   RowReader<(Z::CHP > 0 ? Z::CHP : 8), 1> ropes(lds0 + Z::ROPE, lane, 0);
-  ColumnReader<Z::CH> values(lds0 + Z::VALUE, 0, lane);
+  if constexpr (BF16) {
+    // Scores are one block of 32 keys ahead: their products run beside the
+    // exponentials of the block before, the values' beside the search for the
+    // maximum.  The next step's tile is there from the middle of a step on.
+    ColumnReader<Z::CH> values(lds0 + Z::VALUE, 0, lane);
+    auto next_scores = [&](int row) {
+      f16v x;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < Z::KF; ++i)
+        x = mma<true>(i < Z::CH / 2 ? heads(i, row)
+                                    : ropes(i - Z::CH / 2, row),
+                      q[i], x);
+      return x;
+    };
+    f16v ahead_scores;
+    float m = -INFINITY;
+    if (steps > 0) {
+      wait_tile<kAhead - 1>(steps, std::integral_constant<int, Z::MINE>());
+      lds_barrier();
+      ahead_scores = next_scores(0);
+      hide(ahead_scores, lim, half);
+      m = highest(ahead_scores);
+    }
+    // one block: keys `at` .., the next block's in rows [next, next + 32) of the
+    // tile that the readers are at
+    auto block = [&](int at, int row, int next) {
+      raise(m * p.scale, top, sum, o);
+      const f16v now = ahead_scores;
+      float x[16];
+      u4 pr[2];
+      __builtin_amdgcn_sched_barrier(0);
+      ahead_scores = next_scores(next);
+      soften(now, p.scale, top, sum, x);
+      pack_weights(x, pr);
+      // (here, not where they are used)
+      asm volatile("" : "+v"(pr[0]), "+v"(pr[1]), "+v"(sum));
+      // two reads ahead, then for each product a read, four additions or
+      // multiplications and two exponentials
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+      for (int i = 0; i < Z::KF; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(0x400, 2, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      hide(ahead_scores, lim - at - 32, half);
+      m = highest(ahead_scores);
+      weigh_bf16(values, row, pr, o);
+    };
+    int buf = 0;
 #pragma unroll 1
-  for (int s = 0; s < steps; ++s) {
-    if constexpr (kAhead == 0) {
+    for (int s = 0; s < steps; ++s) {
+      const int at = s * kKeys;
+      if (at < wave_lim) block(at, 0, 32);
+      const bool wrap = buf + 1 == Z::NBUF;
+      const int by = uniform(wrap ? -buf * Z::TILE : Z::TILE);
+      heads.move(by);
+      if (Z::CHP > 0) ropes.move(by);
+      if (s + 1 < steps) {
+        // (the tile after it goes where the last step's was, which every wave
+        // has read by now)
+        wait_vm<0>();
+        lds_barrier();
+        if (s + 2 < steps) stage(s + 2, (buf + 2) % Z::NBUF);
+      }
+      if (at + 32 < wave_lim) block(at + 32, 32, 0);
+      values.move(by);
+      buf = wrap ? 0 : buf + 1;
+    }
+  } else {
+#pragma unroll 1
+    for (int s = 0; s < steps; ++s) {
       lds_barrier();                       // the last step's tile is read
       stage(s, 0);
       wait_vm<0>();
       lds_barrier();
-    } else {
-      wait_tile<kAhead - 1>(steps - s,
-                            std::integral_constant<int, Z::MINE>());
-      lds_barrier();                       // and the last step's tile is read
-      if (s + kAhead < steps) stage(s + kAhead, buf ? buf - 1 : kAhead);
-    }
 #pragma unroll
-    for (int k = 0; k < kKeys; k += 32) {
-      const int at = s * kKeys + k;
-      if (at < wave_lim) {
-        f16v sc = score<BF16>(
-            [&](int i) {
-              return i < Z::CH / 2 ? heads(i, k) : ropes(i - Z::CH / 2, k);
-            },
-            q);
-        float x[16];
-        soften(sc, p.scale, lim - at, half, top, sum, o, x);
-        if constexpr (BF16) {
-          u4 pr[2];
-          pack_weights(x, pr);
-          weigh_bf16(values, k, pr, o);
-        } else {
-          weigh_f32<Z::CH>(lds0 + buf * Z::TILE + Z::VALUE + k * Z::CH * 16, 0,
+      for (int k = 0; k < kKeys; k += 32) {
+        const int at = s * kKeys + k;
+        if (at < wave_lim) {
+          f16v sc = score<false>(
+              [&](int i) {
+                return i < Z::CH / 2 ? heads(i, k) : ropes(i - Z::CH / 2, k);
+              },
+              q);
+          hide(sc, lim - at, half);
+          raise(highest(sc) * p.scale, top, sum, o);
+          float x[16];
+          soften(sc, p.scale, top, sum, x);
+          weigh_f32<Z::CH>(lds0 + Z::VALUE + k * Z::CH * 16, 0,
                            fresh_tid() & 63, x, o);
         }
       }
     }
-    const bool wrap = buf + 1 == Z::NBUF;
-    const int by = uniform(wrap ? -buf * Z::TILE : Z::TILE);
-    buf = wrap ? 0 : buf + 1;
-    heads.move(by);
-    if (Z::CHP > 0) ropes.move(by);
-    if (BF16) values.move(by);
   }
   sum = halves_sum(sum);
   if (tok >= len) return;
