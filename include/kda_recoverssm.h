@@ -596,8 +596,8 @@ typedef struct {
    table or of rows outside [0, num_request_rows) give +0.0.  Rows outside all
    requests are not touched. */
 typedef struct {
-  kda_tensor cache;              /* act [N, block_size, R + P]; R a multiple
-                                    of 64, P of 8 values (fp32: 32, 4) */
+  kda_tensor cache;              /* act [N, block_size, R + P]; R is 128, 256
+                                    or 512, P a multiple of 16 bytes */
   kda_tensor weight;             /* act [H, 2 D, R] */
   kda_tensor key;                /* act [S, H, D]; D is 64 or 128 */
   kda_tensor rope_key;           /* act [S, P], or empty: not gathered */

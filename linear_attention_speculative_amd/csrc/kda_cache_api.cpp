@@ -308,9 +308,11 @@ int plan_expand(const kda_latent_expand_args* a, kda::ExpandParams* p,
                 (long long)H, (long long)(2 * D),
                 (long long)a->cache.shape[2]);
   const int es = elem_size(w.dtype);
-  if (R < 1 || R * es % 128 != 0 || P * es % 16 != 0)
+  if (!latent_dims(R, 0) || P * es % 16 != 0)
     return fail(KDA_E_UNSUPPORTED,
-                "latents take multiples of 128 bytes, rope keys of 16");
+                "latent dims 128, 256 and 512 and rope dims of a multiple of "
+                "16 bytes are supported (got %lld and %lld)",
+                (long long)R, (long long)P);
   KDA_TRY(check_rows(w, "weight"));
   if (!apart(a->key) || !apart(a->value) ||
       (a->rope_key.ndim && !apart(a->rope_key)))

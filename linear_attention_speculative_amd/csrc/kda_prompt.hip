@@ -13,7 +13,7 @@
 // score(), soften() and weigh_bf16() in
 // kda_mma.hpp): a wave has 32 queries of one head, a workgroup
 // eight waves, which share 64 keys and values at a time in LDS.  The expansion
-// is a matrix product of gathered cache rows with W, 128 x 128 a workgroup.
+// is a matrix product of gathered cache rows with W.
 #include "kda_cache.hpp"
 #include "kda_mma.hpp"
 
@@ -55,13 +55,132 @@ __device__ __forceinline__ const char* key_entry(const ExpandParams& p,
   return c.cache + id * c.s_blk + int64_t(pos - e * c.block) * c.s_tok;
 }
 
-// 128 tokens x 128 columns, four waves of 64 x 64; the summed index 128 bytes
-// at a time.  The product is taken transposed (columns of W as rows), so that a
-// lane ends with four neighbouring values of one token.
-template <bool BF16>
+// The rope keys of key rows [s0, s0 + count).
+__device__ __forceinline__ void copy_ropes(const ExpandParams& p,
+                                           const char* const* entry, int s0,
+                                           int count, int offset) {
+  for (int i = threadIdx.x; i < count * p.rope_chunks; i += blockDim.x) {
+    const int t = i / p.rope_chunks, ch = i - t * p.rope_chunks;
+    const char* e = entry[t];
+    if (e)
+      *reinterpret_cast<u4*>(p.rope + (s0 + t) * p.s_rope + ch * 16) =
+          *reinterpret_cast<const u4*>(e == kZeros ? e
+                                                   : e + offset + ch * 16);
+  }
+}
+
+// bf16: a wave keeps the latents of 32 tokens in registers, as the right
+// operand, and the workgroup's 256 tokens go through tiles of 32 KB of W in LDS,
+// two of them under way.  The products are transposed (columns of W as rows):
+// a lane ends with four neighbouring values of one token.  Workgroups take
+// equal runs of (256 tokens, tile of W).  (Both operands through LDS, 128 x 128
+// a workgroup, took 129 us for 8192 tokens of 32 heads.)
+constexpr int kRowTokens = 256, kRowThreads = 512, kRowTile = 32768;
+template <int R>
+__global__ void __launch_bounds__(kRowThreads, 2)
+    kda_latent_expand_rows_kernel(ExpandParams p) {
+  constexpr int CH = R / 8;                    // chunks of a row
+  constexpr int NC = kRowTile / (R * 2);       // columns of a tile
+  constexpr int KF = R / 16, kLoads = kRowTile / 1024 / 8, kBufs = 3;
+  extern __shared__ __align__(16) char smem[];
+  __shared__ const char* entry[kRowTokens];
+  const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
+  const int wave = uniform(tid >> 6);
+  const int tiles = p.H * 2 * p.D / NC;
+  const int64_t total = int64_t((p.S + kRowTokens - 1) / kRowTokens) * tiles;
+  const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+  int64_t at = blockIdx.x * per;
+  const int64_t last = min(at + per, total);
+  const int part_shift = p.D == 64 ? 6 : 7;    // of a column's part
+  const uint32_t lds0 = lds_addr(smem);
+  auto stage = [&](int tile, int buf) {
+    const int l = fresh_tid() & 63;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int i = j * 8 + wave;
+      const int rw = i * 64 / CH + (CH < 64 ? l / CH : 0);
+      const int n = tile * NC + rw;
+      const int h = n >> (part_shift + 1), d = n & (2 * p.D - 1);
+      load_lds(p.w + h * p.s_w_head + d * p.s_w_row +
+                   (((i * 64 + l) % CH) ^ swizzle<CH>(rw)) * 16,
+               uniform(lds0 + buf * kRowTile + i * 1024));
+    }
+  };
+  while (at < last) {
+    // one group of tokens: tiles [c0, c1)
+    const int group = int(at / tiles), c0 = int(at - int64_t(group) * tiles);
+    const int c1 = int(min(int64_t(tiles), c0 + (last - at)));
+    const int s0 = group * kRowTokens;
+    __syncthreads();                           // the last group is done
+    if (tid < kRowTokens) entry[tid] = key_entry(p, s0 + tid);
+    __syncthreads();
+    stage(c0, 0);
+    if (c0 + 1 < c1) stage(c0 + 1, 1);
+    if (c0 == 0) copy_ropes(p, entry, s0, kRowTokens, R * 2);
+    const char* mine = entry[wave * 32 + (lane & 31)];
+    u4 tok[KF];
+    {
+      const char* src = (mine ? mine : kZeros) + half * 16;
+#pragma unroll
+      for (int k = 0; k < KF; ++k)
+        tok[k] = *reinterpret_cast<const u4*>(src + 32 * k);
+#pragma unroll
+      for (int k = 0; k < KF; ++k) asm volatile("" : "+v"(tok[k]));
+    }
+    const int64_t s = s0 + wave * 32 + (lane & 31);
+    char* key = p.key + s * p.s_k_tok;
+    char* value = p.value + s * p.s_v_tok;
+    RowReader<CH, 1> w(lds0, lane, 0);
+    u2 done[NC / 32][4];
+    auto write = [&](int c) {                  // the products of tile c
+#pragma unroll
+      for (int j = 0; j < NC / 32; ++j) {
+        const int n = c * NC + 32 * j;
+        const int h = n >> (part_shift + 1), d = n & (2 * p.D - 1);
+        char* dst = d < p.D ? key + h * p.s_k_head + d * 2
+                            : value + h * p.s_v_head + (d - p.D) * 2;
+        if (mine)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<u2*>(dst + acc_row(4 * e, half) * 2) =
+                done[j][e];
+      }
+    };
+    int buf = 0;
+#pragma unroll 1
+    for (int c = c0; c < c1; ++c) {
+      // (of what is younger than this tile's loads, the next one's alone may be
+      // under way: the stores before them are a tile old)
+      if (c + 1 < c1)
+        wait_vm<kLoads>();
+      else
+        wait_vm<0>();
+      lds_barrier();                           // and the last tile is read
+      if (c > c0) write(c - 1);
+      if (c + 2 < c1) stage(c + 2, buf >= 1 ? buf - 1 : 2);
+#pragma unroll
+      for (int j = 0; j < NC / 32; ++j) {
+        const f16v x = score<true>(
+            [&](int k) { return w(k, 32 * j); }, tok);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          done[j][e] = u2{pack_bf16(x[4 * e], x[4 * e + 1]),
+                          pack_bf16(x[4 * e + 2], x[4 * e + 3])};
+      }
+      const bool wrap = buf + 1 == kBufs;
+      w.move(uniform(wrap ? -buf * kRowTile : kRowTile));
+      buf = wrap ? 0 : buf + 1;
+    }
+    write(c1 - 1);
+    at += c1 - c0;
+  }
+}
+
+// fp32: 128 tokens x 128 columns, four waves of 64 x 64, both operands through
+// LDS, the summed index 128 bytes at a time, transposed as above.
 __global__ void __launch_bounds__(256, 2)
     kda_latent_expand_kernel(ExpandParams p) {
-  constexpr int ES = BF16 ? 2 : 4;
+  constexpr int ES = 4;
   constexpr int kPart = kExpand * 128;         // bytes of one operand's tile
   extern __shared__ __align__(16) char smem[];
   __shared__ const char* entry[kExpand];
@@ -71,17 +190,7 @@ __global__ void __launch_bounds__(256, 2)
   const int s0 = blockIdx.x * kExpand, n0 = blockIdx.y * kExpand;
   if (tid < kExpand) entry[tid] = key_entry(p, s0 + tid);
   __syncthreads();
-  // the rope keys, by the first column of workgroups
-  if (blockIdx.y == 0 && p.rope_chunks > 0) {
-    for (int i = tid; i < kExpand * p.rope_chunks; i += 256) {
-      const int t = i / p.rope_chunks, ch = i - t * p.rope_chunks;
-      const char* e = entry[t];
-      if (e)
-        *reinterpret_cast<u4*>(p.rope + (s0 + t) * p.s_rope + ch * 16) =
-            *reinterpret_cast<const u4*>(
-                e == kZeros ? e : e + int64_t(p.R) * ES + ch * 16);
-    }
-  }
+  if (blockIdx.y == 0) copy_ropes(p, entry, s0, kExpand, p.R * ES);
   // a wave's loads: 8 rows of 128 bytes each, four of tokens, four of W
   const char* src[8];
   const int ch = lane & 7;
@@ -136,8 +245,8 @@ __global__ void __launch_bounds__(256, 2)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = mma<BF16>(a[i], b[j],
-                                                          acc[i][j]);
+        for (int j = 0; j < 2; ++j) acc[i][j] = mma<false>(a[i], b[j],
+                                                           acc[i][j]);
     }
   }
 #pragma unroll
@@ -156,12 +265,7 @@ __global__ void __launch_bounds__(256, 2)
                             : p.value + s * p.s_v_tok + h * p.s_v_head +
                                   (d - p.D) * ES;
         const f16v& v = acc[i][j];
-        if constexpr (BF16)
-          *reinterpret_cast<u2*>(dst) = u2{pack_bf16(v[e], v[e + 1]),
-                                           pack_bf16(v[e + 2], v[e + 3])};
-        else
-          *reinterpret_cast<f4*>(dst) = f4{v[e], v[e + 1], v[e + 2],
-                                           v[e + 3]};
+        *reinterpret_cast<f4*>(dst) = f4{v[e], v[e + 1], v[e + 2], v[e + 3]};
       }
   }
 }
@@ -482,17 +586,31 @@ int launch_latent_prefill(const PromptParams& p, int D, int P, bool bf16,
               : launch_dims<false>(p, D, P, stream);
 }
 
+namespace {
+template <int R>
+int launch_rows(const ExpandParams& p, hipStream_t stream) {
+  const auto kernel = kda_latent_expand_rows_kernel<R>;
+  const hipError_t e = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(kernel),
+      hipFuncAttributeMaxDynamicSharedMemorySize, 3 * kRowTile);
+  if (e != hipSuccess) return int(e);
+  launch_kernel(kernel, dim3(256), dim3(kRowThreads), 3 * kRowTile, stream, p);
+  return int(hipGetLastError());
+}
+}  // namespace
+
 int launch_latent_expand(const ExpandParams& p, bool bf16,
                          hipStream_t stream) {
-  constexpr int lds = 4 * kExpand * 128;
-  const dim3 grid((p.S + kExpand - 1) / kExpand,
-                  (p.H * 2 * p.D + kExpand - 1) / kExpand);
-  if (bf16)
-    launch_kernel(kda_latent_expand_kernel<true>, grid, dim3(256), lds,
-                  stream, p);
-  else
-    launch_kernel(kda_latent_expand_kernel<false>, grid, dim3(256), lds,
-                  stream, p);
+  if (bf16) {
+    if (p.R == 512) return launch_rows<512>(p, stream);
+    if (p.R == 256) return launch_rows<256>(p, stream);
+    if (p.R == 128) return launch_rows<128>(p, stream);
+    return int(hipErrorInvalidValue);
+  }
+  launch_kernel(kda_latent_expand_kernel,
+                dim3((p.S + kExpand - 1) / kExpand,
+                     (p.H * 2 * p.D + kExpand - 1) / kExpand),
+                dim3(256), 4 * kExpand * 128, stream, p);
   return int(hipGetLastError());
 }
 

@@ -179,9 +179,14 @@ EXPAND = [
     dict(lens=[130, 0, 5, 260], H=3, D=128, R=512, P=64, block=16,
          act="bf16"),
     dict(lens=[127, 1, 300], H=5, D=64, R=256, P=64, block=7, act="bf16"),
-    dict(lens=[50, 200], H=2, D=128, R=64, P=8, block=1, act="bf16"),
+    dict(lens=[50, 200], H=2, D=128, R=128, P=8, block=1, act="bf16"),
     dict(lens=[128, 20], H=3, D=64, R=512, P=64, block=100, act="f32"),
-    dict(lens=[40], H=2, D=128, R=32, P=64, block=16, act="f32", rope=False),
+    dict(lens=[40], H=2, D=128, R=128, P=64, block=16, act="f32",
+         rope=False),
+    # groups of tokens and tiles of W shared by workgroups
+    dict(lens=[700, 1, 900], H=9, D=64, R=128, P=64, block=16, act="bf16"),
+    dict(lens=[520], H=33, D=128, R=256, P=0, block=32, act="bf16"),
+    dict(lens=[300, 230], H=2, D=64, R=512, P=64, block=16, act="bf16"),
 ]
 
 
