@@ -82,6 +82,15 @@ __device__ __forceinline__ void load_lds(uint64_t base, uint32_t off,
       : "memory");
 }
 
+// Two registers' worth of four bf16 values of one row of a result's columns,
+// those of registers 8 k + {0..3} and 8 k + {4..7}, as eight neighbouring values:
+// from row 16 k on in lanes 0 .. 31, from row 16 k + 8 on in the others.
+__device__ __forceinline__ u4 neighbours(u2 a, u2 b) {
+  const auto x = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
+  const auto y = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
+  return u4{x[0], y[0], x[1], y[1]};
+}
+
 // Wait until at most N of this wave's global memory operations are under way
 // (they end in the order in which they began).
 template <int N>

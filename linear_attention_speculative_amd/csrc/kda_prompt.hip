@@ -82,6 +82,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   constexpr int CH = R / 8;                    // chunks of a row
   constexpr int NC = kRowTile / (R * 2);       // columns of a tile
   constexpr int KF = R / 16, kLoads = kRowTile / 1024 / 8, kBufs = 3;
+  constexpr int kLine = NC >= 64 ? NC / 32 : 2;    // blocks of 32 columns
   extern __shared__ __align__(16) char smem[];
   __shared__ const char* entry[kRowTokens];
   const int tid = threadIdx.x, lane = tid & 63, half = lane >> 5;
@@ -131,20 +132,26 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     char* key = p.key + s * p.s_k_tok;
     char* value = p.value + s * p.s_v_tok;
     RowReader<CH, 1> w(lds0, lane, 0);
-    u2 done[NC / 32][4];
-    auto write = [&](int c) {                  // the products of tile c
+    // products of tiles that are not written yet: whole lines of 128 bytes are
+    u4 done[kLine][2];
+    auto write = [&](int n0, int count) {      // 32 columns each, from n0 on
+      if (!mine) return;
 #pragma unroll
-      for (int j = 0; j < NC / 32; ++j) {
-        const int n = c * NC + 32 * j;
+      for (int j = 0; j < kLine; ++j) {
+        if (j >= count) break;
+        const int n = n0 + 32 * j;
         const int h = n >> (part_shift + 1), d = n & (2 * p.D - 1);
         char* dst = d < p.D ? key + h * p.s_k_head + d * 2
                             : value + h * p.s_v_head + (d - p.D) * 2;
-        if (mine)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<u2*>(dst + acc_row(4 * e, half) * 2) =
-                done[j][e];
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<u4*>(dst + (16 * e + 8 * half) * 2) = done[j][e];
       }
+    };
+    auto write_second = [&]() {                // a line's second half alone
+      done[0][0] = done[1][0];
+      done[0][1] = done[1][1];
+      write(c0 * NC, 1);
     };
     int buf = 0;
 #pragma unroll 1
@@ -156,22 +163,51 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       else
         wait_vm<0>();
       lds_barrier();                           // and the last tile is read
-      if (c > c0) write(c - 1);
+      if (c > c0) {
+        if constexpr (NC >= 64)
+          write((c - 1) * NC, kLine);
+        else if (c % 2 == 0)
+          c - 1 > c0 ? write((c - 2) * NC, 2) : write_second();
+      }
       if (c + 2 < c1) stage(c + 2, buf >= 1 ? buf - 1 : 2);
 #pragma unroll
       for (int j = 0; j < NC / 32; ++j) {
         const f16v x = score<true>(
             [&](int k) { return w(k, 32 * j); }, tok);
+        u4 v[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          done[j][e] = u2{pack_bf16(x[4 * e], x[4 * e + 1]),
-                          pack_bf16(x[4 * e + 2], x[4 * e + 3])};
+        for (int e = 0; e < 2; ++e)
+          v[e] = neighbours(u2{pack_bf16(x[8 * e], x[8 * e + 1]),
+                               pack_bf16(x[8 * e + 2], x[8 * e + 3])},
+                            u2{pack_bf16(x[8 * e + 4], x[8 * e + 5]),
+                               pack_bf16(x[8 * e + 6], x[8 * e + 7])});
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (NC >= 64) {
+            done[j][e] = v[e];
+          } else {
+            if (c % 2 == 0)
+              done[0][e] = v[e];
+            else
+              done[1][e] = v[e];
+          }
+        }
       }
       const bool wrap = buf + 1 == kBufs;
       w.move(uniform(wrap ? -buf * kRowTile : kRowTile));
       buf = wrap ? 0 : buf + 1;
     }
-    write(c1 - 1);
+    if constexpr (NC >= 64) {
+      write((c1 - 1) * NC, kLine);
+    } else {
+      // the last tile, with the one before it where they share a line
+      if (c1 % 2 == 1)
+        write((c1 - 1) * NC, 1);
+      else if (c1 - 1 > c0)
+        write((c1 - 2) * NC, 2);
+      else
+        write_second();
+    }
     at += c1 - c0;
   }
 }
