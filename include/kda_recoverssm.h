@@ -556,12 +556,10 @@ typedef struct {
    Position j lies in block block_table[row][j / block_size]; positions of a
    null block (<= null_block_id or >= N) or past the table's width are not
    seen.  A query that sees nothing, or whose row is outside
-   [0, num_request_rows), gets +0.0 outputs and lse -inf.  Places of the cache
-   that no query of the tile sees are never read into a product; an entry that
-   is not finite spoils the outputs of all tokens of its request's window (of
-   its tiles of rows), also of those before it.  Arithmetic is fp32; with bf16
-   the weights p are rounded to bf16 before they weigh the latents.  Token rows
-   outside all requests are not touched. */
+   [0, num_request_rows), gets +0.0 outputs and lse -inf.  An entry that is not
+   finite reaches the queries that see it, no others.  Arithmetic is fp32; with
+   bf16 the weights p are rounded to bf16 before they weigh the latents.  Token
+   rows outside all requests are not touched. */
 typedef struct {
   kda_tensor q;                  /* act [T, H, R + P] */
   kda_tensor cache;              /* act [N, block_size, R + P]; R is 128, 256
@@ -621,10 +619,9 @@ typedef struct {
      s_j = softmax_scale * (q_th[0 .. D) . key[j, h] + q_th[D ..) . rope[j]),
      out_th = sum_j softmax(s)_j value[j, h],  lse_th = ln sum_j e^(s_j).
    A query without keys (n_k < n_q) gets +0.0 outputs and lse -inf.  A key or
-   value that is not finite spoils outputs of its head and request, also from
-   up to 255 tokens before it on.  Arithmetic is fp32; with bf16 the weights
-   are rounded to bf16 before they weigh the values.  Token rows outside all
-   requests are not touched. */
+   value that is not finite reaches the queries that see it, no others.
+   Arithmetic is fp32; with bf16 the weights are rounded to bf16 before they
+   weigh the values.  Token rows outside all requests are not touched. */
 typedef struct {
   kda_tensor q;                  /* act [T, H, D + P]; D 64 or 128, P 0 or 64 */
   kda_tensor key;                /* act [S, H, D] */

@@ -30,7 +30,8 @@ struct LatentWriteParams {
   int64_t s_blk, s_tok;      // bytes
   const int64_t* slots;
   int64_t total_slots;       // N * block
-  int32_t T, block, first_slot;  // (slots below first_slot are null)
+  int64_t first_slot;        // (slots below it are null)
+  int32_t T, block;
   int32_t lat_chunks, chunks;    // 16-byte chunks of the latent, of a row
 };
 int launch_latent_write(const LatentWriteParams& p, hipStream_t stream);

@@ -385,6 +385,9 @@ __global__ void __launch_bounds__(256 * RG, RG)
       }
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum += y[e];
+      // (places behind token n hold zeros, those of null blocks too)
+      const int left = lim - s * kTile;
+      const bool all_see = __all(left >= min(n - s * kTile, kTile));
       const char* all = exch + rg * Z::DS * Z::BOX;
       if constexpr (BF16) {
         u4 pr[2];
@@ -395,7 +398,8 @@ __global__ void __launch_bounds__(256 * RG, RG)
                                                    Z::BOX)[l];
           pr[t] = u4{a[0], a[1], b[0], b[1]};
         }
-        weigh_bf16(ColumnReader<Z::CH>(tile, ds * Z::NB, l), 0, pr, o);
+        weigh_bf16(ColumnReader<Z::CH>(tile, ds * Z::NB, l), 0, pr, all_see,
+                   left, o);
       } else {
         float z[16];
 #pragma unroll
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(256 * RG, RG)
 #pragma unroll
           for (int e = 0; e < 4; ++e) z[4 * d + e] = a[e];
         }
-        weigh_f32<Z::CH>(tile, ds * Z::NB, l, z, o);
+        weigh_f32<Z::CH>(tile, ds * Z::NB, z, all_see, left, o);
       }
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) live[k] = live[k + 1];

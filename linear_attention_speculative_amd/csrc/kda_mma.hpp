@@ -300,10 +300,54 @@ __device__ __forceinline__ void pack_weights(const float (&x)[16],
                pack_bf16(x[8 * t + 6], x[8 * t + 7])};
 }
 
-// O^T += V^T P^T: NB blocks of 32 of the values' rows [row, row + 32).
+// Bits of the tokens acc_row(i, half) of a block that a query sees, the first
+// `left` of it.
+__device__ __forceinline__ uint32_t seen_bits(int left, int half) {
+  uint32_t seen = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    seen |= uint32_t(acc_row(i, half) < left) << i;
+  return seen;
+}
+
+// Values that are not finite, at tokens that some of a wave's queries see and
+// others do not: 0 times them is NaN, so they are taken out of the operands, and
+// the largest finite value in their place times 2^100 where a query sees them
+// makes its sum +inf, then -inf (NaN: both, which leaves NaN).
+__device__ __forceinline__ void spoil_bf16(u4 (&v)[2], uint32_t seen, f16v& o) {
+  uint32_t bad = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) bad |= (v[t][e] & 0x7f807f80u) + 0x00800080u;
+  if (!__any(bad & 0x80008000u)) return;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    u4 up, down, is;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      up[e] = down[e] = 0;
+#pragma unroll
+      for (int h = 0; h < 32; h += 16) {
+        const uint32_t w = (v[t][e] >> h) & 0xffffu;
+        if (w == 0x7f80u || (w & 0x7fffu) > 0x7f80u) up[e] |= 0x7f7fu << h;
+        if (w == 0xff80u || (w & 0x7fffu) > 0x7f80u) down[e] |= 0xff7fu << h;
+        if ((w & 0x7f80u) == 0x7f80u) v[t][e] &= 0xffff0000u >> h;
+      }
+      const uint32_t s = seen >> (8 * t + 2 * e);
+      is[e] = ((s & 1) | (s & 2) << 15) * 0x7180u;        // 2^100
+    }
+    o = mma<true>(up, is, o);
+    o = mma<true>(down, is, o);
+  }
+}
+
+// O^T += V^T P^T: NB blocks of 32 of the values' rows [row, row + 32).  Of these
+// tokens each query of the wave sees all (`all`), or the first `left`.
 template <int NB, class Column>
 __device__ __forceinline__ void weigh_bf16(const Column& value_at, int row,
-                                           const u4 (&pr)[2], f16v (&o)[NB]) {
+                                           const u4 (&pr)[2], bool all,
+                                           int left, f16v (&o)[NB]) {
   u4 v[2][2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) v[0][t] = value_at(row + 16 * t, 0);
@@ -312,24 +356,46 @@ __device__ __forceinline__ void weigh_bf16(const Column& value_at, int row,
 #pragma unroll
     for (int t = 0; t < 2; ++t)
       if (k + 1 < NB) v[(k + 1) & 1][t] = value_at(row + 16 * t, k + 1);
+    // (here it takes 1 % of the prompts' time; a loop of its own for such
+    // steps, or two blocks at a time, take more registers than there are)
+    if (!all)
+      spoil_bf16(v[k & 1], seen_bits(left, (fresh_tid() >> 5) & 1), o[k]);
 #pragma unroll
     for (int t = 0; t < 2; ++t) o[k] = mma<true>(v[k & 1][t], pr[t], o[k]);
     __builtin_amdgcn_sched_barrier(0);
   }
 }
 
+// The same for the fp32 values of tokens acc_row(i, lane / 32), by bf16 products
+// (an fp32 one adds to its sum before it overflows: +inf would stay).
+__device__ __forceinline__ void spoil_f32(float& v, int i, int left, f16v& o) {
+  if (!__any(!(fabsf(v) < INFINITY))) return;
+  const bool see = acc_row(i, (fresh_tid() >> 5) & 1) < left;
+  const bool up = v == INFINITY || v != v, down = v == -INFINITY || v != v;
+  if (up || down) v = 0.0f;
+  auto add = [&](uint32_t a) {
+    o = __builtin_amdgcn_mfma_f32_32x32x8bf16_1k(
+        __builtin_bit_cast(s4, u2{a, 0}),
+        __builtin_bit_cast(s4, u2{see ? 0x7180u : 0u, 0}), o, 0, 0, 0);
+  };
+  add(up ? 0x7f7fu : 0u);
+  add(down ? 0xff7fu : 0u);
+}
+
 // fp32: x[i] is the weight of token acc_row(i, lane / 32) of the tile's.
 template <int CHV, int NB>
-__device__ __forceinline__ void weigh_f32(uint32_t values, int blk, int lane,
-                                          const float (&x)[16],
-                                          f16v (&o)[NB]) {
+__device__ __forceinline__ void weigh_f32(uint32_t values, int blk,
+                                          const float (&x)[16], bool all,
+                                          int left, f16v (&o)[NB]) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
+    const int lane = fresh_tid() & 63;
 #pragma unroll
-    for (int k = 0; k < NB; ++k)
-      o[k] = __builtin_amdgcn_mfma_f32_32x32x2f32(
-          column_value<CHV>(values, acc_row(i, lane >> 5), blk + k, lane),
-          x[i], o[k], 0, 0, 0);
+    for (int k = 0; k < NB; ++k) {
+      float v = column_value<CHV>(values, acc_row(i, lane >> 5), blk + k, lane);
+      if (!all) spoil_f32(v, i, left, o[k]);
+      o[k] = __builtin_amdgcn_mfma_f32_32x32x2f32(v, x[i], o[k], 0, 0, 0);
+    }
     if (i & 1) __builtin_amdgcn_sched_barrier(0);
   }
 }

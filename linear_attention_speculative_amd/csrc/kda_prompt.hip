@@ -47,9 +47,9 @@ __device__ __forceinline__ const char* key_entry(const ExpandParams& p,
   if (s >= p.S || s < c.qsl[0] || s >= c.qsl[c.B]) return nullptr;
   const int b = request_of(c.qsl, c.B, s);
   const int row = c.req_idx ? c.req_idx[b] : b;
-  const int pos = s - c.qsl[b];
+  const int pos = s - max(c.qsl[b], 0);
   const int e = pos / c.block;
-  if (row < 0 || row >= c.rows || e >= c.width || pos < 0) return kZeros;
+  if (row < 0 || row >= c.rows || e >= c.width) return kZeros;
   const int id = c.table[row * c.s_tab_row + e * c.s_tab_col];
   if (id <= c.null_id || id >= c.N) return kZeros;
   return c.cache + id * c.s_blk + int64_t(pos - e * c.block) * c.s_tok;
@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
       __builtin_amdgcn_sched_barrier(0);
       hide(ahead_scores, lim - at - 32, half);
       m = highest(ahead_scores);
-      weigh_bf16(values, row, pr, o);
+      weigh_bf16(values, row, pr, __all(lim - at >= 32), lim - at, o);
     };
     int buf = 0;
 #pragma unroll 1
@@ -558,8 +558,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
           raise(highest(sc) * p.scale, top, sum, o);
           float x[16];
           soften(sc, p.scale, top, sum, x);
-          weigh_f32<Z::CH>(lds0 + Z::VALUE + k * Z::CH * 16, 0,
-                           fresh_tid() & 63, x, o);
+          weigh_f32<Z::CH>(lds0 + Z::VALUE + k * Z::CH * 16, 0, x,
+                           __all(lim - at >= 32), lim - at, o);
         }
       }
     }

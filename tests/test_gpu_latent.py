@@ -169,6 +169,48 @@ def test_not_finite_entries_spoil_their_request_alone():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act,R", [("bf16", 512), ("bf16", 128), ("f32", 512),
+                                   ("f32", 256)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_not_finite_entries_of_later_tokens(act, R, value):
+    """A window's tokens do not see the entries of those behind them."""
+    lens, computed = [4, 3, 40], [50, 30, 90]
+    kw = make(lens, computed, H=5, R=R, P=64, block=16, act=act, seed=2)
+    ref = expect(kw)
+    req, table = ints(kw["request_indices"]), ints(kw["block_table"])
+    first = [2, 1, 11]                      # tokens of the windows
+    for b in range(3):
+        pos = computed[b] + first[b]
+        at = kw["cache"][int(table[req[b], pos // 16]), pos % 16]
+        at[3 + 40 * b] = value
+        at[R - 1] = -value
+    run(kw)
+    torch.cuda.synchronize()
+    b_out, b_lse = bounds(ref, act, R + 64)
+    out, lse = f64(kw["out"]), f64(kw["lse"])
+    start = ints(kw["query_start_loc"])
+    for b in range(3):
+        own = slice(start[b], start[b] + first[b])
+        hold(out[own], ref["out"][own], b_out[own], "out")
+        hold(lse[own], ref["lse"][own], b_lse[own], "lse")
+        for t in range(start[b] + first[b], start[b + 1]):
+            # (scores of +-inf, half of them NaN with a latent's second one)
+            assert not np.isfinite(out[t]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [-0.05, 0.0, -3.0])
+def test_scales_not_above_zero(act, scale):
+    kw = make([2, 5], [70, 40], H=9, R=128, P=64, block=16, act=act, seed=5)
+    kw["softmax_scale"] = scale
+    ref = expect(kw)
+    run(kw)
+    torch.cuda.synchronize()
+    check(kw, ref, act)
+
+
+@pytest.mark.gpu
 def test_graph_replays_and_other_stream():
     kw = make([2, 1, 4], [100, 900, 31], H=16, R=512, P=64, block=16,
               act="bf16", seed=6)
@@ -260,6 +302,16 @@ def test_latent_write(act, R, P):
     torch.cuda.synchronize()
     assert np.array_equal(f64(cache)[..., :R + P], ref)
     assert torch.equal(cache[..., R + P:], wide[..., R + P:])
+
+
+@pytest.mark.gpu
+def test_latent_write_null_blocks_past_32_bits_of_slots():
+    cache = torch.zeros((3, 16, 128), device=DEV)
+    kda.latent_write(latent=torch.ones((40, 128), device=DEV), cache=cache,
+                     slot_mapping=torch.arange(40, device=DEV),
+                     null_block_id=(1 << 28) - 1)   # slots below 2^32
+    torch.cuda.synchronize()
+    assert (cache == 0).all()
 
 
 @pytest.mark.gpu

@@ -122,6 +122,41 @@ def test_values_behind_the_last_key_are_not_read_into_sums():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("act,D", [("bf16", 128), ("bf16", 64), ("f32", 128),
+                                   ("f32", 64)])
+def test_not_finite_keys_and_values_of_later_tokens(act, D):
+    """They reach the queries that see them: of a value its own dimension."""
+    n, ahead = 150, 23
+    kw = prompt([n, 40], [n + ahead, 40], H=2, D=D, P=64, act=act, seed=8)
+    ref = expect(kw)
+    want = ref["out"]
+    inf, nan = float("inf"), float("nan")
+    for tok, dim, v in ((20, 3, inf), (41, 33, -inf), (97, 60, nan),
+                        (45, 5, inf), (120, 5, -inf), (149, 9, -inf)):
+        kw["value"][ahead + tok, 1, dim] = v
+        with np.errstate(invalid="ignore"):
+            want[tok:n, 1, dim] += v
+    kw["key"][ahead + 140, 0, 7] = nan
+    want[140:n, 0] = nan
+    ref["lse"][140:n, 0] = nan
+    kda.latent_prefill(**kw)
+    torch.cuda.synchronize()
+    check(kw, ref, act)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [-0.05, 0.0, -2.0])
+def test_scales_not_above_zero(act, scale):
+    kw = prompt([70, 33], [100, 33], H=2, D=64, P=64, act=act, seed=6)
+    kw["softmax_scale"] = scale
+    ref = expect(kw)
+    kda.latent_prefill(**kw)
+    torch.cuda.synchronize()
+    check(kw, ref, act)
+
+
+@pytest.mark.gpu
 def test_prefill_graph_replays_over_other_lengths():
     kw = prompt([200, 100], [250, 100], H=4, D=128, P=64, act="bf16", seed=5)
     kda.latent_prefill(**kw)
@@ -215,6 +250,19 @@ def test_expand_null_blocks_and_rows_outside():
     kda.latent_expand(**kw)
     torch.cuda.synchronize()
     expand_check(kw, ref, "bf16")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_expand_offsets_in_front_of_the_first_row(act):
+    """They are clamped: the first row is the request's position 0."""
+    kw = expansion([40, 30], H=2, D=64, R=128, P=64, block=16, act=act,
+                   seed=9)
+    ref = expand_expect(kw)
+    kw["key_start_loc"][0] = -5
+    kda.latent_expand(**kw)
+    torch.cuda.synchronize()
+    expand_check(kw, ref, act)
 
 
 def test_prefill_refusals():
