@@ -580,7 +580,7 @@ typedef struct {
   int32_t num_request_rows;
   int32_t block_table_width;
   int32_t null_block_id;
-  float softmax_scale;
+  float softmax_scale;           /* finite */
   int32_t pad_;
 } kda_latent_args;
 
@@ -632,7 +632,7 @@ typedef struct {
   const int32_t* query_start_loc;  /* [batch + 1], not decreasing, both */
   const int32_t* key_start_loc;
   int32_t batch;
-  float softmax_scale;
+  float softmax_scale;           /* finite */
 } kda_latent_prefill_args;
 
 /* Arguments of kda_adjust_logits: logits changed in place, before kda_sample.
@@ -650,8 +650,9 @@ typedef struct {
    seen) draft_tokens[s + 1 .. m]; draft_tokens[s] is the history's last token.
    r <= 0, NaN parameters and NULL arrays leave their change out; a request
    without a row of token_ids (NULL, or outside [0, num_request_rows)) has an
-   empty history.  Tokens outside [0, V) are ignored.  Arithmetic is fp32, rounded once.  Entries that nothing changes keep their bits; rows that
-   belong to no request are not touched.
+   empty history.  Tokens outside [0, V) are ignored.  Arithmetic is fp32,
+   rounded once.  Entries that nothing changes keep their bits; rows that belong
+   to no request are not touched.
    A mask row holds a bit for each token, bit v % 32 of word v / 32, 1 =
    allowed; row m's is mask_rows[m] (NULL: m), outside [0, num_masks): none. */
 typedef struct {
@@ -979,12 +980,14 @@ int kda_reset_counter(int32_t* counter, int32_t n, void* stream);
    the gap the event's own marker adds before the next dispatch).  Arms the
    calling thread: the next `launches` kernels that library calls on this
    thread launch (a prefill takes two, the step tables two or, without
-   tokens, one, sampling three to eight, the latent attention two) are dispatched with
-   hipExtLaunchKernel, `start_event` (a hipEvent_t, may be NULL) recording
-   the start of the first of them and `stop_event` (may be NULL) the end of
-   the last.  The counter-clearing kernels (kda_reset_counter, the first
-   use of the no-allocation entry point's array on a device) are not
-   counted.  launches = 0 disarms.  If `pending` is not NULL it receives
+   tokens, one, sampling three to eight, the latent attention two, the
+   changes of logits one or, with masks and other changes, two or more, free
+   lists and compactions one to five, the other operators on caches and blocks
+   one) are dispatched with hipExtLaunchKernel, `start_event` (a hipEvent_t,
+   may be NULL) recording the start of the first of them and `stop_event` (may
+   be NULL) the end of the last.  The counter-clearing kernels
+   (kda_reset_counter, the first use of the no-allocation entry point's array
+   on a device) are not counted.  launches = 0 disarms.  If `pending` is not NULL it receives
    the number of launches the previous arming was still waiting for (0 when
    every armed launch happened, so its stop event was recorded).  The
    events stay the caller's; do not arm the thread while it captures a

@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <cmath>
 #include <initializer_list>
 
 #include "kda_cache.hpp"
@@ -65,10 +66,13 @@ int check_cache(const kda_tensor& t) {
 // The kernels take scales above 0: queries are negated for one below, and a
 // scale of 0 is one that leaves no difference between scores.
 template <class Params>
-void set_scale(float scale, Params* p) {
+int set_scale(float scale, Params* p) {
   p->negate = scale < 0.0f;
   p->scale = (scale < 0.0f ? -scale : scale) * kLog2e;
+  if (!std::isfinite(p->scale))
+    return fail(KDA_E_ARG, "softmax_scale must be finite");
   if (p->scale == 0.0f) p->scale = 0x1p-126f;
+  return KDA_OK;
 }
 
 bool latent_dims(int64_t R, int64_t P) {
@@ -254,7 +258,7 @@ int plan_latent(const kda_latent_args* a, LatentPlan* plan) {
   p.s_lse_tok = a->lse.stride[0];
   p.s_lse_head = a->lse.stride[1];
   p.work = static_cast<char*>(a->workspace);
-  set_scale(a->softmax_scale, &p);
+  KDA_TRY(set_scale(a->softmax_scale, &p));
   p.T = int32_t(T);
   p.H = int32_t(H);
   p.group = kda::latent_groups(T, a->batch, H);
@@ -412,7 +416,7 @@ int plan_prompt(const kda_latent_prefill_args* a, PromptPlan* plan) {
   p.s_lse_head = a->lse.stride[1];
   p.qsl = a->query_start_loc;
   p.ksl = a->key_start_loc;
-  set_scale(a->softmax_scale, &p);
+  KDA_TRY(set_scale(a->softmax_scale, &p));
   p.T = int32_t(T);
   p.S = int32_t(S);
   p.H = int32_t(H);

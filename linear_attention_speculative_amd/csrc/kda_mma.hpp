@@ -83,8 +83,8 @@ __device__ __forceinline__ void load_lds(uint64_t base, uint32_t off,
 }
 
 // Two registers' worth of four bf16 values of one row of a result's columns,
-// those of registers 8 k + {0..3} and 8 k + {4..7}, as eight neighbouring values:
-// from row 16 k on in lanes 0 .. 31, from row 16 k + 8 on in the others.
+// those of registers 8 k + {0..3} and 8 k + {4..7}, as eight neighbouring
+// values: from row 16 k on in lanes 0 .. 31, from row 16 k + 8 on in the others.
 __device__ __forceinline__ u4 neighbours(u2 a, u2 b) {
   const auto x = __builtin_amdgcn_permlane32_swap(a[0], b[0], false, false);
   const auto y = __builtin_amdgcn_permlane32_swap(a[1], b[1], false, false);
@@ -145,8 +145,8 @@ struct RowReader {
 
 // The left operand of a product with the transpose of rows [t, t + 16) of a
 // bf16 tile, t a multiple of 16: result row m = l % 32 is element 32 blk + m of
-// the tile's rows; lane half h sums over rows t + 4 h + {0..3} and t + 8 + 4 h +
-// {0..3}, the order in which a product's result has its own rows.
+// the tile's rows; lane half h sums over rows t + 4 h + {0..3} and t + 8 + 4 h
+// + {0..3}, the order in which a product's result has its own rows.
 template <int CH>
 struct ColumnReader {
   static constexpr int N = CH >= 16 ? 4 : 2;   // blocks of a swizzle's period
@@ -311,9 +311,9 @@ __device__ __forceinline__ uint32_t seen_bits(int left, int half) {
 }
 
 // Values that are not finite, at tokens that some of a wave's queries see and
-// others do not: 0 times them is NaN, so they are taken out of the operands, and
-// the largest finite value in their place times 2^100 where a query sees them
-// makes its sum +inf, then -inf (NaN: both, which leaves NaN).
+// others do not: 0 times them is NaN, so they are taken out of the operands,
+// and the largest finite value in their place times 2^100 where a query sees
+// them makes its sum +inf, then -inf (NaN: both, which leaves NaN).
 __device__ __forceinline__ void spoil_bf16(u4 (&v)[2], uint32_t seen, f16v& o) {
   uint32_t bad = 0;
 #pragma unroll
@@ -342,8 +342,8 @@ __device__ __forceinline__ void spoil_bf16(u4 (&v)[2], uint32_t seen, f16v& o) {
   }
 }
 
-// O^T += V^T P^T: NB blocks of 32 of the values' rows [row, row + 32).  Of these
-// tokens each query of the wave sees all (`all`), or the first `left`.
+// O^T += V^T P^T: NB blocks of 32 of the values' rows [row, row + 32).  Of
+// these tokens each query of the wave sees all (`all`), or the first `left`.
 template <int NB, class Column>
 __device__ __forceinline__ void weigh_bf16(const Column& value_at, int row,
                                            const u4 (&pr)[2], bool all,
@@ -366,8 +366,8 @@ __device__ __forceinline__ void weigh_bf16(const Column& value_at, int row,
   }
 }
 
-// The same for the fp32 values of tokens acc_row(i, lane / 32), by bf16 products
-// (an fp32 one adds to its sum before it overflows: +inf would stay).
+// The same for the fp32 values of tokens acc_row(i, lane / 32), by bf16
+// products (an fp32 one adds to its sum before it overflows: +inf would stay).
 __device__ __forceinline__ void spoil_f32(float& v, int i, int left, f16v& o) {
   if (!__any(!(fabsf(v) < INFINITY))) return;
   const bool see = acc_row(i, (fresh_tid() >> 5) & 1) < left;

@@ -348,6 +348,8 @@ def test_refusals():
     assert chk(lse=ok["lse"].double()) == _abi.KDA_E_DTYPE
     assert chk(lse=ok["lse"][:1].expand(3, 4)) == _abi.KDA_E_LAYOUT
     assert chk(workspace=ok["workspace"][:-1]) == _abi.KDA_E_CAPACITY
+    for scale in (float("inf"), float("nan"), -3.4e38):
+        assert chk(softmax_scale=scale) == _abi.KDA_E_ARG
     assert chk(null_block_id=-1) == _abi.KDA_E_ARG
     with pytest.raises(ValueError, match="row per request"):
         chk(request_indices=None, block_table=ok["block_table"][:1])

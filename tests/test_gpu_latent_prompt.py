@@ -280,6 +280,8 @@ def test_prefill_refusals():
     assert chk(out=ok["out"][:1].expand(7, -1, -1)) == _abi.KDA_E_LAYOUT
     assert chk(key=ok["key"][..., :32], value=ok["value"][..., :32],
                out=ok["out"][..., :32]) == _abi.KDA_E_UNSUPPORTED
+    for scale in (float("inf"), float("nan"), -3.4e38):
+        assert chk(softmax_scale=scale) == _abi.KDA_E_ARG
     wide = torch.zeros((9, 2, 66), dtype=torch.bfloat16)
     assert chk(key=wide[..., :64]) == _abi.KDA_E_UNALIGNED
     with pytest.raises(ValueError, match="entries"):
