@@ -54,6 +54,7 @@ struct LatentParams {
 // Row groups for these sizes, and workspace bytes.
 constexpr int kLatentWorkers = 256;
 int latent_groups(int64_t T, int64_t B, int64_t H);
+int latent_workers(int64_t T, int64_t B, int64_t H, int64_t tokens, int group);
 int64_t latent_work_bytes(int group, int R);
 int launch_latent(const LatentParams& p, int R, int P, bool bf16,
                   hipStream_t stream);

@@ -262,7 +262,9 @@ int plan_latent(const kda_latent_args* a, LatentPlan* plan) {
   p.T = int32_t(T);
   p.H = int32_t(H);
   p.group = kda::latent_groups(T, a->batch, H);
-  p.workers = kda::kLatentWorkers;
+  p.workers = kda::latent_workers(
+      T, a->batch, H, int64_t(a->block_table_width) * a->cache.shape[1],
+      p.group);
   plan->R = int(R);
   plan->P = int(P);
   plan->bf16 = bf16;

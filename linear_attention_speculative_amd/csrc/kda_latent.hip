@@ -534,6 +534,9 @@ __global__ void __launch_bounds__(64 * kJoinWaves)
       for (int j = 0; j < 4; ++j) v[k][j] = parts[at * (8 * R) + j * 64];
     }
   };
+  // (these, too)
+  const int bos = min(max(p.c.qsl[piece.b], 0), p.T);
+  const int rows = (min(max(p.c.qsl[piece.b + 1], bos), p.T) - bos) * p.H;
   fetch(start);
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = f4{0, 0, 0, 0};
@@ -557,11 +560,9 @@ __global__ void __launch_bounds__(64 * kJoinWaves)
         for (int d = 0; d < 4; ++d) acc[j][d] += by * v[k][j][d];
     }
   }
-  const Request r = load_request(p.c, p.T, piece.b);
   const int row = piece.row_tile * 32 * RG + rg * 32 + (lane & 31);
   const int tok = row / p.H, head = row - tok * p.H;
-  char* dst = p.out + int64_t(r.bos + tok) * p.s_out_tok +
-              head * p.s_out_head;
+  char* dst = p.out + int64_t(bos + tok) * p.s_out_tok + head * p.s_out_head;
   // four dimensions of each half from `at` on
   auto write = [&](const f4& o, int at, float by) {
     if constexpr (BF16)
@@ -580,7 +581,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves)
 #pragma unroll
     for (int k = 0; k < kJoinWaves; ++k) sum += sums[k][lane];
   }
-  if (row >= r.q * p.H) return;
+  if (row >= rows) return;
   const float by = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
   if (few) {
 #pragma unroll
@@ -594,7 +595,7 @@ __global__ void __launch_bounds__(64 * kJoinWaves)
     write(o, 32 * u + acc_row(4 * wave, half), by);
   }
   if (p.lse && half == 0 && u == 0 && (few || wave == 0))
-    p.lse[int64_t(r.bos + tok) * p.s_lse_tok + head * p.s_lse_head] =
+    p.lse[int64_t(bos + tok) * p.s_lse_tok + head * p.s_lse_head] =
         sum == 0.0f ? -INFINITY : (top + log2f(sum)) / kLog2e;
 }
 
@@ -658,6 +659,16 @@ int latent_groups(int64_t T, int64_t B, int64_t H) {
   const int64_t rows = B > 0 ? (T + B - 1) / B * H : H;
   if (rows <= 32) return 1;
   return 2;
+}
+
+int latent_workers(int64_t T, int64_t B, int64_t H, int64_t tokens, int group) {
+  // no more than the steps that tables of `tokens` places allow
+  const int64_t tiles = T * H / (32 * group) + B;
+  const int64_t steps = (tokens + kTile - 1) / kTile + kStart;
+  return tiles > kLatentWorkers || steps > kLatentWorkers ||
+                 tiles * steps > kLatentWorkers
+             ? kLatentWorkers
+             : int(tiles * steps);
 }
 
 int64_t latent_work_bytes(int group, int R) {
