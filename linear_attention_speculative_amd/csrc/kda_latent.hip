@@ -28,8 +28,17 @@
 // workspace, and a second kernel joins them.
 //
 // Rounding: S, the statistics and O are fp32 throughout; probabilities are
-// rounded to bf16 for the second product with bf16 caches (2^-9 of a weight
-// each, as the values themselves are).
+// rounded to bf16 for the second product with bf16 caches (half a step, 2^-8 of
+// a weight at most, as the values themselves are).
+//
+// What bounds it (R = 512, P = 64, 32 heads, bf16): for 256 single tokens
+// behind 3000 others on average, the cache's bytes: 199 us, 884 MB at 4.4 TB/s,
+// of which the loop's steps run at 5.0 (1.9 us each), and some 6 us a piece go
+// to its queries, its first tile and its outputs.  For 48 windows of up to 4
+// drafts behind 1500 tokens, two row tiles a request: 46 us, a chain of scores,
+// exchange, weights and sums of 2.3 us a step with one workgroup of eight waves
+// on a CU; the matrix cores are busy for a seventh of it.  The join takes 11 us
+// of the first, 13 us of the second (37 MB of pieces), 5 us of one request.
 #include "kda_cache.hpp"
 #include "kda_mma.hpp"
 
@@ -585,7 +594,8 @@ __global__ void __launch_bounds__(64 * kJoinWaves)
   const float by = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
   if (few) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) write(acc[j], 32 * u + acc_row(4 * j, half), by);
+    for (int j = 0; j < 4; ++j)
+      write(acc[j], 32 * u + acc_row(4 * j, half), by);
   } else {
     f4 o = box[0][wave][lane];
 #pragma unroll

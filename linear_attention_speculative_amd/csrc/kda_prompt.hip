@@ -10,10 +10,18 @@
 // with W.
 //
 // The attention takes both products transposed, with a query a lane (see
-// score(), soften() and weigh_bf16() in
-// kda_mma.hpp): a wave has 32 queries of one head, a workgroup
-// eight waves, which share 64 keys and values at a time in LDS.  The expansion
-// is a matrix product of gathered cache rows with W.
+// score(), soften() and weigh_bf16() in kda_mma.hpp): a wave has 32 queries of
+// one head, a workgroup eight waves, which share 64 keys and values at a time
+// in LDS.  The expansion is a matrix product of gathered cache rows with W.
+//
+// What bounds them (R = 512, P = 64, 32 heads of 128, bf16): the prompt
+// attention is bound by its products, whose operands come from LDS for each of
+// them and whose exponentials run beside them: one prompt of 8192 takes 675 us
+// in a run of calls (690 GFLOP at 1.0 PFLOP/s, the matrix cores busy for half
+// of the cycles at the clock that they leave).  Scores a block of keys ahead of
+// their exponentials took the whole call from 834 us to 798.  The expansion of its 8192 tokens takes 95 us, 69
+// GFLOP and 134 MB of keys and values written: the writes of a token's heads,
+// 128 bytes apart in time, bound it (110 us in pieces of 8 bytes a lane).
 #include "kda_cache.hpp"
 #include "kda_mma.hpp"
 
@@ -70,11 +78,11 @@ __device__ __forceinline__ void copy_ropes(const ExpandParams& p,
 }
 
 // bf16: a wave keeps the latents of 32 tokens in registers, as the right
-// operand, and the workgroup's 256 tokens go through tiles of 32 KB of W in LDS,
-// two of them under way.  The products are transposed (columns of W as rows):
-// a lane ends with four neighbouring values of one token.  Workgroups take
-// equal runs of (256 tokens, tile of W).  (Both operands through LDS, 128 x 128
-// a workgroup, took 129 us for 8192 tokens of 32 heads.)
+// operand, and the workgroup's 256 tokens go through tiles of 32 KB of W in
+// LDS, two of them under way.  The products are transposed (columns of W as
+// rows): a lane ends with four neighbouring values of one token.  Workgroups
+// take equal runs of (256 tokens, tile of W).  (Both operands through LDS, 128
+// x 128 a workgroup, took 129 us for 8192 tokens of 32 heads.)
 constexpr int kRowTokens = 256, kRowThreads = 512, kRowTile = 32768;
 template <int R>
 __global__ void __launch_bounds__(kRowThreads, 2)
@@ -490,8 +498,8 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
       hide(ahead_scores, lim, half);
       m = highest(ahead_scores);
     }
-    // one block: keys `at` .., the next block's in rows [next, next + 32) of the
-    // tile that the readers are at
+    // one block: keys `at` .., the next block's in rows [next, next + 32) of
+    // the tile that the readers are at
     auto block = [&](int at, int row, int next) {
       raise(m * p.scale, top, sum, o);
       const f16v now = ahead_scores;
