@@ -11,9 +11,9 @@
 // What bounds them: copies move 584 MB (64 forks, 32 heads of two layers and a
 // latent cache) in 91 us, at 6.4 TB/s, part of the reads from the last-level
 // cache.  The bookkeeping of 8192 blocks and 512 rows of 40 entries takes 15 us
-// (free lists) and 21 us (compaction) in one workgroup, a chain of its passes
-// over LDS; 16 or 32 rows of the table under way in place of 8, or loads without
-// branches, change nothing.
+// (free lists, half of it the pass over the table in one workgroup) and 10 + 5
+// us (compaction, the table in a launch of its own).  32 rows of the table under
+// way in place of 8 take longer: so does their code to arrive.
 #include "kda_cache.hpp"
 #include "kda_mma.hpp"
 
@@ -314,11 +314,15 @@ __global__ void __launch_bounds__(kThreads)
 // ---- the same in one workgroup ---------------------------------------------------
 
 // Pools of up to kSmallBlocks blocks and tables of up to kSmallEntries entries
-// take one launch each in place of five: all counts and lists fit LDS.
+// take one launch or two in place of five: all counts and lists fit LDS.
 constexpr int kSmallBlocks = 16384;
 constexpr int kSmallRows = 4096;
 constexpr int kSmallEntries = 65536;
 constexpr int kMany = 1024;        // threads
+// Compaction rewrites tables of up to this many entries in that launch, larger
+// ones in a second one with a workgroup a row (512 rows of 40: 10 and 5 us, 20
+// in one; 5 rows of 6: 5 us in one, a launch more in two).
+constexpr int kInside = 1024;
 
 // Exclusive prefix sum over the workgroup's threads, and the total.
 __device__ __forceinline__ int scan_many(int v, int* total, int* red) {
@@ -404,6 +408,7 @@ __global__ void __launch_bounds__(kMany)
   extern __shared__ __align__(16) int32_t refs[];   // [N], then lists
   __shared__ int red[kMany / 64];
   const int tid = threadIdx.x, N = int(p.N);
+  const bool inside = p.rows * p.width <= kInside;
   uint16_t* src = reinterpret_cast<uint16_t*>(refs + N);   // [N / 2 + 1]
   uint16_t* dst = src + N / 2 + 1;
   uint16_t* map = dst + N / 2 + 1;                         // [N]
@@ -438,6 +443,7 @@ __global__ void __launch_bounds__(kMany)
     p.pairs[2 * i + 1] = b;
     if (in) {
       map[a] = uint16_t(b);
+      if (!inside) p.moved[a] = int(i);
       refs[b] = refs[a];
       refs[a] = 0;
     }
@@ -445,7 +451,7 @@ __global__ void __launch_bounds__(kMany)
   if (tid == 0) p.num_pairs[0] = moves;
   __syncthreads();
   for (int i = tid; i < N; i += kMany) p.new_refs[i] = refs[i];
-  if (p.width > 0)
+  if (inside && p.width > 0)
     each_entry(
         p.rows, p.width,
         [&](int r, int j) { return p.table[r * p.s_tab_row + j * p.s_tab_col]; },
@@ -521,6 +527,9 @@ int launch_compact_blocks(const CompactBlocksParams& p, hipStream_t stream) {
     if (e != hipSuccess) return int(e);
     launch_kernel(kda_compact_small_kernel, dim3(1), dim3(kMany),
                   uint32_t(p.N * 2 + 1 + p.rows) * 4, stream, p);
+    if (p.rows * p.width > kInside)
+      launch_kernel(kda_compact_table_kernel, dim3(p.rows), dim3(kThreads), 0,
+                    stream, p);
     return int(hipGetLastError());
   }
   launch_kernel(kda_live_count_kernel, chunks_of(p.N), dim3(kThreads), 0,
