@@ -725,7 +725,8 @@ typedef struct {
   int64_t block_table_strides[2];      /* row, column (elements) */
   const int32_t* free_blocks;    /* [num_free] */
   int32_t* copy_pairs;           /* [num_forks][2] output */
-  int32_t* num_allocated;        /* [1] output: blocks the forks asked for */
+  int32_t* num_allocated;        /* [1] output: blocks the forks asked for, 0
+                                    without forks (which may leave it NULL) */
   int32_t num_forks;
   int32_t num_request_rows;
   int32_t block_table_width;

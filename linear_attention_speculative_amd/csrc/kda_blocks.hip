@@ -90,6 +90,10 @@ __device__ __forceinline__ bool fork_rows(const ForkParams& p, int f, int* a,
 __global__ void __launch_bounds__(kThreads) kda_fork_kernel(ForkParams p) {
   __shared__ int red[kThreads / 64];
   const int f = blockIdx.x, tid = threadIdx.x;
+  if (p.F == 0) {                            // (a count of none is written)
+    if (tid == 0) p.allocated[0] = 0;
+    return;
+  }
   int a, b, n = 0;
   for (int i = tid; i < f; i += kThreads) n += fork_rows(p, i, &a, &b);
 #pragma unroll
@@ -477,7 +481,8 @@ int64_t copy_pieces(int64_t bytes) {
 }
 
 int launch_fork_blocks(const ForkParams& p, hipStream_t stream) {
-  launch_kernel(kda_fork_kernel, dim3(p.F), dim3(kThreads), 0, stream, p);
+  launch_kernel(kda_fork_kernel, dim3(p.F > 0 ? p.F : 1), dim3(kThreads), 0,
+                stream, p);
   return int(hipGetLastError());
 }
 

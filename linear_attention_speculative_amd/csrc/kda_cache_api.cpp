@@ -799,7 +799,7 @@ int kda_fork_blocks(const kda_fork_args* args, void* stream) {
   g_err.clear();
   kda::ForkParams p;
   KDA_TRY(plan_fork(args, &p));
-  if (p.F == 0) return KDA_OK;
+  if (p.F == 0 && !p.allocated) return KDA_OK;
   return device_status(
       kda::launch_fork_blocks(p, static_cast<hipStream_t>(stream)),
       "kda_fork_blocks launch");
