@@ -712,10 +712,11 @@ typedef struct {
      copy_pairs[f] = (the parent's block k, the new one) for kda_copy_blocks,
      num_computed_tokens[b] = c, num_blocks[b] = k + 1 (at most the width).
    A pair is (null, null) where the parent does not hold block k or there is
-   no new block.  A fork with a row outside [0, num_request_rows) or with a =
-   b does nothing and takes no block.  Entries of the child's row behind block
-   k stay.  A child row must not be another fork's row; a parent may have many
-   forks. */
+   no new block.  Where k is past the table (a request at its full length)
+   the fork shares the table's blocks and takes none.  A fork with a row
+   outside [0, num_request_rows) or with a = b does nothing and takes none.
+   Entries of the child's row behind block k stay.  A child row must not be
+   another fork's row; a parent may have many forks. */
 typedef struct {
   const int32_t* parent_rows;    /* [num_forks] */
   const int32_t* child_rows;     /* [num_forks] */

@@ -85,8 +85,15 @@ __device__ __forceinline__ bool fork_rows(const ForkParams& p, int f, int* a,
          p.width > 0;
 }
 
-// One workgroup a fork; a fork's rank among those that do something gives its
-// free block.
+// Whether fork f needs a block of its own: the next token's lies in the table.
+// (No fork's child is a parent, so the lengths read here stay.)
+__device__ __forceinline__ bool fork_takes(const ForkParams& p, int f) {
+  int a, b;
+  return fork_rows(p, f, &a, &b) && max(p.computed[a], 0) / p.block < p.width;
+}
+
+// One workgroup a fork; a fork's rank among those that need a block gives the
+// free one that it takes.
 __global__ void __launch_bounds__(kThreads) kda_fork_kernel(ForkParams p) {
   __shared__ int red[kThreads / 64];
   const int f = blockIdx.x, tid = threadIdx.x;
@@ -95,7 +102,7 @@ __global__ void __launch_bounds__(kThreads) kda_fork_kernel(ForkParams p) {
     return;
   }
   int a, b, n = 0;
-  for (int i = tid; i < f; i += kThreads) n += fork_rows(p, i, &a, &b);
+  for (int i = tid; i < f; i += kThreads) n += fork_takes(p, i);
 #pragma unroll
   for (int s = 32; s > 0; s >>= 1) n += __shfl_xor(n, s);
   if ((tid & 63) == 0) red[tid >> 6] = n;
@@ -103,8 +110,8 @@ __global__ void __launch_bounds__(kThreads) kda_fork_kernel(ForkParams p) {
   int rank = 0;
 #pragma unroll
   for (int k = 0; k < kThreads / 64; ++k) rank += red[k];
+  if (f == p.F - 1 && tid == 0) p.allocated[0] = rank + fork_takes(p, f);
   const bool ok = fork_rows(p, f, &a, &b);
-  if (f == p.F - 1 && tid == 0) p.allocated[0] = rank + ok;
   if (!ok) {
     if (tid < 2) p.pairs[2 * f + tid] = p.null_id;
     return;

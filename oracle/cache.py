@@ -231,10 +231,10 @@ def fork_blocks(*, parent_rows, child_rows, num_computed_tokens, num_blocks,
             continue
         c = max(int(num_computed_tokens[a]), 0)
         k = c // block_size
-        new = int(free[asked]) if asked < len(free) else null_block_id
-        asked += 1
         table[b, :k] = block_table[a, :k]
         if k < width:
+            new = int(free[asked]) if asked < len(free) else null_block_id
+            asked += 1
             table[b, k] = new
             if k < num_blocks[a] and new > null_block_id and \
                     block_table[a, k] > null_block_id:

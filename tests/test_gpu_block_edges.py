@@ -1,9 +1,15 @@
-"""Edges of the block operators: calls without forks."""
+"""Edges of the block operators: calls without forks, forks at the end of the
+table."""
+import numpy as np
 import pytest
 import torch
 
 import linear_attention_speculative_amd as kda
-from tests.test_gpu_blocks import fork_case
+import oracle
+from tests.test_gpu_blocks import fork_case, i32, same
+
+DEV = "cuda"
+I32 = torch.int32
 
 
 @pytest.mark.gpu
@@ -31,3 +37,54 @@ def test_no_forks_take_no_blocks():
         graph.replay()
         torch.cuda.synchronize()
         assert int(kw["num_allocated"]) == 0
+
+
+def full_rows(F, device=DEV):
+    """Forks of which every third parent holds its table's whole width, with
+    a free block for each of the others."""
+    width, block, rows = 4, 8, 2 * F
+    rng = np.random.RandomState(F)
+    comp = np.zeros(rows, np.int64)
+    comp[:F] = rng.randint(0, width * block, size=F)
+    comp[:F:3] = width * block + rng.randint(0, 3, size=len(comp[:F:3]))
+    table = 1 + np.arange(rows * width).reshape(rows, width)
+    fits = comp[:F] // block < width
+    host = dict(parent_rows=np.arange(F), child_rows=F + np.arange(F),
+                num_computed_tokens=comp,
+                num_blocks=np.minimum(comp // block + 1, width),
+                block_table=table, free_blocks=900 + np.arange(fits.sum()),
+                block_size=block, null_block_id=0)
+    return host, fits
+
+
+@pytest.mark.parametrize("F", [1, 7, 300])
+def test_oracle_forks_past_the_table_take_no_block(F):
+    host, fits = full_rows(F)
+    ref = oracle.fork_blocks(**host)
+    assert ref["num_allocated"] == fits.sum()
+    got, k = 900, host["num_computed_tokens"][:F] // 8
+    for f in range(F):
+        child = ref["block_table"][F + f]
+        assert ref["num_blocks"][F + f] == min(k[f] + 1, 4)
+        assert np.array_equal(child[:k[f]], host["block_table"][f, :k[f]])
+        if fits[f]:
+            assert child[k[f]] == got
+            assert list(ref["copy_pairs"][f]) == [
+                host["block_table"][f, k[f]], got]
+            got += 1
+        else:
+            assert list(ref["copy_pairs"][f]) == [0, 0]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("F", [1, 7, 300])
+def test_forks_past_the_table_take_no_block(F):
+    host, fits = full_rows(F)
+    kw = {k: i32(v) if isinstance(v, np.ndarray) else v
+          for k, v in host.items()}
+    kw.update(copy_pairs=torch.full((F, 2), -9, dtype=I32, device=DEV),
+              num_allocated=torch.full((1,), -9, dtype=I32, device=DEV))
+    kda.fork_blocks(**kw)
+    torch.cuda.synchronize()
+    assert int(kw["num_allocated"]) == fits.sum()
+    same(kw, oracle.fork_blocks(**host))
