@@ -558,8 +558,8 @@ typedef struct {
    seen.  A query that sees nothing, or whose row is outside
    [0, num_request_rows), gets +0.0 outputs and lse -inf.  An entry that is not
    finite reaches the queries that see it, no others.  Arithmetic is fp32; with
-   bf16 the weights p are rounded to bf16 before they weigh the latents.  Token
-   rows outside all requests are not touched. */
+   bf16 a weight p weighs the latents as two bf16 values, off by 2^-15 of it at
+   most.  Token rows outside all requests are not touched. */
 typedef struct {
   kda_tensor q;                  /* act [T, H, R + P] */
   kda_tensor cache;              /* act [N, block_size, R + P]; R is 128, 256
@@ -620,8 +620,9 @@ typedef struct {
      out_th = sum_j softmax(s)_j value[j, h],  lse_th = ln sum_j e^(s_j).
    A query without keys (n_k < n_q) gets +0.0 outputs and lse -inf.  A key or
    value that is not finite reaches the queries that see it, no others.
-   Arithmetic is fp32; with bf16 the weights are rounded to bf16 before they
-   weigh the values.  Token rows outside all requests are not touched. */
+   Arithmetic is fp32; with bf16 a weight weighs the values as two bf16 values,
+   off by 2^-15 of it at most.  Token rows outside all requests are not
+   touched. */
 typedef struct {
   kda_tensor q;                  /* act [T, H, D + P]; D 64 or 128, P 0 or 64 */
   kda_tensor key;                /* act [S, H, D] */

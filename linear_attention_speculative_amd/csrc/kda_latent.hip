@@ -27,9 +27,9 @@
 // or ends inside a request leaves its sums (O, maximum, sum, all fp32) in the
 // workspace, and a second kernel joins them.
 //
-// Rounding: S, the statistics and O are fp32 throughout; probabilities are
-// rounded to bf16 for the second product with bf16 caches (half a step, 2^-8 of
-// a weight at most, as the values themselves are).
+// Rounding: S, the statistics and O are fp32 throughout; with bf16 caches the
+// probabilities go into the second product as two bf16 values, which leaves
+// 2^-15 of a weight at most (split_bf16() in kda_mma.hpp).
 //
 // What bounds it (R = 512, P = 64, 32 heads, bf16): for 256 single tokens
 // behind 3000 others on average, the cache's bytes: 199 us, 884 MB at 4.4 TB/s,
@@ -360,11 +360,12 @@ __global__ void __launch_bounds__(256 * RG, RG)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = __builtin_amdgcn_exp2f(x[e] - base);
         char* to = exch + wave * Z::BOX;
-        if constexpr (BF16)
-          reinterpret_cast<u2*>(to)[l] = u2{pack_bf16(y[0], y[1]),
-                                            pack_bf16(y[2], y[3])};
-        else
+        if constexpr (BF16) {
+          const u2 a = split_bf16(y[0], y[1]), b = split_bf16(y[2], y[3]);
+          reinterpret_cast<u4*>(to)[l] = u4{a[0], b[0], a[1], b[1]};
+        } else {
           reinterpret_cast<f4*>(to)[l] = f4{y[0], y[1], y[2], y[3]};
+        }
       };
       float y[4];
       weights(y);
@@ -399,16 +400,17 @@ __global__ void __launch_bounds__(256 * RG, RG)
       const bool all_see = __all(left >= min(n - s * kTile, kTile));
       const char* all = exch + rg * Z::DS * Z::BOX;
       if constexpr (BF16) {
-        u4 pr[2];
+        u4 pr[2], lo[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const u2 a = reinterpret_cast<const u2*>(all + 2 * t * Z::BOX)[l];
-          const u2 b = reinterpret_cast<const u2*>(all + (2 * t + 1) *
+          const u4 a = reinterpret_cast<const u4*>(all + 2 * t * Z::BOX)[l];
+          const u4 b = reinterpret_cast<const u4*>(all + (2 * t + 1) *
                                                    Z::BOX)[l];
           pr[t] = u4{a[0], a[1], b[0], b[1]};
+          lo[t] = u4{a[2], a[3], b[2], b[3]};
         }
-        weigh_bf16(ColumnReader<Z::CH>(tile, ds * Z::NB, l), 0, pr, all_see,
-                   left, o);
+        weigh_bf16(ColumnReader<Z::CH>(tile, ds * Z::NB, l), 0, pr, lo,
+                   all_see, left, o);
       } else {
         float z[16];
 #pragma unroll

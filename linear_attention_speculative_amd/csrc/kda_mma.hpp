@@ -288,16 +288,32 @@ __device__ __forceinline__ void soften(const f16v& s, float scale, float top,
   sum = (part[0] + part[1]) + (part[2] + part[3]);
 }
 
-// The weights of a result's registers as operands: pr[t] holds tokens 16 t + 4
-// h + {0..3} and 16 t + 8 + 4 h + {0..3}, h = lane / 32.
-__device__ __forceinline__ void pack_weights(const float (&x)[16],
-                                             u4 (&pr)[2]) {
+// Two weights as bf16 values in halves: the leading 8 bits of each, and what
+// they leave, rounded.  Together they are off by 2^-15 of a weight at most; one
+// bf16 value would be by 2^-8, as much as the output's own rounding.  The second
+// is kept above 0 (2^-23 of the weight more): values that are not finite meet
+// both, and 0 times infinity would be NaN.
+__device__ __forceinline__ u2 split_bf16(float a, float b) {
+  const uint32_t i = __float_as_uint(a), j = __float_as_uint(b);
+  constexpr float up = 1.0f + 0x1p-23f;
+  return u2{__builtin_amdgcn_perm(j, i, 0x07060302u),
+            pack_bf16(
+                __builtin_fmaf(a, up, -__uint_as_float(i & 0xffff0000u)),
+                __builtin_fmaf(b, up, -__uint_as_float(j & 0xffff0000u)))};
+}
+
+// The weights of a result's registers as operands, in halves: pr[t] and lo[t]
+// hold tokens 16 t + 4 h + {0..3} and 16 t + 8 + 4 h + {0..3}, h = lane / 32.
+__device__ __forceinline__ void pack_weights(const float (&x)[16], u4 (&pr)[2],
+                                             u4 (&lo)[2]) {
 #pragma unroll
   for (int t = 0; t < 2; ++t)
-    pr[t] = u4{pack_bf16(x[8 * t], x[8 * t + 1]),
-               pack_bf16(x[8 * t + 2], x[8 * t + 3]),
-               pack_bf16(x[8 * t + 4], x[8 * t + 5]),
-               pack_bf16(x[8 * t + 6], x[8 * t + 7])};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const u2 w = split_bf16(x[8 * t + 2 * e], x[8 * t + 2 * e + 1]);
+      pr[t][e] = w[0];
+      lo[t][e] = w[1];
+    }
 }
 
 // Bits of the tokens acc_row(i, half) of a block that a query sees, the first
@@ -346,7 +362,8 @@ __device__ __forceinline__ void spoil_bf16(u4 (&v)[2], uint32_t seen, f16v& o) {
 // these tokens each query of the wave sees all (`all`), or the first `left`.
 template <int NB, class Column>
 __device__ __forceinline__ void weigh_bf16(const Column& value_at, int row,
-                                           const u4 (&pr)[2], bool all,
+                                           const u4 (&pr)[2],
+                                           const u4 (&lo)[2], bool all,
                                            int left, f16v (&o)[NB]) {
   u4 v[2][2];
 #pragma unroll
@@ -362,6 +379,8 @@ __device__ __forceinline__ void weigh_bf16(const Column& value_at, int row,
       spoil_bf16(v[k & 1], seen_bits(left, (fresh_tid() >> 5) & 1), o[k]);
 #pragma unroll
     for (int t = 0; t < 2; ++t) o[k] = mma<true>(v[k & 1][t], pr[t], o[k]);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) o[k] = mma<true>(v[k & 1][t], lo[t], o[k]);
     __builtin_amdgcn_sched_barrier(0);
   }
 }

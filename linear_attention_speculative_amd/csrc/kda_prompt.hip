@@ -504,13 +504,14 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
       raise(m * p.scale, top, sum, o);
       const f16v now = ahead_scores;
       float x[16];
-      u4 pr[2];
+      u4 pr[2], lo[2];
       __builtin_amdgcn_sched_barrier(0);
       ahead_scores = next_scores(next);
       soften(now, p.scale, top, sum, x);
-      pack_weights(x, pr);
+      pack_weights(x, pr, lo);
       // (here, not where they are used)
-      asm volatile("" : "+v"(pr[0]), "+v"(pr[1]), "+v"(sum));
+      asm volatile("" : "+v"(pr[0]), "+v"(pr[1]), "+v"(lo[0]), "+v"(lo[1]),
+                   "+v"(sum));
       // two reads ahead, then for each product a read, four additions or
       // multiplications and two exponentials
       __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(64 * kWaves, 2)
       __builtin_amdgcn_sched_barrier(0);
       hide(ahead_scores, lim - at - 32, half);
       m = highest(ahead_scores);
-      weigh_bf16(values, row, pr, __all(lim - at >= 32), lim - at, o);
+      weigh_bf16(values, row, pr, lo, __all(lim - at >= 32), lim - at, o);
     };
     int buf = 0;
 #pragma unroll 1
