@@ -17,6 +17,7 @@ namespace {
 
 constexpr int64_t kI32Max = 0x7fffffff;
 constexpr int64_t kMaxThreads = 0xffffffff;   // work items of a launch
+constexpr int64_t kMaxGroups = kMaxThreads / 256;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 // Strides of a tensor of 16-byte aligned rows (its last dimension).
@@ -576,6 +577,8 @@ int plan_fork(const kda_fork_args* a, kda::ForkParams* p) {
     return fail(KDA_E_ARG, "block_size must be at least 1");
   if (a->null_block_id < 0)
     return fail(KDA_E_ARG, "null_block_id must not be negative");
+  if (a->num_forks > kMaxGroups)
+    return fail(KDA_E_CAPACITY, "too many forks");
   if (a->num_forks > 0) {
     KDA_TRY(check_pointers({a->parent_rows, a->child_rows, a->copy_pairs,
                             a->num_allocated}, {}));
@@ -617,6 +620,8 @@ int check_blocks(const Args* a) {
     return fail(KDA_E_ARG, "null_block_id must not be negative");
   if (a->total_blocks > kMaxBlocks)
     return fail(KDA_E_CAPACITY, "at most 2^28 blocks");
+  if (a->num_request_rows > kMaxGroups)
+    return fail(KDA_E_CAPACITY, "too many request rows");
   if (a->num_request_rows > 0)
     KDA_TRY(check_pointers({a->num_blocks}, {a->num_blocks}));
   KDA_TRY(check_table(a->block_table, a->block_table_strides,

@@ -1,12 +1,13 @@
 """Edges of the block operators: calls without forks, forks at the end of the
-table."""
+table; and sizes past what one launch takes (CPU)."""
 import numpy as np
 import pytest
 import torch
 
 import linear_attention_speculative_amd as kda
 import oracle
-from tests.test_gpu_blocks import fork_case, i32, same
+from linear_attention_speculative_amd import _abi
+from tests.test_gpu_blocks import fork_case, held_case, i32, same
 
 DEV = "cuda"
 I32 = torch.int32
@@ -88,3 +89,33 @@ def test_forks_past_the_table_take_no_block(F):
     torch.cuda.synchronize()
     assert int(kw["num_allocated"]) == fits.sum()
     same(kw, oracle.fork_blocks(**host))
+
+
+def test_more_rows_than_a_launch_are_refused():
+    """A workgroup of 256 a row, a fork, at most 2^32 work items."""
+    n = 1 << 24
+    ok, _ = fork_case(3, 8, 4, 4, device="cpu")
+    lib = _abi.load()
+    a = kda.fork_args(**ok)
+    a.num_forks = n - 1
+    assert lib.kda_check_fork_blocks(a) == _abi.KDA_OK
+    a.num_forks = n
+    assert lib.kda_check_fork_blocks(a) == _abi.KDA_E_CAPACITY
+
+    ok, _ = held_case(6, 4, 30, device="cpu")
+    a = kda.free_args(**ok)
+    a.num_request_rows = n - 1
+    assert lib.kda_check_free_blocks(a) == _abi.KDA_OK
+    a.num_request_rows = n
+    assert lib.kda_check_free_blocks(a) == _abi.KDA_E_CAPACITY
+
+    z = lambda *s: torch.zeros(s, dtype=I32)  # noqa: E731
+    a = kda.compact_blocks_args(
+        ref_counts=ok["ref_counts"], block_table=ok["block_table"],
+        num_blocks=ok["num_blocks"], new_block_table=z(6, 4),
+        new_ref_counts=z(30), copy_pairs=z(15, 2), num_pairs=z(1),
+        workspace=ok["workspace"])
+    a.num_request_rows = n - 1
+    assert lib.kda_check_compact_blocks(a) == _abi.KDA_OK
+    a.num_request_rows = n
+    assert lib.kda_check_compact_blocks(a) == _abi.KDA_E_CAPACITY
