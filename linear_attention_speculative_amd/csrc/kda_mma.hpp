@@ -61,7 +61,11 @@ __device__ __forceinline__ float halves_sum(float v) {
 
 // One wave's load of 64 x 16 bytes into LDS, in lane order, from an address
 // of each lane, or from a uniform one plus an offset of each lane.  The wait
-// is by hand (wait_vm): the compiler keeps no count of these loads.
+// is by hand (wait_vm): the compiler keeps no count of these loads.  (m0 is a
+// reserved register, which the compiler warns of; named, its own settings of m0
+// are not merged across.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds(const char* addr, uint32_t lds) {
   asm volatile(
       "s_mov_b32 m0, %0\n\t"
@@ -69,7 +73,7 @@ __device__ __forceinline__ void load_lds(const char* addr, uint32_t lds) {
       "global_load_lds_dwordx4 %1, off"
       :
       : "s"(lds), "v"(addr)
-      : "memory");
+      : "memory", "m0");
 }
 __device__ __forceinline__ void load_lds(uint64_t base, uint32_t off,
                                          uint32_t lds) {
@@ -79,8 +83,9 @@ __device__ __forceinline__ void load_lds(uint64_t base, uint32_t off,
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(lds), "v"(off), "s"(base)
-      : "memory");
+      : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Two registers' worth of four bf16 values of one row of a result's columns,
 // those of registers 8 k + {0..3} and 8 k + {4..7}, as eight neighbouring

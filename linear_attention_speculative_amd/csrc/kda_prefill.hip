@@ -771,7 +771,9 @@ __device__ __forceinline__ float max_abs(const f4& a, float m) {
 // lane order (no register holds the data, so any number may be in flight).
 // The completion is waited for by hand (wait_vm): the compiler does not see
 // these loads and keeps no count of them.  (m0 is a reserved register, which
-// the compiler sets anew before each use of its own.)
+// the compiler warns of; named, its own settings of m0 are not merged across.)
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void load_lds(const char* base, uint32_t off,
                                          uint32_t lds) {
   asm volatile(
@@ -780,8 +782,9 @@ __device__ __forceinline__ void load_lds(const char* base, uint32_t off,
       "global_load_lds_dwordx4 %1, %2"
       :
       : "s"(lds), "v"(off), "s"(base)
-      : "memory");
+      : "memory", "m0");
 }
+#pragma clang diagnostic pop
 
 // Wait until at most N of this wave's global memory operations are under way
 // (they end in the order in which they began).
