@@ -652,10 +652,17 @@ int launch_latent_expand(const ExpandParams& p, bool bf16,
     if (p.R == 128) return launch_rows<128>(p, stream);
     return int(hipErrorInvalidValue);
   }
+  // (beside the static entries: more than the 64 KB that need no leave)
+  constexpr int lds = 4 * kExpand * 128;
+  static_assert(lds + kExpand * 8 <= 160 * 1024, "LDS");
+  const hipError_t e = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(kda_latent_expand_kernel),
+      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return int(e);
   launch_kernel(kda_latent_expand_kernel,
                 dim3((p.S + kExpand - 1) / kExpand,
                      (p.H * 2 * p.D + kExpand - 1) / kExpand),
-                dim3(256), 4 * kExpand * 128, stream, p);
+                dim3(256), lds, stream, p);
   return int(hipGetLastError());
 }
 
