@@ -984,9 +984,8 @@ int kda_reset_counter(int32_t* counter, int32_t n, void* stream);
    calling thread: the next `launches` kernels that library calls on this
    thread launch (a prefill takes two, the step tables two or, without
    tokens, one, sampling three to eight, the latent attention two, the
-   changes of logits one or, with masks and other changes, two or more, free
-   lists and compactions one to five, the other operators on caches and blocks
-   one) are dispatched with hipExtLaunchKernel, `start_event` (a hipEvent_t,
+   changes of logits one to three (masks one for each 65535 rows), free lists
+   and compactions one to five, the other operators on caches and blocks one) are dispatched with hipExtLaunchKernel, `start_event` (a hipEvent_t,
    may be NULL) recording the start of the first of them and `stop_event` (may
    be NULL) the end of the last.  The counter-clearing kernels
    (kda_reset_counter, the first use of the no-allocation entry point's array

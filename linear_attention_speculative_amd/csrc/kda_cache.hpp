@@ -119,6 +119,7 @@ struct LogitsParams {
   const int32_t* mask_rows;      // [M], or null: row m
   int32_t M, V, B, rows, L, num_bias, num_masks;
   int32_t mask_from;             // first row of a launch of the masks
+  int32_t parts;                 // workgroups that share a request's window
 };
 int launch_adjust_logits(const LogitsParams& p, bool bf16,
                          hipStream_t stream);

@@ -12,7 +12,7 @@
 // their entries in all rows of the window, four under way in each thread.  What
 // bounds that is memory: an entry costs a line of it.  Requests with more
 // tokens than the table takes go through the vocabulary in slices, a word of
-// LDS a token, by several workgroups.  The masks are a kernel of their own
+// LDS a token, by workgroups of their own.  The masks are a kernel of their own
 // behind it, 16 bytes at a time (in one kernel with the rest, the rows under a
 // mask held up their workgroup: 640 rows of 131072 bf16, a quarter of them
 // masked, 118 us).  Those rows, with 1500 tokens of history, now take 51 us in
@@ -31,6 +31,7 @@ constexpr int64_t kMaskRows = 65535;
 constexpr int kPlaces = 8192;      // of the table
 constexpr int kMost = 6144;        // tokens that it takes
 constexpr int kSlice = 4096;       // tokens of a pass without it
+constexpr int kPool = 256;         // workgroups of such passes
 constexpr int kRows = 64;          // rows of a window whose data is in LDS
 // a token of the prompt, one that a row's draft may add, and its count
 constexpr uint32_t kSeen = 1u << 31, kListed = 1u << 30, kCount = kListed - 1;
@@ -105,159 +106,255 @@ __device__ __forceinline__ void change_listed(const LogitsParams& p,
   }
 }
 
+// A request's window, history and parameters.
+struct Request {
+  int start, end;                  // rows of its window
+  const int32_t* history;
+  int known, prompt;
+  bool drafts;
+  Change c;
+  // (`known` is 0 where no penalty needs it)
+  __device__ __forceinline__ Request(const LogitsParams& p, int b)
+      : start(b), end(b + 1), history(nullptr), known(0), prompt(0),
+        c{1.0f, 0.0f, 0.0f, nullptr, nullptr, 0} {
+    if (p.qsl) {
+      start = min(max(p.qsl[b], 0), p.M);
+      end = min(max(p.qsl[b + 1], start), p.M);
+    }
+    if (p.tokens) {
+      const int row = p.req_idx ? p.req_idx[b] : b;
+      if (row >= 0 && row < p.rows) {
+        history = p.tokens + row * p.s_tok;
+        known = min(max(p.known[row], 0), p.L);
+        prompt = p.prompt[row];
+      }
+    }
+    if (p.rep) c.r = p.rep[b];
+    if (p.freq) c.f = p.freq[b];
+    if (p.pres) c.p = p.pres[b];
+    if (!(c.r > 0.0f)) c.r = 1.0f;           // (NaN, too)
+    if (c.f != c.f) c.f = 0.0f;
+    if (c.p != c.p) c.p = 0.0f;
+    if (p.bias_start) {
+      const int lo = min(max(p.bias_start[b], 0), p.num_bias);
+      c.n = min(max(p.bias_start[b + 1], lo), p.num_bias) - lo;
+      c.tokens = p.bias_tokens + lo;
+      c.values = p.bias_values + lo;
+    }
+    const bool counts = c.r != 1.0f || c.f != 0.0f || c.p != 0.0f;
+    if (!counts) known = 0;
+    drafts = counts && p.draft;
+  }
+  // Whether nothing changes, and whether the table takes its tokens.
+  __device__ __forceinline__ bool idle() const {
+    return start >= end || (known == 0 && !drafts && c.n == 0);
+  }
+  __device__ __forceinline__ bool fits() const {
+    return int64_t(known) + c.n + (drafts ? end - start : 0) <= kMost;
+  }
+};
+
+// A window of many rows is shared by several workgroups: part `z` of `parts`,
+// with the rows' data in LDS where it fits.
+__device__ __forceinline__ Rows part_of(const LogitsParams& p,
+                                        const Request& q, int z, int parts,
+                                        int32_t* row_draft,
+                                        int32_t* row_mask) {
+  const int per = (q.end - q.start + parts - 1) / parts;
+  const int first = min(q.start + z * per, q.end);
+  Rows r{q.drafts ? p.draft + first : nullptr, nullptr, first,
+         min(q.end - first, per)};
+  if (p.mask && p.mask_rows) {
+    r.mask_row = p.mask_rows + first;
+    if (r.count <= kRows) {
+      if (int(threadIdx.x) < r.count)
+        row_mask[threadIdx.x] = r.mask_row[threadIdx.x];
+      r.mask_row = row_mask;
+    }
+  }
+  if (q.drafts && r.count <= kRows) {
+    if (int(threadIdx.x) < r.count)
+      row_draft[threadIdx.x] = p.draft[first + threadIdx.x];
+    r.draft = row_draft;
+  }
+  return r;
+}
+
+// What a workgroup has in LDS besides the table or the slice.
+struct Small {
+  int touched, found[kThreads / 64];
+  int32_t row_draft[kRows], row_mask[kRows];
+  uint16_t over[kThreads];
+};
+
+// Request b, part z of its window, by the table if it takes its tokens.
+template <bool BF16>
+__device__ __forceinline__ void adjust_by_table(const LogitsParams& p, int b,
+                                                int z, uint32_t* lds,
+                                                Small& sm) {
+  const int tid = threadIdx.x;
+  const Request q(p, b);
+  if (q.idle() || !q.fits()) return;
+  const Rows r = part_of(p, q, z, p.parts, sm.row_draft, sm.row_mask);
+  if (r.count <= 0) return;
+  int& touched = sm.touched;
+  const Change& c = q.c;
+  const int first = r.first, end = first + r.count;
+
+  uint32_t* key = lds;                       // a token plus one; 0: free
+  uint32_t* word = lds + kPlaces;
+  uint16_t* list = reinterpret_cast<uint16_t*>(lds + 2 * kPlaces);
+  uint32_t* biased = lds + 2 * kPlaces + kPlaces / 2;
+  for (int i = tid; i < kPlaces / 4; i += kThreads) {
+    reinterpret_cast<u4*>(key)[i] = u4{0, 0, 0, 0};
+    reinterpret_cast<u4*>(word)[i] = u4{0, 0, 0, 0};
+    if (p.bias_start) reinterpret_cast<u4*>(biased)[i] = u4{0, 0, 0, 0};
+  }
+  if (tid == 0) touched = 0;
+  __syncthreads();
+  // the place of a token, taken for it if it is new; at most kMost tokens
+  // come, so there is always a free one
+  auto place_of = [&](int token) -> int {
+    if (uint32_t(token) >= uint32_t(p.V)) return -1;
+    const uint32_t k = uint32_t(token) + 1;
+    uint32_t at = (k * 2654435761u) >> 19;
+    while (true) {
+      const uint32_t had = atomicCAS(&key[at], 0u, k);
+      if (had == 0) list[atomicAdd(&touched, 1)] = uint16_t(at);
+      if (had == 0 || had == k) return int(at);
+      at = (at + 1) % kPlaces;
+    }
+  };
+  for (int i = tid; i < q.known; i += kThreads) {
+    const int at = place_of(q.history[i]);
+    if (at < 0) continue;
+    if (i < q.prompt)
+      atomicOr(&word[at], kSeen);
+    else
+      atomicAdd(&word[at], 1u);
+  }
+  if (q.drafts)
+    for (int i = q.start + 1 + tid; i < end; i += kThreads) {
+      const int at = place_of(p.draft[i]);
+      if (at >= 0 && i <= first) atomicAdd(&word[at], 1u);
+    }
+  for (int i = tid; i < c.n; i += kThreads) {
+    const int at = place_of(c.tokens[i]);
+    if (at >= 0) atomicMax(&biased[at], uint32_t(i) + 1);
+  }
+  __syncthreads();
+  change_listed<BF16>(
+      p, c, r, touched, [&](int i) { return int(key[list[i]]) - 1; },
+      [&](int i) { return word[list[i]]; },
+      [&](int i) { return c.n > 0 ? biased[list[i]] : 0u; });
+}
+
+// Requests that the table does not take: each of `count` workgroups looks all
+// requests over and lists them, and the items (request, part of its window,
+// slice of the vocabulary) go round the workgroups.
+template <bool BF16>
+__device__ __forceinline__ void adjust_by_slices(const LogitsParams& p,
+                                                 int number, int count,
+                                                 uint32_t* lds, Small& sm) {
+  uint32_t* words = lds;
+  uint32_t* biased = lds + kSlice;
+  uint16_t* list = reinterpret_cast<uint16_t*>(lds + 2 * kSlice);
+  int& touched = sm.touched;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int slices = (p.V + kSlice - 1) / kSlice, each = slices * p.parts;
+  // (few requests: an item each, whether the table takes it or not, without
+  // the list, which costs a second look at the request)
+  const bool few = int64_t(p.B) * each <= count;
+  int64_t next = number;                     // this workgroup's next item
+  int64_t done = 0;                          // items of the requests before b0
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    int all = p.B;
+    if (!few) {
+      bool mine = false;
+      if (b0 + tid < p.B) {
+        const Request q(p, b0 + tid);
+        mine = !q.idle() && !q.fits();
+      }
+      const uint64_t m = __ballot(mine);
+      __syncthreads();                       // the last list is done
+      if (lane == 0) sm.found[wave] = __popcll(m);
+      __syncthreads();
+      int at = __popcll(m & ((uint64_t(1) << lane) - 1));
+      all = 0;
+      for (int k = 0; k < kThreads / 64; ++k) {
+        at += k < wave ? sm.found[k] : 0;
+        all += sm.found[k];
+      }
+      if (mine) sm.over[at] = uint16_t(tid);
+      __syncthreads();
+    }
+    const int64_t end_item = done + int64_t(all) * each;
+    for (; next < end_item; next += count) {
+      const int in = int(next - done);       // (of 1024 requests: 2^24 at most)
+      const int k = in / each, item = in - k * each;
+      const int z = item / slices, v0 = (item - z * slices) * kSlice;
+      const int nv = min(p.V - v0, kSlice);
+      const Request q(p, b0 + (few ? k : sm.over[k]));
+      if (few && (q.idle() || q.fits())) continue;
+      __syncthreads();                       // the last item is done
+      const Rows r = part_of(p, q, z, p.parts, sm.row_draft,
+                             sm.row_mask);
+      if (r.count <= 0) continue;
+      const Change& c = q.c;
+      const int first = r.first, end = first + r.count;
+      for (int i = tid; i < kSlice / 4; i += kThreads) {
+        reinterpret_cast<u4*>(words)[i] = u4{0, 0, 0, 0};
+        reinterpret_cast<u4*>(biased)[i] = u4{0, 0, 0, 0};
+      }
+      if (tid == 0) touched = 0;
+      __syncthreads();
+      for (int i = tid; i < q.known; i += kThreads) {
+        const uint32_t at = uint32_t(q.history[i]) - uint32_t(v0);
+        if (at >= uint32_t(nv)) continue;
+        if (i < q.prompt)
+          atomicOr(&words[at], kSeen);
+        else
+          atomicAdd(&words[at], 1u);
+      }
+      if (q.drafts)
+        for (int i = q.start + 1 + tid; i < end; i += kThreads) {
+          const uint32_t at = uint32_t(p.draft[i]) - uint32_t(v0);
+          if (at >= uint32_t(nv)) continue;
+          if (i <= first)
+            atomicAdd(&words[at], 1u);
+          else
+            atomicOr(&words[at], kListed);
+        }
+      for (int i = tid; i < c.n; i += kThreads) {
+        const uint32_t at = uint32_t(c.tokens[i]) - uint32_t(v0);
+        if (at < uint32_t(nv)) atomicMax(&biased[at], uint32_t(i) + 1);
+      }
+      __syncthreads();
+      for (int i = tid; i < nv; i += kThreads)
+        if (words[i] | biased[i]) list[atomicAdd(&touched, 1)] = uint16_t(i);
+      __syncthreads();
+      change_listed<BF16>(
+          p, c, r, touched, [&](int i) { return v0 + list[i]; },
+          [&](int i) { return words[list[i]]; },
+          [&](int i) { return biased[list[i]]; });
+    }
+    done = end_item;
+  }
+}
+
+// Workgroups [0, B) x parts: a part of a request each.  Those behind them take
+// what the table does not.
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads)
     kda_adjust_logits_kernel(LogitsParams p) {
   extern __shared__ __align__(16) uint32_t lds[];
-  __shared__ int touched;
-  __shared__ int32_t row_draft[kRows], row_mask[kRows];
-  const int tid = threadIdx.x, b = blockIdx.y;
-  int m0 = b, m1 = b + 1;
-  if (p.qsl) {
-    m0 = min(max(p.qsl[b], 0), p.M);
-    m1 = min(max(p.qsl[b + 1], m0), p.M);
-  }
-  // a window of many rows is shared: rows [first, m1) are this workgroup's
-  const int per = (m1 - m0 + int(gridDim.z) - 1) / int(gridDim.z);
-  const int first = m0 + int(blockIdx.z) * per;
-  const int start = m0;
-  m1 = min(m1, first + per);
-  if (first >= m1) return;
-
-  Change c{1.0f, 0.0f, 0.0f, nullptr, nullptr, 0};
-  const int32_t* history = nullptr;
-  int known = 0, prompt = 0;
-  if (p.tokens) {
-    const int row = p.req_idx ? p.req_idx[b] : b;
-    if (row >= 0 && row < p.rows) {
-      history = p.tokens + row * p.s_tok;
-      known = min(max(p.known[row], 0), p.L);
-      prompt = p.prompt[row];
-    }
-  }
-  if (p.rep) c.r = p.rep[b];
-  if (p.freq) c.f = p.freq[b];
-  if (p.pres) c.p = p.pres[b];
-  if (!(c.r > 0.0f)) c.r = 1.0f;             // (NaN, too)
-  if (c.f != c.f) c.f = 0.0f;
-  if (c.p != c.p) c.p = 0.0f;
-  if (p.bias_start) {
-    const int lo = min(max(p.bias_start[b], 0), p.num_bias);
-    c.n = min(max(p.bias_start[b + 1], lo), p.num_bias) - lo;
-    c.tokens = p.bias_tokens + lo;
-    c.values = p.bias_values + lo;
-  }
-  const bool counts = c.r != 1.0f || c.f != 0.0f || c.p != 0.0f;
-  if (!counts) known = 0;
-  const bool drafts = counts && p.draft;
-  if (!counts && c.n == 0) return;
-  const bool table = int64_t(known) + c.n + (drafts ? m1 - start : 0) <= kMost;
-  if (table && blockIdx.x > 0) return;       // (one workgroup does it all)
-
-  Rows r{drafts ? p.draft + first : nullptr, nullptr, first, m1 - first};
-  if (p.mask && p.mask_rows) {
-    r.mask_row = p.mask_rows + first;
-    if (r.count <= kRows) {
-      if (tid < r.count) row_mask[tid] = r.mask_row[tid];
-      r.mask_row = row_mask;
-    }
-  }
-  if (drafts && r.count <= kRows) {
-    if (tid < r.count) row_draft[tid] = p.draft[first + tid];
-    r.draft = row_draft;
-  }
-
-  if (table) {
-    uint32_t* key = lds;                     // a token plus one; 0: free
-    uint32_t* word = lds + kPlaces;
-    uint16_t* list = reinterpret_cast<uint16_t*>(lds + 2 * kPlaces);
-    uint32_t* biased = lds + 2 * kPlaces + kPlaces / 2;
-    for (int i = tid; i < kPlaces / 4; i += kThreads) {
-      reinterpret_cast<u4*>(key)[i] = u4{0, 0, 0, 0};
-      reinterpret_cast<u4*>(word)[i] = u4{0, 0, 0, 0};
-      if (p.bias_start) reinterpret_cast<u4*>(biased)[i] = u4{0, 0, 0, 0};
-    }
-    if (tid == 0) touched = 0;
-    __syncthreads();
-    // the place of a token, taken for it if it is new; at most kMost tokens
-    // come, so there is always a free one
-    auto place_of = [&](int token) -> int {
-      if (uint32_t(token) >= uint32_t(p.V)) return -1;
-      const uint32_t k = uint32_t(token) + 1;
-      uint32_t at = (k * 2654435761u) >> 19;
-      while (true) {
-        const uint32_t had = atomicCAS(&key[at], 0u, k);
-        if (had == 0) list[atomicAdd(&touched, 1)] = uint16_t(at);
-        if (had == 0 || had == k) return int(at);
-        at = (at + 1) % kPlaces;
-      }
-    };
-    for (int i = tid; i < known; i += kThreads) {
-      const int at = place_of(history[i]);
-      if (at < 0) continue;
-      if (i < prompt)
-        atomicOr(&word[at], kSeen);
-      else
-        atomicAdd(&word[at], 1u);
-    }
-    if (drafts)
-      for (int i = start + 1 + tid; i < m1; i += kThreads) {
-        const int at = place_of(p.draft[i]);
-        if (at >= 0 && i <= first) atomicAdd(&word[at], 1u);
-      }
-    for (int i = tid; i < c.n; i += kThreads) {
-      const int at = place_of(c.tokens[i]);
-      if (at >= 0) atomicMax(&biased[at], uint32_t(i) + 1);
-    }
-    __syncthreads();
-    change_listed<BF16>(
-        p, c, r, touched, [&](int i) { return int(key[list[i]]) - 1; },
-        [&](int i) { return word[list[i]]; },
-        [&](int i) { return c.n > 0 ? biased[list[i]] : 0u; });
-    return;
-  }
-
-  uint32_t* words = lds;
-  uint32_t* biased = lds + kSlice;
-  uint16_t* list = reinterpret_cast<uint16_t*>(lds + 2 * kSlice);
-  for (int v0 = int(blockIdx.x) * kSlice; v0 < p.V;
-       v0 += int(gridDim.x) * kSlice) {
-    const int nv = min(p.V - v0, kSlice);
-    __syncthreads();                         // the last slice is done
-    for (int i = tid; i < kSlice / 2; i += kThreads)
-      reinterpret_cast<u4*>(lds)[i] = u4{0, 0, 0, 0};
-    if (tid == 0) touched = 0;
-    __syncthreads();
-    for (int i = tid; i < known; i += kThreads) {
-      const uint32_t at = uint32_t(history[i]) - uint32_t(v0);
-      if (at >= uint32_t(nv)) continue;
-      if (i < prompt)
-        atomicOr(&words[at], kSeen);
-      else
-        atomicAdd(&words[at], 1u);
-    }
-    if (drafts)
-      for (int i = start + 1 + tid; i < m1; i += kThreads) {
-        const uint32_t at = uint32_t(p.draft[i]) - uint32_t(v0);
-        if (at >= uint32_t(nv)) continue;
-        if (i <= first)
-          atomicAdd(&words[at], 1u);
-        else
-          atomicOr(&words[at], kListed);
-      }
-    for (int i = tid; i < c.n; i += kThreads) {
-      const uint32_t at = uint32_t(c.tokens[i]) - uint32_t(v0);
-      if (at < uint32_t(nv)) atomicMax(&biased[at], uint32_t(i) + 1);
-    }
-    __syncthreads();
-    for (int i = tid; i < nv; i += kThreads)
-      if (words[i] | biased[i]) list[atomicAdd(&touched, 1)] = uint16_t(i);
-    __syncthreads();
-    change_listed<BF16>(
-        p, c, r, touched, [&](int i) { return v0 + list[i]; },
-        [&](int i) { return words[list[i]]; },
-        [&](int i) { return biased[list[i]]; });
-  }
+  __shared__ Small sm;
+  const int x = blockIdx.x - p.B;
+  if (x < 0)
+    adjust_by_table<BF16>(p, blockIdx.x, blockIdx.y, lds, sm);
+  else
+    adjust_by_slices<BF16>(p, x * p.parts + blockIdx.y,
+                           (gridDim.x - p.B) * p.parts, lds, sm);
 }
 
 // Entries that a row's mask does not allow, after the changes.
@@ -318,23 +415,30 @@ namespace {
 template <bool BF16>
 int launch(const LogitsParams& p, hipStream_t stream) {
   if (p.rep || p.freq || p.pres || p.bias_start) {
-    // a workgroup takes some 16 rows of an average window; the slices of
-    // requests that the table does not take are shared by up to 32 (where the
-    // longest history fits, there are none)
+    // a workgroup takes some 16 rows of an average window
     const int64_t rows = (int64_t(p.M) / p.B + 15) / 16;
-    const int64_t z = rows < 1 ? 1 : rows > 64 ? 64 : rows;
-    const int64_t most = int64_t(p.L) + p.num_bias + p.M;
-    const int64_t slices = (int64_t(p.V) + kSlice - 1) / kSlice;
-    const int64_t x = most <= kMost ? 1 : slices > 32 ? 32 : slices;
+    LogitsParams q = p;
+    q.parts = rows < 1 ? 1 : rows > 64 ? 64 : int32_t(rows);
+    // Lengths are on the GPU.  Where the longest history, all biases and all
+    // drafts fit the table no request exceeds it; else there are workgroups for
+    // those that do, one a CU (256 requests of 3000 tokens in rows of 3001: 53
+    // us; in rows of 8192 and more: 53 us, 404 with 32 workgroups a request)
+    int64_t pool = 0;
+    if (int64_t(p.L) + p.num_bias + p.M > kMost) {
+      const int64_t items = int64_t(p.B) * q.parts *
+                            ((p.V + kSlice - 1) / kSlice);
+      pool = ((items < kPool ? items : kPool) + q.parts - 1) / q.parts;
+    }
     constexpr int lds = (3 * kPlaces + kPlaces / 2) * 4;
-    static_assert(lds >= (2 * kSlice + kSlice / 2) * 4, "LDS");
+    static_assert(lds - kPlaces * 4 >= (2 * kSlice + kSlice / 2) * 4 &&
+                  lds + sizeof(Small) <= 160 * 1024, "LDS");
     const auto kernel = kda_adjust_logits_kernel<BF16>;
     const hipError_t e = hipFuncSetAttribute(
         reinterpret_cast<const void*>(kernel),
         hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return int(e);
-    launch_kernel(kernel, dim3(uint32_t(x), p.B, uint32_t(z)), dim3(kThreads),
-                  p.bias_start ? lds : lds - kPlaces * 4, stream, p);
+    launch_kernel(kernel, dim3(uint32_t(p.B + pool), q.parts), dim3(kThreads),
+                  p.bias_start ? lds : lds - kPlaces * 4, stream, q);
   }
   if (p.mask) {
     constexpr int kMaskChunk = 4 * kMaskThreads * (BF16 ? 8 : 4);
