@@ -653,7 +653,8 @@ typedef struct {
    without a row of token_ids (NULL, or outside [0, num_request_rows)) has an
    empty history.  Tokens outside [0, V) are ignored.  Arithmetic is fp32,
    rounded once.  Entries that nothing changes keep their bits; rows that belong
-   to no request are not touched.
+   to no request are not touched.  V is at most 2^20, batch 65535 and M 2^31 -
+   64.
    A mask row holds a bit for each token, bit v % 32 of word v / 32, 1 =
    allowed; row m's is mask_rows[m] (NULL: m), outside [0, num_masks): none. */
 typedef struct {
@@ -717,7 +718,8 @@ typedef struct {
    the fork shares the table's blocks and takes none.  A fork with a row
    outside [0, num_request_rows) or with a = b does nothing and takes none.
    Entries of the child's row behind block k stay.  A child row must not be
-   another fork's row; a parent may have many forks. */
+   another fork's row; a parent may have many forks.  num_forks is below
+   2^24. */
 typedef struct {
   const int32_t* parent_rows;    /* [num_forks] */
   const int32_t* child_rows;     /* [num_forks] */
@@ -746,7 +748,7 @@ typedef struct {
      free_blocks = the blocks i > null_block_id with no reference, in rising
      order, null ids behind them up to N;  num_free = how many they are.
    Released rows outside [0, num_request_rows) are ignored; one may be named
-   twice. */
+   twice.  N is at most 2^28, num_request_rows below 2^24. */
 typedef struct {
   const int32_t* released_rows;  /* [num_released] */
   const int32_t* block_table;    /* [num_request_rows, width] */
@@ -779,7 +781,8 @@ typedef struct {
      num_blocks[r] entries of each row, other entries as they were (may be
      block_table itself);
      new_ref_counts the counts by new id (may be ref_counts itself).
-   With all moves made, the free blocks are null_block_id + n + 1 .. N - 1. */
+   With all moves made, the free blocks are null_block_id + n + 1 .. N - 1.
+   Limits as in kda_free_args. */
 typedef struct {
   const int32_t* ref_counts;     /* [N] */
   const int32_t* block_table;    /* [num_request_rows, width] */

@@ -1,5 +1,6 @@
 """Changes of logits over shapes of a launch: token histories with more columns
-than any request fills, many requests of which a few exceed the table."""
+than any request fills, many requests of which a few exceed the table, and
+more rows than a grid takes."""
 import numpy as np
 import pytest
 import torch
@@ -33,6 +34,24 @@ def test_more_columns_than_tokens(B, V, known):
     kw["prompt_lens"] = i32(lens // 3)
     before = f64(kw["logits"])
     ref, size = expect(kw)
+    kda.adjust_logits(**kw)
+    torch.cuda.synchronize()
+    check(kw, before, ref, size)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_more_rows_than_a_grid(act):
+    """Masks of rows on both sides of the 65535th."""
+    kw = make([30000, 35000, 1, 5100], 41, act=act, seed=2, tail=7, masks=5)
+    for n in ("draft_tokens", "token_ids", "prompt_lens", "token_lens",
+              "request_indices", "repetition_penalty", "frequency_penalty",
+              "presence_penalty"):
+        del kw[n]
+    assert kw["logits"].shape[0] > 65535 + 4000
+    before = f64(kw["logits"])
+    ref, size = expect(kw)
+    assert np.isinf(ref[65500:65535]).any() and np.isinf(ref[65536:]).any()
     kda.adjust_logits(**kw)
     torch.cuda.synchronize()
     check(kw, before, ref, size)
