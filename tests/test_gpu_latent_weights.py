@@ -1,4 +1,5 @@
-"""Softmax weights of the bf16 attention kernels hold 16 bits of each weight."""
+"""Softmax weights of the bf16 attention kernels hold 16 bits of each weight,
+and requests whose block tables exceed what LDS holds of them."""
 import numpy as np
 import pytest
 import torch
@@ -67,3 +68,19 @@ def test_infinite_values_at_any_weight():
     assert (out[199:, :, 4] == -np.inf).all()
     assert np.isfinite(out[:199, :, 4]).all()
     assert np.isfinite(out[:, :, 5:]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_runs_past_the_table_in_lds(act):
+    """512 entries of a block table are in LDS at a time: with a block a token
+    and 140 requests of some 1500 tokens a workgroup's run passes that."""
+    computed = [1400 + 3 * i for i in range(140)]
+    kw = make([1] * 140, computed, H=2, R=128, P=0, block=1, act=act, seed=4)
+    steps = sum(-(-(c + 1) // 32) + 4 for c in computed)
+    assert (steps // 256 - 8) * 32 > 512
+    kw["block_table"][5:60:7, 700:900:3] = 0        # null blocks among them
+    ref = absorbed.expect(kw)
+    absorbed.run(kw)
+    torch.cuda.synchronize()
+    absorbed.check(kw, ref, act)
