@@ -747,6 +747,8 @@ typedef struct {
      hold block i (their first new_num_blocks entries; null ids are none);
      free_blocks = the blocks i > null_block_id with no reference, in rising
      order, null ids behind them up to N;  num_free = how many they are.
+   `pinned` is by block id, and follows the moves of kda_compact_blocks only
+   where its holder moves it.
    Released rows outside [0, num_request_rows) are ignored; one may be named
    twice.  N is at most 2^28, num_request_rows below 2^24. */
 typedef struct {
@@ -781,6 +783,9 @@ typedef struct {
      num_blocks[r] entries of each row, other entries as they were (may be
      block_table itself);
      new_ref_counts the counts by new id (may be ref_counts itself).
+   Blocks that kda_free_blocks found pinned move as the others do: whoever holds
+   ids outside the block table puts destinations for sources in them, and moves
+   the entries of `pinned` likewise, before the next kda_free_blocks.
    With all moves made, the free blocks are null_block_id + n + 1 .. N - 1.
    Limits as in kda_free_args. */
 typedef struct {

@@ -122,7 +122,8 @@ def fork_blocks(*, stream=None, **kwargs) -> None:
     """Child rows that continue their parents' tokens: whole blocks shared, the
     running one new (kda_fork_args in include/kda_recoverssm.h).  Updates
     `block_table`, `num_blocks` and `num_computed_tokens` in place;
-    `BlockPools.copy(copy_pairs)` then copies the running blocks."""
+    `BlockPools.copy(copy_pairs)` then copies the running blocks; of a longer
+    `copy_pairs`, `copy_pairs[:forks]` (the rows behind stay as they were)."""
     _launch(_abi.load().kda_fork_blocks, fork_args(**kwargs), kwargs, stream)
 
 
@@ -203,6 +204,11 @@ def compact_blocks(*, stream=None, **kwargs) -> None:
     """Plans the moves that bring every live block to the lowest ids, and
     rewrites block table and reference counts (kda_compact_blocks_args in
     include/kda_recoverssm.h); `BlockPools.copy(copy_pairs, num_pairs)` then
-    makes the moves."""
+    makes the moves.  Pinned blocks move, too: a holder of ids outside the
+    block table applies the pairs to them and to its `pinned` counts:
+
+        src, dst = copy_pairs[:int(num_pairs)].long().t()
+        pinned[dst], pinned[src] = pinned[src], 0
+    """
     _launch(_abi.load().kda_compact_blocks, compact_blocks_args(**kwargs),
             kwargs, stream)

@@ -1,5 +1,6 @@
 """Edges of the block operators: calls without forks, forks at the end of the
-table; and sizes past what one launch takes (CPU)."""
+table, blocks that a holder outside the table pins, and sizes past what one
+launch takes (CPU)."""
 import numpy as np
 import pytest
 import torch
@@ -7,7 +8,9 @@ import torch
 import linear_attention_speculative_amd as kda
 import oracle
 from linear_attention_speculative_amd import _abi
-from tests.test_gpu_blocks import fork_case, held_case, i32, same
+from tests.latent_check import ints
+from tests.test_gpu_blocks import (compaction, fork_case, held_case, i32,
+                                   same)
 
 DEV = "cuda"
 I32 = torch.int32
@@ -89,6 +92,40 @@ def test_forks_past_the_table_take_no_block(F):
     torch.cuda.synchronize()
     assert int(kw["num_allocated"]) == fits.sum()
     same(kw, oracle.fork_blocks(**host))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [64, 20000])
+def test_pinned_blocks_follow_the_moves(N):
+    """A prefix holder's blocks move with the others: it applies the pairs to
+    its ids and its pins, and the next recount finds them held."""
+    kw, _ = held_case(6, 5, N, seed=2, fill=1.0, released=0.5, pinned=True)
+    ids = torch.tensor([N - 1, N - 3, N - 4], device=DEV)
+    kw["pinned"][ids] = 1
+    pool = torch.arange(N, device=DEV).view(-1, 1).repeat(1, 5).contiguous()
+    text = pool[ids].clone()
+    kda.free_blocks(**kw)
+    kc = compaction(kw, N // 2)
+    kda.compact_blocks(**kc)
+    kda.BlockPools([pool]).copy(kc["copy_pairs"], kc["num_pairs"])
+    # the holder: old id -> new id, pins at their new places
+    src, dst = kc["copy_pairs"][:int(kc["num_pairs"])].long().t()
+    to = torch.arange(N, device=DEV)
+    to[src] = dst
+    ids, pins = to[ids], kw["pinned"].clone()
+    pins[dst], pins[src] = kw["pinned"][src], 0
+    assert torch.equal(pool[ids], text)
+    again = dict(kw, released_rows=kw["released_rows"][:0], pinned=pins,
+                 block_table=kc["new_block_table"],
+                 num_blocks=kw["new_num_blocks"],
+                 new_num_blocks=kw["new_num_blocks"].clone(),
+                 ref_counts=torch.empty_like(kw["ref_counts"]))
+    kda.free_blocks(**again)
+    torch.cuda.synchronize()
+    assert torch.equal(again["ref_counts"].clamp(min=0),
+                       kc["new_ref_counts"].clamp(min=0))
+    free = ints(kw["free_blocks"])[:int(kw["num_free"])]
+    assert not set(ints(ids)) & set(free)
 
 
 def test_more_rows_than_a_launch_are_refused():
