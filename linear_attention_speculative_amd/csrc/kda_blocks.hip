@@ -324,16 +324,25 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- the same in one workgroup ---------------------------------------------------
 
-// Pools of up to kSmallBlocks blocks and tables of up to kSmallEntries entries
-// take one launch or two in place of five: all counts and lists fit LDS.
+// Pools of up to kSmallBlocks blocks take one launch or two in place of five:
+// all counts and lists fit LDS.  The table is read in rounds of kRound rows by
+// 64 columns (each_entry), some 1.8 us each:
+// - free lists count it in that launch for up to kFreeRounds rounds, else in
+//   five launches (8192 blocks, 512 rows of 40, 4 rounds: 13 us, 17 in five;
+//   16384 blocks, 1024 rows of 64, 8 rounds: 27, 19; 4096 rows of 16: 77, 21);
+// - compaction rewrites it in that launch for one round, else in a second one
+//   with a workgroup a row (5 rows of 6: 4.7 us, 5.0 in two; 64 rows of 64:
+//   8.3, 8.4; 512 rows of 8: 18.8, 11.2; 4096 rows of 16: 89, 22, and 23 in
+//   five).
 constexpr int kSmallBlocks = 16384;
-constexpr int kSmallRows = 4096;
-constexpr int kSmallEntries = 65536;
 constexpr int kMany = 1024;        // threads
-// Compaction rewrites tables of up to this many entries in that launch, larger
-// ones in a second one with a workgroup a row (512 rows of 40: 10 and 5 us, 20
-// in one; 5 rows of 6: 5 us in one, a launch more in two).
-constexpr int kInside = 1024;
+constexpr int kAtOnce = 8;         // rows that a wave has under way
+constexpr int kRound = kAtOnce * kMany / 64;
+constexpr int kFreeRounds = 4;
+constexpr int kSmallRows = kFreeRounds * kRound;
+__host__ __device__ constexpr int64_t rounds_of(int64_t rows, int64_t width) {
+  return (rows + kRound - 1) / kRound * ((width + 63) / 64);
+}
 
 // Exclusive prefix sum over the workgroup's threads, and the total.
 __device__ __forceinline__ int scan_many(int v, int* total, int* red) {
@@ -356,11 +365,11 @@ __device__ __forceinline__ int scan_many(int v, int* total, int* red) {
   return before + upto - v;
 }
 
-// Every entry of a table, a wave a row, eight rows under way together.
+// Every entry of a table, a wave a row, kAtOnce rows under way together.
 template <class Load, class Use>
 __device__ __forceinline__ void each_entry(int rows, int width, Load load,
                                            Use use) {
-  constexpr int U = 8, kWaves = kMany / 64;
+  constexpr int U = kAtOnce, kWaves = kMany / 64;
   const int lane = threadIdx.x & 63, w = uniform(threadIdx.x >> 6);
   for (int r0 = w; r0 < rows; r0 += U * kWaves)
     for (int j = lane; j < width; j += 64) {
@@ -419,12 +428,13 @@ __global__ void __launch_bounds__(kMany)
   extern __shared__ __align__(16) int32_t refs[];   // [N], then lists
   __shared__ int red[kMany / 64];
   const int tid = threadIdx.x, N = int(p.N);
-  const bool inside = p.rows * p.width <= kInside;
+  const bool inside = rounds_of(p.rows, p.width) <= 1;
   uint16_t* src = reinterpret_cast<uint16_t*>(refs + N);   // [N / 2 + 1]
   uint16_t* dst = src + N / 2 + 1;
   uint16_t* map = dst + N / 2 + 1;                         // [N]
   int32_t* held = refs + 2 * N + 1;                        // [rows]
-  for (int i = tid; i < p.rows; i += kMany) held[i] = p.held[i];
+  if (inside)
+    for (int i = tid; i < min(p.rows, kRound); i += kMany) held[i] = p.held[i];
   for (int i = tid; i < N; i += kMany) {
     refs[i] = p.refs[i];
     map[i] = uint16_t(i);
@@ -497,10 +507,6 @@ namespace {
 dim3 grid_of(int64_t n) {
   return dim3(uint32_t((n + kThreads - 1) / kThreads));
 }
-bool is_small(int64_t N, int64_t rows, int64_t width) {
-  return N <= kSmallBlocks && rows <= kSmallRows &&
-         rows * width <= kSmallEntries;
-}
 template <class F>
 hipError_t more_lds(F kernel) {
   return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -513,7 +519,8 @@ dim3 chunks_of(int64_t N) {
 }  // namespace
 
 int launch_free_blocks(const FreeParams& p, hipStream_t stream) {
-  if (is_small(p.N, p.rows, p.width)) {
+  if (p.N <= kSmallBlocks && rounds_of(p.rows, p.width) <= kFreeRounds &&
+      p.rows <= kSmallRows) {
     const hipError_t e = more_lds(kda_free_small_kernel);
     if (e != hipSuccess) return int(e);
     launch_kernel(kda_free_small_kernel, dim3(1), dim3(kMany),
@@ -534,12 +541,12 @@ int launch_free_blocks(const FreeParams& p, hipStream_t stream) {
 }
 
 int launch_compact_blocks(const CompactBlocksParams& p, hipStream_t stream) {
-  if (is_small(p.N, p.rows, p.width)) {
+  if (p.N <= kSmallBlocks) {
     const hipError_t e = more_lds(kda_compact_small_kernel);
     if (e != hipSuccess) return int(e);
     launch_kernel(kda_compact_small_kernel, dim3(1), dim3(kMany),
-                  uint32_t(p.N * 2 + 1 + p.rows) * 4, stream, p);
-    if (p.rows * p.width > kInside)
+                  uint32_t(p.N * 2 + 1 + kRound) * 4, stream, p);
+    if (rounds_of(p.rows, p.width) > 1)
       launch_kernel(kda_compact_table_kernel, dim3(p.rows), dim3(kThreads), 0,
                     stream, p);
     return int(hipGetLastError());

@@ -156,3 +156,33 @@ def test_more_rows_than_a_launch_are_refused():
     assert lib.kda_check_compact_blocks(a) == _abi.KDA_OK
     a.num_request_rows = n
     assert lib.kda_check_compact_blocks(a) == _abi.KDA_E_CAPACITY
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("rows,width,N", [
+    # around what one workgroup reads of a table at a time
+    (128, 64, 3000), (129, 64, 3000), (128, 65, 16384), (100, 256, 9000),
+    (512, 64, 5000), (513, 3, 5000), (512, 65, 16384), (3000, 1, 700),
+    (600, 0, 50), (0, 5, 50)])
+def test_tables_around_a_round(rows, width, N):
+    kw, host = held_case(max(rows, 1), max(width, 1), N, seed=rows + width,
+                         fill=0.4, pinned=True)
+    for n in ("num_blocks", "new_num_blocks"):
+        kw[n] = kw[n][:rows]
+    kw["block_table"] = kw["block_table"][:rows, :width]
+    host.update(num_blocks=host["num_blocks"][:rows],
+                block_table=host["block_table"][:rows, :width])
+    ref = oracle.free_blocks(**host)
+    kda.free_blocks(**kw)
+    torch.cuda.synchronize()
+    same(kw, ref)
+    for place in (False, True):
+        kc = compaction(kw, N // 2)
+        if place:
+            kc.update(new_block_table=kw["block_table"].clone())
+            kc.update(block_table=kc["new_block_table"])
+        kda.compact_blocks(**kc)
+        torch.cuda.synchronize()
+        same(kc, oracle.compact_blocks(
+            ref_counts=ref["ref_counts"], block_table=host["block_table"],
+            num_blocks=ref["new_num_blocks"], max_pairs=N // 2))
