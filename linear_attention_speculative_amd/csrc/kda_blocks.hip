@@ -13,7 +13,8 @@
 // cache.  The bookkeeping of 8192 blocks and 512 rows of 40 entries takes 15 us
 // (free lists, half of it the pass over the table in one workgroup) and 10 + 5
 // us (compaction, the table in a launch of its own).  32 rows of the table under
-// way in place of 8 take longer: so does their code to arrive.
+// way in place of 8 take longer: so does their code to arrive.  Forks take 4 to
+// 5 us.
 #include "kda_cache.hpp"
 #include "kda_mma.hpp"
 
@@ -324,11 +325,11 @@ __global__ void __launch_bounds__(kThreads)
 
 // ---- the same in one workgroup ---------------------------------------------------
 
-// Pools of up to kSmallBlocks blocks take one launch or two in place of five:
-// all counts and lists fit LDS.  The table is read in rounds of kRound rows by
-// 64 columns (each_entry), some 1.8 us each:
+// Pools of up to kSmallBlocks blocks take one launch or two in place of four or
+// five: all counts and lists fit LDS.  The table is read in rounds of kRound rows
+// by 64 columns (each_entry), 0.7 to 1.9 us each:
 // - free lists count it in that launch for up to kFreeRounds rounds, else in
-//   five launches (8192 blocks, 512 rows of 40, 4 rounds: 13 us, 17 in five;
+//   four launches (8192 blocks, 512 rows of 40, 4 rounds: 13 us, 17 in four;
 //   16384 blocks, 1024 rows of 64, 8 rounds: 27, 19; 4096 rows of 16: 77, 21);
 // - compaction rewrites it in that launch for one round, else in a second one
 //   with a workgroup a row (5 rows of 6: 4.7 us, 5.0 in two; 64 rows of 64:

@@ -32,13 +32,16 @@
 // 2^-15 of a weight at most (split_bf16() in kda_mma.hpp).
 //
 // What bounds it (R = 512, P = 64, 32 heads, bf16): for 256 single tokens
-// behind 3000 others on average, the cache's bytes: 199 us, 884 MB at 4.4 TB/s,
-// of which the loop's steps run at 5.0 (1.9 us each), and some 6 us a piece go
-// to its queries, its first tile and its outputs.  For 48 windows of up to 4
-// drafts behind 1500 tokens, two row tiles a request: 46 us, a chain of scores,
-// exchange, weights and sums of 2.3 us a step with one workgroup of eight waves
-// on a CU; the matrix cores are busy for a seventh of it.  The join takes 11 us
-// of the first, 13 us of the second (37 MB of pieces), 5 us of one request.
+// behind 3000 others on average, the cache's bytes and a step's chain: 216 us,
+// 884 MB at 4.1 TB/s, of which the loop's steps run at 4.6 (2.0 us each; 1.9
+// with one bf16 value a weight), and some 6 us a piece go to its queries, its
+// first tile and its outputs.  For 48 windows of up to 4 drafts behind 1500
+// tokens, two row tiles a request: 51 us, a chain of scores, exchange, weights
+// and sums of 2.5 us a step with one workgroup of eight waves on a CU; the
+// matrix cores are busy for a fifth of it, and the cache is read once for each
+// row tile.  The join takes 11 us of the first, 13 us of the second (37 MB of
+// pieces), 5 us of one request.  fp32 holds one or two tiles in LDS: 64 tokens
+// behind 3000 take 254 us a call, the 48 windows 203.
 #include "kda_cache.hpp"
 #include "kda_mma.hpp"
 

@@ -15,10 +15,12 @@
 // LDS a token, by workgroups of their own.  The masks are a kernel of their own
 // behind it, 16 bytes at a time (in one kernel with the rest, the rows under a
 // mask held up their workgroup: 640 rows of 131072 bf16, a quarter of them
-// masked, 118 us).  Those rows, with 1500 tokens of history, now take 51 us in
+// masked, 118 us).  Those rows, with 1500 tokens of history, now take 50 us in
 // the table's kernel (91 MB of lines, 1.8 TB/s: one workgroup of 1024 threads a
-// CU, in phases of counting, listing and changing) and 19 us in the masks' (88
-// MB at 4.6 TB/s); a request's single row 6 and 4.
+// request and CU, in phases of counting, listing and changing, of which the
+// largest has three times the mean's entries) and 19 us in the masks' (88 MB at
+// 4.6 TB/s); a request's single row 6 and 4.  The same batch with 8000 tokens of
+// history each, in slices, takes 202 us a call.
 #include "kda_cache.hpp"
 #include "kda_mma.hpp"
 

@@ -15,13 +15,17 @@
 // in LDS.  The expansion is a matrix product of gathered cache rows with W.
 //
 // What bounds them (R = 512, P = 64, 32 heads of 128, bf16): the prompt
-// attention is bound by its products, whose operands come from LDS for each of
-// them and whose exponentials run beside them: one prompt of 8192 takes 675 us
-// in a run of calls (690 GFLOP at 1.0 PFLOP/s, the matrix cores busy for half
-// of the cycles at the clock that they leave).  Scores a block of keys ahead of
-// their exponentials took the whole call from 834 us to 798.  The expansion of its 8192 tokens takes 95 us, 69
-// GFLOP and 134 MB of keys and values written: the writes of a token's heads,
-// 128 bytes apart in time, bound it (110 us in pieces of 8 bytes a lane).
+// attention is bound by the matrix cores.  One prompt of 8192 takes 866 us: 687
+// GFLOP of the operator's, 970 of instructions with the weights' second halves,
+// which run at 1.12 PFLOP/s (a product of 8192^3 in the library: 1.20).  Other
+// orders of instructions within a block of keys take as long.  Scores a block of
+// keys ahead of their exponentials took the whole call from 834 us to 798, with
+// one half.
+// The expansion of its 8192 tokens takes 78 us alone, 69 GFLOP and 134 MB of
+// keys and values written: an operand of W out of LDS feeds one product, so that
+// its reads take as long as the products; and a token's heads are written 128
+// bytes apart in time (110 us in pieces of 8 bytes a lane).
+// fp32: 2048 tokens take 140 us (123 TFLOP/s) and 744 us, one tile in LDS.
 #include "kda_cache.hpp"
 #include "kda_mma.hpp"
 
